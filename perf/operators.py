@@ -1,0 +1,449 @@
+"""Measured cases of the cache-side operators of a decode layer: per-head norm,
+position rotation and append into a paged cache (16/32-bit and 4-bit), reading
+a 4-bit cache back, and decode attention over it.
+
+`run` computes an operator in its plain form (elementary torch operations in
+32 bits, rounded once at the end) or, with `own`, makes the call a user of
+pagedattention_decode_paged_gb300 makes.  `exact` restates the definitions in
+64 bits, one sequence at a time.
+
+The 4-bit cache holds, for each group of 16 consecutive values of a row, 16
+E2M1 codes (two per byte, the lower value in the low nibble) and one E4M3
+scale; a value is code * scale * g with one fp32 factor g for K and one for V.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+EPS = 1e-6
+THETA = 10000.0
+DEV = "cuda"
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+
+def _case(name, op, **kw):
+    c = dict(name=name, op=op, B=1, T=1, H=8, Hkv=8, D=128, bs=16, dtype="bf16", lo=0, hi=0, tail=False,
+             cnt=1, norm=False, rotary=0, pairs=False, window=0, g=1.0)
+    c.update(kw)
+    return c
+
+
+def listed():
+    return [
+        # one request's next token through a grouped-query layer: launch and dependent-load latency
+        _case("rope append 1 token gqa", "append", B=1, H=64, Hkv=8, lo=2047, hi=2047, norm=True, rotary=128),
+        # the Llama-7B-like layer at batch 256, lengths 450..520: one token each, fp16, no norms
+        _case("rope append 256 tokens mha", "append", B=256, H=32, Hkv=32, dtype="f16", lo=450, hi=520, rotary=128),
+        # prompts of a ragged batch through the grouped-query layer, behind a cached prefix of other length
+        _case("rope append prompts gqa", "append", B=8, T=2047, cnt=900, H=64, Hkv=8, lo=0, hi=700, norm=True,
+              rotary=128),
+        # fp32 prompts, half the head rotated in neighbouring pairs, blocks of 8 and an odd length
+        _case("rope append prompts f32", "append", B=3, T=517, cnt=33, H=12, Hkv=4, D=64, bs=8, dtype="f32", lo=0,
+              hi=90, rotary=32, pairs=True),
+        # a serving batch's next tokens into the 4-bit cache, and the written rows read back
+        _case("fp4 append 64 tokens gqa", "append4", B=64, H=64, Hkv=8, lo=100, hi=2047, norm=True, rotary=128, g=0.5),
+        # ragged fp16 prompts quantised into the 4-bit cache, and read back
+        _case("fp4 append prompts", "append4", B=8, T=1023, cnt=300, H=32, Hkv=8, dtype="f16", lo=0, hi=200,
+              rotary=128),
+        # whole cached contexts of a batch turned back into bf16 rows (a prefix that a prompt continues)
+        _case("fp4 gather contexts", "gather4", B=32, T=2048, cnt=1500, Hkv=8, lo=1500, hi=2048, g=0.25),
+        # the 4-request fp32 example: the smallest decode, latency only
+        _case("fp4 decode 4 short f32", "decode4", B=4, H=4, Hkv=4, D=64, dtype="f32", lo=32, hi=128),
+        # the grouped-query layer at batch 32
+        _case("fp4 decode gqa 32 x 2048", "decode4", B=32, H=64, Hkv=8, lo=2048, hi=2048),
+        # long-tail serving mix: 256 requests, median 87 tokens, one head per kv head
+        _case("fp4 decode long tail mha", "decode4", B=256, H=32, Hkv=32, lo=4, hi=4096, tail=True, dtype="f16"),
+        # one request with a very long context: the token axis has to be split
+        _case("fp4 decode 1 x 131071", "decode4", B=1, H=64, Hkv=8, lo=131071, hi=131071, g=0.125),
+        # large batch of long contexts: bandwidth
+        _case("fp4 decode gqa 64 x 8192", "decode4", B=64, H=64, Hkv=8, lo=7000, hi=8192, bs=32),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng: random.Random):
+    op = rng.choice(["append", "append4", "gather4", "decode4", "decode4"])
+    dtype = rng.choice(["f32", "f16", "f16", "bf16", "bf16", "bf16"])
+    four = op != "append"
+    D = rng.choice([64, 128, 128, 256]) if four else rng.choice([32, 64, 128, 128] + ([] if dtype == "f32" else [256]))
+    Hkv = rng.choice([1, 2, 3, 4, 5, 8, 8, 16, 32])
+    grp = rng.choice([1, 1, 2, 3, 4, 5, 7, 8, 8, 16])
+    H = Hkv * grp if Hkv * grp <= 64 else Hkv
+    bs = rng.choice([1, 3, 8, 16, 16, 16, 24, 32, 64, 128])
+    g = rng.choice([1.0, 0.5, 0.0625, 2.0])
+    c = dict(op=op, H=H, Hkv=Hkv, D=D, bs=bs, dtype=dtype, g=g)
+    if op == "decode4":
+        # up to 2^28 cached values of K
+        c["B"] = B = _log(rng, 1, 256)
+        most = max(1, min(131072, (1 << 28) // (B * Hkv * D)))
+        hi = _log(rng, 1, most)
+        c.update(lo=rng.randint(0, hi), hi=hi, tail=rng.random() < 0.25 and hi > 16)
+        c["window"] = _log(rng, 1, 4096) if rng.random() < 0.25 else 0
+    elif op == "gather4":
+        c["B"] = B = _log(rng, 1, 64)
+        most = max(1, min(8192, (1 << 25) // (B * Hkv * D)))
+        T = _log(rng, 1, most)
+        c.update(T=T, cnt=rng.randint(0, T), lo=T, hi=T + rng.randint(0, 300))
+    else:
+        c["B"] = B = _log(rng, 1, 256)
+        most = max(1, min(4096, (1 << 24) // (B * (H + 2 * Hkv) * D)))
+        T = 1 if rng.random() < 0.4 else _log(rng, 1, most)
+        c.update(T=T, cnt=rng.randint(1, T), lo=0, hi=rng.randint(0, 2000), norm=rng.random() < 0.5,
+                 rotary=rng.choice([r for r in (16, 32, 64, 128, 256) if r <= D] + [D, D]), pairs=rng.random() < 0.3)
+    full = _case("", op)
+    full.update(c)
+    del full["name"]
+    return full
+
+
+# --------------------------------------------------------------------------
+# what a case's program has in hand
+# --------------------------------------------------------------------------
+
+def _lengths(case):
+    """Cached tokens and new (or read) tokens of each sequence: part of the case, not of the seed."""
+    r = random.Random(f"{case['B']} {case['T']} {case['lo']} {case['hi']} {case['cnt']} {case['tail']}")
+    lens, cnts = [], []
+    for _ in range(case["B"]):
+        if case["tail"]:
+            n = round(math.exp(math.log(87.0) + r.gauss(0.0, 1.0)))
+            lens.append(max(case["lo"], min(case["hi"], n)))
+        else:
+            lens.append(r.randint(case["lo"], case["hi"]))
+        cnts.append(r.randint(case["cnt"], case["T"]))
+    if not case["tail"]:
+        lens[-1] = case["hi"]
+    cnts[-1] = case["T"]
+    if case["op"] == "gather4":   # the last rows of what is held
+        cnts = [min(n, k) for n, k in zip(lens, cnts)]
+    return lens, cnts
+
+
+def _e2m1(y):
+    """E2M1 codes (sign in bit 3) of fp32 values: nearest, ties to the even code, saturating at 6."""
+    a = y.abs()
+    c = ((a > 0.25).to(torch.uint8) + (a >= 0.75).to(torch.uint8) + (a > 1.25).to(torch.uint8)
+         + (a >= 1.75).to(torch.uint8) + (a > 2.5).to(torch.uint8) + (a >= 3.5).to(torch.uint8) + (a > 5.0).to(torch.uint8))
+    return c | (torch.signbit(y).to(torch.uint8) << 3)
+
+
+def _quantise(x, g):
+    """Codes [..., D/2] (two per byte) and E4M3 scales [..., D/16] of fp32 rows x [..., D]."""
+    G = x.unflatten(-1, (-1, 16))
+    s8 = (G.abs().amax(-1) / (6.0 * g)).clamp(max=448.0).to(torch.float8_e4m3fn)
+    t = s8.float() * g
+    y = torch.where(t[..., None] > 0, G / t[..., None], torch.zeros_like(G))
+    c = _e2m1(y).flatten(-2)
+    return c[..., 0::2] | (c[..., 1::2] << 4), s8.view(torch.uint8)
+
+
+def _values(dev, dtype=torch.float32):
+    return torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0],
+                        device=dev, dtype=dtype)
+
+
+def _dequantise(codes, scales, g, dtype=torch.float32):
+    lut = _values(codes.device, dtype)
+    lo, hi = lut[(codes & 15).long()], lut[(codes >> 4).long()]
+    v = torch.stack((lo, hi), -1).flatten(-2).unflatten(-1, (-1, 16))
+    return (v * scales.view(torch.float8_e4m3fn).to(dtype)[..., None]).flatten(-2) * g
+
+
+def _randn(gen, shape, dtype=torch.float32, scale=1.0):
+    return (torch.randn(shape, generator=gen, device=DEV, dtype=torch.float32) * scale).to(dtype)
+
+
+def prepare(case, seed):
+    c = case
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    dt = DT[c["dtype"]]
+    B, T, H, Hkv, D, bs = c["B"], c["T"], c["H"], c["Hkv"], c["D"], c["bs"]
+    lens, cnts = _lengths(c)
+    append = c["op"] in ("append", "append4")
+    held = [n + (k if append else 0) for n, k in zip(lens, cnts)]
+    nblk = [-(-n // bs) for n in held]
+    MB, NB = max(max(nblk), 1), sum(nblk) + 2
+    perm = torch.randperm(NB, generator=gen, device=DEV).to(torch.int32).cpu()
+    table = torch.full((B, MB), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(nblk):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    s = dict(case=c, table=table.to(DEV), NB=NB, MB=MB, dt=dt, most=max(max(lens), 1),
+             lens=torch.tensor(lens, dtype=torch.int32, device=DEV),
+             cnts=torch.tensor(cnts, dtype=torch.int32, device=DEV), ws={})
+    if append:
+        # the packed output of the layer's projection, rows of all heads of q, k and v beside one another
+        qkv = _randn(gen, (B, T, H + 2 * Hkv, D), dt)
+        s["q"], s["k"], s["v"] = qkv[:, :, :H], qkv[:, :, H:H + Hkv], qkv[:, :, H + Hkv:]
+        if c["norm"]:
+            s["qw"], s["kw"] = (_randn(gen, (D,), torch.float32, 0.1).add_(1.0).to(dt) for _ in range(2))
+        else:
+            s["qw"] = s["kw"] = None
+        n, R = max(held) + 1, c["rotary"]
+        freq = THETA ** (-torch.arange(0, R, 2, device=DEV, dtype=torch.float64) / R)
+        ang = torch.arange(n, device=DEV, dtype=torch.float64)[:, None] * freq
+        s["cos_sin"] = torch.cat((ang.cos(), ang.sin()), 1).float()
+        s["q_out"] = torch.zeros((B, T, H, D), dtype=dt, device=DEV)
+    else:
+        s["q"] = _randn(gen, (B, H, D), dt)
+    if c["op"] == "append":
+        s["pool"] = _randn(gen, (NB, 2, Hkv, bs, D), dt)
+    else:
+        s["pool"] = torch.empty((NB, 2, Hkv, bs, D // 2), dtype=torch.uint8, device=DEV)
+        s["scales"] = torch.empty((NB, 2, Hkv, bs, D // 16), dtype=torch.uint8, device=DEV)
+        step = max(1, (1 << 25) // (2 * Hkv * bs * D))
+        for i in range(0, NB, step):
+            x = _randn(gen, (min(step, NB - i), 2, Hkv, bs, D))
+            s["pool"][i:i + step], s["scales"][i:i + step] = _quantise(x, c["g"])
+        if c["op"] != "decode4":
+            s["k_rows"] = torch.zeros((B, T, Hkv, D), dtype=dt, device=DEV)
+            s["v_rows"] = torch.zeros((B, T, Hkv, D), dtype=dt, device=DEV)
+        if c["op"] == "gather4":
+            s["first"] = s["lens"] - s["cnts"]
+    return s
+
+
+# --------------------------------------------------------------------------
+# one pass
+# --------------------------------------------------------------------------
+
+def _tokens(s, first):
+    """(sequence, token, block, slot, position) of every row t < counts[b] of the padded batch."""
+    c = s["case"]
+    t = torch.arange(c["T"], device=DEV)
+    b, t = torch.nonzero(t[None] < s["cnts"][:, None], as_tuple=True)
+    pos = first[b].long() + t
+    return b, t, s["table"][b, pos // c["bs"]].long(), pos % c["bs"], pos
+
+
+def _rotate(s, x, w, pos):
+    """Norm (when w is given) and rotation of rows x [n, heads, D] at positions pos, in fp32."""
+    c = s["case"]
+    x = x.float()
+    if w is not None:
+        r = (x.double().square().mean(-1, keepdim=True) + EPS).float().double().rsqrt().float()
+        x = (x * r) * w.float()
+    R = c["rotary"]
+    cs = s["cos_sin"][pos][:, None]
+    cos, sin = cs[..., :R // 2], cs[..., R // 2:]
+    y = x.clone()
+    a, b = (slice(0, R, 2), slice(1, R, 2)) if c["pairs"] else (slice(0, R // 2), slice(R // 2, R))
+    y[..., a] = x[..., a] * cos - x[..., b] * sin
+    y[..., b] = x[..., b] * cos + x[..., a] * sin
+    return y
+
+
+def _plain_append(s):
+    b, t, blk, slot, pos = _tokens(s, s["lens"])
+    s["q_out"][b, t] = _rotate(s, s["q"][b, t], s["qw"], pos).to(s["dt"])
+    return b, t, blk, slot, _rotate(s, s["k"][b, t], s["kw"], pos), s["v"][b, t]
+
+
+def _plain_gather(s, first):
+    b, t, blk, slot, _ = _tokens(s, first)
+    g = s["case"]["g"]
+    for half, rows in ((0, s["k_rows"]), (1, s["v_rows"])):
+        rows[b, t] = _dequantise(s["pool"][blk, half, :, slot], s["scales"][blk, half, :, slot], g).to(s["dt"])
+
+
+def _plain_decode(s):
+    c = s["case"]
+    B, H, Hkv, D, bs = c["B"], c["H"], c["Hkv"], c["D"], c["bs"]
+    blk = s["table"].clamp(min=0).long()
+    Lp = s["MB"] * bs
+    pos = torch.arange(Lp, device=DEV)
+    low = (s["lens"] - c["window"]).clamp(min=0) if c["window"] else torch.zeros_like(s["lens"])
+    seen = (pos[None] < s["lens"][:, None]) & (pos[None] >= low[:, None])
+
+    def rows(half):   # [B, Hkv, Lp, D] in fp32
+        x = _dequantise(s["pool"][:, half][blk], s["scales"][:, half][blk], c["g"])
+        return x.transpose(1, 2).reshape(B, Hkv, Lp, D)
+
+    q = s["q"].float().reshape(B, Hkv, H // Hkv, D)
+    x = (q @ rows(0).transpose(-1, -2)) / math.sqrt(D)
+    x = x.masked_fill(~seen[:, None, None], -math.inf)
+    m = x.amax(-1, keepdim=True)
+    w = (x - m.masked_fill(m == -math.inf, 0.0)).exp()
+    o = (w @ rows(1)) / w.sum(-1, keepdim=True).clamp(min=1e-30)
+    return o.reshape(B, H, D).to(s["dt"])
+
+
+def _pools(s):
+    f = s["pool"].view(-1)
+    return f, f[s["pool"].stride(1):]
+
+
+def run(state):
+    s = state
+    c = s["case"]
+    op = c["op"]
+    if own:
+        import pagedattention_decode_paged_gb300 as pa
+        k_pool, v_pool = _pools(s)
+        kw = dict(block_size=c["bs"], num_blocks=s["NB"], block_stride=s["pool"].stride(0))
+        rope = dict(counts=s["cnts"], interleaved=c["pairs"], q_norm=s.get("qw"), k_norm=s.get("kw"), eps=EPS)
+        fp4 = dict(k_scale=c["g"], v_scale=c["g"])
+        if op == "append":
+            pa.paged_kv_append_rope(s["q_out"], s["q"], s["k"], s["v"], k_pool, v_pool, s["table"], s["lens"],
+                                    s["cos_sin"], **rope, **kw)
+            return {"q": s["q_out"], "pool": s["pool"]}
+        if op == "append4":
+            pa.paged_kv_append_rope_fp4(s["q_out"], s["q"], s["k"], s["v"], k_pool, v_pool, s["scales"], s["table"],
+                                        s["lens"], s["cos_sin"], **rope, **fp4, **kw)
+            pa.paged_kv_gather_fp4(s["k_rows"], s["v_rows"], k_pool, v_pool, s["scales"], s["table"], s["lens"],
+                                   s["cnts"], **fp4, **kw)
+            return {"q": s["q_out"], "k": s["k_rows"], "v": s["v_rows"]}
+        if op == "gather4":
+            pa.paged_kv_gather_fp4(s["k_rows"], s["v_rows"], k_pool, v_pool, s["scales"], s["table"], s["first"],
+                                   s["cnts"], **fp4, **kw)
+            return {"k": s["k_rows"], "v": s["v_rows"]}
+        if "fp4" not in s["ws"]:   # kept for the life of the cache, as the library asks
+            s["ws"]["fp4"] = pa.fp4_workspace_for(s["q"], s["table"], num_kv_heads=c["Hkv"], **kw)
+        out = torch.empty_like(s["q"])
+        pa.paged_attention_decode_fp4(out, s["q"], k_pool, v_pool, s["scales"], s["table"], s["lens"],
+                                      1.0 / math.sqrt(c["D"]), s["ws"]["fp4"], num_kv_heads=c["Hkv"],
+                                      window=c["window"], **fp4, **kw)
+        return out
+    if op == "append":
+        b, t, blk, slot, k, v = _plain_append(s)
+        s["pool"][blk, 0, :, slot] = k.to(s["dt"])
+        s["pool"][blk, 1, :, slot] = v
+        return {"q": s["q_out"], "pool": s["pool"]}
+    if op == "append4":
+        b, t, blk, slot, k, v = _plain_append(s)
+        s["pool"][blk, 0, :, slot], s["scales"][blk, 0, :, slot] = _quantise(k, c["g"])
+        s["pool"][blk, 1, :, slot], s["scales"][blk, 1, :, slot] = _quantise(v.float(), c["g"])
+        _plain_gather(s, s["lens"])
+        return {"q": s["q_out"], "k": s["k_rows"], "v": s["v_rows"]}
+    if op == "gather4":
+        _plain_gather(s, s["first"])
+        return {"k": s["k_rows"], "v": s["v_rows"]}
+    return _plain_decode(s)
+
+
+# --------------------------------------------------------------------------
+# what a pass cannot do without
+# --------------------------------------------------------------------------
+
+def work(case):
+    c = case
+    lens, cnts = _lengths(c)
+    es = 4 if c["dtype"] == "f32" else 2
+    H, Hkv, D, R = c["H"], c["Hkv"], c["D"], c["rotary"]
+    n = sum(cnts)
+    row4 = D // 2 + D // 16
+    if c["op"] in ("append", "append4"):
+        spots = set()
+        for p, k in sorted(set(zip(lens, cnts))):
+            spots.update(range(p, p + k))
+        b = n * (H + 2 * Hkv) * D * es + len(spots) * R * 4 + n * H * D * es
+        b += n * 2 * Hkv * D * es if c["op"] == "append" else n * 2 * Hkv * (2 * row4 + D * es)
+        return {"bytes": b, "flops": n * ((H + Hkv) * (3 * R + (4 * D if c["norm"] else 0)))}
+    if c["op"] == "gather4":
+        return {"bytes": n * 2 * Hkv * (row4 + D * es), "flops": n * 4 * Hkv * D}
+    seen = sum(min(x, c["window"]) if c["window"] else x for x in lens)
+    return {"bytes": seen * 2 * Hkv * row4 + 2 * c["B"] * H * D * es, "flops": 4 * seen * H * D}
+
+
+# --------------------------------------------------------------------------
+# the definitions in 64 bits, one sequence at a time
+# --------------------------------------------------------------------------
+
+def _exact_turn(s, x, w, pos):
+    """Rows x [n, heads, D] normed and rotated as complex numbers."""
+    c = s["case"]
+    x = x.double()
+    if w is not None:
+        x = x / (x.pow(2).sum(-1, keepdim=True) / c["D"] + EPS).sqrt() * w.double()
+    R = c["rotary"]
+    cs = s["cos_sin"][pos].double()
+    z = torch.complex(cs[:, :R // 2], cs[:, R // 2:])[:, None]
+    head, rest = x[..., :R], x[..., R:]
+    pair = head.unflatten(-1, (R // 2, 2)) if c["pairs"] else head.unflatten(-1, (2, R // 2)).transpose(-1, -2)
+    turned = torch.view_as_real(torch.view_as_complex(pair.contiguous()) * z)
+    turned = turned if c["pairs"] else turned.transpose(-1, -2)
+    return torch.cat((turned.flatten(-2), rest), -1)
+
+
+def _exact_fp4(x, g):
+    """The values that the 4-bit codes of x [..., D] stand for."""
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=x.device, dtype=torch.float64)
+    e4m3 = torch.arange(127, device=x.device, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+
+    def nearest(v, table):   # ties to the even index
+        i = torch.searchsorted(table, v).clamp(1, table.numel() - 1)
+        lo, hi = table[i - 1], table[i]
+        up = (v - lo > hi - v) | ((v - lo == hi - v) & (i % 2 == 0))
+        return torch.where(up, hi, lo)
+
+    G = x.unflatten(-1, (-1, 16))
+    s = nearest((G.abs().amax(-1, keepdim=True) / (6 * g)).clamp(max=448.0), e4m3)
+    y = torch.where(s > 0, G / (s * g).clamp(min=1e-300), torch.zeros_like(G))
+    return (nearest(y.abs().clamp(max=6.0), grid) * torch.sign(y) * s * g).flatten(-2)
+
+
+def _exact_rows(s, b, half, n0, n1):
+    """Values [n1 - n0, Hkv, D] of tokens n0..n1 of sequence b held in the 4-bit cache."""
+    c = s["case"]
+    j0, j1 = n0 // c["bs"], -(-n1 // c["bs"])
+    blocks = s["table"][b, j0:j1].long()
+    code = s["pool"][blocks, half].transpose(1, 2).flatten(0, 1)[n0 - j0 * c["bs"]:n1 - j0 * c["bs"]]
+    sc = s["scales"][blocks, half].transpose(1, 2).flatten(0, 1)[n0 - j0 * c["bs"]:n1 - j0 * c["bs"]]
+    mag = code.new_tensor([0, 1, 2, 3, 4, 6, 8, 12]).double() / 2
+    nib = torch.stack((code % 16, code // 16), -1).flatten(-2).long()
+    val = mag[nib % 8] * (1 - 2 * (nib // 8)).double()
+    return val * sc.view(torch.float8_e4m3fn).double().repeat_interleave(16, -1) * c["g"]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = case
+    lens, cnts = _lengths(c)
+    if c["op"] in ("append", "append4"):
+        q_out = s["q_out"].double()
+        if c["op"] == "append":
+            pool = s["pool"].double()
+        else:
+            rows = [s["k_rows"].double(), s["v_rows"].double()]
+        for b in range(c["B"]):
+            n = cnts[b]
+            pos = torch.arange(lens[b], lens[b] + n, device=DEV)
+            q_out[b, :n] = _exact_turn(s, s["q"][b, :n], s["qw"], pos)
+            k, v = _exact_turn(s, s["k"][b, :n], s["kw"], pos), s["v"][b, :n].double()
+            if c["op"] == "append":
+                blk = s["table"][b].long()[pos // c["bs"]]
+                pool[blk, 0, :, pos % c["bs"]] = k
+                pool[blk, 1, :, pos % c["bs"]] = v
+            else:
+                rows[0][b, :n], rows[1][b, :n] = _exact_fp4(k, c["g"]), _exact_fp4(v, c["g"])
+        if c["op"] == "append":
+            return {"q": q_out, "pool": pool}
+        return {"q": q_out, "k": rows[0], "v": rows[1]}
+    if c["op"] == "gather4":
+        rows = [s["k_rows"].double(), s["v_rows"].double()]
+        for b in range(c["B"]):
+            for half in (0, 1):
+                rows[half][b, :cnts[b]] = _exact_rows(s, b, half, lens[b] - cnts[b], lens[b])
+        return {"k": rows[0], "v": rows[1]}
+    grp = c["H"] // c["Hkv"]
+    out = torch.zeros((c["B"], c["H"], c["D"]), dtype=torch.float64, device=DEV)
+    for b in range(c["B"]):
+        n0 = max(0, lens[b] - c["window"]) if c["window"] else 0
+        if lens[b] == n0:
+            continue
+        k, v = (_exact_rows(s, b, half, n0, lens[b]).transpose(0, 1) for half in (0, 1))
+        q = s["q"][b].double().view(c["Hkv"], grp, c["D"])
+        w = torch.softmax(torch.einsum("hgd,hld->hgl", q, k) / math.sqrt(c["D"]), -1)
+        out[b] = torch.einsum("hgl,hld->hgd", w, v).reshape(c["H"], c["D"])
+    return out
