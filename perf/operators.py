@@ -140,7 +140,8 @@ def _e2m1(y):
 def _quantise(x, g):
     """Codes [..., D/2] (two per byte) and E4M3 scales [..., D/16] of fp32 rows x [..., D]."""
     G = x.unflatten(-1, (-1, 16))
-    s8 = (G.abs().amax(-1) / (6.0 * g)).clamp(max=448.0).to(torch.float8_e4m3fn)
+    # divided by a tensor: a scalar divisor would become a product with its rounded reciprocal
+    s8 = (G.abs().amax(-1) / torch.full((), 6.0 * g, device=x.device)).clamp(max=448.0).to(torch.float8_e4m3fn)
     t = s8.float() * g
     y = torch.where(t[..., None] > 0, G / t[..., None], torch.zeros_like(G))
     c = _e2m1(y).flatten(-2)
@@ -388,7 +389,8 @@ def _exact_fp4(x, g):
         return torch.where(up, hi, lo)
 
     G = x.unflatten(-1, (-1, 16))
-    s = nearest((G.abs().amax(-1, keepdim=True) / (6 * g)).clamp(max=448.0), e4m3)
+    most = G.abs().amax(-1, keepdim=True)
+    s = nearest((most / torch.full_like(most, 6 * g)).clamp(max=448.0), e4m3)
     y = torch.where(s > 0, G / (s * g).clamp(min=1e-300), torch.zeros_like(G))
     return (nearest(y.abs().clamp(max=6.0), grid) * torch.sign(y) * s * g).flatten(-2)
 
