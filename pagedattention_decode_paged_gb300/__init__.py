@@ -16,7 +16,10 @@ paged_attention_balanced_workspace, paged_attention_decode_balanced
 (persistent load-balanced schedule), paged_kv_append_int8,
 paged_attention_decode_int8 (int8 cache with per-block scales),
 paged_kv_append_fp8, paged_attention_decode_fp8 (fp8 E4M3 cache with
-per-block scales).
+per-block scales), paged_kv_append_rope (per-head norm, position rotation and
+append in one pass; include/pagedattn_rope.h), paged_kv_append_fp4,
+paged_kv_append_rope_fp4, paged_attention_decode_fp4, paged_kv_gather_fp4 (the
+4-bit cache; include/pagedattn_fp4.h).
 """
 from __future__ import annotations
 
@@ -45,7 +48,9 @@ EXPORTED = ("pa_status_string", "pa_version", "paged_kv_append", "paged_attentio
             "paged_kv_append_int8", "paged_attention_decode_int8",
             "paged_kv_append_fp8", "paged_attention_decode_fp8",
             "paged_attention_decode_shared_prefix", "paged_attention_decode_shared_prefix_int8",
-            "paged_attention_decode_shared_prefix_fp8")
+            "paged_attention_decode_shared_prefix_fp8",
+            "paged_kv_append_rope", "paged_kv_append_fp4", "paged_kv_append_rope_fp4",
+            "paged_kv_gather_fp4", "paged_attention_fp4_workspace", "paged_attention_decode_fp4")
 
 
 class PagedAttnError(RuntimeError):
@@ -61,6 +66,20 @@ class Shape(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_blocks", ctypes.c_int64), ("block_stride", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of pa_rope."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class NewRows(ctypes.Structure):
+    """Mirror of pa_new_rows."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("max_tokens", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -125,6 +144,20 @@ def load() -> ctypes.CDLL:
             lib.paged_attention_decode_balanced.restype = ctypes.c_int
             lib.paged_attention_decode_balanced.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                             f32, i32, vp, sz, vp, vp]
+            rp, np_ = ctypes.POINTER(Rope), ctypes.POINTER(NewRows)
+            lib.paged_kv_append_rope.restype = ctypes.c_int
+            lib.paged_kv_append_rope.argtypes = [sp, rp, np_, vp, vp, vp, vp, vp, vp, vp, vp]
+            lib.paged_kv_append_fp4.restype = ctypes.c_int
+            lib.paged_kv_append_fp4.argtypes = [sp, np_, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_kv_append_rope_fp4.restype = ctypes.c_int
+            lib.paged_kv_append_rope_fp4.argtypes = [sp, rp, np_, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_kv_gather_fp4.restype = ctypes.c_int
+            lib.paged_kv_gather_fp4.argtypes = [sp, vp, vp, i32, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_attention_fp4_workspace.restype = sz
+            lib.paged_attention_fp4_workspace.argtypes = [sp]
+            lib.paged_attention_decode_fp4.restype = ctypes.c_int
+            lib.paged_attention_decode_fp4.argtypes = [sp, vp, vp, vp, vp, vp, f32, f32, vp, vp, f32, i32, vp, sz,
+                                                       vp, vp]
             _lib = lib
     return _lib
 
@@ -477,3 +510,207 @@ def paged_attention_decode_shared_prefix_fp8(out, q, k_pool, v_pool, kv_scales, 
                                 kv_scales, block_table, seq_lens, scale, partition_tokens, workspace,
                                 group_first, shared_tokens, num_kv_heads, block_size, num_blocks,
                                 block_stride, err_word, stream, prepare)
+
+
+# ---------------------------------------------------------------------------
+# norm, rotation and append in one pass; the 4-bit cache
+# ---------------------------------------------------------------------------
+
+def rope_table(max_position, rotary_dim, theta=10000.0, device=None) -> torch.Tensor:
+    """cos_sin [max_position][rotary_dim] of the plain rotation: pair i turns by
+    position * theta^(-2i/rotary_dim).  Angles in fp64, so far positions keep
+    their precision; scaled rotations hand in a table of their own."""
+    inv = float(theta) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    ang = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat((ang.cos(), ang.sin()), 1).float()
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor (None and raw addresses aside) lies on the current device,
+    the one the kernels are launched on."""
+    here = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        dev = t.get_device()
+        if here is None:
+            here = torch.cuda.current_device() if dev >= 0 else -2
+        if dev != here:
+            raise ValueError(f"tensor on {t.device}: all tensors must be on the current CUDA device")
+
+
+def _dense(what, t, dtype) -> None:
+    if t is not None and not isinstance(t, int) and not (t.dtype == dtype and t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor")
+
+
+def _new_rows(what, x, like=None):
+    """(batch, tokens, heads, head_dim, token stride) of new rows
+    [B][heads][D] or [B][T][heads][D], possibly a slice of a packed
+    projection output."""
+    shape, st = x.shape, x.stride()
+    if len(shape) == 3:
+        B, H, D = shape
+        T, stride, ok = 1, st[0], True
+    elif len(shape) == 4:
+        B, T, H, D = shape
+        stride = st[0] if T == 1 else st[1]
+        ok = T <= 1 or B <= 1 or st[0] == T * st[1]
+    else:
+        raise ValueError(f"{what} must be [B][heads][D] or [B][T][heads][D]")
+    if B * T <= 1:
+        stride = H * D
+    if not (ok and (D == 1 or st[-1] == 1) and (H == 1 or st[-2] == D)):
+        raise ValueError(f"{what}: the heads of a token must lie one after another, and tokens at one stride")
+    if like is not None and (B, T, D, x.dtype) != like:
+        raise ValueError(f"{what} does not match the keys in batch, tokens, head_dim or dtype")
+    return B, T, H, D, stride
+
+
+def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scale, v_scale, block_table, positions,
+                 counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps, block_size, num_blocks, block_stride,
+                 err_word, stream, prepare):
+    B, T, Hkv, D, ks = _new_rows("k_new", k_new)
+    like = (B, T, D, k_new.dtype)
+    _, _, hv, _, vs = _new_rows("v_new", v_new, like)
+    if hv != Hkv:
+        raise ValueError("k_new and v_new differ in heads")
+    H, qs = Hkv, 0
+    if q is not None:
+        _, _, H, _, qs = _new_rows("q", q, like)
+        if q_out is None or q_out.numel() != B * T * H * D:
+            raise ValueError("q_out must hold batch * tokens * heads * head_dim elements")
+        _dense("q_out", q_out, q.dtype)
+    _dense("block_table", block_table, torch.int32)
+    _dense("positions", positions, torch.int32)
+    _dense("counts", counts, torch.int32)
+    _dense("kv_scales", kv_scales, torch.uint8)
+    if block_table.shape[0] != B or positions.numel() != B or (counts is not None and counts.numel() != B):
+        raise ValueError("block_table, positions and counts must have one row per sequence")
+    fp4 = kv_scales is not None
+    if k_pool.dtype != v_pool.dtype or k_pool.dtype != (torch.uint8 if fp4 else k_new.dtype):
+        raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
+    shape = Shape(B, H, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(k_new.dtype))
+    rows = NewRows(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
+    keep = [shape, rows]
+    args = [ctypes.byref(shape)]
+    if name != "paged_kv_append_fp4":
+        R = 0
+        if cos_sin is not None:
+            _dense("cos_sin", cos_sin, torch.float32)
+            R = cos_sin.shape[1] if rotary_dim is None else rotary_dim
+            if cos_sin.shape[1] != R:
+                raise ValueError("cos_sin must be [max_position][rotary_dim]")
+        for what, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            _dense(what, w, k_new.dtype)
+            if w is not None and w.numel() != D:
+                raise ValueError(f"{what} must hold head_dim elements")
+        rope = Rope(_ptr(cos_sin), cos_sin.shape[0] if R else 0, R, int(interleaved), _ptr(q_norm), _ptr(k_norm), eps)
+        keep.append(rope)
+        args += [ctypes.byref(rope), ctypes.byref(rows), _ptr(q_out)]
+    else:
+        args.append(ctypes.byref(rows))
+    _same_device(k_new, v_new, q, q_out, k_pool, v_pool, kv_scales, block_table, positions, counts, cos_sin, q_norm,
+                 k_norm, err_word)
+    args += [k_pool.data_ptr(), v_pool.data_ptr()]
+    if fp4:
+        args += [kv_scales.data_ptr(), float(k_scale), float(v_scale)]
+    args += [block_table.data_ptr(), positions.data_ptr(), _ptr(counts), _ptr(err_word), _stream(stream)]
+    return _issue(getattr(load(), name), tuple(args), name, prepare, tuple(keep))
+
+
+def paged_kv_append_rope(q_out, q, k_new, v_new, k_pool, v_pool, block_table, positions, cos_sin, *,
+                         counts=None, rotary_dim=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+                         block_size, num_blocks, block_stride, err_word=None, stream=None, prepare=False):
+    """Norm (q_norm, k_norm [D]) and rotate (cos_sin [max_position][rotary_dim],
+    None: no rotation) the new queries and keys, write the queries to q_out and
+    the keys and values at positions[b] + t through block_table.  q, k_new and
+    v_new are [B][heads][D] or, with counts[b] valid tokens, [B][T][heads][D],
+    slices of a packed projection output included; q may be None."""
+    return _append_rows("paged_kv_append_rope", q_out, q, k_new, v_new, k_pool, v_pool, None, 1.0, 1.0, block_table,
+                        positions, counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps, block_size,
+                        num_blocks, block_stride, err_word, stream, prepare)
+
+
+def paged_kv_append_rope_fp4(q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, block_table, positions, cos_sin, *,
+                             counts=None, rotary_dim=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+                             k_scale=1.0, v_scale=1.0, block_size, num_blocks, block_stride, err_word=None,
+                             stream=None, prepare=False):
+    """paged_kv_append_rope into the 4-bit cache: uint8 pools of head_dim/2
+    bytes per row (block_stride in bytes) and kv_scales uint8
+    [num_blocks][2][Hkv][block_size][D/16]."""
+    return _append_rows("paged_kv_append_rope_fp4", q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scale, v_scale,
+                        block_table, positions, counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps,
+                        block_size, num_blocks, block_stride, err_word, stream, prepare)
+
+
+def paged_kv_append_fp4(k_new, v_new, k_pool, v_pool, kv_scales, block_table, positions, *, counts=None, k_scale=1.0,
+                        v_scale=1.0, block_size, num_blocks, block_stride, err_word=None, stream=None, prepare=False):
+    """Quantising append of k_new/v_new [B][Hkv][D] or [B][T][Hkv][D] into the
+    4-bit cache, as they are."""
+    return _append_rows("paged_kv_append_fp4", None, None, k_new, v_new, k_pool, v_pool, kv_scales, k_scale, v_scale,
+                        block_table, positions, counts, None, None, False, None, None, 0.0, block_size, num_blocks,
+                        block_stride, err_word, stream, prepare)
+
+
+def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts, counts=None, *, k_scale=1.0,
+                        v_scale=1.0, block_size, num_blocks, block_stride, err_word=None, stream=None, prepare=False):
+    """Values of tokens starts[b] + t, t < counts[b] (None: all T), of the 4-bit
+    cache into k_out, v_out [B][T][Hkv][D]."""
+    B, T, Hkv, D = k_out.shape
+    if v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out differ in shape")
+    for what, t, dt in (("k_out", k_out, k_out.dtype), ("v_out", v_out, k_out.dtype), ("kv_scales", kv_scales, torch.uint8),
+                        ("block_table", block_table, torch.int32), ("starts", starts, torch.int32),
+                        ("counts", counts, torch.int32)):
+        _dense(what, t, dt)
+    if block_table.shape[0] != B or starts.numel() != B or (counts is not None and counts.numel() != B):
+        raise ValueError("block_table, starts and counts must have one row per sequence")
+    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+        raise ValueError("the pools must be uint8")
+    _same_device(k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts, counts, err_word)
+    shape = Shape(B, Hkv, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(k_out.dtype))
+    args = (ctypes.byref(shape), k_out.data_ptr(), v_out.data_ptr(), T, k_pool.data_ptr(), v_pool.data_ptr(),
+            kv_scales.data_ptr(), float(k_scale), float(v_scale), block_table.data_ptr(), starts.data_ptr(),
+            _ptr(counts), _ptr(err_word), _stream(stream))
+    return _issue(load().paged_kv_gather_fp4, args, "paged_kv_gather_fp4", prepare, (shape,))
+
+
+def paged_attention_fp4_workspace(shape: Shape) -> int:
+    return int(load().paged_attention_fp4_workspace(ctypes.byref(shape)))
+
+
+def fp4_workspace_for(q, block_table, *, num_kv_heads, block_size, num_blocks, block_stride) -> torch.Tensor:
+    """Allocate (through torch) a zero-filled workspace for
+    paged_attention_decode_fp4 on q's device."""
+    shape = decode_shape(q, block_table, num_kv_heads=num_kv_heads, block_size=block_size, num_blocks=num_blocks,
+                         block_stride=block_stride)
+    with torch.cuda.device(q.device):
+        n = paged_attention_fp4_workspace(shape)
+    if n == 0:
+        raise PagedAttnError(PA_ERR_UNSUPPORTED, "paged_attention_fp4_workspace")
+    return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=q.device)
+
+
+def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, seq_lens, scale, workspace, *,
+                               k_scale=1.0, v_scale=1.0, window=0, num_kv_heads, block_size, num_blocks, block_stride,
+                               err_word=None, stream=None, prepare=False):
+    """out[B][H][D] = attention of q over the valid tokens (the last `window` of
+    them when positive) of a 4-bit cache; workspace from fp4_workspace_for."""
+    B, H, D = q.shape
+    if out.shape != q.shape:
+        raise ValueError("out and q differ in shape")
+    for what, t, dt in (("q", q, q.dtype), ("out", out, q.dtype), ("kv_scales", kv_scales, torch.uint8),
+                        ("block_table", block_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
+                        ("workspace", workspace, torch.uint8)):
+        _dense(what, t, dt)
+    if block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table and seq_lens must have one row per sequence")
+    if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
+        raise ValueError("the pools must be uint8")
+    _same_device(q, out, k_pool, v_pool, kv_scales, block_table, seq_lens, workspace, err_word)
+    shape = Shape(B, H, num_kv_heads, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(q.dtype))
+    args = (ctypes.byref(shape), out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            kv_scales.data_ptr(), float(k_scale), float(v_scale), block_table.data_ptr(), seq_lens.data_ptr(),
+            float(scale), int(window), workspace.data_ptr(), workspace.numel(), _ptr(err_word), _stream(stream))
+    return _issue(load().paged_attention_decode_fp4, args, "paged_attention_decode_fp4", prepare, (shape,))

@@ -1,0 +1,662 @@
+// decode_fp4.cu -- decode attention over the 4-bit cache (E2M1 codes, one E4M3
+// scale per 16 values; include/pagedattn_fp4.h) on the tensor cores.
+//
+// The per-block attention decomposition is that of "KV Cache paging in LLM
+// inference" (intelliparadigm.com) s2.2.  An item is a (sequence, kv head,
+// group of query heads); its 16-token tiles are read once for all its heads.
+//
+// Arithmetic of a tile (one warp, mma.sync m16n8k16, fp32 accumulation):
+//   S^T[16 tokens x 8 columns] = K Q^T, then the online softmax down each
+//   column, then O^T[D x 8 columns] += V^T P^T, a column being a query head
+//   (16-bit queries) or the high or low fp16 part of one (fp32 queries: the
+//   parts' products add up to 22 bits).  One cvt turns two E2M1 codes into
+//   fp16, one packed multiply applies the E4M3 scale, exactly; so 4-bit rows
+//   go from the ring into MMA A fragments with no staging and no rounding.
+//   The contraction over head_dim may take its elements in any order: lane
+//   (gid, tig) holds D/8 consecutive bytes of K rows tau(gid), tau(gid) + 8,
+//   and the queries are packed to match.  The contraction over tokens needs
+//   pairs of tokens side by side: two words of two tokens become the words of
+//   their even and odd elements with one shift and one select each, and the
+//   cvt then yields (token, next token) pairs.  tau is a permutation of 0..7
+//   chosen so that the wide K loads and the V loads both miss no bank.
+//   A column is rescaled only when a score passes the reference maximum by
+//   more than 2^8 (weights stay inside fp16), so a tile usually costs one
+//   vote and no shuffles.
+//
+// Work split: the tiles of all items, end to end, are cut into one equal run
+// per CTA and one equal part of that per warp (balanced.cuh's index space).  A
+// warp that covers an item writes its output; partial states of the warps of
+// a CTA meet in shared memory, those of CTAs in the workspace, where the last
+// to arrive merges (in two levels when many share an item), always in the
+// items' order, so that results repeat.
+#include <math.h>
+
+#include "balanced.cuh"
+#include "fp4.cuh"
+#include "pa_rope_fp4.h"
+
+namespace pa {
+
+constexpr int kFp4Warps = 8;
+constexpr int kFp4Threads = kFp4Warps * 32;
+constexpr int kFp4Tile = 16;
+constexpr int kFp4MinTiles = 2;    // tiles per warp below which fewer CTAs share the work
+constexpr int kFp4Flat = 24;       // sharers of an item up to which one level of merging serves
+constexpr int kFp4Group = 16;      // sharers per first-level group above that
+
+template <bool V>
+struct Fp4Bool {
+    static constexpr bool value = V;
+};
+
+template <typename T, int D, int NT>
+struct Fp4Cfg {
+    static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kHeads = NT * 8 / kParts;          // query heads per item
+    static constexpr int kRow = D / 2;                      // code bytes of a row
+    static constexpr int kScRow = D / 16;                   // scale bytes of a row
+    static constexpr int kCodes = 2 * kFp4Tile * kRow;      // K then V codes of a tile
+    static constexpr int kScales = 2 * kFp4Tile * kScRow;
+    static constexpr int kStages = 4;
+    static constexpr int kWarpRing = kStages * (kCodes + kScales);
+    static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
+    static constexpr int kCtasPerSm = NT * D <= 128 ? 2 : 1;
+    // the last record of a warp reuses its own ring
+    static_assert(kWarpRing >= kRec * 4, "a record fits the ring");
+    static constexpr size_t kFixed = (size_t)kFp4Warps * (kWarpRing + kRec * 4);
+    static size_t bytes(int batch) { return kFixed + ((size_t)2 * batch + 1) * 4; }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
+    if constexpr (N == 16) cp_async16(dst, src, bytes);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Row of the tile behind row i of the MMAs' token axis (rows 8..15: + 8), and
+// where 16-byte chunk c of tile row r lies in its row.
+template <int D>
+__device__ __forceinline__ int tau(int i) {
+    return D == 64 ? i ^ ((i >> 2) & 1) : i ^ ((i >> 1) & 1);
+}
+template <int D>
+__device__ __forceinline__ int swizzle(int r, int c) {
+    return D == 64 ? c : D == 128 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
+    if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    if constexpr (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+template <int BYTES>
+__device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
+    uint32_t v;
+    if constexpr (BYTES == 1) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    else if constexpr (BYTES == 2) asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(addr));
+    else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kFp4Threads, (Fp4Cfg<T, D, NT>::kCtasPerSm))
+decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) {
+    using C = Fp4Cfg<T, D, NT>;
+    constexpr int P = C::kParts, HP = C::kHeads, S = C::kStages;
+    constexpr int KW = D / 32;                 // words of a K row per lane
+    constexpr int VW = D / 64;                 // words of a V row per lane
+    constexpr int MT = D / 16;                 // 16-row tiles of O^T
+    const DecodeParams &p = fp.d;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ int32_t scan_tmp[kFp4Warps];
+    __shared__ int32_t rec_first[2 * kFp4Warps], rec_n[2 * kFp4Warps], rec_b[2 * kFp4Warps], rec_it[2 * kFp4Warps];
+    __shared__ int32_t last_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    unsigned char *ring_p = smem + (size_t)warp * C::kWarpRing;
+    const uint32_t ring = smem_u32(ring_p);
+    float *first_rec = reinterpret_cast<float *>(smem + (size_t)kFp4Warps * C::kWarpRing) + (size_t)warp * C::kRec;
+    float *last_rec = reinterpret_cast<float *>(ring_p);
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + C::kFixed);
+    int32_t *lens = pre + p.B + 1;
+
+    grid_dependency_wait();
+    allow_dependents();
+    const int items_per_seq = p.Hkv * units_per_kv;
+    build_schedule<kFp4Tile>(p, items_per_seq, kFp4Tile, pre, lens, scan_tmp);
+    zero_empty_sequences<T>(p, pre);
+    const int32_t Tn = pre[p.B];
+    // CTAs that work: all, unless that leaves their warps less than kFp4MinTiles tiles
+    const int want = (Tn + kFp4Warps * kFp4MinTiles - 1) / (kFp4Warps * kFp4MinTiles);
+    const int nC = min((int)gridDim.x, want);
+    const int cta = blockIdx.x;
+    if (cta >= nC) return;
+    const int32_t c0 = slice_start(cta, Tn, nC), c1 = slice_start(cta + 1, Tn, nC);
+    const int32_t w0 = c0 + slice_start(warp, c1 - c0, kFp4Warps), w1 = c0 + slice_start(warp + 1, c1 - c0, kFp4Warps);
+    if (lane < 2) rec_first[2 * warp + lane] = -1;
+
+    const int grp = p.H / p.Hkv;               // query heads per kv head
+    T *out = reinterpret_cast<T *>(p.out);
+
+    // ---- producer side -------------------------------------------------------
+    // Lane l looks up the block of tile row l % 16, one tile ahead; it copies
+    // that row's K (l < 16) or V scales, and the code rows of its chunk place.
+    TileCursor pc = {};
+    int32_t pt = w0;                           // next tile to fetch
+    int32_t p_tok = 0;                         // its first token
+    int64_t p_blk = -1;
+    int p_slot = 0;
+    bool p_need = false;
+    uint32_t bad_bits = 0;                     // per ring stage: a needed table entry is bad
+    auto look_up = [&]() {                     // of tile pt under cursor pc
+        const int32_t L = lens[pc.b];
+        const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
+        p_tok = t_win / kFp4Tile * kFp4Tile + pc.k * kFp4Tile;
+        const int32_t tok = p_tok + (lane & 15);
+        p_need = tok >= t_win && tok < L;
+        p_blk = -1;
+        if (p_need) {
+            const int32_t j = p.bs_shift >= 0 ? tok >> p.bs_shift : tok / p.bs;
+            p_slot = tok - j * p.bs;
+            p_blk = __ldg(p.block_table + (int64_t)pc.b * p.MB + j);
+        }
+    };
+    auto fetch = [&](int stage) {              // tile pt into `stage`, then step to the next one
+        const bool ok = p_need && p_blk >= 0 && p_blk < p.num_blocks;
+        const bool bad = p_need && !ok;
+        if (__any_sync(0xffffffffu, bad)) {
+            bad_bits |= 1u << stage;
+            if (bad && lane < 16) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+        } else {
+            bad_bits &= ~(1u << stage);
+        }
+        const int hk = units_per_kv == 1 ? pc.it : pc.it / units_per_kv;
+        const int64_t row = (int64_t)hk * p.bs + p_slot;
+        const int64_t off = ok ? p_blk * p.block_stride_bytes + row * C::kRow : -1;
+        const uint32_t codes = ring + stage * (C::kCodes + C::kScales);
+        {
+            const int half = lane >> 4;
+            const int64_t so = ok ? ((p_blk * 2 + half) * p.Hkv * p.bs + row) * C::kScRow : 0;
+            cp_async_small<C::kScRow>(codes + C::kCodes + lane * C::kScRow, fp.scales + so, ok ? C::kScRow : 0);
+        }
+        constexpr int CH = C::kRow / 16;       // 16-byte chunks per row
+#pragma unroll
+        for (int i = 0; i < kFp4Tile * CH / 32; ++i) {
+            const int r = (i * 32 + lane) / CH, c = lane % CH;
+            const int64_t ro = __shfl_sync(0xffffffffu, off, r);
+            const int64_t so = ro < 0 ? 0 : ro + c * 16;
+            const uint32_t dst = codes + r * C::kRow + swizzle<D>(r, c) * 16;
+            cp_async16(dst, p.k_pool + so, ro < 0 ? 0 : 16);
+            cp_async16(dst + kFp4Tile * C::kRow, p.v_pool + so, ro < 0 ? 0 : 16);
+        }
+        if (++pt < w1) {
+            pc.next(pre, items_per_seq);
+            look_up();
+        }
+    };
+
+    // ---- consumer side -------------------------------------------------------
+    uint32_t qf[NT][MT][2];                    // Q^T as MMA B fragments
+    float cs[NT][2];                           // scale * log2(e) * 2^e of columns 2 tig, 2 tig + 1
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+    auto load_q = [&](int b, int it) {
+        const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = P == 2 ? nt * 4 + (gid & 3) : nt * 8 + gid;
+            const bool have = h0 + col < grp;
+            const T *src = reinterpret_cast<const T *>(p.q) + ((int64_t)b * p.H + hk * grp + h0 + col) * D + tig * (D / 4);
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (have) load8(src + 8 * i, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // a power of two that brings the head's largest element into [1, 2)
+            int e = (int)((__float_as_uint(big) >> 23) & 255u) - 127;
+            e = big > 0.f && e < 128 ? min(max(e, -126), 126) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (have) load8(src + 8 * i, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[j] *= down;
+                    if (P == 2 && gid >= 4) x[j] -= __half2float(__float2half_rn(x[j]));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qf[nt][2 * i + j / 2][j & 1] = Elem<__half>::pack2(x[2 * j], x[2 * j + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = P == 2 ? (2 * tig + j) & 3 : 2 * tig + j;
+                cs[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, c * 4);
+                m[nt][j] = -INFINITY;
+                l[nt][j] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+        }
+    };
+
+    auto tile = [&](uint32_t codes, int32_t tok0, int32_t lo, int32_t hi) {
+        const uint32_t sc = codes + C::kCodes;
+        const int rk = tau<D>(gid);
+        // K rows rk and rk + 8 of this lane, and their scales
+        uint32_t kw[2][KW], ks[2][(KW + 1) / 2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = rk + 8 * r;
+            if constexpr (D == 256) {
+                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig) * 16, kw[r]);
+                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig + 1) * 16, kw[r] + 4);
+            } else if constexpr (D == 128) {
+                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, tig) * 16, kw[r]);
+            } else {
+                lds_words<2>(codes + row * C::kRow + tig * 8, kw[r]);
+            }
+            const uint32_t s = lds_bytes<KW / 2>(sc + row * C::kScRow + tig * (KW / 2));
+#pragma unroll
+            for (int i = 0; i < KW / 2; ++i) ks[r][i] = e4m3x2_to_f16x2(__byte_perm(s, 0, i * 0x11));
+        }
+        float c[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
+            const uint32_t a[4] = {hmul2_u32(e2m1x2_to_f16x2<0>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
+                                   hmul2_u32(e2m1x2_to_f16x2<1>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
+            const uint32_t d[4] = {hmul2_u32(e2m1x2_to_f16x2<2>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
+                                   hmul2_u32(e2m1x2_to_f16x2<3>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                MmaOp<__half>::run(c[nt], a, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                MmaOp<__half>::run(c[nt], d, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+            }
+        }
+
+        // scores in the log2 domain; rows outside [lo, hi) weigh nothing
+        const bool in0 = tok0 + rk >= lo && tok0 + rk < hi, in1 = tok0 + rk + 8 >= lo && tok0 + rk + 8 < hi;
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (P == 2) c[nt][i] += __shfl_xor_sync(0xffffffffu, c[nt][i], 2);
+                c[nt][i] = (i < 2 ? in0 : in1) ? c[nt][i] * cs[nt][i & 1] : -INFINITY;
+                over |= c[nt][i] > m[nt][i & 1] + 8.f;
+            }
+        }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(m[nt][j], fmaxf(c[nt][j], c[nt][j + 2]));
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+                    const float f = merge_weight(m[nt][j], mx);
+                    m[nt][j] = mx;
+                    l[nt][j] *= f;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        o[nt][mt][j] *= f;
+                        o[nt][mt][j + 2] *= f;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];                    // P^T as MMA B fragments
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = ex2_approx(c[nt][i] - m[nt][i & 1]);
+                l[nt][i & 1] += w[i];
+                if (P == 2 && tig >= 2) w[i] -= __half2float(__float2half_rn(w[i]));
+            }
+            pf[nt][0] = movmatrix_trans(Elem<__half>::pack2(w[0], w[1]));
+            pf[nt][1] = movmatrix_trans(Elem<__half>::pack2(w[2], w[3]));
+        }
+
+        // V rows of this lane's token pairs (t0, t1) and (t0 + 8, t1 + 8)
+        const int t0 = tau<D>(2 * tig), t1 = tau<D>(2 * tig + 1);
+        const uint32_t vc = codes + kFp4Tile * C::kRow, vs = sc + kFp4Tile * C::kScRow;
+        uint32_t vw[4][VW], ss[2][(VW + 1) / 2];
+        constexpr int VB = VW == 4 ? 2 : 1;    // scale bytes per lane and row
+        uint32_t sb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (i & 1 ? t1 : t0) + 8 * (i >> 1);
+            const int byte = gid * (D / 16);   // of the row
+            lds_words<VW>(vc + row * C::kRow + swizzle<D>(row, byte / 16) * 16 + byte % 16, vw[i]);
+            sb[i] = lds_bytes<VB>(vs + row * C::kScRow + (D == 64 ? gid / 2 : gid * VB));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < VB; ++k) ss[i][k] = e4m3x2_to_f16x2(__byte_perm(sb[2 * i], sb[2 * i + 1], k | ((4 + k) << 4)));
+#pragma unroll
+        for (int v = 0; v < VW; ++v) {
+            uint32_t ev[2], od[2];             // even and odd elements of a token pair
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t a = vw[2 * i][v], b = vw[2 * i + 1][v];
+                ev[i] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+                od[i] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+            }
+            const uint32_t s0 = ss[0][VB == 2 ? v / 2 : 0], s1 = ss[1][VB == 2 ? v / 2 : 0];
+            auto step = [&](int j, uint32_t e0, uint32_t d0, uint32_t e1, uint32_t d1) {
+                const uint32_t a[4] = {hmul2_u32(e0, s0), hmul2_u32(d0, s0), hmul2_u32(e1, s1), hmul2_u32(d1, s1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(o[nt][4 * v + j], a, pf[nt][0], pf[nt][1]);
+            };
+            step(0, e2m1x2_to_f16x2<0>(ev[0]), e2m1x2_to_f16x2<0>(od[0]), e2m1x2_to_f16x2<0>(ev[1]), e2m1x2_to_f16x2<0>(od[1]));
+            step(1, e2m1x2_to_f16x2<1>(ev[0]), e2m1x2_to_f16x2<1>(od[0]), e2m1x2_to_f16x2<1>(ev[1]), e2m1x2_to_f16x2<1>(od[1]));
+            step(2, e2m1x2_to_f16x2<2>(ev[0]), e2m1x2_to_f16x2<2>(od[0]), e2m1x2_to_f16x2<2>(ev[1]), e2m1x2_to_f16x2<2>(od[1]));
+            step(3, e2m1x2_to_f16x2<3>(ev[0]), e2m1x2_to_f16x2<3>(od[0]), e2m1x2_to_f16x2<3>(ev[1]), e2m1x2_to_f16x2<3>(od[1]));
+        }
+    };
+
+    // The state of an item this warp has finished its part of: whole items to
+    // `out`, parts to a record (O [HP][D], m [HP], l [HP]; l < 0: bad table).
+    auto finish = [&](const TileCursor &cc, bool whole, bool bad, float *rec) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], s);
+            }
+            if (P == 2)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[nt][mt][i] += __shfl_xor_sync(0xffffffffu, o[nt][mt][i], 2);
+        }
+        const int hk = cc.it / units_per_kv, h0 = (cc.it - hk * units_per_kv) * HP;
+        const bool writer = P == 1 || tig < 2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = nt * (8 / P) + 2 * tig + j;
+                if (!writer || h0 + col >= grp) continue;
+                const float f = whole ? (bad ? 0.f : fp.v_g / l[nt][j]) : 1.f;
+#pragma unroll
+                for (int v = 0; v < VW; ++v) {
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        x[2 * k] = whole && bad ? 0.f : o[nt][4 * v + k][j] * f;
+                        x[2 * k + 1] = whole && bad ? 0.f : o[nt][4 * v + k][j + 2] * f;
+                    }
+                    const int d = gid * (D / 8) + 8 * v;
+                    if (whole) store8(out + ((int64_t)cc.b * p.H + hk * grp + h0 + col) * D + d, x);
+                    else store8(rec + col * D + d, x);
+                }
+                if (!whole && gid == 0) {
+                    rec[HP * D + col] = m[nt][j];
+                    rec[HP * D + HP + col] = bad ? -1.f : l[nt][j];
+                }
+            }
+    };
+
+    if (w0 < w1) {
+        pc.seek(pre, p.B, items_per_seq, w0);
+        TileCursor cc = pc;
+        look_up();
+#pragma unroll 1
+        for (int s = 0; s < S - 1; ++s) {
+            if (pt < w1) fetch(s);
+            cp_async_commit();
+        }
+        bool fresh = true, bad = false;
+        int32_t lo = 0, hi = 0, base = 0;
+        int stage = 0;
+        for (int32_t t = w0; t < w1; ++t) {
+            if (fresh) {
+                load_q(cc.b, cc.it);
+                hi = lens[cc.b];
+                lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
+                base = lo / kFp4Tile * kFp4Tile;
+                fresh = bad = false;
+            }
+            cp_async_wait<S - 2>();
+            __syncwarp();                      // every lane's copies have landed, and the tile before is read
+            bad |= (bad_bits >> stage) & 1u;
+            if (pt < w1) fetch(stage == 0 ? S - 1 : stage - 1);
+            cp_async_commit();
+            tile(ring + stage * (C::kCodes + C::kScales), base + cc.k * kFp4Tile, lo, hi);
+            stage = stage + 1 == S ? 0 : stage + 1;
+            const bool item_end = cc.k + 1 == cc.n, slice_end = t + 1 == w1;
+            if (item_end || slice_end) {
+                const bool whole = item_end && cc.first >= w0;
+                const int which = slice_end ? 1 : 0;   // a part that ends inside the slice began before it
+                if (which == 1) {
+                    cp_async_wait<0>();
+                    __syncwarp();              // the ring is free for the record
+                }
+                finish(cc, whole, bad, which ? last_rec : first_rec);
+                if (!whole && lane == 0) {
+                    const int r = 2 * warp + which;
+                    rec_first[r] = cc.first;
+                    rec_n[r] = cc.n;
+                    rec_b[r] = cc.b;
+                    rec_it[r] = cc.it;
+                }
+                fresh = true;
+            }
+            if (!slice_end) cc.next(pre, items_per_seq);
+        }
+    }
+    __syncthreads();
+
+    // ---- merges --------------------------------------------------------------
+    // The `n` records rec_at(0..n) of one item into its output, or into the
+    // record dst.  Records in the workspace were written by other CTAs: read at L2.
+    auto merge = [&](auto in_workspace, int n, auto rec_at, int b, int it, bool whole, float *dst) {
+        auto ld = [](const float *a) { return decltype(in_workspace)::value ? __ldcg(a) : *a; };
+        const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
+        const int heads = min(HP, grp - h0);
+        for (int i = threadIdx.x; i < heads * (D / 4); i += kFp4Threads) {
+            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+            float M = -INFINITY;
+            bool bad = false;
+            for (int r = 0; r < n; ++r) {
+                const float *rec = rec_at(r);
+                M = fmaxf(M, ld(rec + HP * D + h));
+                bad |= ld(rec + HP * D + HP + h) < 0.f;
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll 4
+            for (int r = 0; r < n; ++r) {
+                const float *rec = rec_at(r);
+                const float mr = ld(rec + HP * D + h);
+                const float w = merge_weight(mr, M);
+                const float4 *ra = reinterpret_cast<const float4 *>(rec + h * D + d);
+                const float4 a = decltype(in_workspace)::value ? __ldcg(ra) : *ra;
+                sum = fmaf(ld(rec + HP * D + HP + h), w, sum);
+                acc.x = fmaf(a.x, w, acc.x);
+                acc.y = fmaf(a.y, w, acc.y);
+                acc.z = fmaf(a.z, w, acc.z);
+                acc.w = fmaf(a.w, w, acc.w);
+            }
+            if (whole) {
+                const float f = fp.v_g / sum;
+                T *row = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + d;
+                row[0] = Elem<T>::from_float(bad ? 0.f : acc.x * f);
+                row[1] = Elem<T>::from_float(bad ? 0.f : acc.y * f);
+                row[2] = Elem<T>::from_float(bad ? 0.f : acc.z * f);
+                row[3] = Elem<T>::from_float(bad ? 0.f : acc.w * f);
+            } else {
+                __stcg(reinterpret_cast<float4 *>(dst + h * D + d), acc);
+                if (d == 0) {
+                    __stcg(dst + HP * D + h, M);
+                    __stcg(dst + HP * D + HP + h, bad ? -1.f : sum);
+                }
+            }
+        }
+    };
+    constexpr Fp4Bool<false> here{};
+    constexpr Fp4Bool<true> workspace{};
+    auto smem_rec = [&](int r) -> const float * {
+        return (r & 1) ? reinterpret_cast<const float *>(smem + (size_t)(r >> 1) * C::kWarpRing)
+                       : reinterpret_cast<const float *>(smem + (size_t)kFp4Warps * C::kWarpRing) + (size_t)(r >> 1) * C::kRec;
+    };
+    // record `slot` of a CTA: 0 its first item, 1 its last one; 2 and 3 the
+    // merged record of the group of sharers that record 0 or 1 heads
+    auto global_rec = [&](int c, int slot) { return p.records + ((int64_t)c * 4 + slot) * p.rec_floats; };
+
+    int part0 = -1, part1 = -1;                // first records (in shared memory) of items shared with other CTAs
+    for (int r = 0; r < 2 * kFp4Warps;) {
+        if (rec_first[r] < 0) {
+            ++r;
+            continue;
+        }
+        const int r0 = r;
+        int idx[2 * kFp4Warps], n = 0;
+        for (; r < 2 * kFp4Warps && (rec_first[r] < 0 || rec_first[r] == rec_first[r0]); ++r)
+            if (rec_first[r] >= 0) idx[n++] = r;
+        const bool before = rec_first[r0] < c0, whole = !before && rec_first[r0] + rec_n[r0] <= c1;
+        if (!whole) (before ? part0 : part1) = r0;
+        merge(here, n, [&](int i) { return smem_rec(idx[i]); }, rec_b[r0], rec_it[r0], whole,
+              whole ? nullptr : global_rec(cta, before ? 0 : 1));
+    }
+    if (part0 < 0 && part1 < 0) return;
+    // all of this CTA's stores come before its count on a counter
+    auto arrive = [&](int32_t *counter, int sharers) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const bool last = atomicAdd(counter, 1) == sharers - 1;
+            last_flag = last;
+            if (last) *counter = 0;            // nobody else touches it again in this call
+        }
+        __syncthreads();
+        if (last_flag == 0) return false;
+        __threadfence();
+        return true;
+    };
+#pragma unroll 1
+    for (int slot = 0; slot < 2; ++slot) {
+        const int r0 = slot ? part1 : part0;
+        if (r0 < 0) continue;
+        const int32_t first = rec_first[r0];
+        const int o0 = slice_owner(first, Tn, nC), o1 = slice_owner(first + rec_n[r0] - 1, Tn, nC);
+        const int b = rec_b[r0], it = rec_it[r0];
+        int n = o1 - o0 + 1, stride = 1, merged = 0;
+        int32_t *counter = p.counters + (int64_t)b * items_per_seq + it;
+        if (n > kFp4Flat) {
+            // first level: the last of a group of neighbouring sharers merges its records
+            const int g0 = (cta - o0) / kFp4Group * kFp4Group, gslot = g0 == 0 ? 1 : 0;
+            const int gn = min(kFp4Group, n - g0);
+            if (!arrive(p.group_counters + (int64_t)(o0 + g0) * 2 + gslot, gn)) continue;
+            merge(workspace, gn, [&](int i) { return (const float *)global_rec(o0 + g0 + i, g0 + i == 0 ? 1 : 0); }, b, it,
+                  false, global_rec(o0 + g0, 2 + gslot));
+            n = (n + kFp4Group - 1) / kFp4Group;
+            stride = kFp4Group;
+            merged = 2;
+        }
+        if (!arrive(counter, n)) continue;
+        // an item's record is its first CTA's last one and every other CTA's first one
+        merge(workspace, n, [&](int i) { return (const float *)global_rec(o0 + i * stride, merged + (i == 0 ? 1 : 0)); }, b,
+              it, true, nullptr);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+template <typename T, int D, int NT>
+struct Fp4Launch {
+    using C = Fp4Cfg<T, D, NT>;
+    static std::atomic<int> configured[64];
+    static int64_t occupancy[64][2];
+
+    static cudaError_t plan(int batch, int64_t max_tiles, Fp4Plan *plan) {
+        auto kern = decode_fp4_kernel<T, D, NT>;
+        const size_t smem = C::bytes(batch);
+        cudaError_t e = ensure_smem_limit(kern, smem, configured);
+        if (e != cudaSuccess) return e;
+        int per_sm = 0, sms = 0;
+        e = resident_ctas(kern, kFp4Threads, smem, occupancy, &per_sm);
+        if (e != cudaSuccess) return e;
+        e = device_sm_count(&sms);
+        if (e != cudaSuccess) return e;
+        int64_t grid = (int64_t)sms * per_sm;
+        const int64_t cap = (max_tiles + kFp4Warps * kFp4MinTiles - 1) / (kFp4Warps * kFp4MinTiles);
+        plan->grid = (int)(grid > cap ? cap : grid);
+        plan->smem = smem;
+        plan->rec_floats = C::kRec;
+        return cudaSuccess;
+    }
+    static cudaError_t launch(const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream) {
+        if (plan.grid <= 0) return cudaErrorInvalidValue;
+        return launch_clustered(decode_fp4_kernel<T, D, NT>, plan.grid, kFp4Threads, plan.smem, 1, stream, p,
+                                plan.units_per_kv);
+    }
+};
+template <typename T, int D, int NT> std::atomic<int> Fp4Launch<T, D, NT>::configured[64];
+template <typename T, int D, int NT> int64_t Fp4Launch<T, D, NT>::occupancy[64][2] = {};
+
+// f(Fp4Launch<T, D, NT>{}) for the shape's instantiation.
+template <typename T, typename F>
+static cudaError_t dispatch_fp4_typed(int head_dim, int nt, F &&f) {
+    switch (head_dim) {
+        case 64: return nt == 2 ? f(Fp4Launch<T, 64, 2>{}) : f(Fp4Launch<T, 64, 1>{});
+        case 128: return nt == 2 ? f(Fp4Launch<T, 128, 2>{}) : f(Fp4Launch<T, 128, 1>{});
+        case 256: return f(Fp4Launch<T, 256, 1>{});
+    }
+    return cudaErrorInvalidValue;
+}
+template <typename F>
+static cudaError_t dispatch_fp4(int dtype, int head_dim, int nt, F &&f) {
+    switch (dtype) {
+        case PA_F32: return dispatch_fp4_typed<float>(head_dim, nt, f);
+        case PA_F16: return dispatch_fp4_typed<__half>(head_dim, nt, f);
+        case PA_BF16: return dispatch_fp4_typed<__nv_bfloat16>(head_dim, nt, f);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int64_t max_tiles_per_item,
+                            Fp4Plan *plan) {
+    // one 8-column tile per item, or two when the kv head has more columns:
+    // the conversion of a tile, not its MMAs, is what an item costs
+    const int columns = group * (dtype == PA_F32 ? 2 : 1);
+    plan->nt = head_dim <= 128 && columns > 8 ? 2 : 1;
+    const int heads = plan->nt * 8 / (dtype == PA_F32 ? 2 : 1);
+    plan->units_per_kv = (group + heads - 1) / heads;
+    plan->items = (int64_t)batch * kv_heads * plan->units_per_kv;
+    const int64_t total = plan->items * max_tiles_per_item;
+    if (total >= (int64_t)INT32_MAX / 2) return cudaErrorInvalidValue;
+    return dispatch_fp4(dtype, head_dim, plan->nt, [&](auto l) { return l.plan(batch, total, plan); });
+}
+
+cudaError_t launch_decode_fp4(int dtype, const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream) {
+    return dispatch_fp4(dtype, p.d.D, plan.nt, [&](auto l) { return l.launch(p, plan, stream); });
+}
+
+}  // namespace pa
