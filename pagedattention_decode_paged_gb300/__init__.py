@@ -525,98 +525,108 @@ def rope_table(max_position, rotary_dim, theta=10000.0, device=None) -> torch.Te
     return torch.cat((ang.cos(), ang.sin()), 1).float()
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor (None and raw addresses aside) lies on the current device,
-    the one the kernels are launched on."""
-    here = None
-    for t in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        dev = t.get_device()
-        if here is None:
-            here = torch.cuda.current_device() if dev >= 0 else -2
-        if dev != here:
-            raise ValueError(f"tensor on {t.device}: all tensors must be on the current CUDA device")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream() without building a Stream
 
 
-def _dense(what, t, dtype) -> None:
-    if t is not None and not isinstance(t, int) and not (t.dtype == dtype and t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor")
+def _launch_stream(stream, what, *tensors):
+    """The stream a call runs on, after checking that every tensor (None aside)
+    lies on the current device, the one the kernels are launched on."""
+    dev = tensors[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or any(t is not None and t.get_device() != dev for t in tensors):
+        raise ValueError(f"{what}: all tensors must be on the current CUDA device")
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _new_rows(what, x, like=None):
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(**tensors) -> None:
+    """Every tensor (given as name=(tensor, dtype)) is contiguous and of its dtype."""
+    for what, (t, dtype) in tensors.items():
+        if not (t.dtype == dtype and t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor")
+
+
+def _new_rows(what, x):
     """(batch, tokens, heads, head_dim, token stride) of new rows
     [B][heads][D] or [B][T][heads][D], possibly a slice of a packed
     projection output."""
-    shape, st = x.shape, x.stride()
-    if len(shape) == 3:
-        B, H, D = shape
-        T, stride, ok = 1, st[0], True
-    elif len(shape) == 4:
-        B, T, H, D = shape
-        stride = st[0] if T == 1 else st[1]
-        ok = T <= 1 or B <= 1 or st[0] == T * st[1]
+    if x.dim() == 4:
+        B, T, H, D = x.shape
+        sb, stride, sh, sd = x.stride()
+        if T == 1:
+            stride = sb
+        elif B > 1 and sb != T * stride:
+            raise ValueError(f"{what}: tokens must lie at one stride")
+    elif x.dim() == 3:
+        B, H, D = x.shape
+        stride, sh, sd = x.stride()
+        T = 1
     else:
         raise ValueError(f"{what} must be [B][heads][D] or [B][T][heads][D]")
     if B * T <= 1:
         stride = H * D
-    if not (ok and (D == 1 or st[-1] == 1) and (H == 1 or st[-2] == D)):
-        raise ValueError(f"{what}: the heads of a token must lie one after another, and tokens at one stride")
-    if like is not None and (B, T, D, x.dtype) != like:
-        raise ValueError(f"{what} does not match the keys in batch, tokens, head_dim or dtype")
+    if (sd != 1 and D != 1) or (sh != D and H != 1):
+        raise ValueError(f"{what}: the heads of a token must lie one after another")
     return B, T, H, D, stride
 
 
 def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scale, v_scale, block_table, positions,
                  counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps, block_size, num_blocks, block_stride,
                  err_word, stream, prepare):
+    dt = k_new.dtype
+    code = dtype_code(dt)
     B, T, Hkv, D, ks = _new_rows("k_new", k_new)
-    like = (B, T, D, k_new.dtype)
-    _, _, hv, _, vs = _new_rows("v_new", v_new, like)
-    if hv != Hkv:
-        raise ValueError("k_new and v_new differ in heads")
-    H, qs = Hkv, 0
+    *like, vs = _new_rows("v_new", v_new)
+    if like != [B, T, Hkv, D] or v_new.dtype != dt:
+        raise ValueError("k_new and v_new differ in shape or dtype")
+    H, qs, qp = Hkv, 0, None
     if q is not None:
-        _, _, H, _, qs = _new_rows("q", q, like)
-        if q_out is None or q_out.numel() != B * T * H * D:
-            raise ValueError("q_out must hold batch * tokens * heads * head_dim elements")
-        _dense("q_out", q_out, q.dtype)
-    _dense("block_table", block_table, torch.int32)
-    _dense("positions", positions, torch.int32)
-    _dense("counts", counts, torch.int32)
-    _dense("kv_scales", kv_scales, torch.uint8)
-    if block_table.shape[0] != B or positions.numel() != B or (counts is not None and counts.numel() != B):
-        raise ValueError("block_table, positions and counts must have one row per sequence")
+        bq, tq, H, dq, qs = _new_rows("q", q)
+        if (bq, tq, dq) != (B, T, D) or q.dtype != dt:
+            raise ValueError("q does not match the keys in batch, tokens, head_dim or dtype")
+        if q_out is None or q_out.numel() != B * T * H * D or q_out.dtype != dt or not q_out.is_contiguous():
+            raise ValueError(f"q_out must be contiguous, with batch * tokens * heads * head_dim elements of {dt}")
+        qp = q.data_ptr()
+    if not (block_table.dtype == torch.int32 and block_table.is_contiguous() and positions.dtype == torch.int32
+            and positions.is_contiguous()):
+        raise ValueError("block_table and positions must be contiguous torch.int32 tensors")
+    if block_table.shape[0] != B or positions.numel() != B:
+        raise ValueError("block_table and positions must have one row per sequence")
+    if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
+        raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
     fp4 = kv_scales is not None
-    if k_pool.dtype != v_pool.dtype or k_pool.dtype != (torch.uint8 if fp4 else k_new.dtype):
-        raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
-    shape = Shape(B, H, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(k_new.dtype))
-    rows = NewRows(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
-    keep = [shape, rows]
-    args = [ctypes.byref(shape)]
-    if name != "paged_kv_append_fp4":
-        R = 0
-        if cos_sin is not None:
-            _dense("cos_sin", cos_sin, torch.float32)
-            R = cos_sin.shape[1] if rotary_dim is None else rotary_dim
-            if cos_sin.shape[1] != R:
-                raise ValueError("cos_sin must be [max_position][rotary_dim]")
-        for what, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            _dense(what, w, k_new.dtype)
-            if w is not None and w.numel() != D:
-                raise ValueError(f"{what} must hold head_dim elements")
-        rope = Rope(_ptr(cos_sin), cos_sin.shape[0] if R else 0, R, int(interleaved), _ptr(q_norm), _ptr(k_norm), eps)
-        keep.append(rope)
-        args += [ctypes.byref(rope), ctypes.byref(rows), _ptr(q_out)]
-    else:
-        args.append(ctypes.byref(rows))
-    _same_device(k_new, v_new, q, q_out, k_pool, v_pool, kv_scales, block_table, positions, counts, cos_sin, q_norm,
-                 k_norm, err_word)
-    args += [k_pool.data_ptr(), v_pool.data_ptr()]
     if fp4:
-        args += [kv_scales.data_ptr(), float(k_scale), float(v_scale)]
-    args += [block_table.data_ptr(), positions.data_ptr(), _ptr(counts), _ptr(err_word), _stream(stream)]
-    return _issue(getattr(load(), name), tuple(args), name, prepare, tuple(keep))
+        _dense(kv_scales=(kv_scales, torch.uint8))
+    if k_pool.dtype != v_pool.dtype or k_pool.dtype != (torch.uint8 if fp4 else dt):
+        raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
+    R, most = 0, 0
+    if cos_sin is not None:
+        _dense(cos_sin=(cos_sin, torch.float32))
+        most, R = cos_sin.shape
+        if rotary_dim is not None and rotary_dim != R:
+            raise ValueError("cos_sin must be [max_position][rotary_dim]")
+    elif rotary_dim:
+        raise ValueError("a rotation needs cos_sin")
+    if q_norm is not None or k_norm is not None:
+        for what, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None and not (w.dtype == dt and w.is_contiguous() and w.numel() == D):
+                raise ValueError(f"{what} must hold head_dim contiguous elements of {dt}")
+    on = _launch_stream(stream, name, k_new, v_new, q, q_out, k_pool, v_pool, kv_scales, block_table, positions, counts,
+                        cos_sin, q_norm, k_norm, err_word)
+    shape = Shape(B, H, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, code)
+    rows = NewRows(qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
+    pools = (k_pool.data_ptr(), v_pool.data_ptr())
+    if fp4:
+        pools += (kv_scales.data_ptr(), k_scale, v_scale)
+    tail = (block_table.data_ptr(), positions.data_ptr(), _addr(counts), _addr(err_word), on)
+    if name == "paged_kv_append_fp4":
+        return _issue(load().paged_kv_append_fp4, (shape, rows, *pools, *tail), name, prepare)
+    rope = Rope(_addr(cos_sin), most, R, interleaved, _addr(q_norm), _addr(k_norm), eps)
+    return _issue(getattr(load(), name), (shape, rope, rows, _addr(q_out), *pools, *tail), name, prepare)
 
 
 def paged_kv_append_rope(q_out, q, k_new, v_new, k_pool, v_pool, block_table, positions, cos_sin, *,
@@ -658,22 +668,23 @@ def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, st
     """Values of tokens starts[b] + t, t < counts[b] (None: all T), of the 4-bit
     cache into k_out, v_out [B][T][Hkv][D]."""
     B, T, Hkv, D = k_out.shape
+    dt = k_out.dtype
     if v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out differ in shape")
-    for what, t, dt in (("k_out", k_out, k_out.dtype), ("v_out", v_out, k_out.dtype), ("kv_scales", kv_scales, torch.uint8),
-                        ("block_table", block_table, torch.int32), ("starts", starts, torch.int32),
-                        ("counts", counts, torch.int32)):
-        _dense(what, t, dt)
-    if block_table.shape[0] != B or starts.numel() != B or (counts is not None and counts.numel() != B):
-        raise ValueError("block_table, starts and counts must have one row per sequence")
+    _dense(k_out=(k_out, dt), v_out=(v_out, dt), kv_scales=(kv_scales, torch.uint8), block_table=(block_table, torch.int32),
+           starts=(starts, torch.int32))
+    if block_table.shape[0] != B or starts.numel() != B:
+        raise ValueError("block_table and starts must have one row per sequence")
+    if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
+        raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
         raise ValueError("the pools must be uint8")
-    _same_device(k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts, counts, err_word)
-    shape = Shape(B, Hkv, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(k_out.dtype))
-    args = (ctypes.byref(shape), k_out.data_ptr(), v_out.data_ptr(), T, k_pool.data_ptr(), v_pool.data_ptr(),
-            kv_scales.data_ptr(), float(k_scale), float(v_scale), block_table.data_ptr(), starts.data_ptr(),
-            _ptr(counts), _ptr(err_word), _stream(stream))
-    return _issue(load().paged_kv_gather_fp4, args, "paged_kv_gather_fp4", prepare, (shape,))
+    on = _launch_stream(stream, "paged_kv_gather_fp4", k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts,
+                        counts, err_word)
+    shape = Shape(B, Hkv, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(dt))
+    args = (shape, k_out.data_ptr(), v_out.data_ptr(), T, k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(),
+            k_scale, v_scale, block_table.data_ptr(), starts.data_ptr(), _addr(counts), _addr(err_word), on)
+    return _issue(load().paged_kv_gather_fp4, args, "paged_kv_gather_fp4", prepare)
 
 
 def paged_attention_fp4_workspace(shape: Shape) -> int:
@@ -698,19 +709,19 @@ def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, s
     """out[B][H][D] = attention of q over the valid tokens (the last `window` of
     them when positive) of a 4-bit cache; workspace from fp4_workspace_for."""
     B, H, D = q.shape
+    dt = q.dtype
     if out.shape != q.shape:
         raise ValueError("out and q differ in shape")
-    for what, t, dt in (("q", q, q.dtype), ("out", out, q.dtype), ("kv_scales", kv_scales, torch.uint8),
-                        ("block_table", block_table, torch.int32), ("seq_lens", seq_lens, torch.int32),
-                        ("workspace", workspace, torch.uint8)):
-        _dense(what, t, dt)
+    _dense(q=(q, dt), out=(out, dt), kv_scales=(kv_scales, torch.uint8), block_table=(block_table, torch.int32),
+           seq_lens=(seq_lens, torch.int32), workspace=(workspace, torch.uint8))
     if block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError("block_table and seq_lens must have one row per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
         raise ValueError("the pools must be uint8")
-    _same_device(q, out, k_pool, v_pool, kv_scales, block_table, seq_lens, workspace, err_word)
-    shape = Shape(B, H, num_kv_heads, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(q.dtype))
-    args = (ctypes.byref(shape), out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-            kv_scales.data_ptr(), float(k_scale), float(v_scale), block_table.data_ptr(), seq_lens.data_ptr(),
-            float(scale), int(window), workspace.data_ptr(), workspace.numel(), _ptr(err_word), _stream(stream))
-    return _issue(load().paged_attention_decode_fp4, args, "paged_attention_decode_fp4", prepare, (shape,))
+    on = _launch_stream(stream, "paged_attention_decode_fp4", q, out, k_pool, v_pool, kv_scales, block_table, seq_lens,
+                        workspace, err_word)
+    shape = Shape(B, H, num_kv_heads, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(dt))
+    args = (shape, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), k_scale,
+            v_scale, block_table.data_ptr(), seq_lens.data_ptr(), scale, window, workspace.data_ptr(), workspace.numel(),
+            _addr(err_word), on)
+    return _issue(load().paged_attention_decode_fp4, args, "paged_attention_decode_fp4", prepare)
