@@ -126,7 +126,7 @@ pa_status plan_of(const pa_shape *s, int32_t window, pa::Fp4Plan *plan) {
     int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
     if (window > 0 && (int64_t)window + 15 < max_len) max_len = (int64_t)window + 15;
     const cudaError_t e = pa::plan_decode_fp4(s->dtype, s->head_dim, s->num_heads / s->num_kv_heads, s->batch,
-                                              s->num_kv_heads, (max_len + 15) / 16, plan);
+                                              s->num_kv_heads, s->block_size, (max_len + 15) / 16, plan);
     if (e == cudaErrorInvalidValue) {
         (void)cudaGetLastError();   // a too-large shared-memory request is not sticky; drop it
         return PA_ERR_UNSUPPORTED;

@@ -55,10 +55,11 @@ struct Fp4Cfg {
     static constexpr int kHeads = NT * 8 / kParts;          // query heads per item
     static constexpr int kRow = D / 2;                      // code bytes of a row
     static constexpr int kScRow = D / 16;                   // scale bytes of a row
-    static constexpr int kCodes = 2 * kFp4Tile * kRow;      // K then V codes of a tile
-    static constexpr int kScales = 2 * kFp4Tile * kScRow;
+    static constexpr int kHalf = kFp4Tile * kRow;           // K (or V) codes of a tile
+    static constexpr int kScHalf = kFp4Tile * kScRow;
+    static constexpr int kStage = 2 * (kHalf + kScHalf);    // K codes, V codes, K scales, V scales
     static constexpr int kStages = 4;
-    static constexpr int kWarpRing = kStages * (kCodes + kScales);
+    static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
     static constexpr int kCtasPerSm = NT * D <= 128 ? 2 : 1;
     // the last record of a warp reuses its own ring
@@ -67,8 +68,17 @@ struct Fp4Cfg {
     static size_t bytes(int batch) { return kFixed + ((size_t)2 * batch + 1) * 4; }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// `bytes` of the source, zeros behind them
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
+    if constexpr (N == 16) cp_async16(dst, src);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
@@ -106,7 +116,10 @@ __device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
     return v;
 }
 
-template <typename T, int D, int NT>
+// WHOLE: block_size is a multiple of the tile, so the 16 rows of a tile are
+// contiguous and one table entry serves them; else every row is looked up by
+// itself.  Either way a tile is a 16-byte asynchronous copy per lane and chunk.
+template <typename T, int D, int NT, bool WHOLE>
 __global__ void __launch_bounds__(kFp4Threads, (Fp4Cfg<T, D, NT>::kCtasPerSm))
 decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) {
     using C = Fp4Cfg<T, D, NT>;
@@ -147,59 +160,85 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     T *out = reinterpret_cast<T *>(p.out);
 
     // ---- producer side -------------------------------------------------------
-    // Lane l looks up the block of tile row l % 16, one tile ahead; it copies
-    // that row's K (l < 16) or V scales, and the code rows of its chunk place.
+    // Table entries are looked up ahead, so that a tile's copies never wait for
+    // them: WHOLE, of a batch of up to 32 tiles of an item, lane i keeping the
+    // offsets of the i-th; else of one tile, lane l of its row l % 16.
     TileCursor pc = {};
-    int32_t pt = w0;                           // next tile to fetch
-    int32_t p_tok = 0;                         // its first token
-    int64_t p_blk = -1;
-    int p_slot = 0;
-    bool p_need = false;
-    uint32_t bad_bits = 0;                     // per ring stage: a needed table entry is bad
-    auto look_up = [&]() {                     // of tile pt under cursor pc
+    int32_t pt = w0;                           // first tile of the batch
+    int p_i = 0, p_left = 0;                   // the next tile in it, tiles left in it
+    int64_t p_code = 0, p_scale = 0;           // byte offsets of K's codes and scales (the row's if not WHOLE, -1: none)
+    uint32_t p_bad = 0;                        // tiles (rows) whose entry is outside the pool
+    uint32_t bad_bits = 0;                     // ring stages whose tile had a bad table entry
+    const int64_t v_scale_off = (int64_t)p.Hkv * p.bs * C::kScRow;
+    auto look_up = [&]() {                     // the batch from tile pt under cursor pc
         const int32_t L = lens[pc.b];
         const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
-        p_tok = t_win / kFp4Tile * kFp4Tile + pc.k * kFp4Tile;
-        const int32_t tok = p_tok + (lane & 15);
-        p_need = tok >= t_win && tok < L;
-        p_blk = -1;
-        if (p_need) {
-            const int32_t j = p.bs_shift >= 0 ? tok >> p.bs_shift : tok / p.bs;
-            p_slot = tok - j * p.bs;
-            p_blk = __ldg(p.block_table + (int64_t)pc.b * p.MB + j);
-        }
-    };
-    auto fetch = [&](int stage) {              // tile pt into `stage`, then step to the next one
-        const bool ok = p_need && p_blk >= 0 && p_blk < p.num_blocks;
-        const bool bad = p_need && !ok;
-        if (__any_sync(0xffffffffu, bad)) {
-            bad_bits |= 1u << stage;
-            if (bad && lane < 16) report(p.err_word, PA_DEVERR_BAD_BLOCK);
-        } else {
-            bad_bits &= ~(1u << stage);
-        }
+        const int32_t base = t_win / kFp4Tile * kFp4Tile + pc.k * kFp4Tile;
         const int hk = units_per_kv == 1 ? pc.it : pc.it / units_per_kv;
-        const int64_t row = (int64_t)hk * p.bs + p_slot;
-        const int64_t off = ok ? p_blk * p.block_stride_bytes + row * C::kRow : -1;
-        const uint32_t codes = ring + stage * (C::kCodes + C::kScales);
-        {
-            const int half = lane >> 4;
-            const int64_t so = ok ? ((p_blk * 2 + half) * p.Hkv * p.bs + row) * C::kScRow : 0;
-            cp_async_small<C::kScRow>(codes + C::kCodes + lane * C::kScRow, fp.scales + so, ok ? C::kScRow : 0);
+        p_i = 0;
+        p_left = WHOLE ? min(min(32, pc.n - pc.k), w1 - pt) : 1;
+        const int32_t tok = base + (WHOLE ? lane * kFp4Tile : (lane & 15));
+        const bool need = WHOLE ? lane < p_left : tok >= t_win && tok < L;
+        int64_t blk = 0;
+        int slot = 0;
+        if (need) {
+            const int32_t j = p.bs_shift >= 0 ? tok >> p.bs_shift : tok / p.bs;
+            slot = tok - j * p.bs;
+            blk = __ldg(p.block_table + (int64_t)pc.b * p.MB + j);
         }
-        constexpr int CH = C::kRow / 16;       // 16-byte chunks per row
+        const bool bad = blk < 0 || blk >= p.num_blocks;
+        if (bad && (WHOLE || lane < 16)) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+        p_bad = __ballot_sync(0xffffffffu, bad);
+        if (bad) blk = 0;                      // the copies stay inside the pool; the item's output will be zeros
+        const int64_t row = (int64_t)hk * p.bs + slot;
+        p_code = blk * p.block_stride_bytes + row * C::kRow;
+        p_scale = (blk * 2 * p.Hkv * p.bs + row) * C::kScRow;
+        if (!WHOLE && !need) p_code = -1;
+    };
+    constexpr int CH = C::kRow / 16;           // 16-byte chunks per row
+    constexpr int RS = 32 / CH;                // rows per copy instruction
+    const int f_r = lane / CH, f_c = lane % CH;
+    const uint32_t f_dst = f_r * C::kRow + swizzle<D>(f_r, f_c) * 16;
+    // RS rows on, the swizzle is the same, but for D 256 (4 rows a copy) its 4s bit
+    static_assert(RS % 8 == 0 || (D == 256 && RS == 4), "");
+    const uint32_t f_sdst = 2 * C::kHalf + lane * C::kScRow;
+    const int64_t f_soff = (lane & 15) * C::kScRow + (lane >> 4) * v_scale_off;
+    auto fetch = [&](uint32_t slot, int stage) {   // the next tile into the ring
+        if constexpr (WHOLE) {
+            const int64_t off = __shfl_sync(0xffffffffu, p_code, p_i) + f_r * C::kRow + f_c * 16;
+            const int64_t so = __shfl_sync(0xffffffffu, p_scale, p_i) + f_soff;
+            cp_async_small<C::kScRow>(slot + f_sdst, fp.scales + so);
+            const char *ks = p.k_pool + off, *vs = p.v_pool + off;
 #pragma unroll
-        for (int i = 0; i < kFp4Tile * CH / 32; ++i) {
-            const int r = (i * 32 + lane) / CH, c = lane % CH;
-            const int64_t ro = __shfl_sync(0xffffffffu, off, r);
-            const int64_t so = ro < 0 ? 0 : ro + c * 16;
-            const uint32_t dst = codes + r * C::kRow + swizzle<D>(r, c) * 16;
-            cp_async16(dst, p.k_pool + so, ro < 0 ? 0 : 16);
-            cp_async16(dst + kFp4Tile * C::kRow, p.v_pool + so, ro < 0 ? 0 : 16);
+            for (int i = 0; i < 16 / RS; ++i) {
+                const uint32_t dst = slot + (D == 256 && (i & 1) ? f_dst ^ 64u : f_dst) + i * RS * C::kRow;
+                cp_async16(dst, ks + i * RS * C::kRow);
+                cp_async16(dst + C::kHalf, vs + i * RS * C::kRow);
+            }
+            if (p_bad != 0 && ((p_bad >> p_i) & 1u)) bad_bits |= 1u << stage;
+        } else {
+            const bool ok = p_code >= 0;
+            const int64_t so = ok ? p_scale + (lane >> 4) * v_scale_off : 0;
+            cp_async_small<C::kScRow>(slot + f_sdst, fp.scales + so, ok ? C::kScRow : 0);
+#pragma unroll
+            for (int i = 0; i < 16 / RS; ++i) {
+                const int r = i * RS + f_r;
+                const int64_t ro = __shfl_sync(0xffffffffu, p_code, r);
+                const int64_t off = ro < 0 ? 0 : ro + f_c * 16;
+                const uint32_t dst = slot + r * C::kRow + swizzle<D>(r, f_c) * 16;
+                cp_async16(dst, p.k_pool + off, ro < 0 ? 0 : 16);
+                cp_async16(dst + C::kHalf, p.v_pool + off, ro < 0 ? 0 : 16);
+            }
+            if (p_bad != 0) bad_bits |= 1u << stage;
         }
-        if (++pt < w1) {
-            pc.next(pre, items_per_seq);
-            look_up();
+        ++p_i;
+        if (--p_left == 0) {
+            pt += p_i;
+            if (pt < w1) {
+                pc.k += p_i - 1;
+                pc.next(pre, items_per_seq);
+                look_up();
+            }
         }
     };
 
@@ -255,8 +294,10 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         }
     };
 
-    auto tile = [&](uint32_t codes, int32_t tok0, int32_t lo, int32_t hi) {
-        const uint32_t sc = codes + C::kCodes;
+    // with_edge: some rows lie outside [lo, hi) (the first and last tiles of an item)
+    auto tile = [&](auto with_edge, uint32_t codes, int32_t tok0, int32_t lo, int32_t hi) {
+        constexpr bool edge = decltype(with_edge)::value;
+        const uint32_t sc = codes + 2 * C::kHalf;
         const int rk = tau<D>(gid);
         // K rows rk and rk + 8 of this lane, and their scales
         uint32_t kw[2][KW], ks[2][(KW + 1) / 2];
@@ -266,10 +307,8 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             if constexpr (D == 256) {
                 lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig) * 16, kw[r]);
                 lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig + 1) * 16, kw[r] + 4);
-            } else if constexpr (D == 128) {
-                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, tig) * 16, kw[r]);
             } else {
-                lds_words<2>(codes + row * C::kRow + tig * 8, kw[r]);
+                lds_words<KW>(codes + row * C::kRow + (D == 128 ? swizzle<D>(row, tig) * 16 : tig * 8), kw[r]);
             }
             const uint32_t s = lds_bytes<KW / 2>(sc + row * C::kScRow + tig * (KW / 2));
 #pragma unroll
@@ -294,28 +333,43 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             }
         }
 
-        // scores in the log2 domain; rows outside [lo, hi) weigh nothing
-        const bool in0 = tok0 + rk >= lo && tok0 + rk < hi, in1 = tok0 + rk + 8 >= lo && tok0 + rk + 8 < hi;
-        bool over = false;
+        // scores in the log2 domain, relative to the columns' references; rows
+        // outside weigh nothing
+        const bool out0 = tok0 + rk < lo || tok0 + rk >= hi, out1 = tok0 + rk + 8 < lo || tok0 + rk + 8 >= hi;
+        float x[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (P == 2) c[nt][i] += __shfl_xor_sync(0xffffffffu, c[nt][i], 2);
-                c[nt][i] = (i < 2 ? in0 : in1) ? c[nt][i] * cs[nt][i & 1] : -INFINITY;
-                over |= c[nt][i] > m[nt][i & 1] + 8.f;
+                x[nt][i] = fmaf(c[nt][i], cs[nt][i & 1], -m[nt][i & 1]);
             }
+        if constexpr (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < 2 ? out0 : out1) x[nt][i] = -INFINITY;
         }
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) over = over || x[nt][i] > 8.f;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = fmaxf(m[nt][j], fmaxf(c[nt][j], c[nt][j + 2]));
+                    const float y0 = edge && out0 ? -INFINITY : c[nt][j] * cs[nt][j];
+                    const float y1 = edge && out1 ? -INFINITY : c[nt][j + 2] * cs[nt][j];
+                    float mx = fmaxf(m[nt][j], fmaxf(y0, y1));
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
                     const float f = merge_weight(m[nt][j], mx);
                     m[nt][j] = mx;
+                    x[nt][j] = y0 - mx;
+                    x[nt][j + 2] = y1 - mx;
                     l[nt][j] *= f;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -330,7 +384,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = ex2_approx(c[nt][i] - m[nt][i & 1]);
+                w[i] = ex2_approx(x[nt][i]);
                 l[nt][i & 1] += w[i];
                 if (P == 2 && tig >= 2) w[i] -= __half2float(__float2half_rn(w[i]));
             }
@@ -340,7 +394,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 
         // V rows of this lane's token pairs (t0, t1) and (t0 + 8, t1 + 8)
         const int t0 = tau<D>(2 * tig), t1 = tau<D>(2 * tig + 1);
-        const uint32_t vc = codes + kFp4Tile * C::kRow, vs = sc + kFp4Tile * C::kScRow;
+        const uint32_t vc = codes + C::kHalf, vs = sc + C::kScHalf;
         uint32_t vw[4][VW], ss[2][(VW + 1) / 2];
         constexpr int VB = VW == 4 ? 2 : 1;    // scale bytes per lane and row
         uint32_t sb[4];
@@ -350,6 +404,13 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             const int byte = gid * (D / 16);   // of the row
             lds_words<VW>(vc + row * C::kRow + swizzle<D>(row, byte / 16) * 16 + byte % 16, vw[i]);
             sb[i] = lds_bytes<VB>(vs + row * C::kScRow + (D == 64 ? gid / 2 : gid * VB));
+        }
+        if constexpr (edge) {                  // a slot nobody wrote may hold a NaN scale, which a weight of 0 would keep
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int32_t tok = tok0 + (i & 1 ? t1 : t0) + 8 * (i >> 1);
+                if (tok < lo || tok >= hi) sb[i] = 0;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -426,47 +487,50 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         TileCursor cc = pc;
         look_up();
 #pragma unroll 1
-        for (int s = 0; s < S - 1; ++s) {
-            if (pt < w1) fetch(s);
+        for (int i = 0; i < S - 1; ++i) {
+            if (p_left > 0) fetch(ring + i * C::kStage, i);
             cp_async_commit();
         }
-        bool fresh = true, bad = false;
-        int32_t lo = 0, hi = 0, base = 0;
+        int32_t t = w0;
         int stage = 0;
-        for (int32_t t = w0; t < w1; ++t) {
-            if (fresh) {
-                load_q(cc.b, cc.it);
-                hi = lens[cc.b];
-                lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
-                base = lo / kFp4Tile * kFp4Tile;
-                fresh = bad = false;
-            }
-            cp_async_wait<S - 2>();
-            __syncwarp();                      // every lane's copies have landed, and the tile before is read
-            bad |= (bad_bits >> stage) & 1u;
-            if (pt < w1) fetch(stage == 0 ? S - 1 : stage - 1);
-            cp_async_commit();
-            tile(ring + stage * (C::kCodes + C::kScales), base + cc.k * kFp4Tile, lo, hi);
-            stage = stage + 1 == S ? 0 : stage + 1;
-            const bool item_end = cc.k + 1 == cc.n, slice_end = t + 1 == w1;
-            if (item_end || slice_end) {
-                const bool whole = item_end && cc.first >= w0;
-                const int which = slice_end ? 1 : 0;   // a part that ends inside the slice began before it
-                if (which == 1) {
-                    cp_async_wait<0>();
-                    __syncwarp();              // the ring is free for the record
+        while (true) {                         // items (or parts) of this warp's run
+            load_q(cc.b, cc.it);
+            const int32_t hi = lens[cc.b], lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
+            int32_t tok0 = lo / kFp4Tile * kFp4Tile + cc.k * kFp4Tile;
+            const int32_t end = min(w1, cc.first + cc.n);
+            bool bad = false;
+            for (; t < end; ++t, tok0 += kFp4Tile) {
+                cp_async_wait<S - 2>();
+                __syncwarp();                  // every lane's copies have landed, and the tile before is read
+                if (bad_bits != 0) {
+                    bad |= (bad_bits >> stage) & 1u;
+                    bad_bits &= ~(1u << stage);
                 }
-                finish(cc, whole, bad, which ? last_rec : first_rec);
-                if (!whole && lane == 0) {
-                    const int r = 2 * warp + which;
-                    rec_first[r] = cc.first;
-                    rec_n[r] = cc.n;
-                    rec_b[r] = cc.b;
-                    rec_it[r] = cc.it;
-                }
-                fresh = true;
+                const int free_stage = stage == 0 ? S - 1 : stage - 1;
+                if (p_left > 0) fetch(ring + free_stage * C::kStage, free_stage);
+                cp_async_commit();
+                const uint32_t codes = ring + stage * C::kStage;
+                if (tok0 >= lo && tok0 + kFp4Tile <= hi) tile(Fp4Bool<false>{}, codes, tok0, lo, hi);
+                else tile(Fp4Bool<true>{}, codes, tok0, lo, hi);
+                stage = stage + 1 == S ? 0 : stage + 1;
             }
-            if (!slice_end) cc.next(pre, items_per_seq);
+            const bool whole = cc.first >= w0 && cc.first + cc.n <= w1, last = t == w1;
+            if (last) {
+                cp_async_wait<0>();
+                __syncwarp();                  // the ring is free for the record
+            }
+            // a part that ends inside the run began before it
+            finish(cc, whole, bad, last ? last_rec : first_rec);
+            if (!whole && lane == 0) {
+                const int r = 2 * warp + (last ? 1 : 0);
+                rec_first[r] = cc.first;
+                rec_n[r] = cc.n;
+                rec_b[r] = cc.b;
+                rec_it[r] = cc.it;
+            }
+            if (last) break;
+            cc.k = cc.n - 1;
+            cc.next(pre, items_per_seq);
         }
     }
     __syncthreads();
@@ -589,14 +653,14 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 // host side
 // ---------------------------------------------------------------------------
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool WHOLE>
 struct Fp4Launch {
     using C = Fp4Cfg<T, D, NT>;
     static std::atomic<int> configured[64];
     static int64_t occupancy[64][2];
 
     static cudaError_t plan(int batch, int64_t max_tiles, Fp4Plan *plan) {
-        auto kern = decode_fp4_kernel<T, D, NT>;
+        auto kern = decode_fp4_kernel<T, D, NT, WHOLE>;
         const size_t smem = C::bytes(batch);
         cudaError_t e = ensure_smem_limit(kern, smem, configured);
         if (e != cudaSuccess) return e;
@@ -614,35 +678,39 @@ struct Fp4Launch {
     }
     static cudaError_t launch(const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream) {
         if (plan.grid <= 0) return cudaErrorInvalidValue;
-        return launch_clustered(decode_fp4_kernel<T, D, NT>, plan.grid, kFp4Threads, plan.smem, 1, stream, p,
+        return launch_clustered(decode_fp4_kernel<T, D, NT, WHOLE>, plan.grid, kFp4Threads, plan.smem, 1, stream, p,
                                 plan.units_per_kv);
     }
 };
-template <typename T, int D, int NT> std::atomic<int> Fp4Launch<T, D, NT>::configured[64];
-template <typename T, int D, int NT> int64_t Fp4Launch<T, D, NT>::occupancy[64][2] = {};
+template <typename T, int D, int NT, bool WHOLE> std::atomic<int> Fp4Launch<T, D, NT, WHOLE>::configured[64];
+template <typename T, int D, int NT, bool WHOLE> int64_t Fp4Launch<T, D, NT, WHOLE>::occupancy[64][2] = {};
 
-// f(Fp4Launch<T, D, NT>{}) for the shape's instantiation.
+// f(Fp4Launch<...>{}) for the shape's instantiation.
 template <typename T, typename F>
-static cudaError_t dispatch_fp4_typed(int head_dim, int nt, F &&f) {
+static cudaError_t dispatch_fp4_typed(int head_dim, int nt, bool whole, F &&f) {
     switch (head_dim) {
-        case 64: return nt == 2 ? f(Fp4Launch<T, 64, 2>{}) : f(Fp4Launch<T, 64, 1>{});
-        case 128: return nt == 2 ? f(Fp4Launch<T, 128, 2>{}) : f(Fp4Launch<T, 128, 1>{});
-        case 256: return f(Fp4Launch<T, 256, 1>{});
+        case 64:
+            if (whole) return nt == 2 ? f(Fp4Launch<T, 64, 2, true>{}) : f(Fp4Launch<T, 64, 1, true>{});
+            return nt == 2 ? f(Fp4Launch<T, 64, 2, false>{}) : f(Fp4Launch<T, 64, 1, false>{});
+        case 128:
+            if (whole) return nt == 2 ? f(Fp4Launch<T, 128, 2, true>{}) : f(Fp4Launch<T, 128, 1, true>{});
+            return nt == 2 ? f(Fp4Launch<T, 128, 2, false>{}) : f(Fp4Launch<T, 128, 1, false>{});
+        case 256: return whole ? f(Fp4Launch<T, 256, 1, true>{}) : f(Fp4Launch<T, 256, 1, false>{});
     }
     return cudaErrorInvalidValue;
 }
 template <typename F>
-static cudaError_t dispatch_fp4(int dtype, int head_dim, int nt, F &&f) {
+static cudaError_t dispatch_fp4(int dtype, int head_dim, int nt, bool whole, F &&f) {
     switch (dtype) {
-        case PA_F32: return dispatch_fp4_typed<float>(head_dim, nt, f);
-        case PA_F16: return dispatch_fp4_typed<__half>(head_dim, nt, f);
-        case PA_BF16: return dispatch_fp4_typed<__nv_bfloat16>(head_dim, nt, f);
+        case PA_F32: return dispatch_fp4_typed<float>(head_dim, nt, whole, f);
+        case PA_F16: return dispatch_fp4_typed<__half>(head_dim, nt, whole, f);
+        case PA_BF16: return dispatch_fp4_typed<__nv_bfloat16>(head_dim, nt, whole, f);
     }
     return cudaErrorInvalidValue;
 }
 
-cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int64_t max_tiles_per_item,
-                            Fp4Plan *plan) {
+cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int block_size,
+                            int64_t max_tiles_per_item, Fp4Plan *plan) {
     // one 8-column tile per item, or two when the kv head has more columns:
     // the conversion of a tile, not its MMAs, is what an item costs
     const int columns = group * (dtype == PA_F32 ? 2 : 1);
@@ -650,13 +718,14 @@ cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int k
     const int heads = plan->nt * 8 / (dtype == PA_F32 ? 2 : 1);
     plan->units_per_kv = (group + heads - 1) / heads;
     plan->items = (int64_t)batch * kv_heads * plan->units_per_kv;
+    plan->whole_tiles = block_size % kFp4Tile == 0;
     const int64_t total = plan->items * max_tiles_per_item;
     if (total >= (int64_t)INT32_MAX / 2) return cudaErrorInvalidValue;
-    return dispatch_fp4(dtype, head_dim, plan->nt, [&](auto l) { return l.plan(batch, total, plan); });
+    return dispatch_fp4(dtype, head_dim, plan->nt, plan->whole_tiles, [&](auto l) { return l.plan(batch, total, plan); });
 }
 
 cudaError_t launch_decode_fp4(int dtype, const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream) {
-    return dispatch_fp4(dtype, p.d.D, plan.nt, [&](auto l) { return l.launch(p, plan, stream); });
+    return dispatch_fp4(dtype, p.d.D, plan.nt, plan.whole_tiles, [&](auto l) { return l.launch(p, plan, stream); });
 }
 
 }  // namespace pa

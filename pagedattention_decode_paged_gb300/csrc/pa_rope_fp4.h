@@ -74,10 +74,11 @@ struct Fp4Plan {
     int rec_floats = 0;
     int units_per_kv = 1;      // items per (sequence, kv head)
     int nt = 1;                // 8-column MMA tiles per item
+    bool whole_tiles = false;  // the rows of a tile are contiguous
     int64_t items = 0;
 };
-cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int64_t max_tiles_per_item,
-                            Fp4Plan *plan);
+cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int block_size,
+                            int64_t max_tiles_per_item, Fp4Plan *plan);
 cudaError_t launch_decode_fp4(int dtype, const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream);
 
 }  // namespace pa
