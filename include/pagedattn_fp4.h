@@ -107,8 +107,8 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
  * ZERO-FILLED before its first use; every call leaves its counters at zero;
  * calls that may overlap on the GPU (streams, captured graphs) need
  * workspaces of their own.  The size depends on the shape and on the current
- * device and is enough for every window; 0 for a shape this entry point
- * rejects (the schedule keeps two int32 per sequence in shared memory and
+ * device; a workspace may serve other shapes too, on the same device, if it is
+ * large enough for them.  0 for a shape this entry point rejects (the schedule keeps two int32 per sequence in shared memory and
  * counts tiles in int32: PA_ERR_UNSUPPORTED).  (The workspace query has no
  * counterpart on the pages.)
  */

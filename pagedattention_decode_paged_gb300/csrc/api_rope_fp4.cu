@@ -122,9 +122,8 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
 }
 
 // The decode schedule for `s` on the current device.
-pa_status plan_of(const pa_shape *s, int32_t window, pa::Fp4Plan *plan) {
-    int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
-    if (window > 0 && (int64_t)window + 15 < max_len) max_len = (int64_t)window + 15;
+pa_status plan_of(const pa_shape *s, pa::Fp4Plan *plan) {
+    const int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
     const cudaError_t e = pa::plan_decode_fp4(s->dtype, s->head_dim, s->num_heads / s->num_kv_heads, s->batch,
                                               s->num_kv_heads, s->block_size, (max_len + 15) / 16, plan);
     if (e == cudaErrorInvalidValue) {
@@ -135,13 +134,16 @@ pa_status plan_of(const pa_shape *s, int32_t window, pa::Fp4Plan *plan) {
     return plan->grid > 0 ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
+// Records, group counters, then one counter per item.  Only the last part's
+// size depends on the shape: a workspace serves every shape that it is large
+// enough for.
 struct WsLayout {
     size_t group_counters, counters, total;
 };
 WsLayout ws_of(const pa::Fp4Plan &plan) {
     WsLayout w;
-    w.group_counters = (size_t)4 * plan.grid * plan.rec_floats * 4;
-    w.counters = w.group_counters + (size_t)2 * plan.grid * 4;
+    w.group_counters = (size_t)4 * plan.max_grid * pa::kFp4RecFloats * 4;
+    w.counters = w.group_counters + (size_t)2 * plan.max_grid * 4;
     w.total = w.counters + (size_t)plan.items * 4;
     return w;
 }
@@ -219,7 +221,7 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
 size_t paged_attention_fp4_workspace(const pa_shape *shape) {
     if (check_fp4_shape(shape, true) != PA_OK || shape->batch == 0) return 0;
     pa::Fp4Plan plan;
-    if (plan_of(shape, 0, &plan) != PA_OK) return 0;
+    if (plan_of(shape, &plan) != PA_OK) return 0;
     return ws_of(plan).total;
 }
 
@@ -241,7 +243,7 @@ pa_status paged_attention_decode_fp4(const pa_shape *shape, void *out, const voi
         !aligned16(workspace))
         return PA_ERR_MISALIGNED;
     pa::Fp4Plan plan;
-    st = plan_of(shape, window, &plan);
+    st = plan_of(shape, &plan);
     if (st != PA_OK) return st;
     const WsLayout w = ws_of(plan);
     if (workspace_bytes < w.total) return PA_ERR_WORKSPACE;
@@ -271,7 +273,7 @@ pa_status paged_attention_decode_fp4(const pa_shape *shape, void *out, const voi
     p.records = reinterpret_cast<float *>(ws);
     p.group_counters = reinterpret_cast<int32_t *>(ws + w.group_counters);
     p.counters = reinterpret_cast<int32_t *>(ws + w.counters);
-    p.rec_floats = plan.rec_floats;
+    p.rec_floats = pa::kFp4RecFloats;
     f.scales = kv_scales;
     f.v_g = v_scale;
     return pa::launch_decode_fp4(shape->dtype, f, plan, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess

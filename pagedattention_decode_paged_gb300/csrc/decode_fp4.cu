@@ -37,12 +37,11 @@
 
 namespace pa {
 
-constexpr int kFp4Warps = 8;
-constexpr int kFp4Threads = kFp4Warps * 32;
 constexpr int kFp4Tile = 16;
 constexpr int kFp4MinTiles = 2;    // tiles per warp below which fewer CTAs share the work
+constexpr int kFp4OwnTiles = 8;    // tiles per warp up to which a CTA of its own serves an item
 constexpr int kFp4Flat = 24;       // sharers of an item up to which one level of merging serves
-constexpr int kFp4Group = 16;      // sharers per first-level group above that
+constexpr int kFp4Group = 12;      // sharers per first-level group above that
 
 template <bool V>
 struct Fp4Bool {
@@ -58,13 +57,15 @@ struct Fp4Cfg {
     static constexpr int kHalf = kFp4Tile * kRow;           // K (or V) codes of a tile
     static constexpr int kScHalf = kFp4Tile * kScRow;
     static constexpr int kStage = 2 * (kHalf + kScHalf);    // K codes, V codes, K scales, V scales
-    static constexpr int kStages = 4;
+    static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;
     static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
-    static constexpr int kCtasPerSm = NT * D <= 128 ? 2 : 1;
+    // one CTA per SM: of 16 warps where a thread gets along with 128 registers
+    static constexpr int kWarps = NT * D <= 128 ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
     // the last record of a warp reuses its own ring
-    static_assert(kWarpRing >= kRec * 4, "a record fits the ring");
-    static constexpr size_t kFixed = (size_t)kFp4Warps * (kWarpRing + kRec * 4);
+    static_assert(kWarpRing >= kRec * 4 && kRec <= kFp4RecFloats, "a record fits the ring and the workspace");
+    static constexpr size_t kFixed = (size_t)kWarps * (kWarpRing + kRec * 4);
     static size_t bytes(int batch) { return kFixed + ((size_t)2 * batch + 1) * 4; }
 };
 
@@ -120,23 +121,23 @@ __device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
 // contiguous and one table entry serves them; else every row is looked up by
 // itself.  Either way a tile is a 16-byte asynchronous copy per lane and chunk.
 template <typename T, int D, int NT, bool WHOLE>
-__global__ void __launch_bounds__(kFp4Threads, (Fp4Cfg<T, D, NT>::kCtasPerSm))
+__global__ void __launch_bounds__((Fp4Cfg<T, D, NT>::kThreads), 1)
 decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) {
     using C = Fp4Cfg<T, D, NT>;
-    constexpr int P = C::kParts, HP = C::kHeads, S = C::kStages;
+    constexpr int P = C::kParts, HP = C::kHeads, S = C::kStages, W = C::kWarps;
     constexpr int KW = D / 32;                 // words of a K row per lane
     constexpr int VW = D / 64;                 // words of a V row per lane
     constexpr int MT = D / 16;                 // 16-row tiles of O^T
     const DecodeParams &p = fp.d;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ int32_t scan_tmp[kFp4Warps];
-    __shared__ int32_t rec_first[2 * kFp4Warps], rec_n[2 * kFp4Warps], rec_b[2 * kFp4Warps], rec_it[2 * kFp4Warps];
-    __shared__ int32_t last_flag;
+    __shared__ int32_t scan_tmp[W];
+    __shared__ int32_t rec_first[2 * W], rec_n[2 * W], rec_b[2 * W], rec_it[2 * W];
+    __shared__ int32_t arrived[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     unsigned char *ring_p = smem + (size_t)warp * C::kWarpRing;
     const uint32_t ring = smem_u32(ring_p);
-    float *first_rec = reinterpret_cast<float *>(smem + (size_t)kFp4Warps * C::kWarpRing) + (size_t)warp * C::kRec;
+    float *first_rec = reinterpret_cast<float *>(smem + (size_t)W * C::kWarpRing) + (size_t)warp * C::kRec;
     float *last_rec = reinterpret_cast<float *>(ring_p);
     int32_t *pre = reinterpret_cast<int32_t *>(smem + C::kFixed);
     int32_t *lens = pre + p.B + 1;
@@ -147,13 +148,30 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     build_schedule<kFp4Tile>(p, items_per_seq, kFp4Tile, pre, lens, scan_tmp);
     zero_empty_sequences<T>(p, pre);
     const int32_t Tn = pre[p.B];
-    // CTAs that work: all, unless that leaves their warps less than kFp4MinTiles tiles
-    const int want = (Tn + kFp4Warps * kFp4MinTiles - 1) / (kFp4Warps * kFp4MinTiles);
-    const int nC = min((int)gridDim.x, want);
+    // Few, short items: one to a CTA, so that nothing is merged between CTAs.
+    // Else an equal run of tiles to every CTA (fewer CTAs when their warps would
+    // have less than kFp4MinTiles).
     const int cta = blockIdx.x;
-    if (cta >= nC) return;
-    const int32_t c0 = slice_start(cta, Tn, nC), c1 = slice_start(cta + 1, Tn, nC);
-    const int32_t w0 = c0 + slice_start(warp, c1 - c0, kFp4Warps), w1 = c0 + slice_start(warp + 1, c1 - c0, kFp4Warps);
+    int own = p.B * items_per_seq <= (int)gridDim.x;
+    if (own) {
+        bool big = false;
+        for (int b = threadIdx.x; b < p.B; b += C::kThreads)
+            big |= pre[b + 1] - pre[b] > W * kFp4OwnTiles * items_per_seq;
+        own = !__syncthreads_or(big);
+    }
+    const int nC = min((int)gridDim.x, (Tn + W * kFp4MinTiles - 1) / (W * kFp4MinTiles));
+    int32_t c0, c1;
+    if (own) {
+        const int b = min(cta / items_per_seq, p.B - 1), it = cta - b * items_per_seq;
+        const int32_t n = it < items_per_seq ? (pre[b + 1] - pre[b]) / items_per_seq : 0;
+        c0 = pre[b] + it * n;
+        c1 = c0 + n;
+    } else {
+        c0 = cta < nC ? slice_start(cta, Tn, nC) : 0;
+        c1 = cta < nC ? slice_start(cta + 1, Tn, nC) : 0;
+    }
+    if (c0 >= c1) return;
+    const int32_t w0 = c0 + slice_start(warp, c1 - c0, W), w1 = c0 + slice_start(warp + 1, c1 - c0, W);
     if (lane < 2) rec_first[2 * warp + lane] = -1;
 
     const int grp = p.H / p.Hkv;               // query heads per kv head
@@ -194,6 +212,13 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         p_code = blk * p.block_stride_bytes + row * C::kRow;
         p_scale = (blk * 2 * p.Hkv * p.bs + row) * C::kScRow;
         if (!WHOLE && !need) p_code = -1;
+        if (pc.k == 0) {                       // the item's queries, before its first tile is due
+            const char *q = reinterpret_cast<const char *>(p.q) +
+                            ((int64_t)pc.b * p.H + hk * grp + (pc.it - hk * units_per_kv) * HP) * D * sizeof(T);
+            const int heads = min(HP, grp - (pc.it - hk * units_per_kv) * HP);
+            for (int i = lane * 128; i < heads * D * (int)sizeof(T); i += 32 * 128)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+        }
     };
     constexpr int CH = C::kRow / 16;           // 16-byte chunks per row
     constexpr int RS = 32 / CH;                // rows per copy instruction
@@ -438,8 +463,22 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         }
     };
 
+    // A record's O lies as the lanes hold it, so that no store misses a bank: a
+    // slab is four elements of every lane.  Slab i of lane l (two parts: half the
+    // slabs each of lanes tig and tig + 2, which hold the same sums) is head
+    // head_of(i, l), elements dim_of(i, l)...
+    constexpr int SLABS = HP * D / 128;
+    auto slab_of = [](int i, int t) { return P == 2 ? i + (t >> 1) * SLABS : i; };   // (nt, j, v, quarter) of lane's i-th
+    auto head_of = [&](int i, int ln) {
+        const int s = slab_of(i, ln & 3);
+        return s / (4 * VW) * (8 / P) + (P == 2 ? 2 * (ln & 1) : 2 * (ln & 3)) + s / (2 * VW) % 2;
+    };
+    auto dim_of = [&](int i, int ln) {
+        const int s = slab_of(i, ln & 3);
+        return (ln >> 2) * (D / 8) + s / 2 % VW * 8 + s % 2 * 4;
+    };
     // The state of an item this warp has finished its part of: whole items to
-    // `out`, parts to a record (O [HP][D], m [HP], l [HP]; l < 0: bad table).
+    // `out`, parts to a record (O, m [HP], l [HP]; l < 0: bad table).
     auto finish = [&](const TileCursor &cc, bool whole, bool bad, float *rec) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -448,36 +487,50 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 #pragma unroll
                 for (int s = 4; s < 32; s <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], s);
             }
-            if (P == 2)
+            if constexpr (P == 2) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[nt][mt][i] += __shfl_xor_sync(0xffffffffu, o[nt][mt][i], 2);
+            }
         }
         const int hk = cc.it / units_per_kv, h0 = (cc.it - hk * units_per_kv) * HP;
         const bool writer = P == 1 || tig < 2;
+        if (!whole) {
+#pragma unroll
+            for (int s = 0; s < SLABS * P; ++s) {
+                const int nt = s / (4 * VW), j = s / (2 * VW) % 2, mt = s / 2 % VW * 4 + s % 2 * 2;
+                const float4 x = make_float4(o[nt][mt][j], o[nt][mt][j + 2], o[nt][mt + 1][j], o[nt][mt + 1][j + 2]);
+                if (P == 1 || (tig >> 1) == s / SLABS)
+                    *reinterpret_cast<float4 *>(rec + (s % SLABS) * 128 + lane * 4) = x;
+            }
+            if (gid == 0 && writer)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int col = nt * (8 / P) + 2 * tig + j;
+                        rec[HP * D + col] = m[nt][j];
+                        rec[HP * D + HP + col] = bad ? -1.f : l[nt][j];
+                    }
+            return;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int col = nt * (8 / P) + 2 * tig + j;
                 if (!writer || h0 + col >= grp) continue;
-                const float f = whole ? (bad ? 0.f : fp.v_g / l[nt][j]) : 1.f;
+                const float f = fp.v_g / l[nt][j];
 #pragma unroll
                 for (int v = 0; v < VW; ++v) {
                     float x[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        x[2 * k] = whole && bad ? 0.f : o[nt][4 * v + k][j] * f;
-                        x[2 * k + 1] = whole && bad ? 0.f : o[nt][4 * v + k][j + 2] * f;
+                        x[2 * k] = bad ? 0.f : o[nt][4 * v + k][j] * f;
+                        x[2 * k + 1] = bad ? 0.f : o[nt][4 * v + k][j + 2] * f;
                     }
-                    const int d = gid * (D / 8) + 8 * v;
-                    if (whole) store8(out + ((int64_t)cc.b * p.H + hk * grp + h0 + col) * D + d, x);
-                    else store8(rec + col * D + d, x);
-                }
-                if (!whole && gid == 0) {
-                    rec[HP * D + col] = m[nt][j];
-                    rec[HP * D + HP + col] = bad ? -1.f : l[nt][j];
+                    store8(out + ((int64_t)cc.b * p.H + hk * grp + h0 + col) * D + gid * (D / 8) + 8 * v, x);
                 }
             }
     };
@@ -536,116 +589,165 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __syncthreads();
 
     // ---- merges --------------------------------------------------------------
-    // The `n` records rec_at(0..n) of one item into its output, or into the
-    // record dst.  Records in the workspace were written by other CTAs: read at L2.
-    auto merge = [&](auto in_workspace, int n, auto rec_at, int b, int it, bool whole, float *dst) {
-        auto ld = [](const float *a) { return decltype(in_workspace)::value ? __ldcg(a) : *a; };
+    // Element i of a record (a lane's slab) merged over records [r0, r1) of one
+    // item: into the item's output, or into the record dst.  rec_at(r) may be
+    // null (no record).  Records in the workspace were written by other CTAs:
+    // read at L2.  The maximum of all records weighs them; their O is loaded
+    // eight at a time whatever the weights.
+    auto merge_element = [&](auto in_workspace, int i, int r0, int r1, auto rec_at, int b, int it, bool whole, float *dst) {
+        constexpr bool ws = decltype(in_workspace)::value;
+        auto ld = [](const float *a) { return ws ? __ldcg(a) : *a; };
+        const int ln = i & 31, h = head_of(i >> 5, ln);
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
-        const int heads = min(HP, grp - h0);
-        for (int i = threadIdx.x; i < heads * (D / 4); i += kFp4Threads) {
-            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
-            float M = -INFINITY;
-            bool bad = false;
-            for (int r = 0; r < n; ++r) {
-                const float *rec = rec_at(r);
-                M = fmaxf(M, ld(rec + HP * D + h));
-                bad |= ld(rec + HP * D + HP + h) < 0.f;
-            }
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-#pragma unroll 4
-            for (int r = 0; r < n; ++r) {
-                const float *rec = rec_at(r);
-                const float mr = ld(rec + HP * D + h);
-                const float w = merge_weight(mr, M);
-                const float4 *ra = reinterpret_cast<const float4 *>(rec + h * D + d);
-                const float4 a = decltype(in_workspace)::value ? __ldcg(ra) : *ra;
-                sum = fmaf(ld(rec + HP * D + HP + h), w, sum);
-                acc.x = fmaf(a.x, w, acc.x);
-                acc.y = fmaf(a.y, w, acc.y);
-                acc.z = fmaf(a.z, w, acc.z);
-                acc.w = fmaf(a.w, w, acc.w);
-            }
-            if (whole) {
-                const float f = fp.v_g / sum;
-                T *row = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + d;
-                row[0] = Elem<T>::from_float(bad ? 0.f : acc.x * f);
-                row[1] = Elem<T>::from_float(bad ? 0.f : acc.y * f);
-                row[2] = Elem<T>::from_float(bad ? 0.f : acc.z * f);
-                row[3] = Elem<T>::from_float(bad ? 0.f : acc.w * f);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(dst + h * D + d), acc);
-                if (d == 0) {
-                    __stcg(dst + HP * D + h, M);
-                    __stcg(dst + HP * D + HP + h, bad ? -1.f : sum);
+        float M = -INFINITY, sum = 0.f;
+        bool bad = false;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = r0; r < r1; r += 8) {
+            float mr[8], lr[8];
+            float4 a[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float *rec = r + k < r1 ? rec_at(r + k) : nullptr;
+                mr[k] = -INFINITY;
+                lr[k] = 0.f;
+                a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (rec != nullptr) {
+                    mr[k] = ld(rec + HP * D + h);
+                    lr[k] = ld(rec + HP * D + HP + h);
+                    const float4 *ra = reinterpret_cast<const float4 *>(rec + i * 4);
+                    a[k] = ws ? __ldcg(ra) : *ra;
                 }
             }
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, mr[k]);
+            const float f = merge_weight(M, top);
+            M = top;
+            sum *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = merge_weight(mr[k], top);
+                bad |= lr[k] < 0.f;
+                sum = fmaf(lr[k], w, sum);
+                acc.x = fmaf(a[k].x, w, acc.x);
+                acc.y = fmaf(a[k].y, w, acc.y);
+                acc.z = fmaf(a[k].z, w, acc.z);
+                acc.w = fmaf(a[k].w, w, acc.w);
+            }
         }
-    };
-    constexpr Fp4Bool<false> here{};
-    constexpr Fp4Bool<true> workspace{};
-    auto smem_rec = [&](int r) -> const float * {
-        return (r & 1) ? reinterpret_cast<const float *>(smem + (size_t)(r >> 1) * C::kWarpRing)
-                       : reinterpret_cast<const float *>(smem + (size_t)kFp4Warps * C::kWarpRing) + (size_t)(r >> 1) * C::kRec;
+        if (!whole) {
+            __stcg(reinterpret_cast<float4 *>(dst + i * 4), acc);
+            if (dim_of(i >> 5, ln) == 0) {
+                __stcg(dst + HP * D + h, M);
+                __stcg(dst + HP * D + HP + h, bad ? -1.f : sum);
+            }
+        } else if (h0 + h < grp) {
+            const float f = fp.v_g / sum;
+            T *o4 = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + dim_of(i >> 5, ln);
+            const float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(o4) = y;
+            else *reinterpret_cast<uint2 *>(o4) = make_uint2(Elem<T>::pack2(y.x, y.y), Elem<T>::pack2(y.z, y.w));
+        }
     };
     // record `slot` of a CTA: 0 its first item, 1 its last one; 2 and 3 the
     // merged record of the group of sharers that record 0 or 1 heads
     auto global_rec = [&](int c, int slot) { return p.records + ((int64_t)c * 4 + slot) * p.rec_floats; };
-
-    int part0 = -1, part1 = -1;                // first records (in shared memory) of items shared with other CTAs
-    for (int r = 0; r < 2 * kFp4Warps;) {
-        if (rec_first[r] < 0) {
-            ++r;
-            continue;
-        }
-        const int r0 = r;
-        int idx[2 * kFp4Warps], n = 0;
-        for (; r < 2 * kFp4Warps && (rec_first[r] < 0 || rec_first[r] == rec_first[r0]); ++r)
-            if (rec_first[r] >= 0) idx[n++] = r;
-        const bool before = rec_first[r0] < c0, whole = !before && rec_first[r0] + rec_n[r0] <= c1;
-        if (!whole) (before ? part0 : part1) = r0;
-        merge(here, n, [&](int i) { return smem_rec(idx[i]); }, rec_b[r0], rec_it[r0], whole,
-              whole ? nullptr : global_rec(cta, before ? 0 : 1));
-    }
-    if (part0 < 0 && part1 < 0) return;
-    // all of this CTA's stores come before its count on a counter
-    auto arrive = [&](int32_t *counter, int sharers) {
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const bool last = atomicAdd(counter, 1) == sharers - 1;
-            last_flag = last;
-            if (last) *counter = 0;            // nobody else touches it again in this call
-        }
-        __syncthreads();
-        if (last_flag == 0) return false;
-        __threadfence();
-        return true;
+    auto smem_rec = [&](int r) -> const float * {
+        if (rec_first[r] < 0) return nullptr;
+        return (r & 1) ? reinterpret_cast<const float *>(smem + (size_t)(r >> 1) * C::kWarpRing)
+                       : reinterpret_cast<const float *>(smem + (size_t)W * C::kWarpRing) + (size_t)(r >> 1) * C::kRec;
     };
-#pragma unroll 1
-    for (int slot = 0; slot < 2; ++slot) {
-        const int r0 = slot ? part1 : part0;
+
+    // The CTA's records, in the items' order: lane r of every warp looks at
+    // record r; a run of records of one item starts where the item changes.
+    const int32_t mine = lane < 2 * W ? rec_first[lane] : -1;
+    const uint32_t valid = __ballot_sync(0xffffffffu, mine >= 0);
+    if (valid == 0) return;
+    const uint32_t before = valid & ((1u << lane) - 1u);
+    const int32_t prev = __shfl_sync(0xffffffffu, mine, before != 0 ? 31 - __clz(before) : lane);
+    const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0 || prev != mine));
+    // heads the item may have, in rounds of 32 elements: a team of that many warps takes every teams-th item
+    constexpr int ROUNDS = HP * D / 128;
+    const int busy = grp == 1 && NT == 1 && P == 1 ? ROUNDS / 2 : ROUNDS;   // one head: the slabs of j = 0
+    const int team = min(W, busy), teams = W / team;
+    int shared_first = -1, shared_last = -1;   // first records of the items shared with CTAs before and after
+    uint32_t left = starts;
+    for (int g = 0; left != 0; ++g) {
+        const int r0 = __ffs(left) - 1;
+        left &= left - 1;
+        const int r1 = left != 0 ? __ffs(left) - 1 : 2 * W;
+        const int32_t first = rec_first[r0], n = rec_n[r0];
+        const bool whole = first >= c0 && first + n <= c1;
+        if (!whole) (first < c0 ? shared_first : shared_last) = r0;
+        if (g % teams != warp / team % teams || warp >= team * teams) continue;
+        float *dst = whole ? nullptr : global_rec(cta, first < c0 ? 0 : 1);
+        for (int i = (warp % team) * 32 + lane; i < busy * 32; i += team * 32)
+            merge_element(Fp4Bool<false>{}, i, r0, r1, smem_rec, rec_b[r0], rec_it[r0], whole, dst);
+    }
+    if (shared_first < 0 && shared_last < 0) return;
+
+    // ---- items shared between CTAs -------------------------------------------
+    // All of the CTA's stores come before its counts; both items are counted at
+    // once, by lane 0 of warps 0 and 1.
+    __threadfence();
+    __syncthreads();
+    int32_t s_b[2], s_it[2], s_o0[2], s_n[2], s_g0[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r0 = k ? shared_last : shared_first;
+        s_n[k] = 0;
         if (r0 < 0) continue;
         const int32_t first = rec_first[r0];
-        const int o0 = slice_owner(first, Tn, nC), o1 = slice_owner(first + rec_n[r0] - 1, Tn, nC);
-        const int b = rec_b[r0], it = rec_it[r0];
-        int n = o1 - o0 + 1, stride = 1, merged = 0;
-        int32_t *counter = p.counters + (int64_t)b * items_per_seq + it;
+        s_b[k] = rec_b[r0];
+        s_it[k] = rec_it[r0];
+        s_o0[k] = slice_owner(first, Tn, nC);
+        s_n[k] = slice_owner(first + rec_n[r0] - 1, Tn, nC) - s_o0[k] + 1;
+        s_g0[k] = (cta - s_o0[k]) / kFp4Group * kFp4Group;   // the CTA's group of sharers
+    }
+    auto counter_of = [&](int k, bool group) {
+        return group ? p.group_counters + (int64_t)(s_o0[k] + s_g0[k]) * 2 + (s_g0[k] == 0 ? 1 : 0)
+                     : p.counters + (int64_t)s_b[k] * items_per_seq + s_it[k];
+    };
+    auto count = [&](int32_t *counter, int sharers) {        // true for the last of them
+        const bool last = atomicAdd(counter, 1) == sharers - 1;
+        if (last) *counter = 0;                // nobody else touches it again in this call
+        return last;
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (threadIdx.x == 32 * k && s_n[k] > 0) {
+            const bool two = s_n[k] > kFp4Flat;
+            arrived[k] = count(counter_of(k, two), two ? min(kFp4Group, s_n[k] - s_g0[k]) : s_n[k]);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (s_n[k] == 0 || arrived[k] == 0) continue;
+        __threadfence();
+        // an item's record is its first CTA's last one and every other CTA's first one
+        auto rec_of = [&](int i) { return (const float *)global_rec(s_o0[k] + i, i == 0 ? 1 : 0); };
+        int n = s_n[k], stride = 1, level = 0;
         if (n > kFp4Flat) {
-            // first level: the last of a group of neighbouring sharers merges its records
-            const int g0 = (cta - o0) / kFp4Group * kFp4Group, gslot = g0 == 0 ? 1 : 0;
-            const int gn = min(kFp4Group, n - g0);
-            if (!arrive(p.group_counters + (int64_t)(o0 + g0) * 2 + gslot, gn)) continue;
-            merge(workspace, gn, [&](int i) { return (const float *)global_rec(o0 + g0 + i, g0 + i == 0 ? 1 : 0); }, b, it,
-                  false, global_rec(o0 + g0, 2 + gslot));
+            // first level done: the last of the group merges its records
+            const int gslot = s_g0[k] == 0 ? 1 : 0, gn = min(kFp4Group, n - s_g0[k]);
+            for (int i = threadIdx.x; i < busy * 32; i += C::kThreads)
+                merge_element(Fp4Bool<true>{}, i, s_g0[k], s_g0[k] + gn, rec_of, s_b[k], s_it[k], false,
+                              global_rec(s_o0[k] + s_g0[k], 2 + gslot));
             n = (n + kFp4Group - 1) / kFp4Group;
             stride = kFp4Group;
-            merged = 2;
+            level = 2;
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) arrived[k] = count(counter_of(k, false), n);
+            __syncthreads();
+            if (arrived[k] == 0) continue;
+            __threadfence();
         }
-        if (!arrive(counter, n)) continue;
-        // an item's record is its first CTA's last one and every other CTA's first one
-        merge(workspace, n, [&](int i) { return (const float *)global_rec(o0 + i * stride, merged + (i == 0 ? 1 : 0)); }, b,
-              it, true, nullptr);
+        for (int i = threadIdx.x; i < busy * 32; i += C::kThreads)
+            merge_element(Fp4Bool<true>{}, i, 0, n,
+                          [&](int r) { return (const float *)global_rec(s_o0[k] + r * stride, level + (r == 0 ? 1 : 0)); },
+                          s_b[k], s_it[k], true, nullptr);
     }
 }
 
@@ -665,20 +767,22 @@ struct Fp4Launch {
         cudaError_t e = ensure_smem_limit(kern, smem, configured);
         if (e != cudaSuccess) return e;
         int per_sm = 0, sms = 0;
-        e = resident_ctas(kern, kFp4Threads, smem, occupancy, &per_sm);
+        e = resident_ctas(kern, C::kThreads, smem, occupancy, &per_sm);
         if (e != cudaSuccess) return e;
         e = device_sm_count(&sms);
         if (e != cudaSuccess) return e;
-        int64_t grid = (int64_t)sms * per_sm;
-        const int64_t cap = (max_tiles + kFp4Warps * kFp4MinTiles - 1) / (kFp4Warps * kFp4MinTiles);
-        plan->grid = (int)(grid > cap ? cap : grid);
+        const int64_t grid = sms;              // one CTA per SM
+        const int64_t cap = (max_tiles + C::kWarps * kFp4MinTiles - 1) / (C::kWarps * kFp4MinTiles);
+        const int64_t most = cap > plan->items ? cap : plan->items;   // an item to a CTA, or equal runs
+        plan->grid = (int)(grid > most ? most : grid);
+        if (per_sm < 1) plan->grid = 0;
+        plan->max_grid = sms;
         plan->smem = smem;
-        plan->rec_floats = C::kRec;
         return cudaSuccess;
     }
     static cudaError_t launch(const Fp4Decode &p, const Fp4Plan &plan, cudaStream_t stream) {
         if (plan.grid <= 0) return cudaErrorInvalidValue;
-        return launch_clustered(decode_fp4_kernel<T, D, NT, WHOLE>, plan.grid, kFp4Threads, plan.smem, 1, stream, p,
+        return launch_clustered(decode_fp4_kernel<T, D, NT, WHOLE>, plan.grid, C::kThreads, plan.smem, 1, stream, p,
                                 plan.units_per_kv);
     }
 };

@@ -66,12 +66,13 @@ struct Fp4Decode {
 };
 
 // A plan fixes the grid for a shape on the current device.  The workspace
-// holds 4 records per CTA of rec_floats floats, two int32 group counters per
-// CTA, then one int32 counter per item.
+// holds 4 records of kFp4RecFloats floats and two int32 group counters for each
+// CTA of the largest grid, then one int32 counter per item.
+constexpr int kFp4RecFloats = 16 * 128 + 2 * 16;   // the largest item: 16 heads of 128
 struct Fp4Plan {
     int grid = 0;
+    int max_grid = 0;          // of any shape on this device
     size_t smem = 0;
-    int rec_floats = 0;
     int units_per_kv = 1;      // items per (sequence, kv head)
     int nt = 1;                // 8-column MMA tiles per item
     bool whole_tiles = false;  // the rows of a tile are contiguous
