@@ -38,15 +38,12 @@
 namespace pa {
 
 constexpr int kFp4Tile = 16;
-constexpr int kFp4MinTiles = 2;    // tiles per warp below which fewer CTAs share the work
-constexpr int kFp4OwnTiles = 8;    // tiles per warp up to which a CTA of its own serves an item
+constexpr float kFp4Empty = -1e30f;   // reference of a column without scores: far below any, and finite
+constexpr int kFp4Item = 1;        // what an item costs beside its tiles (queries, output), in tiles
+constexpr int kFp4MinTiles = 1;    // tiles per warp below which fewer CTAs share the work
+constexpr int kFp4Snap = 4;        // tiles per warp that a CTA may have above the mean to end where items end
 constexpr int kFp4Flat = 24;       // sharers of an item up to which one level of merging serves
 constexpr int kFp4Group = 12;      // sharers per first-level group above that
-
-template <bool V>
-struct Fp4Bool {
-    static constexpr bool value = V;
-};
 
 template <typename T, int D, int NT>
 struct Fp4Cfg {
@@ -90,6 +87,87 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// A place in the index space of the work: an item of n tiles covers kFp4Item +
+// n places from `first` on, its tiles the last n.
+struct Fp4Cursor {
+    int b, it, n;
+    int32_t first;
+
+    __device__ __forceinline__ void seek(const int32_t *pre, int B, int items_per_seq, int32_t t) {
+        int lo = 0, hi = B;                    // pre[lo] <= t < pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        const int places = (pre[b + 1] - pre[b]) / items_per_seq;
+        it = (t - pre[b]) / places;
+        first = pre[b] + it * places;
+        n = places - kFp4Item;
+    }
+    // To the next item; b is B behind the last one.
+    __device__ __forceinline__ void next(const int32_t *pre, int B, int items_per_seq) {
+        first += n + kFp4Item;
+        if (++it < items_per_seq) return;
+        it = 0;
+        do {
+            ++b;
+        } while (b < B && pre[b + 1] == pre[b]);
+        if (b < B) n = (pre[b + 1] - pre[b]) / items_per_seq - kFp4Item;
+    }
+};
+
+// The schedule in shared memory: pre[b] the first place of sequence b, pre[B]
+// their number, lens[b] the length (-1: invalid).  Sequences with nothing to
+// attend to have no places.
+__device__ __forceinline__ void fp4_schedule(const DecodeParams &p, int items_per_seq, int32_t *pre, int32_t *lens,
+                                             int32_t *scan_tmp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    int32_t s = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int32_t L = p.seq_lens[b];
+        const bool ok = L >= 0 && (int64_t)L <= (int64_t)p.MB * p.bs;
+        const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
+        const int32_t n = ok ? (L - t_win / kFp4Tile * kFp4Tile + kFp4Tile - 1) / kFp4Tile : 0;
+        lens[b] = ok ? L : -1;
+        pre[b] = n > 0 ? (n + kFp4Item) * items_per_seq : 0;
+        s += pre[b];
+        if (!ok && (int)(b % gridDim.x) == (int)blockIdx.x) report(p.err_word, PA_DEVERR_BAD_LEN);
+    }
+    int32_t incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan_tmp[warp] = incl;
+    __syncthreads();
+    int32_t run = incl - s;
+    for (int w = 0; w < warp; ++w) run += scan_tmp[w];
+    for (int b = b0; b < b1; ++b) {
+        const int32_t c = pre[b];
+        pre[b] = run;
+        run += c;
+    }
+    if (threadIdx.x == blockDim.x - 1) pre[p.B] = run;
+    __syncthreads();
+}
+
+// Loads of either shared memory or of what other CTAs wrote (read at L2).
+__device__ __forceinline__ float ld_volatile(const float *p) {
+    float v;
+    asm volatile("ld.volatile.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_volatile4(const float *p) {
+    float4 v;
+    asm volatile("ld.volatile.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 // Row of the tile behind row i of the MMAs' token axis (rows 8..15: + 8), and
 // where 16-byte chunk c of tile row r lies in its row.
 template <int D>
@@ -132,7 +210,10 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ int32_t scan_tmp[W];
     __shared__ int32_t rec_first[2 * W], rec_n[2 * W], rec_b[2 * W], rec_it[2 * W];
-    __shared__ int32_t arrived[2];
+    __shared__ int32_t arrived[2], sharers_of[2];
+    __shared__ const float *list[2][32];       // records to merge
+    __shared__ float *merged_to[2];            // null: the output
+    __shared__ int32_t snap[32 * kFp4Group + 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     unsigned char *ring_p = smem + (size_t)warp * C::kWarpRing;
@@ -145,31 +226,30 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     grid_dependency_wait();
     allow_dependents();
     const int items_per_seq = p.Hkv * units_per_kv;
-    build_schedule<kFp4Tile>(p, items_per_seq, kFp4Tile, pre, lens, scan_tmp);
+    fp4_schedule(p, items_per_seq, pre, lens, scan_tmp);
     zero_empty_sequences<T>(p, pre);
     const int32_t Tn = pre[p.B];
-    // Few, short items: one to a CTA, so that nothing is merged between CTAs.
-    // Else an equal run of tiles to every CTA (fewer CTAs when their warps would
-    // have less than kFp4MinTiles).
-    const int cta = blockIdx.x;
-    int own = p.B * items_per_seq <= (int)gridDim.x;
-    if (own) {
-        bool big = false;
-        for (int b = threadIdx.x; b < p.B; b += C::kThreads)
-            big |= pre[b + 1] - pre[b] > W * kFp4OwnTiles * items_per_seq;
-        own = !__syncthreads_or(big);
-    }
+    // An equal run of places to every CTA (fewer CTAs when their warps would have
+    // less than kFp4MinTiles).  The runs' ends are moved to the nearest ends of
+    // items, and nothing has to be merged between CTAs, if that leaves no CTA
+    // with much more than the mean: the merge costs a CTA 4 to 5 us.
     const int nC = min((int)gridDim.x, (Tn + W * kFp4MinTiles - 1) / (W * kFp4MinTiles));
-    int32_t c0, c1;
-    if (own) {
-        const int b = min(cta / items_per_seq, p.B - 1), it = cta - b * items_per_seq;
-        const int32_t n = it < items_per_seq ? (pre[b + 1] - pre[b]) / items_per_seq : 0;
-        c0 = pre[b] + it * n;
-        c1 = c0 + n;
-    } else {
-        c0 = cta < nC ? slice_start(cta, Tn, nC) : 0;
-        c1 = cta < nC ? slice_start(cta + 1, Tn, nC) : 0;
+    const int cta = blockIdx.x;
+    if (cta >= nC) return;
+    for (int c = threadIdx.x; c <= nC; c += C::kThreads) {
+        int32_t t = slice_start(c, Tn, nC);
+        if (c > 0 && c < nC) {
+            Fp4Cursor x;
+            x.seek(pre, p.B, items_per_seq, t);
+            t = 2 * (t - x.first) <= x.n + kFp4Item ? x.first : x.first + x.n + kFp4Item;
+        }
+        snap[c] = t;
     }
+    __syncthreads();
+    bool over = false;
+    for (int c = threadIdx.x; c < nC; c += C::kThreads) over |= snap[c + 1] - snap[c] > Tn / nC + W * kFp4Snap;
+    const bool cut = __syncthreads_or(over);   // items are cut between CTAs
+    const int32_t c0 = cut ? slice_start(cta, Tn, nC) : snap[cta], c1 = cut ? slice_start(cta + 1, Tn, nC) : snap[cta + 1];
     if (c0 >= c1) return;
     const int32_t w0 = c0 + slice_start(warp, c1 - c0, W), w1 = c0 + slice_start(warp + 1, c1 - c0, W);
     if (lane < 2) rec_first[2 * warp + lane] = -1;
@@ -181,20 +261,29 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     // Table entries are looked up ahead, so that a tile's copies never wait for
     // them: WHOLE, of a batch of up to 32 tiles of an item, lane i keeping the
     // offsets of the i-th; else of one tile, lane l of its row l % 16.
-    TileCursor pc = {};
-    int32_t pt = w0;                           // first tile of the batch
+    Fp4Cursor pc = {};
+    int32_t p_k = 0, p_end = 0;                // the batch's first tile, the last of this warp's run of its item
     int p_i = 0, p_left = 0;                   // the next tile in it, tiles left in it
+    bool p_more = true;                        // there may be a batch behind it
     int64_t p_code = 0, p_scale = 0;           // byte offsets of K's codes and scales (the row's if not WHOLE, -1: none)
     uint32_t p_bad = 0;                        // tiles (rows) whose entry is outside the pool
     uint32_t bad_bits = 0;                     // ring stages whose tile had a bad table entry
     const int64_t v_scale_off = (int64_t)p.Hkv * p.bs * C::kScRow;
-    auto look_up = [&]() {                     // the batch from tile pt under cursor pc
+    auto look_up = [&]() {                     // the batch behind the one that is done
+        p_k += p_i;
+        p_i = 0;
+        if (p_k >= p_end) {
+            pc.next(pre, p.B, items_per_seq);
+            p_k = 0;
+            p_end = min(pc.n, w1 - pc.first - kFp4Item);
+            p_more = pc.b < p.B && p_end > 0;
+            if (!p_more) return;
+        }
         const int32_t L = lens[pc.b];
         const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
-        const int32_t base = t_win / kFp4Tile * kFp4Tile + pc.k * kFp4Tile;
+        const int32_t base = t_win / kFp4Tile * kFp4Tile + p_k * kFp4Tile;
         const int hk = units_per_kv == 1 ? pc.it : pc.it / units_per_kv;
-        p_i = 0;
-        p_left = WHOLE ? min(min(32, pc.n - pc.k), w1 - pt) : 1;
+        p_left = WHOLE ? min(32, p_end - p_k) : 1;
         const int32_t tok = base + (WHOLE ? lane * kFp4Tile : (lane & 15));
         const bool need = WHOLE ? lane < p_left : tok >= t_win && tok < L;
         int64_t blk = 0;
@@ -212,7 +301,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         p_code = blk * p.block_stride_bytes + row * C::kRow;
         p_scale = (blk * 2 * p.Hkv * p.bs + row) * C::kScRow;
         if (!WHOLE && !need) p_code = -1;
-        if (pc.k == 0) {                       // the item's queries, before its first tile is due
+        if (p_k == 0) {                        // the item's queries, before its first tile is due
             const char *q = reinterpret_cast<const char *>(p.q) +
                             ((int64_t)pc.b * p.H + hk * grp + (pc.it - hk * units_per_kv) * HP) * D * sizeof(T);
             const int heads = min(HP, grp - (pc.it - hk * units_per_kv) * HP);
@@ -257,14 +346,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             if (p_bad != 0) bad_bits |= 1u << stage;
         }
         ++p_i;
-        if (--p_left == 0) {
-            pt += p_i;
-            if (pt < w1) {
-                pc.k += p_i - 1;
-                pc.next(pre, items_per_seq);
-                look_up();
-            }
-        }
+        --p_left;
     };
 
     // ---- consumer side -------------------------------------------------------
@@ -278,13 +360,18 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             const int col = P == 2 ? nt * 4 + (gid & 3) : nt * 8 + gid;
             const bool have = h0 + col < grp;
             const T *src = reinterpret_cast<const T *>(p.q) + ((int64_t)b * p.H + hk * grp + h0 + col) * D + tig * (D / 4);
+            constexpr int VEC = D / 4 * (int)sizeof(T) / 16;
+            uint4 raw[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) raw[i] = have ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+            constexpr int PER = 16 / (int)sizeof(T);
             float big = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (have) load8(src + 8 * i, x);
+            for (int i = 0; i < VEC; ++i) {
+                float x[PER];
+                Elem<T>::unpack(raw[i], x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(x[j]));
+                for (int j = 0; j < PER; ++j) big = fmaxf(big, fabsf(x[j]));
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -294,22 +381,25 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (have) load8(src + 8 * i, x);
+            for (int i = 0; i < VEC; ++i) {
+                float x[PER];
+                Elem<T>::unpack(raw[i], x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < PER; ++j) {
                     x[j] *= down;
                     if (P == 2 && gid >= 4) x[j] -= __half2float(__float2half_rn(x[j]));
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) qf[nt][2 * i + j / 2][j & 1] = Elem<__half>::pack2(x[2 * j], x[2 * j + 1]);
+                for (int j = 0; j < PER / 2; ++j) {
+                    const int w = i * (PER / 2) + j;
+                    qf[nt][w / 2][w & 1] = Elem<__half>::pack2(x[2 * j], x[2 * j + 1]);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = P == 2 ? (2 * tig + j) & 3 : 2 * tig + j;
                 cs[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, c * 4);
-                m[nt][j] = -INFINITY;
+                m[nt][j] = kFp4Empty;
                 l[nt][j] = 0.f;
             }
 #pragma unroll
@@ -319,9 +409,8 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         }
     };
 
-    // with_edge: some rows lie outside [lo, hi) (the first and last tiles of an item)
-    auto tile = [&](auto with_edge, uint32_t codes, int32_t tok0, int32_t lo, int32_t hi) {
-        constexpr bool edge = decltype(with_edge)::value;
+    // bias0, bias1: added to the scores of this lane's two rows (0, or -inf outside the item)
+    auto tile = [&](uint32_t codes, float bias0, float bias1) {
         const uint32_t sc = codes + 2 * C::kHalf;
         const int rk = tau<D>(gid);
         // K rows rk and rk + 8 of this lane, and their scales
@@ -358,40 +447,27 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             }
         }
 
-        // scores in the log2 domain, relative to the columns' references; rows
-        // outside weigh nothing
-        const bool out0 = tok0 + rk < lo || tok0 + rk >= hi, out1 = tok0 + rk + 8 < lo || tok0 + rk + 8 >= hi;
+        // scores in the log2 domain, relative to the columns' references
         float x[NT][4];
+        bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (P == 2) c[nt][i] += __shfl_xor_sync(0xffffffffu, c[nt][i], 2);
-                x[nt][i] = fmaf(c[nt][i], cs[nt][i & 1], -m[nt][i & 1]);
+                x[nt][i] = fmaf(c[nt][i], cs[nt][i & 1], (i < 2 ? bias0 : bias1) - m[nt][i & 1]);
+                over = over || x[nt][i] > 8.f;
             }
-        if constexpr (edge) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < 2 ? out0 : out1) x[nt][i] = -INFINITY;
-        }
-        bool over = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) over = over || x[nt][i] > 8.f;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float y0 = edge && out0 ? -INFINITY : c[nt][j] * cs[nt][j];
-                    const float y1 = edge && out1 ? -INFINITY : c[nt][j + 2] * cs[nt][j];
+                    const float y0 = fmaf(c[nt][j], cs[nt][j], bias0), y1 = fmaf(c[nt][j + 2], cs[nt][j], bias1);
                     float mx = fmaxf(m[nt][j], fmaxf(y0, y1));
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-                    const float f = merge_weight(m[nt][j], mx);
+                    const float f = ex2_approx(m[nt][j] - mx);
                     m[nt][j] = mx;
                     x[nt][j] = y0 - mx;
                     x[nt][j + 2] = y1 - mx;
@@ -429,13 +505,6 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             const int byte = gid * (D / 16);   // of the row
             lds_words<VW>(vc + row * C::kRow + swizzle<D>(row, byte / 16) * 16 + byte % 16, vw[i]);
             sb[i] = lds_bytes<VB>(vs + row * C::kScRow + (D == 64 ? gid / 2 : gid * VB));
-        }
-        if constexpr (edge) {                  // a slot nobody wrote may hold a NaN scale, which a weight of 0 would keep
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int32_t tok = tok0 + (i & 1 ? t1 : t0) + 8 * (i >> 1);
-                if (tok < lo || tok >= hi) sb[i] = 0;
-            }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -479,7 +548,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     };
     // The state of an item this warp has finished its part of: whole items to
     // `out`, parts to a record (O, m [HP], l [HP]; l < 0: bad table).
-    auto finish = [&](const TileCursor &cc, bool whole, bool bad, float *rec) {
+    auto finish = [&](const Fp4Cursor &cc, bool whole, bool bad, float *rec) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -537,127 +606,119 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 
     if (w0 < w1) {
         pc.seek(pre, p.B, items_per_seq, w0);
-        TileCursor cc = pc;
-        look_up();
+        Fp4Cursor cc = pc;
+        p_k = max(0, w0 - pc.first - kFp4Item);
+        p_end = min(pc.n, w1 - pc.first - kFp4Item);
 #pragma unroll 1
-        for (int i = 0; i < S - 1; ++i) {
+        for (int i = -1; i < S - 1; ++i) {     // the first batch, and its first tiles
             if (p_left > 0) fetch(ring + i * C::kStage, i);
-            cp_async_commit();
+            if (i >= 0) cp_async_commit();
+            if (p_left == 0 && p_more) look_up();
         }
-        int32_t t = w0;
         int stage = 0;
-        while (true) {                         // items (or parts) of this warp's run
+#pragma unroll 1
+        for (; cc.b < p.B && cc.first < w1; cc.next(pre, p.B, items_per_seq)) {
+            int32_t k = max(0, w0 - cc.first - kFp4Item);
+            const int32_t end = min(cc.n, w1 - cc.first - kFp4Item);
+            if (k >= end) continue;
+            const bool whole = k == 0 && end == cc.n;
             load_q(cc.b, cc.it);
             const int32_t hi = lens[cc.b], lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
-            int32_t tok0 = lo / kFp4Tile * kFp4Tile + cc.k * kFp4Tile;
-            const int32_t end = min(w1, cc.first + cc.n);
             bool bad = false;
-            for (; t < end; ++t, tok0 += kFp4Tile) {
+            int32_t tok0 = (lo / kFp4Tile + k) * kFp4Tile;
+#pragma unroll 1
+            for (; k < end; ++k, tok0 += kFp4Tile) {
                 cp_async_wait<S - 2>();
                 __syncwarp();                  // every lane's copies have landed, and the tile before is read
+                const int free_stage = stage == 0 ? S - 1 : stage - 1;
+                if (p_left > 0) fetch(ring + free_stage * C::kStage, free_stage);
+                cp_async_commit();
+                if (p_left == 0 && p_more) look_up();
                 if (bad_bits != 0) {
                     bad |= (bad_bits >> stage) & 1u;
                     bad_bits &= ~(1u << stage);
                 }
-                const int free_stage = stage == 0 ? S - 1 : stage - 1;
-                if (p_left > 0) fetch(ring + free_stage * C::kStage, free_stage);
-                cp_async_commit();
                 const uint32_t codes = ring + stage * C::kStage;
-                if (tok0 >= lo && tok0 + kFp4Tile <= hi) tile(Fp4Bool<false>{}, codes, tok0, lo, hi);
-                else tile(Fp4Bool<true>{}, codes, tok0, lo, hi);
+                float bias0 = 0.f, bias1 = 0.f;
+                if (tok0 < lo || tok0 + kFp4Tile > hi) {
+                    // rows outside [lo, hi): no weight, and scales of 0, for a slot that
+                    // nobody wrote may hold NaN, which no weight would remove
+                    const int32_t r0 = tok0 + tau<D>(gid), r1 = r0 + 8, r = tok0 + (lane & 15);
+                    bias0 = r0 < lo || r0 >= hi ? -INFINITY : 0.f;
+                    bias1 = r1 < lo || r1 >= hi ? -INFINITY : 0.f;
+                    if (r < lo || r >= hi) {
+#pragma unroll
+                        for (int i = 0; i < C::kScRow; i += 4)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(codes + f_sdst + i), "r"(0) : "memory");
+                    }
+                    __syncwarp();
+                }
+                tile(codes, bias0, bias1);
                 stage = stage + 1 == S ? 0 : stage + 1;
             }
-            const bool whole = cc.first >= w0 && cc.first + cc.n <= w1, last = t == w1;
-            if (last) {
+            if (end < cc.n) {                  // the last part of the run: the ring is free for its record
                 cp_async_wait<0>();
-                __syncwarp();                  // the ring is free for the record
+                __syncwarp();
             }
-            // a part that ends inside the run began before it
-            finish(cc, whole, bad, last ? last_rec : first_rec);
+            finish(cc, whole, bad, end < cc.n ? last_rec : first_rec);
             if (!whole && lane == 0) {
-                const int r = 2 * warp + (last ? 1 : 0);
+                const int r = 2 * warp + (end < cc.n ? 1 : 0);
                 rec_first[r] = cc.first;
                 rec_n[r] = cc.n;
                 rec_b[r] = cc.b;
                 rec_it[r] = cc.it;
             }
-            if (last) break;
-            cc.k = cc.n - 1;
-            cc.next(pre, items_per_seq);
         }
     }
     __syncthreads();
 
     // ---- merges --------------------------------------------------------------
-    // Element i of a record (a lane's slab) merged over records [r0, r1) of one
-    // item: into the item's output, or into the record dst.  rec_at(r) may be
-    // null (no record).  Records in the workspace were written by other CTAs:
-    // read at L2.  The maximum of all records weighs them; their O is loaded
-    // eight at a time whatever the weights.
-    auto merge_element = [&](auto in_workspace, int i, int r0, int r1, auto rec_at, int b, int it, bool whole, float *dst) {
-        constexpr bool ws = decltype(in_workspace)::value;
-        auto ld = [](const float *a) { return ws ? __ldcg(a) : *a; };
-        const int ln = i & 31, h = head_of(i >> 5, ln);
+    // The records of[from, to) of one item, merged into its output, or into
+    // the record dst.  The lists' entries lie in shared memory or in the
+    // workspace, where other CTAs wrote them: volatile loads read L2.  One copy
+    // of this code serves every merge: what a CTA runs once is paid for in
+    // instruction fetches.
+    auto merge = [&](const float *const *of, int from, int to, int b, int it, bool whole, float *dst, int tid, int threads) {
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
-        float M = -INFINITY, sum = 0.f;
-        bool bad = false;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int r = r0; r < r1; r += 8) {
-            float mr[8], lr[8];
-            float4 a[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float *rec = r + k < r1 ? rec_at(r + k) : nullptr;
-                mr[k] = -INFINITY;
-                lr[k] = 0.f;
-                a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (rec != nullptr) {
-                    mr[k] = ld(rec + HP * D + h);
-                    lr[k] = ld(rec + HP * D + HP + h);
-                    const float4 *ra = reinterpret_cast<const float4 *>(rec + i * 4);
-                    a[k] = ws ? __ldcg(ra) : *ra;
+        // heads the item may have, a slab of 32 lanes at a time (one head: the slabs of j = 0)
+        const int elements = (grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS) * 32;
+        for (int i = tid; i < elements; i += threads) {
+            const int ln = i & 31, h = head_of(i >> 5, ln), d = dim_of(i >> 5, ln);
+            float M = kFp4Empty, sum = 0.f;
+            bool bad = false;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int r = from; r < to; ++r) {
+                const float *rec = of[r];
+                const float mr = ld_volatile(rec + HP * D + h), lr = ld_volatile(rec + HP * D + HP + h);
+                const float4 a = ld_volatile4(rec + i * 4);
+                const float top = fmaxf(M, mr), f = ex2_approx(M - top), w = ex2_approx(mr - top);
+                M = top;
+                bad |= lr < 0.f;
+                sum = fmaf(sum, f, lr * w);
+                acc.x = fmaf(acc.x, f, a.x * w);
+                acc.y = fmaf(acc.y, f, a.y * w);
+                acc.z = fmaf(acc.z, f, a.z * w);
+                acc.w = fmaf(acc.w, f, a.w * w);
+            }
+            if (!whole) {
+                *reinterpret_cast<float4 *>(dst + i * 4) = acc;
+                if (d == 0) {
+                    dst[HP * D + h] = M;
+                    dst[HP * D + HP + h] = bad ? -1.f : sum;
                 }
+            } else if (h0 + h < grp) {
+                const float f = fp.v_g / sum;
+                T *o4 = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + d;
+                const float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(o4) = y;
+                else *reinterpret_cast<uint2 *>(o4) = make_uint2(Elem<T>::pack2(y.x, y.y), Elem<T>::pack2(y.z, y.w));
             }
-            float top = M;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, mr[k]);
-            const float f = merge_weight(M, top);
-            M = top;
-            sum *= f;
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float w = merge_weight(mr[k], top);
-                bad |= lr[k] < 0.f;
-                sum = fmaf(lr[k], w, sum);
-                acc.x = fmaf(a[k].x, w, acc.x);
-                acc.y = fmaf(a[k].y, w, acc.y);
-                acc.z = fmaf(a[k].z, w, acc.z);
-                acc.w = fmaf(a[k].w, w, acc.w);
-            }
-        }
-        if (!whole) {
-            __stcg(reinterpret_cast<float4 *>(dst + i * 4), acc);
-            if (dim_of(i >> 5, ln) == 0) {
-                __stcg(dst + HP * D + h, M);
-                __stcg(dst + HP * D + HP + h, bad ? -1.f : sum);
-            }
-        } else if (h0 + h < grp) {
-            const float f = fp.v_g / sum;
-            T *o4 = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + dim_of(i >> 5, ln);
-            const float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(o4) = y;
-            else *reinterpret_cast<uint2 *>(o4) = make_uint2(Elem<T>::pack2(y.x, y.y), Elem<T>::pack2(y.z, y.w));
         }
     };
     // record `slot` of a CTA: 0 its first item, 1 its last one; 2 and 3 the
     // merged record of the group of sharers that record 0 or 1 heads
     auto global_rec = [&](int c, int slot) { return p.records + ((int64_t)c * 4 + slot) * p.rec_floats; };
-    auto smem_rec = [&](int r) -> const float * {
-        if (rec_first[r] < 0) return nullptr;
-        return (r & 1) ? reinterpret_cast<const float *>(smem + (size_t)(r >> 1) * C::kWarpRing)
-                       : reinterpret_cast<const float *>(smem + (size_t)W * C::kWarpRing) + (size_t)(r >> 1) * C::kRec;
-    };
 
     // The CTA's records, in the items' order: lane r of every warp looks at
     // record r; a run of records of one item starts where the item changes.
@@ -667,87 +728,72 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     const uint32_t before = valid & ((1u << lane) - 1u);
     const int32_t prev = __shfl_sync(0xffffffffu, mine, before != 0 ? 31 - __clz(before) : lane);
     const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0 || prev != mine));
-    // heads the item may have, in rounds of 32 elements: a team of that many warps takes every teams-th item
-    constexpr int ROUNDS = HP * D / 128;
-    const int busy = grp == 1 && NT == 1 && P == 1 ? ROUNDS / 2 : ROUNDS;   // one head: the slabs of j = 0
-    const int team = min(W, busy), teams = W / team;
+    if (warp == 0 && mine >= 0)
+        list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kWarpRing)
+                                          : reinterpret_cast<const float *>(smem + (size_t)W * C::kWarpRing) +
+                                                (size_t)(lane >> 1) * C::kRec;
+    __syncthreads();
+    // a team of warps per item, as many as its slabs, the items of a CTA side by side
+    const int team = min(W, grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS), teams = W / team;
     int shared_first = -1, shared_last = -1;   // first records of the items shared with CTAs before and after
     uint32_t left = starts;
+#pragma unroll 1
     for (int g = 0; left != 0; ++g) {
         const int r0 = __ffs(left) - 1;
         left &= left - 1;
-        const int r1 = left != 0 ? __ffs(left) - 1 : 2 * W;
-        const int32_t first = rec_first[r0], n = rec_n[r0];
-        const bool whole = first >= c0 && first + n <= c1;
+        const uint32_t upto = left != 0 ? (1u << (__ffs(left) - 1)) - 1u : 0xffffffffu;
+        const int32_t first = rec_first[r0] + kFp4Item;      // its first tile
+        const bool whole = first >= c0 && first + rec_n[r0] <= c1;
         if (!whole) (first < c0 ? shared_first : shared_last) = r0;
-        if (g % teams != warp / team % teams || warp >= team * teams) continue;
-        float *dst = whole ? nullptr : global_rec(cta, first < c0 ? 0 : 1);
-        for (int i = (warp % team) * 32 + lane; i < busy * 32; i += team * 32)
-            merge_element(Fp4Bool<false>{}, i, r0, r1, smem_rec, rec_b[r0], rec_it[r0], whole, dst);
+        if (g % teams == warp / team)
+            merge(list[0], __popc(valid & ((1u << r0) - 1u)), __popc(valid & upto), rec_b[r0], rec_it[r0], whole,
+                  global_rec(cta, first < c0 ? 0 : 1), (warp % team) * 32 + lane, team * 32);
     }
     if (shared_first < 0 && shared_last < 0) return;
 
     // ---- items shared between CTAs -------------------------------------------
-    // All of the CTA's stores come before its counts; both items are counted at
-    // once, by lane 0 of warps 0 and 1.
-    __threadfence();
-    __syncthreads();
-    int32_t s_b[2], s_it[2], s_o0[2], s_n[2], s_g0[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r0 = k ? shared_last : shared_first;
-        s_n[k] = 0;
-        if (r0 < 0) continue;
-        const int32_t first = rec_first[r0];
-        s_b[k] = rec_b[r0];
-        s_it[k] = rec_it[r0];
-        s_o0[k] = slice_owner(first, Tn, nC);
-        s_n[k] = slice_owner(first + rec_n[r0] - 1, Tn, nC) - s_o0[k] + 1;
-        s_g0[k] = (cta - s_o0[k]) / kFp4Group * kFp4Group;   // the CTA's group of sharers
-    }
-    auto counter_of = [&](int k, bool group) {
-        return group ? p.group_counters + (int64_t)(s_o0[k] + s_g0[k]) * 2 + (s_g0[k] == 0 ? 1 : 0)
-                     : p.counters + (int64_t)s_b[k] * items_per_seq + s_it[k];
-    };
-    auto count = [&](int32_t *counter, int sharers) {        // true for the last of them
-        const bool last = atomicAdd(counter, 1) == sharers - 1;
-        if (last) *counter = 0;                // nobody else touches it again in this call
-        return last;
-    };
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        if (threadIdx.x == 32 * k && s_n[k] > 0) {
-            const bool two = s_n[k] > kFp4Flat;
-            arrived[k] = count(counter_of(k, two), two ? min(kFp4Group, s_n[k] - s_g0[k]) : s_n[k]);
+    // Warp k counts this CTA as one of the sharers of item k (0: shared with CTAs
+    // before, 1: with CTAs behind), and the last of them merges their records.
+    // Many sharers do so in two levels: the last of a group of neighbours merges
+    // the group's, the last of the groups the groups'.
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        __threadfence();                       // all of the CTA's stores come before its counts
+        __syncthreads();
+        if (warp < 2) {
+            const int k = warp, r0 = k ? shared_last : shared_first;
+            int last = 0;
+            if (r0 >= 0 && (level == 0 || arrived[k] == 2)) {
+                const int32_t first = rec_first[r0] + kFp4Item;   // its first tile
+                const int o0 = slice_owner(first, Tn, nC), n = slice_owner(first + rec_n[r0] - 1, Tn, nC) - o0 + 1;
+                const bool two = n > kFp4Flat, grouped = two && level == 0;
+                const int g0 = grouped ? (cta - o0) / kFp4Group * kFp4Group : 0, gslot = g0 == 0 ? 1 : 0;
+                const int sharers = grouped ? min(kFp4Group, n - g0) : two ? (n + kFp4Group - 1) / kFp4Group : n;
+                int32_t *counter = grouped ? p.group_counters + (int64_t)(o0 + g0) * 2 + gslot
+                                           : p.counters + (int64_t)rec_b[r0] * items_per_seq + rec_it[r0];
+                if (lane == 0) {
+                    last = atomicAdd(counter, 1) == sharers - 1;
+                    if (last) *counter = 0;    // nobody else touches it again in this call
+                    sharers_of[k] = sharers;
+                    merged_to[k] = grouped ? global_rec(o0 + g0, 2 + gslot) : nullptr;
+                }
+                last = __shfl_sync(0xffffffffu, last, 0) * (grouped ? 2 : 1);
+                // an item's record is its first CTA's last one and every other CTA's first one
+                const int c = two && !grouped ? lane * kFp4Group : g0 + lane;
+                if (lane < sharers) list[k][lane] = global_rec(o0 + c, (two && !grouped ? 2 : 0) + (c == 0 ? 1 : 0));
+            }
+            if (lane == 0) arrived[k] = last;  // 2: and there is another level
         }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (s_n[k] == 0 || arrived[k] == 0) continue;
+        __syncthreads();
+        const int a0 = arrived[0], a1 = arrived[1];
+        if (a0 == 0 && a1 == 0) return;
         __threadfence();
-        // an item's record is its first CTA's last one and every other CTA's first one
-        auto rec_of = [&](int i) { return (const float *)global_rec(s_o0[k] + i, i == 0 ? 1 : 0); };
-        int n = s_n[k], stride = 1, level = 0;
-        if (n > kFp4Flat) {
-            // first level done: the last of the group merges its records
-            const int gslot = s_g0[k] == 0 ? 1 : 0, gn = min(kFp4Group, n - s_g0[k]);
-            for (int i = threadIdx.x; i < busy * 32; i += C::kThreads)
-                merge_element(Fp4Bool<true>{}, i, s_g0[k], s_g0[k] + gn, rec_of, s_b[k], s_it[k], false,
-                              global_rec(s_o0[k] + s_g0[k], 2 + gslot));
-            n = (n + kFp4Group - 1) / kFp4Group;
-            stride = kFp4Group;
-            level = 2;
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) arrived[k] = count(counter_of(k, false), n);
-            __syncthreads();
-            if (arrived[k] == 0) continue;
-            __threadfence();
-        }
-        for (int i = threadIdx.x; i < busy * 32; i += C::kThreads)
-            merge_element(Fp4Bool<true>{}, i, 0, n,
-                          [&](int r) { return (const float *)global_rec(s_o0[k] + r * stride, level + (r == 0 ? 1 : 0)); },
-                          s_b[k], s_it[k], true, nullptr);
+        // two items: half the CTA for each
+        const int threads = a0 != 0 && a1 != 0 ? C::kThreads / 2 : C::kThreads;
+        const int k = a0 != 0 && (int)threadIdx.x < threads ? 0 : 1, r0 = k ? shared_last : shared_first;
+        merge(list[k], 0, sharers_of[k], rec_b[r0], rec_it[r0], merged_to[k] == nullptr, merged_to[k],
+              (int)threadIdx.x % threads, threads);
+        if (a0 < 2 && a1 < 2) return;
     }
 }
 
@@ -771,12 +817,12 @@ struct Fp4Launch {
         if (e != cudaSuccess) return e;
         e = device_sm_count(&sms);
         if (e != cudaSuccess) return e;
-        const int64_t grid = sms;              // one CTA per SM
+        const int64_t grid = sms < 32 * kFp4Group ? sms : 32 * kFp4Group;   // one CTA per SM; a merge takes 32 records
         const int64_t cap = (max_tiles + C::kWarps * kFp4MinTiles - 1) / (C::kWarps * kFp4MinTiles);
         const int64_t most = cap > plan->items ? cap : plan->items;   // an item to a CTA, or equal runs
         plan->grid = (int)(grid > most ? most : grid);
         if (per_sm < 1) plan->grid = 0;
-        plan->max_grid = sms;
+        plan->max_grid = (int)grid;
         plan->smem = smem;
         return cudaSuccess;
     }
