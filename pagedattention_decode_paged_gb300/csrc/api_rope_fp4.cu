@@ -125,7 +125,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
 pa_status plan_of(const pa_shape *s, pa::Fp4Plan *plan) {
     const int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
     const cudaError_t e = pa::plan_decode_fp4(s->dtype, s->head_dim, s->num_heads / s->num_kv_heads, s->batch,
-                                              s->num_kv_heads, s->block_size, (max_len + 15) / 16, plan);
+                                              s->num_kv_heads, s->block_size, (max_len + 31) / 32 + 1, plan);
     if (e == cudaErrorInvalidValue) {
         (void)cudaGetLastError();   // a too-large shared-memory request is not sticky; drop it
         return PA_ERR_UNSUPPORTED;

@@ -37,7 +37,8 @@
 
 namespace pa {
 
-constexpr int kFp4Tile = 16;
+constexpr int kFp4Tile = 32;       // tokens of a tile: two halves of 16, the MMAs' token axis
+constexpr int kFp4Halves = kFp4Tile / 16;
 constexpr float kFp4Empty = -1e30f;   // reference of a column without scores: far below any, and finite
 constexpr int kFp4Item = 1;        // what an item costs beside its tiles (queries, output), in tiles
 constexpr int kFp4MinTiles = 1;    // tiles per warp below which fewer CTAs share the work
@@ -51,18 +52,20 @@ struct Fp4Cfg {
     static constexpr int kHeads = NT * 8 / kParts;          // query heads per item
     static constexpr int kRow = D / 2;                      // code bytes of a row
     static constexpr int kScRow = D / 16;                   // scale bytes of a row
-    static constexpr int kHalf = kFp4Tile * kRow;           // K (or V) codes of a tile
-    static constexpr int kScHalf = kFp4Tile * kScRow;
-    static constexpr int kStage = 2 * (kHalf + kScHalf);    // K codes, V codes, K scales, V scales
-    static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;
+    static constexpr int kCodes = 16 * kRow;                // K (or V) codes of a half tile
+    static constexpr int kScales = 16 * kScRow;
+    static constexpr int kHalf = 2 * (kCodes + kScales);    // K codes, V codes, K scales, V scales
+    static constexpr int kStage = kFp4Halves * kHalf;
+    static constexpr int kStages = 2;
     static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
-    // one CTA per SM: of 16 warps where a thread gets along with 128 registers
-    static constexpr int kWarps = NT * D <= 128 ? 16 : 8;
+    // one CTA per SM: of 12 warps where a thread gets along with 168 registers
+    static constexpr int kWarps = NT * D <= 128 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
-    // the last record of a warp reuses its own ring
-    static_assert(kWarpRing >= kRec * 4 && kRec <= kFp4RecFloats, "a record fits the ring and the workspace");
-    static constexpr size_t kFixed = (size_t)kWarps * (kWarpRing + kRec * 4);
+    // the last record of a warp takes the place of its ring
+    static constexpr int kRingBytes = kWarpRing > kRec * 4 ? kWarpRing : kRec * 4;
+    static_assert(kRec <= kFp4RecFloats, "a record fits the workspace");
+    static constexpr size_t kFixed = (size_t)kWarps * (kRingBytes + kRec * 4);
     static size_t bytes(int batch) { return kFixed + ((size_t)2 * batch + 1) * 4; }
 };
 
@@ -216,9 +219,9 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __shared__ int32_t snap[32 * kFp4Group + 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    unsigned char *ring_p = smem + (size_t)warp * C::kWarpRing;
+    unsigned char *ring_p = smem + (size_t)warp * C::kRingBytes;
     const uint32_t ring = smem_u32(ring_p);
-    float *first_rec = reinterpret_cast<float *>(smem + (size_t)W * C::kWarpRing) + (size_t)warp * C::kRec;
+    float *first_rec = reinterpret_cast<float *>(smem + (size_t)W * C::kRingBytes) + (size_t)warp * C::kRec;
     float *last_rec = reinterpret_cast<float *>(ring_p);
     int32_t *pre = reinterpret_cast<int32_t *>(smem + C::kFixed);
     int32_t *lens = pre + p.B + 1;
@@ -259,15 +262,15 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 
     // ---- producer side -------------------------------------------------------
     // Table entries are looked up ahead, so that a tile's copies never wait for
-    // them: WHOLE, of a batch of up to 32 tiles of an item, lane i keeping the
-    // offsets of the i-th; else of one tile, lane l of its row l % 16.
+    // them: WHOLE, of a batch of up to 16 tiles of an item, lane i keeping the
+    // offsets of the i-th half tile; else of one tile, lane l of its row l.
     Fp4Cursor pc = {};
     int32_t p_k = 0, p_end = 0;                // the batch's first tile, the last of this warp's run of its item
     int p_i = 0, p_left = 0;                   // the next tile in it, tiles left in it
     bool p_more = true;                        // there may be a batch behind it
-    int64_t p_code = 0, p_scale = 0;           // byte offsets of K's codes and scales (the row's if not WHOLE, -1: none)
-    uint32_t p_bad = 0;                        // tiles (rows) whose entry is outside the pool
-    uint32_t bad_bits = 0;                     // ring stages whose tile had a bad table entry
+    int64_t p_code = -1, p_scale = 0;          // byte offsets of K's codes (-1: nothing to fetch) and scales
+    uint32_t p_bad = 0;                        // half tiles (rows) whose entry is outside the pool
+    uint32_t bad_tiles = 0;                    // bit i: the tile i after the next one had a bad table entry
     const int64_t v_scale_off = (int64_t)p.Hkv * p.bs * C::kScRow;
     auto look_up = [&]() {                     // the batch behind the one that is done
         p_k += p_i;
@@ -283,9 +286,10 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
         const int32_t base = t_win / kFp4Tile * kFp4Tile + p_k * kFp4Tile;
         const int hk = units_per_kv == 1 ? pc.it : pc.it / units_per_kv;
-        p_left = WHOLE ? min(32, p_end - p_k) : 1;
-        const int32_t tok = base + (WHOLE ? lane * kFp4Tile : (lane & 15));
-        const bool need = WHOLE ? lane < p_left : tok >= t_win && tok < L;
+        p_left = WHOLE ? min(32 / kFp4Halves, p_end - p_k) : 1;
+        // tokens [tok, tok + (WHOLE ? 16 : 1)) of this lane; needed if one of them is attended to
+        const int32_t tok = base + lane * (WHOLE ? 16 : 1);
+        const bool need = lane < p_left * (WHOLE ? kFp4Halves : kFp4Tile) && tok < L && tok + (WHOLE ? 16 : 1) > t_win;
         int64_t blk = 0;
         int slot = 0;
         if (need) {
@@ -294,13 +298,11 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             blk = __ldg(p.block_table + (int64_t)pc.b * p.MB + j);
         }
         const bool bad = blk < 0 || blk >= p.num_blocks;
-        if (bad && (WHOLE || lane < 16)) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+        if (bad) report(p.err_word, PA_DEVERR_BAD_BLOCK);
         p_bad = __ballot_sync(0xffffffffu, bad);
-        if (bad) blk = 0;                      // the copies stay inside the pool; the item's output will be zeros
         const int64_t row = (int64_t)hk * p.bs + slot;
-        p_code = blk * p.block_stride_bytes + row * C::kRow;
+        p_code = need && !bad ? blk * p.block_stride_bytes + row * C::kRow : -1;
         p_scale = (blk * 2 * p.Hkv * p.bs + row) * C::kScRow;
-        if (!WHOLE && !need) p_code = -1;
         if (p_k == 0) {                        // the item's queries, before its first tile is due
             const char *q = reinterpret_cast<const char *>(p.q) +
                             ((int64_t)pc.b * p.H + hk * grp + (pc.it - hk * units_per_kv) * HP) * D * sizeof(T);
@@ -315,36 +317,41 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     const uint32_t f_dst = f_r * C::kRow + swizzle<D>(f_r, f_c) * 16;
     // RS rows on, the swizzle is the same, but for D 256 (4 rows a copy) its 4s bit
     static_assert(RS % 8 == 0 || (D == 256 && RS == 4), "");
-    const uint32_t f_sdst = 2 * C::kHalf + lane * C::kScRow;
-    const int64_t f_soff = (lane & 15) * C::kScRow + (lane >> 4) * v_scale_off;
-    auto fetch = [&](uint32_t slot, int stage) {   // the next tile into the ring
-        if constexpr (WHOLE) {
-            const int64_t off = __shfl_sync(0xffffffffu, p_code, p_i) + f_r * C::kRow + f_c * 16;
-            const int64_t so = __shfl_sync(0xffffffffu, p_scale, p_i) + f_soff;
-            cp_async_small<C::kScRow>(slot + f_sdst, fp.scales + so);
-            const char *ks = p.k_pool + off, *vs = p.v_pool + off;
+    const uint32_t f_sdst = 2 * C::kCodes + lane * C::kScRow;
+    const char *f_k = p.k_pool + f_r * C::kRow + f_c * 16, *f_v = p.v_pool + f_r * C::kRow + f_c * 16;
+    const uint8_t *f_s = fp.scales + (lane & 15) * C::kScRow + (lane >> 4) * v_scale_off;
+    auto fetch = [&](uint32_t slot) {          // the next tile into the ring
 #pragma unroll
-            for (int i = 0; i < 16 / RS; ++i) {
-                const uint32_t dst = slot + (D == 256 && (i & 1) ? f_dst ^ 64u : f_dst) + i * RS * C::kRow;
-                cp_async16(dst, ks + i * RS * C::kRow);
-                cp_async16(dst + C::kHalf, vs + i * RS * C::kRow);
-            }
-            if (p_bad != 0 && ((p_bad >> p_i) & 1u)) bad_bits |= 1u << stage;
-        } else {
-            const bool ok = p_code >= 0;
-            const int64_t so = ok ? p_scale + (lane >> 4) * v_scale_off : 0;
-            cp_async_small<C::kScRow>(slot + f_sdst, fp.scales + so, ok ? C::kScRow : 0);
+        for (int half = 0; half < kFp4Halves; ++half, slot += C::kHalf) {
+            if constexpr (WHOLE) {
+                const int64_t off = __shfl_sync(0xffffffffu, p_code, p_i * kFp4Halves + half);
+                const int64_t so = __shfl_sync(0xffffffffu, p_scale, p_i * kFp4Halves + half);
+                if (off < 0) continue;         // nothing there that is attended to, or a bad entry
+                cp_async_small<C::kScRow>(slot + f_sdst, f_s + so);
+                const char *ks = f_k + off, *vs = f_v + off;
 #pragma unroll
-            for (int i = 0; i < 16 / RS; ++i) {
-                const int r = i * RS + f_r;
-                const int64_t ro = __shfl_sync(0xffffffffu, p_code, r);
-                const int64_t off = ro < 0 ? 0 : ro + f_c * 16;
-                const uint32_t dst = slot + r * C::kRow + swizzle<D>(r, f_c) * 16;
-                cp_async16(dst, p.k_pool + off, ro < 0 ? 0 : 16);
-                cp_async16(dst + C::kHalf, p.v_pool + off, ro < 0 ? 0 : 16);
+                for (int i = 0; i < 16 / RS; ++i) {
+                    const uint32_t dst = slot + (D == 256 && (i & 1) ? f_dst ^ 64u : f_dst) + i * RS * C::kRow;
+                    cp_async16(dst, ks + i * RS * C::kRow);
+                    cp_async16(dst + C::kCodes, vs + i * RS * C::kRow);
+                }
+            } else {
+                const int64_t mine = __shfl_sync(0xffffffffu, p_code, half * 16 + (lane & 15));
+                const int64_t so = __shfl_sync(0xffffffffu, p_scale, half * 16 + (lane & 15));
+                if (mine >= 0) cp_async_small<C::kScRow>(slot + f_sdst, fp.scales + so + (lane >> 4) * v_scale_off);
+#pragma unroll
+                for (int i = 0; i < 16 / RS; ++i) {
+                    const int r = i * RS + f_r;
+                    const int64_t off = __shfl_sync(0xffffffffu, p_code, half * 16 + r);
+                    if (off < 0) continue;
+                    const uint32_t dst = slot + r * C::kRow + swizzle<D>(r, f_c) * 16;
+                    cp_async16(dst, p.k_pool + off + f_c * 16);
+                    cp_async16(dst + C::kCodes, p.v_pool + off + f_c * 16);
+                }
             }
-            if (p_bad != 0) bad_bits |= 1u << stage;
         }
+        if (p_bad != 0 && (!WHOLE || ((p_bad >> (p_i * kFp4Halves)) & ((1u << kFp4Halves) - 1u)) != 0))
+            bad_tiles |= 1u << (S - 2);
         ++p_i;
         --p_left;
     };
@@ -352,7 +359,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     // ---- consumer side -------------------------------------------------------
     uint32_t qf[NT][MT][2];                    // Q^T as MMA B fragments
     float cs[NT][2];                           // scale * log2(e) * 2^e of columns 2 tig, 2 tig + 1
-    float o[NT][MT][4], m[NT][2], l[NT][2];
+    float o[NT][MT][4], m[NT][2], l[NT][2], nm[kFp4Halves][2][NT][2];
     auto load_q = [&](int b, int it) {
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
 #pragma unroll
@@ -409,69 +416,82 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         }
     };
 
-    // bias0, bias1: added to the scores of this lane's two rows (0, or -inf outside the item)
-    auto tile = [&](uint32_t codes, float bias0, float bias1) {
-        const uint32_t sc = codes + 2 * C::kHalf;
+    // Scores are taken relative to the columns' references m: nm[half][r][.] is
+    // -m, or -inf if this lane's row r of the half lies outside the item.
+    auto tile = [&](uint32_t slot) {
         const int rk = tau<D>(gid);
-        // K rows rk and rk + 8 of this lane, and their scales
-        uint32_t kw[2][KW], ks[2][(KW + 1) / 2];
+        float c[kFp4Halves][NT][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = rk + 8 * r;
-            if constexpr (D == 256) {
-                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig) * 16, kw[r]);
-                lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig + 1) * 16, kw[r] + 4);
-            } else {
-                lds_words<KW>(codes + row * C::kRow + (D == 128 ? swizzle<D>(row, tig) * 16 : tig * 8), kw[r]);
+        for (int half = 0; half < kFp4Halves; ++half) {
+            const uint32_t codes = slot + half * C::kHalf, sc = codes + 2 * C::kCodes;
+            // K rows rk and rk + 8 of this lane, and their scales
+            uint32_t kw[2][KW], ks[2][(KW + 1) / 2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = rk + 8 * r;
+                if constexpr (D == 256) {
+                    lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig) * 16, kw[r]);
+                    lds_words<4>(codes + row * C::kRow + swizzle<D>(row, 2 * tig + 1) * 16, kw[r] + 4);
+                } else {
+                    lds_words<KW>(codes + row * C::kRow + (D == 128 ? swizzle<D>(row, tig) * 16 : tig * 8), kw[r]);
+                }
+                const uint32_t s = lds_bytes<KW / 2>(sc + row * C::kScRow + tig * (KW / 2));
+#pragma unroll
+                for (int i = 0; i < KW / 2; ++i) ks[r][i] = e4m3x2_to_f16x2(__byte_perm(s, 0, i * 0x11));
             }
-            const uint32_t s = lds_bytes<KW / 2>(sc + row * C::kScRow + tig * (KW / 2));
 #pragma unroll
-            for (int i = 0; i < KW / 2; ++i) ks[r][i] = e4m3x2_to_f16x2(__byte_perm(s, 0, i * 0x11));
-        }
-        float c[NT][4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < 4; ++i) c[half][nt][i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+            for (int w = 0; w < KW; ++w) {
+                const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
+                const uint32_t a[4] = {hmul2_u32(e2m1x2_to_f16x2<0>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
+                                       hmul2_u32(e2m1x2_to_f16x2<1>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
+                const uint32_t d[4] = {hmul2_u32(e2m1x2_to_f16x2<2>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
+                                       hmul2_u32(e2m1x2_to_f16x2<3>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
-            const uint32_t a[4] = {hmul2_u32(e2m1x2_to_f16x2<0>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<0>(kw[1][w]), s1),
-                                   hmul2_u32(e2m1x2_to_f16x2<1>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<1>(kw[1][w]), s1)};
-            const uint32_t d[4] = {hmul2_u32(e2m1x2_to_f16x2<2>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<2>(kw[1][w]), s1),
-                                   hmul2_u32(e2m1x2_to_f16x2<3>(kw[0][w]), s0), hmul2_u32(e2m1x2_to_f16x2<3>(kw[1][w]), s1)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                MmaOp<__half>::run(c[nt], a, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-                MmaOp<__half>::run(c[nt], d, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    MmaOp<__half>::run(c[half][nt], a, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                    MmaOp<__half>::run(c[half][nt], d, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                }
             }
         }
 
         // scores in the log2 domain, relative to the columns' references
-        float x[NT][4];
+        float x[kFp4Halves][NT][4];
         bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int half = 0; half < kFp4Halves; ++half)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (P == 2) c[nt][i] += __shfl_xor_sync(0xffffffffu, c[nt][i], 2);
-                x[nt][i] = fmaf(c[nt][i], cs[nt][i & 1], (i < 2 ? bias0 : bias1) - m[nt][i & 1]);
-                over = over || x[nt][i] > 8.f;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (P == 2) c[half][nt][i] += __shfl_xor_sync(0xffffffffu, c[half][nt][i], 2);
+                    x[half][nt][i] = fmaf(c[half][nt][i], cs[nt][i & 1], nm[half][i >> 1][nt][i & 1]);
+                    over = over || x[half][nt][i] > 8.f;
+                }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float y0 = fmaf(c[nt][j], cs[nt][j], bias0), y1 = fmaf(c[nt][j + 2], cs[nt][j], bias1);
-                    float mx = fmaxf(m[nt][j], fmaxf(y0, y1));
+                    float y[2 * kFp4Halves], mx = m[nt][j];
+#pragma unroll
+                    for (int i = 0; i < 2 * kFp4Halves; ++i) {
+                        y[i] = nm[i / 2][i & 1][nt][j] == -INFINITY ? -INFINITY : c[i / 2][nt][(i & 1) * 2 + j] * cs[nt][j];
+                        mx = fmaxf(mx, y[i]);
+                    }
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
                     const float f = ex2_approx(m[nt][j] - mx);
                     m[nt][j] = mx;
-                    x[nt][j] = y0 - mx;
-                    x[nt][j + 2] = y1 - mx;
                     l[nt][j] *= f;
+#pragma unroll
+                    for (int i = 0; i < 2 * kFp4Halves; ++i) {
+                        if (nm[i / 2][i & 1][nt][j] != -INFINITY) nm[i / 2][i & 1][nt][j] = -mx;
+                        x[i / 2][nt][(i & 1) * 2 + j] = y[i] - mx;
+                    }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         o[nt][mt][j] *= f;
@@ -479,56 +499,61 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
                     }
                 }
         }
-        uint32_t pf[NT][2];                    // P^T as MMA B fragments
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+        for (int half = 0; half < kFp4Halves; ++half) {
+            const uint32_t codes = slot + half * C::kHalf;
+            uint32_t pf[NT][2];                // P^T as MMA B fragments
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = ex2_approx(x[half][nt][i]);
+                    l[nt][i & 1] += w[i];
+                    if (P == 2 && tig >= 2) w[i] -= __half2float(__float2half_rn(w[i]));
+                }
+                pf[nt][0] = movmatrix_trans(Elem<__half>::pack2(w[0], w[1]));
+                pf[nt][1] = movmatrix_trans(Elem<__half>::pack2(w[2], w[3]));
+            }
+
+            // V rows of this lane's token pairs (t0, t1) and (t0 + 8, t1 + 8)
+            const int t0 = tau<D>(2 * tig), t1 = tau<D>(2 * tig + 1);
+            const uint32_t vc = codes + C::kCodes, vs = codes + 2 * C::kCodes + C::kScales;
+            uint32_t vw[4][VW], ss[2][(VW + 1) / 2];
+            constexpr int VB = VW == 4 ? 2 : 1;    // scale bytes per lane and row
+            uint32_t sb[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = ex2_approx(x[nt][i]);
-                l[nt][i & 1] += w[i];
-                if (P == 2 && tig >= 2) w[i] -= __half2float(__float2half_rn(w[i]));
+                const int row = (i & 1 ? t1 : t0) + 8 * (i >> 1);
+                const int byte = gid * (D / 16);   // of the row
+                lds_words<VW>(vc + row * C::kRow + swizzle<D>(row, byte / 16) * 16 + byte % 16, vw[i]);
+                sb[i] = lds_bytes<VB>(vs + row * C::kScRow + (D == 64 ? gid / 2 : gid * VB));
             }
-            pf[nt][0] = movmatrix_trans(Elem<__half>::pack2(w[0], w[1]));
-            pf[nt][1] = movmatrix_trans(Elem<__half>::pack2(w[2], w[3]));
-        }
-
-        // V rows of this lane's token pairs (t0, t1) and (t0 + 8, t1 + 8)
-        const int t0 = tau<D>(2 * tig), t1 = tau<D>(2 * tig + 1);
-        const uint32_t vc = codes + C::kHalf, vs = sc + C::kScHalf;
-        uint32_t vw[4][VW], ss[2][(VW + 1) / 2];
-        constexpr int VB = VW == 4 ? 2 : 1;    // scale bytes per lane and row
-        uint32_t sb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = (i & 1 ? t1 : t0) + 8 * (i >> 1);
-            const int byte = gid * (D / 16);   // of the row
-            lds_words<VW>(vc + row * C::kRow + swizzle<D>(row, byte / 16) * 16 + byte % 16, vw[i]);
-            sb[i] = lds_bytes<VB>(vs + row * C::kScRow + (D == 64 ? gid / 2 : gid * VB));
-        }
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+                for (int k = 0; k < VB; ++k)
+                    ss[i][k] = e4m3x2_to_f16x2(__byte_perm(sb[2 * i], sb[2 * i + 1], k | ((4 + k) << 4)));
 #pragma unroll
-            for (int k = 0; k < VB; ++k) ss[i][k] = e4m3x2_to_f16x2(__byte_perm(sb[2 * i], sb[2 * i + 1], k | ((4 + k) << 4)));
+            for (int v = 0; v < VW; ++v) {
+                uint32_t ev[2], od[2];         // even and odd elements of a token pair
 #pragma unroll
-        for (int v = 0; v < VW; ++v) {
-            uint32_t ev[2], od[2];             // even and odd elements of a token pair
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t a = vw[2 * i][v], b = vw[2 * i + 1][v];
+                    ev[i] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+                    od[i] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                }
+                const uint32_t s0 = ss[0][VB == 2 ? v / 2 : 0], s1 = ss[1][VB == 2 ? v / 2 : 0];
+                auto step = [&](int j, uint32_t e0, uint32_t d0, uint32_t e1, uint32_t d1) {
+                    const uint32_t a[4] = {hmul2_u32(e0, s0), hmul2_u32(d0, s0), hmul2_u32(e1, s1), hmul2_u32(d1, s1)};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t a = vw[2 * i][v], b = vw[2 * i + 1][v];
-                ev[i] = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
-                od[i] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+                    for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(o[nt][4 * v + j], a, pf[nt][0], pf[nt][1]);
+                };
+                step(0, e2m1x2_to_f16x2<0>(ev[0]), e2m1x2_to_f16x2<0>(od[0]), e2m1x2_to_f16x2<0>(ev[1]), e2m1x2_to_f16x2<0>(od[1]));
+                step(1, e2m1x2_to_f16x2<1>(ev[0]), e2m1x2_to_f16x2<1>(od[0]), e2m1x2_to_f16x2<1>(ev[1]), e2m1x2_to_f16x2<1>(od[1]));
+                step(2, e2m1x2_to_f16x2<2>(ev[0]), e2m1x2_to_f16x2<2>(od[0]), e2m1x2_to_f16x2<2>(ev[1]), e2m1x2_to_f16x2<2>(od[1]));
+                step(3, e2m1x2_to_f16x2<3>(ev[0]), e2m1x2_to_f16x2<3>(od[0]), e2m1x2_to_f16x2<3>(ev[1]), e2m1x2_to_f16x2<3>(od[1]));
             }
-            const uint32_t s0 = ss[0][VB == 2 ? v / 2 : 0], s1 = ss[1][VB == 2 ? v / 2 : 0];
-            auto step = [&](int j, uint32_t e0, uint32_t d0, uint32_t e1, uint32_t d1) {
-                const uint32_t a[4] = {hmul2_u32(e0, s0), hmul2_u32(d0, s0), hmul2_u32(e1, s1), hmul2_u32(d1, s1)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(o[nt][4 * v + j], a, pf[nt][0], pf[nt][1]);
-            };
-            step(0, e2m1x2_to_f16x2<0>(ev[0]), e2m1x2_to_f16x2<0>(od[0]), e2m1x2_to_f16x2<0>(ev[1]), e2m1x2_to_f16x2<0>(od[1]));
-            step(1, e2m1x2_to_f16x2<1>(ev[0]), e2m1x2_to_f16x2<1>(od[0]), e2m1x2_to_f16x2<1>(ev[1]), e2m1x2_to_f16x2<1>(od[1]));
-            step(2, e2m1x2_to_f16x2<2>(ev[0]), e2m1x2_to_f16x2<2>(od[0]), e2m1x2_to_f16x2<2>(ev[1]), e2m1x2_to_f16x2<2>(od[1]));
-            step(3, e2m1x2_to_f16x2<3>(ev[0]), e2m1x2_to_f16x2<3>(od[0]), e2m1x2_to_f16x2<3>(ev[1]), e2m1x2_to_f16x2<3>(od[1]));
         }
     };
 
@@ -611,11 +636,12 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         p_end = min(pc.n, w1 - pc.first - kFp4Item);
 #pragma unroll 1
         for (int i = -1; i < S - 1; ++i) {     // the first batch, and its first tiles
-            if (p_left > 0) fetch(ring + i * C::kStage, i);
+            bad_tiles >>= 1;
+            if (p_left > 0) fetch(ring + i * C::kStage);
             if (i >= 0) cp_async_commit();
             if (p_left == 0 && p_more) look_up();
         }
-        int stage = 0;
+        uint32_t now = ring, free_slot = ring + (S - 1) * C::kStage;   // the tile's slot, that of the tile before
 #pragma unroll 1
         for (; cc.b < p.B && cc.first < w1; cc.next(pre, p.B, items_per_seq)) {
             int32_t k = max(0, w0 - cc.first - kFp4Item);
@@ -624,37 +650,50 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             const bool whole = k == 0 && end == cc.n;
             load_q(cc.b, cc.it);
             const int32_t hi = lens[cc.b], lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
+            // tiles with rows outside the item: its first (of a window) and its last
+            const int32_t lo_edge = lo % kFp4Tile != 0 ? 0 : -1, hi_edge = hi % kFp4Tile != 0 ? cc.n - 1 : -1;
+            int32_t first_k = k;               // where nm is to be set anew
             bool bad = false;
-            int32_t tok0 = (lo / kFp4Tile + k) * kFp4Tile;
 #pragma unroll 1
-            for (; k < end; ++k, tok0 += kFp4Tile) {
+            for (; k < end; ++k) {
                 cp_async_wait<S - 2>();
                 __syncwarp();                  // every lane's copies have landed, and the tile before is read
-                const int free_stage = stage == 0 ? S - 1 : stage - 1;
-                if (p_left > 0) fetch(ring + free_stage * C::kStage, free_stage);
+                if (bad_tiles != 0) {
+                    bad |= bad_tiles & 1u;
+                    bad_tiles >>= 1;
+                }
+                if (p_left > 0) fetch(free_slot);
                 cp_async_commit();
                 if (p_left == 0 && p_more) look_up();
-                if (bad_bits != 0) {
-                    bad |= (bad_bits >> stage) & 1u;
-                    bad_bits &= ~(1u << stage);
-                }
-                const uint32_t codes = ring + stage * C::kStage;
-                float bias0 = 0.f, bias1 = 0.f;
-                if (tok0 < lo || tok0 + kFp4Tile > hi) {
-                    // rows outside [lo, hi): no weight, and scales of 0, for a slot that
-                    // nobody wrote may hold NaN, which no weight would remove
-                    const int32_t r0 = tok0 + tau<D>(gid), r1 = r0 + 8, r = tok0 + (lane & 15);
-                    bias0 = r0 < lo || r0 >= hi ? -INFINITY : 0.f;
-                    bias1 = r1 < lo || r1 >= hi ? -INFINITY : 0.f;
-                    if (r < lo || r >= hi) {
+                const bool edge = k == lo_edge || k == hi_edge;
+                if (edge || k == first_k) {
+                    // rows outside: no weight, and scales of 0, for a slot that nobody
+                    // wrote may hold NaN, which no weight would remove
+                    const int32_t tok0 = (lo / kFp4Tile + k) * kFp4Tile;
 #pragma unroll
-                        for (int i = 0; i < C::kScRow; i += 4)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(codes + f_sdst + i), "r"(0) : "memory");
+                    for (int half = 0; half < kFp4Halves; ++half) {
+                        const int32_t r = tok0 + half * 16 + (lane & 15);
+                        if (r < lo || r >= hi) {
+#pragma unroll
+                            for (int i = 0; i < C::kScRow; i += 4)
+                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(now + half * C::kHalf + f_sdst + i), "r"(0)
+                                             : "memory");
+                        }
+#pragma unroll
+                        for (int row = 0; row < 2; ++row) {
+                            const int32_t rr = tok0 + half * 16 + tau<D>(gid) + 8 * row;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) nm[half][row][nt][j] = rr < lo || rr >= hi ? -INFINITY : -m[nt][j];
+                        }
                     }
                     __syncwarp();
                 }
-                tile(codes, bias0, bias1);
-                stage = stage + 1 == S ? 0 : stage + 1;
+                tile(now);
+                if (k == lo_edge) first_k = k + 1;   // the rows are inside again
+                free_slot = now;
+                now = now + C::kStage == ring + S * C::kStage ? ring : now + C::kStage;
             }
             if (end < cc.n) {                  // the last part of the run: the ring is free for its record
                 cp_async_wait<0>();
@@ -729,8 +768,8 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     const int32_t prev = __shfl_sync(0xffffffffu, mine, before != 0 ? 31 - __clz(before) : lane);
     const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0 || prev != mine));
     if (warp == 0 && mine >= 0)
-        list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kWarpRing)
-                                          : reinterpret_cast<const float *>(smem + (size_t)W * C::kWarpRing) +
+        list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kRingBytes)
+                                          : reinterpret_cast<const float *>(smem + (size_t)W * C::kRingBytes) +
                                                 (size_t)(lane >> 1) * C::kRec;
     __syncthreads();
     // a team of warps per item, as many as its slabs, the items of a CTA side by side
@@ -868,7 +907,7 @@ cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int k
     const int heads = plan->nt * 8 / (dtype == PA_F32 ? 2 : 1);
     plan->units_per_kv = (group + heads - 1) / heads;
     plan->items = (int64_t)batch * kv_heads * plan->units_per_kv;
-    plan->whole_tiles = block_size % kFp4Tile == 0;
+    plan->whole_tiles = block_size % 16 == 0;
     const int64_t total = plan->items * max_tiles_per_item;
     if (total >= (int64_t)INT32_MAX / 2) return cudaErrorInvalidValue;
     return dispatch_fp4(dtype, head_dim, plan->nt, plan->whole_tiles, [&](auto l) { return l.plan(batch, total, plan); });
