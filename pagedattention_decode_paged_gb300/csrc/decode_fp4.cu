@@ -90,6 +90,20 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// W equal runs of T places: run w starts at floor(w T / W), here without a
+// 64-bit division.
+struct Fp4Runs {
+    int32_t T, W, q, r;
+    __device__ __forceinline__ Fp4Runs(int32_t places, int32_t runs) : T(places), W(runs), q(places / runs), r(places % runs) {}
+    __device__ __forceinline__ int32_t start(int32_t w) const { return w * q + w * r / W; }
+    __device__ __forceinline__ int32_t owner(int32_t t) const {   // of place t
+        int32_t w = min(W - 1, (int32_t)(((float)t + 0.5f) * ((float)W / (float)T)));
+        while (w > 0 && start(w) > t) --w;
+        while (w + 1 < W && start(w + 1) <= t) ++w;
+        return w;
+    }
+};
+
 // A place in the index space of the work: an item of n tiles covers kFp4Item +
 // n places from `first` on, its tiles the last n.
 struct Fp4Cursor {
@@ -217,6 +231,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __shared__ const float *list[2][32];       // records to merge
     __shared__ float *merged_to[2];            // null: the output
     __shared__ int32_t snap[32 * kFp4Group + 1];
+    __shared__ int32_t group_rec[2 * W + 1];   // of the items merged in this CTA: first record, and its place in list[0]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     unsigned char *ring_p = smem + (size_t)warp * C::kRingBytes;
@@ -239,8 +254,9 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     const int nC = min((int)gridDim.x, (Tn + W * kFp4MinTiles - 1) / (W * kFp4MinTiles));
     const int cta = blockIdx.x;
     if (cta >= nC) return;
+    const Fp4Runs runs(Tn, nC);
     for (int c = threadIdx.x; c <= nC; c += C::kThreads) {
-        int32_t t = slice_start(c, Tn, nC);
+        int32_t t = runs.start(c);
         if (c > 0 && c < nC) {
             Fp4Cursor x;
             x.seek(pre, p.B, items_per_seq, t);
@@ -250,11 +266,12 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     }
     __syncthreads();
     bool over = false;
-    for (int c = threadIdx.x; c < nC; c += C::kThreads) over |= snap[c + 1] - snap[c] > Tn / nC + W * kFp4Snap;
+    for (int c = threadIdx.x; c < nC; c += C::kThreads) over |= snap[c + 1] - snap[c] > runs.q + W * kFp4Snap;
     const bool cut = __syncthreads_or(over);   // items are cut between CTAs
-    const int32_t c0 = cut ? slice_start(cta, Tn, nC) : snap[cta], c1 = cut ? slice_start(cta + 1, Tn, nC) : snap[cta + 1];
+    const int32_t c0 = cut ? runs.start(cta) : snap[cta], c1 = cut ? runs.start(cta + 1) : snap[cta + 1];
     if (c0 >= c1) return;
-    const int32_t w0 = c0 + slice_start(warp, c1 - c0, W), w1 = c0 + slice_start(warp + 1, c1 - c0, W);
+    const Fp4Runs warp_runs(c1 - c0, W);
+    const int32_t w0 = c0 + warp_runs.start(warp), w1 = c0 + warp_runs.start(warp + 1);
     if (lane < 2) rec_first[2 * warp + lane] = -1;
 
     const int grp = p.H / p.Hkv;               // query heads per kv head
@@ -712,47 +729,63 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __syncthreads();
 
     // ---- merges --------------------------------------------------------------
-    // The records of[from, to) of one item, merged into its output, or into
-    // the record dst.  The lists' entries lie in shared memory or in the
-    // workspace, where other CTAs wrote them: volatile loads read L2.  One copy
+    // Element i (a lane's slab) of the records of[from, to) of one item, merged into
+    // its output, or into the record dst.  The records lie in shared memory or in
+    // the workspace, where other CTAs wrote them: volatile loads read L2.  One copy
     // of this code serves every merge: what a CTA runs once is paid for in
     // instruction fetches.
-    auto merge = [&](const float *const *of, int from, int to, int b, int it, bool whole, float *dst, int tid, int threads) {
+    constexpr int kBatch = 8;                  // records loaded at a time
+    const int elements = (grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS) * 32;   // one head: the slabs of j = 0
+    auto merge = [&](const float *const *of, int from, int to, int b, int it, float *dst, int i) {
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
-        // heads the item may have, a slab of 32 lanes at a time (one head: the slabs of j = 0)
-        const int elements = (grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS) * 32;
-        for (int i = tid; i < elements; i += threads) {
-            const int ln = i & 31, h = head_of(i >> 5, ln), d = dim_of(i >> 5, ln);
-            float M = kFp4Empty, sum = 0.f;
-            bool bad = false;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int r = from; r < to; ++r) {
-                const float *rec = of[r];
-                const float mr = ld_volatile(rec + HP * D + h), lr = ld_volatile(rec + HP * D + HP + h);
-                const float4 a = ld_volatile4(rec + i * 4);
-                const float top = fmaxf(M, mr), f = ex2_approx(M - top), w = ex2_approx(mr - top);
-                M = top;
-                bad |= lr < 0.f;
-                sum = fmaf(sum, f, lr * w);
-                acc.x = fmaf(acc.x, f, a.x * w);
-                acc.y = fmaf(acc.y, f, a.y * w);
-                acc.z = fmaf(acc.z, f, a.z * w);
-                acc.w = fmaf(acc.w, f, a.w * w);
+        const int ln = i & 31, h = head_of(i >> 5, ln), d = dim_of(i >> 5, ln);
+        float M = kFp4Empty, sum = 0.f;
+        bool bad = false;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int r = from; r < to; r += kBatch) {
+            const float *rec[kBatch];
+            float mr[kBatch], lr[kBatch];
+            float4 a[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) rec[k] = of[min(r + k, to - 1)];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                mr[k] = ld_volatile(rec[k] + HP * D + h);
+                lr[k] = ld_volatile(rec[k] + HP * D + HP + h);
+                a[k] = ld_volatile4(rec[k] + i * 4);
             }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(dst + i * 4) = acc;
-                if (d == 0) {
-                    dst[HP * D + h] = M;
-                    dst[HP * D + HP + h] = bad ? -1.f : sum;
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mr[k]);
+            const float f = ex2_approx(M - top);
+            M = top;
+            sum *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (r + k < to) {
+                    const float w = ex2_approx(mr[k] - top);
+                    bad |= lr[k] < 0.f;
+                    sum = fmaf(lr[k], w, sum);
+                    acc.x = fmaf(a[k].x, w, acc.x);
+                    acc.y = fmaf(a[k].y, w, acc.y);
+                    acc.z = fmaf(a[k].z, w, acc.z);
+                    acc.w = fmaf(a[k].w, w, acc.w);
                 }
-            } else if (h0 + h < grp) {
-                const float f = fp.v_g / sum;
-                T *o4 = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + d;
-                const float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-                if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(o4) = y;
-                else *reinterpret_cast<uint2 *>(o4) = make_uint2(Elem<T>::pack2(y.x, y.y), Elem<T>::pack2(y.z, y.w));
+        }
+        if (dst != nullptr) {
+            *reinterpret_cast<float4 *>(dst + i * 4) = acc;
+            if (d == 0) {
+                dst[HP * D + h] = M;
+                dst[HP * D + HP + h] = bad ? -1.f : sum;
             }
+        } else if (h0 + h < grp) {
+            const float f = fp.v_g / sum;
+            T *o4 = out + ((int64_t)b * p.H + hk * grp + h0 + h) * D + d;
+            const float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(o4) = y;
+            else *reinterpret_cast<uint2 *>(o4) = make_uint2(Elem<T>::pack2(y.x, y.y), Elem<T>::pack2(y.z, y.w));
         }
     };
     // record `slot` of a CTA: 0 its first item, 1 its last one; 2 and 3 the
@@ -766,27 +799,27 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     if (valid == 0) return;
     const uint32_t before = valid & ((1u << lane) - 1u);
     const int32_t prev = __shfl_sync(0xffffffffu, mine, before != 0 ? 31 - __clz(before) : lane);
-    const uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (before == 0 || prev != mine));
-    if (warp == 0 && mine >= 0)
-        list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kRingBytes)
-                                          : reinterpret_cast<const float *>(smem + (size_t)W * C::kRingBytes) +
-                                                (size_t)(lane >> 1) * C::kRec;
+    const bool starts_item = mine >= 0 && (before == 0 || prev != mine);
+    const uint32_t starts = __ballot_sync(0xffffffffu, starts_item);
+    const int groups = __popc(starts), first_group = __ffs(starts) - 1, last_group = 31 - __clz(starts);
+    // whether the first and the last of the items lie partly with the CTAs before and behind
+    const int32_t first_tile = rec_first[first_group] + kFp4Item, last_tile = rec_first[last_group] + kFp4Item;
+    const int shared_first = first_tile < c0 ? first_group : -1;
+    const int shared_last = last_tile >= c0 && last_tile + rec_n[last_group] > c1 ? last_group : -1;
+    if (warp == 0) {
+        if (mine >= 0)
+            list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kRingBytes)
+                                                 : reinterpret_cast<const float *>(smem + (size_t)W * C::kRingBytes) +
+                                                       (size_t)(lane >> 1) * C::kRec;
+        if (starts_item) group_rec[__popc(starts & ((1u << lane) - 1u))] = lane | __popc(before) << 8;
+        if (lane == 0) group_rec[groups] = __popc(valid) << 8;
+    }
     __syncthreads();
-    // a team of warps per item, as many as its slabs, the items of a CTA side by side
-    const int team = min(W, grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS), teams = W / team;
-    int shared_first = -1, shared_last = -1;   // first records of the items shared with CTAs before and after
-    uint32_t left = starts;
 #pragma unroll 1
-    for (int g = 0; left != 0; ++g) {
-        const int r0 = __ffs(left) - 1;
-        left &= left - 1;
-        const uint32_t upto = left != 0 ? (1u << (__ffs(left) - 1)) - 1u : 0xffffffffu;
-        const int32_t first = rec_first[r0] + kFp4Item;      // its first tile
-        const bool whole = first >= c0 && first + rec_n[r0] <= c1;
-        if (!whole) (first < c0 ? shared_first : shared_last) = r0;
-        if (g % teams == warp / team)
-            merge(list[0], __popc(valid & ((1u << r0) - 1u)), __popc(valid & upto), rec_b[r0], rec_it[r0], whole,
-                  global_rec(cta, first < c0 ? 0 : 1), (warp % team) * 32 + lane, team * 32);
+    for (int i = threadIdx.x; i < groups * elements; i += C::kThreads) {
+        const int g = i / elements, r0 = group_rec[g] & 255;
+        float *dst = r0 == shared_first ? global_rec(cta, 0) : r0 == shared_last ? global_rec(cta, 1) : nullptr;
+        merge(list[0], group_rec[g] >> 8, group_rec[g + 1] >> 8, rec_b[r0], rec_it[r0], dst, i - g * elements);
     }
     if (shared_first < 0 && shared_last < 0) return;
 
@@ -804,7 +837,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             int last = 0;
             if (r0 >= 0 && (level == 0 || arrived[k] == 2)) {
                 const int32_t first = rec_first[r0] + kFp4Item;   // its first tile
-                const int o0 = slice_owner(first, Tn, nC), n = slice_owner(first + rec_n[r0] - 1, Tn, nC) - o0 + 1;
+                const int o0 = runs.owner(first), n = runs.owner(first + rec_n[r0] - 1) - o0 + 1;
                 const bool two = n > kFp4Flat, grouped = two && level == 0;
                 const int g0 = grouped ? (cta - o0) / kFp4Group * kFp4Group : 0, gslot = g0 == 0 ? 1 : 0;
                 const int sharers = grouped ? min(kFp4Group, n - g0) : two ? (n + kFp4Group - 1) / kFp4Group : n;
@@ -830,8 +863,9 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         // two items: half the CTA for each
         const int threads = a0 != 0 && a1 != 0 ? C::kThreads / 2 : C::kThreads;
         const int k = a0 != 0 && (int)threadIdx.x < threads ? 0 : 1, r0 = k ? shared_last : shared_first;
-        merge(list[k], 0, sharers_of[k], rec_b[r0], rec_it[r0], merged_to[k] == nullptr, merged_to[k],
-              (int)threadIdx.x % threads, threads);
+#pragma unroll 1
+        for (int i = (int)threadIdx.x % threads; i < elements; i += threads)
+            merge(list[k], 0, sharers_of[k], rec_b[r0], rec_it[r0], merged_to[k], i);
         if (a0 < 2 && a1 < 2) return;
     }
 }
