@@ -15,7 +15,7 @@
  *     g  is one fp32 factor for all keys (k_scale), one for all values
  *        (v_scale), given with every call: 1, or what brings the largest
  *        magnitude of the cache near 6 * 448 when E4M3's range would not
- *        cover it.
+ *        cover it; from 2^-64 to 2^64 (others: PA_ERR_INVALID_ARG).
  *   That is 4.5 bits per value.  The products value(c) * value(s) are exact
  *   in fp16.
  *

@@ -9,7 +9,8 @@ namespace {
 
 int elem_size(int32_t dtype) { return dtype == PA_F32 ? 4 : 2; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool factor_ok(float g) { return isfinite(g) && g > 0.f; }
+// far enough inside fp32 that no scale times factor over- or underflows
+bool factor_ok(float g) { return g >= 0x1p-64f && g <= 0x1p64f; }
 
 // Sizes common to every entry point; `row_bytes`: bytes of a cache row,
 // `stride_bytes`: block_stride in bytes.

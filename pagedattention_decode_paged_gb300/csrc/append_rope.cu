@@ -9,58 +9,174 @@
 //
 // Every element is read once and written once, so the kernel is bound by HBM
 // for prompts and by launch and the dependent loads (position, table entry and
-// cosines, rows) for single tokens.  D/8 lanes hold a row, 8 elements each:
-// 16 bytes of a 16-bit type, so a warp moves whole 128-byte lines.  The mean
-// square is a shuffle sum over those lanes; a rotation pair (i, i + R/2) lies
-// R/16 lanes apart and is one shuffle per element, a pair (2i, 2i + 1) lies
-// in one lane.  A thread keeps its cosines and sines for all the heads of a
-// token that it visits.  The rotation is written with separately rounded
-// products and sums: a few more instructions than fused ones, hidden behind
-// the loads, and the 4-bit codes then are those of the stated formula.
+// cosines) for single tokens.  D/8 lanes hold a row, 8 elements each in two
+// chunks of 4.  With pairs (i, i + R/2) a lane takes chunk i and chunk i + R/2
+// (kSplit): each chunk of a row is still read in whole 128-byte lines, both
+// elements of a pair are in one lane, and its 4 cosines and sines serve both
+// chunks.  With pairs (2i, 2i + 1), or none, the chunks are neighbours.  Only
+// where the halves of R cut a 4-bit group of 16 (R not a multiple of 32) are
+// neighbouring chunks kept and the other elements of the pairs fetched by
+// shuffles (kShuffle).
+//
+// A warp takes a run of the rows of one token: it keeps the token's cosines,
+// sines and the weights for all of them, has kRopeRows rows' loads in flight,
+// and goes through queries, keys and values in loops of their own, which need
+// no per-row selection.  Products and sums are rounded separately, two at a
+// time (f32x2): the results are those of the stated formula operation by
+// operation, and so are the 4-bit codes.
+//
+// Quotients of the 4-bit scheme: q = x r, then q - r (q t - x), with r the
+// correctly rounded reciprocal of t, is the correctly rounded quotient (P. W.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) where nothing over- or underflows; a group with a NaN or a
+// magnitude that could overflow takes IEEE divisions instead.
+#include <float.h>
+
 #include "fp4.cuh"
 #include "pa_rope_fp4.h"
 
 namespace pa {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 8;
+constexpr int kRopeThreads = kRopeWarps * 32;
+constexpr int kRopeRows = 4;       // iterations of rows in flight per warp
+enum RopeMode { kSplit, kNeighbours, kShuffle };
 
-// The row's 8 elements of this lane as 4-bit codes into `dst` (4 bytes) and
-// the group's scale into `sdst`: a group of 16 is two neighbouring lanes.
-// All lanes of the warp call; `write` says whose row goes to the cache.
-__device__ __forceinline__ void store_fp4(const float (&x)[8], float g, bool write, uint32_t *dst, uint8_t *sdst,
-                                          bool first_of_group) {
-    float a = 0.f;
+// --- two fp32 values in one register pair -------------------------------------
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// 4 elements of T: as they are in memory, and as fp32 pairs.
+template <typename T>
+struct Chunk {
+    uint2 v;
+    __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ void unpack(float2 (&x)[2]) const {
+        Elem<T>::unpack2(v.x, x[0].x, x[0].y);
+        Elem<T>::unpack2(v.y, x[1].x, x[1].y);
+    }
+    __device__ __forceinline__ void pack(const float2 (&x)[2]) {
+        v = make_uint2(Elem<T>::pack2(x[0].x, x[0].y), Elem<T>::pack2(x[1].x, x[1].y));
+    }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint2 *>(p) = v; }
+    static __device__ __forceinline__ void load2(const T *p, Chunk &a, Chunk &b) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        a.v = make_uint2(w.x, w.y);
+        b.v = make_uint2(w.z, w.w);
+    }
+    static __device__ __forceinline__ void store2(T *p, const Chunk &a, const Chunk &b) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(a.v.x, a.v.y, b.v.x, b.v.y);
+    }
+};
+template <>
+struct Chunk<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void unpack(float2 (&x)[2]) const { x[0] = make_float2(v.x, v.y), x[1] = make_float2(v.z, v.w); }
+    __device__ __forceinline__ void pack(const float2 (&x)[2]) { v = make_float4(x[0].x, x[0].y, x[1].x, x[1].y); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = v; }
+    static __device__ __forceinline__ void load2(const float *p, Chunk &a, Chunk &b) { a.load(p), b.load(p + 4); }
+    static __device__ __forceinline__ void store2(float *p, const Chunk &a, const Chunk &b) { a.store(p), b.store(p + 4); }
+};
+
+// --- 4-bit groups ---------------------------------------------------------------
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float largest(const float2 (&x)[2]) {
+    return max_nan(max_nan(fabsf(x[0].x), fabsf(x[0].y)), max_nan(fabsf(x[1].x), fabsf(x[1].y)));
+}
+// The factor of one half of the cache: 6 g, its reciprocal, and the magnitude
+// up to which no quotient overflows.
+struct Factor {
+    float g, six_g, r6, limit;
+};
+__device__ __forceinline__ Factor factor_of(float g) {
+    Factor f;
+    f.g = g;
+    f.six_g = __fmul_rn(6.f, g);
+    f.r6 = __frcp_rn(f.six_g);
+    f.limit = f.six_g * 1024.f;
+    return f;
+}
+// The E4M3 code of a group with largest magnitude a, and the value t that its
+// codes are multiples of.
+__device__ __forceinline__ uint32_t group_scale(float a, const Factor &f, float &t) {
+    float q;
+    if (a <= f.limit) {
+        q = __fmul_rn(a, f.r6);
+        q = __fmaf_rn(__fmaf_rn(-q, f.six_g, a), f.r6, q);
+    } else {
+        q = a == a ? __fdiv_rn(a, f.six_g) : 0.f;
+    }
+    const uint32_t code = f32_to_e4m3(q);
+    t = __fmul_rn(f16x2_to_float2(e4m3x2_to_f16x2(code)).x, f.g);
+    return code;
+}
+// Two bytes of codes of x / t; `plain` if the group's largest magnitude was
+// within the factor's limit.
+__device__ __forceinline__ uint32_t group_codes(const float2 (&x)[2], float t, bool plain) {
+    if (!(t > 0.f)) return 0;
+    float2 y[2];
+    if (plain) {
+        const float2 tt = both(t), minus_r = both(-__frcp_rn(t));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));   // a NaN loses against a number
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    const uint32_t code = f32_to_e4m3(__fdiv_rn(a, __fmul_rn(6.f, g)));
-    const float t = __fmul_rn(f16x2_to_float2(e4m3x2_to_f16x2(code)).x, g);
-    if (!write) return;
-    uint32_t w = 0;
-    if (t > 0.f) {
+        for (int j = 0; j < 2; ++j) {              // (q t - x) (-r) + q keeps the sign of a zero
+            const float2 minus_x = mul2(x[j], both(-1.f));
+            y[j] = mul2(minus_x, minus_r);
+            y[j] = fma2(fma2(y[j], tt, minus_x), minus_r, y[j]);
+        }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float lo = __fdiv_rn(x[2 * j], t), hi = __fdiv_rn(x[2 * j + 1], t);
-            lo = lo == lo ? lo : 0.f;
-            hi = hi == hi ? hi : 0.f;
-            w |= f32x2_to_e2m1x2(lo, hi) << (8 * j);
+        for (int j = 0; j < 2; ++j) {
+            y[j].x = x[j].x == x[j].x ? __fdiv_rn(x[j].x, t) : 0.f;
+            y[j].y = x[j].y == x[j].y ? __fdiv_rn(x[j].y, t) : 0.f;
         }
     }
-    *dst = w;
-    if (first_of_group) *sdst = (uint8_t)code;
+    return f32x2_to_e2m1x2(y[0].x, y[0].y) | f32x2_to_e2m1x2(y[1].x, y[1].y) << 8;
 }
 
-// grid: x = sequence, y = stripe of tokens, z = stripe of rows of a token.
-template <typename T, int D, bool FP4>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p) {
+enum RowKind { kQuery, kKey, kValue };
+template <RowKind K>
+struct Kind {
+    static constexpr RowKind value = K;
+};
+
+// grid: x = sequence, y = 8 warps of (token, run of its rows) each.
+template <typename T, int D, bool FP4, RopeMode MODE>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int runs) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int LPR = D / 8;                     // lanes per row
-    constexpr int RPB = kRopeThreads / LPR;        // rows per pass
+    constexpr int RPW = 32 / LPR;                  // rows per iteration of a warp
     const int b = blockIdx.x;
     const int n = p.counts != nullptr ? p.counts[b] : p.T;
     const int32_t start = p.positions[b];
-    const bool reporter = threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    const bool reporter = threadIdx.x == 0 && blockIdx.y == 0;
     if (n < 0 || n > p.T) {
         if (reporter) report(p.err_word, PA_DEVERR_BAD_LEN);
         return;
@@ -69,123 +185,262 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
                          (p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
     if (bad_pos && reporter) report(p.err_word, PA_DEVERR_BAD_POS);
 
+    const int lane = threadIdx.x & 31, sub = lane % LPR, lr = lane / LPR;
     const int HQ = p.q != nullptr ? p.H : 0;
-    const int rows = HQ + 2 * p.Hkv;               // of a token
-    const int per_pass = RPB / rows > 1 ? RPB / rows : 1;   // tokens side by side when rows are few
-    const int lr = threadIdx.x / LPR, sub = threadIdx.x % LPR, d0 = sub * 8;
-    const int side = per_pass > 1 ? lr / rows : 0;
-    const int first_row = per_pass > 1 ? lr - side * rows : lr + (int)blockIdx.z * RPB;
-    const int row_step = per_pass > 1 ? rows : RPB * (int)gridDim.z;
-    const bool lane_rot = d0 < p.R;
-    const int half = p.R / 16;                     // lanes between the two elements of a pair
-    const int partner = !p.pairs && lane_rot ? (int)(threadIdx.x & 31) + (sub < half ? half : -half) : (int)(threadIdx.x & 31);
+    // iterations over queries, then keys, then values of a token
+    const int nq = (HQ + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
+    const int per_run = (nq + 2 * nk + runs - 1) / runs;
+    // this lane's chunks, and whether they are rotated
+    const bool turn = sub < p.R / 8;
+    const bool apart = MODE == kSplit && turn;
+    const int da = apart ? 4 * sub : 8 * sub, db = apart ? p.R / 2 + 4 * sub : 8 * sub + 4;
+    const int half = p.R / 16;                     // kShuffle: lanes between the two elements of a pair
+    const int partner = MODE == kShuffle && turn ? lane + (sub < half ? half : -half) : lane;
 
-    for (int t0 = (int)blockIdx.y * per_pass; t0 < n; t0 += (int)gridDim.y * per_pass) {
-        const int t = t0 + side;
-        const bool live = t < n && side < per_pass;
-        const int32_t pos = start + t;
+    const int64_t units = (int64_t)n * runs;
+#pragma unroll 1
+    for (int64_t unit = (int64_t)blockIdx.y * kRopeWarps + (threadIdx.x >> 5); unit < units;
+         unit += (int64_t)gridDim.y * kRopeWarps) {
+        const int t = units <= INT32_MAX ? (int)((uint32_t)unit / (uint32_t)runs) : (int)(unit / runs);
+        const int run = (int)(unit - (int64_t)t * runs);
+        const int i0 = run * per_run, i1 = min(i0 + per_run, nq + 2 * nk);
         const int64_t token = (int64_t)b * p.T + t;
-        int64_t blk = -1;
-        int slot = 0;
-        float c[8], s[8];
+        if (bad_pos) {                             // zeros for the queries, nothing for the cache
+            Chunk<T> z;
+            z.zero();
+            for (int i = i0; i < min(i1, nq); ++i) {
+                const int h = i * RPW + lr;
+                if (h < HQ) Chunk<T>::store2(reinterpret_cast<T *>(p.q_out) + (token * p.H + h) * D + 8 * sub, z, z);
+            }
+            continue;
+        }
+        const int32_t pos = start + t;
+        const int32_t bj = pos / p.bs, slot = pos - bj * p.bs;
+        const int64_t blk = __ldg(p.block_table + (int64_t)b * p.MB + bj);
+        // cosines and sines: of pairs of elements, -sine first where the formula subtracts
+        float2 c[MODE == kSplit ? 2 : 4], s[MODE == kSplit ? 2 : 4], ns[2];
+        if (turn) {
+            const float *cs = p.cos_sin + (int64_t)pos * p.R;
+            if constexpr (MODE == kShuffle) {
+                const int i = sub < half ? 8 * sub : 8 * sub - p.R / 2;
+                float c8[8], s8[8];
+                load8(cs + i, c8);
+                load8(cs + p.R / 2 + i, s8);
+                const float sign = sub < half ? -1.f : 1.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
-        if (live && !bad_pos) {
-            const int j = pos / p.bs;
-            slot = pos - j * p.bs;
-            blk = p.block_table[(int64_t)b * p.MB + j];
-            if (lane_rot) {
-                const float *cs = p.cos_sin + (int64_t)pos * p.R;
-                if (p.pairs) {
-                    const float4 c4 = *reinterpret_cast<const float4 *>(cs + d0 / 2);
-                    const float4 s4 = *reinterpret_cast<const float4 *>(cs + p.R / 2 + d0 / 2);
-                    c[0] = c[1] = c4.x, c[2] = c[3] = c4.y, c[4] = c[5] = c4.z, c[6] = c[7] = c4.w;
-                    s[0] = -s4.x, s[1] = s4.x, s[2] = -s4.y, s[3] = s4.y;
-                    s[4] = -s4.z, s[5] = s4.z, s[6] = -s4.w, s[7] = s4.w;
+                for (int j = 0; j < 4; ++j) {
+                    c[j] = make_float2(c8[2 * j], c8[2 * j + 1]);
+                    s[j] = make_float2(sign * s8[2 * j], sign * s8[2 * j + 1]);
+                }
+            } else {
+                const float4 c4 = *reinterpret_cast<const float4 *>(cs + 4 * sub);
+                const float4 s4 = *reinterpret_cast<const float4 *>(cs + p.R / 2 + 4 * sub);
+                if constexpr (MODE == kSplit) {
+                    c[0] = make_float2(c4.x, c4.y), c[1] = make_float2(c4.z, c4.w);
+                    s[0] = make_float2(s4.x, s4.y), s[1] = make_float2(s4.z, s4.w);
+                    ns[0] = make_float2(-s4.x, -s4.y), ns[1] = make_float2(-s4.z, -s4.w);
                 } else {
-                    const int i = sub < half ? d0 : d0 - p.R / 2;
-                    load8(cs + i, c);
-                    load8(cs + p.R / 2 + i, s);
-                    if (sub < half)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) s[k] = -s[k];
+                    c[0] = both(c4.x), c[1] = both(c4.y), c[2] = both(c4.z), c[3] = both(c4.w);
+                    s[0] = make_float2(-s4.x, s4.x), s[1] = make_float2(-s4.y, s4.y);
+                    s[2] = make_float2(-s4.z, s4.z), s[3] = make_float2(-s4.w, s4.w);
                 }
             }
         }
         const bool to_cache = blk >= 0 && blk < p.num_blocks;
-        if (live && !bad_pos && !to_cache && first_row == 0 && sub == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+        if (!to_cache && run == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
 
-        // whole warps stay together: the shuffles below need every lane
-        for (int r = first_row; __any_sync(0xffffffffu, live && r < rows); r += row_step) {
-            const bool mine = live && r < rows;
-            const bool is_q = r < HQ, is_v = r >= HQ + p.Hkv;
-            const int h = is_q ? r : (is_v ? r - HQ - p.Hkv : r - HQ);
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (mine && !bad_pos) {
-                const T *src = is_q   ? reinterpret_cast<const T *>(p.q) + token * p.q_stride
-                               : is_v ? reinterpret_cast<const T *>(p.v) + token * p.v_stride
-                                      : reinterpret_cast<const T *>(p.k) + token * p.k_stride;
-                load8(src + (int64_t)h * D + d0, x);
+        // iterations [from, to) over `heads` rows of one kind from src on
+        auto rows = [&](auto kind, int from, int to, int heads, const T *src, const void *weight) {
+            constexpr RowKind K = decltype(kind)::value;
+            if (from >= to) return;
+            const bool norm = K != kValue && weight != nullptr;
+            float2 wa[2], wb[2];
+            if (norm) {
+                Chunk<T> w0, w1;
+                w0.load(reinterpret_cast<const T *>(weight) + da);
+                w1.load(reinterpret_cast<const T *>(weight) + db);
+                w0.unpack(wa);
+                w1.unpack(wb);
             }
-            const T *w = reinterpret_cast<const T *>(is_q ? p.q_weight : p.k_weight);
-            if (p.q_weight != nullptr || p.k_weight != nullptr) {
-                float sq = 0.f;
+            src += (int64_t)(from * RPW + lr) * D;
+            T *dst = nullptr;                      // of this lane's first row
+            int64_t step = RPW * D;
+            if constexpr (K == kQuery) {
+                dst = reinterpret_cast<T *>(p.q_out) + (token * p.H + from * RPW + lr) * D;
+            } else if constexpr (!FP4) {
+                step *= p.bs;
+                dst = reinterpret_cast<T *>((K == kKey ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes) +
+                      ((int64_t)(from * RPW + lr) * p.bs + slot) * D;
+            }
+            uint8_t *cdst = nullptr, *sdst = nullptr;
+            if constexpr (FP4 && K != kQuery) {
+                const int64_t row = (int64_t)(from * RPW + lr) * p.bs + slot;
+                cdst = reinterpret_cast<uint8_t *>(K == kKey ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes + row * (D / 2);
+                sdst = p.scales + ((blk * 2 + (K == kValue)) * p.Hkv * p.bs + row) * (D / 16);
+            }
+            const bool write = K == kQuery || to_cache;
+#pragma unroll 1
+            for (int i = from; i < to; i += kRopeRows) {
+                Chunk<T> ra[kRopeRows], rb[kRopeRows];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
-#pragma unroll
-                for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                if (!is_v && w != nullptr && mine && !bad_pos) {
-                    const float rstd = __frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps));
-                    float wf[8];
-                    load8(w + d0, wf);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], rstd), wf[j]);
+                for (int u = 0; u < kRopeRows; ++u) {
+                    ra[u].zero();
+                    rb[u].zero();
+                    if (i + u < to && (i + u) * RPW + lr < heads) {
+                        if constexpr (MODE == kSplit) ra[u].load(src + u * RPW * D + da), rb[u].load(src + u * RPW * D + db);
+                        else Chunk<T>::load2(src + u * RPW * D + da, ra[u], rb[u]);
+                    }
                 }
-            }
-            if (p.R > 0) {
-                float y[8];
-                if (p.pairs) {
+                src += kRopeRows * RPW * D;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+                for (int u = 0; u < kRopeRows; ++u) {
+                    if (i + u >= to) break;        // the same for the whole warp
+                    const bool mine = write && (i + u) * RPW + lr < heads;
+                    float2 x[2], y[2];
+                    ra[u].unpack(x);
+                    rb[u].unpack(y);
+                    if (norm) {
+                        float2 q2 = mul2(x[0], x[0]);
+                        q2 = fma2(x[1], x[1], q2);
+                        q2 = fma2(y[0], y[0], q2);
+                        q2 = fma2(y[1], y[1], q2);
+                        float sq = q2.x + q2.y;
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                        const float2 rstd = both(__frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps)));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            x[j] = mul2(mul2(x[j], rstd), wa[j]);
+                            y[j] = mul2(mul2(y[j], rstd), wb[j]);
+                        }
+                    }
+                    if constexpr (K != kValue) {
+                        if constexpr (MODE == kShuffle) {
+                            float2 ox[2], oy[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                ox[j].x = __shfl_sync(0xffffffffu, x[j].x, partner);
+                                ox[j].y = __shfl_sync(0xffffffffu, x[j].y, partner);
+                                oy[j].x = __shfl_sync(0xffffffffu, y[j].x, partner);
+                                oy[j].y = __shfl_sync(0xffffffffu, y[j].y, partner);
+                            }
+                            if (turn) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    x[j] = add2(mul2(x[j], c[j]), mul2(ox[j], s[j]));
+                                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(oy[j], s[j + 2]));
+                                }
+                            }
+                        } else if (turn) {
+                            if constexpr (MODE == kSplit) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const float2 v = x[j], w = y[j];
+                                    x[j] = add2(mul2(v, c[j]), mul2(w, ns[j]));
+                                    y[j] = add2(mul2(w, c[j]), mul2(v, s[j]));
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    x[j] = add2(mul2(x[j], c[j]), mul2(make_float2(x[j].y, x[j].x), s[j]));
+                                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(make_float2(y[j].y, y[j].x), s[j + 2]));
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (!FP4 || K == kQuery) {
+                        if (mine) {
+                            if constexpr (K != kValue) {   // values go as they came, to the last bit
+                                ra[u].pack(x);
+                                rb[u].pack(y);
+                            }
+                            T *to_row = dst + u * step;
+                            if constexpr (MODE == kSplit) ra[u].store(to_row + da), rb[u].store(to_row + db);
+                            else Chunk<T>::store2(to_row + da, ra[u], rb[u]);
+                        }
+                    } else {
+                        // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
+                        const Factor f = factor_of(K == kKey ? p.k_g : p.v_g);
+                        float ma = largest(x), mb = largest(y);
+                        if (!apart) ma = mb = max_nan(ma, mb);
+                        ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+                        if constexpr (MODE == kSplit) {
+                            mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                            const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
+                            if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
+                            else mb = ma;
+                        } else {
+                            mb = ma;
+                        }
+                        // a NaN counts as 0: the largest of the others
+                        const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
+                        if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
+                            float va = 0.f, vb = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+                                vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
+                            }
+                            if (!apart) va = vb = fmaxf(va, vb);
+                            va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
+                            vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
+                            const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
+                            if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
+                            if (ma != ma) ma = va;
+                            if (mb != mb) mb = vb;
+                        }
+                        float ta, tb;
+                        const uint32_t ca = group_scale(ma, f, ta);
+                        uint32_t cb = ca;
+                        tb = ta;
+                        if (apart) cb = group_scale(mb, f, tb);
+                        const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
+                        if (mine) {
+                            uint8_t *cd = cdst + (int64_t)u * RPW * p.bs * (D / 2), *sd = sdst + (int64_t)u * RPW * p.bs * (D / 16);
+                            if (apart) {
+                                *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
+                                *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
+                                if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
+                            } else {
+                                *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
+                                if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
+                            }
+                        }
+                    }
+                }
+                if constexpr (!FP4 || K == kQuery) {
+                    dst += kRopeRows * step;
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], partner);
+                    cdst += (int64_t)kRopeRows * RPW * p.bs * (D / 2);
+                    sdst += (int64_t)kRopeRows * RPW * p.bs * (D / 16);
                 }
-                if (lane_rot && !is_v)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]));
             }
-            if (mine && is_q) store8(reinterpret_cast<T *>(p.q_out) + (token * p.H + h) * D + d0, x);
-            const int64_t row = (int64_t)h * p.bs + slot;
-            char *pool = (is_v ? p.v_pool : p.k_pool) + blk * p.block_stride_bytes;
-            const bool write = mine && !is_q && to_cache;
-            if constexpr (FP4) {
-                uint8_t *sd = p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * (D / 16) + sub / 2;
-                store_fp4(x, is_v ? p.v_g : p.k_g, write, reinterpret_cast<uint32_t *>(pool + row * (D / 2)) + sub, sd,
-                          (sub & 1) == 0);
-            } else {
-                if (write) store8(reinterpret_cast<T *>(pool) + row * D + d0, x);
-            }
-        }
+        };
+        rows(Kind<kQuery>{}, i0, min(i1, nq), HQ, reinterpret_cast<const T *>(p.q) + token * p.q_stride, p.q_weight);
+        rows(Kind<kKey>{}, max(i0 - nq, 0), min(i1 - nq, nk), p.Hkv, reinterpret_cast<const T *>(p.k) + token * p.k_stride,
+             p.k_weight);
+        rows(Kind<kValue>{}, max(i0 - nq - nk, 0), min(i1 - nq - nk, nk), p.Hkv,
+             reinterpret_cast<const T *>(p.v) + token * p.v_stride, nullptr);
     }
 }
 
-template <typename T, int D, bool FP4>
-static cudaError_t launch_one(const RopeAppendParams &p, cudaStream_t stream) {
-    constexpr int RPB = kRopeThreads / (D / 8);
-    const int rows = (p.q != nullptr ? p.H : 0) + 2 * p.Hkv;
+template <typename T, int D, bool FP4, RopeMode MODE>
+static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
+    constexpr int RPW = 32 / (D / 8);
+    const int iterations = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW + 2 * ((p.Hkv + RPW - 1) / RPW);
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int per_pass = RPB / rows > 1 ? RPB / rows : 1;
-    int64_t gy = ((int64_t)p.T + per_pass - 1) / per_pass;
+    // Runs per token: one iteration each while that leaves warps to spare (single
+    // tokens: the shortest way), else up to eight, which amortise what a token costs.
+    const int64_t tokens = (int64_t)p.B * p.T, warps = (int64_t)sms * 2 * kRopeWarps;
+    int64_t runs = warps / tokens;
+    const int64_t least = (iterations + 2 * kRopeRows - 1) / (2 * kRopeRows);
+    runs = runs < least ? least : (runs > iterations ? iterations : runs);
+    int64_t gy = ((int64_t)p.T * runs + kRopeWarps - 1) / kRopeWarps;
     gy = gy > 65535 ? 65535 : gy;
-    // few tokens: a token's rows over several CTAs, until every SM has one
-    const int passes = (rows + RPB - 1) / RPB;
-    int64_t gz = 2 * (int64_t)sms / ((int64_t)p.B * gy);
-    gz = gz < 1 ? 1 : (gz > passes ? passes : gz);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.B, (unsigned)gy, (unsigned)gz);
+    cfg.gridDim = dim3((unsigned)p.B, (unsigned)gy, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -193,7 +448,16 @@ static cudaError_t launch_one(const RopeAppendParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = PA_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4>, p);
+    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4, MODE>, p, (int)runs);
+}
+
+template <typename T, int D, bool FP4>
+static cudaError_t launch_one(const RopeAppendParams &p, cudaStream_t stream) {
+    if (p.R == 0 || p.pairs) return launch_mode<T, D, FP4, kNeighbours>(p, stream);
+    if constexpr (FP4) {
+        if (p.R % 32 != 0) return launch_mode<T, D, FP4, kShuffle>(p, stream);
+    }
+    return launch_mode<T, D, FP4, kSplit>(p, stream);
 }
 
 bool rope_append_supported(int dtype, int head_dim, bool fp4) {
