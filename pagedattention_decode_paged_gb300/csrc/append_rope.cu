@@ -18,10 +18,10 @@
 // neighbouring chunks kept and the other elements of the pairs fetched by
 // shuffles (kShuffle).
 //
-// A warp takes a run of the rows of one token: it keeps the token's cosines,
-// sines and the weights for all of them, has kRopeRows rows' loads in flight,
-// and goes through queries, keys and values in loops of their own, which need
-// no per-row selection.  Products and sums are rounded separately, two at a
+// A warp takes a run of the queries of one token, or of its keys with the values
+// beside them: up to 8 rows a lane, all of whose loads are issued at once, before
+// the positions, table entries and cosines that they do not depend on.
+// Products and sums are rounded separately, two at a
 // time (f32x2): the results are those of the stated formula operation by
 // operation, and so are the 4-bit codes.
 //
@@ -37,9 +37,8 @@
 
 namespace pa {
 
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 4;
 constexpr int kRopeThreads = kRopeWarps * 32;
-constexpr int kRopeRows = 4;       // iterations of rows in flight per warp
 enum RopeMode { kSplit, kNeighbours, kShuffle };
 
 // --- two fp32 values in one register pair -------------------------------------
@@ -160,36 +159,27 @@ __device__ __forceinline__ uint32_t group_codes(const float2 (&x)[2], float t, b
     return f32x2_to_e2m1x2(y[0].x, y[0].y) | f32x2_to_e2m1x2(y[1].x, y[1].y) << 8;
 }
 
-enum RowKind { kQuery, kKey, kValue };
-template <RowKind K>
-struct Kind {
-    static constexpr RowKind value = K;
-};
+// grid: x = sequence, y = kRopeWarps (token, run of its rows) each.  q_run,
+// kv_run: iterations of rows in a run (at most QB of queries, QB / 2 of keys).
+template <typename T>
+constexpr int kRopeBatch = sizeof(T) == 2 ? 8 : 4;
 
-// grid: x = sequence, y = 8 warps of (token, run of its rows) each.
 template <typename T, int D, bool FP4, RopeMode MODE>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int runs) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 5 : 4)
+rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, const int kv_run) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int LPR = D / 8;                     // lanes per row
     constexpr int RPW = 32 / LPR;                  // rows per iteration of a warp
+    constexpr int QB = kRopeBatch<T>, KB = QB / 2;
     const int b = blockIdx.x;
-    const int n = p.counts != nullptr ? p.counts[b] : p.T;
-    const int32_t start = p.positions[b];
-    const bool reporter = threadIdx.x == 0 && blockIdx.y == 0;
-    if (n < 0 || n > p.T) {
-        if (reporter) report(p.err_word, PA_DEVERR_BAD_LEN);
-        return;
-    }
-    const bool bad_pos = start < 0 || (int64_t)start + n > (int64_t)p.MB * p.bs ||
-                         (p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
-    if (bad_pos && reporter) report(p.err_word, PA_DEVERR_BAD_POS);
+    const int n = p.counts != nullptr ? __ldg(p.counts + b) : p.T;
+    const int32_t start = __ldg(p.positions + b);
 
     const int lane = threadIdx.x & 31, sub = lane % LPR, lr = lane / LPR;
     const int HQ = p.q != nullptr ? p.H : 0;
-    // iterations over queries, then keys, then values of a token
-    const int nq = (HQ + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
-    const int per_run = (nq + 2 * nk + runs - 1) / runs;
+    const int nq = (HQ + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;   // iterations over queries, over keys
+    const int q_runs = (nq + q_run - 1) / q_run, runs = q_runs + (nk + kv_run - 1) / kv_run;
     // this lane's chunks, and whether they are rotated
     const bool turn = sub < p.R / 8;
     const bool apart = MODE == kSplit && turn;
@@ -197,26 +187,58 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int half = p.R / 16;                     // kShuffle: lanes between the two elements of a pair
     const int partner = MODE == kShuffle && turn ? lane + (sub < half ? half : -half) : lane;
 
-    const int64_t units = (int64_t)n * runs;
+    const int64_t units = (int64_t)p.T * runs;     // of padded tokens: their rows are memory like the others
 #pragma unroll 1
     for (int64_t unit = (int64_t)blockIdx.y * kRopeWarps + (threadIdx.x >> 5); unit < units;
          unit += (int64_t)gridDim.y * kRopeWarps) {
         const int t = units <= INT32_MAX ? (int)((uint32_t)unit / (uint32_t)runs) : (int)(unit / runs);
         const int run = (int)(unit - (int64_t)t * runs);
-        const int i0 = run * per_run, i1 = min(i0 + per_run, nq + 2 * nk);
+        const bool queries = run < q_runs;
+        const int from = queries ? run * q_run : (run - q_runs) * kv_run;
+        const int count = queries ? min(q_run, nq - from) : min(kv_run, nk - from);
+        const int heads = queries ? HQ : p.Hkv;
         const int64_t token = (int64_t)b * p.T + t;
+
+        // padding is not read; a single token's row is memory whatever its count
+        if (p.T > 1 && n >= 0 && n <= p.T && t >= n) return;
+        // the rows: queries in the first QB places, or KB of keys and KB of values
+        Chunk<T> ra[QB], rb[QB];
+        {
+            const T *src = (queries ? reinterpret_cast<const T *>(p.q) + token * p.q_stride
+                                    : reinterpret_cast<const T *>(p.k) + token * p.k_stride) + (int64_t)(from * RPW + lr) * D;
+            const T *src_v = reinterpret_cast<const T *>(p.v) + token * p.v_stride + (int64_t)(from * RPW + lr) * D;
+#pragma unroll
+            for (int u = 0; u < QB; ++u) {
+                const int i = queries || u < KB ? u : u - KB;
+                const T *row = (queries || u < KB ? src : src_v) + i * RPW * D;
+                ra[u].zero();
+                rb[u].zero();
+                if (i < count && (from + i) * RPW + lr < heads) {
+                    if constexpr (MODE == kSplit) ra[u].load(row + da), rb[u].load(row + db);
+                    else Chunk<T>::load2(row + da, ra[u], rb[u]);
+                }
+            }
+        }
+        if (n < 0 || n > p.T) {
+            if (unit == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_LEN);
+            return;
+        }
+        const bool bad_pos = start < 0 || (int64_t)start + n > (int64_t)p.MB * p.bs ||
+                             (p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
+        if (bad_pos && unit == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_POS);
+        if (t >= n) return;
         if (bad_pos) {                             // zeros for the queries, nothing for the cache
             Chunk<T> z;
             z.zero();
-            for (int i = i0; i < min(i1, nq); ++i) {
-                const int h = i * RPW + lr;
+            for (int i = 0; i < (queries ? count : 0); ++i) {
+                const int h = (from + i) * RPW + lr;
                 if (h < HQ) Chunk<T>::store2(reinterpret_cast<T *>(p.q_out) + (token * p.H + h) * D + 8 * sub, z, z);
             }
             continue;
         }
         const int32_t pos = start + t;
         const int32_t bj = pos / p.bs, slot = pos - bj * p.bs;
-        const int64_t blk = __ldg(p.block_table + (int64_t)b * p.MB + bj);
+        const int64_t blk = queries ? 0 : __ldg(p.block_table + (int64_t)b * p.MB + bj);
         // cosines and sines: of pairs of elements, -sine first where the formula subtracts
         float2 c[MODE == kSplit ? 2 : 4], s[MODE == kSplit ? 2 : 4], ns[2];
         if (turn) {
@@ -246,197 +268,187 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
                 }
             }
         }
-        const bool to_cache = blk >= 0 && blk < p.num_blocks;
-        if (!to_cache && run == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
-
-        // iterations [from, to) over `heads` rows of one kind from src on
-        auto rows = [&](auto kind, int from, int to, int heads, const T *src, const void *weight) {
-            constexpr RowKind K = decltype(kind)::value;
-            if (from >= to) return;
-            const bool norm = K != kValue && weight != nullptr;
-            float2 wa[2], wb[2];
-            if (norm) {
-                Chunk<T> w0, w1;
-                w0.load(reinterpret_cast<const T *>(weight) + da);
-                w1.load(reinterpret_cast<const T *>(weight) + db);
-                w0.unpack(wa);
-                w1.unpack(wb);
-            }
-            src += (int64_t)(from * RPW + lr) * D;
-            T *dst = nullptr;                      // of this lane's first row
-            int64_t step = RPW * D;
-            if constexpr (K == kQuery) {
-                dst = reinterpret_cast<T *>(p.q_out) + (token * p.H + from * RPW + lr) * D;
-            } else if constexpr (!FP4) {
-                step *= p.bs;
-                dst = reinterpret_cast<T *>((K == kKey ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes) +
-                      ((int64_t)(from * RPW + lr) * p.bs + slot) * D;
-            }
-            uint8_t *cdst = nullptr, *sdst = nullptr;
-            if constexpr (FP4 && K != kQuery) {
-                const int64_t row = (int64_t)(from * RPW + lr) * p.bs + slot;
-                cdst = reinterpret_cast<uint8_t *>(K == kKey ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes + row * (D / 2);
-                sdst = p.scales + ((blk * 2 + (K == kValue)) * p.Hkv * p.bs + row) * (D / 16);
-            }
-            const bool write = K == kQuery || to_cache;
-#pragma unroll 1
-            for (int i = from; i < to; i += kRopeRows) {
-                Chunk<T> ra[kRopeRows], rb[kRopeRows];
+        const void *weight = queries ? p.q_weight : p.k_weight;
+        float2 wa[2], wb[2];
+        if (weight != nullptr) {
+            Chunk<T> w0, w1;
+            w0.load(reinterpret_cast<const T *>(weight) + da);
+            w1.load(reinterpret_cast<const T *>(weight) + db);
+            w0.unpack(wa);
+            w1.unpack(wb);
+        }
+        // norm and rotation of a row
+        auto turned = [&](float2 (&x)[2], float2 (&y)[2]) {
+            if (weight != nullptr) {
+                float2 q2 = mul2(x[0], x[0]);
+                q2 = fma2(x[1], x[1], q2);
+                q2 = fma2(y[0], y[0], q2);
+                q2 = fma2(y[1], y[1], q2);
+                float sq = q2.x + q2.y;
 #pragma unroll
-                for (int u = 0; u < kRopeRows; ++u) {
-                    ra[u].zero();
-                    rb[u].zero();
-                    if (i + u < to && (i + u) * RPW + lr < heads) {
-                        if constexpr (MODE == kSplit) ra[u].load(src + u * RPW * D + da), rb[u].load(src + u * RPW * D + db);
-                        else Chunk<T>::load2(src + u * RPW * D + da, ra[u], rb[u]);
+                for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+                const float2 rstd = both(__frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps)));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[j] = mul2(mul2(x[j], rstd), wa[j]);
+                    y[j] = mul2(mul2(y[j], rstd), wb[j]);
+                }
+            }
+            if constexpr (MODE == kShuffle) {
+                float2 ox[2], oy[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    ox[j].x = __shfl_sync(0xffffffffu, x[j].x, partner);
+                    ox[j].y = __shfl_sync(0xffffffffu, x[j].y, partner);
+                    oy[j].x = __shfl_sync(0xffffffffu, y[j].x, partner);
+                    oy[j].y = __shfl_sync(0xffffffffu, y[j].y, partner);
+                }
+                if (turn) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x[j] = add2(mul2(x[j], c[j]), mul2(ox[j], s[j]));
+                        y[j] = add2(mul2(y[j], c[j + 2]), mul2(oy[j], s[j + 2]));
                     }
                 }
-                src += kRopeRows * RPW * D;
+            } else if (turn) {
+                if constexpr (MODE == kSplit) {
 #pragma unroll
-                for (int u = 0; u < kRopeRows; ++u) {
-                    if (i + u >= to) break;        // the same for the whole warp
-                    const bool mine = write && (i + u) * RPW + lr < heads;
-                    float2 x[2], y[2];
-                    ra[u].unpack(x);
-                    rb[u].unpack(y);
-                    if (norm) {
-                        float2 q2 = mul2(x[0], x[0]);
-                        q2 = fma2(x[1], x[1], q2);
-                        q2 = fma2(y[0], y[0], q2);
-                        q2 = fma2(y[1], y[1], q2);
-                        float sq = q2.x + q2.y;
-#pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                        const float2 rstd = both(__frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps)));
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            x[j] = mul2(mul2(x[j], rstd), wa[j]);
-                            y[j] = mul2(mul2(y[j], rstd), wb[j]);
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 v = x[j], w = y[j];
+                        x[j] = add2(mul2(v, c[j]), mul2(w, ns[j]));
+                        y[j] = add2(mul2(w, c[j]), mul2(v, s[j]));
                     }
-                    if constexpr (K != kValue) {
-                        if constexpr (MODE == kShuffle) {
-                            float2 ox[2], oy[2];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                ox[j].x = __shfl_sync(0xffffffffu, x[j].x, partner);
-                                ox[j].y = __shfl_sync(0xffffffffu, x[j].y, partner);
-                                oy[j].x = __shfl_sync(0xffffffffu, y[j].x, partner);
-                                oy[j].y = __shfl_sync(0xffffffffu, y[j].y, partner);
-                            }
-                            if (turn) {
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    x[j] = add2(mul2(x[j], c[j]), mul2(ox[j], s[j]));
-                                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(oy[j], s[j + 2]));
-                                }
-                            }
-                        } else if (turn) {
-                            if constexpr (MODE == kSplit) {
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const float2 v = x[j], w = y[j];
-                                    x[j] = add2(mul2(v, c[j]), mul2(w, ns[j]));
-                                    y[j] = add2(mul2(w, c[j]), mul2(v, s[j]));
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    x[j] = add2(mul2(x[j], c[j]), mul2(make_float2(x[j].y, x[j].x), s[j]));
-                                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(make_float2(y[j].y, y[j].x), s[j + 2]));
-                                }
-                            }
-                        }
-                    }
-                    if constexpr (!FP4 || K == kQuery) {
-                        if (mine) {
-                            if constexpr (K != kValue) {   // values go as they came, to the last bit
-                                ra[u].pack(x);
-                                rb[u].pack(y);
-                            }
-                            T *to_row = dst + u * step;
-                            if constexpr (MODE == kSplit) ra[u].store(to_row + da), rb[u].store(to_row + db);
-                            else Chunk<T>::store2(to_row + da, ra[u], rb[u]);
-                        }
-                    } else {
-                        // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
-                        const Factor f = factor_of(K == kKey ? p.k_g : p.v_g);
-                        float ma = largest(x), mb = largest(y);
-                        if (!apart) ma = mb = max_nan(ma, mb);
-                        ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-                        if constexpr (MODE == kSplit) {
-                            mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-                            const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
-                            if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
-                            else mb = ma;
-                        } else {
-                            mb = ma;
-                        }
-                        // a NaN counts as 0: the largest of the others
-                        const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
-                        if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
-                            float va = 0.f, vb = 0.f;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-                                vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
-                            }
-                            if (!apart) va = vb = fmaxf(va, vb);
-                            va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
-                            vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
-                            const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
-                            if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
-                            if (ma != ma) ma = va;
-                            if (mb != mb) mb = vb;
-                        }
-                        float ta, tb;
-                        const uint32_t ca = group_scale(ma, f, ta);
-                        uint32_t cb = ca;
-                        tb = ta;
-                        if (apart) cb = group_scale(mb, f, tb);
-                        const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
-                        if (mine) {
-                            uint8_t *cd = cdst + (int64_t)u * RPW * p.bs * (D / 2), *sd = sdst + (int64_t)u * RPW * p.bs * (D / 16);
-                            if (apart) {
-                                *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
-                                *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
-                                if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
-                            } else {
-                                *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
-                                if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
-                            }
-                        }
-                    }
-                }
-                if constexpr (!FP4 || K == kQuery) {
-                    dst += kRopeRows * step;
                 } else {
-                    cdst += (int64_t)kRopeRows * RPW * p.bs * (D / 2);
-                    sdst += (int64_t)kRopeRows * RPW * p.bs * (D / 16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x[j] = add2(mul2(x[j], c[j]), mul2(make_float2(x[j].y, x[j].x), s[j]));
+                        y[j] = add2(mul2(y[j], c[j + 2]), mul2(make_float2(y[j].y, y[j].x), s[j + 2]));
+                    }
                 }
             }
         };
-        rows(Kind<kQuery>{}, i0, min(i1, nq), HQ, reinterpret_cast<const T *>(p.q) + token * p.q_stride, p.q_weight);
-        rows(Kind<kKey>{}, max(i0 - nq, 0), min(i1 - nq, nk), p.Hkv, reinterpret_cast<const T *>(p.k) + token * p.k_stride,
-             p.k_weight);
-        rows(Kind<kValue>{}, max(i0 - nq - nk, 0), min(i1 - nq - nk, nk), p.Hkv,
-             reinterpret_cast<const T *>(p.v) + token * p.v_stride, nullptr);
+        auto put = [&](T *dst, const Chunk<T> &ca, const Chunk<T> &cb) {
+            if constexpr (MODE == kSplit) ca.store(dst + da), cb.store(dst + db);
+            else Chunk<T>::store2(dst + da, ca, cb);
+        };
+        if (queries) {
+            T *dst = reinterpret_cast<T *>(p.q_out) + (token * p.H + from * RPW + lr) * D;
+#pragma unroll
+            for (int u = 0; u < QB; ++u) {
+                if (u >= count) break;             // the same for the whole warp
+                float2 x[2], y[2];
+                ra[u].unpack(x);
+                rb[u].unpack(y);
+                turned(x, y);
+                if ((from + u) * RPW + lr < HQ) {
+                    ra[u].pack(x);
+                    rb[u].pack(y);
+                    put(dst + u * RPW * D, ra[u], rb[u]);
+                }
+            }
+            continue;
+        }
+
+        const bool to_cache = blk >= 0 && blk < p.num_blocks;
+        if (!to_cache && run == q_runs && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+        const int64_t first = (int64_t)(from * RPW + lr) * p.bs + slot;   // this lane's first row in the block
+        // quantising takes a few hundred instructions: one copy of them, the rows
+        // moved up to it
+#pragma unroll(FP4 ? 1 : QB)
+        for (int u = 0; u < QB; ++u) {
+            const int i = u < KB ? u : u - KB;
+            const bool is_v = u >= KB;
+            Chunk<T> &row_a = ra[FP4 ? 0 : u], &row_b = rb[FP4 ? 0 : u];
+            if (FP4 && u > 0) {
+#pragma unroll
+                for (int j = 0; j + 1 < QB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
+            }
+            if (i >= count) continue;              // the same for the whole warp
+            const bool mine = to_cache && (from + i) * RPW + lr < p.Hkv;
+            const int64_t row = first + (int64_t)i * RPW * p.bs;
+            char *pool = (is_v ? p.v_pool : p.k_pool) + blk * p.block_stride_bytes;
+            float2 x[2], y[2];
+            if (FP4 || !is_v) {
+                row_a.unpack(x);
+                row_b.unpack(y);
+            }
+            if (!is_v) turned(x, y);
+            if constexpr (!FP4) {
+                if (mine) {
+                    if (!is_v) {                   // values go as they came, to the last bit
+                        row_a.pack(x);
+                        row_b.pack(y);
+                    }
+                    put(reinterpret_cast<T *>(pool) + row * D, row_a, row_b);
+                }
+            } else {
+                // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
+                const Factor f = factor_of(is_v ? p.v_g : p.k_g);
+                float ma = largest(x), mb = largest(y);
+                if (!apart) ma = mb = max_nan(ma, mb);
+                ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+                if constexpr (MODE == kSplit) {
+                    mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                    const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
+                    if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
+                    else mb = ma;
+                } else {
+                    mb = ma;
+                }
+                // a NaN counts as 0: the largest of the others
+                const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
+                if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
+                    float va = 0.f, vb = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+                        vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
+                    }
+                    if (!apart) va = vb = fmaxf(va, vb);
+                    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
+                    vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
+                    const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
+                    if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
+                    if (ma != ma) ma = va;
+                    if (mb != mb) mb = vb;
+                }
+                float ta, tb;
+                const uint32_t ca = group_scale(ma, f, ta);
+                uint32_t cb = ca;
+                tb = ta;
+                if (apart) cb = group_scale(mb, f, tb);
+                const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
+                if (mine) {
+                    char *cd = pool + row * (D / 2);
+                    uint8_t *sd = p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * (D / 16);
+                    if (apart) {
+                        *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
+                        *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
+                        if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
+                    } else {
+                        *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
+                        if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
+                    }
+                }
+            }
+        }
     }
 }
 
 template <typename T, int D, bool FP4, RopeMode MODE>
 static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
-    constexpr int RPW = 32 / (D / 8);
-    const int iterations = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW + 2 * ((p.Hkv + RPW - 1) / RPW);
+    constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T>;
+    const int nq = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // Runs per token: one iteration each while that leaves warps to spare (single
-    // tokens: the shortest way), else up to eight, which amortise what a token costs.
-    const int64_t tokens = (int64_t)p.B * p.T, warps = (int64_t)sms * 2 * kRopeWarps;
-    int64_t runs = warps / tokens;
-    const int64_t least = (iterations + 2 * kRopeRows - 1) / (2 * kRopeRows);
-    runs = runs < least ? least : (runs > iterations ? iterations : runs);
+    // Rows per run: as many as are loaded at once, which amortises what a token
+    // costs; fewer for few tokens, until every SM has 16 warps at most.
+    const int64_t tokens = (int64_t)p.B * p.T, warps = (int64_t)sms * 16;
+    int q_run = QB, kv_run = QB / 2;
+    while (q_run > 1 && tokens * ((nq + q_run / 2 - 1) / (q_run / 2) + (nk + kv_run - 1) / kv_run) <= warps) q_run /= 2;
+    while (kv_run > 1 && tokens * ((nq + q_run - 1) / q_run + (nk + kv_run / 2 - 1) / (kv_run / 2)) <= warps) kv_run /= 2;
+    const int64_t runs = (nq + q_run - 1) / q_run + (nk + kv_run - 1) / kv_run;
     int64_t gy = ((int64_t)p.T * runs + kRopeWarps - 1) / kRopeWarps;
     gy = gy > 65535 ? 65535 : gy;
     cudaLaunchConfig_t cfg = {};
@@ -448,7 +460,7 @@ static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = PA_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4, MODE>, p, (int)runs);
+    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4, MODE>, p, q_run, kv_run);
 }
 
 template <typename T, int D, bool FP4>
