@@ -12,6 +12,13 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // far enough inside fp32 that no scale times factor over- or underflows
 bool factor_ok(float g) { return g >= 0x1p-64f && g <= 0x1p64f; }
 
+// log2 of a power of two, else -1
+int32_t log2_or_none(int32_t n) {
+    for (int sh = 0; sh < 31; ++sh)
+        if ((1 << sh) == n) return sh;
+    return -1;
+}
+
 // Sizes common to every entry point; `row_bytes`: bytes of a cache row,
 // `stride_bytes`: block_stride in bytes.
 pa_status check_sizes(const pa_shape *s, int64_t row_bytes, int64_t stride_bytes) {
@@ -106,6 +113,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
     p.Hkv = s->num_kv_heads;
     p.MB = s->max_blocks_per_seq;
     p.bs = s->block_size;
+    p.bs_shift = log2_or_none(s->block_size);
     if (rope != nullptr) {
         p.cos_sin = rope->cos_sin;
         p.max_position = rope->max_position;
@@ -212,6 +220,7 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
     p.Hkv = shape->num_kv_heads;
     p.MB = shape->max_blocks_per_seq;
     p.bs = shape->block_size;
+    p.bs_shift = log2_or_none(shape->block_size);
     p.k_g = k_scale;
     p.v_g = v_scale;
     return pa::launch_gather_fp4(shape->dtype, shape->head_dim, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -265,9 +274,7 @@ pa_status paged_attention_decode_fp4(const pa_shape *shape, void *out, const voi
     p.D = shape->head_dim;
     p.MB = shape->max_blocks_per_seq;
     p.bs = shape->block_size;
-    p.bs_shift = -1;
-    for (int sh = 0; sh < 31; ++sh)
-        if ((1 << sh) == shape->block_size) p.bs_shift = sh;
+    p.bs_shift = log2_or_none(shape->block_size);
     p.window = window;
     p.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
     char *ws = static_cast<char *>(workspace);

@@ -159,276 +159,276 @@ __device__ __forceinline__ uint32_t group_codes(const float2 (&x)[2], float t, b
     return f32x2_to_e2m1x2(y[0].x, y[0].y) | f32x2_to_e2m1x2(y[1].x, y[1].y) << 8;
 }
 
-// grid: x = sequence, y = kRopeWarps (token, run of its rows) each.  q_run,
-// kv_run: iterations of rows in a run (at most QB of queries, QB / 2 of keys).
-template <typename T>
+// grid: x = kRopeWarps tokens of the padded batch each, y = run: of kv_run
+// iterations of keys and values, then of q_run iterations of queries (at most
+// KB and QB), so that the warps of a CTA do the same.
+template <typename T, bool FP4>
 constexpr int kRopeBatch = sizeof(T) == 2 ? 8 : 4;
+// Quantising a row takes as long as turning several: fewer to a run, so that the
+// warps of a CTA finish together (f16 prompts into the 4-bit cache: 4 keys and 4
+// values a run 50 us, 1 of each 41 us, before runs had CTAs of their own).
+template <typename T, bool FP4>
+constexpr int kKeyBatch = FP4 ? 2 : kRopeBatch<T, FP4> / 2;
 
 template <typename T, int D, bool FP4, RopeMode MODE>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 5 : 4)
-rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, const int kv_run) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 5)
+rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, const int kv_run, const int kv_runs) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int LPR = D / 8;                     // lanes per row
     constexpr int RPW = 32 / LPR;                  // rows per iteration of a warp
-    constexpr int QB = kRopeBatch<T>, KB = QB / 2;
-    const int b = blockIdx.x;
+    constexpr int QB = kRopeBatch<T, FP4>, KB = kKeyBatch<T, FP4>;
+    const int64_t token = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    if (token >= (int64_t)p.B * p.T) return;
+    const int b = p.T == 1 ? (int)token : token <= INT32_MAX ? (int)((uint32_t)token / (uint32_t)p.T) : (int)(token / p.T);
+    const int t = (int)(token - (int64_t)b * p.T);
     const int n = p.counts != nullptr ? __ldg(p.counts + b) : p.T;
     const int32_t start = __ldg(p.positions + b);
 
     const int lane = threadIdx.x & 31, sub = lane % LPR, lr = lane / LPR;
     const int HQ = p.q != nullptr ? p.H : 0;
     const int nq = (HQ + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;   // iterations over queries, over keys
-    const int q_runs = (nq + q_run - 1) / q_run, runs = q_runs + (nk + kv_run - 1) / kv_run;
+    const bool queries = (int)blockIdx.y >= kv_runs;
+    const int from = queries ? ((int)blockIdx.y - kv_runs) * q_run : (int)blockIdx.y * kv_run;
+    const int count = queries ? min(q_run, nq - from) : min(kv_run, nk - from);
+    const int heads = queries ? HQ : p.Hkv;
     // this lane's chunks, and whether they are rotated
+    const bool reporter = t == 0 && blockIdx.y == 0 && lane == 0;
     const bool turn = sub < p.R / 8;
     const bool apart = MODE == kSplit && turn;
     const int da = apart ? 4 * sub : 8 * sub, db = apart ? p.R / 2 + 4 * sub : 8 * sub + 4;
     const int half = p.R / 16;                     // kShuffle: lanes between the two elements of a pair
     const int partner = MODE == kShuffle && turn ? lane + (sub < half ? half : -half) : lane;
 
-    const int64_t units = (int64_t)p.T * runs;     // of padded tokens: their rows are memory like the others
-#pragma unroll 1
-    for (int64_t unit = (int64_t)blockIdx.y * kRopeWarps + (threadIdx.x >> 5); unit < units;
-         unit += (int64_t)gridDim.y * kRopeWarps) {
-        const int t = units <= INT32_MAX ? (int)((uint32_t)unit / (uint32_t)runs) : (int)(unit / runs);
-        const int run = (int)(unit - (int64_t)t * runs);
-        const bool queries = run < q_runs;
-        const int from = queries ? run * q_run : (run - q_runs) * kv_run;
-        const int count = queries ? min(q_run, nq - from) : min(kv_run, nk - from);
-        const int heads = queries ? HQ : p.Hkv;
-        const int64_t token = (int64_t)b * p.T + t;
-
-        // padding is not read; a single token's row is memory whatever its count
-        if (p.T > 1 && n >= 0 && n <= p.T && t >= n) return;
-        // the rows: queries in the first QB places, or KB of keys and KB of values
-        Chunk<T> ra[QB], rb[QB];
-        {
-            const T *src = (queries ? reinterpret_cast<const T *>(p.q) + token * p.q_stride
-                                    : reinterpret_cast<const T *>(p.k) + token * p.k_stride) + (int64_t)(from * RPW + lr) * D;
-            const T *src_v = reinterpret_cast<const T *>(p.v) + token * p.v_stride + (int64_t)(from * RPW + lr) * D;
+    // padding is not read; a first token's row is memory whatever the count
+    if (t > 0 && n >= 0 && n <= p.T && t >= n) return;
+    // the rows: queries in the first QB places, or KB of keys and KB of values
+    Chunk<T> ra[QB], rb[QB];
+    {
+        const T *src = (queries ? reinterpret_cast<const T *>(p.q) + token * p.q_stride
+                                : reinterpret_cast<const T *>(p.k) + token * p.k_stride) + (int64_t)(from * RPW + lr) * D;
+        const T *src_v = reinterpret_cast<const T *>(p.v) + token * p.v_stride + (int64_t)(from * RPW + lr) * D;
 #pragma unroll
-            for (int u = 0; u < QB; ++u) {
-                const int i = queries || u < KB ? u : u - KB;
-                const T *row = (queries || u < KB ? src : src_v) + i * RPW * D;
-                ra[u].zero();
-                rb[u].zero();
-                if (i < count && (from + i) * RPW + lr < heads) {
-                    if constexpr (MODE == kSplit) ra[u].load(row + da), rb[u].load(row + db);
-                    else Chunk<T>::load2(row + da, ra[u], rb[u]);
-                }
-            }
-        }
-        if (n < 0 || n > p.T) {
-            if (unit == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_LEN);
-            return;
-        }
-        const bool bad_pos = start < 0 || (int64_t)start + n > (int64_t)p.MB * p.bs ||
-                             (p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
-        if (bad_pos && unit == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_POS);
-        if (t >= n) return;
-        if (bad_pos) {                             // zeros for the queries, nothing for the cache
-            Chunk<T> z;
-            z.zero();
-            for (int i = 0; i < (queries ? count : 0); ++i) {
-                const int h = (from + i) * RPW + lr;
-                if (h < HQ) Chunk<T>::store2(reinterpret_cast<T *>(p.q_out) + (token * p.H + h) * D + 8 * sub, z, z);
-            }
-            continue;
-        }
-        const int32_t pos = start + t;
-        const int32_t bj = pos / p.bs, slot = pos - bj * p.bs;
-        const int64_t blk = queries ? 0 : __ldg(p.block_table + (int64_t)b * p.MB + bj);
-        // cosines and sines: of pairs of elements, -sine first where the formula subtracts
-        float2 c[MODE == kSplit ? 2 : 4], s[MODE == kSplit ? 2 : 4], ns[2];
-        if (turn) {
-            const float *cs = p.cos_sin + (int64_t)pos * p.R;
-            if constexpr (MODE == kShuffle) {
-                const int i = sub < half ? 8 * sub : 8 * sub - p.R / 2;
-                float c8[8], s8[8];
-                load8(cs + i, c8);
-                load8(cs + p.R / 2 + i, s8);
-                const float sign = sub < half ? -1.f : 1.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    c[j] = make_float2(c8[2 * j], c8[2 * j + 1]);
-                    s[j] = make_float2(sign * s8[2 * j], sign * s8[2 * j + 1]);
-                }
-            } else {
-                const float4 c4 = *reinterpret_cast<const float4 *>(cs + 4 * sub);
-                const float4 s4 = *reinterpret_cast<const float4 *>(cs + p.R / 2 + 4 * sub);
-                if constexpr (MODE == kSplit) {
-                    c[0] = make_float2(c4.x, c4.y), c[1] = make_float2(c4.z, c4.w);
-                    s[0] = make_float2(s4.x, s4.y), s[1] = make_float2(s4.z, s4.w);
-                    ns[0] = make_float2(-s4.x, -s4.y), ns[1] = make_float2(-s4.z, -s4.w);
-                } else {
-                    c[0] = both(c4.x), c[1] = both(c4.y), c[2] = both(c4.z), c[3] = both(c4.w);
-                    s[0] = make_float2(-s4.x, s4.x), s[1] = make_float2(-s4.y, s4.y);
-                    s[2] = make_float2(-s4.z, s4.z), s[3] = make_float2(-s4.w, s4.w);
-                }
-            }
-        }
-        const void *weight = queries ? p.q_weight : p.k_weight;
-        float2 wa[2], wb[2];
-        if (weight != nullptr) {
-            Chunk<T> w0, w1;
-            w0.load(reinterpret_cast<const T *>(weight) + da);
-            w1.load(reinterpret_cast<const T *>(weight) + db);
-            w0.unpack(wa);
-            w1.unpack(wb);
-        }
-        // norm and rotation of a row
-        auto turned = [&](float2 (&x)[2], float2 (&y)[2]) {
-            if (weight != nullptr) {
-                float2 q2 = mul2(x[0], x[0]);
-                q2 = fma2(x[1], x[1], q2);
-                q2 = fma2(y[0], y[0], q2);
-                q2 = fma2(y[1], y[1], q2);
-                float sq = q2.x + q2.y;
-#pragma unroll
-                for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                const float2 rstd = both(__frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps)));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    x[j] = mul2(mul2(x[j], rstd), wa[j]);
-                    y[j] = mul2(mul2(y[j], rstd), wb[j]);
-                }
-            }
-            if constexpr (MODE == kShuffle) {
-                float2 ox[2], oy[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    ox[j].x = __shfl_sync(0xffffffffu, x[j].x, partner);
-                    ox[j].y = __shfl_sync(0xffffffffu, x[j].y, partner);
-                    oy[j].x = __shfl_sync(0xffffffffu, y[j].x, partner);
-                    oy[j].y = __shfl_sync(0xffffffffu, y[j].y, partner);
-                }
-                if (turn) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x[j] = add2(mul2(x[j], c[j]), mul2(ox[j], s[j]));
-                        y[j] = add2(mul2(y[j], c[j + 2]), mul2(oy[j], s[j + 2]));
-                    }
-                }
-            } else if (turn) {
-                if constexpr (MODE == kSplit) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float2 v = x[j], w = y[j];
-                        x[j] = add2(mul2(v, c[j]), mul2(w, ns[j]));
-                        y[j] = add2(mul2(w, c[j]), mul2(v, s[j]));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x[j] = add2(mul2(x[j], c[j]), mul2(make_float2(x[j].y, x[j].x), s[j]));
-                        y[j] = add2(mul2(y[j], c[j + 2]), mul2(make_float2(y[j].y, y[j].x), s[j + 2]));
-                    }
-                }
-            }
-        };
-        auto put = [&](T *dst, const Chunk<T> &ca, const Chunk<T> &cb) {
-            if constexpr (MODE == kSplit) ca.store(dst + da), cb.store(dst + db);
-            else Chunk<T>::store2(dst + da, ca, cb);
-        };
-        if (queries) {
-            T *dst = reinterpret_cast<T *>(p.q_out) + (token * p.H + from * RPW + lr) * D;
-#pragma unroll
-            for (int u = 0; u < QB; ++u) {
-                if (u >= count) break;             // the same for the whole warp
-                float2 x[2], y[2];
-                ra[u].unpack(x);
-                rb[u].unpack(y);
-                turned(x, y);
-                if ((from + u) * RPW + lr < HQ) {
-                    ra[u].pack(x);
-                    rb[u].pack(y);
-                    put(dst + u * RPW * D, ra[u], rb[u]);
-                }
-            }
-            continue;
-        }
-
-        const bool to_cache = blk >= 0 && blk < p.num_blocks;
-        if (!to_cache && run == q_runs && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
-        const int64_t first = (int64_t)(from * RPW + lr) * p.bs + slot;   // this lane's first row in the block
-        // quantising takes a few hundred instructions: one copy of them, the rows
-        // moved up to it
-#pragma unroll(FP4 ? 1 : QB)
         for (int u = 0; u < QB; ++u) {
-            const int i = u < KB ? u : u - KB;
-            const bool is_v = u >= KB;
-            Chunk<T> &row_a = ra[FP4 ? 0 : u], &row_b = rb[FP4 ? 0 : u];
-            if (FP4 && u > 0) {
+            const int i = queries || u < KB ? u : u - KB;
+            const T *row = (queries || u < KB ? src : src_v) + i * RPW * D;
+            ra[u].zero();
+            rb[u].zero();
+            if (i < count && (queries || u < 2 * KB) && (from + i) * RPW + lr < heads) {
+                if constexpr (MODE == kSplit) ra[u].load(row + da), rb[u].load(row + db);
+                else Chunk<T>::load2(row + da, ra[u], rb[u]);
+            }
+        }
+    }
+    if (n < 0 || n > p.T) {
+        if (reporter) report(p.err_word, PA_DEVERR_BAD_LEN);
+        return;
+    }
+    const bool bad_pos = start < 0 || (int64_t)start + n > (int64_t)p.MB * p.bs ||
+                         (p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
+    if (bad_pos && reporter) report(p.err_word, PA_DEVERR_BAD_POS);
+    if (t >= n) return;
+    if (bad_pos) {                             // zeros for the queries, nothing for the cache
+        Chunk<T> z;
+        z.zero();
+        for (int i = 0; i < (queries ? count : 0); ++i) {
+            const int h = (from + i) * RPW + lr;
+            if (h < HQ) Chunk<T>::store2(reinterpret_cast<T *>(p.q_out) + (token * p.H + h) * D + 8 * sub, z, z);
+        }
+        return;
+    }
+    const int32_t pos = start + t;
+    const int32_t bj = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.bs, slot = pos - bj * p.bs;
+    const int64_t blk = queries ? 0 : __ldg(p.block_table + (int64_t)b * p.MB + bj);
+    // cosines and sines: of pairs of elements, -sine first where the formula subtracts
+    float2 c[MODE == kSplit ? 2 : 4], s[MODE == kSplit ? 2 : 4], ns[2];
+    if (turn) {
+        const float *cs = p.cos_sin + (int64_t)pos * p.R;
+        if constexpr (MODE == kShuffle) {
+            const int i = sub < half ? 8 * sub : 8 * sub - p.R / 2;
+            float c8[8], s8[8];
+            load8(cs + i, c8);
+            load8(cs + p.R / 2 + i, s8);
+            const float sign = sub < half ? -1.f : 1.f;
 #pragma unroll
-                for (int j = 0; j + 1 < QB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
+            for (int j = 0; j < 4; ++j) {
+                c[j] = make_float2(c8[2 * j], c8[2 * j + 1]);
+                s[j] = make_float2(sign * s8[2 * j], sign * s8[2 * j + 1]);
             }
-            if (i >= count) continue;              // the same for the whole warp
-            const bool mine = to_cache && (from + i) * RPW + lr < p.Hkv;
-            const int64_t row = first + (int64_t)i * RPW * p.bs;
-            char *pool = (is_v ? p.v_pool : p.k_pool) + blk * p.block_stride_bytes;
-            float2 x[2], y[2];
-            if (FP4 || !is_v) {
-                row_a.unpack(x);
-                row_b.unpack(y);
+        } else {
+            const float4 c4 = *reinterpret_cast<const float4 *>(cs + 4 * sub);
+            const float4 s4 = *reinterpret_cast<const float4 *>(cs + p.R / 2 + 4 * sub);
+            if constexpr (MODE == kSplit) {
+                c[0] = make_float2(c4.x, c4.y), c[1] = make_float2(c4.z, c4.w);
+                s[0] = make_float2(s4.x, s4.y), s[1] = make_float2(s4.z, s4.w);
+                ns[0] = make_float2(-s4.x, -s4.y), ns[1] = make_float2(-s4.z, -s4.w);
+            } else {
+                c[0] = both(c4.x), c[1] = both(c4.y), c[2] = both(c4.z), c[3] = both(c4.w);
+                s[0] = make_float2(-s4.x, s4.x), s[1] = make_float2(-s4.y, s4.y);
+                s[2] = make_float2(-s4.z, s4.z), s[3] = make_float2(-s4.w, s4.w);
             }
-            if (!is_v) turned(x, y);
-            if constexpr (!FP4) {
-                if (mine) {
-                    if (!is_v) {                   // values go as they came, to the last bit
-                        row_a.pack(x);
-                        row_b.pack(y);
-                    }
-                    put(reinterpret_cast<T *>(pool) + row * D, row_a, row_b);
+        }
+    }
+    const void *weight = queries ? p.q_weight : p.k_weight;
+    float2 wa[2], wb[2];
+    if (weight != nullptr) {
+        Chunk<T> w0, w1;
+        w0.load(reinterpret_cast<const T *>(weight) + da);
+        w1.load(reinterpret_cast<const T *>(weight) + db);
+        w0.unpack(wa);
+        w1.unpack(wb);
+    }
+    // norm and rotation of a row
+    auto turned = [&](float2 (&x)[2], float2 (&y)[2]) {
+        if (weight != nullptr) {
+            float2 q2 = mul2(x[0], x[0]);
+            q2 = fma2(x[1], x[1], q2);
+            q2 = fma2(y[0], y[0], q2);
+            q2 = fma2(y[1], y[1], q2);
+            float sq = q2.x + q2.y;
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            const float2 rstd = both(__frsqrt_rn(__fadd_rn(sq * (1.f / D), p.eps)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[j] = mul2(mul2(x[j], rstd), wa[j]);
+                y[j] = mul2(mul2(y[j], rstd), wb[j]);
+            }
+        }
+        if constexpr (MODE == kShuffle) {
+            float2 ox[2], oy[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ox[j].x = __shfl_sync(0xffffffffu, x[j].x, partner);
+                ox[j].y = __shfl_sync(0xffffffffu, x[j].y, partner);
+                oy[j].x = __shfl_sync(0xffffffffu, y[j].x, partner);
+                oy[j].y = __shfl_sync(0xffffffffu, y[j].y, partner);
+            }
+            if (turn) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[j] = add2(mul2(x[j], c[j]), mul2(ox[j], s[j]));
+                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(oy[j], s[j + 2]));
+                }
+            }
+        } else if (turn) {
+            if constexpr (MODE == kSplit) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 v = x[j], w = y[j];
+                    x[j] = add2(mul2(v, c[j]), mul2(w, ns[j]));
+                    y[j] = add2(mul2(w, c[j]), mul2(v, s[j]));
                 }
             } else {
-                // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
-                const Factor f = factor_of(is_v ? p.v_g : p.k_g);
-                float ma = largest(x), mb = largest(y);
-                if (!apart) ma = mb = max_nan(ma, mb);
-                ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-                if constexpr (MODE == kSplit) {
-                    mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-                    const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
-                    if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
-                    else mb = ma;
-                } else {
-                    mb = ma;
-                }
-                // a NaN counts as 0: the largest of the others
-                const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
-                if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
-                    float va = 0.f, vb = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-                        vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
-                    }
-                    if (!apart) va = vb = fmaxf(va, vb);
-                    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
-                    vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
-                    const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
-                    if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
-                    if (ma != ma) ma = va;
-                    if (mb != mb) mb = vb;
+                for (int j = 0; j < 2; ++j) {
+                    x[j] = add2(mul2(x[j], c[j]), mul2(make_float2(x[j].y, x[j].x), s[j]));
+                    y[j] = add2(mul2(y[j], c[j + 2]), mul2(make_float2(y[j].y, y[j].x), s[j + 2]));
                 }
-                float ta, tb;
-                const uint32_t ca = group_scale(ma, f, ta);
-                uint32_t cb = ca;
-                tb = ta;
-                if (apart) cb = group_scale(mb, f, tb);
-                const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
-                if (mine) {
-                    char *cd = pool + row * (D / 2);
-                    uint8_t *sd = p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * (D / 16);
-                    if (apart) {
-                        *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
-                        *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
-                        if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
-                    } else {
-                        *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
-                        if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
-                    }
+            }
+        }
+    };
+    auto put = [&](T *dst, const Chunk<T> &ca, const Chunk<T> &cb) {
+        if constexpr (MODE == kSplit) ca.store(dst + da), cb.store(dst + db);
+        else Chunk<T>::store2(dst + da, ca, cb);
+    };
+    if (queries) {
+        T *dst = reinterpret_cast<T *>(p.q_out) + (token * p.H + from * RPW + lr) * D;
+#pragma unroll
+        for (int u = 0; u < QB; ++u) {
+            if (u >= count) break;             // the same for the whole warp
+            float2 x[2], y[2];
+            ra[u].unpack(x);
+            rb[u].unpack(y);
+            turned(x, y);
+            if ((from + u) * RPW + lr < HQ) {
+                ra[u].pack(x);
+                rb[u].pack(y);
+                put(dst + u * RPW * D, ra[u], rb[u]);
+            }
+        }
+        return;
+    }
+
+    const bool to_cache = blk >= 0 && blk < p.num_blocks;
+    if (!to_cache && blockIdx.y == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+    const int64_t first = (int64_t)(from * RPW + lr) * p.bs + slot;   // this lane's first row in the block
+    // quantising takes a few hundred instructions: one copy of them, the rows
+    // moved up to it
+#pragma unroll(FP4 ? 1 : QB)
+    for (int u = 0; u < 2 * KB; ++u) {
+        const int i = u < KB ? u : u - KB;
+        const bool is_v = u >= KB;
+        Chunk<T> &row_a = ra[FP4 ? 0 : u], &row_b = rb[FP4 ? 0 : u];
+        if (FP4 && u > 0) {
+#pragma unroll
+            for (int j = 0; j + 1 < 2 * KB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
+        }
+        if (i >= count) continue;              // the same for the whole warp
+        const bool mine = to_cache && (from + i) * RPW + lr < p.Hkv;
+        const int64_t row = first + (int64_t)i * RPW * p.bs;
+        char *pool = (is_v ? p.v_pool : p.k_pool) + blk * p.block_stride_bytes;
+        float2 x[2], y[2];
+        if (FP4 || !is_v) {
+            row_a.unpack(x);
+            row_b.unpack(y);
+        }
+        if (!is_v) turned(x, y);
+        if constexpr (!FP4) {
+            if (mine) {
+                if (!is_v) {                   // values go as they came, to the last bit
+                    row_a.pack(x);
+                    row_b.pack(y);
+                }
+                put(reinterpret_cast<T *>(pool) + row * D, row_a, row_b);
+            }
+        } else {
+            // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
+            const Factor f = factor_of(is_v ? p.v_g : p.k_g);
+            float ma = largest(x), mb = largest(y);
+            if (!apart) ma = mb = max_nan(ma, mb);
+            ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+            if constexpr (MODE == kSplit) {
+                mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
+                if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
+                else mb = ma;
+            } else {
+                mb = ma;
+            }
+            // a NaN counts as 0: the largest of the others
+            const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
+            if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
+                float va = 0.f, vb = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+                    vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
+                }
+                if (!apart) va = vb = fmaxf(va, vb);
+                va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
+                vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
+                const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
+                if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
+                if (ma != ma) ma = va;
+                if (mb != mb) mb = vb;
+            }
+            float ta, tb;
+            const uint32_t ca = group_scale(ma, f, ta);
+            uint32_t cb = ca;
+            tb = ta;
+            if (apart) cb = group_scale(mb, f, tb);
+            const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
+            if (mine) {
+                char *cd = pool + row * (D / 2);
+                uint8_t *sd = p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * (D / 16);
+                if (apart) {
+                    *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
+                    *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
+                    if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
+                } else {
+                    *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
+                    if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
                 }
             }
         }
@@ -437,7 +437,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
 
 template <typename T, int D, bool FP4, RopeMode MODE>
 static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
-    constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T>;
+    constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T, FP4>, KB = kKeyBatch<T, FP4>;
     const int nq = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
@@ -445,14 +445,15 @@ static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
     // Rows per run: as many as are loaded at once, which amortises what a token
     // costs; fewer for few tokens, until every SM has 16 warps at most.
     const int64_t tokens = (int64_t)p.B * p.T, warps = (int64_t)sms * 16;
-    int q_run = QB, kv_run = QB / 2;
+    int q_run = QB, kv_run = KB;
     while (q_run > 1 && tokens * ((nq + q_run / 2 - 1) / (q_run / 2) + (nk + kv_run - 1) / kv_run) <= warps) q_run /= 2;
     while (kv_run > 1 && tokens * ((nq + q_run - 1) / q_run + (nk + kv_run / 2 - 1) / (kv_run / 2)) <= warps) kv_run /= 2;
-    const int64_t runs = (nq + q_run - 1) / q_run + (nk + kv_run - 1) / kv_run;
-    int64_t gy = ((int64_t)p.T * runs + kRopeWarps - 1) / kRopeWarps;
-    gy = gy > 65535 ? 65535 : gy;
+    const int kv_runs = (nk + kv_run - 1) / kv_run, runs = (nq + q_run - 1) / q_run + kv_runs;
+    if (runs > 65535) return cudaErrorInvalidValue;
+    const int64_t gx = (tokens + kRopeWarps - 1) / kRopeWarps;
+    if (gx > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.B, (unsigned)gy, 1);
+    cfg.gridDim = dim3((unsigned)gx, (unsigned)runs, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -460,7 +461,7 @@ static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = PA_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4, MODE>, p, q_run, kv_run);
+    return cudaLaunchKernelEx(&cfg, rope_append_kernel<T, D, FP4, MODE>, p, q_run, kv_run, kv_runs);
 }
 
 template <typename T, int D, bool FP4>

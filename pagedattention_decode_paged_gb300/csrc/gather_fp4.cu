@@ -1,22 +1,25 @@
 // gather_fp4.cu -- rows of the 4-bit cache back as values.
 //
-// Bound by HBM: D/2 + D/16 bytes read and D elements written per row.  A
-// thread turns one group of 16 codes (8 bytes) and its scale into 16 values
-// (32 bytes of a 16-bit type); the groups of all heads of a token, K then V,
-// are spread over the lanes of a warp, so that the output of a token is
-// written in whole lines and the table is looked up once per token.
+// Bound by HBM: D/2 + D/16 bytes read and D elements written per row, so mostly
+// by writes.  A thread turns as many codes as make 16 bytes of output (8 of a
+// 16-bit type, 4 of fp32), so that every store of a warp is 512 contiguous bytes
+// (32 bytes a thread, stored as two halves, took 58.3 us where this takes GATH us:
+// 32 contexts of 1500 to 2048 tokens, 8 heads of 128, bf16).  The pieces of all
+// heads of a token, K then V, are spread over the lanes of a warp, which looks
+// up the table once for the token.
 #include "fp4.cuh"
 #include "pa_rope_fp4.h"
 
 namespace pa {
 
 constexpr int kGatherThreads = 256;
+constexpr int kGatherPieces = 8;   // pieces in flight per lane
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_fp4_kernel(const __grid_constant__ GatherFp4Params p) {
     grid_dependency_wait();
     allow_dependents();
-    constexpr int G = D / 16;                      // groups per row
+    constexpr int E = 16 / (int)sizeof(T), G = D / E;   // elements of a piece, pieces of a row
     const int b = blockIdx.x;
     const int n = p.counts != nullptr ? p.counts[b] : p.T;
     const int32_t start = p.starts[b];
@@ -40,54 +43,56 @@ __global__ void __launch_bounds__(kGatherThreads) gather_fp4_kernel(const __grid
         int64_t blk = -1;
         int slot = 0;
         if (!bad_pos) {
-            const int j = pos / p.bs;
+            const int j = p.bs_shift >= 0 ? pos >> p.bs_shift : pos / p.bs;
             slot = pos - j * p.bs;
-            blk = p.block_table[(int64_t)b * p.MB + j];
+            blk = __ldg(p.block_table + (int64_t)b * p.MB + j);
         }
         const bool ok = blk >= 0 && blk < p.num_blocks;
         if (!bad_pos && !ok && piece0 == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
         const int64_t token = (int64_t)b * p.T + t;
-        for (int i = piece0; i < per_token; i += per_warp > 1 ? per_token : 32) {
-            const int gi = i % G;
-            const int r = i / G;
-            const bool is_v = r >= p.Hkv;
-            const int h = is_v ? r - p.Hkv : r;
-            float x[16];
+        const int stride = per_warp > 1 ? per_token : 32;
+#pragma unroll 1
+        for (int i0 = piece0; i0 < per_token; i0 += kGatherPieces * stride) {
+            uint32_t w[kGatherPieces], sc[kGatherPieces];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-            if (ok) {
-                const int64_t row = (int64_t)h * p.bs + slot;
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>((is_v ? p.v_pool : p.k_pool) +
-                                                                      blk * p.block_stride_bytes + row * (D / 2)) + gi);
-                const uint32_t sc = __ldg(p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * G + gi);
-                const uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
-                const float g = is_v ? p.v_g : p.k_g;
-                const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t f[4] = {e2m1x2_to_f16x2<0>(ww[k]), e2m1x2_to_f16x2<1>(ww[k]),
-                                           e2m1x2_to_f16x2<2>(ww[k]), e2m1x2_to_f16x2<3>(ww[k])};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = f16x2_to_float2(hmul2_u32(f[j], s2));
-                        x[8 * k + 2 * j] = v.x * g;
-                        x[8 * k + 2 * j + 1] = v.y * g;
-                    }
+            for (int u = 0; u < kGatherPieces; ++u) {
+                const int i = i0 + u * stride;
+                w[u] = sc[u] = 0;
+                if (ok && i < per_token) {
+                    const int r = i / G, h = r < p.Hkv ? r : r - p.Hkv;
+                    const int64_t row = (int64_t)h * p.bs + slot;
+                    const uint8_t *codes = (r < p.Hkv ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes + row * (D / 2) + i % G * (E / 2);
+                    if constexpr (E == 8) w[u] = __ldg(reinterpret_cast<const uint32_t *>(codes));
+                    else w[u] = __ldg(reinterpret_cast<const uint16_t *>(codes));
+                    sc[u] = __ldg(p.scales + ((blk * 2 + (r < p.Hkv ? 0 : 1)) * p.Hkv * p.bs + row) * (D / 16) + i % G * E / 16);
                 }
             }
-            T *dst = reinterpret_cast<T *>(is_v ? p.v_out : p.k_out) + (token * p.Hkv + h) * D + gi * 16;
-            float lo[8], hi[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lo[j] = x[j], hi[j] = x[8 + j];
-            store8(dst, lo);
-            store8(dst + 8, hi);
+            for (int u = 0; u < kGatherPieces; ++u) {
+                const int i = i0 + u * stride;
+                if (i >= per_token) break;
+                const int r = i / G, h = r < p.Hkv ? r : r - p.Hkv;
+                const float g = r < p.Hkv ? p.k_g : p.v_g;
+                const uint32_t s2 = e4m3x2_to_f16x2(sc[u] | (sc[u] << 8));
+                T *dst = reinterpret_cast<T *>(r < p.Hkv ? p.k_out : p.v_out) + (token * p.Hkv + h) * D + i % G * E;
+                const float2 a = f16x2_to_float2(hmul2_u32(e2m1x2_to_f16x2<0>(w[u]), s2));
+                const float2 c = f16x2_to_float2(hmul2_u32(e2m1x2_to_f16x2<1>(w[u]), s2));
+                if constexpr (E == 8) {
+                    const float2 d = f16x2_to_float2(hmul2_u32(e2m1x2_to_f16x2<2>(w[u]), s2));
+                    const float2 e = f16x2_to_float2(hmul2_u32(e2m1x2_to_f16x2<3>(w[u]), s2));
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(Elem<T>::pack2(a.x * g, a.y * g), Elem<T>::pack2(c.x * g, c.y * g),
+                                                                 Elem<T>::pack2(d.x * g, d.y * g), Elem<T>::pack2(e.x * g, e.y * g));
+                } else {
+                    *reinterpret_cast<float4 *>(dst) = make_float4(a.x * g, a.y * g, c.x * g, c.y * g);
+                }
+            }
         }
     }
 }
 
 template <typename T, int D>
 static cudaError_t launch_one(const GatherFp4Params &p, cudaStream_t stream) {
-    const int per_token = 2 * p.Hkv * (D / 16);
+    const int per_token = 2 * p.Hkv * (D * (int)sizeof(T) / 16);
     const int per_cta = (kGatherThreads / 32) * (32 / per_token > 1 ? 32 / per_token : 1);
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);

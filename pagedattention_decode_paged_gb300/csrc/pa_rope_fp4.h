@@ -28,6 +28,7 @@ struct RopeAppendParams {
     int64_t num_blocks;
     int64_t block_stride_bytes;
     int32_t B, T, H, Hkv, MB, bs;
+    int32_t bs_shift;          // log2(bs) when bs is a power of two, else -1
     int32_t max_position, R, pairs;
     float eps;
     float k_g, v_g;
@@ -50,6 +51,7 @@ struct GatherFp4Params {
     int64_t num_blocks;
     int64_t block_stride_bytes;
     int32_t B, T, Hkv, MB, bs;
+    int32_t bs_shift;
     float k_g, v_g;
 };
 
