@@ -123,40 +123,90 @@ __device__ __forceinline__ Factor factor_of(float g) {
     return f;
 }
 // The E4M3 code of a group with largest magnitude a, and the value t that its
-// codes are multiples of.
-__device__ __forceinline__ uint32_t group_scale(float a, const Factor &f, float &t) {
-    float q;
-    if (a <= f.limit) {
-        q = __fmul_rn(a, f.r6);
-        q = __fmaf_rn(__fmaf_rn(-q, f.six_g, a), f.r6, q);
-    } else {
-        q = a == a ? __fdiv_rn(a, f.six_g) : 0.f;
-    }
-    const uint32_t code = f32_to_e4m3(q);
-    t = __fmul_rn(f16x2_to_float2(e4m3x2_to_f16x2(code)).x, f.g);
-    return code;
+// codes are multiples of; a within the factor's limit (Markstein), or any.
+__device__ __forceinline__ float group_value(uint32_t code, const Factor &f) {
+    return __fmul_rn(f16x2_to_float2(e4m3x2_to_f16x2(code)).x, f.g);
 }
-// Two bytes of codes of x / t; `plain` if the group's largest magnitude was
-// within the factor's limit.
-__device__ __forceinline__ uint32_t group_codes(const float2 (&x)[2], float t, bool plain) {
-    if (!(t > 0.f)) return 0;
-    float2 y[2];
-    if (plain) {
-        const float2 tt = both(t), minus_r = both(-__frcp_rn(t));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {              // (q t - x) (-r) + q keeps the sign of a zero
-            const float2 minus_x = mul2(x[j], both(-1.f));
-            y[j] = mul2(minus_x, minus_r);
-            y[j] = fma2(fma2(y[j], tt, minus_x), minus_r, y[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            y[j].x = x[j].x == x[j].x ? __fdiv_rn(x[j].x, t) : 0.f;
-            y[j].y = x[j].y == x[j].y ? __fdiv_rn(x[j].y, t) : 0.f;
-        }
-    }
+__device__ __forceinline__ uint32_t group_scale(float a, const Factor &f) {
+    const float q = __fmul_rn(a, f.r6);
+    return f32_to_e4m3(__fmaf_rn(__fmaf_rn(-q, f.six_g, a), f.r6, q));
+}
+__device__ __forceinline__ uint32_t group_scale_any(float a, const Factor &f) { return f32_to_e4m3(__fdiv_rn(a, f.six_g)); }
+// Two bytes of codes of x / t, r the reciprocal of t > 0; or any x and t.
+__device__ __forceinline__ uint32_t pack_codes(const float2 (&y)[2]) {
     return f32x2_to_e2m1x2(y[0].x, y[0].y) | f32x2_to_e2m1x2(y[1].x, y[1].y) << 8;
+}
+__device__ __forceinline__ uint32_t group_codes(const float2 (&x)[2], float t, float r) {
+    float2 y[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {                  // (q t - x) (-r) + q keeps the sign of a zero
+        const float2 minus_x = mul2(x[j], both(-1.f));
+        y[j] = mul2(minus_x, both(-r));
+        y[j] = fma2(fma2(y[j], both(t), minus_x), both(-r), y[j]);
+    }
+    return pack_codes(y);
+}
+__device__ __forceinline__ uint32_t group_codes_any(const float2 (&x)[2], float t) {
+    float2 y[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        y[j].x = x[j].x == x[j].x ? __fdiv_rn(x[j].x, t) : 0.f;
+        y[j].y = x[j].y == x[j].y ? __fdiv_rn(x[j].y, t) : 0.f;
+    }
+    return t > 0.f ? pack_codes(y) : 0;
+}
+
+// Quantise a row: chunks x and y of this lane.  A group of 16 is 4 lanes' chunks x
+// or chunks y if they are `apart` (SPLIT only), else 2 lanes' both chunks.  The
+// scale of a lane pair's two groups is found by one lane of the pair each.  Codes
+// go to cd + da / 2, cd + db / 2, scales to sd, if `mine`.
+template <bool SPLIT>
+__device__ __forceinline__ void store_fp4(const float2 (&x)[2], const float2 (&y)[2], const Factor &f, bool apart, bool mine,
+                                          int sub, int da, int db, uint8_t *cd, uint8_t *sd) {
+    const unsigned all = 0xffffffffu;
+    float mx = largest(x), my = largest(y);
+    if (!apart) mx = my = max_nan(mx, my);
+    mx = max_nan(mx, __shfl_xor_sync(all, mx, 1));
+    if constexpr (SPLIT) {
+        my = max_nan(my, __shfl_xor_sync(all, my, 1));
+        const float fx = __shfl_xor_sync(all, mx, 2), fy = __shfl_xor_sync(all, my, 2);
+        if (apart) mx = max_nan(mx, fx), my = max_nan(my, fy);
+    }
+    const bool odd = (sub & 1) != 0;
+    uint32_t code, wx, wy;                         // of this lane's group; the codes of both chunks
+    if (__all_sync(all, mx <= f.limit && (!SPLIT || my <= f.limit))) {
+        code = group_scale(SPLIT && odd ? my : mx, f);
+        const float t = group_value(code, f), r = t > 0.f ? __frcp_rn(t) : 0.f;
+        float tx = t, ty = t, rx = r, ry = r;
+        if constexpr (SPLIT) {
+            const float ot = __shfl_xor_sync(all, t, 1), orr = __shfl_xor_sync(all, r, 1);
+            tx = odd ? ot : t, ty = odd ? t : ot;
+            rx = odd ? orr : r, ry = odd ? r : orr;
+        }
+        wx = tx > 0.f ? group_codes(x, tx, rx) : 0;
+        wy = ty > 0.f ? group_codes(y, ty, ry) : 0;
+    } else {                                       // a NaN counts as 0
+        float vx = fmaxf(fmaxf(fabsf(x[0].x), fabsf(x[0].y)), fmaxf(fmaxf(fabsf(x[1].x), fabsf(x[1].y)), 0.f));
+        float vy = fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fmaxf(fabsf(y[1].x), fabsf(y[1].y)), 0.f));
+        if (!apart) vx = vy = fmaxf(vx, vy);
+        vx = fmaxf(vx, __shfl_xor_sync(all, vx, 1));
+        vy = fmaxf(vy, __shfl_xor_sync(all, vy, 1));
+        const float fx = __shfl_xor_sync(all, vx, 2), fy = __shfl_xor_sync(all, vy, 2);
+        if (apart) vx = fmaxf(vx, fx), vy = fmaxf(vy, fy);
+        const uint32_t cx = group_scale_any(vx, f), cy = group_scale_any(vy, f);
+        wx = group_codes_any(x, group_value(cx, f));
+        wy = group_codes_any(y, group_value(cy, f));
+        code = SPLIT && odd ? cy : cx;
+    }
+    if (!mine) return;
+    if (apart) {
+        *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)wx;
+        *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)wy;
+        if (sub % 4 < 2) sd[(odd ? db : da) / 16] = (uint8_t)code;
+    } else {
+        *reinterpret_cast<uint32_t *>(cd + da / 2) = wx | wy << 16;
+        if (!odd) sd[da / 16] = (uint8_t)code;
+    }
 }
 
 // grid: x = kRopeWarps tokens of the padded batch each, y = run: of kv_run
@@ -178,6 +228,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
     constexpr int LPR = D / 8;                     // lanes per row
     constexpr int RPW = 32 / LPR;                  // rows per iteration of a warp
     constexpr int QB = kRopeBatch<T, FP4>, KB = kKeyBatch<T, FP4>;
+    static_assert(2 * KB <= QB, "");
     const int64_t token = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     if (token >= (int64_t)p.B * p.T) return;
     const int b = p.T == 1 ? (int)token : token <= INT32_MAX ? (int)((uint32_t)token / (uint32_t)p.T) : (int)(token / p.T);
@@ -215,8 +266,9 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
             ra[u].zero();
             rb[u].zero();
             if (i < count && (queries || u < 2 * KB) && (from + i) * RPW + lr < heads) {
-                if constexpr (MODE == kSplit) ra[u].load(row + da), rb[u].load(row + db);
-                else Chunk<T>::load2(row + da, ra[u], rb[u]);
+                // values that are quantised: neighbouring chunks, one group a lane
+                if (MODE == kSplit && !(FP4 && !queries && u >= KB)) ra[u].load(row + da), rb[u].load(row + db);
+                else Chunk<T>::load2(row + 8 * sub, ra[u], rb[u]);
             }
         }
     }
@@ -353,84 +405,52 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
     const bool to_cache = blk >= 0 && blk < p.num_blocks;
     if (!to_cache && blockIdx.y == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_BLOCK);
     const int64_t first = (int64_t)(from * RPW + lr) * p.bs + slot;   // this lane's first row in the block
-    // quantising takes a few hundred instructions: one copy of them, the rows
-    // moved up to it
-#pragma unroll(FP4 ? 1 : QB)
-    for (int u = 0; u < 2 * KB; ++u) {
-        const int i = u < KB ? u : u - KB;
-        const bool is_v = u >= KB;
-        Chunk<T> &row_a = ra[FP4 ? 0 : u], &row_b = rb[FP4 ? 0 : u];
-        if (FP4 && u > 0) {
+    if constexpr (FP4) {
+        const Factor fk = factor_of(p.k_g), fv = factor_of(p.v_g);
+        const int64_t code_step = (int64_t)RPW * p.bs * (D / 2), scale_step = (int64_t)RPW * p.bs * (D / 16);
+        uint8_t *cd = reinterpret_cast<uint8_t *>(p.k_pool) + blk * p.block_stride_bytes + first * (D / 2);
+        uint8_t *sd = p.scales + (blk * 2 * p.Hkv * p.bs + first) * (D / 16);
+        // one copy of the code for the keys, one for the values: the rows move up to it
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+            float2 x[2], y[2];
+            ra[0].unpack(x);
+            rb[0].unpack(y);
+            turned(x, y);
+            store_fp4<MODE == kSplit>(x, y, fk, apart, to_cache && (from + i) * RPW + lr < p.Hkv, sub, da, db, cd + i * code_step,
+                                      sd + i * scale_step);
 #pragma unroll
-            for (int j = 0; j + 1 < 2 * KB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
+            for (int j = 0; j + 1 < KB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
         }
-        if (i >= count) continue;              // the same for the whole warp
-        const bool mine = to_cache && (from + i) * RPW + lr < p.Hkv;
-        const int64_t row = first + (int64_t)i * RPW * p.bs;
-        char *pool = (is_v ? p.v_pool : p.k_pool) + blk * p.block_stride_bytes;
-        float2 x[2], y[2];
-        if (FP4 || !is_v) {
-            row_a.unpack(x);
-            row_b.unpack(y);
-        }
-        if (!is_v) turned(x, y);
-        if constexpr (!FP4) {
-            if (mine) {
-                if (!is_v) {                   // values go as they came, to the last bit
-                    row_a.pack(x);
-                    row_b.pack(y);
-                }
-                put(reinterpret_cast<T *>(pool) + row * D, row_a, row_b);
-            }
-        } else {
-            // a group of 16 is 4 lanes' chunks a, or chunks b, or 2 lanes' both chunks
-            const Factor f = factor_of(is_v ? p.v_g : p.k_g);
-            float ma = largest(x), mb = largest(y);
-            if (!apart) ma = mb = max_nan(ma, mb);
-            ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-            if constexpr (MODE == kSplit) {
-                mb = max_nan(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-                const float fa = __shfl_xor_sync(0xffffffffu, ma, 2), fb = __shfl_xor_sync(0xffffffffu, mb, 2);
-                if (apart) ma = max_nan(ma, fa), mb = max_nan(mb, fb);
-                else mb = ma;
-            } else {
-                mb = ma;
-            }
-            // a NaN counts as 0: the largest of the others
-            const bool plain_a = ma <= f.limit, plain_b = mb <= f.limit;
-            if (__any_sync(0xffffffffu, ma != ma || mb != mb)) {
-                float va = 0.f, vb = 0.f;
+        cd = reinterpret_cast<uint8_t *>(p.v_pool) + blk * p.block_stride_bytes + first * (D / 2);
+        sd += (int64_t)p.Hkv * p.bs * (D / 16);
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+            float2 x[2], y[2];
+            ra[KB].unpack(x);
+            rb[KB].unpack(y);
+            store_fp4<false>(x, y, fv, false, to_cache && (from + i) * RPW + lr < p.Hkv, sub, 8 * sub, 8 * sub + 4,
+                             cd + i * code_step, sd + i * scale_step);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    va = fmaxf(va, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-                    vb = fmaxf(vb, fmaxf(fabsf(y[j].x), fabsf(y[j].y)));
-                }
-                if (!apart) va = vb = fmaxf(va, vb);
-                va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
-                vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
-                const float fa = __shfl_xor_sync(0xffffffffu, va, 2), fb = __shfl_xor_sync(0xffffffffu, vb, 2);
-                if (apart) va = fmaxf(va, fa), vb = fmaxf(vb, fb);
-                if (ma != ma) ma = va;
-                if (mb != mb) mb = vb;
+            for (int j = KB; j + 1 < 2 * KB; ++j) ra[j] = ra[j + 1], rb[j] = rb[j + 1];
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2 * KB; ++u) {
+            const int i = u < KB ? u : u - KB;
+            if (i >= count) continue;              // the same for the whole warp
+            if (u < KB) {                          // values go as they came, to the last bit
+                float2 x[2], y[2];
+                ra[u].unpack(x);
+                rb[u].unpack(y);
+                turned(x, y);
+                ra[u].pack(x);
+                rb[u].pack(y);
             }
-            float ta, tb;
-            const uint32_t ca = group_scale(ma, f, ta);
-            uint32_t cb = ca;
-            tb = ta;
-            if (apart) cb = group_scale(mb, f, tb);
-            const uint32_t xa = group_codes(x, ta, plain_a), xb = group_codes(y, tb, plain_b);
-            if (mine) {
-                char *cd = pool + row * (D / 2);
-                uint8_t *sd = p.scales + ((blk * 2 + (is_v ? 1 : 0)) * p.Hkv * p.bs + row) * (D / 16);
-                if (apart) {
-                    *reinterpret_cast<uint16_t *>(cd + da / 2) = (uint16_t)xa;
-                    *reinterpret_cast<uint16_t *>(cd + db / 2) = (uint16_t)xb;
-                    if (sub % 4 == 0) sd[da / 16] = (uint8_t)ca, sd[db / 16] = (uint8_t)cb;
-                } else {
-                    *reinterpret_cast<uint32_t *>(cd + da / 2) = xa | xb << 16;
-                    if (sub % 2 == 0) sd[da / 16] = (uint8_t)ca;
-                }
-            }
+            if (to_cache && (from + i) * RPW + lr < p.Hkv)
+                put(reinterpret_cast<T *>((u < KB ? p.k_pool : p.v_pool) + blk * p.block_stride_bytes) +
+                        (first + (int64_t)i * RPW * p.bs) * D,
+                    ra[u], rb[u]);
         }
     }
 }
