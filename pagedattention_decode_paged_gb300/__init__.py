@@ -89,6 +89,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load the in-tree library; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not LIB_PATH.exists():
@@ -532,7 +534,11 @@ def _launch_stream(stream, what, *tensors):
     """The stream a call runs on, after checking that every tensor (None aside)
     lies on the current device, the one the kernels are launched on."""
     dev = tensors[0].get_device()
-    if dev < 0 or dev != torch.cuda.current_device() or any(t is not None and t.get_device() != dev for t in tensors):
+    ok = dev >= 0 and dev == torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            ok = False
+    if not ok:
         raise ValueError(f"{what}: all tensors must be on the current CUDA device")
     if stream is None:
         return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
@@ -543,11 +549,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dense(**tensors) -> None:
-    """Every tensor (given as name=(tensor, dtype)) is contiguous and of its dtype."""
-    for what, (t, dtype) in tensors.items():
-        if not (t.dtype == dtype and t.is_contiguous()):
-            raise ValueError(f"{what} must be a contiguous {dtype} tensor")
+def _dense(what, dtype, *tensors) -> None:
+    for t in tensors:
+        if t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {dtype} tensors")
 
 
 def _new_rows(what, x):
@@ -591,21 +596,19 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
         if q_out is None or q_out.numel() != B * T * H * D or q_out.dtype != dt or not q_out.is_contiguous():
             raise ValueError(f"q_out must be contiguous, with batch * tokens * heads * head_dim elements of {dt}")
         qp = q.data_ptr()
-    if not (block_table.dtype == torch.int32 and block_table.is_contiguous() and positions.dtype == torch.int32
-            and positions.is_contiguous()):
-        raise ValueError("block_table and positions must be contiguous torch.int32 tensors")
+    _dense("block_table and positions", torch.int32, block_table, positions)
     if block_table.shape[0] != B or positions.numel() != B:
         raise ValueError("block_table and positions must have one row per sequence")
     if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
         raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
     fp4 = kv_scales is not None
     if fp4:
-        _dense(kv_scales=(kv_scales, torch.uint8))
+        _dense("kv_scales", torch.uint8, kv_scales)
     if k_pool.dtype != v_pool.dtype or k_pool.dtype != (torch.uint8 if fp4 else dt):
         raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
     R, most = 0, 0
     if cos_sin is not None:
-        _dense(cos_sin=(cos_sin, torch.float32))
+        _dense("cos_sin", torch.float32, cos_sin)
         most, R = cos_sin.shape
         if rotary_dim is not None and rotary_dim != R:
             raise ValueError("cos_sin must be [max_position][rotary_dim]")
@@ -671,8 +674,9 @@ def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, st
     dt = k_out.dtype
     if v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out differ in shape")
-    _dense(k_out=(k_out, dt), v_out=(v_out, dt), kv_scales=(kv_scales, torch.uint8), block_table=(block_table, torch.int32),
-           starts=(starts, torch.int32))
+    _dense("k_out and v_out", dt, k_out, v_out)
+    _dense("kv_scales", torch.uint8, kv_scales)
+    _dense("block_table and starts", torch.int32, block_table, starts)
     if block_table.shape[0] != B or starts.numel() != B:
         raise ValueError("block_table and starts must have one row per sequence")
     if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
@@ -712,8 +716,9 @@ def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, s
     dt = q.dtype
     if out.shape != q.shape:
         raise ValueError("out and q differ in shape")
-    _dense(q=(q, dt), out=(out, dt), kv_scales=(kv_scales, torch.uint8), block_table=(block_table, torch.int32),
-           seq_lens=(seq_lens, torch.int32), workspace=(workspace, torch.uint8))
+    _dense("q and out", dt, q, out)
+    _dense("kv_scales and workspace", torch.uint8, kv_scales, workspace)
+    _dense("block_table and seq_lens", torch.int32, block_table, seq_lens)
     if block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError("block_table and seq_lens must have one row per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:

@@ -212,13 +212,11 @@ __device__ __forceinline__ void store_fp4(const float2 (&x)[2], const float2 (&y
 // grid: x = kRopeWarps tokens of the padded batch each, y = run: of kv_run
 // iterations of keys and values, then of q_run iterations of queries (at most
 // KB and QB), so that the warps of a CTA do the same.
-template <typename T, bool FP4>
+// Iterations of queries a run has at most, as many as keep their registers; half
+// as many of keys, with their values (f16 prompts into the 4-bit cache: 1 of
+// each 41 us, 2 31.9 us, 4 28.8 us, where the first had no CTAs of their own).
+template <typename T>
 constexpr int kRopeBatch = sizeof(T) == 2 ? 8 : 4;
-// Quantising a row takes as long as turning several: fewer to a run, so that the
-// warps of a CTA finish together (f16 prompts into the 4-bit cache: 4 keys and 4
-// values a run 50 us, 1 of each 41 us, before runs had CTAs of their own).
-template <typename T, bool FP4>
-constexpr int kKeyBatch = FP4 ? 2 : kRopeBatch<T, FP4> / 2;
 
 template <typename T, int D, bool FP4, RopeMode MODE>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 5)
@@ -227,8 +225,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
     allow_dependents();
     constexpr int LPR = D / 8;                     // lanes per row
     constexpr int RPW = 32 / LPR;                  // rows per iteration of a warp
-    constexpr int QB = kRopeBatch<T, FP4>, KB = kKeyBatch<T, FP4>;
-    static_assert(2 * KB <= QB, "");
+    constexpr int QB = kRopeBatch<T>, KB = QB / 2;
     const int64_t token = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     if (token >= (int64_t)p.B * p.T) return;
     const int b = p.T == 1 ? (int)token : token <= INT32_MAX ? (int)((uint32_t)token / (uint32_t)p.T) : (int)(token / p.T);
@@ -457,7 +454,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
 
 template <typename T, int D, bool FP4, RopeMode MODE>
 static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
-    constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T, FP4>, KB = kKeyBatch<T, FP4>;
+    constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T>, KB = QB / 2;
     const int nq = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);

@@ -3,7 +3,7 @@
 // Bound by HBM: D/2 + D/16 bytes read and D elements written per row, so mostly
 // by writes.  A thread turns as many codes as make 16 bytes of output (8 of a
 // 16-bit type, 4 of fp32), so that every store of a warp is 512 contiguous bytes
-// (32 bytes a thread, stored as two halves, took 58.3 us where this takes GATH us:
+// (32 bytes a thread, stored as two halves, took 58.3 us where this takes 55.6 us:
 // 32 contexts of 1500 to 2048 tokens, 8 heads of 128, bf16).  The pieces of all
 // heads of a token, K then V, are spread over the lanes of a warp, which looks
 // up the table once for the token.
