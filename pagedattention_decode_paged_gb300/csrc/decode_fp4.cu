@@ -39,7 +39,7 @@ namespace pa {
 
 constexpr int kFp4Tile = 32;       // tokens of a tile: two halves of 16, the MMAs' token axis
 constexpr int kFp4Halves = kFp4Tile / 16;
-constexpr float kFp4Empty = -1e30f;   // reference of a column without scores: far below any, and finite
+constexpr float kFp4Empty = -3.402823466e38f;   // reference of a column without scores: below any, and finite
 constexpr int kFp4Item = 1;        // what an item costs beside its tiles (queries, output), in tiles
 constexpr int kFp4MinTiles = 1;    // tiles per warp below which fewer CTAs share the work
 constexpr int kFp4Snap = 4;        // tiles per warp that a CTA may have above the mean to end where items end
@@ -90,12 +90,23 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// W equal runs of T places: run w starts at floor(w T / W), here without a
-// 64-bit division.
+// Tiles of a sequence of L tokens.
+__device__ __forceinline__ int32_t fp4_window_start(int32_t L, int32_t window) {
+    return window > 0 && L > window ? L - window : 0;
+}
+__device__ __forceinline__ int32_t fp4_tiles(int32_t L, int32_t window) {
+    return (L - fp4_window_start(L, window) / kFp4Tile * kFp4Tile + kFp4Tile - 1) / kFp4Tile;
+}
+
+// W equal runs of T places: run w starts at floor(w T / W).  With T = q W + r
+// that is w q + floor(w r / W), and w r + 1/2 over W is further from an integer
+// than fp32 rounds it for every W up to 1024, so no division is needed.
 struct Fp4Runs {
     int32_t T, W, q, r;
-    __device__ __forceinline__ Fp4Runs(int32_t places, int32_t runs) : T(places), W(runs), q(places / runs), r(places % runs) {}
-    __device__ __forceinline__ int32_t start(int32_t w) const { return w * q + w * r / W; }
+    float inv;
+    __device__ __forceinline__ Fp4Runs(int32_t places, int32_t runs)
+        : T(places), W(runs), q(places / runs), r(places % runs), inv(1.f / (float)runs) {}
+    __device__ __forceinline__ int32_t start(int32_t w) const { return w * q + (int32_t)(((float)(w * r) + 0.5f) * inv); }
     __device__ __forceinline__ int32_t owner(int32_t t) const {   // of place t
         int32_t w = min(W - 1, (int32_t)(((float)t + 0.5f) * ((float)W / (float)T)));
         while (w > 0 && start(w) > t) --w;
@@ -110,7 +121,7 @@ struct Fp4Cursor {
     int b, it, n;
     int32_t first;
 
-    __device__ __forceinline__ void seek(const int32_t *pre, int B, int items_per_seq, int32_t t) {
+    __device__ __forceinline__ void seek(const int32_t *pre, const int32_t *lens, int32_t window, int B, int32_t t) {
         int lo = 0, hi = B;                    // pre[lo] <= t < pre[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -118,20 +129,23 @@ struct Fp4Cursor {
             else hi = mid;
         }
         b = lo;
-        const int places = (pre[b + 1] - pre[b]) / items_per_seq;
-        it = (t - pre[b]) / places;
+        n = fp4_tiles(lens[b], window);
+        // the quotient is below 2^20, so that in fp32 it is off by one at most
+        const int32_t places = n + kFp4Item, at = t - pre[b];
+        it = (int32_t)__fdividef((float)at, (float)places);
+        if (it * places > at) --it;
+        else if ((it + 1) * places <= at) ++it;
         first = pre[b] + it * places;
-        n = places - kFp4Item;
     }
     // To the next item; b is B behind the last one.
-    __device__ __forceinline__ void next(const int32_t *pre, int B, int items_per_seq) {
+    __device__ __forceinline__ void next(const int32_t *pre, const int32_t *lens, int32_t window, int B, int items_per_seq) {
         first += n + kFp4Item;
         if (++it < items_per_seq) return;
         it = 0;
         do {
             ++b;
         } while (b < B && pre[b + 1] == pre[b]);
-        if (b < B) n = (pre[b + 1] - pre[b]) / items_per_seq - kFp4Item;
+        if (b < B) n = fp4_tiles(lens[b], window);
     }
 };
 
@@ -147,8 +161,7 @@ __device__ __forceinline__ void fp4_schedule(const DecodeParams &p, int items_pe
     for (int b = b0; b < b1; ++b) {
         const int32_t L = p.seq_lens[b];
         const bool ok = L >= 0 && (int64_t)L <= (int64_t)p.MB * p.bs;
-        const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
-        const int32_t n = ok ? (L - t_win / kFp4Tile * kFp4Tile + kFp4Tile - 1) / kFp4Tile : 0;
+        const int32_t n = ok ? fp4_tiles(L, p.window) : 0;
         lens[b] = ok ? L : -1;
         pre[b] = n > 0 ? (n + kFp4Item) * items_per_seq : 0;
         s += pre[b];
@@ -243,6 +256,11 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 
     grid_dependency_wait();
     allow_dependents();
+    // the table is on its way to L2 while the lengths are read: a line per thread
+    {
+        const int64_t line = (int64_t)threadIdx.x * gridDim.x + blockIdx.x;
+        if (line * 32 < (int64_t)p.B * p.MB) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.block_table + line * 32));
+    }
     const int items_per_seq = p.Hkv * units_per_kv;
     fp4_schedule(p, items_per_seq, pre, lens, scan_tmp);
     zero_empty_sequences<T>(p, pre);
@@ -259,7 +277,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         int32_t t = runs.start(c);
         if (c > 0 && c < nC) {
             Fp4Cursor x;
-            x.seek(pre, p.B, items_per_seq, t);
+            x.seek(pre, lens, p.window, p.B, t);
             t = 2 * (t - x.first) <= x.n + kFp4Item ? x.first : x.first + x.n + kFp4Item;
         }
         snap[c] = t;
@@ -293,14 +311,14 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         p_k += p_i;
         p_i = 0;
         if (p_k >= p_end) {
-            pc.next(pre, p.B, items_per_seq);
+            pc.next(pre, lens, p.window, p.B, items_per_seq);
             p_k = 0;
             p_end = min(pc.n, w1 - pc.first - kFp4Item);
             p_more = pc.b < p.B && p_end > 0;
             if (!p_more) return;
         }
         const int32_t L = lens[pc.b];
-        const int32_t t_win = p.window > 0 && L > p.window ? L - p.window : 0;
+        const int32_t t_win = fp4_window_start(L, p.window);
         const int32_t base = t_win / kFp4Tile * kFp4Tile + p_k * kFp4Tile;
         const int hk = units_per_kv == 1 ? pc.it : pc.it / units_per_kv;
         p_left = WHOLE ? min(32 / kFp4Halves, p_end - p_k) : 1;
@@ -647,7 +665,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     };
 
     if (w0 < w1) {
-        pc.seek(pre, p.B, items_per_seq, w0);
+        pc.seek(pre, lens, p.window, p.B, w0);
         Fp4Cursor cc = pc;
         p_k = max(0, w0 - pc.first - kFp4Item);
         p_end = min(pc.n, w1 - pc.first - kFp4Item);
@@ -660,13 +678,13 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         }
         uint32_t now = ring, free_slot = ring + (S - 1) * C::kStage;   // the tile's slot, that of the tile before
 #pragma unroll 1
-        for (; cc.b < p.B && cc.first < w1; cc.next(pre, p.B, items_per_seq)) {
+        for (; cc.b < p.B && cc.first < w1; cc.next(pre, lens, p.window, p.B, items_per_seq)) {
             int32_t k = max(0, w0 - cc.first - kFp4Item);
             const int32_t end = min(cc.n, w1 - cc.first - kFp4Item);
             if (k >= end) continue;
             const bool whole = k == 0 && end == cc.n;
             load_q(cc.b, cc.it);
-            const int32_t hi = lens[cc.b], lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
+            const int32_t hi = lens[cc.b], lo = fp4_window_start(hi, p.window);
             // tiles with rows outside the item: its first (of a window) and its last
             const int32_t lo_edge = lo % kFp4Tile != 0 ? 0 : -1, hi_edge = hi % kFp4Tile != 0 ? cc.n - 1 : -1;
             int32_t first_k = k;               // where nm is to be set anew
