@@ -87,9 +87,9 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
 /*
  * paged_attention_decode_fp4 -- paged_attention_decode over the values the
  * codes stand for ([PG] s2.2), over the last `window` valid tokens when window
- * > 0 ([BUG] s5.3), on a persistent grid that gives every CTA an equal run of
- * 16-token tiles of all (sequence, kv head) items, so that ragged batches and
- * single long contexts alike keep the whole GPU busy; an item cut between
+ * > 0 ([BUG] s5.3), on a persistent grid that gives every CTA about equal runs
+ * of 32-token tiles of all (sequence, kv head) items, so that ragged batches
+ * and single long contexts alike keep the whole GPU busy; an item cut between
  * CTAs is finished by the last of them (the log-sum-exp merge of the
  * split-KV pair), in a fixed order, so results repeat from call to call.
  *
@@ -108,9 +108,11 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
  * calls that may overlap on the GPU (streams, captured graphs) need
  * workspaces of their own.  The size depends on the shape and on the current
  * device; a workspace may serve other shapes too, on the same device, if it is
- * large enough for them.  0 for a shape this entry point rejects (the schedule keeps two int32 per sequence in shared memory and
- * counts tiles in int32: PA_ERR_UNSUPPORTED).  (The workspace query has no
- * counterpart on the pages.)
+ * large enough for them.  0 for a shape this entry point rejects: the schedule
+ * keeps two int32 per sequence in shared memory and counts tokens and tiles in
+ * int32 (PA_ERR_UNSUPPORTED: too many sequences, 2^30 tiles of all items, or a
+ * table row of 2^31 - 1024 tokens).  scale * k_scale must be finite in fp32.
+ * (The workspace query has no counterpart on the pages.)
  */
 size_t paged_attention_fp4_workspace(const pa_shape *shape);
 

@@ -89,7 +89,8 @@ typedef struct pa_new_rows {
  * written (its queries are).
  *
  * Shapes: head_dim a power of two, 32..256 (16-bit) or 16..128 (fp32); others
- * give PA_ERR_UNSUPPORTED.  One launch on `stream`.
+ * give PA_ERR_UNSUPPORTED.  More than 65536 heads of a kind, or a padded batch
+ * of 2^31 tokens, give PA_ERR_INVALID_ARG.  One launch on `stream`.
  */
 pa_status paged_kv_append_rope(const pa_shape *shape, const pa_rope *rope, const pa_new_rows *rows,
                                void *q_out, void *k_pool, void *v_pool,

@@ -576,6 +576,8 @@ def _new_rows(what, x):
         stride = H * D
     if (sd != 1 and D != 1) or (sh != D and H != 1):
         raise ValueError(f"{what}: the heads of a token must lie one after another")
+    if stride < H * D:                         # expanded or overlapping tokens; 0 would mean rows without gaps
+        raise ValueError(f"{what}: every token must have rows of its own")
     return B, T, H, D, stride
 
 

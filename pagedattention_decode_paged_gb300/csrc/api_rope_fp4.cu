@@ -27,7 +27,7 @@ pa_status check_sizes(const pa_shape *s, int64_t row_bytes, int64_t stride_bytes
         return PA_ERR_INVALID_ARG;
     // positions and lengths are int32: the row must address fewer than 2^31 tokens
     if ((int64_t)s->max_blocks_per_seq * s->block_size > INT32_MAX) return PA_ERR_INVALID_ARG;
-    if (s->num_heads > (1 << 20)) return PA_ERR_INVALID_ARG;
+    if (s->num_heads > 65536 || s->num_kv_heads > 65536) return PA_ERR_INVALID_ARG;   // the grid's second axis holds them
     if (stride_bytes < (int64_t)s->num_kv_heads * s->block_size * row_bytes) return PA_ERR_INVALID_ARG;
     if (stride_bytes % 16 != 0) return PA_ERR_MISALIGNED;
     return PA_OK;
@@ -82,6 +82,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
     const int64_t ks = rows->k_stride != 0 ? rows->k_stride : kv_row;
     const int64_t vs = rows->v_stride != 0 ? rows->v_stride : kv_row;
     if ((q && qs < q_row) || ks < kv_row || vs < kv_row) return PA_ERR_INVALID_ARG;
+    if ((int64_t)s->batch * rows->max_tokens > INT32_MAX) return PA_ERR_INVALID_ARG;
     if (s->batch == 0 || rows->max_tokens == 0) return PA_OK;
     if (rows->k == nullptr || rows->v == nullptr || k_pool == nullptr || v_pool == nullptr ||
         block_table == nullptr || positions == nullptr || (q && q_out == nullptr) || (fp4 && kv_scales == nullptr))
@@ -133,6 +134,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
 // The decode schedule for `s` on the current device.
 pa_status plan_of(const pa_shape *s, pa::Fp4Plan *plan) {
     const int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
+    if (max_len > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;   // a batch of look-ups past the last token stays in int32
     const cudaError_t e = pa::plan_decode_fp4(s->dtype, s->head_dim, s->num_heads / s->num_kv_heads, s->batch,
                                               s->num_kv_heads, s->block_size, (max_len + 31) / 32 + 1, plan);
     if (e == cudaErrorInvalidValue) {
@@ -245,6 +247,8 @@ pa_status paged_attention_decode_fp4(const pa_shape *shape, void *out, const voi
     pa_status st = check_fp4_shape(shape, true);
     if (st != PA_OK) return st;
     if (window < 0 || !isfinite(scale) || !factor_ok(k_scale) || !factor_ok(v_scale)) return PA_ERR_INVALID_ARG;
+    const float scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
+    if (!isfinite(scale_log2)) return PA_ERR_INVALID_ARG;
     if (shape->batch == 0) return PA_OK;
     if (out == nullptr || q == nullptr || k_pool == nullptr || v_pool == nullptr || kv_scales == nullptr ||
         block_table == nullptr || seq_lens == nullptr || workspace == nullptr)
@@ -276,7 +280,7 @@ pa_status paged_attention_decode_fp4(const pa_shape *shape, void *out, const voi
     p.bs = shape->block_size;
     p.bs_shift = log2_or_none(shape->block_size);
     p.window = window;
-    p.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
+    p.scale_log2 = scale_log2;
     char *ws = static_cast<char *>(workspace);
     p.records = reinterpret_cast<float *>(ws);
     p.group_counters = reinterpret_cast<int32_t *>(ws + w.group_counters);

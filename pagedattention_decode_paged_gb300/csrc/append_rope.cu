@@ -228,7 +228,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
     constexpr int QB = kRopeBatch<T>, KB = QB / 2;
     const int64_t token = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     if (token >= (int64_t)p.B * p.T) return;
-    const int b = p.T == 1 ? (int)token : token <= INT32_MAX ? (int)((uint32_t)token / (uint32_t)p.T) : (int)(token / p.T);
+    const int b = p.T == 1 ? (int)token : (int)((uint32_t)token / (uint32_t)p.T);
     const int t = (int)(token - (int64_t)b * p.T);
     const int n = p.counts != nullptr ? __ldg(p.counts + b) : p.T;
     const int32_t start = __ldg(p.positions + b);
@@ -468,7 +468,6 @@ static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
     const int kv_runs = (nk + kv_run - 1) / kv_run, runs = (nq + q_run - 1) / q_run + kv_runs;
     if (runs > 65535) return cudaErrorInvalidValue;
     const int64_t gx = (tokens + kRopeWarps - 1) / kRopeWarps;
-    if (gx > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)gx, (unsigned)runs, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);

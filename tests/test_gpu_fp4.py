@@ -257,6 +257,71 @@ def test_decode_on_a_side_stream_and_in_graphs():
         held_to(out, c.reference(lens=new))
 
 
+def test_decode_scores_far_below_any_reference():
+    """Every score the same, about -1e34: all tokens of a tile weigh the same (a
+    rounding of such a score would outweigh any other), the output is the
+    values' mean."""
+    c = Cache(lens=[32, 7], H=2, Hkv=2, dtype=F32, seed=14)
+    c.pool[:, 0], c.scales[:, 0] = 0x22, torch.where(c.scales[:, 0] == 0x7F, c.scales[:, 0], torch.full_like(c.scales[:, 0], 0x38))
+    c.q = torch.full_like(c.q, -1e33)          # keys of ones: 128 products of -1e33
+    c.to_gpu()
+    out = c.decode()
+    for b, n in enumerate((32, 7)):
+        v = ref.cached_rows(c.pool, c.scales, c.table[b], c.bs, 0, n, (1.0, 1.0))[1]
+        mean, size = v.mean(1), v.abs().mean(1)
+        # equal weights of 1: n/16 + 32 fp32 sums at most, the quotient, the last rounding
+        off = (out[b].double().cpu() - mean).abs()
+        assert (off <= size * (n / 16 + 36) * 2.0 ** -23).all()
+
+
+def test_decode_of_empty_sequences_only():
+    c = Cache(lens=[0, 0, 0], H=8, Hkv=2).to_gpu()
+    assert not c.decode().any()
+
+
+def test_decode_one_workspace_serves_smaller_shapes_too():
+    big = Cache(lens=[3000] * 9, H=32, Hkv=8, seed=15).to_gpu()
+    held_to(big.decode(), big.reference())
+    for kw in (dict(lens=[5000], H=8, Hkv=1), dict(lens=[40000], H=4, Hkv=2, dtype=F32, D=64), dict(lens=[9, 700], D=256, dtype=F16)):
+        c = Cache(seed=16, **kw).to_gpu()
+        held_to(c.decode(ws=big.ws), c.reference())
+    held_to(big.decode(), big.reference())
+    assert not big.counters().any()
+
+
+def test_decode_pools_in_any_order_and_apart():
+    """Values before keys in a block; keys and values in allocations of their own."""
+    c = Cache(lens=[100, 33], H=4, Hkv=2, seed=17).to_gpu()
+    want, pool = c.decode(), c.g["pool"]
+    call = lambda out, k, v, stride: pa.paged_attention_decode_fp4(
+        out, c.g["q"], k, v, c.g["scales"], c.g["table"], c.g["lens"], c.scale, c.ws, num_kv_heads=c.Hkv,
+        block_size=c.bs, num_blocks=c.NB, block_stride=stride)
+    flipped, out = pool.flip(1).contiguous().view(-1), torch.empty_like(want)
+    call(out, flipped[pool.stride(1):], flipped, pool.stride(0))
+    assert torch.equal(out, want)
+    k, v = pool[:, 0].contiguous(), pool[:, 1].contiguous()
+    call(out.zero_(), k.view(-1), v.view(-1), k.stride(0))
+    assert torch.equal(out, want)
+
+
+def test_two_decodes_at_once_on_two_streams():
+    """Each with its own workspace, many times over."""
+    cs = [Cache(lens=[20000, 33], H=8, Hkv=2, seed=18).to_gpu(), Cache(lens=[700] * 12, H=8, Hkv=8, seed=19).to_gpu()]
+    want = [c.decode() for c in cs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for c, stream in zip(cs, streams):
+        with torch.cuda.stream(stream):
+            outs.append(c.decode(prepare=True))
+    for _ in range(20):
+        for out, call in outs:
+            call()
+    torch.cuda.synchronize()
+    for (out, _), w in zip(outs, want):
+        assert torch.equal(out, w)
+
+
 # --- reading rows back -------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])

@@ -288,6 +288,19 @@ def test_offsets_past_32_bits():
     for got, x in ((ko, k), (vo, v)):
         want = ref.dequantise(*ref.quantise(x.cpu().float(), 1.0), 1.0)
         assert torch.equal(got.cpu().double(), want)       # at most 6 significant bits: bf16 holds them
+    # and attended to, against the same rows in a small pool
+    q = torch.randn(2, 2 * Hkv, D, dtype=BF16, device="cuda")
+    lens = torch.tensor([32, 19], dtype=torch.int32, device="cuda")
+    ids = table.flatten().long()
+    near, near_scales = pool[ids].contiguous(), scales[ids].contiguous()
+    outs = []
+    for p, sc, tb in ((pool, scales, table), (near, near_scales, torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2))):
+        kw = dict(num_kv_heads=Hkv, block_size=bs, num_blocks=p.shape[0], block_stride=p.stride(0))
+        outs.append(torch.empty_like(q))
+        pa.paged_attention_decode_fp4(outs[-1], q, p.view(-1), p.view(-1)[p.stride(1):], sc, tb, lens, D ** -0.5,
+                                      pa.fp4_workspace_for(q, tb, **kw), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs) and torch.isfinite(outs[0]).all()
 
 
 @pytest.mark.parametrize("fp4", [False, True])
@@ -324,3 +337,71 @@ def test_matches_the_plain_append_without_norm_and_rotation():
                               s.counts.cuda(), block_size=s.bs, num_blocks=s.NB, block_stride=stride[0])
     torch.cuda.synchronize()
     assert torch.equal(pool, other)
+
+
+@pytest.mark.parametrize("g", [1.0, 0.37, 5.3e-7, 1.9e11, 2.0 ** -64, 2.0 ** 64])
+def test_quotients_beside_every_border(g):
+    """Keys a few steps of binary32 from t * (border between two codes), group
+    maxima of values as close to 6 g * (border between two scales): codes and
+    scales are those of IEEE division, byte for byte."""
+    rng = torch.Generator().manual_seed(21)
+    T, Hkv, D, bs = 2048, 4, 64, 16
+
+    def steps(x):
+        """x moved by -3..3 steps of binary32."""
+        return (x.view(torch.int32) + torch.randint(-3, 4, x.shape, generator=rng, dtype=torch.int32)).view(torch.float32)
+
+    shape = (1, T, Hkv, D // 16)
+    val = ref.E4M3[torch.randint(1, 127, shape, generator=rng)].float()
+    t = (val * torch.tensor(g, dtype=torch.float32))[..., None]
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])[torch.randint(0, 7, (*shape, 16), generator=rng)]
+    k = steps(border * t)
+    k[..., 0] = (6 * torch.tensor(g, dtype=torch.float32) * val)
+    k = (k * (torch.randint(0, 2, k.shape, generator=rng) * 2 - 1)).flatten(-2)
+    mids = ((ref.E4M3[1:127] + ref.E4M3[0:126]) / 2).float()[torch.randint(0, 126, shape, generator=rng)]
+    v = torch.randn((*shape, 16), generator=rng).clamp(-1, 1) * 0.5 * mids[..., None] * g
+    v[..., 5] = steps(6 * torch.tensor(g, dtype=torch.float32) * mids)
+    v = v.flatten(-2)
+    NB = T // bs
+    pool = torch.zeros((NB, 2, Hkv, bs, D // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((NB, 2, Hkv, bs, D // 16), dtype=torch.uint8, device="cuda")
+    table = torch.arange(NB, dtype=torch.int32, device="cuda").view(1, NB)
+    flat = pool.view(-1)
+    pa.paged_kv_append_fp4(k.cuda(), v.cuda(), flat, flat[pool.stride(1):], scales, table,
+                           torch.zeros(1, dtype=torch.int32, device="cuda"), k_scale=g, v_scale=g, block_size=bs,
+                           num_blocks=NB, block_stride=pool.stride(0))
+    torch.cuda.synchronize()
+    for half, x in ((0, k), (1, v)):
+        codes, sc = ref.quantise(x[0], g)
+        rows = lambda y: y[:, half].transpose(1, 2).reshape(T, Hkv, -1).cpu()
+        assert torch.equal(rows(scales), sc)
+        assert torch.equal(rows(pool), codes)
+
+
+def test_positions_of_empty_sequences_are_checked():
+    """As in paged_kv_append_tokens, a position is checked whatever the count."""
+    for fp4 in (False, True):
+        s = Step(B=2, T=3, counts=[0, 2], fp4=fp4, seed=13)
+        s.pos[0] = -1
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = s.gpu(err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == pa.DEVERR_BAD_POS
+        s.check(*out)
+
+
+def test_two_appends_at_once_on_two_streams():
+    """Different sequences of one cache, on two streams, many times over."""
+    a, b = Step(B=2, T=40, fp4=True, seed=14), Step(B=2, T=40, fp4=True, seed=15)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for s, stream in zip((a, b), streams):
+        with torch.cuda.stream(stream):
+            outs.append(s.gpu(prepare=True))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for out, stream in zip(outs, streams):
+            out[3]()
+    torch.cuda.synchronize()
+    for s, out in zip((a, b), outs):
+        s.check(*out[:3])

@@ -133,6 +133,9 @@ def test_append_refuses_bad_arguments(lib, fp4):
                  dict(max_blocks_per_seq=1 << 28)):
         assert call(lib, make(**over), rope(), rows()) == INVALID, over
     assert call(lib, make(block_stride=2 * 2 * 16 * 128 + 4), rope(), rows()) == MISALIGNED
+    for over in (dict(num_heads=65537), dict(num_kv_heads=65537, block_stride=1 << 40)):
+        assert call(lib, make(**over), rope(), rows(q_stride=1 << 30, k_stride=1 << 30, v_stride=1 << 30)) == INVALID, over
+    assert call(lib, make(batch=1 << 16), rope(), rows(max_tokens=1 << 15)) == INVALID
     # nothing to do: refused or accepted before any pointer is looked at
     assert call(lib, make(batch=0), rope(), rows()) == OK
     assert call(lib, s, rope(), rows(max_tokens=0, k=None), kp=None) == OK
@@ -144,7 +147,7 @@ def test_append_refuses_bad_arguments(lib, fp4):
 
 
 def test_fp4_refuses_bad_factors_and_scales(lib):
-    for g in (0.0, -1.0, float("inf"), float("nan")):
+    for g in (0.0, -1.0, float("inf"), float("nan"), 2.0 ** -65, 2.0 ** 65):
         assert call_rope4(lib, shape4(), rope(), rows(), kg=g) == INVALID
         assert call_rope4(lib, shape4(), rope(), rows(), vg=g) == INVALID
     assert call_rope4(lib, shape4(), rope(), rows(), sc=None) == INVALID
@@ -192,6 +195,8 @@ def test_decode_refuses_bad_arguments(lib):
     # more tiles than the schedule's int32 indices hold
     assert call(s=shape4(batch=1 << 14, num_heads=64, num_kv_heads=64, max_blocks_per_seq=1 << 16,
                          block_stride=1 << 20)) == UNSUPPORTED
+    assert call(s=shape4(block_size=1, max_blocks_per_seq=(1 << 31) - 1000, block_stride=1 << 20)) == UNSUPPORTED
+    assert call(scale=3e38, kg=2.0) == INVALID
     assert pa.paged_attention_fp4_workspace(shape4(batch=0)) == 0
     assert pa.paged_attention_fp4_workspace(shape4(head_dim=32)) == 0
 
@@ -251,6 +256,11 @@ def test_new_rows_accepts_slices_of_a_packed_projection():
     assert pa._new_rows("k", packed[:, 1:2, 8:9]) == (3, 1, 1, 64, 5 * 12 * 64)
     with pytest.raises(ValueError):                     # sequences further apart than their tokens
         pa._new_rows("k", packed[:, :4, 8:10])
+    one = torch.zeros(1, 1, 2, 64)
+    assert pa._new_rows("k", one.expand(1, 1, 2, 64)) == (1, 1, 2, 64, 128)
+    for x in (one.expand(3, 1, 2, 64), one.expand(1, 5, 2, 64), one[0].expand(3, 2, 64)):
+        with pytest.raises(ValueError):                 # tokens that share their rows
+            pa._new_rows("k", x)
 
 
 # --- the restatements themselves -------------------------------------------------
