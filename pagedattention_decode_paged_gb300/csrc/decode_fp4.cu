@@ -3,9 +3,10 @@
 //
 // The per-block attention decomposition is that of "KV Cache paging in LLM
 // inference" (intelliparadigm.com) s2.2.  An item is a (sequence, kv head,
-// group of query heads); its 16-token tiles are read once for all its heads.
+// group of query heads); its 32-token tiles are read once for all its heads.
 //
-// Arithmetic of a tile (one warp, mma.sync m16n8k16, fp32 accumulation):
+// Arithmetic of a tile (one warp, two halves of 16 tokens, mma.sync m16n8k16,
+// fp32 accumulation):
 //   S^T[16 tokens x 8 columns] = K Q^T, then the online softmax down each
 //   column, then O^T[D x 8 columns] += V^T P^T, a column being a query head
 //   (16-bit queries) or the high or low fp16 part of one (fp32 queries: the
@@ -23,8 +24,20 @@
 //   more than 2^8 (weights stay inside fp16), so a tile usually costs one
 //   vote and no shuffles.
 //
-// Work split: the tiles of all items, end to end, are cut into one equal run
-// per CTA and one equal part of that per warp (balanced.cuh's index space).  A
+// What bounds it: 4.5 bits per value are so few that a tile's conversions (570
+// instructions for 4.6 KB at head_dim 128, half of them on the pipe of the
+// integer and conversion instructions) take nearly as long as its bytes.  64
+// sequences of 7000 to 8192 tokens, 64 heads on 8, bf16: 102 us where the bytes
+// take 83 us at the copy rate, the tile loop itself 88 us; with 16-token tiles the
+// loop took 121 us.  What is left is what a launch costs beside its tiles: lengths,
+// table entries and first tiles one after another (6 us until the first tile is
+// multiplied), the merge of a CTA's warps (2 us) and, if items are cut between
+// CTAs, of the CTAs (3 to 6 us).  32 x 2048 tokens: 23.2 us (bytes 11.3); 256
+// sequences of 4 to 4096 tokens, 32 heads each, f16: 48 us (24.8); one of 131071:
+// 36.8 us (22.3).
+//
+// Work split: the tiles of all items, end to end, are cut into about equal runs,
+// one per CTA, and each into equal parts, one per warp (Fp4Cursor, Fp4Runs).  A
 // warp that covers an item writes its output; partial states of the warps of
 // a CTA meet in shared memory, those of CTAs in the workspace, where the last
 // to arrive merges (in two levels when many share an item), always in the
@@ -40,11 +53,23 @@ namespace pa {
 constexpr int kFp4Tile = 32;       // tokens of a tile: two halves of 16, the MMAs' token axis
 constexpr int kFp4Halves = kFp4Tile / 16;
 constexpr float kFp4Empty = -3.402823466e38f;   // reference of a column without scores: below any, and finite
-constexpr int kFp4Item = 1;        // what an item costs beside its tiles (queries, output), in tiles
-constexpr int kFp4MinTiles = 1;    // tiles per warp below which fewer CTAs share the work
-constexpr int kFp4Snap = 4;        // tiles per warp that a CTA may have above the mean to end where items end
-constexpr int kFp4Flat = 24;       // sharers of an item up to which one level of merging serves
-constexpr int kFp4Group = 12;      // sharers per first-level group above that
+// The rules of the split, each with what the other side of it took:
+// - what an item costs beside its tiles (queries, output), in tiles.  256 ragged
+//   sequences of 32 heads: 65.7 us at 0, 48.1 at 1, 52.5 at 2; others within 1 us.
+constexpr int kFp4Item = 1;
+// - tiles per warp below which fewer CTAs share the work.  4 sequences of up to 128
+//   tokens: 7.1 us at 1, 8.0 at 2, 9.8 at 4; 4 of 2048: 13.1, 14.4, 14.4 us.
+constexpr int kFp4MinTiles = 1;
+// - tiles per warp that a CTA may have above the mean to end where items end.  32 x
+//   2048 tokens: 25.7 us at 0 (items are cut), 23.3 at 2 to 8; the ragged batch:
+//   51.3 at 0 to 3, 48.1 at 4 to 8.
+constexpr int kFp4Snap = 4;
+// - sharers of an item up to which one level of merging serves (at most 32).  19 CTAs
+//   to an item: 38.7 us in two levels, 36.8 in one.
+constexpr int kFp4Flat = 24;
+// - sharers per first-level group above that.  152 CTAs to an item: 18.6 us with 6,
+//   18.0 with 12, 18.5 with 18.
+constexpr int kFp4Group = 12;
 
 template <typename T, int D, int NT>
 struct Fp4Cfg {
@@ -56,10 +81,11 @@ struct Fp4Cfg {
     static constexpr int kScales = 16 * kScRow;
     static constexpr int kHalf = 2 * (kCodes + kScales);    // K codes, V codes, K scales, V scales
     static constexpr int kStage = kFp4Halves * kHalf;
-    static constexpr int kStages = 2;
+    static constexpr int kStages = 2;                       // a third changes nothing, and takes room from the schedule
     static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
-    // one CTA per SM: of 12 warps where a thread gets along with 168 registers
+    // one CTA per SM: of 12 warps where a thread gets along with 168 registers (8
+    // warps: 58.7 us where 12 take 48.1 on the ragged batch, 25.5 and 23.3 on 32 x 2048)
     static constexpr int kWarps = NT * D <= 128 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
     // the last record of a warp takes the place of its ring
@@ -225,9 +251,10 @@ __device__ __forceinline__ uint32_t lds_bytes(uint32_t addr) {
     return v;
 }
 
-// WHOLE: block_size is a multiple of the tile, so the 16 rows of a tile are
+// WHOLE: block_size is a multiple of 16, so the 16 rows of half a tile are
 // contiguous and one table entry serves them; else every row is looked up by
-// itself.  Either way a tile is a 16-byte asynchronous copy per lane and chunk.
+// itself (32 x 2048 in blocks of 16: 27.3 us so, 23.3 whole).  Either way a tile is
+// a 16-byte asynchronous copy per lane and chunk.
 template <typename T, int D, int NT, bool WHOLE>
 __global__ void __launch_bounds__((Fp4Cfg<T, D, NT>::kThreads), 1)
 decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) {
@@ -268,7 +295,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     // An equal run of places to every CTA (fewer CTAs when their warps would have
     // less than kFp4MinTiles).  The runs' ends are moved to the nearest ends of
     // items, and nothing has to be merged between CTAs, if that leaves no CTA
-    // with much more than the mean: the merge costs a CTA 4 to 5 us.
+    // with much more than the mean.
     const int nC = min((int)gridDim.x, (Tn + W * kFp4MinTiles - 1) / (W * kFp4MinTiles));
     const int cta = blockIdx.x;
     if (cta >= nC) return;
@@ -752,7 +779,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     // the workspace, where other CTAs wrote them: volatile loads read L2.  One copy
     // of this code serves every merge: what a CTA runs once is paid for in
     // instruction fetches.
-    constexpr int kBatch = 8;                  // records loaded at a time
+    constexpr int kBatch = 8;                  // records loaded at a time (12: 48.8 us for 48.1; 4: 37.6 for 37.0)
     const int elements = (grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS) * 32;   // one head: the slabs of j = 0
     auto merge = [&](const float *const *of, int from, int to, int b, int it, float *dst, int i) {
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
@@ -952,8 +979,9 @@ static cudaError_t dispatch_fp4(int dtype, int head_dim, int nt, bool whole, F &
 
 cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int kv_heads, int block_size,
                             int64_t max_tiles_per_item, Fp4Plan *plan) {
-    // one 8-column tile per item, or two when the kv head has more columns:
-    // the conversion of a tile, not its MMAs, is what an item costs
+    // one 8-column tile per item, or two when the kv head has more columns: the
+    // conversion of a tile, not its MMAs, is what an item costs (32 x 2048 tokens,
+    // 16 heads to each of 4: 19.8 us with two, 22.7 in two items of one)
     const int columns = group * (dtype == PA_F32 ? 2 : 1);
     plan->nt = head_dim <= 128 && columns > 8 ? 2 : 1;
     const int heads = plan->nt * 8 / (dtype == PA_F32 ? 2 : 1);
