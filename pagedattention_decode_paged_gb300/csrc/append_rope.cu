@@ -8,8 +8,11 @@
 // include/pagedattn_fp4.h state them).
 //
 // Every element is read once and written once, so the kernel is bound by HBM
-// for prompts and by launch and the dependent loads (position, table entry and
-// cosines) for single tokens.  D/8 lanes hold a row, 8 elements each in two
+// for prompts (8 of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 554 MB in 88 us,
+// 6.3 TB/s, 93% of the copy rate) and by launch and the dependent loads (position,
+// table entry and cosines) for single tokens (1: 1.9 us; 256 of 32 + 32 heads: 2.8
+// us).  Into the 4-bit cache keys and values take three times their bytes' time: the
+// arithmetic of the codes (f16 prompts, 32 + 8 heads: 27.9 us, 13 of them theirs).  D/8 lanes hold a row, 8 elements each in two
 // chunks of 4.  With pairs (i, i + R/2) a lane takes chunk i and chunk i + R/2
 // (kSplit): each chunk of a row is still read in whole 128-byte lines, both
 // elements of a pair are in one lane, and its 4 cosines and sines serve both
@@ -37,7 +40,10 @@
 
 namespace pa {
 
-constexpr int kRopeWarps = 4;
+// Warps per CTA: small ones, whose slots are free again as soon as both are done
+// (8 prompts of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 125.7 us at 8, 93.0 at
+// 4, 88.0 at 2, 89.3 at 1).
+constexpr int kRopeWarps = 2;
 constexpr int kRopeThreads = kRopeWarps * 32;
 enum RopeMode { kSplit, kNeighbours, kShuffle };
 
@@ -211,15 +217,22 @@ __device__ __forceinline__ void store_fp4(const float2 (&x)[2], const float2 (&y
 
 // grid: x = kRopeWarps tokens of the padded batch each, y = run: of kv_run
 // iterations of keys and values, then of q_run iterations of queries (at most
-// KB and QB), so that the warps of a CTA do the same.
+// KB and QB), so that the warps of a CTA do the same (runs of a token side by
+// side instead: equal).
 // Iterations of queries a run has at most, as many as keep their registers; half
-// as many of keys, with their values (f16 prompts into the 4-bit cache: 1 of
-// each 41 us, 2 31.9 us, 4 28.8 us, where the first had no CTAs of their own).
+// as many of keys, with their values (f16 prompts into the 4-bit cache, 4 warps to a
+// CTA: 1 of each 41 us, 2 31.9 us, 4 28.8 us, where the first had no CTAs of their own;
+// bf16 prompts: 99.8 us with 4 of queries, 93.0 with 8).
 template <typename T>
 constexpr int kRopeBatch = sizeof(T) == 2 ? 8 : 4;
+// CTAs per SM that registers have to do for: up to where values are spilled (the
+// prompts above: 91.4 us at 12, 88.0 at 14, 95.7 at 15; f16 prompts into the 4-bit
+// cache: 28.4 us at 10, 27.9 at 11, 28.6 at 13).
+template <typename T, bool FP4>
+constexpr int kRopeCtas = sizeof(T) == 4 ? 10 : FP4 ? 11 : 14;
 
 template <typename T, int D, bool FP4, RopeMode MODE>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 5)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas<T, FP4>)
 rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, const int kv_run, const int kv_runs) {
     grid_dependency_wait();
     allow_dependents();
@@ -460,11 +473,19 @@ static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     // Rows per run: as many as are loaded at once, which amortises what a token
-    // costs; fewer for few tokens, until every SM has 16 warps at most.
-    const int64_t tokens = (int64_t)p.B * p.T, warps = (int64_t)sms * 16;
+    // costs; fewer for few tokens, the longer of the two runs first (a quantised
+    // row takes about as long as four others), until every SM has 12 warps at most
+    // (1 token: 3.2 us with full runs, 1.9 so; 64 tokens into the 4-bit cache: 5.0 and
+    // 2.9, 3.3 where SMs may have 16 or 24; 256 tokens: 2.8, 3.2 at 24).
+    const int64_t tokens = (int64_t)p.B * p.T, most = (int64_t)sms * 12;
     int q_run = QB, kv_run = KB;
-    while (q_run > 1 && tokens * ((nq + q_run / 2 - 1) / (q_run / 2) + (nk + kv_run - 1) / kv_run) <= warps) q_run /= 2;
-    while (kv_run > 1 && tokens * ((nq + q_run - 1) / q_run + (nk + kv_run / 2 - 1) / (kv_run / 2)) <= warps) kv_run /= 2;
+    auto fits = [&](int q, int kv) { return q >= 1 && kv >= 1 && tokens * ((nq + q - 1) / q + (nk + kv - 1) / kv) <= most; };
+    for (;;) {
+        const bool kv_first = kv_run * (FP4 ? 4 : 2) >= q_run, kv = fits(q_run, kv_run / 2), q = fits(q_run / 2, kv_run);
+        if (kv && (kv_first || !q)) kv_run /= 2;
+        else if (q) q_run /= 2;
+        else break;
+    }
     const int kv_runs = (nk + kv_run - 1) / kv_run, runs = (nq + q_run - 1) / q_run + kv_runs;
     if (runs > 65535) return cudaErrorInvalidValue;
     const int64_t gx = (tokens + kRopeWarps - 1) / kRopeWarps;
