@@ -68,7 +68,8 @@ KERNEL_SOURCES = {"decode_simt": "decode_simt.cu", "decode_gqa_tc": "decode_gqa_
                   "decode_prefix_tc": "decode_prefix_tc.cu",
                   "decode_prefix_int8_tc": "decode_int8_tc.cu",
                   "decode_prefix_fp8_tc": "decode_int8_tc.cu",
-                  "append_tokens": "append.cu"}
+                  "append_tokens": "append.cu",
+                  "rope_append": "append_rope.cu", "decode_fp4": "decode_fp4.cu", "gather_fp4": "gather_fp4.cu"}
 
 
 # ---------------------------------------------------------------------------

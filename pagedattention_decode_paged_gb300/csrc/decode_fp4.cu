@@ -28,13 +28,12 @@
 // instructions for 4.6 KB at head_dim 128, half of them on the pipe of the
 // integer and conversion instructions) take nearly as long as its bytes.  64
 // sequences of 7000 to 8192 tokens, 64 heads on 8, bf16: 102 us where the bytes
-// take 83 us at the copy rate, the tile loop itself 88 us; with 16-token tiles the
-// loop took 121 us.  What is left is what a launch costs beside its tiles: lengths,
+// take 83 us at the copy rate, the tile loop itself 88 us; with 16-token tiles 121 us.  What is left is what a launch costs beside its tiles: lengths,
 // table entries and first tiles one after another (6 us until the first tile is
 // multiplied), the merge of a CTA's warps (2 us) and, if items are cut between
-// CTAs, of the CTAs (3 to 6 us).  32 x 2048 tokens: 23.2 us (bytes 11.3); 256
-// sequences of 4 to 4096 tokens, 32 heads each, f16: 48 us (24.8); one of 131071:
-// 36.8 us (22.3).
+// CTAs, of the CTAs (3 to 5 us).  32 x 2048 tokens: 23.2 us (bytes 11.3); 256
+// sequences of 4 to 4096 tokens, 32 heads each, f16: 47.5 us (24.8); one of 131071:
+// 36.0 us (22.3).
 //
 // Work split: the tiles of all items, end to end, are cut into about equal runs,
 // one per CTA, and each into equal parts, one per warp (Fp4Cursor, Fp4Runs).  A
@@ -55,21 +54,22 @@ constexpr int kFp4Halves = kFp4Tile / 16;
 constexpr float kFp4Empty = -3.402823466e38f;   // reference of a column without scores: below any, and finite
 // The rules of the split, each with what the other side of it took:
 // - what an item costs beside its tiles (queries, output), in tiles.  256 ragged
-//   sequences of 32 heads: 65.7 us at 0, 48.1 at 1, 52.5 at 2; others within 1 us.
+//   sequences of 32 heads: 65.3 us at 0, 47.6 at 1, 52.4 at 2; others within 1 us.
 constexpr int kFp4Item = 1;
 // - tiles per warp below which fewer CTAs share the work.  4 sequences of up to 128
-//   tokens: 7.1 us at 1, 8.0 at 2, 9.8 at 4; 4 of 2048: 13.1, 14.4, 14.4 us.
+//   tokens: 7.0 us at 1, 7.7 at 2, 9.5 at 4; 4 of 2048: 13.2, 14.1, 14.2 us.
 constexpr int kFp4MinTiles = 1;
 // - tiles per warp that a CTA may have above the mean to end where items end.  32 x
-//   2048 tokens: 25.7 us at 0 (items are cut), 23.3 at 2 to 8; the ragged batch:
-//   51.3 at 0 to 3, 48.1 at 4 to 8.
+//   2048 tokens: 25.1 us at 0 (items are cut), 23.1 at 2 to 8; the ragged batch:
+//   50.4 at 0 to 3, 47.5 at 4 to 8.
 constexpr int kFp4Snap = 4;
 // - sharers of an item up to which one level of merging serves (at most 32).  19 CTAs
-//   to an item: 38.7 us in two levels, 36.8 in one.
+//   to an item: 37.6 us in two levels, 35.9 in one.
 constexpr int kFp4Flat = 24;
-// - sharers per first-level group above that.  152 CTAs to an item: 18.6 us with 6,
-//   18.0 with 12, 18.5 with 18.
+// - sharers per first-level group above that.  152 CTAs to an item: 17.3 us with 10,
+//   12 or 16.
 constexpr int kFp4Group = 12;
+constexpr int kFp4Groups = 16;     // such groups: the largest grid has kFp4Groups * kFp4Group CTAs
 
 template <typename T, int D, int NT>
 struct Fp4Cfg {
@@ -85,13 +85,17 @@ struct Fp4Cfg {
     static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
     // one CTA per SM: of 12 warps where a thread gets along with 168 registers (8
-    // warps: 58.7 us where 12 take 48.1 on the ragged batch, 25.5 and 23.3 on 32 x 2048)
+    // warps: 58.9 us where 12 take 47.6 on the ragged batch, 25.0 and 23.3 on 32 x 2048)
     static constexpr int kWarps = NT * D <= 128 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
     // the last record of a warp takes the place of its ring
     static constexpr int kRingBytes = kWarpRing > kRec * 4 ? kWarpRing : kRec * 4;
     static_assert(kRec <= kFp4RecFloats, "a record fits the workspace");
     static constexpr size_t kFixed = (size_t)kWarps * (kRingBytes + kRec * 4);
+    static constexpr int kMost = kFixed / (kRec * 4) < 32 ? (int)(kFixed / (kRec * 4)) : 32;   // records merged at once
+    static constexpr int kFlat = kFp4Flat < kMost ? kFp4Flat : kMost;
+    static_assert(kMost >= kFp4Group && kMost >= kFp4Groups, "the records of either level fit");
+    static_assert(kRec % 4 == 0 && kFp4RecFloats % 4 == 0, "records are whole 16-byte pieces");
     static size_t bytes(int batch) { return kFixed + ((size_t)2 * batch + 1) * 4; }
 };
 
@@ -212,15 +216,14 @@ __device__ __forceinline__ void fp4_schedule(const DecodeParams &p, int items_pe
     __syncthreads();
 }
 
-// Loads of either shared memory or of what other CTAs wrote (read at L2).
-__device__ __forceinline__ float ld_volatile(const float *p) {
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
     float v;
-    asm volatile("ld.volatile.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float4 ld_volatile4(const float *p) {
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.volatile.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
@@ -268,10 +271,11 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __shared__ int32_t scan_tmp[W];
     __shared__ int32_t rec_first[2 * W], rec_n[2 * W], rec_b[2 * W], rec_it[2 * W];
     __shared__ int32_t arrived[2], sharers_of[2];
-    __shared__ const float *list[2][32];       // records to merge
+    __shared__ uint32_t rec_at[32];            // records to merge, in shared memory
+    __shared__ const float *source[2][32];     // those of other CTAs, in the workspace
     __shared__ float *merged_to[2];            // null: the output
-    __shared__ int32_t snap[32 * kFp4Group + 1];
-    __shared__ int32_t group_rec[2 * W + 1];   // of the items merged in this CTA: first record, and its place in list[0]
+    __shared__ int32_t snap[kFp4Groups * kFp4Group + 1];
+    __shared__ int32_t group_rec[2 * W + 1];   // of the items merged in this CTA: first record, and its place in rec_at
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     unsigned char *ring_p = smem + (size_t)warp * C::kRingBytes;
@@ -774,14 +778,14 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     __syncthreads();
 
     // ---- merges --------------------------------------------------------------
-    // Element i (a lane's slab) of the records of[from, to) of one item, merged into
-    // its output, or into the record dst.  The records lie in shared memory or in
-    // the workspace, where other CTAs wrote them: volatile loads read L2.  One copy
-    // of this code serves every merge: what a CTA runs once is paid for in
-    // instruction fetches.
-    constexpr int kBatch = 8;                  // records loaded at a time (12: 48.8 us for 48.1; 4: 37.6 for 37.0)
+    // Element i (a lane's slab) of the records rec_at[from, to) of one item, merged
+    // into its output, or into the record dst.  One copy of this code serves every
+    // merge, and a short one: what a CTA runs once is paid for in instruction fetches
+    // (8 records at a time: 47.8 us for 47.4 on the ragged batch, 36.1 for 35.9 on 1 x
+    // 131071).
+    constexpr int kBatch = 4;                  // records loaded at a time
     const int elements = (grp == 1 && NT == 1 && P == 1 ? SLABS / 2 : SLABS) * 32;   // one head: the slabs of j = 0
-    auto merge = [&](const float *const *of, int from, int to, int b, int it, float *dst, int i) {
+    auto merge = [&](int from, int to, int b, int it, float *dst, int i) {
         const int hk = it / units_per_kv, h0 = (it - hk * units_per_kv) * HP;
         const int ln = i & 31, h = head_of(i >> 5, ln), d = dim_of(i >> 5, ln);
         float M = kFp4Empty, sum = 0.f;
@@ -789,16 +793,16 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int r = from; r < to; r += kBatch) {
-            const float *rec[kBatch];
+            uint32_t rec[kBatch];
             float mr[kBatch], lr[kBatch];
             float4 a[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) rec[k] = of[min(r + k, to - 1)];
+            for (int k = 0; k < kBatch; ++k) rec[k] = rec_at[min(r + k, to - 1)];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                mr[k] = ld_volatile(rec[k] + HP * D + h);
-                lr[k] = ld_volatile(rec[k] + HP * D + HP + h);
-                a[k] = ld_volatile4(rec[k] + i * 4);
+                mr[k] = lds_f32(rec[k] + (HP * D + h) * 4);
+                lr[k] = lds_f32(rec[k] + (HP * D + HP + h) * 4);
+                a[k] = lds_f32x4(rec[k] + i * 16);
             }
             float top = M;
 #pragma unroll
@@ -853,9 +857,8 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     const int shared_last = last_tile >= c0 && last_tile + rec_n[last_group] > c1 ? last_group : -1;
     if (warp == 0) {
         if (mine >= 0)
-            list[0][__popc(before)] = (lane & 1) ? reinterpret_cast<const float *>(smem + (size_t)(lane >> 1) * C::kRingBytes)
-                                                 : reinterpret_cast<const float *>(smem + (size_t)W * C::kRingBytes) +
-                                                       (size_t)(lane >> 1) * C::kRec;
+            rec_at[__popc(before)] = smem_u32(smem) + ((lane & 1) ? (lane >> 1) * C::kRingBytes
+                                                                  : W * C::kRingBytes + (lane >> 1) * C::kRec * 4);
         if (starts_item) group_rec[__popc(starts & ((1u << lane) - 1u))] = lane | __popc(before) << 8;
         if (lane == 0) group_rec[groups] = __popc(valid) << 8;
     }
@@ -864,7 +867,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
     for (int i = threadIdx.x; i < groups * elements; i += C::kThreads) {
         const int g = i / elements, r0 = group_rec[g] & 255;
         float *dst = r0 == shared_first ? global_rec(cta, 0) : r0 == shared_last ? global_rec(cta, 1) : nullptr;
-        merge(list[0], group_rec[g] >> 8, group_rec[g + 1] >> 8, rec_b[r0], rec_it[r0], dst, i - g * elements);
+        merge(group_rec[g] >> 8, group_rec[g + 1] >> 8, rec_b[r0], rec_it[r0], dst, i - g * elements);
     }
     if (shared_first < 0 && shared_last < 0) return;
 
@@ -883,7 +886,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             if (r0 >= 0 && (level == 0 || arrived[k] == 2)) {
                 const int32_t first = rec_first[r0] + kFp4Item;   // its first tile
                 const int o0 = runs.owner(first), n = runs.owner(first + rec_n[r0] - 1) - o0 + 1;
-                const bool two = n > kFp4Flat, grouped = two && level == 0;
+                const bool two = n > C::kFlat, grouped = two && level == 0;
                 const int g0 = grouped ? (cta - o0) / kFp4Group * kFp4Group : 0, gslot = g0 == 0 ? 1 : 0;
                 const int sharers = grouped ? min(kFp4Group, n - g0) : two ? (n + kFp4Group - 1) / kFp4Group : n;
                 int32_t *counter = grouped ? p.group_counters + (int64_t)(o0 + g0) * 2 + gslot
@@ -897,7 +900,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
                 last = __shfl_sync(0xffffffffu, last, 0) * (grouped ? 2 : 1);
                 // an item's record is its first CTA's last one and every other CTA's first one
                 const int c = two && !grouped ? lane * kFp4Group : g0 + lane;
-                if (lane < sharers) list[k][lane] = global_rec(o0 + c, (two && !grouped ? 2 : 0) + (c == 0 ? 1 : 0));
+                if (lane < sharers) source[k][lane] = global_rec(o0 + c, (two && !grouped ? 2 : 0) + (c == 0 ? 1 : 0));
             }
             if (lane == 0) arrived[k] = last;  // 2: and there is another level
         }
@@ -905,12 +908,27 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
         const int a0 = arrived[0], a1 = arrived[1];
         if (a0 == 0 && a1 == 0) return;
         __threadfence();
-        // two items: half the CTA for each
-        const int threads = a0 != 0 && a1 != 0 ? C::kThreads / 2 : C::kThreads;
-        const int k = a0 != 0 && (int)threadIdx.x < threads ? 0 : 1, r0 = k ? shared_last : shared_first;
 #pragma unroll 1
-        for (int i = (int)threadIdx.x % threads; i < elements; i += threads)
-            merge(list[k], 0, sharers_of[k], rec_b[r0], rec_it[r0], merged_to[k], i);
+        for (int k = 0; k < 2; ++k) {
+            if ((k ? a1 : a0) == 0) continue;
+            // the records into shared memory, where the CTA's own have been merged, all of
+            // them on their way at once
+            constexpr int kPieces = C::kRec / 4;
+            const int n = sharers_of[k], r0 = k ? shared_last : shared_first;
+#pragma unroll 1
+            for (int i = threadIdx.x; i < n * kPieces; i += C::kThreads) {
+                const int r = i / kPieces;
+                cp_async16(smem_u32(smem) + i * 16, source[k][r] + (i - r * kPieces) * 4);
+            }
+            if ((int)threadIdx.x < n) rec_at[threadIdx.x] = smem_u32(smem) + threadIdx.x * C::kRec * 4;
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+#pragma unroll 1
+            for (int i = threadIdx.x; i < elements; i += C::kThreads)
+                merge(0, n, rec_b[r0], rec_it[r0], merged_to[k], i);
+            __syncthreads();                   // before the next records come
+        }
         if (a0 < 2 && a1 < 2) return;
     }
 }
@@ -935,7 +953,7 @@ struct Fp4Launch {
         if (e != cudaSuccess) return e;
         e = device_sm_count(&sms);
         if (e != cudaSuccess) return e;
-        const int64_t grid = sms < 32 * kFp4Group ? sms : 32 * kFp4Group;   // one CTA per SM; a merge takes 32 records
+        const int64_t grid = sms < kFp4Groups * kFp4Group ? sms : kFp4Groups * kFp4Group;   // one CTA per SM
         const int64_t cap = (max_tiles + C::kWarps * kFp4MinTiles - 1) / (C::kWarps * kFp4MinTiles);
         const int64_t most = cap > plan->items ? cap : plan->items;   // an item to a CTA, or equal runs
         plan->grid = (int)(grid > most ? most : grid);
@@ -981,7 +999,7 @@ cudaError_t plan_decode_fp4(int dtype, int head_dim, int group, int batch, int k
                             int64_t max_tiles_per_item, Fp4Plan *plan) {
     // one 8-column tile per item, or two when the kv head has more columns: the
     // conversion of a tile, not its MMAs, is what an item costs (32 x 2048 tokens,
-    // 16 heads to each of 4: 19.8 us with two, 22.7 in two items of one)
+    // 16 heads to each of 4: 20.1 us with two, 22.8 in two items of one)
     const int columns = group * (dtype == PA_F32 ? 2 : 1);
     plan->nt = head_dim <= 128 && columns > 8 ? 2 : 1;
     const int heads = plan->nt * 8 / (dtype == PA_F32 ? 2 : 1);
