@@ -325,7 +325,8 @@ def test_two_decodes_at_once_on_two_streams():
 # --- reading rows back -------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
-@pytest.mark.parametrize("D,Hkv,bs", [(64, 1, 16), (64, 2, 3), (128, 8, 16), (128, 1, 1), (256, 5, 24)])
+@pytest.mark.parametrize("D,Hkv,bs", [(64, 1, 16), (64, 2, 3), (64, 3, 16), (64, 7, 8), (128, 8, 16), (128, 1, 1), (256, 5, 24),
+                                       (256, 1, 16)])
 def test_gather_rows(D, Hkv, bs, dtype):
     lens = [40, 0, 100, 7]
     c = Cache(lens=lens, H=Hkv, Hkv=Hkv, D=D, bs=bs, dtype=dtype, k_scale=0.375, v_scale=3.0, seed=D).to_gpu()
