@@ -24,6 +24,7 @@ paged_kv_append_rope_fp4, paged_attention_decode_fp4, paged_kv_gather_fp4 (the
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 from pathlib import Path
 
@@ -81,6 +82,10 @@ class NewRows(ctypes.Structure):
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
                 ("max_tokens", ctypes.c_int32)]
 
+
+# The three structs as bytes (a third of a Structure's time to build).
+_SHAPE, _ROPE, _ROWS = struct.Struct("@6i2qi0q"), struct.Struct("@P3i2Pf0q"), struct.Struct("@3P3qi0q")
+assert [s.size for s in (_SHAPE, _ROPE, _ROWS)] == [ctypes.sizeof(t) for t in (Shape, Rope, NewRows)]
 
 _lock = threading.Lock()
 _lib = None
@@ -146,19 +151,19 @@ def load() -> ctypes.CDLL:
             lib.paged_attention_decode_balanced.restype = ctypes.c_int
             lib.paged_attention_decode_balanced.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                             f32, i32, vp, sz, vp, vp]
-            rp, np_ = ctypes.POINTER(Rope), ctypes.POINTER(NewRows)
+            # structs by address: a Structure's byref, or its bytes
             lib.paged_kv_append_rope.restype = ctypes.c_int
-            lib.paged_kv_append_rope.argtypes = [sp, rp, np_, vp, vp, vp, vp, vp, vp, vp, vp]
+            lib.paged_kv_append_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
             lib.paged_kv_append_fp4.restype = ctypes.c_int
-            lib.paged_kv_append_fp4.argtypes = [sp, np_, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_kv_append_fp4.argtypes = [vp, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
             lib.paged_kv_append_rope_fp4.restype = ctypes.c_int
-            lib.paged_kv_append_rope_fp4.argtypes = [sp, rp, np_, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_kv_append_rope_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
             lib.paged_kv_gather_fp4.restype = ctypes.c_int
-            lib.paged_kv_gather_fp4.argtypes = [sp, vp, vp, i32, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
+            lib.paged_kv_gather_fp4.argtypes = [vp, vp, vp, i32, vp, vp, vp, f32, f32, vp, vp, vp, vp, vp]
             lib.paged_attention_fp4_workspace.restype = sz
             lib.paged_attention_fp4_workspace.argtypes = [sp]
             lib.paged_attention_decode_fp4.restype = ctypes.c_int
-            lib.paged_attention_decode_fp4.argtypes = [sp, vp, vp, vp, vp, vp, f32, f32, vp, vp, f32, i32, vp, sz,
+            lib.paged_attention_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, f32, i32, vp, sz,
                                                        vp, vp]
             _lib = lib
     return _lib
@@ -172,9 +177,12 @@ def version() -> int:
     return int(load().pa_version())
 
 
+_DTYPE_CODES = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+
+
 def dtype_code(dtype: torch.dtype) -> int:
     try:
-        return {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}[dtype]
+        return _DTYPE_CODES[dtype]
     except KeyError:
         raise TypeError(f"unsupported dtype {dtype}") from None
 
@@ -559,16 +567,17 @@ def _new_rows(what, x):
     """(batch, tokens, heads, head_dim, token stride) of new rows
     [B][heads][D] or [B][T][heads][D], possibly a slice of a packed
     projection output."""
-    if x.dim() == 4:
-        B, T, H, D = x.shape
-        sb, stride, sh, sd = x.stride()
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 4:
+        B, T, H, D = shape
+        sb, stride, sh, sd = strides
         if T == 1:
             stride = sb
         elif B > 1 and sb != T * stride:
             raise ValueError(f"{what}: tokens must lie at one stride")
-    elif x.dim() == 3:
-        B, H, D = x.shape
-        stride, sh, sd = x.stride()
+    elif len(shape) == 3:
+        B, H, D = shape
+        stride, sh, sd = strides
         T = 1
     else:
         raise ValueError(f"{what} must be [B][heads][D] or [B][T][heads][D]")
@@ -587,26 +596,28 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
     dt = k_new.dtype
     code = dtype_code(dt)
     B, T, Hkv, D, ks = _new_rows("k_new", k_new)
-    *like, vs = _new_rows("v_new", v_new)
-    if like != [B, T, Hkv, D] or v_new.dtype != dt:
+    b, t, h, d, vs = _new_rows("v_new", v_new)
+    if b != B or t != T or h != Hkv or d != D or v_new.dtype != dt:
         raise ValueError("k_new and v_new differ in shape or dtype")
-    H, qs, qp = Hkv, 0, None
+    H, qs, qp = Hkv, 0, 0
     if q is not None:
-        bq, tq, H, dq, qs = _new_rows("q", q)
-        if (bq, tq, dq) != (B, T, D) or q.dtype != dt:
+        b, t, H, d, qs = _new_rows("q", q)
+        if b != B or t != T or d != D or q.dtype != dt:
             raise ValueError("q does not match the keys in batch, tokens, head_dim or dtype")
         if q_out is None or q_out.numel() != B * T * H * D or q_out.dtype != dt or not q_out.is_contiguous():
             raise ValueError(f"q_out must be contiguous, with batch * tokens * heads * head_dim elements of {dt}")
         qp = q.data_ptr()
     _dense("block_table and positions", torch.int32, block_table, positions)
-    if block_table.shape[0] != B or positions.numel() != B:
+    rows, MB = block_table.shape
+    if rows != B or positions.numel() != B:
         raise ValueError("block_table and positions must have one row per sequence")
     if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
         raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
     fp4 = kv_scales is not None
     if fp4:
         _dense("kv_scales", torch.uint8, kv_scales)
-    if k_pool.dtype != v_pool.dtype or k_pool.dtype != (torch.uint8 if fp4 else dt):
+    pool_dtype = torch.uint8 if fp4 else dt
+    if k_pool.dtype != pool_dtype or v_pool.dtype != pool_dtype:
         raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
     R, most = 0, 0
     if cos_sin is not None:
@@ -616,21 +627,20 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
             raise ValueError("cos_sin must be [max_position][rotary_dim]")
     elif rotary_dim:
         raise ValueError("a rotation needs cos_sin")
-    if q_norm is not None or k_norm is not None:
-        for what, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is not None and not (w.dtype == dt and w.is_contiguous() and w.numel() == D):
-                raise ValueError(f"{what} must hold head_dim contiguous elements of {dt}")
+    for w in (q_norm, k_norm):
+        if w is not None and not (w.dtype == dt and w.is_contiguous() and w.numel() == D):
+            raise ValueError(f"q_norm and k_norm must hold head_dim contiguous elements of {dt}")
     on = _launch_stream(stream, name, k_new, v_new, q, q_out, k_pool, v_pool, kv_scales, block_table, positions, counts,
                         cos_sin, q_norm, k_norm, err_word)
-    shape = Shape(B, H, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, code)
-    rows = NewRows(qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
+    shape = _SHAPE.pack(B, H, Hkv, D, block_size, MB, num_blocks, block_stride, code)
+    rows = _ROWS.pack(qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
     pools = (k_pool.data_ptr(), v_pool.data_ptr())
     if fp4:
         pools += (kv_scales.data_ptr(), k_scale, v_scale)
     tail = (block_table.data_ptr(), positions.data_ptr(), _addr(counts), _addr(err_word), on)
     if name == "paged_kv_append_fp4":
         return _issue(load().paged_kv_append_fp4, (shape, rows, *pools, *tail), name, prepare)
-    rope = Rope(_addr(cos_sin), most, R, interleaved, _addr(q_norm), _addr(k_norm), eps)
+    rope = _ROPE.pack(_addr(cos_sin) or 0, most, R, interleaved, _addr(q_norm) or 0, _addr(k_norm) or 0, eps)
     return _issue(getattr(load(), name), (shape, rope, rows, _addr(q_out), *pools, *tail), name, prepare)
 
 
@@ -679,7 +689,8 @@ def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, st
     _dense("k_out and v_out", dt, k_out, v_out)
     _dense("kv_scales", torch.uint8, kv_scales)
     _dense("block_table and starts", torch.int32, block_table, starts)
-    if block_table.shape[0] != B or starts.numel() != B:
+    rows, MB = block_table.shape
+    if rows != B or starts.numel() != B:
         raise ValueError("block_table and starts must have one row per sequence")
     if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
         raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
@@ -687,7 +698,7 @@ def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, st
         raise ValueError("the pools must be uint8")
     on = _launch_stream(stream, "paged_kv_gather_fp4", k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts,
                         counts, err_word)
-    shape = Shape(B, Hkv, Hkv, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(dt))
+    shape = _SHAPE.pack(B, Hkv, Hkv, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
     args = (shape, k_out.data_ptr(), v_out.data_ptr(), T, k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(),
             k_scale, v_scale, block_table.data_ptr(), starts.data_ptr(), _addr(counts), _addr(err_word), on)
     return _issue(load().paged_kv_gather_fp4, args, "paged_kv_gather_fp4", prepare)
@@ -721,13 +732,14 @@ def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, s
     _dense("q and out", dt, q, out)
     _dense("kv_scales and workspace", torch.uint8, kv_scales, workspace)
     _dense("block_table and seq_lens", torch.int32, block_table, seq_lens)
-    if block_table.shape[0] != B or seq_lens.numel() != B:
+    rows, MB = block_table.shape
+    if rows != B or seq_lens.numel() != B:
         raise ValueError("block_table and seq_lens must have one row per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
         raise ValueError("the pools must be uint8")
     on = _launch_stream(stream, "paged_attention_decode_fp4", q, out, k_pool, v_pool, kv_scales, block_table, seq_lens,
                         workspace, err_word)
-    shape = Shape(B, H, num_kv_heads, D, block_size, block_table.shape[1], num_blocks, block_stride, dtype_code(dt))
+    shape = _SHAPE.pack(B, H, num_kv_heads, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
     args = (shape, out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), k_scale,
             v_scale, block_table.data_ptr(), seq_lens.data_ptr(), scale, window, workspace.data_ptr(), workspace.numel(),
             _addr(err_word), on)
