@@ -573,7 +573,7 @@ def _new_rows(what, x):
         sb, stride, sh, sd = strides
         if T == 1:
             stride = sb
-        elif B > 1 and sb != T * stride:
+        elif B > 1 and T > 0 and sb != T * stride:
             raise ValueError(f"{what}: tokens must lie at one stride")
     elif len(shape) == 3:
         B, H, D = shape

@@ -405,3 +405,13 @@ def test_two_appends_at_once_on_two_streams():
     torch.cuda.synchronize()
     for s, out in zip((a, b), outs):
         s.check(*out[:3])
+
+
+def test_nothing_to_append_is_a_no_op():
+    """No tokens, or no sequences: accepted, and nothing is written."""
+    for kw in (dict(B=3, T=0), dict(B=2, T=4, counts=[0, 0])):
+        for fp4 in (False, True):
+            s = Step(fp4=fp4, seed=16, **kw)
+            out = s.gpu()
+            torch.cuda.synchronize()
+            s.check(*out)

@@ -256,6 +256,7 @@ def test_new_rows_accepts_slices_of_a_packed_projection():
     assert pa._new_rows("k", packed[:, 1:2, 8:9]) == (3, 1, 1, 64, 5 * 12 * 64)
     with pytest.raises(ValueError):                     # sequences further apart than their tokens
         pa._new_rows("k", packed[:, :4, 8:10])
+    assert pa._new_rows("k", packed[:, :0, 8:10]) == (3, 0, 2, 64, 128)      # no tokens: nothing to stride over
     one = torch.zeros(1, 1, 2, 64)
     assert pa._new_rows("k", one.expand(1, 1, 2, 64)) == (1, 1, 2, 64, 128)
     for x in (one.expand(3, 1, 2, 64), one.expand(1, 5, 2, 64), one[0].expand(3, 2, 64)):
