@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -125,19 +126,23 @@ struct ReduceParams {
 // microseconds of host time, more than a small launch itself.  `configured`
 // is the caller's per-kernel record (largest limit set so far, per device):
 // kernels of one signature share a function-pointer type, so the record
-// cannot live in this template.
+// cannot live in this template.  One host thread at a time raises limits, so
+// that a smaller one never lands on a larger one that is recorded.
+inline std::mutex &smem_limit_mutex() {
+    static std::mutex m;
+    return m;
+}
 template <typename Kern>
 inline cudaError_t ensure_smem_limit(Kern kern, size_t bytes, std::atomic<int> (&configured)[64]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && configured[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (configured[dev].load(std::memory_order_acquire) >= (int)bytes) return cudaSuccess;
+    const std::lock_guard<std::mutex> raising(smem_limit_mutex());
+    if (configured[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) {
-        int cur = configured[dev].load(std::memory_order_relaxed);
-        while (cur < (int)bytes && !configured[dev].compare_exchange_weak(cur, (int)bytes)) {
-        }
-    }
+    if (e == cudaSuccess) configured[dev].store((int)bytes, std::memory_order_release);
     return e;
 }
 
