@@ -941,23 +941,19 @@ template <typename T, int D, int NT, bool WHOLE>
 struct Fp4Launch {
     using C = Fp4Cfg<T, D, NT>;
     static std::atomic<int> configured[64];
-    static int64_t occupancy[64][2];
 
     static cudaError_t plan(int batch, int64_t max_tiles, Fp4Plan *plan) {
         auto kern = decode_fp4_kernel<T, D, NT, WHOLE>;
         const size_t smem = C::bytes(batch);
         cudaError_t e = ensure_smem_limit(kern, smem, configured);
         if (e != cudaSuccess) return e;
-        int per_sm = 0, sms = 0;
-        e = resident_ctas(kern, C::kThreads, smem, occupancy, &per_sm);
-        if (e != cudaSuccess) return e;
+        int sms = 0;                               // what the limit allows, an SM holds
         e = device_sm_count(&sms);
         if (e != cudaSuccess) return e;
         const int64_t grid = sms < kFp4Groups * kFp4Group ? sms : kFp4Groups * kFp4Group;   // one CTA per SM
         const int64_t cap = (max_tiles + C::kWarps * kFp4MinTiles - 1) / (C::kWarps * kFp4MinTiles);
         const int64_t most = cap > plan->items ? cap : plan->items;   // an item to a CTA, or equal runs
         plan->grid = (int)(grid > most ? most : grid);
-        if (per_sm < 1) plan->grid = 0;
         plan->max_grid = (int)grid;
         plan->smem = smem;
         return cudaSuccess;
@@ -969,7 +965,6 @@ struct Fp4Launch {
     }
 };
 template <typename T, int D, int NT, bool WHOLE> std::atomic<int> Fp4Launch<T, D, NT, WHOLE>::configured[64];
-template <typename T, int D, int NT, bool WHOLE> int64_t Fp4Launch<T, D, NT, WHOLE>::occupancy[64][2] = {};
 
 // f(Fp4Launch<...>{}) for the shape's instantiation.
 template <typename T, typename F>

@@ -138,6 +138,7 @@ inline cudaError_t ensure_smem_limit(Kern kern, size_t bytes, std::atomic<int> (
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (bytes > (size_t)INT32_MAX) return cudaErrorInvalidValue;
     if (configured[dev].load(std::memory_order_acquire) >= (int)bytes) return cudaSuccess;
     const std::lock_guard<std::mutex> raising(smem_limit_mutex());
     if (configured[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
@@ -165,22 +166,25 @@ inline cudaError_t device_sm_count(int *count) {
 
 // CTAs of `kern` (block threads, `smem` bytes of dynamic shared memory) that
 // one SM holds at once, cached per device for the last smem size asked.
-// `cache` is the caller's per-kernel record: {smem, result} per device.
+// `cache` is the caller's per-kernel record, per device: smem + 1 and the
+// result (low 16 bits) in one word, so that no host thread sees one without
+// the other.
 template <typename Kern>
-inline cudaError_t resident_ctas(Kern kern, int block, size_t smem, int64_t (&cache)[64][2],
+inline cudaError_t resident_ctas(Kern kern, int block, size_t smem, std::atomic<int64_t> (&cache)[64],
                                  int *count) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (cache[dev][0] != (int64_t)smem + 1) {
+    int64_t known = cache[dev].load(std::memory_order_relaxed);
+    if (known >> 16 != (int64_t)smem + 1) {
         int n = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, block, smem);
         if (e != cudaSuccess) return e;
-        cache[dev][0] = (int64_t)smem + 1;
-        cache[dev][1] = n;
+        known = ((int64_t)smem + 1) << 16 | n;
+        cache[dev].store(known, std::memory_order_relaxed);
     }
-    *count = (int)cache[dev][1];
+    *count = (int)(known & 0xffff);
     return cudaSuccess;
 }
 

@@ -1,5 +1,5 @@
 """CPU checks that the per-kernel records of the host side (the shared-memory
-limit) hold when two host threads plan their first launches at once.  A small
+limit, the resident CTAs) hold when two host threads plan launches at once.  A small
 program compiled against csrc/pa_internal.h stands in for the CUDA runtime with
 fakes that bring the threads into the order that hurts; its waits are bounded."""
 import subprocess
@@ -18,6 +18,7 @@ PROGRAM = r"""
 #include <cuda_runtime.h>
 
 static cudaError_t cudaFuncSetAttribute(void (*)(int), cudaFuncAttribute, int bytes);
+static cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int *n, void (*)(int), int, size_t smem);
 
 #include "pa_internal.h"
 
@@ -42,6 +43,11 @@ static cudaError_t cudaFuncSetAttribute(void (*)(int), cudaFuncAttribute, int by
     return cudaSuccess;
 }
 
+static cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int *n, void (*)(int), int, size_t smem) {
+    *n = smem == 1000 ? 3 : 1;
+    return cudaSuccess;
+}
+
 static void kern(int) {}
 
 int main() {
@@ -52,6 +58,25 @@ int main() {
     a.join();
     b.join();
     printf("limit %d recorded %d status %d %d\n", limit.load(), configured[0].load(), (int)small, (int)large);
+
+    // what an int does not hold is refused, not cut to what it holds
+    printf("huge %d\n", (int)(pa::ensure_smem_limit(kern, ((size_t)1 << 32) + 8, configured) == cudaErrorInvalidValue));
+
+    // two sizes asked for in turn, by two threads: each gets the answer to its own
+    static std::atomic<int64_t> cache[64];
+    std::atomic<int> wrong{0}, ready{0};
+    auto ask = [&](size_t smem, int want) {
+        ++ready;
+        for (int i = 0; i < 1000000 && ready.load() < 2; ++i) {}
+        for (int i = 0; i < 300000; ++i) {
+            int n = 0;
+            if (pa::resident_ctas(kern, 32, smem, cache, &n) != cudaSuccess || n != want) ++wrong;
+        }
+    };
+    std::thread c([&] { ask(1000, 3); }), d([&] { ask(2000, 1); });
+    c.join();
+    d.join();
+    printf("wrong %d\n", wrong.load());
     return 0;
 }
 """
@@ -71,3 +96,11 @@ def said(tmp_path_factory):
 
 def test_a_recorded_limit_is_the_kernels_limit(said):
     assert "limit 2000 recorded 2000 status 0 0" in said, said
+
+
+def test_resident_ctas_are_those_of_the_size_asked_for(said):
+    assert "wrong 0" in said, said
+
+
+def test_sizes_past_an_int_are_refused(said):
+    assert "huge 1" in said, said
