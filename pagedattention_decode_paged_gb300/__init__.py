@@ -536,13 +536,14 @@ def rope_table(max_position, rotary_dim, theta=10000.0, device=None) -> torch.Te
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream() without building a Stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # of a process that has used one
 
 
 def _launch_stream(stream, what, *tensors):
     """The stream a call runs on, after checking that every tensor (None aside)
     lies on the current device, the one the kernels are launched on."""
     dev = tensors[0].get_device()
-    ok = dev >= 0 and dev == torch.cuda.current_device()
+    ok = dev >= 0 and dev == _current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             ok = False
@@ -561,6 +562,19 @@ def _dense(what, dtype, *tensors) -> None:
     for t in tensors:
         if t.dtype != dtype or not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous {dtype} tensors")
+
+
+def _pools_hold(k_pool, v_pool, kv_scales, heads, D, block_size, num_blocks, block_stride) -> None:
+    """Refuse pools and scales that end before num_blocks blocks do.  A pool is
+    where its memory begins; how far it reaches, its storage says."""
+    row = D if kv_scales is None else D // 2
+    size = k_pool.element_size()
+    need = ((num_blocks - 1) * block_stride + heads * block_size * row) * size
+    for pool in (k_pool, v_pool):
+        if pool.untyped_storage().nbytes() - pool.storage_offset() * size < need:
+            raise ValueError("the pools must hold num_blocks blocks, block_stride apart")
+    if kv_scales is not None and kv_scales.numel() < num_blocks * 2 * heads * block_size * (D // 16):
+        raise ValueError("kv_scales must be [num_blocks][2][kv heads][block_size][head_dim/16]")
 
 
 def _new_rows(what, x):
@@ -619,6 +633,7 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
     pool_dtype = torch.uint8 if fp4 else dt
     if k_pool.dtype != pool_dtype or v_pool.dtype != pool_dtype:
         raise ValueError("the pools must be uint8 (4-bit cache) or of the new rows' dtype")
+    _pools_hold(k_pool, v_pool, kv_scales, Hkv, D, block_size, num_blocks, block_stride)
     R, most = 0, 0
     if cos_sin is not None:
         _dense("cos_sin", torch.float32, cos_sin)
@@ -696,6 +711,7 @@ def paged_kv_gather_fp4(k_out, v_out, k_pool, v_pool, kv_scales, block_table, st
         raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
         raise ValueError("the pools must be uint8")
+    _pools_hold(k_pool, v_pool, kv_scales, Hkv, D, block_size, num_blocks, block_stride)
     on = _launch_stream(stream, "paged_kv_gather_fp4", k_out, v_out, k_pool, v_pool, kv_scales, block_table, starts,
                         counts, err_word)
     shape = _SHAPE.pack(B, Hkv, Hkv, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
@@ -737,6 +753,7 @@ def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, s
         raise ValueError("block_table and seq_lens must have one row per sequence")
     if k_pool.dtype != torch.uint8 or v_pool.dtype != torch.uint8:
         raise ValueError("the pools must be uint8")
+    _pools_hold(k_pool, v_pool, kv_scales, num_kv_heads, D, block_size, num_blocks, block_stride)
     on = _launch_stream(stream, "paged_attention_decode_fp4", q, out, k_pool, v_pool, kv_scales, block_table, seq_lens,
                         workspace, err_word)
     shape = _SHAPE.pack(B, H, num_kv_heads, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
