@@ -28,10 +28,16 @@ extern "C" {
  *             Row p of cos_sin (device fp32 [max_position][R]) holds the R/2
  *             cosines, then the R/2 sines, of cache position p; elements from
  *             R on pass unchanged.
- * Value rows pass unchanged.  The arithmetic is binary32 with every product
- * and sum rounded by itself (no fused multiply-add in the rotation, so the
- * results are those of the formula evaluated operation by operation), and
- * one rounding to the target type at the end.
+ * Value rows pass unchanged.  The arithmetic is binary32, with one rounding to
+ * the target type at the end.  The norm's and the rotation's products and the
+ * rotation's sums are each rounded by themselves (no fused multiply-add), so
+ * that the rotation is the formula evaluated operation by operation; the mean
+ * square is summed in the kernel's own order, with fused multiply-adds, before
+ * eps is added and r taken with a rounding each.
+ * The sum of a row's squares has to stay within binary32.  Where it passes
+ * 2^128 (a root mean square of 1.6e18 at head_dim 128) r is 0 and the row
+ * zeros; where every square is 0 (elements below 2^-75) and eps is 0, r is
+ * infinite and the row NaN or infinities.
  * R must be a multiple of 16 not above head_dim (0: no rotation, cos_sin
  * may be NULL); cos_sin and the weights 16-byte aligned; eps >= 0 and finite
  * when there is a weight.
