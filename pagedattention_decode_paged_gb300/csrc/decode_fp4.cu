@@ -20,9 +20,11 @@
 //   their even and odd elements with one shift and one select each, and the
 //   cvt then yields (token, next token) pairs.  tau is a permutation of 0..7
 //   chosen so that the wide K loads and the V loads both miss no bank.
-//   A column is rescaled only when a score passes the reference maximum by
-//   more than 2^8 (weights stay inside fp16), so a tile usually costs one
-//   vote and no shuffles.
+//   A column's weights are taken against a reference 2^7 below its largest
+//   score, and rescaled only when a score passes the reference by more than
+//   2^15, so that a tile usually costs one vote and no shuffles.  Inside fp16
+//   that leaves the most room below the largest weight: 11 bits down to 2^-21
+//   of it, 2^-32 of it below.
 //
 // What bounds it: 4.5 bits per value are so few that a tile's conversions (570
 // instructions for 4.6 KB at head_dim 128, half of them on the pipe of the
@@ -51,6 +53,7 @@ namespace pa {
 
 constexpr int kFp4Tile = 32;       // tokens of a tile: two halves of 16, the MMAs' token axis
 constexpr int kFp4Halves = kFp4Tile / 16;
+constexpr float kFp4Below = 7.f, kFp4Over = 15.f;   // log2 of a column's largest weight when it is rescaled, and before it is
 constexpr float kFp4Empty = -3.402823466e38f;   // reference of a column without scores: below any, and finite
 // The rules of the split, each with what the other side of it took:
 // - what an item costs beside its tiles (queries, output), in tiles.  256 ragged
@@ -535,14 +538,14 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
                 for (int i = 0; i < 4; ++i) {
                     if (P == 2) c[half][nt][i] += __shfl_xor_sync(0xffffffffu, c[half][nt][i], 2);
                     x[half][nt][i] = fmaf(c[half][nt][i], cs[nt][i & 1], nm[half][i >> 1][nt][i & 1]);
-                    over = over || x[half][nt][i] > 8.f;
+                    over = over || x[half][nt][i] > kFp4Over;
                 }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float y[2 * kFp4Halves], mx = m[nt][j];
+                    float y[2 * kFp4Halves], mx = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 2 * kFp4Halves; ++i) {
                         y[i] = nm[i / 2][i & 1][nt][j] == -INFINITY ? -INFINITY : c[i / 2][nt][(i & 1) * 2 + j] * cs[nt][j];
@@ -550,6 +553,7 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
                     }
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+                    mx = fmaxf(m[nt][j], mx - kFp4Below);
                     const float f = ex2_approx(m[nt][j] - mx);
                     m[nt][j] = mx;
                     l[nt][j] *= f;
