@@ -93,15 +93,15 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
  * CTAs is finished by the last of them (the log-sum-exp merge of the
  * split-KV pair), in a fixed order, so results repeat from call to call.
  *
- * Numerics: 16-bit queries are read as fp16 after an exact scaling of each
- * head by a power of two (elements below 2^-14 of the head's largest keep an
- * absolute error of 2^-25 of it); keys and values are exact; scores, softmax
- * and sums are fp32; the weights enter the second product in fp16, off by at
- * most 2^-11 of themselves or 2^-32 of the largest, whichever is more.  fp32
- * queries and weights are carried as two fp16 parts (weights: 2^-22 of
- * themselves or 2^-32 of the largest).  Device checks, zeros and PA_DEVERR_*
- * bits are those of paged_attention_decode.  A NaN scale (0x7F, 0xFF) inside
- * the attended length makes the outputs it meets NaN.
+ * Numerics: each head's queries are scaled by a power of two, exactly, and
+ * read as fp16 (16-bit queries: exact, elements below 2^-28 of the head's
+ * largest to 2^-39 of it) or as two fp16 parts (fp32: off by at most 2^-22 of
+ * themselves or 2^-39 of the largest, whichever is more); keys and values are
+ * exact; scores, softmax and sums are fp32; the weights enter the second
+ * product in fp16, off by at most 2^-11 of themselves or 2^-32 of the largest,
+ * or, with fp32 queries, as two parts: 2^-22 and 2^-32.  Device checks, zeros
+ * and PA_DEVERR_* bits are those of paged_attention_decode.  A NaN scale
+ * (0x7F, 0xFF) inside the attended length makes the outputs it meets NaN.
  *
  * Workspace: as for paged_attention_decode_balanced -- at least
  * paged_attention_fp4_workspace() bytes on the device, 16-byte aligned,

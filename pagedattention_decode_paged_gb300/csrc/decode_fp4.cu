@@ -451,9 +451,11 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // a power of two that brings the head's largest element into [1, 2)
+            // a power of two that brings the head's largest element into [2^14, 2^15), as
+            // far below fp16's largest value as leaves its parts the most bits; no
+            // further than `up` is a normal number
             int e = (int)((__float_as_uint(big) >> 23) & 255u) - 127;
-            e = big > 0.f && e < 128 ? min(max(e, -126), 126) : 0;
+            e = big > 0.f && e < 128 ? max(e, -112) - 14 : 0;
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll

@@ -64,6 +64,19 @@ def held(c):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype,below", [(BF16, 20), (F16, 18), (F32, 12), (F32, 17)])
+def test_query_elements_far_below_the_largest(dtype, below, D):
+    """One element of each query is 2^below times the others, where every key is
+    zero: the scores are those of the others."""
+    c = Cache(lens=[100, 33, 1, 700], H=8, Hkv=2, D=D, dtype=dtype, seed=41)
+    c.scales[:, 0, :, :, 0] = torch.where(c.scales[:, 0, :, :, 0] == 0x7F, 0x7F, 0).to(torch.uint8)
+    c.q = (c.q.float() * 2.0 ** -(below - 8)).to(dtype)
+    c.q[:, :, 5] = 256.0
+    c.scale = 2.0 ** (below - 8) / math.sqrt(D)
+    held(c)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("bits", [14.4, 20.6])
 def test_weights_far_below_the_largest(bits, dtype, D):
