@@ -43,6 +43,7 @@
 // a CTA meet in shared memory, those of CTAs in the workspace, where the last
 // to arrive merges (in two levels when many share an item), always in the
 // items' order, so that results repeat.
+#include <float.h>
 #include <math.h>
 
 #include "balanced.cuh"
@@ -476,7 +477,8 @@ decode_fp4_kernel(const __grid_constant__ Fp4Decode fp, const int units_per_kv) 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = P == 2 ? (2 * tig + j) & 3 : 2 * tig + j;
-                cs[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, c * 4);
+                // finite, so that it leaves a product of 0 (masked rows among them) as it is
+                cs[nt][j] = fminf(fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, up, c * 4), -FLT_MAX), FLT_MAX);
                 m[nt][j] = kFp4Empty;
                 l[nt][j] = 0.f;
             }

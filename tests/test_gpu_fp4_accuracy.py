@@ -93,3 +93,15 @@ def test_weights_far_below_the_largest(bits, dtype, D):
         c.scales[blk, 1, :, 0] = 0
     c.scale = bits * math.log(2.0) / 16
     held(c)
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 128), (BF16, 256)])
+def test_a_scaled_query_past_binary32_where_keys_are_zero(dtype, D):
+    """The query's largest element times the scale is no fp32 number; every key
+    is zero there and the score finite."""
+    c = Cache(lens=[100, 33, 1, 64], H=4, Hkv=2, D=D, dtype=dtype, seed=43)
+    c.scales[:, 0, :, :, 0] = torch.where(c.scales[:, 0, :, :, 0] == 0x7F, 0x7F, 0).to(torch.uint8)
+    c.q = torch.zeros_like(c.q)
+    c.q[:, :, 5] = 1e38
+    c.scale = 1e38
+    held(c)
