@@ -60,7 +60,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
     if (fp4) {
         st = check_fp4_shape(s, false);
     } else {
-        if (!pa::rope_append_supported(s->dtype, s->head_dim, false)) return PA_ERR_UNSUPPORTED;
+        if (!pa::rope_append_supported(s->dtype, s->head_dim)) return PA_ERR_UNSUPPORTED;
         st = check_sizes(s, (int64_t)s->head_dim * elem_size(s->dtype), s->block_stride * elem_size(s->dtype));
     }
     if (st != PA_OK) return st;

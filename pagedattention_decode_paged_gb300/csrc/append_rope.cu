@@ -32,8 +32,6 @@
 // Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990) where nothing over- or underflows; a group with a NaN or a
 // magnitude that could overflow takes IEEE divisions instead.
-#include <float.h>
-
 #include "fp4.cuh"
 #include "pa_rope_fp4.h"
 
@@ -507,8 +505,7 @@ static cudaError_t launch_one(const RopeAppendParams &p, cudaStream_t stream) {
     return launch_mode<T, D, FP4, kSplit>(p, stream);
 }
 
-bool rope_append_supported(int dtype, int head_dim, bool fp4) {
-    if (fp4) return fp4_head_dim(head_dim);
+bool rope_append_supported(int dtype, int head_dim) {
     if (dtype == PA_F32) return head_dim == 16 || head_dim == 32 || head_dim == 64 || head_dim == 128;
     return head_dim == 32 || head_dim == 64 || head_dim == 128 || head_dim == 256;
 }

@@ -56,19 +56,12 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// 8 consecutive elements of T <-> fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T *src, float (&x)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *(reinterpret_cast<const float4 *>(src) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(src);
-        Elem<T>::unpack(a, x);
-    }
+// 8 consecutive elements: fp32 in, T out.
+__device__ __forceinline__ void load8(const float *src, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(src), b = *(reinterpret_cast<const float4 *>(src) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-
 template <typename T>
 __device__ __forceinline__ void store8(T *dst, const float (&x)[8]) {
     if constexpr (sizeof(T) == 4) {

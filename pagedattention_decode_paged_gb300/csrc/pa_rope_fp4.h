@@ -34,8 +34,8 @@ struct RopeAppendParams {
     float k_g, v_g;
 };
 
-// fp4: write the 4-bit cache (head_dim 64/128/256), else a cache of `dtype`.
-bool rope_append_supported(int dtype, int head_dim, bool fp4);
+// fp4: write the 4-bit cache (fp4_head_dim), else a cache of `dtype` (rope_append_supported).
+bool rope_append_supported(int dtype, int head_dim);
 cudaError_t launch_rope_append(int dtype, int head_dim, bool fp4, const RopeAppendParams &p, cudaStream_t stream);
 
 struct GatherFp4Params {
