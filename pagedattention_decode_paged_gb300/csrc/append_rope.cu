@@ -8,18 +8,19 @@
 // include/pagedattn_fp4.h state them).
 //
 // Every element is read once and written once, so the kernel is bound by HBM
-// for prompts (8 of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 554 MB in 88 us,
-// 6.3 TB/s, 93% of the copy rate) and by launch and the dependent loads (position,
-// table entry and cosines) for single tokens (1: 1.9 us; 256 of 32 + 32 heads: 2.8
+// for prompts (8 of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 554 MB in 89 us,
+// 6.2 TB/s, 92% of the copy rate) and by launch and the dependent loads (position,
+// table entry and cosines) for single tokens (1: 1.9 us; 256 of 32 + 32 heads: 2.9
 // us).  Into the 4-bit cache keys and values take three times their bytes' time: the
-// arithmetic of the codes (f16 prompts, 32 + 8 heads: 27.9 us, 13 of them theirs).  D/8 lanes hold a row, 8 elements each in two
-// chunks of 4.  With pairs (i, i + R/2) a lane takes chunk i and chunk i + R/2
-// (kSplit): each chunk of a row is still read in whole 128-byte lines, both
-// elements of a pair are in one lane, and its 4 cosines and sines serve both
-// chunks.  With pairs (2i, 2i + 1), or none, the chunks are neighbours.  Only
-// where the halves of R cut a 4-bit group of 16 (R not a multiple of 32) are
-// neighbouring chunks kept and the other elements of the pairs fetched by
-// shuffles (kShuffle).
+// arithmetic of the codes (f16 prompts, 32 + 8 heads: 28.3 us, 13 of them theirs).
+//
+// D/8 lanes hold a row, 8 elements each in two chunks of 4.  With pairs (i, i + R/2)
+// a lane takes chunk i and chunk i + R/2 (kSplit): each chunk of a row is still read
+// in whole 128-byte lines, both elements of a pair are in one lane, and its 4
+// cosines and sines serve both chunks.  With pairs (2i, 2i + 1), or none, the chunks
+// are neighbours.  Only where the halves of R cut a 4-bit group of 16 (R not a
+// multiple of 32) are neighbouring chunks kept and the other elements of the pairs
+// fetched by shuffles (kShuffle).
 //
 // A warp takes a run of the queries of one token, or of its keys with the values
 // beside them: up to 8 rows a lane, all of whose loads are issued at once, before
@@ -38,8 +39,8 @@
 namespace pa {
 
 // Warps per CTA: small ones, whose slots are free again as soon as both are done
-// (8 prompts of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 125.7 us at 8, 93.0 at
-// 4, 88.0 at 2, 89.3 at 1).
+// (8 prompts of 900 to 2047 tokens, 64 + 8 heads of 128, bf16: 97.8 us at 8, 91.5 at
+// 4, 89.3 at 2, 90.5 at 1, with as many registers).
 constexpr int kRopeWarps = 2;
 constexpr int kRopeThreads = kRopeWarps * 32;
 enum RopeMode { kSplit, kNeighbours, kShuffle };
@@ -215,14 +216,19 @@ __device__ __forceinline__ void store_fp4(const float2 (&x)[2], const float2 (&y
 // KB and QB), so that the warps of a CTA do the same (runs of a token side by
 // side instead: equal).
 // Iterations of queries a run has at most, as many as keep their registers; half
-// as many of keys, with their values (f16 prompts into the 4-bit cache, 4 warps to a
-// CTA: 1 of each 41 us, 2 31.9 us, 4 28.8 us, where the first had no CTAs of their own;
-// bf16 prompts: 99.8 us with 4 of queries, 93.0 with 8).
+// as many of keys, with their values (half of these: 100.1 us for 89.3 on the bf16
+// prompts, 32.5 for 28.3 on f16 ones into the 4-bit cache, 104.4 for 98.5 on fp32 ones
+// of 32 + 8 heads and 63.2 for 47.9 on such into the 4-bit cache; fp32 as 16-bit types:
+// 99.7 and 51.6).
 template <typename T>
 constexpr int kRopeBatch = sizeof(T) == 2 ? 8 : 4;
-// CTAs per SM that registers have to do for: up to where values are spilled (the
-// prompts above: 91.4 us at 12, 88.0 at 14, 95.7 at 15; f16 prompts into the 4-bit
-// cache: 28.4 us at 10, 27.9 at 11, 28.6 at 13).
+// CTAs per SM that registers have to do for (the bf16 prompts above: 93.1 us at 12,
+// 89.3 at 13 and 14, 97.5 at 15; f16 ones into the 4-bit cache: 28.9 at 10, 28.3 at 11,
+// 28.1 at 12, 29.0 at 13; fp32: 98.5 from 8 to 12, into the 4-bit cache 53.5 at 8, 47.9
+// at 10, 45.9 at 12).  The 16-bit kernels of the 4-bit cache, which would take up to 96
+// registers, spill at 80: a thread stores 16 to 24 bytes and loads 52 to 60, with pairs
+// by shuffles 52 to 56 and 216 to 220; so do those of head_dim 256 with pairs in
+// halves, 4 and 8 bytes at 72.
 template <typename T, bool FP4>
 constexpr int kRopeCtas = sizeof(T) == 4 ? 10 : FP4 ? 11 : 14;
 

@@ -26,16 +26,22 @@
 //   that leaves the most room below the largest weight: 11 bits down to 2^-21
 //   of it, 2^-32 of it below.
 //
+//   The weights of 16-bit queries are rounded to fp16 for the second product, and
+//   not for their sum: f16 outputs of the ragged batch below are 2.6e-4 from the
+//   definition, of which their own rounding is 2.1e-4; with two parts for them too
+//   they were no further than that, and took 52.9 us for 47.7, 114.5 for 101.5 on
+//   64 long sequences.
+//
 // What bounds it: 4.5 bits per value are so few that a tile's conversions (570
 // instructions for 4.6 KB at head_dim 128, half of them on the pipe of the
 // integer and conversion instructions) take nearly as long as its bytes.  64
 // sequences of 7000 to 8192 tokens, 64 heads on 8, bf16: 102 us where the bytes
-// take 83 us at the copy rate, the tile loop itself 88 us; with 16-token tiles 121 us.  What is left is what a launch costs beside its tiles: lengths,
-// table entries and first tiles one after another (6 us until the first tile is
-// multiplied), the merge of a CTA's warps (2 us) and, if items are cut between
-// CTAs, of the CTAs (3 to 5 us).  32 x 2048 tokens: 23.2 us (bytes 11.3); 256
-// sequences of 4 to 4096 tokens, 32 heads each, f16: 47.5 us (24.8); one of 131071:
-// 36.0 us (22.3).
+// take 83 us at the copy rate, the tile loop itself 88 us; with 16-token tiles 121
+// us.  What is left is what a launch costs beside its tiles: lengths, table entries
+// and first tiles one after another (6 us until the first tile is multiplied), the
+// merge of a CTA's warps (2 us) and, if items are cut between CTAs, of the CTAs (3 to
+// 5 us).  32 x 2048 tokens: 23.1 us (bytes 11.3); 256 sequences of 4 to 4096 tokens,
+// 32 heads each, f16: 47.7 us (24.8); one of 131071: 35.8 us (22.3).
 //
 // Work split: the tiles of all items, end to end, are cut into about equal runs,
 // one per CTA, and each into equal parts, one per warp (Fp4Cursor, Fp4Runs).  A
@@ -58,7 +64,11 @@ constexpr float kFp4Below = 7.f, kFp4Over = 15.f;   // log2 of a column's larges
 constexpr float kFp4Empty = -3.402823466e38f;   // reference of a column without scores: below any, and finite
 // The rules of the split, each with what the other side of it took:
 // - what an item costs beside its tiles (queries, output), in tiles.  256 ragged
-//   sequences of 32 heads: 65.3 us at 0, 47.6 at 1, 52.4 at 2; others within 1 us.
+//   sequences of 4 to 4096 tokens, median 87: f16, 32 heads of 128 65.6 us at 0, 47.7
+//   at 1, 52.7 at 2; 16 heads of 256 (bf16) 65.6, 47.2 and 50.6, of 128 (fp32) 41.0,
+//   30.6 and 33.3; but 32 heads of 64 (f16; fp32) 54.1, 38.4 and 37.4; 56.5, 40.3 and
+//   38.4, 16 query heads to a kv head of 64 (f16) 29.2, 21.2 and 19.6, 8 to one of 256
+//   (bf16) 47.7, 38.3 and 34.9.  One figure for all is within 10% of the best.
 constexpr int kFp4Item = 1;
 // - tiles per warp below which fewer CTAs share the work.  4 sequences of up to 128
 //   tokens: 7.0 us at 1, 7.7 at 2, 9.5 at 4; 4 of 2048: 13.2, 14.1, 14.2 us.
@@ -89,7 +99,8 @@ struct Fp4Cfg {
     static constexpr int kWarpRing = kStages * kStage;
     static constexpr int kRec = kHeads * D + 2 * kHeads;    // O, then m, then l
     // one CTA per SM: of 12 warps where a thread gets along with 168 registers (8
-    // warps: 58.9 us where 12 take 47.6 on the ragged batch, 25.0 and 23.3 on 32 x 2048)
+    // warps: 58.9 us where 12 take 47.6 on the ragged batch, 25.0 and 23.3 on 32 x 2048;
+    // the 16-bit kernels of head_dim 64 with two column tiles spill 8 bytes)
     static constexpr int kWarps = NT * D <= 128 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
     // the last record of a warp takes the place of its ring
