@@ -111,8 +111,10 @@ pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, i
  * device; a workspace may serve other shapes too, on the same device, if it is
  * large enough for them.  0 for a shape this entry point rejects: the schedule
  * keeps two int32 per sequence in shared memory and counts tokens and tiles in
- * int32 (PA_ERR_UNSUPPORTED: too many sequences, 2^30 tiles of all items, or a
- * table row of 2^31 - 1024 tokens).  scale * k_scale must be finite in fp32.
+ * int32 (PA_ERR_UNSUPPORTED: more sequences than fit, 2^30 tiles of all items,
+ * or a table row of 2^31 - 1024 tokens).  8000 sequences always fit at head_dim
+ * 64 and 128, 2000 at 256; a larger batch goes in several calls.  scale *
+ * k_scale must be finite in fp32.
  * (The workspace query has no counterpart on the pages.)
  */
 size_t paged_attention_fp4_workspace(const pa_shape *shape);
