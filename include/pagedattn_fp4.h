@@ -71,11 +71,12 @@ pa_status paged_kv_append_rope_fp4(const pa_shape *shape, const pa_rope *rope,
  *
  * k_out, v_out are [batch][max_tokens][num_kv_heads][head_dim] of the shape's
  * dtype: row t < counts[b] (counts NULL: max_tokens) gets the values of token
- * starts[b] + t, rounded once to the dtype; rows t >= counts[b] are left as
- * they were.  num_heads is not used.  counts[b] outside [0, max_tokens] gives
- * PA_DEVERR_BAD_LEN and writes nothing; starts[b] < 0 or starts[b] +
- * counts[b] past the table row gives PA_DEVERR_BAD_POS, a token whose entry
- * is outside [0, num_blocks) PA_DEVERR_BAD_BLOCK, and the rows concerned
+ * starts[b] + t: value(c) * value(s), exact, times g in IEEE binary32, then
+ * rounded to the dtype; rows t >= counts[b] are left as they were.  num_heads
+ * is not used.  counts[b] outside [0, max_tokens] gives PA_DEVERR_BAD_LEN and
+ * writes nothing; starts[b] < 0 or starts[b] + counts[b] past the table row
+ * gives PA_DEVERR_BAD_POS, a token whose entry is outside [0, num_blocks)
+ * PA_DEVERR_BAD_BLOCK, and the rows concerned
  * are zeros.  The translation is that of [BM] s5.2.
  */
 pa_status paged_kv_gather_fp4(const pa_shape *shape, void *k_out, void *v_out, int32_t max_tokens,
