@@ -1,8 +1,8 @@
-"""GPU checks of paged_kv_append_rope and its 4-bit forms where the earlier
-tests do not go: batches of so many tokens that a warp takes full runs of rows
-(8 iterations of queries, 4 of keys with their values; fp32 half of that) and
-shorter last ones; single tokens of every type; the plain 4-bit append in each
-of its forms, with counts and device errors, byte for byte."""
+"""GPU checks of paged_kv_append_rope and its 4-bit forms beyond those of
+tests/test_gpu_rope_append.py: batches of so many tokens that a warp takes full
+runs of rows (8 iterations of queries, 4 of keys with their values; fp32 half of
+that) and shorter last ones; single tokens of every type; the plain 4-bit append
+in each of its forms, with counts and device errors, byte for byte."""
 import pytest
 import torch
 
