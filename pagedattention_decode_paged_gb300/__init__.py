@@ -19,7 +19,10 @@ paged_kv_append_fp8, paged_attention_decode_fp8 (fp8 E4M3 cache with
 per-block scales), paged_kv_append_rope (per-head norm, position rotation and
 append in one pass; include/pagedattn_rope.h), paged_kv_append_fp4,
 paged_kv_append_rope_fp4, paged_attention_decode_fp4, paged_kv_gather_fp4 (the
-4-bit cache; include/pagedattn_fp4.h).
+4-bit cache; include/pagedattn_fp4.h), paged_kv_append_rope_axes (positions of
+several axes; include/pagedattn_axes.h), paged_attention_chunk,
+paged_attention_chunk_diff (attention of several new tokens per sequence, and
+its differential form; include/pagedattn_chunk.h).
 """
 from __future__ import annotations
 
@@ -51,7 +54,9 @@ EXPORTED = ("pa_status_string", "pa_version", "paged_kv_append", "paged_attentio
             "paged_attention_decode_shared_prefix", "paged_attention_decode_shared_prefix_int8",
             "paged_attention_decode_shared_prefix_fp8",
             "paged_kv_append_rope", "paged_kv_append_fp4", "paged_kv_append_rope_fp4",
-            "paged_kv_gather_fp4", "paged_attention_fp4_workspace", "paged_attention_decode_fp4")
+            "paged_kv_gather_fp4", "paged_attention_fp4_workspace", "paged_attention_decode_fp4",
+            "paged_kv_append_rope_axes", "paged_attention_chunk_workspace", "paged_attention_chunk",
+            "paged_attention_chunk_diff")
 
 
 class PagedAttnError(RuntimeError):
@@ -83,9 +88,21 @@ class NewRows(ctypes.Structure):
                 ("max_tokens", ctypes.c_int32)]
 
 
-# The three structs as bytes (a third of a Structure's time to build).
+class RopeAxes(ctypes.Structure):
+    """Mirror of pa_rope_axes."""
+    _fields_ = [("positions", ctypes.c_void_p), ("num_axes", ctypes.c_int32), ("pair_axis", ctypes.c_void_p)]
+
+
+class Diff(ctypes.Structure):
+    """Mirror of pa_diff."""
+    _fields_ = [("lambdas", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("out_scale", ctypes.c_float)]
+
+
+# The structs as bytes (a third of a Structure's time to build).
 _SHAPE, _ROPE, _ROWS = struct.Struct("@6i2qi0q"), struct.Struct("@P3i2Pf0q"), struct.Struct("@3P3qi0q")
-assert [s.size for s in (_SHAPE, _ROPE, _ROWS)] == [ctypes.sizeof(t) for t in (Shape, Rope, NewRows)]
+_DIFF = struct.Struct("@2P2f0q")
+assert [s.size for s in (_SHAPE, _ROPE, _ROWS, _DIFF)] == [ctypes.sizeof(t) for t in (Shape, Rope, NewRows, Diff)]
 
 _lock = threading.Lock()
 _lib = None
@@ -165,6 +182,16 @@ def load() -> ctypes.CDLL:
             lib.paged_attention_decode_fp4.restype = ctypes.c_int
             lib.paged_attention_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, f32, f32, vp, vp, f32, i32, vp, sz,
                                                        vp, vp]
+            lib.paged_kv_append_rope_axes.restype = ctypes.c_int
+            lib.paged_kv_append_rope_axes.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            lib.paged_attention_chunk_workspace.restype = sz
+            lib.paged_attention_chunk_workspace.argtypes = [sp]
+            lib.paged_attention_chunk.restype = ctypes.c_int
+            lib.paged_attention_chunk.argtypes = [vp, vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp, vp, f32, i32, vp, sz,
+                                                  vp, vp]
+            lib.paged_attention_chunk_diff.restype = ctypes.c_int
+            lib.paged_attention_chunk_diff.argtypes = [vp, vp, vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp, vp, f32, i32,
+                                                       vp, sz, vp, vp]
             _lib = lib
     return _lib
 
@@ -606,7 +633,7 @@ def _new_rows(what, x):
 
 def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scale, v_scale, block_table, positions,
                  counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps, block_size, num_blocks, block_stride,
-                 err_word, stream, prepare):
+                 err_word, stream, prepare, axis_positions=None, pair_axis=None):
     dt = k_new.dtype
     code = dtype_code(dt)
     B, T, Hkv, D, ks = _new_rows("k_new", k_new)
@@ -645,8 +672,13 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
     for w in (q_norm, k_norm):
         if w is not None and not (w.dtype == dt and w.is_contiguous() and w.numel() == D):
             raise ValueError(f"q_norm and k_norm must hold head_dim contiguous elements of {dt}")
+    if pair_axis is not None:
+        _dense("axis_positions", torch.int32, axis_positions)
+        A = axis_positions.shape[0]
+        if axis_positions.numel() != A * B * T or R == 0 or len(pair_axis) != R // 2:
+            raise ValueError("axis_positions must be [axes][B][T], pair_axis rotary_dim/2 axes")
     on = _launch_stream(stream, name, k_new, v_new, q, q_out, k_pool, v_pool, kv_scales, block_table, positions, counts,
-                        cos_sin, q_norm, k_norm, err_word)
+                        cos_sin, q_norm, k_norm, err_word, axis_positions)
     shape = _SHAPE.pack(B, H, Hkv, D, block_size, MB, num_blocks, block_stride, code)
     rows = _ROWS.pack(qp, k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, T)
     pools = (k_pool.data_ptr(), v_pool.data_ptr())
@@ -656,6 +688,11 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
     if name == "paged_kv_append_fp4":
         return _issue(load().paged_kv_append_fp4, (shape, rows, *pools, *tail), name, prepare)
     rope = _ROPE.pack(_addr(cos_sin) or 0, most, R, interleaved, _addr(q_norm) or 0, _addr(k_norm) or 0, eps)
+    if pair_axis is not None:
+        pairs = ctypes.create_string_buffer(bytes(pair_axis), R // 2)
+        axes = RopeAxes(axis_positions.data_ptr(), A, ctypes.addressof(pairs))
+        return _issue(load().paged_kv_append_rope_axes,
+                      (shape, rope, ctypes.byref(axes), rows, _addr(q_out), *pools, *tail), name, prepare, (axes, pairs))
     return _issue(getattr(load(), name), (shape, rope, rows, _addr(q_out), *pools, *tail), name, prepare)
 
 
@@ -670,6 +707,31 @@ def paged_kv_append_rope(q_out, q, k_new, v_new, k_pool, v_pool, block_table, po
     return _append_rows("paged_kv_append_rope", q_out, q, k_new, v_new, k_pool, v_pool, None, 1.0, 1.0, block_table,
                         positions, counts, cos_sin, rotary_dim, interleaved, q_norm, k_norm, eps, block_size,
                         num_blocks, block_stride, err_word, stream, prepare)
+
+
+def rope_axes(sections, cyclic=False) -> bytes:
+    """pair_axis of paged_kv_append_rope_axes: sections[a] pairs turn by axis a,
+    one section after another or, cyclic, the axes in turn while they have
+    pairs left."""
+    left = [int(n) for n in sections]
+    if min(left) < 0 or len(left) > 4:
+        raise ValueError("rope_axes: up to 4 sections of 0 pairs or more")
+    if not cyclic:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for i in range(max(left)) for a, n in enumerate(left) if i < n)
+
+
+def paged_kv_append_rope_axes(q_out, q, k_new, v_new, k_pool, v_pool, block_table, positions, axis_positions, cos_sin,
+                              pair_axis, *, counts=None, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+                              block_size, num_blocks, block_stride, err_word=None, stream=None, prepare=False):
+    """paged_kv_append_rope for tokens with positions on several axes: pair i
+    turns by axis_positions[pair_axis[i]] ([axes][B][T] int32); pair_axis is
+    bytes (or ints) of rotary_dim/2 axes, see rope_axes."""
+    if cos_sin is None or axis_positions is None:
+        raise ValueError("axes need cos_sin and axis_positions")
+    return _append_rows("paged_kv_append_rope_axes", q_out, q, k_new, v_new, k_pool, v_pool, None, 1.0, 1.0, block_table,
+                        positions, counts, cos_sin, None, interleaved, q_norm, k_norm, eps, block_size, num_blocks,
+                        block_stride, err_word, stream, prepare, axis_positions, pair_axis)
 
 
 def paged_kv_append_rope_fp4(q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, block_table, positions, cos_sin, *,
@@ -761,3 +823,80 @@ def paged_attention_decode_fp4(out, q, k_pool, v_pool, kv_scales, block_table, s
             v_scale, block_table.data_ptr(), seq_lens.data_ptr(), scale, window, workspace.data_ptr(), workspace.numel(),
             _addr(err_word), on)
     return _issue(load().paged_attention_decode_fp4, args, "paged_attention_decode_fp4", prepare)
+
+
+# ---------------------------------------------------------------------------
+# attention of several new tokens per sequence
+# ---------------------------------------------------------------------------
+
+def paged_attention_chunk_workspace(shape: Shape) -> int:
+    return int(load().paged_attention_chunk_workspace(ctypes.byref(shape)))
+
+
+def chunk_workspace_for(q, block_table, *, num_kv_heads, block_size, num_blocks, block_stride) -> torch.Tensor:
+    """Allocate (through torch) a workspace for paged_attention_chunk and
+    paged_attention_chunk_diff on q's device; q is [B][H][D] or [B][T][H][D]."""
+    shape = make_shape(batch=q.shape[0], num_heads=q.shape[-2], num_kv_heads=num_kv_heads, head_dim=q.shape[-1],
+                       block_size=block_size, max_blocks_per_seq=block_table.shape[1], num_blocks=num_blocks,
+                       block_stride=block_stride, dtype=q.dtype)
+    with torch.cuda.device(q.device):
+        n = paged_attention_chunk_workspace(shape)
+    if n == 0:
+        raise PagedAttnError(PA_ERR_UNSUPPORTED, "paged_attention_chunk_workspace")
+    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=q.device)
+
+
+def _attend_rows(name, out, q, k_pool, v_pool, block_table, positions, scale, workspace, counts, window, num_kv_heads,
+                 block_size, num_blocks, block_stride, err_word, stream, prepare, lambdas=None, norm=None, eps=0.0,
+                 out_scale=1.0):
+    dt = q.dtype
+    B, T, H, D, qs = _new_rows("q", q)
+    if out.numel() != B * T * H * D or out.dtype != dt or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous, with batch * tokens * heads * head_dim elements of {dt}")
+    _dense("block_table and positions", torch.int32, block_table, positions)
+    rows, MB = block_table.shape
+    if rows != B or positions.numel() != B:
+        raise ValueError("block_table and positions must have one row per sequence")
+    if counts is not None and not (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == B):
+        raise ValueError("counts must be a contiguous torch.int32 tensor with one entry per sequence")
+    _dense("workspace", torch.uint8, workspace)
+    if k_pool.dtype != dt or v_pool.dtype != dt:
+        raise ValueError("the pools must be of the queries' dtype")
+    _pools_hold(k_pool, v_pool, None, num_kv_heads, D, block_size, num_blocks, block_stride)
+    on = _launch_stream(stream, name, q, out, k_pool, v_pool, block_table, positions, counts, workspace, err_word,
+                        lambdas, norm)
+    shape = _SHAPE.pack(B, H, num_kv_heads, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
+    args = (out.data_ptr(), q.data_ptr(), qs, T, k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+            positions.data_ptr(), _addr(counts), scale, window, workspace.data_ptr(), workspace.numel(), _addr(err_word),
+            on)
+    if lambdas is None:
+        return _issue(load().paged_attention_chunk, (shape, *args), name, prepare)
+    if lambdas.dtype != torch.float32 or not lambdas.is_contiguous() or lambdas.numel() != H:
+        raise ValueError("lambdas must hold one contiguous torch.float32 element per head")
+    if norm is not None and not (norm.dtype == dt and norm.is_contiguous() and norm.numel() == D):
+        raise ValueError(f"norm must hold head_dim contiguous elements of {dt}")
+    diff = _DIFF.pack(lambdas.data_ptr(), _addr(norm) or 0, eps, out_scale)
+    return _issue(load().paged_attention_chunk_diff, (shape, diff, *args), name, prepare)
+
+
+def paged_attention_chunk(out, q, k_pool, v_pool, block_table, positions, scale, workspace, *, counts=None, window=0,
+                          num_kv_heads, block_size, num_blocks, block_stride, err_word=None, stream=None, prepare=False):
+    """out[B][T][H][D] = attention of the new tokens' queries q ([B][H][D] or
+    [B][T][H][D], a slice of a packed projection output included) over the
+    cache: token t < counts[b] (None: all T) of sequence b sees positions up to
+    its own, positions[b] + t (the last `window` of them when positive).
+    Workspace from chunk_workspace_for."""
+    return _attend_rows("paged_attention_chunk", out, q, k_pool, v_pool, block_table, positions, scale, workspace, counts,
+                        window, num_kv_heads, block_size, num_blocks, block_stride, err_word, stream, prepare)
+
+
+def paged_attention_chunk_diff(out, q, k_pool, v_pool, block_table, positions, lambdas, scale, workspace, *, counts=None,
+                               norm=None, eps=1e-5, out_scale=1.0, window=0, num_kv_heads, block_size, num_blocks,
+                               block_stride, err_word=None, stream=None, prepare=False):
+    """paged_attention_chunk with the difference of two softmax maps (queries and
+    keys of the first map in the first half of a row, of the second in the
+    second): (softmax1 - lambdas[h] softmax2) V, then the norm over the head
+    with weight norm [D] (None: none) and out_scale."""
+    return _attend_rows("paged_attention_chunk_diff", out, q, k_pool, v_pool, block_table, positions, scale, workspace,
+                        counts, window, num_kv_heads, block_size, num_blocks, block_stride, err_word, stream, prepare,
+                        lambdas, norm, eps, out_scale)

@@ -1,0 +1,159 @@
+// api_chunk.cu -- the extern "C" entry points of include/pagedattn_chunk.h:
+// host-side validation, kernel selection and launches.  Nothing here allocates
+// device memory or synchronises the host.
+#include <math.h>
+
+#include <algorithm>
+
+#include "pa_chunk.h"
+
+namespace pa {
+
+bool chunk_supported(int dtype, int head_dim, bool diff) {
+    if (dtype == PA_F32) return (head_dim == 16 && !diff) || head_dim == 32 || head_dim == 64 || head_dim == 128;
+    return head_dim == 32 || head_dim == 64 || head_dim == 128 || head_dim == 256;
+}
+
+}  // namespace pa
+
+namespace {
+
+int elem_size(int32_t dtype) { return dtype == PA_F32 ? 4 : 2; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+pa_status check_shape(const pa_shape *s, bool diff) {
+    if (s == nullptr) return PA_ERR_INVALID_ARG;
+    if (s->dtype != PA_F32 && s->dtype != PA_F16 && s->dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->num_heads <= 0 || s->num_kv_heads <= 0 || s->head_dim <= 0 || s->block_size <= 0 ||
+        s->max_blocks_per_seq <= 0 || s->num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (s->num_heads % s->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (!pa::chunk_supported(s->dtype, s->head_dim, diff)) return PA_ERR_UNSUPPORTED;
+    if (s->block_stride < (int64_t)s->num_kv_heads * s->block_size * s->head_dim) return PA_ERR_INVALID_ARG;
+    const int64_t max_len = (int64_t)s->max_blocks_per_seq * s->block_size;
+    if (max_len > INT32_MAX) return PA_ERR_INVALID_ARG;
+    if (max_len > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;   // a tile past the last position stays in int32
+    if (s->block_stride * elem_size(s->dtype) % 16 != 0) return PA_ERR_MISALIGNED;
+    return PA_OK;
+}
+
+// The kernel for a shape, and its plan on the current device.
+cudaError_t plan_of(const pa_shape *s, bool diff, pa::ChunkPlan *plan) {
+    if (s->dtype == PA_F32) return pa::plan_chunk_f32(s->head_dim, diff, plan);
+    return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, plan);
+}
+cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const pa::ChunkPlan &plan, cudaStream_t stream) {
+    if (s->dtype == PA_F32) return pa::launch_chunk_f32(s->head_dim, p, plan, stream);
+    return pa::launch_chunk_mma(s->dtype, s->head_dim, p, plan, stream);
+}
+
+// Two records per CTA, then its cut.
+size_t cuts_at(const pa::ChunkPlan &plan) { return ((size_t)2 * plan.grid * plan.rec_floats * 4 + 15) & ~(size_t)15; }
+size_t ws_bytes(const pa::ChunkPlan &plan) { return cuts_at(plan) + (size_t)plan.grid * sizeof(int4); }
+
+pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, int64_t q_stride, int32_t max_tokens,
+              const void *k_pool, const void *v_pool, const int32_t *block_table, const int32_t *positions,
+              const int32_t *counts, float scale, int32_t window, void *workspace, size_t workspace_bytes,
+              int32_t *err_word, pa_stream_t stream) {
+    pa_status st = check_shape(s, diff != nullptr);
+    if (st != PA_OK) return st;
+    if (max_tokens < 0 || window < 0 || !isfinite(scale)) return PA_ERR_INVALID_ARG;
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (!isfinite(scale_log2)) return PA_ERR_INVALID_ARG;
+    if (diff != nullptr) {
+        if (!isfinite(diff->out_scale)) return PA_ERR_INVALID_ARG;
+        if (diff->norm_weight != nullptr && !(isfinite(diff->eps) && diff->eps >= 0.f)) return PA_ERR_INVALID_ARG;
+        if (!aligned16(diff->norm_weight)) return PA_ERR_MISALIGNED;
+    }
+    const int es = elem_size(s->dtype), G = s->num_heads / s->num_kv_heads;
+    const int64_t q_row = (int64_t)s->num_heads * s->head_dim, qs = q_stride != 0 ? q_stride : q_row;
+    if (qs < q_row) return PA_ERR_INVALID_ARG;
+    if ((int64_t)s->batch * max_tokens > INT32_MAX) return PA_ERR_INVALID_ARG;
+    if ((int64_t)max_tokens * G > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;
+    if (s->batch == 0 || max_tokens == 0) return PA_OK;
+    if (out == nullptr || q == nullptr || k_pool == nullptr || v_pool == nullptr || block_table == nullptr ||
+        positions == nullptr || workspace == nullptr || (diff != nullptr && diff->lambdas == nullptr))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || qs * es % 16 != 0 || !aligned16(k_pool) || !aligned16(v_pool) ||
+        !aligned16(workspace))
+        return PA_ERR_MISALIGNED;
+    pa::ChunkPlan plan;
+    if (plan_of(s, diff != nullptr, &plan) != cudaSuccess) return PA_ERR_CUDA;
+    if (workspace_bytes < ws_bytes(plan)) return PA_ERR_WORKSPACE;
+    pa::ChunkParams p{};
+    p.q = q;
+    p.q_stride = qs;
+    p.out = out;
+    p.k_pool = static_cast<const char *>(k_pool);
+    p.v_pool = static_cast<const char *>(v_pool);
+    p.block_table = block_table;
+    p.positions = positions;
+    p.counts = counts;
+    p.err_word = err_word;
+    p.num_blocks = s->num_blocks;
+    p.block_stride_bytes = s->block_stride * es;
+    p.rows_per_block = (int32_t)(s->block_stride / s->head_dim);
+    p.B = s->batch;
+    p.T = max_tokens;
+    p.H = s->num_heads;
+    p.Hkv = s->num_kv_heads;
+    p.G = G;
+    p.MB = s->max_blocks_per_seq;
+    p.bs = s->block_size;
+    p.bs_shift = -1;
+    for (int sh = 0; sh < 31; ++sh)
+        if ((1 << sh) == s->block_size) p.bs_shift = sh;
+    p.window = window;
+    p.scale_log2 = scale_log2;
+    if (diff != nullptr) {
+        p.lambdas = diff->lambdas;
+        p.norm_weight = diff->norm_weight;
+        p.eps = diff->eps;
+        p.out_scale = diff->out_scale;
+    }
+    p.records = static_cast<float *>(workspace);
+    p.cuts = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + cuts_at(plan));
+    p.rec_floats = plan.rec_floats;
+    const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+    if (launch(s, p, plan, on) != cudaSuccess) return PA_ERR_CUDA;
+    return pa::launch_chunk_merge(s->dtype, s->head_dim, p, plan, on) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t paged_attention_chunk_workspace(const pa_shape *shape) {
+    if (check_shape(shape, false) != PA_OK || shape->batch == 0) return 0;
+    size_t n = 0;
+    for (int diff = 0; diff < 2; ++diff) {
+        pa::ChunkPlan plan;
+        if (!pa::chunk_supported(shape->dtype, shape->head_dim, diff != 0)) continue;
+        if (plan_of(shape, diff != 0, &plan) != cudaSuccess) return 0;
+        n = std::max(n, ws_bytes(plan));
+    }
+    return n;
+}
+
+pa_status paged_attention_chunk(const pa_shape *shape, void *out, const void *q, int64_t q_stride,
+                                int32_t max_tokens, const void *k_pool, const void *v_pool,
+                                const int32_t *block_table, const int32_t *positions,
+                                const int32_t *counts, float scale, int32_t window, void *workspace,
+                                size_t workspace_bytes, int32_t *err_word, pa_stream_t stream) {
+    return run(shape, nullptr, out, q, q_stride, max_tokens, k_pool, v_pool, block_table, positions, counts, scale,
+               window, workspace, workspace_bytes, err_word, stream);
+}
+
+pa_status paged_attention_chunk_diff(const pa_shape *shape, const pa_diff *diff, void *out,
+                                     const void *q, int64_t q_stride, int32_t max_tokens,
+                                     const void *k_pool, const void *v_pool,
+                                     const int32_t *block_table, const int32_t *positions,
+                                     const int32_t *counts, float scale, int32_t window,
+                                     void *workspace, size_t workspace_bytes, int32_t *err_word,
+                                     pa_stream_t stream) {
+    if (diff == nullptr) return PA_ERR_INVALID_ARG;
+    return run(shape, diff, out, q, q_stride, max_tokens, k_pool, v_pool, block_table, positions, counts, scale, window,
+               workspace, workspace_bytes, err_word, stream);
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
-// api_rope_fp4.cu -- the extern "C" entry points of include/pagedattn_rope.h
-// and include/pagedattn_fp4.h: host-side validation and launches.  Nothing
+// api_rope_fp4.cu -- the extern "C" entry points of include/pagedattn_rope.h,
+// include/pagedattn_axes.h and include/pagedattn_fp4.h: host-side validation and launches.  Nothing
 // here allocates device memory or synchronises the host.
 #include <math.h>
 
@@ -49,9 +49,10 @@ pa_status check_fp4_shape(const pa_shape *s, bool grouped) {
     return grouped && s->num_heads % s->num_kv_heads != 0 ? PA_ERR_INVALID_ARG : PA_OK;
 }
 
-// The append entry points: `rope` null without norm and rotation, `fp4` the
-// 4-bit cache (kv_scales, k_g, v_g).
-pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows, bool with_q, void *q_out,
+// The append entry points: `rope` null without norm and rotation, `axes` null
+// for positions of one axis, `fp4` the 4-bit cache (kv_scales, k_g, v_g).
+pa_status append(const pa_shape *s, const pa_rope *rope, const pa_rope_axes *axes, const pa_new_rows *rows, bool with_q,
+                 void *q_out,
                  void *k_pool, void *v_pool, bool fp4, uint8_t *kv_scales, float k_g, float v_g,
                  const int32_t *block_table, const int32_t *positions, const int32_t *counts, int32_t *err_word,
                  pa_stream_t stream) {
@@ -74,6 +75,12 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
         if (!aligned16(rope->cos_sin) || !aligned16(rope->q_weight) || !aligned16(rope->k_weight))
             return PA_ERR_MISALIGNED;
     }
+    if (axes != nullptr) {
+        if (rope->rotary_dim == 0 || axes->num_axes < 1 || axes->num_axes > 4 || axes->pair_axis == nullptr)
+            return PA_ERR_INVALID_ARG;
+        for (int i = 0; i < rope->rotary_dim / 2; ++i)
+            if (axes->pair_axis[i] >= axes->num_axes) return PA_ERR_INVALID_ARG;
+    }
     if (fp4 && (!factor_ok(k_g) || !factor_ok(v_g))) return PA_ERR_INVALID_ARG;
     const int es = elem_size(s->dtype);
     const bool q = with_q && rows->q != nullptr;
@@ -85,7 +92,8 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
     if ((int64_t)s->batch * rows->max_tokens > INT32_MAX) return PA_ERR_INVALID_ARG;
     if (s->batch == 0 || rows->max_tokens == 0) return PA_OK;
     if (rows->k == nullptr || rows->v == nullptr || k_pool == nullptr || v_pool == nullptr ||
-        block_table == nullptr || positions == nullptr || (q && q_out == nullptr) || (fp4 && kv_scales == nullptr))
+        block_table == nullptr || positions == nullptr || (q && q_out == nullptr) || (fp4 && kv_scales == nullptr) ||
+        (axes != nullptr && axes->positions == nullptr))
         return PA_ERR_INVALID_ARG;
     if ((q && (!aligned16(rows->q) || !aligned16(q_out) || qs * es % 16 != 0)) || !aligned16(rows->k) ||
         !aligned16(rows->v) || ks * es % 16 != 0 || vs * es % 16 != 0 || !aligned16(k_pool) || !aligned16(v_pool) ||
@@ -126,6 +134,14 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_new_rows *rows
     }
     p.k_g = k_g;
     p.v_g = v_g;
+    if (axes != nullptr) {
+        p.axis_positions = axes->positions;
+        p.axes = axes->num_axes;
+        for (int i = 0; i < rope->rotary_dim / 2; ++i) p.pair_axis[i / 4] |= (uint8_t)(axes->pair_axis[i] << 2 * (i % 4));
+        return pa::launch_rope_append_axes(s->dtype, s->head_dim, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     return pa::launch_rope_append(s->dtype, s->head_dim, fp4, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -168,7 +184,16 @@ pa_status paged_kv_append_rope(const pa_shape *shape, const pa_rope *rope, const
                                const int32_t *block_table, const int32_t *positions,
                                const int32_t *counts, int32_t *err_word, pa_stream_t stream) {
     if (rope == nullptr) return PA_ERR_INVALID_ARG;
-    return append(shape, rope, rows, true, q_out, k_pool, v_pool, false, nullptr, 1.f, 1.f, block_table, positions,
+    return append(shape, rope, nullptr, rows, true, q_out, k_pool, v_pool, false, nullptr, 1.f, 1.f, block_table, positions,
+                  counts, err_word, stream);
+}
+
+pa_status paged_kv_append_rope_axes(const pa_shape *shape, const pa_rope *rope, const pa_rope_axes *axes,
+                                    const pa_new_rows *rows, void *q_out, void *k_pool, void *v_pool,
+                                    const int32_t *block_table, const int32_t *positions,
+                                    const int32_t *counts, int32_t *err_word, pa_stream_t stream) {
+    if (rope == nullptr || axes == nullptr) return PA_ERR_INVALID_ARG;
+    return append(shape, rope, axes, rows, true, q_out, k_pool, v_pool, false, nullptr, 1.f, 1.f, block_table, positions,
                   counts, err_word, stream);
 }
 
@@ -176,7 +201,7 @@ pa_status paged_kv_append_fp4(const pa_shape *shape, const pa_new_rows *rows, ui
                               uint8_t *v_pool, uint8_t *kv_scales, float k_scale, float v_scale,
                               const int32_t *block_table, const int32_t *positions,
                               const int32_t *counts, int32_t *err_word, pa_stream_t stream) {
-    return append(shape, nullptr, rows, false, nullptr, k_pool, v_pool, true, kv_scales, k_scale, v_scale,
+    return append(shape, nullptr, nullptr, rows, false, nullptr, k_pool, v_pool, true, kv_scales, k_scale, v_scale,
                   block_table, positions, counts, err_word, stream);
 }
 
@@ -187,7 +212,7 @@ pa_status paged_kv_append_rope_fp4(const pa_shape *shape, const pa_rope *rope,
                                    const int32_t *positions, const int32_t *counts,
                                    int32_t *err_word, pa_stream_t stream) {
     if (rope == nullptr) return PA_ERR_INVALID_ARG;
-    return append(shape, rope, rows, true, q_out, k_pool, v_pool, true, kv_scales, k_scale, v_scale, block_table,
+    return append(shape, rope, nullptr, rows, true, q_out, k_pool, v_pool, true, kv_scales, k_scale, v_scale, block_table,
                   positions, counts, err_word, stream);
 }
 

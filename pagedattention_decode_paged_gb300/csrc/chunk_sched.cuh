@@ -1,0 +1,298 @@
+// chunk_sched.cuh -- the schedule of attention of several new tokens, and the
+// last step of a row.
+//
+// The query rows of a (sequence, kv head) are numbered token by token, the G
+// heads of the group beside one another: row n is head n % G of token n / G.
+// An item is R consecutive rows of them (the last may have fewer) with the
+// tiles of KT cache positions that its tokens attend to.  Laid end to end,
+// sequence by sequence, head by head and item by item, the tiles of all items
+// form one index space [0, total); CTA w of W takes the slice [w*total/W,
+// (w+1)*total/W), the same number of tiles whatever the mix of lengths.
+//
+// An item cut by slice ends is shared by consecutive CTAs.  Each publishes the
+// softmax state of its share (per row the running maximum, the running sum
+// and the weighted sum of V: what the per-block aggregation of "KV Cache
+// paging in LLM inference", intelliparadigm.com, s2.2, carries from block to
+// block) as a record, slot 0 if the share ends the slice's first item, slot 1
+// if it begins an item that goes on in the next slice; and CTA w writes
+// cuts[w]: which item its slice begins inside of, if that item's first tile
+// belongs to the slice before, and the last CTA that shares it.  The second
+// launch joins them.  No CTA waits for another.
+//
+// The counts and positions are on the device, so every CTA builds the sums over
+// sequences itself.  How many tiles the first items of a sequence have is in
+// closed form a sum of floor((a i + b) / m).
+#pragma once
+
+#include "pa_chunk.h"
+#include "pa_device.cuh"
+
+namespace pa {
+namespace chunk {
+
+constexpr int kGroups = 1024;              // sums over sequences kept in shared memory
+
+// One item and the share [k0, k1) of its tiles that this CTA takes.
+struct Item {
+    int b, hk, i;              // sequence, kv head, item of the head
+    int pos, cnt, nq;          // of the sequence: position of its first new token, new tokens, items per head
+    int lo, n;                 // first tile of cache positions, tiles
+    int k0, k1;
+};
+
+// New tokens of sequence b and where they start; 0 when there is nothing to do
+// or an argument is out of range (*error: the PA_DEVERR bit).
+__device__ __forceinline__ int seq_of(const ChunkParams &p, int b, int *pos, int *error) {
+    const int cnt = p.counts != nullptr ? __ldg(p.counts + b) : p.T;
+    *pos = __ldg(p.positions + b);
+    *error = 0;
+    if (cnt < 0 || cnt > p.T) {
+        *error = PA_DEVERR_BAD_LEN;
+        return 0;
+    }
+    if (*pos < 0 || (int64_t)*pos + cnt > (int64_t)p.MB * p.bs) {
+        *error = PA_DEVERR_BAD_POS;
+        return 0;
+    }
+    return cnt;
+}
+
+// sum over i < n of floor((a i + b) / m)
+__device__ __forceinline__ int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
+    uint64_t s = 0;
+    for (;;) {
+        if (a >= m) {
+            s += (n * (n - 1) / 2) * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            s += n * (b / m);
+            b %= m;
+        }
+        const uint64_t y = a * n + b;
+        if (y < m) return (int64_t)s;
+        n = y / m;
+        b = y % m;
+        const uint64_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+template <int R, int KT>
+struct Sched {
+    // tiles of item i
+    static __device__ __forceinline__ int tiles(const ChunkParams &p, int pos, int cnt, int i, int *lo) {
+        const uint32_t rows = (uint32_t)cnt * (uint32_t)p.G, r0 = (uint32_t)i * R;
+        const uint32_t last = min(r0 + (uint32_t)R, rows) - 1;
+        const int hi = (int)((uint32_t)pos + last / (uint32_t)p.G) / KT;
+        *lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos + r0 / (uint32_t)p.G - p.window + 1) / KT : 0;
+        return hi - *lo + 1;
+    }
+    static __device__ __forceinline__ int items(const ChunkParams &p, int cnt) {
+        return (int)(((int64_t)cnt * p.G + R - 1) / R);
+    }
+    // tiles of the first n items of the nq of a head
+    static __device__ __forceinline__ int64_t tiles_before(const ChunkParams &p, int pos, int cnt, int nq, int n) {
+        int64_t s = 0;
+        int lo;
+        if (n <= 4) {
+            for (int i = 0; i < n; ++i) s += tiles(p, pos, cnt, i, &lo);
+            return s;
+        }
+        if (n == nq) s += tiles(p, pos, cnt, --n, &lo);   // the last may have fewer rows
+        const uint64_t m = (uint64_t)p.G * KT;
+        s += n + floor_sum(n, m, R, (uint64_t)pos * p.G + (R - 1));
+        if (p.window > 0) {
+            // items whose first token's window begins past position 0
+            const int64_t b = ((int64_t)pos - p.window + 1) * p.G;
+            const int64_t skip = b >= 0 ? 0 : (-b + R - 1) / R;
+            if (skip < n) s -= floor_sum(n - skip, m, R, skip * R + b);
+        }
+        return s;
+    }
+
+    int64_t at, end;           // tile of the current share's first tile, end of the slice
+    Item x;
+    int64_t first;             // the current item's first tile
+
+    // Sums over groups of sequences; pre: [kGroups + 1] in shared memory.  All
+    // threads of the CTA call it; it ends with a barrier.  Returns the sequences
+    // of a group.
+    static __device__ __forceinline__ int build(const ChunkParams &p, int64_t *pre) {
+        const int per = (p.B + kGroups - 1) / kGroups, groups = (p.B + per - 1) / per;
+        for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+            int64_t s = 0;
+            for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) {
+                int pos, error;
+                const int cnt = seq_of(p, b, &pos, &error);
+                if (cnt > 0) {
+                    const int nq = items(p, cnt);
+                    s += p.Hkv * tiles_before(p, pos, cnt, nq, nq);
+                }
+            }
+            pre[g + 1] = s;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {                    // inclusive sums, 32 at a time
+            int64_t run = 0;
+            for (int g0 = 0; g0 < groups; g0 += 32) {
+                const int g = g0 + threadIdx.x;
+                int64_t v = g < groups ? pre[g + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                    if ((int)threadIdx.x >= o) v += y;
+                }
+                if (g < groups) pre[g + 1] = run + v;
+                run += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (threadIdx.x == 0) pre[0] = 0;
+        }
+        __syncthreads();
+        return per;
+    }
+
+    __device__ __forceinline__ void load_seq(const ChunkParams &p, int b) {
+        int error;
+        x.b = b;
+        x.cnt = seq_of(p, b, &x.pos, &error);
+        x.nq = x.cnt > 0 ? items(p, x.cnt) : 0;
+    }
+    __device__ __forceinline__ void share(const ChunkParams &p) {
+        x.n = tiles(p, x.pos, x.cnt, x.i, &x.lo);
+        x.k0 = (int)(at - first);
+        x.k1 = (int)min((int64_t)x.n, end - first);
+    }
+    // The first share of slice [begin, finish), which is not empty.
+    __device__ __forceinline__ void seek(const ChunkParams &p, const int64_t *pre, int per, int64_t begin, int64_t finish) {
+        at = begin;
+        end = finish;
+        int lo = 0, hi = (p.B + per - 1) / per;    // pre[lo] <= at < pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        int64_t off = at - pre[lo], head = 0;
+        int b = lo * per;
+        for (;; ++b) {
+            load_seq(p, b);
+            if (x.cnt == 0) continue;
+            head = tiles_before(p, x.pos, x.cnt, x.nq, x.nq);
+            if (off < head * p.Hkv) break;
+            off -= head * p.Hkv;
+        }
+        x.hk = (int)(off / head);
+        off -= x.hk * head;
+        int i0 = 0, i1 = x.nq;                     // tiles_before(i0) <= off < tiles_before(i1)
+        int64_t before = 0;
+        while (i1 - i0 > 1) {
+            const int mid = (i0 + i1) >> 1;
+            const int64_t v = tiles_before(p, x.pos, x.cnt, x.nq, mid);
+            if (v <= off) i0 = mid, before = v;
+            else i1 = mid;
+        }
+        x.i = i0;
+        first = at - (off - before);
+        share(p);
+    }
+    // The next share of the slice; false at its end.
+    __device__ __forceinline__ bool next(const ChunkParams &p) {
+        at = first + x.n;
+        if (at >= end) return false;
+        first = at;
+        if (++x.i == x.nq) {
+            x.i = 0;
+            if (++x.hk == p.Hkv) {
+                x.hk = 0;
+                do load_seq(p, x.b + 1);
+                while (x.cnt == 0);
+            }
+        }
+        share(p);
+        return true;
+    }
+    __device__ __forceinline__ bool cut() const { return x.k0 > 0 || x.k1 < x.n; }
+};
+
+// Working CTAs of the grid: no more than there are tiles.
+__device__ __forceinline__ int working(int64_t total, int grid) { return (int)min((int64_t)grid, total); }
+__device__ __forceinline__ int64_t slice_begin(int w, int64_t total, int W) { return w * total / W; }
+__device__ __forceinline__ int slice_owner(int64_t t, int64_t total, int W) { return (int)(((t + 1) * W - 1) / total); }
+
+// This CTA's entry of the cuts, from the first share of its slice (has: it has
+// one).  x: item's sequence (-1: nothing begins to be joined here), kv head,
+// item of the head, last CTA that shares it.
+template <int R, int KT>
+__device__ __forceinline__ int4 cut_entry(const Sched<R, KT> &s, bool has, int64_t total, int W) {
+    if (!has || s.x.k0 == 0 || s.first < slice_begin((int)blockIdx.x - 1, total, W)) return make_int4(-1, 0, 0, 0);
+    return make_int4(s.x.b, s.x.hk, s.x.i, slice_owner(s.first + s.x.n - 1, total, W));
+}
+
+// Report sequences whose arguments are out of range, and zero the rows of
+// those whose positions are; sequence b is CTA b % gridDim's.
+template <typename T>
+__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D) {
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        int pos, error;
+        seq_of(p, b, &pos, &error);
+        if (error == 0) continue;
+        if (threadIdx.x == 0) report(p.err_word, error);
+        if (error != PA_DEVERR_BAD_POS) continue;
+        const int cnt = p.counts != nullptr ? p.counts[b] : p.T;
+        const int64_t row = (int64_t)p.H * D, n = cnt * row;
+        T *out = reinterpret_cast<T *>(p.out) + (int64_t)b * p.T * row;
+        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) out[i] = Elem<T>::from_float(0.f);
+    }
+}
+
+// Byte offset in the pools of the row that holds cache position t of kv head
+// hk of sequence b, or -1 when its table entry is out of range.
+__device__ __forceinline__ int64_t row_offset(const ChunkParams &p, int b, int hk, int t, int row_bytes) {
+    const int j = p.bs_shift >= 0 ? t >> p.bs_shift : t / p.bs;
+    const int32_t blk = __ldg(p.block_table + (int64_t)b * p.MB + j);
+    if (blk < 0 || blk >= p.num_blocks) return -1;
+    return blk * p.block_stride_bytes + ((int64_t)hk * p.bs + (t - j * p.bs)) * row_bytes;
+}
+
+// The last step of a row, by one warp: lane l has elements l*N .. l*N + N - 1
+// (N = D / 32, or one element for the first D lanes) of the first map's
+// weighted sum in o, already divided by its sum, and of the second map's in o2
+// (differential form).  A row that attended to a bad block is zeros.
+template <typename T, int D, bool DIFF>
+__device__ __forceinline__ void finish_row(const ChunkParams &p, const float *o, const float *o2, bool bad, int64_t token,
+                                           int head) {
+    constexpr int N = D >= 32 ? D / 32 : 1;
+    const int lane = threadIdx.x & 31;
+    float y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = o[i];
+    if constexpr (DIFF) {
+        const float lam = __ldg(p.lambdas + head);
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            y[i] -= lam * o2[i];
+            sq += y[i] * y[i];
+        }
+        if (p.norm_weight != nullptr) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+            const float r = 1.f / sqrtf(sq * (1.f / D) + p.eps);
+            const T *w = reinterpret_cast<const T *>(p.norm_weight) + lane * N;
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] = y[i] * r * Elem<T>::to_float(w[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] *= p.out_scale;
+    }
+    T *dst = reinterpret_cast<T *>(p.out) + (token * p.H + head) * D + lane * N;
+    if (D >= 32 || lane < D) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i] = Elem<T>::from_float(bad ? 0.f : y[i]);
+    }
+}
+
+}  // namespace chunk
+}  // namespace pa

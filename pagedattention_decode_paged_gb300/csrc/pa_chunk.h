@@ -1,0 +1,60 @@
+// pa_chunk.h -- parameter block and launchers of attention of several new
+// tokens per sequence (include/pagedattn_chunk.h), shared between the C-ABI
+// layer (api_chunk.cu) and the kernel translation units.
+#pragma once
+
+#include "pa_internal.h"
+#include "pagedattn_chunk.h"
+
+namespace pa {
+
+struct ChunkParams {
+    const void *q;
+    int64_t q_stride;          // elements from token row to token row
+    void *out;                 // [B][T][H][D]
+    const char *k_pool;
+    const char *v_pool;
+    const int32_t *block_table;
+    const int32_t *positions;
+    const int32_t *counts;     // null: T for every sequence
+    int32_t *err_word;
+    int64_t num_blocks;
+    int64_t block_stride_bytes;
+    int32_t rows_per_block;    // block_stride / head_dim (tensor-map row pitch per block)
+    int32_t B, T, H, Hkv, G, MB, bs;   // G = H / Hkv
+    int32_t bs_shift;          // log2(bs) when bs is a power of two, else -1
+    int32_t window;
+    float scale_log2;          // scale * log2(e)
+    // differential form: lambdas not null
+    const float *lambdas;
+    const void *norm_weight;
+    float eps;
+    float out_scale;
+    // workspace: per CTA two records of the rows' softmax states, and one cut
+    float *records;
+    int4 *cuts;
+    int32_t rec_floats;
+};
+
+// What a kernel variant needs of the workspace on the current device.
+struct ChunkPlan {
+    int grid = 0;
+    int rows = 0;              // query rows of an item (of each map)
+    int maps = 1;
+    int rec_floats = 0;        // floats of a record: rows * maps of head_dim, their maxima and their sums
+};
+inline int chunk_rec_floats(int rows_all_maps, int head_dim) { return rows_all_maps * (head_dim + 2); }
+
+bool chunk_supported(int dtype, int head_dim, bool diff);
+
+// fp32 on the CUDA cores, 16-bit on mma.sync (any block size).
+cudaError_t plan_chunk_f32(int head_dim, bool diff, ChunkPlan *plan);
+cudaError_t launch_chunk_f32(int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
+cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
+cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
+
+// Join the rows that the attention kernel of `plan` left in records.
+cudaError_t launch_chunk_merge(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan,
+                               cudaStream_t stream);
+
+}  // namespace pa
