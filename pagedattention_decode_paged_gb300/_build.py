@@ -24,8 +24,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "append.cu", "decode_simt.cu", "decode_gqa_tc.cu", "decode_balanced_simt.cu",
            "decode_balanced_tc.cu", "decode_int8.cu", "decode_prefix_tc.cu", "reduce.cu",
            "decode_int8_tc.cu", "decode_gqa_umma.cu", "append_rope.cu", "gather_fp4.cu", "decode_fp4.cu",
-           "api_rope_fp4.cu", "append_axes.cu", "chunk_mma.cu", "chunk_f32.cu", "chunk_merge.cu",
-           "api_chunk.cu"]
+           "api_rope_fp4.cu", "append_axes.cu", "chunk_umma.cu", "chunk_mma.cu", "chunk_f32.cu",
+           "chunk_merge.cu", "api_chunk.cu"]
 
 
 def _nvcc() -> str:

@@ -4,8 +4,8 @@
 #include <math.h>
 #include <mutex>
 
+#include "pa_chunk.h"
 #include "pa_device.cuh"
-#include "pa_internal.h"
 
 namespace {
 
@@ -497,6 +497,14 @@ BalWs balanced_ws(const pa::BalancedPlan &plan) {
 }
 
 }  // namespace
+
+namespace pa {
+
+bool chunk_pool_map(CUtensorMap *map, const pa_shape *s, const void *pool, int box_rows) {
+    return cached_pool_map(map, s, pool, false, box_rows, s->head_dim == 128 ? 2 : 0);
+}
+
+}  // namespace pa
 
 extern "C" {
 

@@ -37,14 +37,46 @@ pa_status check_shape(const pa_shape *s, bool diff) {
     return PA_OK;
 }
 
-// The kernel for a shape, and its plan on the current device.
-cudaError_t plan_of(const pa_shape *s, bool diff, pa::ChunkPlan *plan) {
-    if (s->dtype == PA_F32) return pa::plan_chunk_f32(s->head_dim, diff, plan);
-    return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, plan);
+// Rows of the tcgen05 kernel's boxes: what divides a tile of 128 positions and a
+// block; 0 where the pool does not fit them (rows of a block in whole groups of
+// 8, TMA row coordinates in int32).
+int umma_box_rows(const pa_shape *s) {
+    if (!pa::chunk_umma_supported(s->dtype, s->head_dim) || s->block_size % 8 != 0) return 0;
+    if (s->block_stride % (8 * s->head_dim) != 0) return 0;
+    if (s->num_blocks > (int64_t)INT32_MAX / (s->block_stride / s->head_dim)) return 0;
+    int rows = 128;
+    while (s->block_size % rows != 0) rows /= 2;
+    return rows;
 }
-cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const pa::ChunkPlan &plan, cudaStream_t stream) {
-    if (s->dtype == PA_F32) return pa::launch_chunk_f32(s->head_dim, p, plan, stream);
-    return pa::launch_chunk_mma(s->dtype, s->head_dim, p, plan, stream);
+
+// The kernel for a call, and its plan on the current device.
+enum Kernel { kF32, kMma, kUmma };
+struct Choice {
+    Kernel kernel;
+    int box_rows = 0;
+    pa::ChunkPlan plan;
+};
+cudaError_t choose(const pa_shape *s, bool diff, float scale_log2, Choice *c) {
+    if (s->dtype == PA_F32) {
+        c->kernel = kF32;
+        return pa::plan_chunk_f32(s->head_dim, diff, &c->plan);
+    }
+    c->box_rows = umma_box_rows(s);
+    // the tcgen05 kernel takes the maximum before it scales
+    if (c->box_rows > 0 && scale_log2 > 0.f) {
+        c->kernel = kUmma;
+        return pa::plan_chunk_umma(s->dtype, s->head_dim, diff, &c->plan);
+    }
+    c->kernel = kMma;
+    return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, &c->plan);
+}
+cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const Choice &c, cudaStream_t stream) {
+    if (c.kernel == kF32) return pa::launch_chunk_f32(s->head_dim, p, c.plan, stream);
+    if (c.kernel == kMma) return pa::launch_chunk_mma(s->dtype, s->head_dim, p, c.plan, stream);
+    CUtensorMap kmap, vmap;
+    if (!pa::chunk_pool_map(&kmap, s, p.k_pool, c.box_rows) || !pa::chunk_pool_map(&vmap, s, p.v_pool, c.box_rows))
+        return cudaErrorInvalidValue;
+    return pa::launch_chunk_umma(s->dtype, s->head_dim, p, kmap, vmap, c.box_rows, c.plan, stream);
 }
 
 // Two records per CTA, then its cut.
@@ -77,8 +109,9 @@ pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, 
     if (!aligned16(out) || !aligned16(q) || qs * es % 16 != 0 || !aligned16(k_pool) || !aligned16(v_pool) ||
         !aligned16(workspace))
         return PA_ERR_MISALIGNED;
-    pa::ChunkPlan plan;
-    if (plan_of(s, diff != nullptr, &plan) != cudaSuccess) return PA_ERR_CUDA;
+    Choice c;
+    if (choose(s, diff != nullptr, scale_log2, &c) != cudaSuccess) return PA_ERR_CUDA;
+    const pa::ChunkPlan &plan = c.plan;
     if (workspace_bytes < ws_bytes(plan)) return PA_ERR_WORKSPACE;
     pa::ChunkParams p{};
     p.q = q;
@@ -115,7 +148,7 @@ pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, 
     p.cuts = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + cuts_at(plan));
     p.rec_floats = plan.rec_floats;
     const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
-    if (launch(s, p, plan, on) != cudaSuccess) return PA_ERR_CUDA;
+    if (launch(s, p, c, on) != cudaSuccess) return PA_ERR_CUDA;
     return pa::launch_chunk_merge(s->dtype, s->head_dim, p, plan, on) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -126,11 +159,11 @@ extern "C" {
 size_t paged_attention_chunk_workspace(const pa_shape *shape) {
     if (check_shape(shape, false) != PA_OK || shape->batch == 0) return 0;
     size_t n = 0;
-    for (int diff = 0; diff < 2; ++diff) {
-        pa::ChunkPlan plan;
-        if (!pa::chunk_supported(shape->dtype, shape->head_dim, diff != 0)) continue;
-        if (plan_of(shape, diff != 0, &plan) != cudaSuccess) return 0;
-        n = std::max(n, ws_bytes(plan));
+    for (int i = 0; i < 4; ++i) {              // with and without a second map, scales of either sign
+        Choice c;
+        if (!pa::chunk_supported(shape->dtype, shape->head_dim, i % 2 != 0)) continue;
+        if (choose(shape, i % 2 != 0, i < 2 ? 1.f : -1.f, &c) != cudaSuccess) return 0;
+        n = std::max(n, ws_bytes(c.plan));
     }
     return n;
 }

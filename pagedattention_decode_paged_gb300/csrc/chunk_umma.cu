@@ -1,0 +1,782 @@
+// chunk_umma.cu -- attention of several new tokens on the fifth-generation
+// tensor cores (tcgen05.mma, scores, weights and outputs in tensor memory),
+// 16-bit types, head_dim 64 and 128, blocks of a multiple of 8 tokens.
+//
+// An item is 256 query rows in two tiles of 128 (in the differential form 128
+// rows, a tile for each map), a step a tile of 128 cache positions:
+//     S_s = Q_s K^T                M = 128 rows, N = 128 positions, K = head_dim
+//     O_s += P_s V                 M = 128 rows, N = head_dim, K = 128 positions
+// with P_s = 2^(scale log2(e) (S_s - m)) by the 128 threads of tile s, a row
+// each, between the two.  K and V arrive by TMA as 128-byte swizzled rows, K the
+// K-major B operand of the first product, V the MN-major B operand of the
+// second; P is the A operand of the second in tensor memory, over the columns
+// that S had.  While the threads of one tile take the exponentials of a step the
+// tensor core multiplies for the other.
+//
+// Roles (512 threads): warps 0-3 and 4-7 the rows of tile 0 and 1; warp 8 the
+// copies of K and V; warp 9 the products (one thread) and tensor memory; warps 10
+// and 11 the query rows; warps 12-15 look over those V tiles that not all rows
+// see alike: positions that no row sees become zeros, and where another is not
+// finite the rows' threads weigh that tile's values one by one, each only
+// those it sees (the product would let 0 times them reach every row).
+//
+// m is the maximum at the time it was last taken: O is rescaled only when a row's
+// maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
+// of a row above 1.
+#include "chunk_sched.cuh"
+#include "umma.cuh"
+
+namespace pa {
+
+namespace {
+
+using namespace chunk;
+
+constexpr int kThreads = 512;
+constexpr int kKT = 128;                   // cache positions per tile
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kFixWarp = 12;
+constexpr float kLazy = 8.f;
+constexpr int kBadRing = 8;
+
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ bool non_finite(uint32_t w) {   // of either half
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// 128-byte swizzled rows: K and V tiles are [16 groups of 8 rows][D/64][8 rows]
+// [128 bytes], query tiles [E/64 or 1][128 rows][128 bytes].
+template <int D, bool DIFF>
+struct Layout {
+    static constexpr int E = DIFF ? D / 2 : D;
+    static constexpr uint32_t kGroup = 8 * D * 2;             // 8 rows of K or V
+    static constexpr uint32_t kTile = kKT * D * 2;
+    static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 4;   // tiles in flight or waiting
+    static constexpr uint32_t kQSlab = 128 * 128;
+    static constexpr uint32_t kQTile = (E <= 64 ? 1 : E / 64) * kQSlab;
+    static constexpr uint32_t kQ = 0;                         // two query tiles
+    static constexpr uint32_t kKRing = 2 * kQTile, kVRing = kKRing + kK * kTile;
+    static constexpr uint32_t kBars = kVRing + kV * kTile;
+    enum {
+        K_FULL = 0,                // [kK] the tile's copies have landed
+        K_EMPTY = K_FULL + kK,     // [kK] the products that read it are done
+        V_FULL = K_EMPTY + kK,     // [kV]
+        V_EMPTY = V_FULL + kV,     // [kV]
+        READY = V_EMPTY + kV,      // [kV] the tile has been looked over
+        S_FULL = READY + kV,       // [2] scores
+        P_FULL = S_FULL + 2,       // [2] weights
+        O_DONE = P_FULL + 2,       // [2] last product of an item
+        O_FREE = O_DONE + 2,       // [2] its result has been read
+        Q_FULL = O_FREE + 2,       // [2] query rows
+        Q_FREE = Q_FULL + 2,       // [2]
+        PAIR = Q_FREE + 2,         // differential form: the threads of both tiles
+        END = PAIR + 1,
+        NBARS = END + 1
+    };
+    static constexpr uint32_t kTmem = kBars + NBARS * 8;
+    static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
+    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][4] a V tile's 32 rows are not all finite
+    static constexpr uint32_t kSched = kOdd + kBadRing * 16;
+    static constexpr uint32_t kPair = kSched + 128;           // differential form: [2][128] sums, then squares
+    static constexpr uint32_t kEnd = kPair + (DIFF ? 2 * 128 * 4 : 0);
+    static constexpr uint32_t kPre = kKRing;                  // before the first copy
+    static constexpr size_t kBytes = 1024 + kEnd;
+    static constexpr uint32_t kColS = 0, kColO = 256;         // S_s at 128 s, O_s at 256 + D s
+    static_assert(kBytes <= 232448, "shared memory per CTA");
+    static_assert((kGroups + 1) * 8 <= kK * kTile, "the sums fit the ring");
+};
+
+// The two tiles of a share: which steps each takes part in, and what its rows see.
+template <bool DIFF>
+struct Share {
+    int n0, nrows;             // first row, rows of the item
+    int need_lo, need_hi;      // positions that some row sees
+    int a[2], e[2];            // steps of each tile (in tiles of the item)
+    int t_first[2], t_last[2]; // tokens of its first and last row
+    __device__ __forceinline__ Share(const ChunkParams &p, const Item &x) {
+        constexpr int R = DIFF ? 128 : 256;
+        n0 = x.i * R;
+        nrows = min(R, x.cnt * p.G - n0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r0 = DIFF ? 0 : s * 128, nr = min(128, nrows - r0);
+            if (nr <= 0) {
+                a[s] = e[s] = 0;
+                t_first[s] = t_last[s] = t_last[0];
+                continue;
+            }
+            t_first[s] = (n0 + r0) / p.G;
+            t_last[s] = (n0 + r0 + nr - 1) / p.G;
+            const int lo = p.window > 0 ? max(0, x.pos + t_first[s] - p.window + 1) / kKT : 0;
+            a[s] = max(x.k0, lo - x.lo);
+            e[s] = min(x.k1, (x.pos + t_last[s]) / kKT + 1 - x.lo);
+        }
+        need_lo = p.window > 0 ? max(0, x.pos + t_first[0] - p.window + 1) : 0;
+        need_hi = x.pos + t_last[1];
+    }
+    __device__ __forceinline__ int begin(int s) const { return s ? a[1] : a[0]; }
+    __device__ __forceinline__ int finish(int s) const { return s ? e[1] : e[0]; }
+    __device__ __forceinline__ bool active(int s, int k) const { return k >= begin(s) && k < finish(s); }
+    // not all rows of tiles [s, last] see all positions of step k
+    __device__ __forceinline__ bool partial(const ChunkParams &p, const Item &x, int k, int s, int last) const {
+        const int t0 = (x.lo + k) * kKT;
+        return t0 + kKT - 1 > x.pos + (s ? t_first[1] : t_first[0]) || (p.window > 0 && t0 < x.pos + (last ? t_last[1] : t_last[0]) - p.window + 1);
+    }
+};
+
+}  // namespace
+
+template <typename T, int D, bool DIFF>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_umma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ ChunkParams p, const int box_rows) {
+    using L = Layout<D, DIFF>;
+    constexpr int E = L::E, R = DIFF ? 128 : 256;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kIdescS = f16_idesc(kBf16, false, false, 128, kKT);
+    constexpr uint32_t kIdescO = f16_idesc(kBf16, false, true, 128, D);
+    using Schedule = Sched<R, kKT>;
+    grid_dependency_wait();
+    allow_dependents();
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + L::kBars + i * 8; };
+    volatile uint32_t *badm = reinterpret_cast<volatile uint32_t *>(smem + L::kBad);
+    volatile uint32_t *oddm = reinterpret_cast<volatile uint32_t *>(smem + L::kOdd);
+    auto odd_tile = [&](uint32_t step) {
+        const volatile uint32_t *o = oddm + step % kBadRing * 4;
+        return (o[0] | o[1] | o[2] | o[3]) != 0;
+    };
+    int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::NBARS; ++i) {
+            int count = 1;
+            if (i >= L::READY && i < L::S_FULL) count = 4;            // the looking warps
+            if (i == L::S_FULL || i == L::S_FULL + 1) count = 2;      // the products, and what their warp knows
+            if (i == L::P_FULL || i == L::P_FULL + 1) count = 4;      // the warps of a tile
+            if (i == L::O_FREE || i == L::O_FREE + 1) count = DIFF ? 8 : 4;
+            if (i == L::PAIR) count = 8;
+            mbar_init(bar(i), count);
+        }
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(sb + L::kTmem, 512);
+        tmem_relinquish();
+        tc05_fence_before_sync();
+    }
+    zero_bad_sequences<T>(p, D);
+    const int per = Schedule::build(p, pre);
+    const int64_t total = pre[(p.B + per - 1) / per];
+    const int W = working(total, gridDim.x);
+    const bool has = (int)blockIdx.x < W;
+    Schedule it;
+    if (threadIdx.x == 0) {
+        if (has) it.seek(p, pre, per, slice_begin(blockIdx.x, total, W), slice_begin(blockIdx.x + 1, total, W));
+        p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
+        static_assert(sizeof(Schedule) <= 128, "the schedule's place");
+        *reinterpret_cast<Schedule *>(smem + L::kSched) = it;
+        fence_proxy_async_smem();              // the ring's copies come after the sums
+    }
+    __syncthreads();
+    tc05_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
+    it = *reinterpret_cast<const Schedule *>(smem + L::kSched);
+    bool abort = false;
+
+    if (warp >= kProducerWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (!has) {
+        } else if (warp == kProducerWarp) {
+            // lane s copies box s (box_rows positions) of each tile; table entries are
+            // looked up a tile ahead
+            const int boxes = kKT / box_rows;
+            const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
+            uint32_t g = 0;
+            do {
+                const Share<DIFF> sh(p, it.x);
+                auto look_up = [&](int k, bool &needed) -> int32_t {   // row of the box, -1 bad
+                    const int t = (it.x.lo + k) * kKT + lane * box_rows;
+                    needed = k < it.x.k1 && lane < boxes && t <= sh.need_hi && t + box_rows > sh.need_lo;
+                    if (!needed) return 0;
+                    const int j = p.bs_shift >= 0 ? t >> p.bs_shift : t / p.bs;
+                    const int32_t blk = __ldg(p.block_table + (int64_t)it.x.b * p.MB + j);
+                    if (blk < 0 || (int64_t)blk >= p.num_blocks) return -1;
+                    return blk * p.rows_per_block + it.x.hk * p.bs + (t - j * p.bs);
+                };
+                bool needed, ahead_needed;
+                int32_t y = look_up(it.x.k0, needed);
+                for (int k = it.x.k0; k < it.x.k1 && !abort; ++k, ++g) {
+                    const int32_t ahead = look_up(k + 1, ahead_needed);
+                    const bool bad = needed && y < 0, take = needed && y >= 0;
+                    // a bit per 8 rows, as the looking warps and the rows' threads test them
+                    const uint32_t bits = __reduce_or_sync(
+                        0xffffffffu, bad ? (uint32_t)(((1u << (box_rows / 8)) - 1) << (lane * (box_rows / 8))) : 0u);
+                    const uint32_t bytes = __reduce_add_sync(0xffffffffu, take ? box_bytes : 0u);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t n = half ? L::kV : L::kK, slot = g % n, round = g / n;
+                        const uint32_t full = bar((half ? L::V_FULL : L::K_FULL) + slot);
+                        if (round > 0 && !mbar_wait(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
+                        abort = __any_sync(0xffffffffu, abort);
+                        if (abort) break;
+                        if (lane == 0) {
+                            if (half == 0) badm[g % kBadRing] = bits;
+                            mbar_arrive_expect_tx(full, bytes);
+                        }
+                        __syncwarp();
+                        if (take) {
+                            const uint32_t dst = sb + (half ? L::kVRing : L::kKRing) + slot * L::kTile + lane * box_bytes;
+                            const CUtensorMap *map = half ? &vmap : &kmap;
+                            if (D == 128) tma_4d_g2s(dst, map, 0, 0, 0, y >> 3, full);
+                            else tma_2d_g2s(dst, map, 0, y, full);
+                        }
+                    }
+                    y = ahead;
+                    needed = ahead_needed;
+                }
+            } while (!abort && it.next(p));
+            // every copy has landed before the CTA may exit
+            for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
+            for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
+        } else if (warp == kMmaWarp) {
+            if (lane == 0) {
+                uint32_t g = 0, ns[2] = {0, 0}, items[2] = {0, 0};
+                do {
+                    const Share<DIFF> sh(p, it.x);
+                    for (int k = it.x.k0 - 1; k < it.x.k1 && !abort; ++k) {
+                        const bool pv = k >= it.x.k0, qk = k + 1 < it.x.k1;
+                        const uint32_t step = g + (uint32_t)(k - it.x.k0);            // of k (pv)
+                        const uint32_t vs = step % L::kV, ks = (step + 1) % L::kK;
+                        const uint32_t k_parity = ((step + 1) / L::kK) & 1;
+                        if (pv && !mbar_wait(bar(L::READY + vs), (step / L::kV) & 1)) abort = true;
+                        bool k_here = false;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (abort) break;
+                            if (pv && sh.active(s, k)) {
+                                if (!mbar_wait(bar(L::P_FULL + s), (ns[s] - 1) & 1)) abort = true;
+                                if (k == sh.begin(s) && items[s] > 1 && !mbar_wait(bar(L::O_FREE + s), items[s] & 1)) abort = true;
+                                if (abort) break;
+                                tc05_fence_after_sync();
+                                if (!odd_tile(step)) {
+                                    const uint32_t vb = sb + L::kVRing + vs * L::kTile;
+#pragma unroll
+                                    for (int kk = 0; kk < kKT / 16; ++kk)
+                                        umma_f16_ts(tmem + L::kColO + s * D, tmem + s * 128 + kk * 8,
+                                                    sw128_desc(vb + kk * 2 * L::kGroup, 1024, L::kGroup), kIdescO,
+                                                    k > sh.begin(s) || kk > 0);
+                                }
+                                if (k == sh.finish(s) - 1) umma_commit(bar(L::O_DONE + s));
+                            }
+                            if (qk && sh.active(s, k + 1)) {
+                                if (!k_here) k_here = mbar_wait(bar(L::K_FULL + ks), k_parity);
+                                if (!k_here) abort = true;
+                                if (k + 1 == sh.begin(s)) {
+                                    if (!mbar_wait(bar(L::Q_FULL + s), items[s] & 1)) abort = true;
+                                    ++items[s];
+                                }
+                                if (abort) break;
+                                tc05_fence_after_sync();
+                                const uint32_t kb = sb + L::kKRing + ks * L::kTile, qb = sb + L::kQ + s * L::kQTile;
+#pragma unroll
+                                for (int kk = 0; kk < E / 16; ++kk) {
+                                    // step kk of the row: of the map's half in the differential form
+                                    const int d = DIFF ? s * E + kk * 16 : kk * 16;
+                                    umma_f16(tmem + L::kColS + s * 128, sw128_desc(qb + (kk >> 2) * L::kQSlab + (kk & 3) * 32, 0, 1024),
+                                             sw128_desc(kb + (d >> 6) * 1024 + (d & 63) * 2, 0, L::kGroup), kIdescS, kk > 0);
+                                }
+                                umma_commit(bar(L::S_FULL + s));
+                                mbar_arrive(bar(L::S_FULL + s));
+                                ++ns[s];
+                                if (k + 1 == sh.finish(s) - 1) umma_commit(bar(L::Q_FREE + s));
+                            }
+                        }
+                        if (abort) break;
+                        if (qk && !k_here && !mbar_wait(bar(L::K_FULL + ks), k_parity)) abort = true;
+                        if (pv) umma_commit(bar(L::V_EMPTY + vs));
+                        if (qk) umma_commit(bar(L::K_EMPTY + ks));
+                    }
+                    g += (uint32_t)(it.x.k1 - it.x.k0);
+                } while (!abort && it.next(p));
+                // every product has completed before tensor memory is freed
+                umma_commit(bar(L::END));
+                mbar_wait(bar(L::END), 0);
+            }
+            __syncwarp();
+        } else if (warp < kFixWarp) {
+            // query rows of tile s; rows that are not there are zeros
+            const int s = warp - kQWarp;
+            uint32_t items = 0;
+            do {
+                const Share<DIFF> sh(p, it.x);
+                if (sh.begin(s) >= sh.finish(s)) continue;
+                if (items > 0 && !mbar_wait(bar(L::Q_FREE + s), (items - 1) & 1)) abort = true;
+                abort = __any_sync(0xffffffffu, abort);
+                if (abort) break;
+                constexpr int C = E / 8, RPI = 32 / C;   // lanes of a row, rows at once
+                const int ch = lane % C;
+                const uint32_t qb = sb + L::kQ + s * L::kQTile + (ch >> 3) * L::kQSlab;
+#pragma unroll 4
+                for (int r = lane / C; r < 128; r += RPI) {
+                    const int n = sh.n0 + (DIFF ? 0 : s * 128) + r;
+                    const bool there = n < sh.n0 + sh.nrows;
+                    const T *src = reinterpret_cast<const T *>(p.q);
+                    if (there)
+                        src += ((int64_t)it.x.b * p.T + n / p.G) * p.q_stride + (int64_t)(it.x.hk * p.G + n % p.G) * D +
+                               (DIFF ? s * E : 0) + ch * 8;
+                    cp16(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, there);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::Q_FULL + s));
+                ++items;
+            } while (it.next(p));
+        } else {
+            // V tiles, a row of a tile to a thread
+            const int r = threadIdx.x - kFixWarp * 32;
+            uint32_t g = 0;
+            do {
+                const Share<DIFF> sh(p, it.x);
+                for (int k = it.x.k0; k < it.x.k1 && !abort; ++k, ++g) {
+                    const uint32_t slot = g % L::kV;
+                    if (!mbar_wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) abort = true;
+                    abort = __any_sync(0xffffffffu, abort);
+                    if (abort) break;
+                    const uint32_t bad = badm[g % kBadRing];
+                    bool odd = false;
+                    if (bad != 0 || sh.partial(p, it.x, k, 0, 1)) {
+                        const int t = (it.x.lo + k) * kKT + r;
+                        uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (r >> 3) * L::kGroup + (r & 7) * 128);
+                        const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (r >> 3) & 1) != 0;
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint4 &v = row[h * 64 + ((c + r) & 7)];    // neighbouring rows' chunks in other banks
+                                if (unseen) v = make_uint4(0, 0, 0, 0);
+                                else odd |= non_finite<T>(v.x) || non_finite<T>(v.y) || non_finite<T>(v.z) || non_finite<T>(v.w);
+                            }
+                        fence_proxy_async_smem();
+                    }
+                    // the word was last read for step g - kBadRing, whose tile has left the ring
+                    odd = __any_sync(0xffffffffu, odd);
+                    if (lane == 0) {
+                        oddm[g % kBadRing * 4 + (warp - kFixWarp)] = odd;
+                        mbar_arrive(bar(L::READY + slot));
+                    }
+                }
+            } while (!abort && it.next(p));
+        }
+    } else {
+        // ------------------------------------------------------------------
+        // the rows of tile s: thread r has row r, the tensor-memory lane of its
+        // warp's quarter
+        // ------------------------------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int s = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
+        const float scale = p.scale_log2;
+        uint32_t g = 0, ns = 0, items = 0, pairs = 0;
+        float *pair = reinterpret_cast<float *>(smem + L::kPair);
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            if (!abort && !mbar_wait(b, parity)) abort = true;
+            abort = __any_sync(0xffffffffu, abort);
+            return !abort;
+        };
+        if (has) do {
+            const Item &x = it.x;
+            const Share<DIFF> sh(p, x);
+            const int row = (DIFF ? 0 : s * 128) + r, n = sh.n0 + row;   // row of the item
+            const bool there = row < sh.nrows;
+            const int pos = x.pos + n / p.G;
+            const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
+            const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            float m = -INFINITY, l = 0.f;
+            bool row_bad = false;
+            for (int k = sh.begin(s); k < sh.finish(s); ++k) {
+                if (!wait(bar(L::S_FULL + s), ns & 1)) break;
+                ++ns;
+                tc05_fence_after_sync();
+                uint32_t v[128];
+                auto f = [&v](int i) { return __uint_as_float(v[i]); };
+                tmem_ld32(col_s, v);
+                tmem_ld32(col_s + 32, v + 32);
+                tmem_ld32(col_s + 64, v + 64);
+                tmem_ld32(col_s + 96, v + 96);
+                const uint32_t step = g + (uint32_t)(k - x.k0);
+                const uint32_t bad = badm[step % kBadRing];
+                const int t0 = (x.lo + k) * kKT;
+                tmem_wait_ld();
+                if (sh.partial(p, x, k, s, s)) {
+                    const int lo = row_lo - t0, hi = row_hi - t0;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i < lo || i > hi) v[i] = 0xff800000u;
+                }
+                if (bad != 0) {
+                    const int b0 = max(0, row_lo - t0) >> 3, b1 = min(kKT - 1, row_hi - t0) >> 3;   // groups of 8 it sees
+                    if (b0 <= b1 && (bad >> b0 << b0 & (0xffffu >> (15 - b1))) != 0) row_bad = true;
+                }
+                float m4[4] = {f(0), f(1), f(2), f(3)};
+#pragma unroll
+                for (int i = 4; i < 128; i += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (i + 4 + j < 128) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
+                        else m4[j] = fmaxf(m4[j], f(i + j));
+                    }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const bool grown = (mx - m) * scale > kLazy;
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float alpha = grown ? ex2_approx((m - mx) * scale) : 1.f;
+                    if (grown) m = mx;
+                    l *= alpha;
+                    if (k > sh.begin(s)) {
+                        // the products before S are done when S is there
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(col_o + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st16(col_o + c, o);
+                        }
+                    }
+                }
+                const float nb = m == -INFINITY ? 0.f : -m * scale;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 e = fma2(make_float2(f(c + 2 * i), f(c + 2 * i + 1)), make_float2(scale, scale), make_float2(nb, nb));
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        sum[i & 1] = add2(sum[i & 1], e);
+                        w[i] = Elem<T>::pack2(e.x, e.y);
+                    }
+                    tmem_st16(col_s + c / 2, w);
+                }
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+                tmem_wait_st();
+                if (bad != 0 || sh.partial(p, x, k, 0, 1)) {
+                    const uint32_t slot = step % L::kV;
+                    if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
+                    if (odd_tile(step)) {
+                        float o[D];
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t t[16];
+                            if (k > sh.begin(s)) {
+                                tmem_ld16(col_o + c, t);
+                                tmem_wait_ld();
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[c + i] = k > sh.begin(s) ? __uint_as_float(t[i]) : 0.f;
+                        }
+                        // the first product of an item waits until the last one's result has been read; so
+                        // does this: the same threads have read it
+#pragma unroll 1
+                        for (int c = 0; c < 64; ++c) {
+                            uint32_t w2;
+                            tmem_ld1(col_s + c, w2);
+                            tmem_wait_ld();
+                            float w[2];
+                            Elem<T>::unpack2(w2, w[0], w[1]);
+#pragma unroll 1
+                            for (int j = 0; j < 2; ++j) {
+                                const int t = 2 * c + j;
+                                if (t0 + t < row_lo || t0 + t > row_hi) continue;
+                                const unsigned char *vr = smem + L::kVRing + slot * L::kTile + (t >> 3) * L::kGroup + (t & 7) * 128;
+                                const float wt = j ? w[1] : w[0];
+#pragma unroll
+                                for (int ch = 0; ch < D / 8; ++ch) {
+                                    const uint4 q = *reinterpret_cast<const uint4 *>(vr + (ch >> 3) * 1024 + (((ch & 7) ^ (t & 7)) << 4));
+                                    float e[8];
+                                    Elem<T>::unpack(q, e);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) o[ch * 8 + i] += wt * e[i];
+                                }
+                            }
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t t[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) t[i] = __float_as_uint(o[c + i]);
+                            tmem_st16(col_o + c, t);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                tc05_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::P_FULL + s));
+            }
+            g += (uint32_t)(x.k1 - x.k0);
+            if (abort) break;
+            const bool mine = sh.begin(s) < sh.finish(s);
+            if (row_bad) l = -1.f;
+            if (row_bad && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+            if (it.cut()) {
+                if (mine && !wait(bar(L::O_DONE + s), items & 1)) break;
+                tc05_fence_after_sync();
+                float *rec = p.records + ((int64_t)blockIdx.x * 2 + (x.k0 == 0)) * p.rec_floats;
+                float *dst = rec + (s * 128 + r) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0;
+                    if (mine) {
+                        tmem_ld16(col_o + c, o);
+                        tmem_wait_ld();
+                    }
+                    if (there)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+                if (there) {
+                    rec[256 * D + s * 128 + r] = m == -INFINITY ? -INFINITY : m * scale;
+                    rec[256 * D + 256 + s * 128 + r] = l;
+                }
+            } else if constexpr (!DIFF) {
+                if (mine) {
+                    if (!wait(bar(L::O_DONE + s), items & 1)) break;
+                    tc05_fence_after_sync();
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    T *dst = reinterpret_cast<T *>(p.out) +
+                             (((int64_t)x.b * p.T + n / p.G) * p.H + x.hk * p.G + n % p.G) * D;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32], w[16];
+                        tmem_ld32(col_o + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = row_bad ? 0u
+                                           : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        if (there)
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                    }
+                }
+            } else {
+                // both maps: the threads of tile s take columns [s D/2, (s + 1) D/2) of the row
+                if (!wait(bar(L::O_DONE), items & 1)) break;
+                if (!wait(bar(L::O_DONE + 1), items & 1)) break;
+                tc05_fence_after_sync();
+                pair[s * 128 + r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::PAIR));
+                if (!wait(bar(L::PAIR), pairs++ & 1)) break;
+                const float l0 = pair[r], l1 = pair[128 + r];
+                const bool zero = l0 < 0.f || l1 < 0.f;
+                const int head = x.hk * p.G + n % p.G;
+                const float f0 = l0 == 0.f ? 0.f : 1.f / l0;
+                const float f1 = there ? -__ldg(p.lambdas + head) * (l1 == 0.f ? 0.f : 1.f / l1) : 0.f;
+                float y[D / 2], sq = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t o0[16], o1[16];
+                    tmem_ld16(tmem + lanes + L::kColO + s * (D / 2) + c, o0);
+                    tmem_ld16(tmem + lanes + L::kColO + D + s * (D / 2) + c, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        y[c + i] = fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o0[i]) * f0);
+                        sq = fmaf(y[c + i], y[c + i], sq);
+                    }
+                }
+                float f2 = p.out_scale;
+                const T *w = reinterpret_cast<const T *>(p.norm_weight);
+                if (w != nullptr) {
+                    // every thread has read the sums before squares take their place
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::PAIR));
+                    if (!wait(bar(L::PAIR), pairs++ & 1)) break;
+                    pair[s * 128 + r] = sq;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::PAIR));
+                    if (!wait(bar(L::PAIR), pairs++ & 1)) break;
+                    sq = pair[r] + pair[128 + r];
+                    f2 *= 1.f / sqrtf(sq * (1.f / D) + p.eps);
+                }
+                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)x.b * p.T + n / p.G) * p.H + head) * D + s * (D / 2);
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 8) {
+                    float wf[8];
+                    if (w != nullptr) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(w + s * (D / 2) + c));
+                        Elem<T>::unpack(q, wf);
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = y[c + 2 * i] * f2 * (w != nullptr ? wf[2 * i] : 1.f);
+                        const float b = y[c + 2 * i + 1] * f2 * (w != nullptr ? wf[2 * i + 1] : 1.f);
+                        o[i] = zero ? 0u : Elem<T>::pack2(a, b);
+                    }
+                    if (there) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                // the next item's sums come after all have read these
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::PAIR));
+                if (!wait(bar(L::PAIR), pairs++ & 1)) break;
+            }
+            if (mine) {
+                ++items;
+                tc05_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (DIFF) {
+                        mbar_arrive(bar(L::O_FREE));
+                        mbar_arrive(bar(L::O_FREE + 1));
+                    } else {
+                        mbar_arrive(bar(L::O_FREE + s));
+                    }
+                }
+            }
+        } while (it.next(p));
+    }
+    if (abort && lane == 0) report(p.err_word, PA_DEVERR_TIMEOUT);
+    __syncwarp();
+    tc05_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc05_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+namespace {
+
+template <typename T, int D, bool DIFF>
+cudaError_t plan_one(ChunkPlan *plan) {
+    static std::atomic<int> limit[64];
+    int sms = 0;
+    cudaError_t e = ensure_smem_limit(chunk_umma_kernel<T, D, DIFF>, Layout<D, DIFF>::kBytes, limit);
+    if (e != cudaSuccess) return e;
+    e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    plan->grid = sms;
+    plan->maps = DIFF ? 2 : 1;
+    plan->rows = 256 / plan->maps;
+    plan->rec_floats = chunk_rec_floats(256, D);
+    return cudaSuccess;
+}
+
+template <typename T, int D, bool DIFF>
+cudaError_t launch_one(const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int box_rows,
+                       const ChunkPlan &plan, cudaStream_t stream) {
+    return launch_clustered(chunk_umma_kernel<T, D, DIFF>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
+                            vmap, p, box_rows);
+}
+
+}  // namespace
+
+bool chunk_umma_supported(int dtype, int head_dim) {
+    return (dtype == PA_F16 || dtype == PA_BF16) && (head_dim == 64 || head_dim == 128);
+}
+
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan) {
+    if (dtype == PA_F16) {
+        if (head_dim == 64) return diff ? plan_one<__half, 64, true>(plan) : plan_one<__half, 64, false>(plan);
+        return diff ? plan_one<__half, 128, true>(plan) : plan_one<__half, 128, false>(plan);
+    }
+    if (head_dim == 64) return diff ? plan_one<__nv_bfloat16, 64, true>(plan) : plan_one<__nv_bfloat16, 64, false>(plan);
+    return diff ? plan_one<__nv_bfloat16, 128, true>(plan) : plan_one<__nv_bfloat16, 128, false>(plan);
+}
+
+cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                              int box_rows, const ChunkPlan &plan, cudaStream_t stream) {
+    const bool diff = plan.maps == 2;
+    auto go = [&](auto kern64, auto kern64d, auto kern128, auto kern128d) {
+        if (head_dim == 64) return diff ? kern64d(p, kmap, vmap, box_rows, plan, stream) : kern64(p, kmap, vmap, box_rows, plan, stream);
+        return diff ? kern128d(p, kmap, vmap, box_rows, plan, stream) : kern128(p, kmap, vmap, box_rows, plan, stream);
+    };
+    if (dtype == PA_F16)
+        return go(launch_one<__half, 64, false>, launch_one<__half, 64, true>, launch_one<__half, 128, false>,
+                  launch_one<__half, 128, true>);
+    return go(launch_one<__nv_bfloat16, 64, false>, launch_one<__nv_bfloat16, 64, true>, launch_one<__nv_bfloat16, 128, false>,
+              launch_one<__nv_bfloat16, 128, true>);
+}
+
+}  // namespace pa

@@ -53,6 +53,17 @@ cudaError_t launch_chunk_f32(int head_dim, const ChunkParams &p, const ChunkPlan
 cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
 cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
 
+// 16-bit types, head_dim 64 and 128, on tcgen05; tensor maps of the pools in
+// boxes of box_rows rows, a divisor of 128 and of the block size.
+bool chunk_umma_supported(int dtype, int head_dim);
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
+cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                              int box_rows, const ChunkPlan &plan, cudaStream_t stream);
+
+// A pool's tensor map in 128-byte swizzled boxes of box_rows rows (api.cu):
+// head_dim 64 as [rows][64], head_dim 128 as [rows / 8][2][8][64].
+bool chunk_pool_map(CUtensorMap *map, const pa_shape *s, const void *pool, int box_rows);
+
 // Join the rows that the attention kernel of `plan` left in records.
 cudaError_t launch_chunk_merge(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan,
                                cudaStream_t stream);
