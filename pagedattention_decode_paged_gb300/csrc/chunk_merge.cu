@@ -35,29 +35,54 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll
         for (int map = 0; map < MAPS; ++map) {
             const int row = map * rows + r;
+            // lane s has the weight of share s, 32 shares at a time
             float M = -INFINITY;
             for (int s = lane; s < sharers; s += 32) {
-                const float *rec = record(s) + (int64_t)rows * MAPS * D;
-                M = fmaxf(M, __ldg(rec + row));
-                bad |= __ldg(rec + rows * MAPS + row) < 0.f;
+                const float *ml = record(s) + (int64_t)rows * MAPS * D + row;
+                M = fmaxf(M, __ldg(ml));
+                bad |= __ldg(ml + rows * MAPS) < 0.f;
             }
             M = warp_max_f32(M);
             bad = __any_sync(0xffffffffu, bad);
             float L = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[map][i] = 0.f;
-#pragma unroll 4
-            for (int s = 0; s < sharers; ++s) {
-                const float *rec = record(s);
-                const float *ml = rec + (int64_t)rows * MAPS * D;
-                const float f = merge_weight(__ldg(ml + row), M);
-                L += f * __ldg(ml + rows * MAPS + row);
-                const float *a = rec + (int64_t)row * D + lane * N;
-                if (D >= 32 || lane < D) {
+            for (int s0 = 0; s0 < sharers; s0 += 32) {
+                float f = 0.f;
+                if (s0 + lane < sharers) {
+                    const float *ml = record(s0 + lane) + (int64_t)rows * MAPS * D + row;
+                    f = merge_weight(__ldg(ml), M);
+                    L += f * __ldg(ml + rows * MAPS);
+                }
+                const int here = min(32, sharers - s0);
+                // 8 shares' values on their way at once
+                for (int s1 = 0; s1 < here; s1 += 8) {
+                    float a[8][N];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) o[map][i] += f * __ldg(a + i);
+                    for (int j = 0; j < 8; ++j) {
+                        const float *src = record(s0 + min(s1 + j, here - 1)) + (int64_t)row * D + lane * N;
+                        if (D >= 32 || lane < D) {
+                            if constexpr (N % 4 == 0) {
+#pragma unroll
+                                for (int i = 0; i < N; i += 4)
+                                    *reinterpret_cast<float4 *>(a[j] + i) = __ldg(reinterpret_cast<const float4 *>(src + i));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < N; ++i) a[j][i] = __ldg(src + i);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float fj = __shfl_sync(0xffffffffu, f, min(s1 + j, 31));
+                        if (s1 + j < here)
+#pragma unroll
+                            for (int i = 0; i < N; ++i) o[map][i] += fj * a[j][i];
+                    }
                 }
             }
+#pragma unroll
+            for (int h = 16; h > 0; h >>= 1) L += __shfl_xor_sync(0xffffffffu, L, h);
             const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
             for (int i = 0; i < N; ++i) o[map][i] *= inv;

@@ -57,22 +57,31 @@ __device__ __forceinline__ int seq_of(const ChunkParams &p, int b, int *pos, int
     return cnt;
 }
 
+// a / b: a 64-bit quotient costs some hundred cycles, and these are almost
+// always small
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // sum over i < n of floor((a i + b) / m)
 __device__ __forceinline__ int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
     uint64_t s = 0;
     for (;;) {
         if (a >= m) {
-            s += (n * (n - 1) / 2) * (a / m);
-            a %= m;
+            const uint64_t q = quotient(a, m);
+            s += (n * (n - 1) / 2) * q;
+            a -= q * m;
         }
         if (b >= m) {
-            s += n * (b / m);
-            b %= m;
+            const uint64_t q = quotient(b, m);
+            s += n * q;
+            b -= q * m;
         }
         const uint64_t y = a * n + b;
         if (y < m) return (int64_t)s;
-        n = y / m;
-        b = y % m;
+        n = quotient(y, m);
+        b = y - n * m;
         const uint64_t t = m;
         m = a;
         a = t;
@@ -183,7 +192,7 @@ struct Sched {
             if (off < head * p.Hkv) break;
             off -= head * p.Hkv;
         }
-        x.hk = (int)(off / head);
+        x.hk = (int)quotient(off, head);
         off -= x.hk * head;
         int i0 = 0, i1 = x.nq;                     // tiles_before(i0) <= off < tiles_before(i1)
         int64_t before = 0;
@@ -218,8 +227,10 @@ struct Sched {
 
 // Working CTAs of the grid: no more than there are tiles.
 __device__ __forceinline__ int working(int64_t total, int grid) { return (int)min((int64_t)grid, total); }
-__device__ __forceinline__ int64_t slice_begin(int w, int64_t total, int W) { return w * total / W; }
-__device__ __forceinline__ int slice_owner(int64_t t, int64_t total, int W) { return (int)(((t + 1) * W - 1) / total); }
+__device__ __forceinline__ int64_t slice_begin(int w, int64_t total, int W) { return (int64_t)quotient(w * total, W); }
+__device__ __forceinline__ int slice_owner(int64_t t, int64_t total, int W) {
+    return (int)quotient((t + 1) * W - 1, total);
+}
 
 // This CTA's entry of the cuts, from the first share of its slice (has: it has
 // one).  x: item's sequence (-1: nothing begins to be joined here), kv head,
@@ -231,9 +242,10 @@ __device__ __forceinline__ int4 cut_entry(const Sched<R, KT> &s, bool has, int64
 }
 
 // Report sequences whose arguments are out of range, and zero the rows of
-// those whose positions are; sequence b is CTA b % gridDim's.
+// those whose positions are; sequence b is CTA b % gridDim's.  The first `threads`
+// threads of the CTA call it.
 template <typename T>
-__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D) {
+__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D, int threads) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         int pos, error;
         seq_of(p, b, &pos, &error);
@@ -243,7 +255,7 @@ __device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D) 
         const int cnt = p.counts != nullptr ? p.counts[b] : p.T;
         const int64_t row = (int64_t)p.H * D, n = cnt * row;
         T *out = reinterpret_cast<T *>(p.out) + (int64_t)b * p.T * row;
-        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) out[i] = Elem<T>::from_float(0.f);
+        for (int64_t i = threadIdx.x; i < n; i += threads) out[i] = Elem<T>::from_float(0.f);
     }
 }
 

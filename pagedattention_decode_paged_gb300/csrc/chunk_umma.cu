@@ -14,8 +14,8 @@
 // tensor core multiplies for the other.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the rows of tile 0 and 1; warp 8 the
-// copies of K and V; warp 9 the products (one thread) and tensor memory; warps 10
-// and 11 the query rows; warps 12-15 look over those V tiles that not all rows
+// schedule and the copies of K and V; warp 9 the products (one thread) and tensor
+// memory; warps 10 and 11 the query rows; warps 12-15 look over those V tiles that not all rows
 // see alike: positions that no row sees become zeros, and where another is not
 // finite the rows' threads weigh that tile's values one by one, each only
 // those it sees (the product would let 0 times them reach every row).
@@ -37,6 +37,60 @@ constexpr int kKT = 128;                   // cache positions per tile
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kFixWarp = 12;
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
+constexpr int kItems = 4;                  // items of the schedule that roles may be apart
+
+// What the roles know of an item: the CTA's share [k0, k1) of its steps, which
+// steps each tile takes part in and what its rows see.
+struct Share {
+    int b, hk, n0, nrows;      // sequence, kv head, first row, rows
+    int pos, lo;               // position of the sequence's first new token, first tile of positions
+    int k0, k1;                // k0 < 0: no more items
+    int cut;                   // the share is not the whole item
+    int need_lo, need_hi;      // positions that some row sees
+    int a[2], e[2];            // steps of each tile
+    int all_lo[2], all_hi[2];  // positions that all its rows see
+    __device__ __forceinline__ int begin(int s) const { return s ? a[1] : a[0]; }
+    __device__ __forceinline__ int finish(int s) const { return s ? e[1] : e[0]; }
+    __device__ __forceinline__ bool active(int s, int k) const { return k >= begin(s) && k < finish(s); }
+    // not all rows of tile s, of all tiles see all positions of step k
+    __device__ __forceinline__ bool partial(int s, int k) const {
+        const int t0 = (lo + k) * kKT;
+        return t0 + kKT - 1 > (s ? all_hi[1] : all_hi[0]) || t0 < (s ? all_lo[1] : all_lo[0]);
+    }
+    __device__ __forceinline__ bool partial(int k) const {
+        const int t0 = (lo + k) * kKT;
+        return t0 + kKT - 1 > all_hi[0] || t0 < all_lo[1];
+    }
+    template <bool DIFF>
+    __device__ __forceinline__ void set(const ChunkParams &p, const Item &x, bool is_cut) {
+        constexpr int R = DIFF ? 128 : 256;
+        b = x.b;
+        hk = x.hk;
+        pos = x.pos;
+        lo = x.lo;
+        k0 = x.k0;
+        k1 = x.k1;
+        cut = is_cut;
+        n0 = x.i * R;
+        nrows = min(R, x.cnt * p.G - n0);
+        need_lo = 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r0 = DIFF ? 0 : s * 128, nr = min(128, nrows - r0);
+            a[s] = e[s] = 0;
+            if (s == 1) all_lo[1] = all_lo[0], all_hi[1] = all_hi[0];
+            if (nr <= 0) continue;
+            const int first = pos + (n0 + r0) / p.G, last = pos + (n0 + r0 + nr - 1) / p.G;
+            const int seen = p.window > 0 ? max(0, first - p.window + 1) : 0;
+            a[s] = max(k0, seen / kKT - lo);
+            e[s] = max(a[s], min(k1, last / kKT + 1 - lo));
+            all_hi[s] = first;
+            all_lo[s] = p.window > 0 ? max(0, last - p.window + 1) : 0;
+            if (s == 0) need_lo = seen;
+            need_hi = last;
+        }
+    }
+};
 
 // 32 columns of this thread's lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
@@ -132,59 +186,23 @@ struct Layout {
         O_FREE = O_DONE + 2,       // [2] its result has been read
         Q_FULL = O_FREE + 2,       // [2] query rows
         Q_FREE = Q_FULL + 2,       // [2]
-        PAIR = Q_FREE + 2,         // differential form: the threads of both tiles
+        ITEM_FULL = Q_FREE + 2,    // [kItems] the item is there
+        ITEM_EMPTY = ITEM_FULL + kItems,   // [kItems] all who need it are done with it
+        PAIR = ITEM_EMPTY + kItems,   // differential form: the threads of both tiles
         END = PAIR + 1,
         NBARS = END + 1
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
     static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
     static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][4] a V tile's 32 rows are not all finite
-    static constexpr uint32_t kSched = kOdd + kBadRing * 16;
-    static constexpr uint32_t kPair = kSched + 128;           // differential form: [2][128] sums, then squares
+    static constexpr uint32_t kItem = kOdd + kBadRing * 16;   // [kItems]
+    static constexpr uint32_t kPair = kItem + kItems * sizeof(Share);   // differential form: [2][128] sums, then squares
     static constexpr uint32_t kEnd = kPair + (DIFF ? 2 * 128 * 4 : 0);
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
     static constexpr size_t kBytes = 1024 + kEnd;
     static constexpr uint32_t kColS = 0, kColO = 256;         // S_s at 128 s, O_s at 256 + D s
     static_assert(kBytes <= 232448, "shared memory per CTA");
     static_assert((kGroups + 1) * 8 <= kK * kTile, "the sums fit the ring");
-};
-
-// The two tiles of a share: which steps each takes part in, and what its rows see.
-template <bool DIFF>
-struct Share {
-    int n0, nrows;             // first row, rows of the item
-    int need_lo, need_hi;      // positions that some row sees
-    int a[2], e[2];            // steps of each tile (in tiles of the item)
-    int t_first[2], t_last[2]; // tokens of its first and last row
-    __device__ __forceinline__ Share(const ChunkParams &p, const Item &x) {
-        constexpr int R = DIFF ? 128 : 256;
-        n0 = x.i * R;
-        nrows = min(R, x.cnt * p.G - n0);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int r0 = DIFF ? 0 : s * 128, nr = min(128, nrows - r0);
-            if (nr <= 0) {
-                a[s] = e[s] = 0;
-                t_first[s] = t_last[s] = t_last[0];
-                continue;
-            }
-            t_first[s] = (n0 + r0) / p.G;
-            t_last[s] = (n0 + r0 + nr - 1) / p.G;
-            const int lo = p.window > 0 ? max(0, x.pos + t_first[s] - p.window + 1) / kKT : 0;
-            a[s] = max(x.k0, lo - x.lo);
-            e[s] = min(x.k1, (x.pos + t_last[s]) / kKT + 1 - x.lo);
-        }
-        need_lo = p.window > 0 ? max(0, x.pos + t_first[0] - p.window + 1) : 0;
-        need_hi = x.pos + t_last[1];
-    }
-    __device__ __forceinline__ int begin(int s) const { return s ? a[1] : a[0]; }
-    __device__ __forceinline__ int finish(int s) const { return s ? e[1] : e[0]; }
-    __device__ __forceinline__ bool active(int s, int k) const { return k >= begin(s) && k < finish(s); }
-    // not all rows of tiles [s, last] see all positions of step k
-    __device__ __forceinline__ bool partial(const ChunkParams &p, const Item &x, int k, int s, int last) const {
-        const int t0 = (x.lo + k) * kKT;
-        return t0 + kKT - 1 > x.pos + (s ? t_first[1] : t_first[0]) || (p.window > 0 && t0 < x.pos + (last ? t_last[1] : t_last[0]) - p.window + 1);
-    }
 };
 
 }  // namespace
@@ -222,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == L::P_FULL || i == L::P_FULL + 1) count = 4;      // the warps of a tile
             if (i == L::O_FREE || i == L::O_FREE + 1) count = DIFF ? 8 : 4;
             if (i == L::PAIR) count = 8;
+            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 15;   // 8 warps of rows, 1, 2, 4
             mbar_init(bar(i), count);
         }
         prefetch_tensormap(&kmap);
@@ -233,36 +252,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
         tc05_fence_before_sync();
     }
-    zero_bad_sequences<T>(p, D);
-    const int per = Schedule::build(p, pre);
-    const int64_t total = pre[(p.B + per - 1) / per];
-    const int W = working(total, gridDim.x);
-    const bool has = (int)blockIdx.x < W;
+    const int per = Schedule::build(p, pre);       // ends with a barrier
     Schedule it;
-    if (threadIdx.x == 0) {
+    bool has = false;
+    if (warp == kProducerWarp) {
+        const int64_t total = pre[(p.B + per - 1) / per];
+        const int W = working(total, gridDim.x);
+        has = (int)blockIdx.x < W;
         if (has) it.seek(p, pre, per, slice_begin(blockIdx.x, total, W), slice_begin(blockIdx.x + 1, total, W));
-        p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
-        static_assert(sizeof(Schedule) <= 128, "the schedule's place");
-        *reinterpret_cast<Schedule *>(smem + L::kSched) = it;
-        fence_proxy_async_smem();              // the ring's copies come after the sums
+        if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
+        __syncwarp();
+        fence_proxy_async_smem();                  // the ring's copies come after the sums
     }
-    __syncthreads();
     tc05_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
-    it = *reinterpret_cast<const Schedule *>(smem + L::kSched);
+    const Share *ring = reinterpret_cast<const Share *>(smem + L::kItem);
     bool abort = false;
+    // item i of the CTA, or null at the end (or after a wait that gave up)
+    auto item = [&](uint32_t i) -> const Share * {
+        if (!mbar_wait(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
+        const Share *x = ring + i % kItems;
+        return abort || x->k0 < 0 ? nullptr : x;
+    };
+    auto item_done = [&](uint32_t i) { mbar_arrive(bar(L::ITEM_EMPTY + i % kItems)); };   // one lane of a warp
 
     if (warp >= kProducerWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (!has) {
-        } else if (warp == kProducerWarp) {
+        if (warp == kProducerWarp) {
             // lane s copies box s (box_rows positions) of each tile; table entries are
             // looked up a tile ahead
             const int boxes = kKT / box_rows;
             const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
-            uint32_t g = 0;
-            do {
-                const Share<DIFF> sh(p, it.x);
+            uint32_t g = 0, i = 0;
+            auto publish = [&](bool stop) {
+                if (i >= kItems && !mbar_wait(bar(L::ITEM_EMPTY + i % kItems), (i / kItems - 1) & 1)) abort = true;
+                abort = __any_sync(0xffffffffu, abort);
+                Share *x = reinterpret_cast<Share *>(smem + L::kItem) + i % kItems;
+                if (lane == 0) {
+                    if (stop) x->k0 = -1;
+                    else x->set<DIFF>(p, it.x, it.cut());
+                    mbar_arrive(bar(L::ITEM_FULL + i % kItems));
+                }
+                __syncwarp();
+                ++i;
+                return x;
+            };
+            while (has && !abort) {
+                const Share &sh = *publish(false);
                 auto look_up = [&](int k, bool &needed) -> int32_t {   // row of the box, -1 bad
                     const int t = (it.x.lo + k) * kKT + lane * box_rows;
                     needed = k < it.x.k1 && lane < boxes && t <= sh.need_hi && t + box_rows > sh.need_lo;
@@ -303,18 +339,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y = ahead;
                     needed = ahead_needed;
                 }
-            } while (!abort && it.next(p));
+                has = it.next(p);
+            }
+            publish(true);
             // every copy has landed before the CTA may exit
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
             for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
         } else if (warp == kMmaWarp) {
             if (lane == 0) {
-                uint32_t g = 0, ns[2] = {0, 0}, items[2] = {0, 0};
-                do {
-                    const Share<DIFF> sh(p, it.x);
-                    for (int k = it.x.k0 - 1; k < it.x.k1 && !abort; ++k) {
-                        const bool pv = k >= it.x.k0, qk = k + 1 < it.x.k1;
-                        const uint32_t step = g + (uint32_t)(k - it.x.k0);            // of k (pv)
+                uint32_t g = 0, i = 0, ns[2] = {0, 0}, items[2] = {0, 0};
+                for (const Share *x; (x = item(i)) != nullptr; ++i) {
+                    const Share sh = *x;
+                    item_done(i);
+                    for (int k = sh.k0 - 1; k < sh.k1 && !abort; ++k) {
+                        const bool pv = k >= sh.k0, qk = k + 1 < sh.k1;
+                        const uint32_t step = g + (uint32_t)(k - sh.k0);              // of k (pv)
                         const uint32_t vs = step % L::kV, ks = (step + 1) % L::kK;
                         const uint32_t k_parity = ((step + 1) / L::kK) & 1;
                         if (pv && !mbar_wait(bar(L::READY + vs), (step / L::kV) & 1)) abort = true;
@@ -365,57 +404,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (pv) umma_commit(bar(L::V_EMPTY + vs));
                         if (qk) umma_commit(bar(L::K_EMPTY + ks));
                     }
-                    g += (uint32_t)(it.x.k1 - it.x.k0);
-                } while (!abort && it.next(p));
+                    g += (uint32_t)(sh.k1 - sh.k0);
+                }
                 // every product has completed before tensor memory is freed
                 umma_commit(bar(L::END));
                 mbar_wait(bar(L::END), 0);
             }
             __syncwarp();
         } else if (warp < kFixWarp) {
-            // query rows of tile s; rows that are not there are zeros
+            // query rows of tile s (the scores of rows that are not there go nowhere)
             const int s = warp - kQWarp;
-            uint32_t items = 0;
-            do {
-                const Share<DIFF> sh(p, it.x);
-                if (sh.begin(s) >= sh.finish(s)) continue;
+            uint32_t items = 0, i = 0;
+            for (const Share *x; (x = item(i)) != nullptr; ++i) {
+                const int n0 = x->n0 + (DIFF ? 0 : s * 128), nr = min(128, x->nrows - (DIFF ? 0 : s * 128));
+                const int b = x->b, hk = x->hk;
+                const bool active = x->begin(s) < x->finish(s);
+                __syncwarp();
+                if (lane == 0) item_done(i);
+                if (!active) continue;
                 if (items > 0 && !mbar_wait(bar(L::Q_FREE + s), (items - 1) & 1)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
                 if (abort) break;
                 constexpr int C = E / 8, RPI = 32 / C;   // lanes of a row, rows at once
                 const int ch = lane % C;
                 const uint32_t qb = sb + L::kQ + s * L::kQTile + (ch >> 3) * L::kQSlab;
-#pragma unroll 4
-                for (int r = lane / C; r < 128; r += RPI) {
-                    const int n = sh.n0 + (DIFF ? 0 : s * 128) + r;
-                    const bool there = n < sh.n0 + sh.nrows;
-                    const T *src = reinterpret_cast<const T *>(p.q);
-                    if (there)
-                        src += ((int64_t)it.x.b * p.T + n / p.G) * p.q_stride + (int64_t)(it.x.hk * p.G + n % p.G) * D +
+                const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride + (int64_t)hk * p.G * D +
                                (DIFF ? s * E : 0) + ch * 8;
-                    cp16(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, there);
+                int t = (n0 + lane / C) / p.G, h = (n0 + lane / C) - t * p.G;
+#pragma unroll 4
+                for (int r = lane / C; r < nr; r += RPI) {
+                    cp16(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D, true);
+                    for (h += RPI; h >= p.G; h -= p.G) ++t;
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::Q_FULL + s));
                 ++items;
-            } while (it.next(p));
+            }
         } else {
             // V tiles, a row of a tile to a thread
             const int r = threadIdx.x - kFixWarp * 32;
-            uint32_t g = 0;
-            do {
-                const Share<DIFF> sh(p, it.x);
-                for (int k = it.x.k0; k < it.x.k1 && !abort; ++k, ++g) {
+            uint32_t g = 0, i = 0;
+            for (const Share *x; (x = item(i)) != nullptr; ++i) {
+                const Share &sh = *x;
+                for (int k = sh.k0; k < sh.k1 && !abort; ++k, ++g) {
                     const uint32_t slot = g % L::kV;
                     if (!mbar_wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) abort = true;
                     abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
                     const uint32_t bad = badm[g % kBadRing];
                     bool odd = false;
-                    if (bad != 0 || sh.partial(p, it.x, k, 0, 1)) {
-                        const int t = (it.x.lo + k) * kKT + r;
+                    if (bad != 0 || sh.partial(k)) {
+                        const int t = (sh.lo + k) * kKT + r;
                         uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (r >> 3) * L::kGroup + (r & 7) * 128);
                         const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (r >> 3) & 1) != 0;
 #pragma unroll
@@ -435,7 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(bar(L::READY + slot));
                     }
                 }
-            } while (!abort && it.next(p));
+                __syncwarp();
+                if (lane == 0) item_done(i);
+            }
         }
     } else {
         // ------------------------------------------------------------------
@@ -447,26 +490,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
         const float scale = p.scale_log2;
-        uint32_t g = 0, ns = 0, items = 0, pairs = 0;
+        uint32_t g = 0, i = 0, ns = 0, items = 0, pairs = 0;
+        zero_bad_sequences<T>(p, D, 256);
         float *pair = reinterpret_cast<float *>(smem + L::kPair);
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (!abort && !mbar_wait(b, parity)) abort = true;
             abort = __any_sync(0xffffffffu, abort);
             return !abort;
         };
-        if (has) do {
-            const Item &x = it.x;
-            const Share<DIFF> sh(p, x);
+        for (const Share *xi; (xi = item(i)) != nullptr; ++i) {
+            const Share &sh = *xi;
             const int row = (DIFF ? 0 : s * 128) + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;
-            const int pos = x.pos + n / p.G;
+            const bool idle = (DIFF ? 0 : s * 128) + (warp & 3) * 32 >= sh.nrows;   // none of the warp's rows is
+            const int pos = sh.pos + n / p.G;
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            const int k_end = sh.finish(s);
             float m = -INFINITY, l = 0.f;
             bool row_bad = false;
-            for (int k = sh.begin(s); k < sh.finish(s); ++k) {
+            for (int k = sh.begin(s); k < k_end; ++k) {
                 if (!wait(bar(L::S_FULL + s), ns & 1)) break;
                 ++ns;
+                if (idle) {
+                    if (lane == 0) mbar_arrive(bar(L::P_FULL + s));
+                    continue;
+                }
                 tc05_fence_after_sync();
                 uint32_t v[128];
                 auto f = [&v](int i) { return __uint_as_float(v[i]); };
@@ -474,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(col_s + 32, v + 32);
                 tmem_ld32(col_s + 64, v + 64);
                 tmem_ld32(col_s + 96, v + 96);
-                const uint32_t step = g + (uint32_t)(k - x.k0);
+                const uint32_t step = g + (uint32_t)(k - sh.k0);
                 const uint32_t bad = badm[step % kBadRing];
-                const int t0 = (x.lo + k) * kKT;
+                const int t0 = (sh.lo + k) * kKT;
                 tmem_wait_ld();
-                if (sh.partial(p, x, k, s, s)) {
+                if (sh.partial(s, k)) {
                     const int lo = row_lo - t0, hi = row_hi - t0;
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
@@ -533,53 +582,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 tmem_wait_st();
-                if (bad != 0 || sh.partial(p, x, k, 0, 1)) {
+                if (bad != 0 || sh.partial(k)) {
                     const uint32_t slot = step % L::kV;
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
                     if (odd_tile(step)) {
-                        float o[D];
-#pragma unroll
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t t[16];
-                            if (k > sh.begin(s)) {
-                                tmem_ld16(col_o + c, t);
-                                tmem_wait_ld();
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[c + i] = k > sh.begin(s) ? __uint_as_float(t[i]) : 0.f;
-                        }
-                        // the first product of an item waits until the last one's result has been read; so
-                        // does this: the same threads have read it
+                        // O of the first step is these threads' to write: they have read the last item's
 #pragma unroll 1
-                        for (int c = 0; c < 64; ++c) {
-                            uint32_t w2;
-                            tmem_ld1(col_s + c, w2);
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o32[32];
+                            float o[32];
+                            tmem_ld32(col_o + c0, o32);
                             tmem_wait_ld();
-                            float w[2];
-                            Elem<T>::unpack2(w2, w[0], w[1]);
-#pragma unroll 1
-                            for (int j = 0; j < 2; ++j) {
-                                const int t = 2 * c + j;
-                                if (t0 + t < row_lo || t0 + t > row_hi) continue;
-                                const unsigned char *vr = smem + L::kVRing + slot * L::kTile + (t >> 3) * L::kGroup + (t & 7) * 128;
-                                const float wt = j ? w[1] : w[0];
 #pragma unroll
-                                for (int ch = 0; ch < D / 8; ++ch) {
-                                    const uint4 q = *reinterpret_cast<const uint4 *>(vr + (ch >> 3) * 1024 + (((ch & 7) ^ (t & 7)) << 4));
+                            for (int i = 0; i < 32; ++i) o[i] = k > sh.begin(s) ? __uint_as_float(o32[i]) : 0.f;
+#pragma unroll 1
+                            for (int t = 0; t < kKT; ++t) {
+                                uint32_t w2;
+                                tmem_ld1(col_s + t / 2, w2);
+                                tmem_wait_ld();
+                                float w[2];
+                                Elem<T>::unpack2(w2, w[0], w[1]);
+                                const float wt = (t & 1) ? w[1] : w[0];
+                                const bool sees = t0 + t >= row_lo && t0 + t <= row_hi;
+                                const unsigned char *vr = smem + L::kVRing + slot * L::kTile + (t >> 3) * L::kGroup +
+                                                          (c0 >> 6) * 1024 + (t & 7) * 128;
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    const int ch = ((c0 & 63) >> 3) + h;
+                                    const uint4 q = *reinterpret_cast<const uint4 *>(vr + ((ch ^ (t & 7)) << 4));
                                     float e[8];
                                     Elem<T>::unpack(q, e);
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) o[ch * 8 + i] += wt * e[i];
+                                    for (int i = 0; i < 8; ++i) o[h * 8 + i] = sees ? fmaf(wt, e[i], o[h * 8 + i]) : o[h * 8 + i];
                                 }
                             }
-                            __syncwarp();
-                        }
 #pragma unroll
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t t[16];
+                            for (int i = 0; i < 32; i += 16) {
+                                uint32_t t[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) t[i] = __float_as_uint(o[c + i]);
-                            tmem_st16(col_o + c, t);
+                                for (int j = 0; j < 16; ++j) t[j] = __float_as_uint(o[i + j]);
+                                tmem_st16(col_o + c0 + i, t);
+                            }
                         }
                         tmem_wait_st();
                     }
@@ -588,15 +631,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::P_FULL + s));
             }
-            g += (uint32_t)(x.k1 - x.k0);
+            g += (uint32_t)(sh.k1 - sh.k0);
             if (abort) break;
-            const bool mine = sh.begin(s) < sh.finish(s);
+            const bool mine = sh.begin(s) < k_end;
             if (row_bad) l = -1.f;
             if (row_bad && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
-            if (it.cut()) {
+            if (sh.cut) {
                 if (mine && !wait(bar(L::O_DONE + s), items & 1)) break;
                 tc05_fence_after_sync();
-                float *rec = p.records + ((int64_t)blockIdx.x * 2 + (x.k0 == 0)) * p.rec_floats;
+                float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
                 float *dst = rec + (s * 128 + r) * D;
 #pragma unroll
                 for (int c = 0; c < D; c += 16) {
@@ -622,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05_fence_after_sync();
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     T *dst = reinterpret_cast<T *>(p.out) +
-                             (((int64_t)x.b * p.T + n / p.G) * p.H + x.hk * p.G + n % p.G) * D;
+                             (((int64_t)sh.b * p.T + n / p.G) * p.H + sh.hk * p.G + n % p.G) * D;
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32], w[16];
@@ -649,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(bar(L::PAIR), pairs++ & 1)) break;
                 const float l0 = pair[r], l1 = pair[128 + r];
                 const bool zero = l0 < 0.f || l1 < 0.f;
-                const int head = x.hk * p.G + n % p.G;
+                const int head = sh.hk * p.G + n % p.G;
                 const float f0 = l0 == 0.f ? 0.f : 1.f / l0;
                 const float f1 = there ? -__ldg(p.lambdas + head) * (l1 == 0.f ? 0.f : 1.f / l1) : 0.f;
                 float y[D / 2], sq = 0.f;
@@ -679,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sq = pair[r] + pair[128 + r];
                     f2 *= 1.f / sqrtf(sq * (1.f / D) + p.eps);
                 }
-                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)x.b * p.T + n / p.G) * p.H + head) * D + s * (D / 2);
+                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + n / p.G) * p.H + head) * D + s * (D / 2);
 #pragma unroll
                 for (int c = 0; c < D / 2; c += 8) {
                     float wf[8];
@@ -714,7 +757,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-        } while (it.next(p));
+            __syncwarp();
+            if (lane == 0) item_done(i);
+        }
     }
     if (abort && lane == 0) report(p.err_word, PA_DEVERR_TIMEOUT);
     __syncwarp();
