@@ -504,6 +504,20 @@ bool chunk_pool_map(CUtensorMap *map, const pa_shape *s, const void *pool, int b
     return cached_pool_map(map, s, pool, false, box_rows, s->head_dim == 128 ? 2 : 0);
 }
 
+bool chunk_query_map(CUtensorMap *map, const pa_shape *s, const void *q, int64_t q_stride, int64_t tokens, int q_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)s->num_heads, (cuuint64_t)tokens, (cuuint64_t)(s->head_dim / 64)};
+    cuuint64_t strides[3] = {(cuuint64_t)s->head_dim * 2, (cuuint64_t)q_stride * 2, 128};
+    cuuint32_t box[4] = {64, (cuuint32_t)(s->num_heads / s->num_kv_heads), (cuuint32_t)q_tokens, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType dt =
+        s->dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(map, dt, 4, const_cast<void *>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa
 
 extern "C" {

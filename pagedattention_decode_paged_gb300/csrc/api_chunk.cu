@@ -76,7 +76,13 @@ cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const Choice &c,
     CUtensorMap kmap, vmap;
     if (!pa::chunk_pool_map(&kmap, s, p.k_pool, c.box_rows) || !pa::chunk_pool_map(&vmap, s, p.v_pool, c.box_rows))
         return cudaErrorInvalidValue;
-    return pa::launch_chunk_umma(s->dtype, s->head_dim, p, kmap, vmap, c.box_rows, c.plan, stream);
+    // a tile of 128 rows is whole tokens; no more of them than there are
+    CUtensorMap qmap{};
+    int q_tokens = 128 % p.G == 0 ? std::min(128 / p.G, p.T) : 0;
+    if (q_tokens > 0 && (p.q_stride * 2 >= (int64_t)1 << 40 ||
+                         !pa::chunk_query_map(&qmap, s, p.q, p.q_stride, (int64_t)p.B * p.T, q_tokens)))
+        q_tokens = 0;
+    return pa::launch_chunk_umma(s->dtype, s->head_dim, p, kmap, vmap, c.box_rows, qmap, q_tokens, c.plan, stream);
 }
 
 // Two records per CTA, then its cut.

@@ -17,7 +17,7 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeY = 8;
 
 template <typename T, int D, bool DIFF>
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows) {
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows, const int fold) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int N = D >= 32 ? D / 32 : 1, MAPS = DIFF ? 2 : 1;
@@ -25,10 +25,17 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     const int4 c = p.cuts[w];
     if (c.x < 0) return;
     const int lane = threadIdx.x & 31;
-    const int sharers = c.w - w + 2;
+    const int ctas = c.w - w + 2;
     const int cnt = p.counts != nullptr ? __ldg(p.counts + c.x) : p.T;
     const int n0 = c.z * rows, valid = min(rows, cnt * p.G - n0);
-    auto record = [&](int s) { return p.records + ((int64_t)(s == 0 ? (w - 1) * 2 + 1 : (w - 1 + s) * 2)) * p.rec_floats; };
+    // states of a row: one of each CTA, or two (a short item's rows r and fold + r)
+    const bool two = valid <= fold;
+    const int sharers = two ? 2 * ctas : ctas;
+    auto record = [&](int s) {
+        const int cta = two ? s >> 1 : s;
+        return p.records + ((int64_t)(cta == 0 ? (w - 1) * 2 + 1 : (w - 1 + cta) * 2)) * p.rec_floats;
+    };
+    auto row_of = [&](int s, int row) { return two && (s & 1) ? fold + row : row; };
     for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < valid; r += kMergeY * (kMergeThreads / 32)) {
         float o[MAPS][N];
         bool bad = false;
@@ -38,7 +45,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
             // lane s has the weight of share s, 32 shares at a time
             float M = -INFINITY;
             for (int s = lane; s < sharers; s += 32) {
-                const float *ml = record(s) + (int64_t)rows * MAPS * D + row;
+                const float *ml = record(s) + (int64_t)rows * MAPS * D + row_of(s, row);
                 M = fmaxf(M, __ldg(ml));
                 bad |= __ldg(ml + rows * MAPS) < 0.f;
             }
@@ -50,7 +57,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
             for (int s0 = 0; s0 < sharers; s0 += 32) {
                 float f = 0.f;
                 if (s0 + lane < sharers) {
-                    const float *ml = record(s0 + lane) + (int64_t)rows * MAPS * D + row;
+                    const float *ml = record(s0 + lane) + (int64_t)rows * MAPS * D + row_of(s0 + lane, row);
                     f = merge_weight(__ldg(ml), M);
                     L += f * __ldg(ml + rows * MAPS);
                 }
@@ -60,7 +67,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
                     float a[8][N];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float *src = record(s0 + min(s1 + j, here - 1)) + (int64_t)row * D + lane * N;
+                        const int s = s0 + min(s1 + j, here - 1);
+                        const float *src = record(s) + (int64_t)row_of(s, row) * D + lane * N;
                         if (D >= 32 || lane < D) {
                             if constexpr (N % 4 == 0) {
 #pragma unroll
@@ -103,8 +111,8 @@ cudaError_t launch_typed(const ChunkParams &p, const ChunkPlan &plan, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = PA_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (plan.maps == 2) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, true>, p, plan.rows);
-    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, false>, p, plan.rows);
+    if (plan.maps == 2) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, true>, p, plan.rows, plan.fold);
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, false>, p, plan.rows, plan.fold);
 }
 
 }  // namespace

@@ -58,8 +58,9 @@ __device__ __forceinline__ int seq_of(const ChunkParams &p, int b, int *pos, int
 }
 
 // a / b: a 64-bit quotient costs some hundred cycles, and these are almost
-// always small
-__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+// always small.  Not inlined: what a launch spends on its schedule is for the most
+// part instructions that are fetched for the first time.
+static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) {
     if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
     return a / b;
 }
@@ -102,7 +103,7 @@ struct Sched {
         return (int)(((int64_t)cnt * p.G + R - 1) / R);
     }
     // tiles of the first n items of the nq of a head
-    static __device__ __forceinline__ int64_t tiles_before(const ChunkParams &p, int pos, int cnt, int nq, int n) {
+    static __device__ __noinline__ int64_t tiles_before(const ChunkParams &p, int pos, int cnt, int nq, int n) {
         int64_t s = 0;
         int lo;
         if (n <= 4) {
@@ -173,7 +174,8 @@ struct Sched {
         x.k0 = (int)(at - first);
         x.k1 = (int)min((int64_t)x.n, end - first);
     }
-    // The first share of slice [begin, finish), which is not empty.
+    // The first share of slice [begin, finish), which is not empty.  Whole warps
+    // call it.
     __device__ __forceinline__ void seek(const ChunkParams &p, const int64_t *pre, int per, int64_t begin, int64_t finish) {
         at = begin;
         end = finish;
@@ -194,13 +196,33 @@ struct Sched {
         }
         x.hk = (int)quotient(off, head);
         off -= x.hk * head;
-        int i0 = 0, i1 = x.nq;                     // tiles_before(i0) <= off < tiles_before(i1)
+        // items 32 at a time, a lane each; past many of them, from where the sums lead
+        int i0 = 0;
         int64_t before = 0;
-        while (i1 - i0 > 1) {
-            const int mid = (i0 + i1) >> 1;
-            const int64_t v = tiles_before(p, x.pos, x.cnt, x.nq, mid);
-            if (v <= off) i0 = mid, before = v;
-            else i1 = mid;
+        for (int step = 1 << 30; x.nq > 256 && step >= 64; step >>= 1) {
+            if (i0 + step >= x.nq) continue;
+            const int64_t v = tiles_before(p, x.pos, x.cnt, x.nq, i0 + step);
+            if (v <= off) i0 += step, before = v;
+        }
+        const int lane = threadIdx.x & 31;
+        for (;; i0 += 32) {
+            int first_tile;
+            const int n = i0 + lane < x.nq ? tiles(p, x.pos, x.cnt, i0 + lane, &first_tile) : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            // the first lane whose items reach past off
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > off);
+            if (past != 0) {
+                const int l = __ffs(past) - 1;
+                before += __shfl_sync(0xffffffffu, incl - n, l);
+                i0 += l;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
         x.i = i0;
         first = at - (off - before);

@@ -9,16 +9,20 @@
 // with P_s = 2^(scale log2(e) (S_s - m)) by the 128 threads of tile s, a row
 // each, between the two.  K and V arrive by TMA as 128-byte swizzled rows, K the
 // K-major B operand of the first product, V the MN-major B operand of the
-// second; P is the A operand of the second in tensor memory, over the columns
-// that S had.  While the threads of one tile take the exponentials of a step the
-// tensor core multiplies for the other.
+// second; P is the A operand of the second in tensor memory, at head_dim 128 over
+// the columns that S had (tensor memory is full), at 64 beside them.  While the
+// threads of one tile take the exponentials of a step the tensor core multiplies
+// for the other.  An item of up to 128 rows (single tokens, ends of prompts) has
+// its steps dealt to the two tiles in turn instead, and their states are joined
+// at its end.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the rows of tile 0 and 1; warp 8 the
 // schedule and the copies of K and V; warp 9 the products (one thread) and tensor
-// memory; warps 10 and 11 the query rows; warps 12-15 look over those V tiles that not all rows
-// see alike: positions that no row sees become zeros, and where another is not
-// finite the rows' threads weigh that tile's values one by one, each only
-// those it sees (the product would let 0 times them reach every row).
+// memory; warps 10 and 11 the query rows of tile 0 and 1; warps 14 and 15 look
+// over those V tiles that not all rows see alike: positions that no row sees
+// become zeros, and where another is not finite the rows' threads weigh that
+// tile's values one by one, each only those it sees (the product would let 0
+// times them reach every row).
 //
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
 // maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
@@ -34,7 +38,7 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kKT = 128;                   // cache positions per tile
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kFixWarp = 12;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kFixWarp = 14;
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
 constexpr int kItems = 4;                  // items of the schedule that roles may be apart
@@ -47,11 +51,11 @@ struct Share {
     int k0, k1;                // k0 < 0: no more items
     int cut;                   // the share is not the whole item
     int need_lo, need_hi;      // positions that some row sees
-    int a[2], e[2];            // steps of each tile
+    int a[2], e[2];            // steps of each tile: a, a + stride, ... below e
+    int stride;                // 2: both tiles are the same rows, with steps in turn
     int all_lo[2], all_hi[2];  // positions that all its rows see
     __device__ __forceinline__ int begin(int s) const { return s ? a[1] : a[0]; }
     __device__ __forceinline__ int finish(int s) const { return s ? e[1] : e[0]; }
-    __device__ __forceinline__ bool active(int s, int k) const { return k >= begin(s) && k < finish(s); }
     // not all rows of tile s, of all tiles see all positions of step k
     __device__ __forceinline__ bool partial(int s, int k) const {
         const int t0 = (lo + k) * kKT;
@@ -89,6 +93,11 @@ struct Share {
             if (s == 0) need_lo = seen;
             need_hi = last;
         }
+        stride = !DIFF && nrows <= 128 ? 2 : 1;
+        if (stride == 2) {
+            a[1] = min(k0 + 1, k1);
+            e[1] = k1;
+        }
     }
 };
 
@@ -113,6 +122,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
         : "r"(taddr)
         : "memory");
 }
+// Wait for this thread's loads.  The registers they fill pass through, so that
+// nothing that uses them comes before the wait.
+__device__ __forceinline__ void pin16(uint32_t *r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_landed(uint32_t *r) {
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; i += 16) pin16(r + i);
+}
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
 }
@@ -125,16 +146,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+// D[tmem] (+)= A * B[smem] with A in shared or tensor memory.  Descriptors are
+// given as their halves: only the low one, with the address, differs between the
+// products of a tile.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                        bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+// A place in a ring of n: slot and the parity of its round.
+template <int N>
+struct Place {
+    uint32_t slot = 0, parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -170,7 +218,8 @@ struct Layout {
     static constexpr uint32_t kTile = kKT * D * 2;
     static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 4;   // tiles in flight or waiting
     static constexpr uint32_t kQSlab = 128 * 128;
-    static constexpr uint32_t kQTile = (E <= 64 ? 1 : E / 64) * kQSlab;
+    static constexpr int kQSlabs = E <= 64 ? 1 : E / 64;     // (rows of 64 elements stay whole in the differential form)
+    static constexpr uint32_t kQTile = kQSlabs * kQSlab;
     static constexpr uint32_t kQ = 0;                         // two query tiles
     static constexpr uint32_t kKRing = 2 * kQTile, kVRing = kKRing + kK * kTile;
     static constexpr uint32_t kBars = kVRing + kV * kTile;
@@ -181,26 +230,32 @@ struct Layout {
         V_EMPTY = V_FULL + kV,     // [kV]
         READY = V_EMPTY + kV,      // [kV] the tile has been looked over
         S_FULL = READY + kV,       // [2] scores
-        P_FULL = S_FULL + 2,       // [2] weights
-        O_DONE = P_FULL + 2,       // [2] last product of an item
+        S_FREE = S_FULL + 2,       // [2] P apart from S: the scores have been read
+        P_HALF = S_FREE + 2,       // [2] weights of the first 64 positions
+        P_FULL = P_HALF + 2,       // [2] all weights
+        P_EMPTY = P_FULL + 2,      // [2] P apart from S: the product that reads the weights is done
+        O_DONE = P_EMPTY + 2,      // [2] last product of an item
         O_FREE = O_DONE + 2,       // [2] its result has been read
         Q_FULL = O_FREE + 2,       // [2] query rows
         Q_FREE = Q_FULL + 2,       // [2]
         ITEM_FULL = Q_FREE + 2,    // [kItems] the item is there
         ITEM_EMPTY = ITEM_FULL + kItems,   // [kItems] all who need it are done with it
-        PAIR = ITEM_EMPTY + kItems,   // differential form: the threads of both tiles
-        END = PAIR + 1,
+        PAIR = ITEM_EMPTY + kItems,   // sums and maxima (or squares) of rows for the other tile's threads
+        PAIR_FREE = PAIR + 1,         // have been read
+        END = PAIR_FREE + 1,
         NBARS = END + 1
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
     static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
-    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][4] a V tile's 32 rows are not all finite
-    static constexpr uint32_t kItem = kOdd + kBadRing * 16;   // [kItems]
-    static constexpr uint32_t kPair = kItem + kItems * sizeof(Share);   // differential form: [2][128] sums, then squares
-    static constexpr uint32_t kEnd = kPair + (DIFF ? 2 * 128 * 4 : 0);
+    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][2] a V tile's 64 rows are not all finite
+    static constexpr uint32_t kItem = kOdd + kBadRing * 8;    // [kItems]
+    static constexpr uint32_t kPair = kItem + kItems * sizeof(Share);   // [2][128] sums and maxima (or squares) of rows
+    static constexpr uint32_t kEnd = kPair + 2 * 128 * 4;
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
     static constexpr size_t kBytes = 1024 + kEnd;
-    static constexpr uint32_t kColS = 0, kColO = 256;         // S_s at 128 s, O_s at 256 + D s
+    static constexpr bool kApart = D == 64;                   // P has columns of its own
+    static constexpr uint32_t kColS = 0, kColO = D == 64 ? 384 : 256;   // S_s at 128 s, O_s D columns each
+    static constexpr uint32_t kColP = kApart ? 256 : 0, kPStep = kApart ? 64 : 128;
     static_assert(kBytes <= 232448, "shared memory per CTA");
     static_assert((kGroups + 1) * 8 <= kK * kTile, "the sums fit the ring");
 };
@@ -210,7 +265,8 @@ struct Layout {
 template <typename T, int D, bool DIFF>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_umma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ ChunkParams p, const int box_rows) {
+                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkParams p, const int box_rows,
+                      const int q_tokens) {
     using L = Layout<D, DIFF>;
     constexpr int E = L::E, R = DIFF ? 128 : 256;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -226,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *badm = reinterpret_cast<volatile uint32_t *>(smem + L::kBad);
     volatile uint32_t *oddm = reinterpret_cast<volatile uint32_t *>(smem + L::kOdd);
     auto odd_tile = [&](uint32_t step) {
-        const volatile uint32_t *o = oddm + step % kBadRing * 4;
-        return (o[0] | o[1] | o[2] | o[3]) != 0;
+        const volatile uint32_t *o = oddm + step % kBadRing * 2;
+        return (o[0] | o[1]) != 0;
     };
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -235,16 +291,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::NBARS; ++i) {
             int count = 1;
-            if (i >= L::READY && i < L::S_FULL) count = 4;            // the looking warps
+            if (i >= L::READY && i < L::S_FULL) count = 2;            // the looking warps
             if (i == L::S_FULL || i == L::S_FULL + 1) count = 2;      // the products, and what their warp knows
-            if (i == L::P_FULL || i == L::P_FULL + 1) count = 4;      // the warps of a tile
-            if (i == L::O_FREE || i == L::O_FREE + 1) count = DIFF ? 8 : 4;
-            if (i == L::PAIR) count = 8;
-            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 15;   // 8 warps of rows, 1, 2, 4
+            if (i >= L::S_FREE && i < L::P_EMPTY) count = 4;          // the warps of a tile
+            if (i == L::O_FREE || i == L::O_FREE + 1) count = 8;      // twice those of a tile, or both tiles'
+            if (i == L::PAIR) count = DIFF ? 8 : 4;
+            if (i == L::PAIR_FREE) count = 4;
+            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 13;   // 8 warps of rows, 1, 2, 2
             mbar_init(bar(i), count);
         }
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
+        if (q_tokens > 0) prefetch_tensormap(&qmap);
         mbar_init_fence();
     }
     if (warp == kMmaWarp) {
@@ -347,103 +405,156 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
         } else if (warp == kMmaWarp) {
             if (lane == 0) {
-                uint32_t g = 0, i = 0, ns[2] = {0, 0}, items[2] = {0, 0};
+                // descriptors: 128-byte swizzling, version 1, distance of 8-row groups in the high half
+                constexpr uint32_t kFlags = (1u << 14) | (2u << 29);
+                constexpr uint32_t kQHi = kFlags | (1024 >> 4), kKvHi = kFlags | (L::kGroup >> 4);
+                const uint32_t q_lo = (sb + L::kQ) >> 4, k_lo = (sb + L::kKRing) >> 4;
+                const uint32_t v_lo = ((sb + L::kVRing) >> 4) | ((1024 >> 4) << 16);
+                uint32_t step = 0, i = 0, qn[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0}, items[2] = {0, 0};
+                Place<L::kK> kp;
+                Place<L::kV> vp;
+                auto wait = [&](int b, uint32_t parity) {
+                    if (!abort && !mbar_wait(bar(b), parity)) abort = true;
+                };
                 for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                    const Share sh = *x;
+                    const int k0 = x->k0, k1 = x->k1, stride = x->stride;
+                    const int a[2] = {x->a[0], x->a[1]}, e[2] = {x->e[0], x->e[1]};
                     item_done(i);
-                    for (int k = sh.k0 - 1; k < sh.k1 && !abort; ++k) {
-                        const bool pv = k >= sh.k0, qk = k + 1 < sh.k1;
-                        const uint32_t step = g + (uint32_t)(k - sh.k0);              // of k (pv)
-                        const uint32_t vs = step % L::kV, ks = (step + 1) % L::kK;
-                        const uint32_t k_parity = ((step + 1) / L::kK) & 1;
-                        if (pv && !mbar_wait(bar(L::READY + vs), (step / L::kV) & 1)) abort = true;
-                        bool k_here = false;
+                    bool q_here[2] = {false, false}, k_here = false;
+                    // O_s += P_s V of step k
+                    auto weigh = [&](int s, int k) {
+                        if (k == a[s]) {
+                            if (items[s] > 0) wait(L::O_FREE + s, (items[s] - 1) & 1);
+                            ++items[s];
+                        }
+                        wait(L::P_HALF + s, np[s] & 1);
+                        if (abort) return;
+                        tc05_fence_after_sync();
+                        const bool odd = odd_tile(step);
+                        const uint32_t col_o = tmem + L::kColO + s * D, col_p = tmem + L::kColP + s * L::kPStep;
+                        const uint32_t lo = v_lo + vp.slot * (L::kTile >> 4);
+                        if (!odd) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_ts(col_o, col_p + kk * 8, lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k > a[s]);
+                        }
+                        wait(L::P_FULL + s, np[s]++ & 1);
+                        if (abort) return;
+                        tc05_fence_after_sync();
+                        if (!odd) {
+#pragma unroll
+                            for (int kk = 4; kk < 8; ++kk)
+                                umma_ts(col_o, col_p + kk * 8, lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
+                        }
+                        if (L::kApart) umma_commit(bar(L::P_EMPTY + s));
+                        if (k + stride >= e[s]) umma_commit(bar(L::O_DONE + s));
+                    };
+                    // S_s = Q_s K^T of step k
+                    auto score = [&](int s, int k) {
+                        const int qs = stride == 2 ? 0 : s;
+                        if (!q_here[qs]) {
+                            wait(L::Q_FULL + qs, qn[qs]++ & 1);
+                            q_here[qs] = true;
+                        }
+                        if (!k_here) wait(L::K_FULL + kp.slot, kp.parity);
+                        k_here = true;
+                        if (L::kApart && ns[s] > 0) wait(L::S_FREE + s, (ns[s] - 1) & 1);
+                        if (abort) return;
+                        tc05_fence_after_sync();
+                        const uint32_t qlo = q_lo + qs * (L::kQTile >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
+                        const uint32_t lo = k_lo + kp.slot * (L::kTile >> 4) + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
+#pragma unroll
+                        for (int kk = 0; kk < E / 16; ++kk)
+                            umma_ss(tmem + L::kColS + s * 128, qlo + (kk >> 2) * (L::kQSlab >> 4) + (kk & 3) * 2, kQHi,
+                                    lo + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kKvHi, kIdescS, kk > 0);
+                        umma_commit(bar(L::S_FULL + s));
+                        mbar_arrive(bar(L::S_FULL + s));
+                        ++ns[s];
+                        if (k + 1 >= e[qs]) umma_commit(bar(L::Q_FREE + qs));
+                    };
+                    for (int k = k0 - stride; k < k1 && !abort; ++k) {
+                        const int kq = k + stride;
+                        const bool pv = k >= k0, qk = kq < k1;
+                        if (pv) wait(L::READY + vp.slot, vp.parity);
+                        k_here = false;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            if (abort) break;
-                            if (pv && sh.active(s, k)) {
-                                if (!mbar_wait(bar(L::P_FULL + s), (ns[s] - 1) & 1)) abort = true;
-                                if (k == sh.begin(s) && items[s] > 1 && !mbar_wait(bar(L::O_FREE + s), items[s] & 1)) abort = true;
-                                if (abort) break;
-                                tc05_fence_after_sync();
-                                if (!odd_tile(step)) {
-                                    const uint32_t vb = sb + L::kVRing + vs * L::kTile;
-#pragma unroll
-                                    for (int kk = 0; kk < kKT / 16; ++kk)
-                                        umma_f16_ts(tmem + L::kColO + s * D, tmem + s * 128 + kk * 8,
-                                                    sw128_desc(vb + kk * 2 * L::kGroup, 1024, L::kGroup), kIdescO,
-                                                    k > sh.begin(s) || kk > 0);
-                                }
-                                if (k == sh.finish(s) - 1) umma_commit(bar(L::O_DONE + s));
-                            }
-                            if (qk && sh.active(s, k + 1)) {
-                                if (!k_here) k_here = mbar_wait(bar(L::K_FULL + ks), k_parity);
-                                if (!k_here) abort = true;
-                                if (k + 1 == sh.begin(s)) {
-                                    if (!mbar_wait(bar(L::Q_FULL + s), items[s] & 1)) abort = true;
-                                    ++items[s];
-                                }
-                                if (abort) break;
-                                tc05_fence_after_sync();
-                                const uint32_t kb = sb + L::kKRing + ks * L::kTile, qb = sb + L::kQ + s * L::kQTile;
-#pragma unroll
-                                for (int kk = 0; kk < E / 16; ++kk) {
-                                    // step kk of the row: of the map's half in the differential form
-                                    const int d = DIFF ? s * E + kk * 16 : kk * 16;
-                                    umma_f16(tmem + L::kColS + s * 128, sw128_desc(qb + (kk >> 2) * L::kQSlab + (kk & 3) * 32, 0, 1024),
-                                             sw128_desc(kb + (d >> 6) * 1024 + (d & 63) * 2, 0, L::kGroup), kIdescS, kk > 0);
-                                }
-                                umma_commit(bar(L::S_FULL + s));
-                                mbar_arrive(bar(L::S_FULL + s));
-                                ++ns[s];
-                                if (k + 1 == sh.finish(s) - 1) umma_commit(bar(L::Q_FREE + s));
+                            const bool turn = stride == 1 || ((k - k0) & 1) == s;
+                            const bool w = pv && turn && k >= a[s] && k < e[s], q = qk && turn && kq >= a[s] && kq < e[s];
+                            if (L::kApart) {
+                                if (q && !abort) score(s, kq);
+                                if (w && !abort) weigh(s, k);
+                            } else {
+                                if (w && !abort) weigh(s, k);
+                                if (q && !abort) score(s, kq);
                             }
                         }
                         if (abort) break;
-                        if (qk && !k_here && !mbar_wait(bar(L::K_FULL + ks), k_parity)) abort = true;
-                        if (pv) umma_commit(bar(L::V_EMPTY + vs));
-                        if (qk) umma_commit(bar(L::K_EMPTY + ks));
+                        if (pv) {
+                            umma_commit(bar(L::V_EMPTY + vp.slot));
+                            vp.next();
+                            ++step;
+                        }
+                        if (qk) {
+                            if (!k_here) wait(L::K_FULL + kp.slot, kp.parity);
+                            umma_commit(bar(L::K_EMPTY + kp.slot));
+                            kp.next();
+                        }
                     }
-                    g += (uint32_t)(sh.k1 - sh.k0);
+                    if (abort) break;
                 }
                 // every product has completed before tensor memory is freed
                 umma_commit(bar(L::END));
                 mbar_wait(bar(L::END), 0);
             }
             __syncwarp();
-        } else if (warp < kFixWarp) {
-            // query rows of tile s (the scores of rows that are not there go nowhere)
+        } else if (warp < kQWarp + 2) {
+            // query rows of tile s (the scores of rows that are not there go nowhere):
+            // one copy a slab where a tile is whole tokens, else rows of 16-byte copies
             const int s = warp - kQWarp;
             uint32_t items = 0, i = 0;
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                const int n0 = x->n0 + (DIFF ? 0 : s * 128), nr = min(128, x->nrows - (DIFF ? 0 : s * 128));
+                const int r0 = DIFF ? 0 : s * 128, n0 = x->n0 + r0, nr = min(128, x->nrows - r0);
                 const int b = x->b, hk = x->hk;
-                const bool active = x->begin(s) < x->finish(s);
+                const bool active = x->begin(s) < x->finish(s) && !(s == 1 && x->stride == 2);
                 __syncwarp();
                 if (lane == 0) item_done(i);
                 if (!active) continue;
                 if (items > 0 && !mbar_wait(bar(L::Q_FREE + s), (items - 1) & 1)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
                 if (abort) break;
-                constexpr int C = E / 8, RPI = 32 / C;   // lanes of a row, rows at once
-                const int ch = lane % C;
-                const uint32_t qb = sb + L::kQ + s * L::kQTile + (ch >> 3) * L::kQSlab;
-                const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride + (int64_t)hk * p.G * D +
-                               (DIFF ? s * E : 0) + ch * 8;
-                int t = (n0 + lane / C) / p.G, h = (n0 + lane / C) - t * p.G;
+                const uint32_t qb = sb + L::kQ + s * L::kQTile, full = bar(L::Q_FULL + s);
+                if (q_tokens > 0) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(full, (uint32_t)(L::kQSlabs * q_tokens * p.G * 128));
+#pragma unroll
+                        for (int h = 0; h < L::kQSlabs; ++h)
+                            tma_4d_g2s(qb + h * L::kQSlab, &qmap, 0, hk * p.G, b * p.T + n0 / p.G, DIFF && E == 64 ? s : h, full);
+                    }
+                    __syncwarp();
+                } else {
+                    constexpr int EQ = E < 64 ? 64 : E;      // elements of a row in the tile
+                    constexpr int C = EQ / 8, RPI = 32 / C;  // lanes of a row, rows at once
+                    const int ch = lane % C;
+                    const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride + (int64_t)hk * p.G * D +
+                                   (DIFF && E == 64 ? s * E : 0) + ch * 8;
+                    int t = (n0 + lane / C) / p.G, h = (n0 + lane / C) - t * p.G;
 #pragma unroll 4
-                for (int r = lane / C; r < nr; r += RPI) {
-                    cp16(qb + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D, true);
-                    for (h += RPI; h >= p.G; h -= p.G) ++t;
+                    for (int r = lane / C; r < nr; r += RPI) {
+                        cp16(qb + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D, true);
+                        for (h += RPI; h >= p.G; h -= p.G) ++t;
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::Q_FULL + s));
                 ++items;
             }
-        } else {
-            // V tiles, a row of a tile to a thread
+            // copies have landed before the CTA may exit
+            if (items > 0) mbar_wait(bar(L::Q_FULL + s), (items - 1) & 1);
+        } else if (warp >= kFixWarp) {
+            // V tiles, two rows of a tile to a thread
             const int r = threadIdx.x - kFixWarp * 32;
             uint32_t g = 0, i = 0;
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
@@ -456,23 +567,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bad = badm[g % kBadRing];
                     bool odd = false;
                     if (bad != 0 || sh.partial(k)) {
-                        const int t = (sh.lo + k) * kKT + r;
-                        uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (r >> 3) * L::kGroup + (r & 7) * 128);
-                        const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (r >> 3) & 1) != 0;
+#pragma unroll 1
+                        for (int rr = r; rr < kKT; rr += 64) {
+                            const int t = (sh.lo + k) * kKT + rr;
+                            uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (rr >> 3) * L::kGroup +
+                                                                   (rr & 7) * 128);
+                            const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (rr >> 3) & 1) != 0;
 #pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
+                            for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                uint4 &v = row[h * 64 + ((c + r) & 7)];    // neighbouring rows' chunks in other banks
-                                if (unseen) v = make_uint4(0, 0, 0, 0);
-                                else odd |= non_finite<T>(v.x) || non_finite<T>(v.y) || non_finite<T>(v.z) || non_finite<T>(v.w);
-                            }
+                                for (int c = 0; c < 8; ++c) {
+                                    uint4 &v = row[h * 64 + ((c + rr) & 7)];   // neighbouring rows' chunks in other banks
+                                    if (unseen) v = make_uint4(0, 0, 0, 0);
+                                    else odd |= non_finite<T>(v.x) || non_finite<T>(v.y) || non_finite<T>(v.z) || non_finite<T>(v.w);
+                                }
+                        }
                         fence_proxy_async_smem();
                     }
                     // the word was last read for step g - kBadRing, whose tile has left the ring
                     odd = __any_sync(0xffffffffu, odd);
                     if (lane == 0) {
-                        oddm[g % kBadRing * 4 + (warp - kFixWarp)] = odd;
+                        oddm[g % kBadRing * 2 + (warp - kFixWarp)] = odd;
                         mbar_arrive(bar(L::READY + slot));
                     }
                 }
@@ -489,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
+        const uint32_t col_p = tmem + lanes + L::kColP + s * L::kPStep;
         const float scale = p.scale_log2;
-        uint32_t g = 0, i = 0, ns = 0, items = 0, pairs = 0;
+        uint32_t g = 0, i = 0, ns = 0, pairs = 0, items[2] = {0, 0};
         zero_bad_sequences<T>(p, D, 256);
         float *pair = reinterpret_cast<float *>(smem + L::kPair);
         auto wait = [&](uint32_t b, uint32_t parity) {
@@ -500,64 +616,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (const Share *xi; (xi = item(i)) != nullptr; ++i) {
             const Share &sh = *xi;
-            const int row = (DIFF ? 0 : s * 128) + r, n = sh.n0 + row;   // row of the item
+            const int stride = sh.stride;
+            const int r0 = DIFF || stride == 2 ? 0 : s * 128, row = r0 + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;
-            const bool idle = (DIFF ? 0 : s * 128) + (warp & 3) * 32 >= sh.nrows;   // none of the warp's rows is
+            const bool idle = r0 + (warp & 3) * 32 >= sh.nrows;       // none of the warp's rows is
             const int pos = sh.pos + n / p.G;
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const int k_end = sh.finish(s);
             float m = -INFINITY, l = 0.f;
             bool row_bad = false;
-            for (int k = sh.begin(s); k < k_end; ++k) {
+            for (int k = sh.begin(s); k < k_end; k += stride) {
                 if (!wait(bar(L::S_FULL + s), ns & 1)) break;
                 ++ns;
                 if (idle) {
-                    if (lane == 0) mbar_arrive(bar(L::P_FULL + s));
+                    // in step with the others: an arrival for the next step would count for this one
+                    if (L::kApart && lane == 0) mbar_arrive(bar(L::S_FREE + s));
+                    if (L::kApart && ns > 1 && !wait(bar(L::P_EMPTY + s), ns & 1)) break;
+                    if (lane == 0) {
+                        mbar_arrive(bar(L::P_HALF + s));
+                        mbar_arrive(bar(L::P_FULL + s));
+                    }
                     continue;
                 }
                 tc05_fence_after_sync();
                 uint32_t v[128];
                 auto f = [&v](int i) { return __uint_as_float(v[i]); };
+                // the maximum of the first half while the second is on its way
                 tmem_ld32(col_s, v);
                 tmem_ld32(col_s + 32, v + 32);
-                tmem_ld32(col_s + 64, v + 64);
-                tmem_ld32(col_s + 96, v + 96);
                 const uint32_t step = g + (uint32_t)(k - sh.k0);
                 const uint32_t bad = badm[step % kBadRing];
                 const int t0 = (sh.lo + k) * kKT;
-                tmem_wait_ld();
+                tmem_landed<64>(v);
+                tmem_ld32(col_s + 64, v + 64);
+                tmem_ld32(col_s + 96, v + 96);
+                float m4[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m4[j] = fmaxf(f(j), f(j + 4));
+#pragma unroll
+                for (int i = 8; i < 64; i += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
+                tmem_landed<64>(v + 64);
+                if (L::kApart) {
+                    tc05_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::S_FREE + s));
+                }
                 if (sh.partial(s, k)) {
                     const int lo = row_lo - t0, hi = row_hi - t0;
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (i < lo || i > hi) v[i] = 0xff800000u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        m4[j] = -INFINITY;
+#pragma unroll
+                        for (int i = j; i < 64; i += 4) m4[j] = fmaxf(m4[j], f(i));
+                    }
                 }
                 if (bad != 0) {
                     const int b0 = max(0, row_lo - t0) >> 3, b1 = min(kKT - 1, row_hi - t0) >> 3;   // groups of 8 it sees
                     if (b0 <= b1 && (bad >> b0 << b0 & (0xffffu >> (15 - b1))) != 0) row_bad = true;
                 }
-                float m4[4] = {f(0), f(1), f(2), f(3)};
 #pragma unroll
-                for (int i = 4; i < 128; i += 8)
+                for (int i = 64; i < 128; i += 8)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (i + 4 + j < 128) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
-                        else m4[j] = fmaxf(m4[j], f(i + j));
-                    }
+                    for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                // the products before S (P over S), or those that read the last weights, are done
+                if (L::kApart && ns > 1 && !wait(bar(L::P_EMPTY + s), ns & 1)) break;
                 const bool grown = (mx - m) * scale > kLazy;
                 if (__any_sync(0xffffffffu, grown)) {
                     const float alpha = grown ? ex2_approx((m - mx) * scale) : 1.f;
                     if (grown) m = mx;
                     l *= alpha;
                     if (k > sh.begin(s)) {
-                        // the products before S are done when S is there
 #pragma unroll
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(col_o + c, o);
-                            tmem_wait_ld();
+                            tmem_landed<16>(o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                             tmem_st16(col_o + c, o);
@@ -577,7 +717,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = Elem<T>::pack2(e.x, e.y);
                     }
-                    tmem_st16(col_s + c / 2, w);
+                    tmem_st16(col_p + c / 2, w);
+                    if (c == 32) {                 // the product of the first 64 positions may begin
+                        tmem_wait_st();
+                        tc05_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::P_HALF + s));
+                    }
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
@@ -592,14 +738,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t o32[32];
                             float o[32];
                             tmem_ld32(col_o + c0, o32);
-                            tmem_wait_ld();
+                            tmem_landed<32>(o32);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = k > sh.begin(s) ? __uint_as_float(o32[i]) : 0.f;
 #pragma unroll 1
                             for (int t = 0; t < kKT; ++t) {
                                 uint32_t w2;
-                                tmem_ld1(col_s + t / 2, w2);
+                                tmem_ld1(col_p + t / 2, w2);
                                 tmem_wait_ld();
+                                asm volatile("" : "+r"(w2));
                                 float w[2];
                                 Elem<T>::unpack2(w2, w[0], w[1]);
                                 const float wt = (t & 1) ? w[1] : w[0];
@@ -633,12 +780,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             g += (uint32_t)(sh.k1 - sh.k0);
             if (abort) break;
-            const bool mine = sh.begin(s) < k_end;
+            const bool active[2] = {sh.a[0] < sh.e[0], sh.a[1] < sh.e[1]};
+            const bool mine = s ? active[1] : active[0];
+            const uint32_t done[2] = {items[0] & 1, items[1] & 1};
+            items[0] += active[0];
+            items[1] += active[1];
             if (row_bad) l = -1.f;
             if (row_bad && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+            uint32_t mask = 0;                     // whose O this warp has read, all of it or with the other tile's warps
+            uint32_t weight = 2;
             if (sh.cut) {
-                if (mine && !wait(bar(L::O_DONE + s), items & 1)) break;
+                if (mine && !wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
                 tc05_fence_after_sync();
+                mask = mine ? 1u << s : 0;
                 float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
                 float *dst = rec + (s * 128 + r) * D;
 #pragma unroll
@@ -648,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i) o[i] = 0;
                     if (mine) {
                         tmem_ld16(col_o + c, o);
-                        tmem_wait_ld();
+                        tmem_landed<16>(o);
                     }
                     if (there)
 #pragma unroll
@@ -660,32 +814,101 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rec[256 * D + 256 + s * 128 + r] = l;
                 }
             } else if constexpr (!DIFF) {
-                if (mine) {
-                    if (!wait(bar(L::O_DONE + s), items & 1)) break;
-                    tc05_fence_after_sync();
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    T *dst = reinterpret_cast<T *>(p.out) +
-                             (((int64_t)sh.b * p.T + n / p.G) * p.H + sh.hk * p.G + n % p.G) * D;
+                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + n / p.G) * p.H + sh.hk * p.G + n % p.G) * D;
+                if (stride == 1) {
+                    if (mine) {
+                        if (!wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
+                        tc05_fence_after_sync();
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32], w[16];
-                        tmem_ld32(col_o + c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32], w[16];
+                            tmem_ld32(col_o + c, o);
+                            tmem_landed<32>(o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = row_bad ? 0u
-                                           : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                        if (there)
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = row_bad ? 0u
+                                               : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                            if (there)
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                                for (int i = 0; i < 16; i += 4)
+                                    *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        }
+                        mask = 1u << s;
                     }
+                } else if (active[1]) {
+                    // the same rows in both tiles: those of tile 0 join the states
+                    const float ms = m == -INFINITY ? -INFINITY : m * scale;
+                    if (s == 1) {
+                        if (pairs > 0 && !wait(bar(L::PAIR_FREE), (pairs - 1) & 1)) break;
+                        pair[r] = ms;
+                        pair[128 + r] = l;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::PAIR));
+                    } else {
+                        if (!wait(bar(L::PAIR), pairs & 1)) break;
+                        const float m1 = pair[r], l1 = pair[128 + r];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::PAIR_FREE));
+                        if (!wait(bar(L::O_DONE), done[0]) || !wait(bar(L::O_DONE + 1), done[1])) break;
+                        tc05_fence_after_sync();
+                        if (!idle) {
+                            const bool zero = l < 0.f || l1 < 0.f;
+                            const float M = fmaxf(ms, m1);
+                            float f0 = merge_weight(ms, M), f1 = merge_weight(m1, M);
+                            const float sum = f0 * l + f1 * l1, inv = sum == 0.f ? 0.f : 1.f / sum;
+                            f0 *= inv;
+                            f1 *= inv;
+#pragma unroll
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o0[16], o1[16], w[8];
+                                tmem_ld16(col_o + c, o0);
+                                tmem_ld16(col_o + D + c, o1);
+                                tmem_landed<16>(o0);
+                                pin16(o1);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float a = fmaf(__uint_as_float(o1[2 * i]), f1, __uint_as_float(o0[2 * i]) * f0);
+                                    const float b = fmaf(__uint_as_float(o1[2 * i + 1]), f1, __uint_as_float(o0[2 * i + 1]) * f0);
+                                    w[i] = zero ? 0u : Elem<T>::pack2(a, b);
+                                }
+                                if (there)
+#pragma unroll
+                                    for (int i = 0; i < 8; i += 4)
+                                        *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                            }
+                        }
+                        mask = 3;
+                    }
+                    ++pairs;
+                } else if (s == 0) {
+                    if (!wait(bar(L::O_DONE), done[0])) break;
+                    tc05_fence_after_sync();
+                    if (!idle) {
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16], w[8];
+                            tmem_ld16(col_o + c, o);
+                            tmem_landed<16>(o);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                w[i] = row_bad ? 0u
+                                               : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                            if (there)
+#pragma unroll
+                                for (int i = 0; i < 8; i += 4)
+                                    *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        }
+                    }
+                    mask = 1;
                 }
             } else {
                 // both maps: the threads of tile s take columns [s D/2, (s + 1) D/2) of the row
-                if (!wait(bar(L::O_DONE), items & 1)) break;
-                if (!wait(bar(L::O_DONE + 1), items & 1)) break;
+                if (!wait(bar(L::O_DONE), done[0]) || !wait(bar(L::O_DONE + 1), done[1])) break;
                 tc05_fence_after_sync();
+                mask = 3;
+                weight = 1;
                 pair[s * 128 + r] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::PAIR));
@@ -701,7 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o0[16], o1[16];
                     tmem_ld16(tmem + lanes + L::kColO + s * (D / 2) + c, o0);
                     tmem_ld16(tmem + lanes + L::kColO + D + s * (D / 2) + c, o1);
-                    tmem_wait_ld();
+                    tmem_landed<16>(o0);
+                    pin16(o1);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         y[c + i] = fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o0[i]) * f0);
@@ -744,17 +968,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(L::PAIR));
                 if (!wait(bar(L::PAIR), pairs++ & 1)) break;
             }
-            if (mine) {
-                ++items;
+            if (mask != 0) {
                 tc05_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (DIFF) {
-                        mbar_arrive(bar(L::O_FREE));
-                        mbar_arrive(bar(L::O_FREE + 1));
-                    } else {
-                        mbar_arrive(bar(L::O_FREE + s));
-                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (mask >> t & 1) mbar_arrive_n(bar(L::O_FREE + t), weight);
                 }
             }
             __syncwarp();
@@ -784,15 +1004,16 @@ cudaError_t plan_one(ChunkPlan *plan) {
     plan->grid = sms;
     plan->maps = DIFF ? 2 : 1;
     plan->rows = 256 / plan->maps;
+    plan->fold = DIFF ? 0 : 128;
     plan->rec_floats = chunk_rec_floats(256, D);
     return cudaSuccess;
 }
 
 template <typename T, int D, bool DIFF>
 cudaError_t launch_one(const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int box_rows,
-                       const ChunkPlan &plan, cudaStream_t stream) {
+                       const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan, cudaStream_t stream) {
     return launch_clustered(chunk_umma_kernel<T, D, DIFF>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
-                            vmap, p, box_rows);
+                            vmap, qmap, p, box_rows, q_tokens);
 }
 
 }  // namespace
@@ -811,11 +1032,12 @@ cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan)
 }
 
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                              int box_rows, const ChunkPlan &plan, cudaStream_t stream) {
+                              int box_rows, const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan,
+                              cudaStream_t stream) {
     const bool diff = plan.maps == 2;
     auto go = [&](auto kern64, auto kern64d, auto kern128, auto kern128d) {
-        if (head_dim == 64) return diff ? kern64d(p, kmap, vmap, box_rows, plan, stream) : kern64(p, kmap, vmap, box_rows, plan, stream);
-        return diff ? kern128d(p, kmap, vmap, box_rows, plan, stream) : kern128(p, kmap, vmap, box_rows, plan, stream);
+        if (head_dim == 64) return diff ? kern64d(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream) : kern64(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream);
+        return diff ? kern128d(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream) : kern128(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream);
     };
     if (dtype == PA_F16)
         return go(launch_one<__half, 64, false>, launch_one<__half, 64, true>, launch_one<__half, 128, false>,

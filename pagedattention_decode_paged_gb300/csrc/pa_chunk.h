@@ -41,6 +41,7 @@ struct ChunkPlan {
     int grid = 0;
     int rows = 0;              // query rows of an item (of each map)
     int maps = 1;
+    int fold = 0;              // an item of up to `fold` rows has two states of each: row r and row fold + r
     int rec_floats = 0;        // floats of a record: rows * maps of head_dim, their maxima and their sums
 };
 inline int chunk_rec_floats(int rows_all_maps, int head_dim) { return rows_all_maps * (head_dim + 2); }
@@ -57,12 +58,18 @@ cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, cons
 // boxes of box_rows rows, a divisor of 128 and of the block size.
 bool chunk_umma_supported(int dtype, int head_dim);
 cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
+// qmap: the queries in boxes of q_tokens tokens of a group's heads (q_tokens 0:
+// a tile is not whole tokens, and the map is not used).
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                              int box_rows, const ChunkPlan &plan, cudaStream_t stream);
+                              int box_rows, const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan,
+                              cudaStream_t stream);
 
 // A pool's tensor map in 128-byte swizzled boxes of box_rows rows (api.cu):
 // head_dim 64 as [rows][64], head_dim 128 as [rows / 8][2][8][64].
 bool chunk_pool_map(CUtensorMap *map, const pa_shape *s, const void *pool, int box_rows);
+// The queries' tensor map: [D / 64][tokens][heads][64 elements], boxes of one
+// slab of q_tokens tokens of G heads.
+bool chunk_query_map(CUtensorMap *map, const pa_shape *s, const void *q, int64_t q_stride, int64_t tokens, int q_tokens);
 
 // Join the rows that the attention kernel of `plan` left in records.
 cudaError_t launch_chunk_merge(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan,
