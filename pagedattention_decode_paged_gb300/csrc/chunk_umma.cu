@@ -27,6 +27,8 @@
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
 // maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
 // of a row above 1.
+#include <type_traits>
+
 #include "chunk_sched.cuh"
 #include "umma.cuh"
 
@@ -172,17 +174,12 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
-// A place in a ring of n: slot and the parity of its round.
-template <int N>
-struct Place {
-    uint32_t slot = 0, parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == N) {
-            slot = 0;
-            parity ^= 1;
-        }
-    }
-};
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -281,9 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return sb + L::kBars + i * 8; };
     volatile uint32_t *badm = reinterpret_cast<volatile uint32_t *>(smem + L::kBad);
     volatile uint32_t *oddm = reinterpret_cast<volatile uint32_t *>(smem + L::kOdd);
-    auto odd_tile = [&](uint32_t step) {
-        const volatile uint32_t *o = oddm + step % kBadRing * 2;
-        return (o[0] | o[1]) != 0;
+    auto odd_words = [&](uint32_t step) {
+        return *reinterpret_cast<const volatile uint64_t *>(oddm + step % kBadRing * 2);
     };
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -404,109 +400,126 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
             for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
         } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                // descriptors: 128-byte swizzling, version 1, distance of 8-row groups in the high half
-                constexpr uint32_t kFlags = (1u << 14) | (2u << 29);
-                constexpr uint32_t kQHi = kFlags | (1024 >> 4), kKvHi = kFlags | (L::kGroup >> 4);
-                const uint32_t q_lo = (sb + L::kQ) >> 4, k_lo = (sb + L::kKRing) >> 4;
-                const uint32_t v_lo = ((sb + L::kVRing) >> 4) | ((1024 >> 4) << 16);
-                uint32_t step = 0, i = 0, qn[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0}, items[2] = {0, 0};
-                Place<L::kK> kp;
-                Place<L::kV> vp;
-                auto wait = [&](int b, uint32_t parity) {
-                    if (!abort && !mbar_wait(bar(b), parity)) abort = true;
-                };
-                for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                    const int k0 = x->k0, k1 = x->k1, stride = x->stride;
-                    const int a[2] = {x->a[0], x->a[1]}, e[2] = {x->e[0], x->e[1]};
-                    item_done(i);
-                    bool q_here[2] = {false, false}, k_here = false;
+            // The whole warp walks the steps, so that what the products are given is
+            // known to be the same in all lanes; one lane issues them.
+            const bool leader = elect_one();
+            // descriptors: 128-byte swizzling, version 1, distance of 8-row groups in the high half
+            constexpr uint32_t kFlags = (1u << 14) | (2u << 29);
+            constexpr uint32_t kQHi = kFlags | (1024 >> 4), kKvHi = kFlags | (L::kGroup >> 4);
+            const uint32_t base = __shfl_sync(0xffffffffu, sb, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t q_lo = (base + L::kQ) >> 4;
+            uint32_t k_lo = (base + L::kKRing) >> 4, v_lo = ((base + L::kVRing) >> 4) | ((1024 >> 4) << 16);   // of the slot
+            uint32_t step = 0, i = 0, ks = 0, vs = 0;
+            // a bit per barrier: the parity of the round that is waited for next
+            uint32_t phase = 0;
+            constexpr uint32_t kPhK = 1u << 0, kPhV = 1u << 1, kPhQ = 1u << 2, kPhP = 1u << 4, kPhO = 1u << 6, kPhS = 1u << 8;
+            uint32_t begun = 0;                    // bits 0, 1: a tile has had scores; 2, 3: an item
+            auto wait = [&](int b, uint32_t bit) {
+                if (!mbar_wait(bar(b), (phase & bit) != 0)) abort = true;
+                phase ^= bit;
+            };
+            for (const Share *x; (x = item(i)) != nullptr; ++i) {
+                auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+                const int k0 = same(x->k0), k1 = same(x->k1), stride = same(x->stride);
+                const int a0 = same(x->a[0]), a1 = same(x->a[1]), e0 = same(x->e[0]), e1 = same(x->e[1]);
+                if (leader) item_done(i);
+                uint32_t q_here = 0;
+                for (int k = k0 - stride; k < k1; ++k) {
+                    const int kq = k + stride;
+                    const bool pv = k >= k0, qk = kq < k1;
+                    bool k_here = false;
+                    uint64_t odd = 0;
+                    if (pv) {
+                        wait(L::READY + vs, kPhV);
+                        if (vs != L::kV - 1) phase ^= kPhV;        // one parity for the ring's round
+                        odd = odd_words(step);
+                    }
                     // O_s += P_s V of step k
-                    auto weigh = [&](int s, int k) {
-                        if (k == a[s]) {
-                            if (items[s] > 0) wait(L::O_FREE + s, (items[s] - 1) & 1);
-                            ++items[s];
+                    auto weigh = [&](auto tile) {
+                        constexpr int s = decltype(tile)::value;
+                        const int a = s ? a1 : a0, e = s ? e1 : e0;
+                        if (k == a) {
+                            if (begun & (4u << s)) wait(L::O_FREE + s, kPhO << s);
+                            begun |= 4u << s;
                         }
-                        wait(L::P_HALF + s, np[s] & 1);
-                        if (abort) return;
+                        const uint32_t ph = (phase & (kPhP << s)) != 0;
+                        if (!mbar_wait(bar(L::P_HALF + s), ph)) abort = true;
                         tc05_fence_after_sync();
-                        const bool odd = odd_tile(step);
-                        const uint32_t col_o = tmem + L::kColO + s * D, col_p = tmem + L::kColP + s * L::kPStep;
-                        const uint32_t lo = v_lo + vp.slot * (L::kTile >> 4);
-                        if (!odd) {
+                        const uint32_t col_o = tm + L::kColO + s * D, col_p = tm + L::kColP + s * L::kPStep;
+                        if (leader && odd == 0) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ts(col_o, col_p + kk * 8, lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k > a[s]);
+                                umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k != a);
                         }
-                        wait(L::P_FULL + s, np[s]++ & 1);
-                        if (abort) return;
+                        wait(L::P_FULL + s, kPhP << s);
                         tc05_fence_after_sync();
-                        if (!odd) {
+                        if (leader) {
+                            if (odd == 0) {
 #pragma unroll
-                            for (int kk = 4; kk < 8; ++kk)
-                                umma_ts(col_o, col_p + kk * 8, lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
-                        }
-                        if (L::kApart) umma_commit(bar(L::P_EMPTY + s));
-                        if (k + stride >= e[s]) umma_commit(bar(L::O_DONE + s));
-                    };
-                    // S_s = Q_s K^T of step k
-                    auto score = [&](int s, int k) {
-                        const int qs = stride == 2 ? 0 : s;
-                        if (!q_here[qs]) {
-                            wait(L::Q_FULL + qs, qn[qs]++ & 1);
-                            q_here[qs] = true;
-                        }
-                        if (!k_here) wait(L::K_FULL + kp.slot, kp.parity);
-                        k_here = true;
-                        if (L::kApart && ns[s] > 0) wait(L::S_FREE + s, (ns[s] - 1) & 1);
-                        if (abort) return;
-                        tc05_fence_after_sync();
-                        const uint32_t qlo = q_lo + qs * (L::kQTile >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
-                        const uint32_t lo = k_lo + kp.slot * (L::kTile >> 4) + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
-#pragma unroll
-                        for (int kk = 0; kk < E / 16; ++kk)
-                            umma_ss(tmem + L::kColS + s * 128, qlo + (kk >> 2) * (L::kQSlab >> 4) + (kk & 3) * 2, kQHi,
-                                    lo + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kKvHi, kIdescS, kk > 0);
-                        umma_commit(bar(L::S_FULL + s));
-                        mbar_arrive(bar(L::S_FULL + s));
-                        ++ns[s];
-                        if (k + 1 >= e[qs]) umma_commit(bar(L::Q_FREE + qs));
-                    };
-                    for (int k = k0 - stride; k < k1 && !abort; ++k) {
-                        const int kq = k + stride;
-                        const bool pv = k >= k0, qk = kq < k1;
-                        if (pv) wait(L::READY + vp.slot, vp.parity);
-                        k_here = false;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const bool turn = stride == 1 || ((k - k0) & 1) == s;
-                            const bool w = pv && turn && k >= a[s] && k < e[s], q = qk && turn && kq >= a[s] && kq < e[s];
-                            if (L::kApart) {
-                                if (q && !abort) score(s, kq);
-                                if (w && !abort) weigh(s, k);
-                            } else {
-                                if (w && !abort) weigh(s, k);
-                                if (q && !abort) score(s, kq);
+                                for (int kk = 4; kk < 8; ++kk)
+                                    umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
                             }
+                            if (L::kApart) umma_commit(bar(L::P_EMPTY + s));
+                            if (k + stride >= e) umma_commit(bar(L::O_DONE + s));
                         }
-                        if (abort) break;
-                        if (pv) {
-                            umma_commit(bar(L::V_EMPTY + vp.slot));
-                            vp.next();
-                            ++step;
+                    };
+                    // S_s = Q_s K^T of step kq
+                    auto score = [&](auto tile) {
+                        constexpr int s = decltype(tile)::value;
+                        const int qs = stride == 2 ? 0 : s;
+                        if (!(q_here >> qs & 1)) wait(L::Q_FULL + qs, kPhQ << qs);
+                        q_here |= 1u << qs;
+                        if (!k_here) wait(L::K_FULL + ks, kPhK);
+                        k_here = true;
+                        if (L::kApart) {
+                            if (begun & (1u << s)) wait(L::S_FREE + s, kPhS << s);
+                            begun |= 1u << s;
                         }
-                        if (qk) {
-                            if (!k_here) wait(L::K_FULL + kp.slot, kp.parity);
-                            umma_commit(bar(L::K_EMPTY + kp.slot));
-                            kp.next();
+                        tc05_fence_after_sync();
+                        const uint32_t a_lo = q_lo + qs * (L::kQTile >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
+                        const uint32_t b_lo = k_lo + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < E / 16; ++kk)
+                                umma_ss(tm + L::kColS + s * 128, a_lo + (kk >> 2) * (L::kQSlab >> 4) + (kk & 3) * 2, kQHi,
+                                        b_lo + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kKvHi, kIdescS, kk > 0);
+                            umma_commit(bar(L::S_FULL + s));
+                            mbar_arrive(bar(L::S_FULL + s));
+                            if (kq + 1 >= (qs ? e1 : e0)) umma_commit(bar(L::Q_FREE + qs));
                         }
-                    }
+                    };
+                    auto both = [&](auto tile) {
+                        constexpr int s = decltype(tile)::value;
+                        const bool turn = stride == 1 || ((k - k0) & 1) == s;
+                        const int a = s ? a1 : a0, e = s ? e1 : e0;
+                        const bool w = pv && turn && k >= a && k < e, q = qk && turn && kq >= a && kq < e;
+                        if (L::kApart && q) score(tile);
+                        if (w) weigh(tile);
+                        if (!L::kApart && q) score(tile);
+                    };
+                    both(std::integral_constant<int, 0>());
+                    both(std::integral_constant<int, 1>());
+                    if (qk && !k_here) wait(L::K_FULL + ks, kPhK);
+                    abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
+                    if (pv) {
+                        if (leader) umma_commit(bar(L::V_EMPTY + vs));
+                        v_lo += L::kTile >> 4;
+                        ++step;
+                        if (++vs == L::kV) vs = 0, v_lo -= L::kV * (L::kTile >> 4);
+                    }
+                    if (qk) {
+                        if (leader) umma_commit(bar(L::K_EMPTY + ks));
+                        k_lo += L::kTile >> 4;
+                        if (ks != L::kK - 1) phase ^= kPhK;
+                        if (++ks == L::kK) ks = 0, k_lo -= L::kK * (L::kTile >> 4);
+                    }
                 }
-                // every product has completed before tensor memory is freed
-                umma_commit(bar(L::END));
-                mbar_wait(bar(L::END), 0);
+                if (abort) break;
             }
+            // every product has completed before tensor memory is freed
+            if (leader) umma_commit(bar(L::END));
+            mbar_wait(bar(L::END), 0);
             __syncwarp();
         } else if (warp < kQWarp + 2) {
             // query rows of tile s (the scores of rows that are not there go nowhere):
@@ -731,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bad != 0 || sh.partial(k)) {
                     const uint32_t slot = step % L::kV;
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
-                    if (odd_tile(step)) {
+                    if (odd_words(step) != 0) {
                         // O of the first step is these threads' to write: they have read the last item's
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
