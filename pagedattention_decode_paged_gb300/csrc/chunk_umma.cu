@@ -17,8 +17,8 @@
 // at its end.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the rows of tile 0 and 1; warp 8 the
-// schedule and the copies of K and V; warp 9 the products (one thread) and tensor
-// memory; warps 10 and 11 the query rows of tile 0 and 1; warps 14 and 15 look
+// schedule and the copies of K and V; warps 9 and 12 the products of tile 0 and 1,
+// warp 9 tensor memory; warps 10 and 11 the query rows; warps 14 and 15 look
 // over those V tiles that not all rows see alike: positions that no row sees
 // become zeros, and where another is not finite the rows' threads weigh that
 // tile's values one by one, each only those it sees (the product would let 0
@@ -40,7 +40,7 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kKT = 128;                   // cache positions per tile
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kFixWarp = 14;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kMmaWarp1 = 12, kFixWarp = 14;
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
 constexpr int kItems = 4;                  // items of the schedule that roles may be apart
@@ -239,8 +239,9 @@ struct Layout {
         ITEM_EMPTY = ITEM_FULL + kItems,   // [kItems] all who need it are done with it
         PAIR = ITEM_EMPTY + kItems,   // sums and maxima (or squares) of rows for the other tile's threads
         PAIR_FREE = PAIR + 1,         // have been read
-        END = PAIR_FREE + 1,
-        NBARS = END + 1
+        TURN = PAIR_FREE + 1,      // [2] the tensor core is tile s's to use
+        END = TURN + 2,            // [2]
+        NBARS = END + 2
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
     static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
@@ -288,12 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < L::NBARS; ++i) {
             int count = 1;
             if (i >= L::READY && i < L::S_FULL) count = 2;            // the looking warps
+            if (i >= L::K_EMPTY && i < L::K_EMPTY + L::kK) count = 2; // the products of both tiles
+            if (i >= L::V_EMPTY && i < L::V_EMPTY + L::kV) count = 2;
             if (i == L::S_FULL || i == L::S_FULL + 1) count = 2;      // the products, and what their warp knows
+            if (i == L::Q_FREE || i == L::Q_FREE + 1) count = 2;
             if (i >= L::S_FREE && i < L::P_EMPTY) count = 4;          // the warps of a tile
             if (i == L::O_FREE || i == L::O_FREE + 1) count = 8;      // twice those of a tile, or both tiles'
             if (i == L::PAIR) count = DIFF ? 8 : 4;
             if (i == L::PAIR_FREE) count = 4;
-            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 13;   // 8 warps of rows, 1, 2, 2
+            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 14;   // 8 warps of rows, 2, 2, 2
             mbar_init(bar(i), count);
         }
         prefetch_tensormap(&kmap);
@@ -399,59 +403,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every copy has landed before the CTA may exit
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
             for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
-        } else if (warp == kMmaWarp) {
-            // The whole warp walks the steps, so that what the products are given is
-            // known to be the same in all lanes; one lane issues them.
+        } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+            // Products of tile s.  The whole warp walks the steps, so that what the
+            // products are given is known to be the same in all lanes; one lane issues
+            // them.  The two warps take turns at the tensor core: while one issues, the
+            // other walks on and waits, and the tiles stay half a step apart (left to
+            // themselves both products, then both exponentials, run side by side).
+            const int s = __shfl_sync(0xffffffffu, warp == kMmaWarp ? 0 : 1, 0);
             const bool leader = elect_one();
             // descriptors: 128-byte swizzling, version 1, distance of 8-row groups in the high half
             constexpr uint32_t kFlags = (1u << 14) | (2u << 29);
             constexpr uint32_t kQHi = kFlags | (1024 >> 4), kKvHi = kFlags | (L::kGroup >> 4);
             const uint32_t base = __shfl_sync(0xffffffffu, sb, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t q_lo = (base + L::kQ) >> 4;
-            uint32_t k_lo = (base + L::kKRing) >> 4, v_lo = ((base + L::kVRing) >> 4) | ((1024 >> 4) << 16);   // of the slot
-            uint32_t step = 0, i = 0, ks = 0, vs = 0;
+            const uint32_t col_s = tm + L::kColS + s * 128, col_o = tm + L::kColO + s * D, col_p = tm + L::kColP + s * L::kPStep;
+            const uint32_t q_lo = ((base + L::kQ) >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
+            // of the slot
+            uint32_t k_lo = ((base + L::kKRing) >> 4) + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
+            uint32_t v_lo = ((base + L::kVRing) >> 4) | ((1024 >> 4) << 16);
+            const uint32_t bars = base + L::kBars, of_s = s * 8;
+            uint32_t step = 0, i = 0, ks = 0, vs = 0, items = 0, turns = 0;
             // a bit per barrier: the parity of the round that is waited for next
             uint32_t phase = 0;
-            constexpr uint32_t kPhK = 1u << 0, kPhV = 1u << 1, kPhQ = 1u << 2, kPhP = 1u << 4, kPhO = 1u << 6, kPhS = 1u << 8;
-            uint32_t begun = 0;                    // bits 0, 1: a tile has had scores; 2, 3: an item
-            auto wait = [&](int b, uint32_t bit) {
-                if (!mbar_wait(bar(b), (phase & bit) != 0)) abort = true;
+            constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
+            bool scored = false;
+            auto wait = [&](uint32_t b, uint32_t bit) {
+                if (!mbar_wait(b, (phase & bit) != 0)) abort = true;
                 phase ^= bit;
             };
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
                 auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
                 const int k0 = same(x->k0), k1 = same(x->k1), stride = same(x->stride);
-                const int a0 = same(x->a[0]), a1 = same(x->a[1]), e0 = same(x->e[0]), e1 = same(x->e[1]);
+                const int a = same(x->begin(s)), e = same(x->finish(s));
+                const int qs = stride == 2 ? 0 : s;
+                const bool q_shared = stride == 2 && k1 - k0 > 1;   // by both warps
+                const bool q0_loaded = same(x->a[0] < x->e[0]) != 0;
+                const uint32_t a_lo = q_lo + qs * (L::kQTile >> 4);
                 if (leader) item_done(i);
-                uint32_t q_here = 0;
+                bool q_here = false;
                 for (int k = k0 - stride; k < k1; ++k) {
                     const int kq = k + stride;
                     const bool pv = k >= k0, qk = kq < k1;
-                    bool k_here = false;
+                    const bool turn = stride == 1 || ((k - k0) & 1) == s;
+                    const bool w = pv && turn && k >= a && k < e, q = qk && turn && kq >= a && kq < e;
                     uint64_t odd = 0;
+                    // what the batch needs, before its turn
                     if (pv) {
-                        wait(L::READY + vs, kPhV);
+                        wait(bars + (L::READY + vs) * 8, kPhV);
                         if (vs != L::kV - 1) phase ^= kPhV;        // one parity for the ring's round
-                        odd = odd_words(step);
                     }
-                    // O_s += P_s V of step k
-                    auto weigh = [&](auto tile) {
-                        constexpr int s = decltype(tile)::value;
-                        const int a = s ? a1 : a0, e = s ? e1 : e0;
-                        if (k == a) {
-                            if (begun & (4u << s)) wait(L::O_FREE + s, kPhO << s);
-                            begun |= 4u << s;
+                    if (qk) {
+                        wait(bars + (L::K_FULL + ks) * 8, kPhK);
+                        if (ks != L::kK - 1) phase ^= kPhK;
+                    }
+                    if (q && !q_here) {
+                        // (in turn on one query tile, both warps wait for each of its rounds)
+                        wait(bars + (L::Q_FULL + qs) * 8, qs == s ? kPhQ : kPhQ1);
+                        q_here = true;
+                    }
+                    if (w) {
+                        odd = odd_words(step);
+                        if (k == a && items++ > 0) wait(bars + L::O_FREE * 8 + of_s, kPhO);
+                    }
+                    if (L::kApart && q) {
+                        if (scored) wait(bars + L::S_FREE * 8 + of_s, kPhS);
+                        scored = true;
+                    }
+                    if (!L::kApart && w && !mbar_wait(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                    if (turns > 0 || s == 1) wait(bars + L::TURN * 8 + of_s, kPhT);
+                    ++turns;
+                    tc05_fence_after_sync();
+                    // S = Q K^T of step kq
+                    auto score = [&]() {
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < E / 16; ++kk)
+                                umma_ss(col_s, a_lo + (kk >> 2) * (L::kQSlab >> 4) + (kk & 3) * 2, kQHi,
+                                        k_lo + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kKvHi, kIdescS, kk > 0);
+                            umma_commit(bars + L::S_FULL * 8 + of_s);
+                            mbar_arrive(bars + L::S_FULL * 8 + of_s);
+                            if (kq + stride >= e) {        // a tile of the queries is free when both warps say so
+                                umma_commit(bars + (L::Q_FREE + qs) * 8);
+                                if (!q_shared) mbar_arrive(bars + (L::Q_FREE + qs) * 8);
+                            }
                         }
-                        const uint32_t ph = (phase & (kPhP << s)) != 0;
-                        if (!mbar_wait(bar(L::P_HALF + s), ph)) abort = true;
-                        tc05_fence_after_sync();
-                        const uint32_t col_o = tm + L::kColO + s * D, col_p = tm + L::kColP + s * L::kPStep;
+                    };
+                    if (L::kApart && q) score();
+                    if (w) {
+                        // O += P V of step k
+                        if (L::kApart) {
+                            if (!mbar_wait(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                            tc05_fence_after_sync();
+                        }
                         if (leader && odd == 0) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k != a);
                         }
-                        wait(L::P_FULL + s, kPhP << s);
+                        wait(bars + L::P_FULL * 8 + of_s, kPhP);
                         tc05_fence_after_sync();
                         if (leader) {
                             if (odd == 0) {
@@ -459,67 +507,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int kk = 4; kk < 8; ++kk)
                                     umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
                             }
-                            if (L::kApart) umma_commit(bar(L::P_EMPTY + s));
-                            if (k + stride >= e) umma_commit(bar(L::O_DONE + s));
+                            if (L::kApart) umma_commit(bars + L::P_EMPTY * 8 + of_s);
+                            if (k + stride >= e) umma_commit(bars + L::O_DONE * 8 + of_s);
                         }
-                    };
-                    // S_s = Q_s K^T of step kq
-                    auto score = [&](auto tile) {
-                        constexpr int s = decltype(tile)::value;
-                        const int qs = stride == 2 ? 0 : s;
-                        if (!(q_here >> qs & 1)) wait(L::Q_FULL + qs, kPhQ << qs);
-                        q_here |= 1u << qs;
-                        if (!k_here) wait(L::K_FULL + ks, kPhK);
-                        k_here = true;
-                        if (L::kApart) {
-                            if (begun & (1u << s)) wait(L::S_FREE + s, kPhS << s);
-                            begun |= 1u << s;
-                        }
-                        tc05_fence_after_sync();
-                        const uint32_t a_lo = q_lo + qs * (L::kQTile >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
-                        const uint32_t b_lo = k_lo + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
-                        if (leader) {
-#pragma unroll
-                            for (int kk = 0; kk < E / 16; ++kk)
-                                umma_ss(tm + L::kColS + s * 128, a_lo + (kk >> 2) * (L::kQSlab >> 4) + (kk & 3) * 2, kQHi,
-                                        b_lo + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, kKvHi, kIdescS, kk > 0);
-                            umma_commit(bar(L::S_FULL + s));
-                            mbar_arrive(bar(L::S_FULL + s));
-                            if (kq + 1 >= (qs ? e1 : e0)) umma_commit(bar(L::Q_FREE + qs));
-                        }
-                    };
-                    auto both = [&](auto tile) {
-                        constexpr int s = decltype(tile)::value;
-                        const bool turn = stride == 1 || ((k - k0) & 1) == s;
-                        const int a = s ? a1 : a0, e = s ? e1 : e0;
-                        const bool w = pv && turn && k >= a && k < e, q = qk && turn && kq >= a && kq < e;
-                        if (L::kApart && q) score(tile);
-                        if (w) weigh(tile);
-                        if (!L::kApart && q) score(tile);
-                    };
-                    both(std::integral_constant<int, 0>());
-                    both(std::integral_constant<int, 1>());
-                    if (qk && !k_here) wait(L::K_FULL + ks, kPhK);
-                    abort = __any_sync(0xffffffffu, abort);
-                    if (abort) break;
+                    }
+                    if (!L::kApart && q) score();
+                    if (leader) mbar_arrive(bars + L::TURN * 8 + (of_s ^ 8));
                     if (pv) {
-                        if (leader) umma_commit(bar(L::V_EMPTY + vs));
+                        if (leader) umma_commit(bars + (L::V_EMPTY + vs) * 8);
                         v_lo += L::kTile >> 4;
                         ++step;
                         if (++vs == L::kV) vs = 0, v_lo -= L::kV * (L::kTile >> 4);
                     }
                     if (qk) {
-                        if (leader) umma_commit(bar(L::K_EMPTY + ks));
+                        if (leader) umma_commit(bars + (L::K_EMPTY + ks) * 8);
                         k_lo += L::kTile >> 4;
-                        if (ks != L::kK - 1) phase ^= kPhK;
                         if (++ks == L::kK) ks = 0, k_lo -= L::kK * (L::kTile >> 4);
                     }
+                    if (abort) break;
                 }
                 if (abort) break;
+                // rounds of query tile 0 that warp 12 had nothing of pass all the same
+                if (s == 1 && q0_loaded && !(stride == 2 && q_here)) phase ^= kPhQ1;
             }
             // every product has completed before tensor memory is freed
-            if (leader) umma_commit(bar(L::END));
-            mbar_wait(bar(L::END), 0);
+            if (leader) umma_commit(bars + (L::END + s) * 8);
+            mbar_wait(bars + (L::END + s) * 8, 0);
             __syncwarp();
         } else if (warp < kQWarp + 2) {
             // query rows of tile s (the scores of rows that are not there go nowhere):
