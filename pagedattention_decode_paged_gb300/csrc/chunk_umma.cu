@@ -239,15 +239,16 @@ struct Layout {
         ITEM_EMPTY = ITEM_FULL + kItems,   // [kItems] all who need it are done with it
         PAIR = ITEM_EMPTY + kItems,   // sums and maxima (or squares) of rows for the other tile's threads
         PAIR_FREE = PAIR + 1,         // have been read
-        TURN = PAIR_FREE + 1,      // [2] the tensor core is tile s's to use
+        WARM = PAIR_FREE + 1,      // the rows' threads have been through a step
+        TURN = WARM + 1,           // [2] the tensor core is tile s's to use
         END = TURN + 2,            // [2]
         NBARS = END + 2
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
     static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
     static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][2] a V tile's 64 rows are not all finite
-    static constexpr uint32_t kItem = kOdd + kBadRing * 8;    // [kItems]
-    static constexpr uint32_t kPair = kItem + kItems * sizeof(Share);   // [2][128] sums and maxima (or squares) of rows
+    static constexpr uint32_t kItem = kOdd + kBadRing * 8;    // [kItems], and one of no rows
+    static constexpr uint32_t kPair = (kItem + (kItems + 1) * sizeof(Share) + 15) & ~15u;   // [2][128] sums and maxima (or squares) of rows
     static constexpr uint32_t kEnd = kPair + 2 * 128 * 4;
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
     static constexpr size_t kBytes = 1024 + kEnd;
@@ -297,9 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == L::O_FREE || i == L::O_FREE + 1) count = 8;      // twice those of a tile, or both tiles'
             if (i == L::PAIR) count = DIFF ? 8 : 4;
             if (i == L::PAIR_FREE) count = 4;
+            if (i == L::WARM) count = 8;
             if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 14;   // 8 warps of rows, 2, 2, 2
             mbar_init(bar(i), count);
         }
+        Share *none = reinterpret_cast<Share *>(smem + L::kItem) + kItems;
+        *none = Share{};
+        none->stride = none->k1 = none->e[0] = none->e[1] = 1;
+        none->all_hi[0] = none->all_hi[1] = -1;    // as a tile that not all rows see alike
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
         if (q_tokens > 0) prefetch_tensormap(&qmap);
@@ -426,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
             bool scored = false;
+            if (!mbar_wait(bar(L::WARM), 0)) abort = true;
             auto wait = [&](uint32_t b, uint32_t bit) {
                 if (!mbar_wait(b, (phase & bit) != 0)) abort = true;
                 phase ^= bit;
@@ -640,12 +647,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             abort = __any_sync(0xffffffffu, abort);
             return !abort;
         };
-        for (const Share *xi; (xi = item(i)) != nullptr; ++i) {
+        // The first time through is a step of no rows on whatever tensor memory holds,
+        // while the first tiles are on their way: it fetches the instructions.
+        bool warm = false;
+        for (;;) {
+            const Share *xi = warm ? item(i) : ring + kItems;
+            if (xi == nullptr) break;
             const Share &sh = *xi;
             const int stride = sh.stride;
             const int r0 = DIFF || stride == 2 ? 0 : s * 128, row = r0 + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;
-            const bool idle = r0 + (warp & 3) * 32 >= sh.nrows;       // none of the warp's rows is
+            const bool idle = warm && r0 + (warp & 3) * 32 >= sh.nrows;   // none of the warp's rows is
             const int pos = sh.pos + n / p.G;
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
@@ -653,8 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             bool row_bad = false;
             for (int k = sh.begin(s); k < k_end; k += stride) {
-                if (!wait(bar(L::S_FULL + s), ns & 1)) break;
-                ++ns;
+                if (warm) {
+                    if (!wait(bar(L::S_FULL + s), ns & 1)) break;
+                    ++ns;
+                }
                 if (idle) {
                     // in step with the others: an arrival for the next step would count for this one
                     if (L::kApart && lane == 0) mbar_arrive(bar(L::S_FREE + s));
@@ -668,12 +682,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc05_fence_after_sync();
                 uint32_t v[128];
                 auto f = [&v](int i) { return __uint_as_float(v[i]); };
-                // the maximum of the first half while the second is on its way
-                tmem_ld32(col_s, v);
-                tmem_ld32(col_s + 32, v + 32);
                 const uint32_t step = g + (uint32_t)(k - sh.k0);
                 const uint32_t bad = badm[step % kBadRing];
                 const int t0 = (sh.lo + k) * kKT;
+                // Code that runs seldom is kept in loops: what it costs is its fetch (the
+                // first step of a launch takes four times the others).
+                if (sh.partial(s, k)) {
+                    const int lo = row_lo - t0;
+                    const uint32_t range = (uint32_t)(row_hi - row_lo);
+#pragma unroll 1
+                    for (int c = 0; c < kKT; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(col_s + c, x);
+                        tmem_landed<32>(x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if ((uint32_t)(c + i - lo) > range) x[i] = 0xff800000u;
+                        tmem_st16(col_s + c, x);
+                        tmem_st16(col_s + c + 16, x + 16);
+                    }
+                    tmem_wait_st();
+                }
+                // the maximum of the first half while the second is on its way
+                tmem_ld32(col_s, v);
+                tmem_ld32(col_s + 32, v + 32);
                 tmem_landed<64>(v);
                 tmem_ld32(col_s + 64, v + 64);
                 tmem_ld32(col_s + 96, v + 96);
@@ -688,19 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (L::kApart) {
                     tc05_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::S_FREE + s));
-                }
-                if (sh.partial(s, k)) {
-                    const int lo = row_lo - t0, hi = row_hi - t0;
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i < lo || i > hi) v[i] = 0xff800000u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        m4[j] = -INFINITY;
-#pragma unroll
-                        for (int i = j; i < 64; i += 4) m4[j] = fmaxf(m4[j], f(i));
-                    }
+                    if (lane == 0 && warm) mbar_arrive(bar(L::S_FREE + s));
                 }
                 if (bad != 0) {
                     const int b0 = max(0, row_lo - t0) >> 3, b1 = min(kKT - 1, row_hi - t0) >> 3;   // groups of 8 it sees
@@ -719,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (grown) m = mx;
                     l *= alpha;
                     if (k > sh.begin(s)) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(col_o + c, o);
@@ -748,13 +768,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                         tc05_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(L::P_HALF + s));
+                        if (lane == 0 && warm) mbar_arrive(bar(L::P_HALF + s));
                     }
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 tmem_wait_st();
-                if (bad != 0 || sh.partial(k)) {
+                if (warm && (bad != 0 || sh.partial(k))) {
                     const uint32_t slot = step % L::kV;
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
                     if (odd_words(step) != 0) {
@@ -802,7 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc05_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::P_FULL + s));
+                if (lane == 0 && warm) mbar_arrive(bar(L::P_FULL + s));
+            }
+            if (!warm) {
+                if (lane == 0) mbar_arrive(bar(L::WARM));
+                warm = true;
+                continue;
             }
             g += (uint32_t)(sh.k1 - sh.k0);
             if (abort) break;
@@ -821,18 +846,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mask = mine ? 1u << s : 0;
                 float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
                 float *dst = rec + (s * 128 + r) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(col_o + c, o);
+                    tmem_landed<32>(o);
+                    if (!mine)
 #pragma unroll
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0;
-                    if (mine) {
-                        tmem_ld16(col_o + c, o);
-                        tmem_landed<16>(o);
-                    }
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
                     if (there)
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
+                        for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
                 if (there) {
@@ -846,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
                         tc05_fence_after_sync();
                         const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             uint32_t o[32], w[16];
                             tmem_ld32(col_o + c, o);
@@ -885,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float sum = f0 * l + f1 * l1, inv = sum == 0.f ? 0.f : 1.f / sum;
                             f0 *= inv;
                             f1 *= inv;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t o0[16], o1[16], w[8];
                                 tmem_ld16(col_o + c, o0);
@@ -912,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05_fence_after_sync();
                     if (!idle) {
                         const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16], w[8];
                             tmem_ld16(col_o + c, o);
@@ -944,23 +968,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int head = sh.hk * p.G + n % p.G;
                 const float f0 = l0 == 0.f ? 0.f : 1.f / l0;
                 const float f1 = there ? -__ldg(p.lambdas + head) * (l1 == 0.f ? 0.f : 1.f / l1) : 0.f;
-                float y[D / 2], sq = 0.f;
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 16) {
+                // 16 columns of the difference
+                auto difference = [&](int c, float (&y)[16]) {
                     uint32_t o0[16], o1[16];
                     tmem_ld16(tmem + lanes + L::kColO + s * (D / 2) + c, o0);
                     tmem_ld16(tmem + lanes + L::kColO + D + s * (D / 2) + c, o1);
                     tmem_landed<16>(o0);
                     pin16(o1);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        y[c + i] = fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o0[i]) * f0);
-                        sq = fmaf(y[c + i], y[c + i], sq);
-                    }
-                }
+                    for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o0[i]) * f0);
+                };
                 float f2 = p.out_scale;
                 const T *w = reinterpret_cast<const T *>(p.norm_weight);
                 if (w != nullptr) {
+                    float sq = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 16) {
+                        float y[16];
+                        difference(c, y);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sq = fmaf(y[i], y[i], sq);
+                    }
                     // every thread has read the sums before squares take their place
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(L::PAIR));
@@ -973,21 +1001,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f2 *= 1.f / sqrtf(sq * (1.f / D) + p.eps);
                 }
                 T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + n / p.G) * p.H + head) * D + s * (D / 2);
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
+                    float y[16];
+                    difference(c, y);
 #pragma unroll
-                for (int c = 0; c < D / 2; c += 8) {
-                    float wf[8];
-                    if (w != nullptr) {
-                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(w + s * (D / 2) + c));
-                        Elem<T>::unpack(q, wf);
-                    }
-                    uint32_t o[4];
+                    for (int h = 0; h < 16; h += 8) {
+                        float wf[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = y[c + 2 * i] * f2 * (w != nullptr ? wf[2 * i] : 1.f);
-                        const float b = y[c + 2 * i + 1] * f2 * (w != nullptr ? wf[2 * i + 1] : 1.f);
-                        o[i] = zero ? 0u : Elem<T>::pack2(a, b);
+                        for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+                        if (w != nullptr) Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(w + s * (D / 2) + c + h)), wf);
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = zero ? 0u : Elem<T>::pack2(y[h + 2 * i] * f2 * wf[2 * i], y[h + 2 * i + 1] * f2 * wf[2 * i + 1]);
+                        if (there) *reinterpret_cast<uint4 *>(dst + c + h) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    if (there) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 // the next item's sums come after all have read these
                 __syncwarp();
@@ -1005,6 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) item_done(i);
+            ++i;
         }
     }
     if (abort && lane == 0) report(p.err_word, PA_DEVERR_TIMEOUT);
