@@ -87,7 +87,7 @@ cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const Choice &c,
 
 // Two records per CTA, then its cut.
 size_t cuts_at(const pa::ChunkPlan &plan) { return ((size_t)2 * plan.grid * plan.rec_floats * 4 + 15) & ~(size_t)15; }
-size_t ws_bytes(const pa::ChunkPlan &plan) { return cuts_at(plan) + (size_t)plan.grid * sizeof(int4); }
+size_t ws_bytes(const pa::ChunkPlan &plan) { return cuts_at(plan) + (size_t)plan.grid * sizeof(pa::ChunkCut); }
 
 pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, int64_t q_stride, int32_t max_tokens,
               const void *k_pool, const void *v_pool, const int32_t *block_table, const int32_t *positions,
@@ -137,6 +137,8 @@ pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, 
     p.H = s->num_heads;
     p.Hkv = s->num_kv_heads;
     p.G = G;
+    for (p.g_shift = 0; (int64_t)1 << p.g_shift < G;) ++p.g_shift;
+    p.g_mul = (uint32_t)((((uint64_t)1 << (31 + p.g_shift)) + G - 1) / G);
     p.MB = s->max_blocks_per_seq;
     p.bs = s->block_size;
     p.bs_shift = -1;
@@ -151,7 +153,7 @@ pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, 
         p.out_scale = diff->out_scale;
     }
     p.records = static_cast<float *>(workspace);
-    p.cuts = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + cuts_at(plan));
+    p.cuts = reinterpret_cast<pa::ChunkCut *>(static_cast<char *>(workspace) + cuts_at(plan));
     p.rec_floats = plan.rec_floats;
     const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
     if (launch(s, p, c, on) != cudaSuccess) return PA_ERR_CUDA;

@@ -55,27 +55,27 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
 
     zero_bad_sequences<float>(p, D, kThreads);
-    const int per = Sched<R, kKT>::build(p, pre);
-    const int64_t total = pre[(p.B + per - 1) / per];
-    const int W = working(total, gridDim.x);
+    const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
+    const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
     Sched<R, kKT> it;
-    const bool has = (int)blockIdx.x < W;
-    if (has) it.seek(p, pre, per, slice_begin(blockIdx.x, total, W), slice_begin(blockIdx.x + 1, total, W));
-    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
+    const bool has = (int)blockIdx.x < slices.W;
+    if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
+    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
     if (!has) return;
 
     const int map = DIFF ? ty / 8 : 0;         // of this thread's rows 4 ty .. 4 ty + 3
     do {
         const Item x = it.x;
         const int n0 = x.i * R, nrows = min(R, x.cnt * p.G - n0);
-        const int tmin = n0 / p.G, tmax = (n0 + nrows - 1) / p.G;
+        const int tmin = (int)by_group(p, n0), tmax = (int)by_group(p, n0 + nrows - 1);
         const int need_lo = p.window > 0 ? max(0, x.pos + tmin - p.window + 1) : 0, need_hi = x.pos + tmax;
         const int wlo_max = p.window > 0 ? max(0, x.pos + tmax - p.window + 1) : 0;
         for (int c = tid; c < kRows * (E / 4); c += kThreads) {
             const int row = c / (E / 4), ch = c % (E / 4), r = row % R, m = row / R, n = n0 + r;
             const float *src = reinterpret_cast<const float *>(p.q);
             if (r < nrows)
-                src += ((int64_t)x.b * p.T + n / p.G) * p.q_stride + (int64_t)(x.hk * p.G + n % p.G) * D + m * E + ch * 4;
+                src += ((int64_t)x.b * p.T + by_group(p, n)) * p.q_stride +
+                       (int64_t)(x.hk * p.G + (n - (int)by_group(p, n) * p.G)) * D + m * E + ch * 4;
             cp16(sb + L::kQ + (row * L::kQPitch + ch * 4) * 4, src, r < nrows);
         }
         auto look_up = [&](int k) -> int64_t {     // place of row tid of tile k: -1 not needed, -2 bad
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (ty * 4 + i) % R;
-            const int pos = x.pos + (n0 + r) / p.G;
+            const int pos = x.pos + (int)by_group(p, n0 + r);
             row_hi[i] = r < nrows ? pos : INT32_MAX;           // rows that are not there may see anything
             row_lo[i] = r < nrows && p.window > 0 ? max(0, pos - p.window + 1) : 0;
         }
@@ -242,10 +242,12 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = ty * 4 + i;
-            float *dst = cut ? rec + row * D : sk + row * L::kPitch;
             const float inv = cut ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
-            for (int j = 0; j < NV; ++j) dst[tx * V + (j / V) * 16 * V + j % V] = o[i][j] * inv;
+            for (int j = 0; j < NV; ++j) {
+                const int c = tx * V + (j / V) * 16 * V + j % V;
+                *(cut ? record_at(rec, kRows, row, c) : sk + row * L::kPitch + c) = o[i][j] * inv;
+            }
             if (tx == 0) {
                 if (cut) {
                     rec[kRows * D + row] = m[i];
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
                 const int n = n0 + r, e = D >= 32 ? lane * N : lane & (D - 1);
                 finish_row<float, D, DIFF>(p, sk + r * L::kPitch + e, sk + (kRows / 2 + r) * L::kPitch + e,
                                            sums[r] < 0.f || (DIFF && sums[kRows / 2 + r] < 0.f),
-                                           (int64_t)x.b * p.T + n / p.G, x.hk * p.G + n % p.G);
+                                           (int64_t)x.b * p.T + by_group(p, n), x.hk * p.G + n - (int)by_group(p, n) * p.G);
             }
             __syncthreads();
         }

@@ -3,10 +3,13 @@
 // the log-sum-exp identity (rescale each share's sum and weighted V by
 // 2^(m_s - M) for the overall maximum M), as the split-KV reduce does.
 //
-// CTA (w, y) reads cuts[w]; where an item begins to be cut there, its rows are
-// spread over the warps of the y.  A row's records are read once, 128 bytes
-// and more at a time; at most two records per CTA of the first launch exist,
-// so the whole launch reads at most 2 * grid of them.
+// CTA (w, y) reads cuts[w]; where an item begins to be cut there, it joins rows
+// 32 y to 32 y + 31 of it: lane r has row r, warp g a part of the columns, so
+// that a record's rows are read in whole lines, each once; at most two records
+// per CTA of the first launch exist, so the whole launch reads at most 2 * grid
+// of them.  Few rows leave lanes over: those take the records in turn (1 token of 8
+// heads behind 131071 of them, 38 records each: 123 us without).  The joined
+// rows go through shared memory to a warp each.
 #include "chunk_sched.cuh"
 
 namespace pa {
@@ -14,96 +17,104 @@ namespace pa {
 namespace {
 
 constexpr int kMergeThreads = 256;
-constexpr int kMergeY = 8;
+constexpr int kMergeRows = 32;
 
+// rows: of a map in a record.
 template <typename T, int D, bool DIFF>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows, const int fold) {
     grid_dependency_wait();
     allow_dependents();
-    constexpr int N = D >= 32 ? D / 32 : 1, MAPS = DIFF ? 2 : 1;
+    constexpr int MAPS = DIFF ? 2 : 1;
+    constexpr int WARPS = kMergeThreads / 32, PARTS = D / 4 < WARPS ? D / 4 : WARPS, C4 = D / 4 / PARTS;   // float4 of a thread
+    __shared__ float joined[kMergeRows][D + 4];
+    __shared__ int zero[kMergeRows];
     const int w = blockIdx.x;
-    const int4 c = p.cuts[w];
-    if (c.x < 0) return;
-    const int lane = threadIdx.x & 31;
-    const int ctas = c.w - w + 2;
-    const int cnt = p.counts != nullptr ? __ldg(p.counts + c.x) : p.T;
-    const int n0 = c.z * rows, valid = min(rows, cnt * p.G - n0);
+    const ChunkCut cut = p.cuts[w];
+    const int r0 = blockIdx.y * kMergeRows;
+    if (cut.b < 0 || r0 >= cut.rows) return;
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     // states of a row: one of each CTA, or two (a short item's rows r and fold + r)
-    const bool two = valid <= fold;
-    const int sharers = two ? 2 * ctas : ctas;
+    const int two = cut.rows <= fold ? 1 : 0, states = (cut.last - w + 2) << two, all = rows * MAPS;
     auto record = [&](int s) {
-        const int cta = two ? s >> 1 : s;
-        return p.records + ((int64_t)(cta == 0 ? (w - 1) * 2 + 1 : (w - 1 + cta) * 2)) * p.rec_floats;
+        const int cta = s >> two;
+        return p.records + (int64_t)(cta == 0 ? (w - 1) * 2 + 1 : (w - 1 + cta) * 2) * p.rec_floats;
     };
-    auto row_of = [&](int s, int row) { return two && (s & 1) ? fold + row : row; };
-    for (int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < valid; r += kMergeY * (kMergeThreads / 32)) {
-        float o[MAPS][N];
-        bool bad = false;
-#pragma unroll
+    // rows of a warp: 8, 16 or 32; lanes `take` and on of a row take every `step`th state
+    const int left = cut.rows - r0, lrows = left <= 8 ? 8 : left <= 16 ? 16 : 32, step = 32 / lrows, take = lane / lrows;
+    const int i_row = lane & (lrows - 1);
+    const int r = r0 + min(i_row, left - 1);
+    bool bad = false;
+    if (part < PARTS) {
+#pragma unroll 1
         for (int map = 0; map < MAPS; ++map) {
-            const int row = map * rows + r;
-            // lane s has the weight of share s, 32 shares at a time
+            auto row_of = [&](int s) { return map * rows + r + ((s & two) != 0 ? fold : 0); };
             float M = -INFINITY;
-            for (int s = lane; s < sharers; s += 32) {
-                const float *ml = record(s) + (int64_t)rows * MAPS * D + row_of(s, row);
+#pragma unroll 8
+            for (int s = take; s < states; s += step) {
+                const float *ml = record(s) + (int64_t)all * D + row_of(s);
                 M = fmaxf(M, __ldg(ml));
-                bad |= __ldg(ml + rows * MAPS) < 0.f;
+                bad |= __ldg(ml + all) < 0.f;
             }
-            M = warp_max_f32(M);
-            bad = __any_sync(0xffffffffu, bad);
+            for (int h = lrows; h < 32; h <<= 1) {
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, h));
+                bad |= __shfl_xor_sync(0xffffffffu, (int)bad, h) != 0;
+            }
             float L = 0.f;
+            float4 acc[C4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[map][i] = 0.f;
-            for (int s0 = 0; s0 < sharers; s0 += 32) {
-                float f = 0.f;
-                if (s0 + lane < sharers) {
-                    const float *ml = record(s0 + lane) + (int64_t)rows * MAPS * D + row_of(s0 + lane, row);
-                    f = merge_weight(__ldg(ml), M);
-                    L += f * __ldg(ml + rows * MAPS);
-                }
-                const int here = min(32, sharers - s0);
-                // 8 shares' values on their way at once
-                for (int s1 = 0; s1 < here; s1 += 8) {
-                    float a[8][N];
+            for (int i = 0; i < C4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int s = take; s < states; s += step) {
+                const int row = row_of(s);
+                const float *rec = record(s), *ml = rec + (int64_t)all * D + row;
+                const float f = merge_weight(__ldg(ml), M);
+                L += f * __ldg(ml + all);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int s = s0 + min(s1 + j, here - 1);
-                        const float *src = record(s) + (int64_t)row_of(s, row) * D + lane * N;
-                        if (D >= 32 || lane < D) {
-                            if constexpr (N % 4 == 0) {
-#pragma unroll
-                                for (int i = 0; i < N; i += 4)
-                                    *reinterpret_cast<float4 *>(a[j] + i) = __ldg(reinterpret_cast<const float4 *>(src + i));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < N; ++i) a[j][i] = __ldg(src + i);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float fj = __shfl_sync(0xffffffffu, f, min(s1 + j, 31));
-                        if (s1 + j < here)
-#pragma unroll
-                            for (int i = 0; i < N; ++i) o[map][i] += fj * a[j][i];
-                    }
+                for (int i = 0; i < C4; ++i) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(rec) + (part * C4 + i) * all + row);
+                    acc[i].x += f * v.x, acc[i].y += f * v.y, acc[i].z += f * v.z, acc[i].w += f * v.w;
                 }
             }
+            for (int h = lrows; h < 32; h <<= 1) {
+                L += __shfl_xor_sync(0xffffffffu, L, h);
 #pragma unroll
-            for (int h = 16; h > 0; h >>= 1) L += __shfl_xor_sync(0xffffffffu, L, h);
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+                for (int i = 0; i < C4; ++i) {
+                    acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, h);
+                    acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, h);
+                    acc[i].z += __shfl_xor_sync(0xffffffffu, acc[i].z, h);
+                    acc[i].w += __shfl_xor_sync(0xffffffffu, acc[i].w, h);
+                }
+            }
+            float inv = L == 0.f ? 0.f : 1.f / L;
+            if (map == 1) {                        // o_1 - lambda o_2
+                const uint32_t n = cut.n0 + r;
+                inv *= -__ldg(p.lambdas + cut.hk * p.G + (int)(n - chunk::by_group(p, n) * p.G));
+            }
+            if (take != 0) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[map][i] *= inv;
+            for (int i = 0; i < C4; ++i) {
+                float4 &y = *reinterpret_cast<float4 *>(&joined[i_row][(part * C4 + i) * 4]);
+                const float4 before = map == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : y;
+                y = make_float4(fmaf(acc[i].x, inv, before.x), fmaf(acc[i].y, inv, before.y), fmaf(acc[i].z, inv, before.z),
+                                fmaf(acc[i].w, inv, before.w));
+            }
         }
-        const int n = n0 + r;
-        chunk::finish_row<T, D, DIFF>(p, o[0], o[MAPS - 1], bad, (int64_t)c.x * p.T + n / p.G, c.y * p.G + n % p.G);
+        if (part == 0 && take == 0) zero[i_row] = bad;
+    }
+    __syncthreads();
+    constexpr int N = D >= 32 ? D / 32 : 1;
+    const int at = D >= 32 ? lane * N : lane & (D - 1);
+    for (int i = part; i < min(kMergeRows, cut.rows - r0); i += WARPS) {
+        const uint32_t n = cut.n0 + r0 + i, t = chunk::by_group(p, n);
+        chunk::finish_row<T, D, DIFF>(p, &joined[i][at], nullptr, zero[i] != 0, (int64_t)cut.b * p.T + t,
+                                      cut.hk * p.G + (int)(n - t * p.G));
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)plan.grid, kMergeY, 1);
+    cfg.gridDim = dim3((unsigned)plan.grid, (unsigned)((plan.rows + kMergeRows - 1) / kMergeRows), 1);
     cfg.blockDim = dim3(kMergeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -81,13 +81,12 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     zero_bad_sequences<T>(p, D, kThreads);
-    const int per = Sched<R, kKT>::build(p, pre);
-    const int64_t total = pre[(p.B + per - 1) / per];
-    const int W = working(total, gridDim.x);
+    const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
+    const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
     Sched<R, kKT> it;
-    const bool has = (int)blockIdx.x < W;
-    if (has) it.seek(p, pre, per, slice_begin(blockIdx.x, total, W), slice_begin(blockIdx.x + 1, total, W));
-    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
+    const bool has = (int)blockIdx.x < slices.W;
+    if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
+    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
     if (!has) return;
 
     const int map = DIFF ? warp >> 1 : 0;
@@ -95,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     do {
         const Item x = it.x;
         const int n0 = x.i * R, nrows = min(R, x.cnt * p.G - n0);
-        const int tmin = n0 / p.G, tmax = (n0 + nrows - 1) / p.G;
+        const int tmin = (int)by_group(p, n0), tmax = (int)by_group(p, n0 + nrows - 1);
         const int need_lo = p.window > 0 ? max(0, x.pos + tmin - p.window + 1) : 0, need_hi = x.pos + tmax;
         const int wlo_max = p.window > 0 ? max(0, x.pos + tmax - p.window + 1) : 0;
         // query rows: row m * R + r holds map m of row r
@@ -103,7 +102,8 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
             const int row = c / (E / 8), ch = c % (E / 8), r = row % R, m = row / R, n = n0 + r;
             const T *src = reinterpret_cast<const T *>(p.q);
             if (r < nrows)
-                src += ((int64_t)x.b * p.T + n / p.G) * p.q_stride + (int64_t)(x.hk * p.G + n % p.G) * D + m * E + ch * 8;
+                src += ((int64_t)x.b * p.T + by_group(p, n)) * p.q_stride +
+                       (int64_t)(x.hk * p.G + (n - (int)by_group(p, n) * p.G)) * D + m * E + ch * 8;
             cp16(sb + L::kQ + at<E>(row, ch), src, r < nrows);
         }
         // places of the rows of tile k: -1 not needed, -2 bad
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = wr + lane / 4 + 8 * h;
-            const int pos = x.pos + (n0 + r) / p.G;
+            const int pos = x.pos + (int)by_group(p, n0 + r);
             row_hi[h] = r < nrows ? pos : INT32_MAX;           // rows that are not there may see anything
             row_lo[h] = r < nrows && p.window > 0 ? max(0, pos - p.window + 1) : 0;
         }
@@ -298,11 +298,13 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = warp * 16 + lane / 4 + 8 * h;
-            float *dst = cut ? rec + row * D : stage + row * L::kPitch;
             const float inv = cut ? 1.f : l[h] == 0.f ? 0.f : 1.f / l[h];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2 *>(dst + i * 8 + (lane & 3) * 2) = make_float2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+            for (int i = 0; i < D / 8; ++i) {
+                const int c = i * 8 + (lane & 3) * 2;
+                float *dst = cut ? record_at(rec, kRows, row, c) : stage + row * L::kPitch + c;
+                *reinterpret_cast<float2 *>(dst) = make_float2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
+            }
             if ((lane & 3) == 0) {
                 if (cut) {
                     rec[kRows * D + row] = m[h];
@@ -318,8 +320,8 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
                 const int n = n0 + r;
                 finish_row<T, D, DIFF>(p, stage + r * L::kPitch + lane * (D / 32),
                                        stage + (kRows / 2 + r) * L::kPitch + lane * (D / 32),
-                                       sums[r] < 0.f || (DIFF && sums[kRows / 2 + r] < 0.f), (int64_t)x.b * p.T + n / p.G,
-                                       x.hk * p.G + n % p.G);
+                                       sums[r] < 0.f || (DIFF && sums[kRows / 2 + r] < 0.f), (int64_t)x.b * p.T + by_group(p, n),
+                                       x.hk * p.G + n - (int)by_group(p, n) * p.G);
             }
             __syncthreads();
         }

@@ -17,7 +17,9 @@
 // if it begins an item that goes on in the next slice; and CTA w writes
 // cuts[w]: which item its slice begins inside of, if that item's first tile
 // belongs to the slice before, and the last CTA that shares it.  The second
-// launch joins them.  No CTA waits for another.
+// launch joins them.  No CTA waits for another.  In a record 4 neighbouring
+// columns of neighbouring rows lie side by side, so that a row to a thread is
+// written and read in whole lines.
 //
 // The counts and positions are on the device, so every CTA builds the sums over
 // sequences itself.  How many tiles the first items of a sequence have is in
@@ -65,6 +67,13 @@ static __device__ __noinline__ uint64_t quotient(uint64_t a, uint64_t b) {
     return a / b;
 }
 
+// n / G for n < 2^31: with l = ceil(log2 G), the product with ceil(2^(31 + l) / G),
+// shifted right by 31 + l (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", theorem 4.2).
+__device__ __forceinline__ uint32_t by_group(const ChunkParams &p, uint32_t n) {
+    return p.g_shift == 0 ? n : __umulhi(n, p.g_mul) >> (p.g_shift - 1);
+}
+
 // sum over i < n of floor((a i + b) / m)
 __device__ __forceinline__ int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
     uint64_t s = 0;
@@ -95,8 +104,8 @@ struct Sched {
     static __device__ __forceinline__ int tiles(const ChunkParams &p, int pos, int cnt, int i, int *lo) {
         const uint32_t rows = (uint32_t)cnt * (uint32_t)p.G, r0 = (uint32_t)i * R;
         const uint32_t last = min(r0 + (uint32_t)R, rows) - 1;
-        const int hi = (int)((uint32_t)pos + last / (uint32_t)p.G) / KT;
-        *lo = p.window > 0 ? (int)max((int64_t)0, (int64_t)pos + r0 / (uint32_t)p.G - p.window + 1) / KT : 0;
+        const int hi = (int)((uint32_t)pos + by_group(p, last)) / KT;
+        *lo = p.window > 0 ? max(0, pos + (int)by_group(p, r0) - p.window + 1) / KT : 0;
         return hi - *lo + 1;
     }
     static __device__ __forceinline__ int items(const ChunkParams &p, int cnt) {
@@ -126,12 +135,13 @@ struct Sched {
     Item x;
     int64_t first;             // the current item's first tile
 
-    // Sums over groups of sequences; pre: [kGroups + 1] in shared memory.  All
-    // threads of the CTA call it; it ends with a barrier.  Returns the sequences
-    // of a group.
-    static __device__ __forceinline__ int build(const ChunkParams &p, int64_t *pre) {
+    // Sums over groups of sequences; pre: [kGroups + 1] in shared memory.  Threads
+    // 0 to n - 1 (whole warps) call it, with a named barrier of their own; it ends
+    // with that barrier.  Returns the sequences of a group.
+    static __device__ __forceinline__ int build(const ChunkParams &p, int64_t *pre, int tid, int n, int barrier) {
         const int per = (p.B + kGroups - 1) / kGroups, groups = (p.B + per - 1) / per;
-        for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+        auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(n) : "memory"); };
+        for (int g = tid; g < groups; g += n) {
             int64_t s = 0;
             for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) {
                 int pos, error;
@@ -143,23 +153,23 @@ struct Sched {
             }
             pre[g + 1] = s;
         }
-        __syncthreads();
-        if (threadIdx.x < 32) {                    // inclusive sums, 32 at a time
+        sync();
+        if (tid < 32) {                            // inclusive sums, 32 at a time
             int64_t run = 0;
             for (int g0 = 0; g0 < groups; g0 += 32) {
-                const int g = g0 + threadIdx.x;
+                const int g = g0 + tid;
                 int64_t v = g < groups ? pre[g + 1] : 0;
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-                    if ((int)threadIdx.x >= o) v += y;
+                    if (tid >= o) v += y;
                 }
                 if (g < groups) pre[g + 1] = run + v;
                 run += __shfl_sync(0xffffffffu, v, 31);
             }
-            if (threadIdx.x == 0) pre[0] = 0;
+            if (tid == 0) pre[0] = 0;
         }
-        __syncthreads();
+        sync();
         return per;
     }
 
@@ -209,7 +219,7 @@ struct Sched {
             int first_tile;
             const int n = i0 + lane < x.nq ? tiles(p, x.pos, x.cnt, i0 + lane, &first_tile) : 0;
             int incl = n;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
@@ -247,21 +257,37 @@ struct Sched {
     __device__ __forceinline__ bool cut() const { return x.k0 > 0 || x.k1 < x.n; }
 };
 
-// Working CTAs of the grid: no more than there are tiles.
-__device__ __forceinline__ int working(int64_t total, int grid) { return (int)min((int64_t)grid, total); }
-__device__ __forceinline__ int64_t slice_begin(int w, int64_t total, int W) { return (int64_t)quotient(w * total, W); }
-__device__ __forceinline__ int slice_owner(int64_t t, int64_t total, int W) {
-    return (int)quotient((t + 1) * W - 1, total);
-}
+// Slices: the working CTAs of the grid, no more than there are tiles; CTA w's
+// begins at floor(w total / W) = w q + floor(w r / W) with total = q W + r.
+struct Slices {
+    int64_t total, q;
+    int W, r;
+    __device__ __forceinline__ Slices(int64_t tiles, int grid) : total(tiles) {
+        W = (int)min((int64_t)grid, total);
+        q = W > 0 ? (int64_t)quotient(total, W) : 0;
+        r = (int)(total - q * W);
+    }
+    __device__ __forceinline__ int64_t begin(int w) const { return w * q + (uint32_t)(w * r) / (uint32_t)W; }
+    __device__ __forceinline__ int owner(int64_t t) const { return (int)quotient((t + 1) * W - 1, total); }
+};
 
 // This CTA's entry of the cuts, from the first share of its slice (has: it has
-// one).  x: item's sequence (-1: nothing begins to be joined here), kv head,
-// item of the head, last CTA that shares it.
+// one).
 template <int R, int KT>
-__device__ __forceinline__ int4 cut_entry(const Sched<R, KT> &s, bool has, int64_t total, int W) {
-    if (!has || s.x.k0 == 0 || s.first < slice_begin((int)blockIdx.x - 1, total, W)) return make_int4(-1, 0, 0, 0);
-    return make_int4(s.x.b, s.x.hk, s.x.i, slice_owner(s.first + s.x.n - 1, total, W));
+__device__ __forceinline__ ChunkCut cut_entry(const ChunkParams &p, const Sched<R, KT> &s, bool has, const Slices &sl) {
+    ChunkCut c{};
+    c.b = -1;
+    if (!has || s.x.k0 == 0 || s.first < sl.begin((int)blockIdx.x - 1)) return c;
+    c.b = s.x.b;
+    c.hk = s.x.hk;
+    c.n0 = s.x.i * R;
+    c.rows = min(R, s.x.cnt * p.G - c.n0);
+    c.last = sl.owner(s.first + s.x.n - 1);
+    return c;
 }
+
+// Columns c to c + 3 of a row of a record (of `rows` rows in all).
+__device__ __forceinline__ float *record_at(float *rec, int rows, int row, int c) { return rec + ((c >> 2) * rows + row) * 4 + (c & 3); }
 
 // Report sequences whose arguments are out of range, and zero the rows of
 // those whose positions are; sequence b is CTA b % gridDim's.  The first `threads`
@@ -293,7 +319,8 @@ __device__ __forceinline__ int64_t row_offset(const ChunkParams &p, int b, int h
 // The last step of a row, by one warp: lane l has elements l*N .. l*N + N - 1
 // (N = D / 32, or one element for the first D lanes) of the first map's
 // weighted sum in o, already divided by its sum, and of the second map's in o2
-// (differential form).  A row that attended to a bad block is zeros.
+// (differential form; null: the difference is taken already).  A row that
+// attended to a bad block is zeros.
 template <typename T, int D, bool DIFF>
 __device__ __forceinline__ void finish_row(const ChunkParams &p, const float *o, const float *o2, bool bad, int64_t token,
                                            int head) {
@@ -307,7 +334,7 @@ __device__ __forceinline__ void finish_row(const ChunkParams &p, const float *o,
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            y[i] -= lam * o2[i];
+            if (o2 != nullptr) y[i] -= lam * o2[i];
             sq += y[i] * y[i];
         }
         if (p.norm_weight != nullptr) {

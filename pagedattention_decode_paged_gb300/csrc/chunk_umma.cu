@@ -86,7 +86,7 @@ struct Share {
             a[s] = e[s] = 0;
             if (s == 1) all_lo[1] = all_lo[0], all_hi[1] = all_hi[0];
             if (nr <= 0) continue;
-            const int first = pos + (n0 + r0) / p.G, last = pos + (n0 + r0 + nr - 1) / p.G;
+            const int first = pos + (int)by_group(p, n0 + r0), last = pos + (int)by_group(p, n0 + r0 + nr - 1);
             const int seen = p.window > 0 ? max(0, first - p.window + 1) : 0;
             a[s] = max(k0, seen / kKT - lo);
             e[s] = max(a[s], min(k1, last / kKT + 1 - lo));
@@ -138,6 +138,18 @@ __device__ __forceinline__ void tmem_landed(uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+// 32 columns of 16 lanes as the accumulators of a warp-level product have them: of
+// every 8 columns this thread gets columns 2 (lane % 4) and the next of lane / 4
+// in r[4 j], r[4 j + 1], of lane / 4 + 8 in r[4 j + 2], r[4 j + 3]
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -204,6 +216,77 @@ template <typename T>
 __device__ __forceinline__ bool non_finite(uint32_t w) {   // of either half
     constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
     return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// x[j] of lane i of a quad to x[i] of lane j
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4]) {
+    const bool odd = (threadIdx.x & 1) != 0, high = (threadIdx.x & 2) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + 1], 1);
+        if (odd) x[j] = y;
+        else x[j + 1] = y;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, high ? x[j] : x[j + 2], 2);
+        if (high) x[j] = y;
+        else x[j + 2] = y;
+    }
+}
+
+// Columns [0, N) of a warp's 32 rows to memory: O_a f0, with BOTH + O_b f1, each
+// times its element of w (null: 1).  Lane r has row r's factors, where it goes
+// (row), whether it goes at all (there), and whether it is zeros.  Quads of lanes
+// store 64 bytes of a row: a row to a lane would touch 32 lines with every store.
+template <typename T, int N, bool BOTH>
+__device__ __forceinline__ void store_rows(uint32_t o_a, uint32_t o_b, float f0, float f1, T *row, bool there, bool zero,
+                                           const T *w) {
+    const int lane = threadIdx.x & 31, q = lane & 3;
+    const uint32_t go = __ballot_sync(0xffffffffu, there), clear = __ballot_sync(0xffffffffu, zero);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        float fa[2], fb[2];
+        T *dst[2];
+        const int r0 = half * 16 + (lane >> 2);
+        if ((go >> (half * 16)) == 0) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            fa[h] = __shfl_sync(0xffffffffu, f0, r0 + 8 * h);
+            fb[h] = BOTH ? __shfl_sync(0xffffffffu, f1, r0 + 8 * h) : 0.f;
+            dst[h] = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r0 + 8 * h)) + q * 8;
+        }
+#pragma unroll 1
+        for (int c = 0; c < N; c += 32) {
+            uint32_t a[16], b[16];
+            tmem_ld_quads(o_a + ((uint32_t)(half * 16) << 16) + c, a);
+            if (BOTH) tmem_ld_quads(o_b + ((uint32_t)(half * 16) << 16) + c, b);
+            tmem_landed<16>(a);
+            if (BOTH) pin16(b);
+            uint32_t x[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float w0 = 1.f, w1 = 1.f;
+                if (w != nullptr) Elem<T>::unpack2(__ldg(reinterpret_cast<const uint32_t *>(w + c + j * 8 + q * 2)), w0, w1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float y0 = __uint_as_float(a[4 * j + 2 * h]) * fa[h], y1 = __uint_as_float(a[4 * j + 2 * h + 1]) * fa[h];
+                    if (BOTH) {
+                        y0 = fmaf(__uint_as_float(b[4 * j + 2 * h]), fb[h], y0);
+                        y1 = fmaf(__uint_as_float(b[4 * j + 2 * h + 1]), fb[h], y1);
+                    }
+                    x[h][j] = Elem<T>::pack2(y0 * w0, y1 * w1);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                quad_transpose(x[h]);
+                if (clear >> (r0 + 8 * h) & 1) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
+                if (go >> (r0 + 8 * h) & 1)
+                    *reinterpret_cast<uint4 *>(dst[h] + c) = make_uint4(x[h][0], x[h][1], x[h][2], x[h][3]);
+            }
+        }
+    }
 }
 
 // 128-byte swizzled rows: K and V tiles are [16 groups of 8 rows][D/64][8 rows]
@@ -316,18 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
         tc05_fence_before_sync();
     }
-    const int per = Schedule::build(p, pre);       // ends with a barrier
-    Schedule it;
-    bool has = false;
-    if (warp == kProducerWarp) {
-        const int64_t total = pre[(p.B + per - 1) / per];
-        const int W = working(total, gridDim.x);
-        has = (int)blockIdx.x < W;
-        if (has) it.seek(p, pre, per, slice_begin(blockIdx.x, total, W), slice_begin(blockIdx.x + 1, total, W));
-        if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(it, has, total, W);
-        __syncwarp();
-        fence_proxy_async_smem();                  // the ring's copies come after the sums
-    }
+    __syncthreads();
     tc05_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
     const Share *ring = reinterpret_cast<const Share *>(smem + L::kItem);
@@ -341,10 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto item_done = [&](uint32_t i) { mbar_arrive(bar(L::ITEM_EMPTY + i % kItems)); };   // one lane of a warp
 
     if (warp >= kProducerWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int per = Schedule::build(p, pre, threadIdx.x - kProducerWarp * 32, kThreads - kProducerWarp * 32, 1);
         if (warp == kProducerWarp) {
             // lane s copies box s (box_rows positions) of each tile; table entries are
             // looked up a tile ahead
+            const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
+            Schedule it;
+            bool has = (int)blockIdx.x < slices.W;
+            if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
+            if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
+            __syncwarp();
+            fence_proxy_async_smem();              // the ring's copies come after the sums
             const int boxes = kKT / box_rows;
             const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
             uint32_t g = 0, i = 0;
@@ -562,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(full, (uint32_t)(L::kQSlabs * q_tokens * p.G * 128));
 #pragma unroll
                         for (int h = 0; h < L::kQSlabs; ++h)
-                            tma_4d_g2s(qb + h * L::kQSlab, &qmap, 0, hk * p.G, b * p.T + n0 / p.G, DIFF && E == 64 ? s : h, full);
+                            tma_4d_g2s(qb + h * L::kQSlab, &qmap, 0, hk * p.G, b * p.T + (int)by_group(p, n0), DIFF && E == 64 ? s : h, full);
                     }
                     __syncwarp();
                 } else {
@@ -571,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int ch = lane % C;
                     const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride + (int64_t)hk * p.G * D +
                                    (DIFF && E == 64 ? s * E : 0) + ch * 8;
-                    int t = (n0 + lane / C) / p.G, h = (n0 + lane / C) - t * p.G;
+                    int t = (int)by_group(p, n0 + lane / C), h = (n0 + lane / C) - t * p.G;
 #pragma unroll 4
                     for (int r = lane / C; r < nr; r += RPI) {
                         cp16(qb + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D, true);
@@ -633,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rows of tile s: thread r has row r, the tensor-memory lane of its
         // warp's quarter
         // ------------------------------------------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
@@ -658,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r0 = DIFF || stride == 2 ? 0 : s * 128, row = r0 + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;
             const bool idle = warm && r0 + (warp & 3) * 32 >= sh.nrows;   // none of the warp's rows is
-            const int pos = sh.pos + n / p.G;
+            const int tok = (int)by_group(p, n), head = sh.hk * p.G + n - tok * p.G, pos = sh.pos + tok;
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const int k_end = sh.finish(s);
@@ -838,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             items[1] += active[1];
             if (row_bad) l = -1.f;
             if (row_bad && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+            T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + tok) * p.H + head) * D;
             uint32_t mask = 0;                     // whose O this warp has read, all of it or with the other tile's warps
             uint32_t weight = 2;
             if (sh.cut) {
@@ -845,7 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc05_fence_after_sync();
                 mask = mine ? 1u << s : 0;
                 float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
-                float *dst = rec + (s * 128 + r) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -857,33 +937,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (there)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(dst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            *reinterpret_cast<uint4 *>(record_at(rec, 256, s * 128 + r, c + i)) =
+                                make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
                 if (there) {
                     rec[256 * D + s * 128 + r] = m == -INFINITY ? -INFINITY : m * scale;
                     rec[256 * D + 256 + s * 128 + r] = l;
                 }
             } else if constexpr (!DIFF) {
-                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + n / p.G) * p.H + sh.hk * p.G + n % p.G) * D;
                 if (stride == 1) {
                     if (mine) {
                         if (!wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
                         tc05_fence_after_sync();
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32], w[16];
-                            tmem_ld32(col_o + c, o);
-                            tmem_landed<32>(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                w[i] = row_bad ? 0u
-                                               : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                            if (there)
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4)
-                                    *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                        }
+                        store_rows<T, D, false>(col_o, 0, l == 0.f ? 0.f : 1.f / l, 0.f, dst, there, row_bad, nullptr);
                         mask = 1u << s;
                     }
                 } else if (active[1]) {
@@ -905,28 +971,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!idle) {
                             const bool zero = l < 0.f || l1 < 0.f;
                             const float M = fmaxf(ms, m1);
-                            float f0 = merge_weight(ms, M), f1 = merge_weight(m1, M);
+                            const float f0 = merge_weight(ms, M), f1 = merge_weight(m1, M);
                             const float sum = f0 * l + f1 * l1, inv = sum == 0.f ? 0.f : 1.f / sum;
-                            f0 *= inv;
-                            f1 *= inv;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o0[16], o1[16], w[8];
-                                tmem_ld16(col_o + c, o0);
-                                tmem_ld16(col_o + D + c, o1);
-                                tmem_landed<16>(o0);
-                                pin16(o1);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float a = fmaf(__uint_as_float(o1[2 * i]), f1, __uint_as_float(o0[2 * i]) * f0);
-                                    const float b = fmaf(__uint_as_float(o1[2 * i + 1]), f1, __uint_as_float(o0[2 * i + 1]) * f0);
-                                    w[i] = zero ? 0u : Elem<T>::pack2(a, b);
-                                }
-                                if (there)
-#pragma unroll
-                                    for (int i = 0; i < 8; i += 4)
-                                        *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                            }
+                            store_rows<T, D, true>(col_o, col_o + D, f0 * inv, f1 * inv, dst, there, zero, nullptr);
                         }
                         mask = 3;
                     }
@@ -934,23 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (s == 0) {
                     if (!wait(bar(L::O_DONE), done[0])) break;
                     tc05_fence_after_sync();
-                    if (!idle) {
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16], w[8];
-                            tmem_ld16(col_o + c, o);
-                            tmem_landed<16>(o);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                w[i] = row_bad ? 0u
-                                               : Elem<T>::pack2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                            if (there)
-#pragma unroll
-                                for (int i = 0; i < 8; i += 4)
-                                    *reinterpret_cast<uint4 *>(dst + c + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                        }
-                    }
+                    if (!idle) store_rows<T, D, false>(col_o, 0, l == 0.f ? 0.f : 1.f / l, 0.f, dst, there, row_bad, nullptr);
                     mask = 1;
                 }
             } else {
@@ -965,7 +996,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(bar(L::PAIR), pairs++ & 1)) break;
                 const float l0 = pair[r], l1 = pair[128 + r];
                 const bool zero = l0 < 0.f || l1 < 0.f;
-                const int head = sh.hk * p.G + n % p.G;
                 const float f0 = l0 == 0.f ? 0.f : 1.f / l0;
                 const float f1 = there ? -__ldg(p.lambdas + head) * (l1 == 0.f ? 0.f : 1.f / l1) : 0.f;
                 // 16 columns of the difference
@@ -1000,24 +1030,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sq = pair[r] + pair[128 + r];
                     f2 *= 1.f / sqrtf(sq * (1.f / D) + p.eps);
                 }
-                T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + n / p.G) * p.H + head) * D + s * (D / 2);
-#pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
-                    float y[16];
-                    difference(c, y);
-#pragma unroll
-                    for (int h = 0; h < 16; h += 8) {
-                        float wf[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) wf[i] = 1.f;
-                        if (w != nullptr) Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(w + s * (D / 2) + c + h)), wf);
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i] = zero ? 0u : Elem<T>::pack2(y[h + 2 * i] * f2 * wf[2 * i], y[h + 2 * i + 1] * f2 * wf[2 * i + 1]);
-                        if (there) *reinterpret_cast<uint4 *>(dst + c + h) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                }
+                const uint32_t o = tmem + lanes + L::kColO + s * (D / 2);
+                store_rows<T, D / 2, true>(o, o + D, f0 * f2, f1 * f2, dst + s * (D / 2), there, zero,
+                                           w != nullptr ? w + s * (D / 2) : nullptr);
                 // the next item's sums come after all have read these
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::PAIR));

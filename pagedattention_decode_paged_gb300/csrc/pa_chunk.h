@@ -22,6 +22,7 @@ struct ChunkParams {
     int64_t block_stride_bytes;
     int32_t rows_per_block;    // block_stride / head_dim (tensor-map row pitch per block)
     int32_t B, T, H, Hkv, G, MB, bs;   // G = H / Hkv
+    uint32_t g_mul, g_shift;   // quotients by G: chunk::by_group
     int32_t bs_shift;          // log2(bs) when bs is a power of two, else -1
     int32_t window;
     float scale_log2;          // scale * log2(e)
@@ -32,8 +33,18 @@ struct ChunkParams {
     float out_scale;
     // workspace: per CTA two records of the rows' softmax states, and one cut
     float *records;
-    int4 *cuts;
+    struct ChunkCut *cuts;
     int32_t rec_floats;
+};
+
+// What the second launch joins for a CTA: rows of an item that CTA w - 1 began
+// and CTAs w to last went on with.
+struct ChunkCut {
+    int32_t b;                 // sequence; -1: nothing
+    int32_t hk;                // kv head
+    int32_t n0, rows;          // first of the head's rows, rows
+    int32_t last;
+    int32_t pad[3];
 };
 
 // What a kernel variant needs of the workspace on the current device.
