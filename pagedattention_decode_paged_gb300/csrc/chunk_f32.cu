@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
 
-    zero_bad_sequences<float>(p, D, kThreads);
+    zero_bad_sequences<float>(p, D, tid, kThreads);
     const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
     const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
     Sched<R, kKT> it;

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    zero_bad_sequences<T>(p, D, kThreads);
+    zero_bad_sequences<T>(p, D, tid, kThreads);
     const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
     const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
     Sched<R, kKT> it;

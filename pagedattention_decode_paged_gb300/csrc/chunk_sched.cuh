@@ -290,20 +290,20 @@ __device__ __forceinline__ ChunkCut cut_entry(const ChunkParams &p, const Sched<
 __device__ __forceinline__ float *record_at(float *rec, int rows, int row, int c) { return rec + ((c >> 2) * rows + row) * 4 + (c & 3); }
 
 // Report sequences whose arguments are out of range, and zero the rows of
-// those whose positions are; sequence b is CTA b % gridDim's.  The first `threads`
-// threads of the CTA call it.
+// those whose positions are; sequence b is CTA b % gridDim's.  Called by `threads`
+// threads, this one `tid`.
 template <typename T>
-__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D, int threads) {
+__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D, int tid, int threads) {
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         int pos, error;
         seq_of(p, b, &pos, &error);
         if (error == 0) continue;
-        if (threadIdx.x == 0) report(p.err_word, error);
+        if (tid == 0) report(p.err_word, error);
         if (error != PA_DEVERR_BAD_POS) continue;
         const int cnt = p.counts != nullptr ? p.counts[b] : p.T;
         const int64_t row = (int64_t)p.H * D, n = cnt * row;
         T *out = reinterpret_cast<T *>(p.out) + (int64_t)b * p.T * row;
-        for (int64_t i = threadIdx.x; i < n; i += threads) out[i] = Elem<T>::from_float(0.f);
+        for (int64_t i = tid; i < n; i += threads) out[i] = Elem<T>::from_float(0.f);
     }
 }
 

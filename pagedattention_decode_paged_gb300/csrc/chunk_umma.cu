@@ -16,13 +16,13 @@
 // its steps dealt to the two tiles in turn instead, and their states are joined
 // at its end.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the rows of tile 0 and 1; warp 8 the
-// schedule and the copies of K and V; warps 9 and 12 the products of tile 0 and 1,
-// warp 9 tensor memory; warps 10 and 11 the query rows; warps 14 and 15 look
-// over those V tiles that not all rows see alike: positions that no row sees
-// become zeros, and where another is not finite the rows' threads weigh that
-// tile's values one by one, each only those it sees (the product would let 0
-// times them reach every row).
+// Roles (512 threads): warps 0-3 and 4-7 the weights of tile 0 and 1; warp 8 the
+// schedule and the copies of K and V; warps 9 and 10 the products of tile 0 and 1,
+// warp 9 tensor memory; warp 11 the query rows; warps 12-15 the outputs, while the
+// others are at the next item, and before that a look at those V tiles that not all
+// rows see alike: positions that no row sees become zeros, and where another is
+// not finite the rows' threads weigh that tile's values one by one, each only
+// those it sees (the product would let 0 times them reach every row).
 //
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
 // maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
@@ -40,7 +40,7 @@ using namespace chunk;
 
 constexpr int kThreads = 512;
 constexpr int kKT = 128;                   // cache positions per tile
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kMmaWarp1 = 12, kFixWarp = 14;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 11, kOutWarp = 12;
 constexpr float kLazy = 8.f;
 constexpr int kBadRing = 8;
 constexpr int kItems = 4;                  // items of the schedule that roles may be apart
@@ -183,9 +183,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
         ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
-}
 // True in one lane of the warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -210,12 +207,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ bool non_finite(uint32_t w) {   // of either half
-    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-    return (w & e) == e || ((w >> 16) & e) == e;
 }
 
 // x[j] of lane i of a quad to x[i] of lane j
@@ -320,21 +311,21 @@ struct Layout {
         Q_FREE = Q_FULL + 2,       // [2]
         ITEM_FULL = Q_FREE + 2,    // [kItems] the item is there
         ITEM_EMPTY = ITEM_FULL + kItems,   // [kItems] all who need it are done with it
-        PAIR = ITEM_EMPTY + kItems,   // sums and maxima (or squares) of rows for the other tile's threads
-        PAIR_FREE = PAIR + 1,         // have been read
-        WARM = PAIR_FREE + 1,      // the rows' threads have been through a step
+        ROWS_FULL = ITEM_EMPTY + kItems,   // [2] an item's sums and maxima of rows
+        ROWS_FREE = ROWS_FULL + 2, // [2] have been read
+        WARM = ROWS_FREE + 2,      // the weights' threads have been through a step
         TURN = WARM + 1,           // [2] the tensor core is tile s's to use
         END = TURN + 2,            // [2]
         NBARS = END + 2
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
     static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
-    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][2] a V tile's 64 rows are not all finite
-    static constexpr uint32_t kItem = kOdd + kBadRing * 8;    // [kItems], and one of no rows
-    static constexpr uint32_t kPair = (kItem + (kItems + 1) * sizeof(Share) + 15) & ~15u;   // [2][128] sums and maxima (or squares) of rows
-    static constexpr uint32_t kEnd = kPair + 2 * 128 * 4;
+    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][4] a V tile's 32 rows are not all finite
+    static constexpr uint32_t kItem = kOdd + kBadRing * 16;   // [kItems], and one of no rows
+    static constexpr uint32_t kRows = (kItem + (kItems + 1) * sizeof(Share) + 15) & ~15u;   // [2][2][128] sums and maxima of rows
+    static constexpr uint32_t kEnd = kRows + 2 * 2 * 128 * 4;
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
-    static constexpr size_t kBytes = 1024 + kEnd;
+    static constexpr size_t kBytes = kEnd;
     static constexpr bool kApart = D == 64;                   // P has columns of its own
     static constexpr uint32_t kColS = 0, kColO = D == 64 ? 384 : 256;   // S_s at 128 s, O_s D columns each
     static constexpr uint32_t kColP = kApart ? 256 : 0, kPStep = kApart ? 64 : 128;
@@ -357,14 +348,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     using Schedule = Sched<R, kKT>;
     grid_dependency_wait();
     allow_dependents();
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) unsigned char smem[];   // swizzled tiles: 1024-byte aligned
     const uint32_t sb = smem_u32(smem);
     auto bar = [&](int i) { return sb + L::kBars + i * 8; };
     volatile uint32_t *badm = reinterpret_cast<volatile uint32_t *>(smem + L::kBad);
     volatile uint32_t *oddm = reinterpret_cast<volatile uint32_t *>(smem + L::kOdd);
     auto odd_words = [&](uint32_t step) {
-        return *reinterpret_cast<const volatile uint64_t *>(oddm + step % kBadRing * 2);
+        const volatile uint64_t *o = reinterpret_cast<const volatile uint64_t *>(oddm + step % kBadRing * 4);
+        return o[0] | o[1];
     };
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -372,17 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::NBARS; ++i) {
             int count = 1;
-            if (i >= L::READY && i < L::S_FULL) count = 2;            // the looking warps
+            if (i >= L::READY && i < L::S_FULL) count = 4;            // the looking warps
             if (i >= L::K_EMPTY && i < L::K_EMPTY + L::kK) count = 2; // the products of both tiles
             if (i >= L::V_EMPTY && i < L::V_EMPTY + L::kV) count = 2;
             if (i == L::S_FULL || i == L::S_FULL + 1) count = 2;      // the products, and what their warp knows
             if (i == L::Q_FREE || i == L::Q_FREE + 1) count = 2;
             if (i >= L::S_FREE && i < L::P_EMPTY) count = 4;          // the warps of a tile
-            if (i == L::O_FREE || i == L::O_FREE + 1) count = 8;      // twice those of a tile, or both tiles'
-            if (i == L::PAIR) count = DIFF ? 8 : 4;
-            if (i == L::PAIR_FREE) count = 4;
+            if (i == L::O_FREE || i == L::O_FREE + 1) count = 4;      // the warps of the outputs
+            if (i >= L::ROWS_FULL && i < L::WARM) count = 4;
             if (i == L::WARM) count = 8;
-            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 14;   // 8 warps of rows, 2, 2, 2
+            if (i >= L::ITEM_EMPTY && i < L::ITEM_EMPTY + kItems) count = 15;   // 8 warps of weights, 2, 1, 4
             mbar_init(bar(i), count);
         }
         Share *none = reinterpret_cast<Share *>(smem + L::kItem) + kItems;
@@ -489,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every copy has landed before the CTA may exit
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
             for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
-        } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+        } else if (warp < kQWarp) {
             // Products of tile s.  The whole warp walks the steps, so that what the
             // products are given is known to be the same in all lanes; one lane issues
             // them.  The two warps take turns at the tensor core: while one issues, the
@@ -614,95 +604,229 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (abort) break;
                 }
                 if (abort) break;
-                // rounds of query tile 0 that warp 12 had nothing of pass all the same
+                // rounds of query tile 0 that warp 10 had nothing of pass all the same
                 if (s == 1 && q0_loaded && !(stride == 2 && q_here)) phase ^= kPhQ1;
             }
             // every product has completed before tensor memory is freed
             if (leader) umma_commit(bars + (L::END + s) * 8);
             mbar_wait(bars + (L::END + s) * 8, 0);
             __syncwarp();
-        } else if (warp < kQWarp + 2) {
-            // query rows of tile s (the scores of rows that are not there go nowhere):
-            // one copy a slab where a tile is whole tokens, else rows of 16-byte copies
-            const int s = warp - kQWarp;
-            uint32_t items = 0, i = 0;
+        } else if (warp == kQWarp) {
+            // query rows (the scores of rows that are not there go nowhere): one copy a
+            // slab where a tile is whole tokens, else rows of 16-byte copies
+            uint32_t items[2] = {0, 0}, i = 0;
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                const int r0 = DIFF ? 0 : s * 128, n0 = x->n0 + r0, nr = min(128, x->nrows - r0);
-                const int b = x->b, hk = x->hk;
-                const bool active = x->begin(s) < x->finish(s) && !(s == 1 && x->stride == 2);
+                const int x_n0 = x->n0, nrows = x->nrows, b = x->b, hk = x->hk;
+                const bool active[2] = {x->a[0] < x->e[0], x->a[1] < x->e[1] && x->stride == 1};
                 __syncwarp();
                 if (lane == 0) item_done(i);
-                if (!active) continue;
-                if (items > 0 && !mbar_wait(bar(L::Q_FREE + s), (items - 1) & 1)) abort = true;
-                abort = __any_sync(0xffffffffu, abort);
-                if (abort) break;
-                const uint32_t qb = sb + L::kQ + s * L::kQTile, full = bar(L::Q_FULL + s);
-                if (q_tokens > 0) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(full, (uint32_t)(L::kQSlabs * q_tokens * p.G * 128));
 #pragma unroll
-                        for (int h = 0; h < L::kQSlabs; ++h)
-                            tma_4d_g2s(qb + h * L::kQSlab, &qmap, 0, hk * p.G, b * p.T + (int)by_group(p, n0), DIFF && E == 64 ? s : h, full);
-                    }
-                    __syncwarp();
-                } else {
-                    constexpr int EQ = E < 64 ? 64 : E;      // elements of a row in the tile
-                    constexpr int C = EQ / 8, RPI = 32 / C;  // lanes of a row, rows at once
-                    const int ch = lane % C;
-                    const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride + (int64_t)hk * p.G * D +
-                                   (DIFF && E == 64 ? s * E : 0) + ch * 8;
-                    int t = (int)by_group(p, n0 + lane / C), h = (n0 + lane / C) - t * p.G;
-#pragma unroll 4
-                    for (int r = lane / C; r < nr; r += RPI) {
-                        cp16(qb + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D, true);
-                        for (h += RPI; h >= p.G; h -= p.G) ++t;
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full);
-                }
-                ++items;
-            }
-            // copies have landed before the CTA may exit
-            if (items > 0) mbar_wait(bar(L::Q_FULL + s), (items - 1) & 1);
-        } else if (warp >= kFixWarp) {
-            // V tiles, two rows of a tile to a thread
-            const int r = threadIdx.x - kFixWarp * 32;
-            uint32_t g = 0, i = 0;
-            for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                const Share &sh = *x;
-                for (int k = sh.k0; k < sh.k1 && !abort; ++k, ++g) {
-                    const uint32_t slot = g % L::kV;
-                    if (!mbar_wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) abort = true;
+                for (int s = 0; s < 2; ++s) {
+                    if (!active[s]) continue;
+                    if (items[s] > 0 && !mbar_wait(bar(L::Q_FREE + s), (items[s] - 1) & 1)) abort = true;
                     abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
+                    const int r0 = DIFF ? 0 : s * 128, n0 = x_n0 + r0, nr = min(128, nrows - r0);
+                    const uint32_t qb = sb + L::kQ + s * L::kQTile, full = bar(L::Q_FULL + s);
+                    if (q_tokens > 0) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, (uint32_t)(L::kQSlabs * q_tokens * p.G * 128));
+#pragma unroll
+                            for (int h = 0; h < L::kQSlabs; ++h)
+                                tma_4d_g2s(qb + h * L::kQSlab, &qmap, 0, hk * p.G, b * p.T + (int)by_group(p, n0),
+                                           DIFF && E == 64 ? s : h, full);
+                        }
+                        __syncwarp();
+                    } else {
+                        constexpr int EQ = E < 64 ? 64 : E;      // elements of a row in the tile
+                        constexpr int C = EQ / 8, RPI = 32 / C;  // lanes of a row, rows at once
+                        const int ch = lane % C;
+                        const T *src = reinterpret_cast<const T *>(p.q) + (int64_t)b * p.T * p.q_stride +
+                                       (int64_t)hk * p.G * D + (DIFF && E == 64 ? s * E : 0) + ch * 8;
+                        int t = (int)by_group(p, n0 + lane / C), h = (n0 + lane / C) - t * p.G;
+#pragma unroll 4
+                        for (int r = lane / C; r < nr; r += RPI) {
+                            cp16(qb + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + t * p.q_stride + h * D,
+                                 true);
+                            for (h += RPI; h >= p.G; h -= p.G) ++t;
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full);
+                    }
+                    ++items[s];
+                }
+                if (abort) break;
+            }
+            // copies have landed before the CTA may exit
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (items[s] > 0) mbar_wait(bar(L::Q_FULL + s), (items[s] - 1) & 1);
+        } else {
+            // V tiles, a row of a tile to a thread, then the item's outputs, a row to a
+            // thread: tensor memory of the warp's quarter
+            const int r = (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const float *rows = reinterpret_cast<const float *>(smem + L::kRows);
+            uint32_t g = 0, i = 0, done[2] = {0, 0};
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                if (!abort && !mbar_wait(b, parity)) abort = true;
+                abort = __any_sync(0xffffffffu, abort);
+                return !abort;
+            };
+            zero_bad_sequences<T>(p, D, threadIdx.x - kOutWarp * 32, 128);
+            for (const Share *x; (x = item(i)) != nullptr; ++i) {
+                const Share &sh = *x;
+                for (int k = sh.k0; k < sh.k1; ++k, ++g) {
+                    const uint32_t slot = g % L::kV;
+                    if (!wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) break;
                     const uint32_t bad = badm[g % kBadRing];
                     bool odd = false;
                     if (bad != 0 || sh.partial(k)) {
+                        const int t = (sh.lo + k) * kKT + r;
+                        uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (r >> 3) * L::kGroup + (r & 7) * 128);
+                        const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (r >> 3) & 1) != 0;
+                        // an exponent of all ones carries into the sign's place
+                        constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+                        uint32_t carry = 0;
 #pragma unroll 1
-                        for (int rr = r; rr < kKT; rr += 64) {
-                            const int t = (sh.lo + k) * kKT + rr;
-                            uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (rr >> 3) * L::kGroup +
-                                                                   (rr & 7) * 128);
-                            const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (rr >> 3) & 1) != 0;
+                        for (int h = 0; h < D / 64; ++h) {
+                            uint4 v[8];
 #pragma unroll
-                            for (int h = 0; h < D / 64; ++h)
+                            for (int c = 0; c < 8; ++c) v[c] = row[h * 64 + ((c + r) & 7)];   // neighbouring rows: other banks
 #pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    uint4 &v = row[h * 64 + ((c + rr) & 7)];   // neighbouring rows' chunks in other banks
-                                    if (unseen) v = make_uint4(0, 0, 0, 0);
-                                    else odd |= non_finite<T>(v.x) || non_finite<T>(v.y) || non_finite<T>(v.z) || non_finite<T>(v.w);
-                                }
+                            for (int c = 0; c < 8; ++c) {
+                                carry |= ((v[c].x & 0x7fff7fffu) + kOne) | ((v[c].y & 0x7fff7fffu) + kOne) |
+                                         ((v[c].z & 0x7fff7fffu) + kOne) | ((v[c].w & 0x7fff7fffu) + kOne);
+                                if (unseen) row[h * 64 + c] = make_uint4(0, 0, 0, 0);
+                            }
                         }
+                        odd = !unseen && (carry & 0x80008000u) != 0;
                         fence_proxy_async_smem();
                     }
                     // the word was last read for step g - kBadRing, whose tile has left the ring
                     odd = __any_sync(0xffffffffu, odd);
                     if (lane == 0) {
-                        oddm[g % kBadRing * 2 + (warp - kFixWarp)] = odd;
+                        oddm[g % kBadRing * 4 + (warp & 3)] = odd;
                         mbar_arrive(bar(L::READY + slot));
                     }
+                }
+                if (abort) break;
+                const bool active[2] = {sh.a[0] < sh.e[0], sh.a[1] < sh.e[1]};
+                float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (!active[s]) continue;
+                    if (!wait(bar(L::ROWS_FULL + s), done[s] & 1)) break;
+                    l[s] = rows[s * 256 + r];
+                    m[s] = rows[s * 256 + 128 + r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::ROWS_FREE + s));
+                }
+                if (abort) break;
+                const bool same = DIFF || sh.stride == 2;          // both tiles are the same rows
+                auto place = [&](int row, int &head) {             // of a row's output
+                    const int n = sh.n0 + row, tok = (int)by_group(p, n);
+                    head = sh.hk * p.G + n - tok * p.G;
+                    return reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + tok) * p.H + head) * D;
+                };
+                auto o_done = [&](int s) {
+                    const bool ok = wait(bar(L::O_DONE + s), done[s] & 1);
+                    ++done[s];
+                    tc05_fence_after_sync();
+                    return ok;
+                };
+                auto o_free = [&](int s) {
+                    tc05_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::O_FREE + s));
+                };
+                const uint32_t o0 = tmem + lanes + L::kColO, o1 = o0 + D;
+                if (sh.cut || !same) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int row = same ? r : s * 128 + r;
+                        const bool there = row < sh.nrows;
+                        if (active[s] && !o_done(s)) break;
+                        if (l[s] < 0.f && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+                        if (sh.cut) {
+                            float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
+                            if (__any_sync(0xffffffffu, there)) {
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16((s ? o1 : o0) + c, o);
+                                    tmem_landed<16>(o);
+                                    if (!active[s])
+#pragma unroll
+                                        for (int j = 0; j < 16; ++j) o[j] = 0;
+                                    if (there)
+#pragma unroll
+                                        for (int j = 0; j < 16; j += 4)
+                                            *reinterpret_cast<uint4 *>(record_at(rec, 256, s * 128 + r, c + j)) =
+                                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                                }
+                                if (there) {
+                                    rec[256 * D + s * 128 + r] = m[s];
+                                    rec[256 * D + 256 + s * 128 + r] = l[s];
+                                }
+                            }
+                        } else {
+                            int head;
+                            T *dst = place(row, head);
+                            store_rows<T, D, false>(s ? o1 : o0, 0, l[s] == 0.f ? 0.f : 1.f / l[s], 0.f, dst, there, l[s] < 0.f, nullptr);
+                        }
+                        if (active[s]) o_free(s);
+                    }
+                    if (abort) break;
+                } else {
+                    const bool there = r < sh.nrows, zero = l[0] < 0.f || l[1] < 0.f;
+                    if (!o_done(0) || (active[1] && !o_done(1))) break;
+                    if (zero && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+                    if (__any_sync(0xffffffffu, there)) {
+                        int head;
+                        T *dst = place(r, head);
+                        float f0, f1;
+                        const T *w = nullptr;
+                        if constexpr (DIFF) {
+                            f0 = l[0] == 0.f ? 0.f : p.out_scale / l[0];
+                            f1 = there && l[1] != 0.f ? -__ldg(p.lambdas + head) * p.out_scale / l[1] : 0.f;
+                            w = reinterpret_cast<const T *>(p.norm_weight);
+                            if (w != nullptr) {
+                                // (out_scale is in both: the squares are taken without it)
+                                const float g0 = l[0] == 0.f ? 0.f : 1.f / l[0];
+                                const float g1 = there && l[1] != 0.f ? -__ldg(p.lambdas + head) / l[1] : 0.f;
+                                float sq = 0.f;
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t a[16], b[16];
+                                    tmem_ld16(o0 + c, a);
+                                    tmem_ld16(o1 + c, b);
+                                    tmem_landed<16>(a);
+                                    pin16(b);
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) {
+                                        const float y = fmaf(__uint_as_float(b[j]), g1, __uint_as_float(a[j]) * g0);
+                                        sq = fmaf(y, y, sq);
+                                    }
+                                }
+                                const float rs = 1.f / sqrtf(sq * (1.f / D) + p.eps);
+                                f0 *= rs;
+                                f1 *= rs;
+                            }
+                        } else {
+                            const float M = fmaxf(m[0], m[1]);
+                            const float w0 = merge_weight(m[0], M), w1 = merge_weight(m[1], M);
+                            const float sum = w0 * l[0] + w1 * l[1], inv = sum == 0.f ? 0.f : 1.f / sum;
+                            f0 = w0 * inv;
+                            f1 = w1 * inv;
+                        }
+                        if (active[1]) store_rows<T, D, true>(o0, o1, f0, f1, dst, there, zero, w);
+                        else store_rows<T, D, false>(o0, 0, f0, 0.f, dst, there, zero, w);
+                    }
+                    o_free(0);
+                    if (active[1]) o_free(1);
                 }
                 __syncwarp();
                 if (lane == 0) item_done(i);
@@ -719,9 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
         const uint32_t col_p = tmem + lanes + L::kColP + s * L::kPStep;
         const float scale = p.scale_log2;
-        uint32_t g = 0, i = 0, ns = 0, pairs = 0, items[2] = {0, 0};
-        zero_bad_sequences<T>(p, D, 256);
-        float *pair = reinterpret_cast<float *>(smem + L::kPair);
+        uint32_t g = 0, i = 0, ns = 0, items = 0;
+        float *rows = reinterpret_cast<float *>(smem + L::kRows);
         auto wait = [&](uint32_t b, uint32_t parity) {
             if (!abort && !mbar_wait(b, parity)) abort = true;
             abort = __any_sync(0xffffffffu, abort);
@@ -738,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r0 = DIFF || stride == 2 ? 0 : s * 128, row = r0 + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;
             const bool idle = warm && r0 + (warp & 3) * 32 >= sh.nrows;   // none of the warp's rows is
-            const int tok = (int)by_group(p, n), head = sh.hk * p.G + n - tok * p.G, pos = sh.pos + tok;
+            const int pos = sh.pos + (int)by_group(p, n);
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const int k_end = sh.finish(s);
@@ -858,7 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t slot = step % L::kV;
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
                     if (odd_words(step) != 0) {
-                        // O of the first step is these threads' to write: they have read the last item's
+                        // O of the first step: once the last item's has been read
+                        if (k == sh.begin(s) && items > 0 && !wait(bar(L::O_FREE + s), (items - 1) & 1)) break;
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t o32[32];
@@ -911,141 +1035,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             g += (uint32_t)(sh.k1 - sh.k0);
             if (abort) break;
-            const bool active[2] = {sh.a[0] < sh.e[0], sh.a[1] < sh.e[1]};
-            const bool mine = s ? active[1] : active[0];
-            const uint32_t done[2] = {items[0] & 1, items[1] & 1};
-            items[0] += active[0];
-            items[1] += active[1];
-            if (row_bad) l = -1.f;
-            if (row_bad && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
-            T *dst = reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + tok) * p.H + head) * D;
-            uint32_t mask = 0;                     // whose O this warp has read, all of it or with the other tile's warps
-            uint32_t weight = 2;
-            if (sh.cut) {
-                if (mine && !wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
-                tc05_fence_after_sync();
-                mask = mine ? 1u << s : 0;
-                float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(col_o + c, o);
-                    tmem_landed<32>(o);
-                    if (!mine)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0;
-                    if (there)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(record_at(rec, 256, s * 128 + r, c + i)) =
-                                make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                }
-                if (there) {
-                    rec[256 * D + s * 128 + r] = m == -INFINITY ? -INFINITY : m * scale;
-                    rec[256 * D + 256 + s * 128 + r] = l;
-                }
-            } else if constexpr (!DIFF) {
-                if (stride == 1) {
-                    if (mine) {
-                        if (!wait(bar(L::O_DONE + s), done[s ? 1 : 0])) break;
-                        tc05_fence_after_sync();
-                        store_rows<T, D, false>(col_o, 0, l == 0.f ? 0.f : 1.f / l, 0.f, dst, there, row_bad, nullptr);
-                        mask = 1u << s;
-                    }
-                } else if (active[1]) {
-                    // the same rows in both tiles: those of tile 0 join the states
-                    const float ms = m == -INFINITY ? -INFINITY : m * scale;
-                    if (s == 1) {
-                        if (pairs > 0 && !wait(bar(L::PAIR_FREE), (pairs - 1) & 1)) break;
-                        pair[r] = ms;
-                        pair[128 + r] = l;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(L::PAIR));
-                    } else {
-                        if (!wait(bar(L::PAIR), pairs & 1)) break;
-                        const float m1 = pair[r], l1 = pair[128 + r];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(L::PAIR_FREE));
-                        if (!wait(bar(L::O_DONE), done[0]) || !wait(bar(L::O_DONE + 1), done[1])) break;
-                        tc05_fence_after_sync();
-                        if (!idle) {
-                            const bool zero = l < 0.f || l1 < 0.f;
-                            const float M = fmaxf(ms, m1);
-                            const float f0 = merge_weight(ms, M), f1 = merge_weight(m1, M);
-                            const float sum = f0 * l + f1 * l1, inv = sum == 0.f ? 0.f : 1.f / sum;
-                            store_rows<T, D, true>(col_o, col_o + D, f0 * inv, f1 * inv, dst, there, zero, nullptr);
-                        }
-                        mask = 3;
-                    }
-                    ++pairs;
-                } else if (s == 0) {
-                    if (!wait(bar(L::O_DONE), done[0])) break;
-                    tc05_fence_after_sync();
-                    if (!idle) store_rows<T, D, false>(col_o, 0, l == 0.f ? 0.f : 1.f / l, 0.f, dst, there, row_bad, nullptr);
-                    mask = 1;
-                }
-            } else {
-                // both maps: the threads of tile s take columns [s D/2, (s + 1) D/2) of the row
-                if (!wait(bar(L::O_DONE), done[0]) || !wait(bar(L::O_DONE + 1), done[1])) break;
-                tc05_fence_after_sync();
-                mask = 3;
-                weight = 1;
-                pair[s * 128 + r] = l;
+            if (sh.begin(s) < k_end) {             // sums and maxima to the warps of the outputs
+                if (items > 0 && !wait(bar(L::ROWS_FREE + s), (items - 1) & 1)) break;
+                ++items;
+                rows[s * 256 + r] = row_bad ? -1.f : l;
+                rows[s * 256 + 128 + r] = m == -INFINITY ? -INFINITY : m * scale;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::PAIR));
-                if (!wait(bar(L::PAIR), pairs++ & 1)) break;
-                const float l0 = pair[r], l1 = pair[128 + r];
-                const bool zero = l0 < 0.f || l1 < 0.f;
-                const float f0 = l0 == 0.f ? 0.f : 1.f / l0;
-                const float f1 = there ? -__ldg(p.lambdas + head) * (l1 == 0.f ? 0.f : 1.f / l1) : 0.f;
-                // 16 columns of the difference
-                auto difference = [&](int c, float (&y)[16]) {
-                    uint32_t o0[16], o1[16];
-                    tmem_ld16(tmem + lanes + L::kColO + s * (D / 2) + c, o0);
-                    tmem_ld16(tmem + lanes + L::kColO + D + s * (D / 2) + c, o1);
-                    tmem_landed<16>(o0);
-                    pin16(o1);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o0[i]) * f0);
-                };
-                float f2 = p.out_scale;
-                const T *w = reinterpret_cast<const T *>(p.norm_weight);
-                if (w != nullptr) {
-                    float sq = 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 16) {
-                        float y[16];
-                        difference(c, y);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) sq = fmaf(y[i], y[i], sq);
-                    }
-                    // every thread has read the sums before squares take their place
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::PAIR));
-                    if (!wait(bar(L::PAIR), pairs++ & 1)) break;
-                    pair[s * 128 + r] = sq;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::PAIR));
-                    if (!wait(bar(L::PAIR), pairs++ & 1)) break;
-                    sq = pair[r] + pair[128 + r];
-                    f2 *= 1.f / sqrtf(sq * (1.f / D) + p.eps);
-                }
-                const uint32_t o = tmem + lanes + L::kColO + s * (D / 2);
-                store_rows<T, D / 2, true>(o, o + D, f0 * f2, f1 * f2, dst + s * (D / 2), there, zero,
-                                           w != nullptr ? w + s * (D / 2) : nullptr);
-                // the next item's sums come after all have read these
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::PAIR));
-                if (!wait(bar(L::PAIR), pairs++ & 1)) break;
-            }
-            if (mask != 0) {
-                tc05_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (mask >> t & 1) mbar_arrive_n(bar(L::O_FREE + t), weight);
-                }
+                if (lane == 0) mbar_arrive(bar(L::ROWS_FULL + s));
             }
             __syncwarp();
             if (lane == 0) item_done(i);
