@@ -139,18 +139,6 @@ __device__ __forceinline__ void tmem_landed(uint32_t *r) {
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
 }
-// 32 columns of 16 lanes as the accumulators of a warp-level product have them: of
-// every 8 columns this thread gets columns 2 (lane % 4) and the next of lane / 4
-// in r[4 j], r[4 j + 1], of lane / 4 + 8 in r[4 j + 2], r[4 j + 3]
-__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -209,72 +197,44 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
-// x[j] of lane i of a quad to x[i] of lane j
-__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4]) {
-    const bool odd = (threadIdx.x & 1) != 0, high = (threadIdx.x & 2) != 0;
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? x[j] : x[j + 1], 1);
-        if (odd) x[j] = y;
-        else x[j + 1] = y;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t y = __shfl_xor_sync(0xffffffffu, high ? x[j] : x[j + 2], 2);
-        if (high) x[j] = y;
-        else x[j + 2] = y;
-    }
-}
-
-// Columns [0, N) of a warp's 32 rows to memory: O_a f0, with BOTH + O_b f1, each
-// times its element of w (null: 1).  Lane r has row r's factors, where it goes
-// (row), whether it goes at all (there), and whether it is zeros.  Quads of lanes
-// store 64 bytes of a row: a row to a lane would touch 32 lines with every store.
+// Columns [0, N) of a row to memory: O_a f0, with BOTH + O_b f1, each times its
+// element of w (null: 1); zeros if `zero`, nothing unless `there`.  32 bytes a store
+// where rows are so aligned (wide): a row to a lane touches 32 lines with every
+// store, and half as many stores take half the time.
 template <typename T, int N, bool BOTH>
-__device__ __forceinline__ void store_rows(uint32_t o_a, uint32_t o_b, float f0, float f1, T *row, bool there, bool zero,
-                                           const T *w) {
-    const int lane = threadIdx.x & 31, q = lane & 3;
-    const uint32_t go = __ballot_sync(0xffffffffu, there), clear = __ballot_sync(0xffffffffu, zero);
+__device__ __forceinline__ void store_row(uint32_t o_a, uint32_t o_b, float f0, float f1, T *row, bool there, bool zero,
+                                          const T *w, bool wide) {
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        float fa[2], fb[2];
-        T *dst[2];
-        const int r0 = half * 16 + (lane >> 2);
-        if ((go >> (half * 16)) == 0) break;
+    for (int c = 0; c < N; c += 16) {
+        uint32_t a[16], b[16], x[8];
+        tmem_ld16(o_a + c, a);
+        if (BOTH) tmem_ld16(o_b + c, b);
+        tmem_landed<16>(a);
+        if (BOTH) pin16(b);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            fa[h] = __shfl_sync(0xffffffffu, f0, r0 + 8 * h);
-            fb[h] = BOTH ? __shfl_sync(0xffffffffu, f1, r0 + 8 * h) : 0.f;
-            dst[h] = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r0 + 8 * h)) + q * 8;
-        }
-#pragma unroll 1
-        for (int c = 0; c < N; c += 32) {
-            uint32_t a[16], b[16];
-            tmem_ld_quads(o_a + ((uint32_t)(half * 16) << 16) + c, a);
-            if (BOTH) tmem_ld_quads(o_b + ((uint32_t)(half * 16) << 16) + c, b);
-            tmem_landed<16>(a);
-            if (BOTH) pin16(b);
-            uint32_t x[2][4];
+        for (int h = 0; h < 16; h += 8) {
+            float wf[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float w0 = 1.f, w1 = 1.f;
-                if (w != nullptr) Elem<T>::unpack2(__ldg(reinterpret_cast<const uint32_t *>(w + c + j * 8 + q * 2)), w0, w1);
+            for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+            if (BOTH && w != nullptr) Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(w + c + h)), wf);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float y0 = __uint_as_float(a[4 * j + 2 * h]) * fa[h], y1 = __uint_as_float(a[4 * j + 2 * h + 1]) * fa[h];
-                    if (BOTH) {
-                        y0 = fmaf(__uint_as_float(b[4 * j + 2 * h]), fb[h], y0);
-                        y1 = fmaf(__uint_as_float(b[4 * j + 2 * h + 1]), fb[h], y1);
-                    }
-                    x[h][j] = Elem<T>::pack2(y0 * w0, y1 * w1);
+            for (int i = 0; i < 4; ++i) {
+                float y0 = __uint_as_float(a[h + 2 * i]) * f0, y1 = __uint_as_float(a[h + 2 * i + 1]) * f0;
+                if (BOTH) {
+                    y0 = fmaf(__uint_as_float(b[h + 2 * i]), f1, y0) * wf[2 * i];
+                    y1 = fmaf(__uint_as_float(b[h + 2 * i + 1]), f1, y1) * wf[2 * i + 1];
                 }
+                x[h / 2 + i] = zero ? 0u : Elem<T>::pack2(y0, y1);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                quad_transpose(x[h]);
-                if (clear >> (r0 + 8 * h) & 1) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0;
-                if (go >> (r0 + 8 * h) & 1)
-                    *reinterpret_cast<uint4 *>(dst[h] + c) = make_uint4(x[h][0], x[h][1], x[h][2], x[h][3]);
+        }
+        if (there) {
+            if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + c), "r"(x[0]), "r"(x[1]),
+                             "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                             : "memory");
+            } else {
+                *reinterpret_cast<uint4 *>(row + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4 *>(row + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
             }
         }
     }
@@ -676,11 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return !abort;
             };
             zero_bad_sequences<T>(p, D, threadIdx.x - kOutWarp * 32, 128);
-            for (const Share *x; (x = item(i)) != nullptr; ++i) {
-                const Share &sh = *x;
-                for (int k = sh.k0; k < sh.k1; ++k, ++g) {
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+            // look over the V tile of step k of an item, tile g of the CTA
+            auto look = [&](const Share &sh, int k) {
                     const uint32_t slot = g % L::kV;
-                    if (!wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) break;
+                    if (!wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) return;
                     const uint32_t bad = badm[g % kBadRing];
                     bool odd = false;
                     if (bad != 0 || sh.partial(k)) {
@@ -711,7 +671,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         oddm[g % kBadRing * 4 + (warp & 3)] = odd;
                         mbar_arrive(bar(L::READY + slot));
                     }
-                }
+                    ++g;
+            };
+            int ahead = 0;                         // tiles of the item that have been looked over already
+            for (const Share *x = item(i); x != nullptr; ++i) {
+                const Share &sh = *x;
+                for (int k = sh.k0 + ahead; k < sh.k1 && !abort; ++k) look(sh, k);
+                if (abort) break;
+                // the next item's first tiles, if they are there, before the outputs
+                const Share *following = item(i + 1);
+                ahead = 0;
+                if (following != nullptr)
+                    while (ahead < 2 && following->k0 + ahead < following->k1 && !abort &&
+                           __all_sync(0xffffffffu, mbar_test(bar(L::V_FULL + g % L::kV), (g / L::kV) & 1)))
+                        look(*following, following->k0 + ahead++);
                 if (abort) break;
                 const bool active[2] = {sh.a[0] < sh.e[0], sh.a[1] < sh.e[1]};
                 float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
@@ -775,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             int head;
                             T *dst = place(row, head);
-                            store_rows<T, D, false>(s ? o1 : o0, 0, l[s] == 0.f ? 0.f : 1.f / l[s], 0.f, dst, there, l[s] < 0.f, nullptr);
+                            store_row<T, D, false>(s ? o1 : o0, 0, l[s] == 0.f ? 0.f : 1.f / l[s], 0.f, dst, there, l[s] < 0.f, nullptr,
+                                                   wide);
                         }
                         if (active[s]) o_free(s);
                     }
@@ -822,14 +796,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             f0 = w0 * inv;
                             f1 = w1 * inv;
                         }
-                        if (active[1]) store_rows<T, D, true>(o0, o1, f0, f1, dst, there, zero, w);
-                        else store_rows<T, D, false>(o0, 0, f0, 0.f, dst, there, zero, w);
+                        if (DIFF || active[1]) store_row<T, D, true>(o0, o1, f0, f1, dst, there, zero, w, wide);
+                        else store_row<T, D, false>(o0, 0, f0, 0.f, dst, there, zero, nullptr, wide);
                     }
                     o_free(0);
                     if (active[1]) o_free(1);
                 }
                 __syncwarp();
                 if (lane == 0) item_done(i);
+                x = following;
             }
         }
     } else {
