@@ -58,11 +58,7 @@ struct Share {
     int all_lo[2], all_hi[2];  // positions that all its rows see
     __device__ __forceinline__ int begin(int s) const { return s ? a[1] : a[0]; }
     __device__ __forceinline__ int finish(int s) const { return s ? e[1] : e[0]; }
-    // not all rows of tile s, of all tiles see all positions of step k
-    __device__ __forceinline__ bool partial(int s, int k) const {
-        const int t0 = (lo + k) * kKT;
-        return t0 + kKT - 1 > (s ? all_hi[1] : all_hi[0]) || t0 < (s ? all_lo[1] : all_lo[0]);
-    }
+    // not all rows see all positions of step k
     __device__ __forceinline__ bool partial(int k) const {
         const int t0 = (lo + k) * kKT;
         return t0 + kKT - 1 > all_hi[0] || t0 < all_lo[1];
@@ -673,18 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ++g;
             };
-            int ahead = 0;                         // tiles of the item that have been looked over already
+            int ahead = 0;                         // of the item's tiles, looked over already
             for (const Share *x = item(i); x != nullptr; ++i) {
                 const Share &sh = *x;
                 for (int k = sh.k0 + ahead; k < sh.k1 && !abort; ++k) look(sh, k);
                 if (abort) break;
-                // the next item's first tiles, if they are there, before the outputs
+                // The next item's first tile before the outputs, or it would wait for them (8
+                // prompts of 900 to 2047 tokens, 64 heads: 486 us after them, 445 so; two
+                // tiles: 460).  Its copy waits for no output.
                 const Share *following = item(i + 1);
                 ahead = 0;
-                if (following != nullptr)
-                    while (ahead < 2 && following->k0 + ahead < following->k1 && !abort &&
-                           __all_sync(0xffffffffu, mbar_test(bar(L::V_FULL + g % L::kV), (g / L::kV) & 1)))
-                        look(*following, following->k0 + ahead++);
+                if (following != nullptr) look(*following, following->k0 + ahead++);
                 if (abort) break;
                 const bool active[2] = {sh.a[0] < sh.e[0], sh.a[1] < sh.e[1]};
                 float l[2] = {0.f, 0.f}, m[2] = {-INFINITY, -INFINITY};
@@ -839,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = sh.pos + (int)by_group(p, n);
             const int row_hi = there ? pos : INT32_MAX;                // rows that are not there may see anything
             const int row_lo = there && p.window > 0 ? max(0, pos - p.window + 1) : 0;
-            const int k_end = sh.finish(s);
+            const int k_end = sh.finish(s), k_base = sh.k0, t_base = sh.lo * kKT;
+            const int all_hi = sh.all_hi[s], all_lo = sh.all_lo[s], item_hi = sh.all_hi[0], item_lo = sh.all_lo[1];
             float m = -INFINITY, l = 0.f;
             bool row_bad = false;
             for (int k = sh.begin(s); k < k_end; k += stride) {
@@ -860,12 +856,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc05_fence_after_sync();
                 uint32_t v[128];
                 auto f = [&v](int i) { return __uint_as_float(v[i]); };
-                const uint32_t step = g + (uint32_t)(k - sh.k0);
+                const uint32_t step = g + (uint32_t)(k - k_base);
                 const uint32_t bad = badm[step % kBadRing];
-                const int t0 = (sh.lo + k) * kKT;
+                const int t0 = t_base + k * kKT;
                 // Code that runs seldom is kept in loops: what it costs is its fetch (the
                 // first step of a launch takes four times the others).
-                if (sh.partial(s, k)) {
+                if (t0 + kKT - 1 > all_hi || t0 < all_lo) {
                     const int lo = row_lo - t0;
                     const uint32_t range = (uint32_t)(row_hi - row_lo);
 #pragma unroll 1
@@ -952,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 tmem_wait_st();
-                if (warm && (bad != 0 || sh.partial(k))) {
+                if (warm && (bad != 0 || t0 + kKT - 1 > item_hi || t0 < item_lo)) {
                     const uint32_t slot = step % L::kV;
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
                     if (odd_words(step) != 0) {
