@@ -21,6 +21,15 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
 
+// two products and sums at once: half the instructions
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 template <int D, bool DIFF>
 struct Layout {
     static constexpr int E = DIFF ? D / 2 : D;
@@ -55,11 +64,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
 
     zero_bad_sequences<float>(p, D, tid, kThreads);
-    const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
-    const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
+    Slices slices;
     Sched<R, kKT> it;
-    const bool has = (int)blockIdx.x < slices.W;
-    if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
+    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices)
+                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1));
     if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
     if (!has) return;
 
@@ -125,27 +133,32 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
             __syncthreads();
             // scores of rows 4 ty + i and positions tx + 16 j
             float s[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-            const float *q = sq + ty * 4 * L::kQPitch, *kk = sk + tx * L::kPitch + map * E;
-#pragma unroll 4
-            for (int d = 0; d < E; d += 4) {
-                float4 a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(q + i * L::kQPitch + d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(kk + j * 16 * L::kPitch + d);
+            {
+                float2 e[4][4];                    // sums over even and odd d
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
-                    }
+                    for (int j = 0; j < 4; ++j) e[i][j] = make_float2(0.f, 0.f);
+                const float *q = sq + ty * 4 * L::kQPitch, *kk = sk + tx * L::kPitch + map * E;
+#pragma unroll 2
+                for (int d = 0; d < E; d += 4) {
+                    float4 a[4], b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(q + i * L::kQPitch + d);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(kk + j * 16 * L::kPitch + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            e[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), e[i][j]);
+                            e[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), e[i][j]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] = e[i][j].x + e[i][j].y;
             }
             const int t0 = (x.lo + k) * kKT;
             const bool partial = t0 < wlo_max || t0 + kKT - 1 > x.pos + tmin;
@@ -185,35 +198,59 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sk[(ty * 4 + i) * L::kPPitch + tx + 16 * j] = s[i][j];
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
+            // Where rows of the tile see different positions, a value that is not finite
+            // must not reach the rows that do not see it, as 0 times it would.
+            bool odd = false;
+            if (partial)
+                for (int c = tid; c < kKT * (D / 4); c += kThreads) {      // what this thread has copied
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sv + c / (D / 4) * L::kPitch + c % (D / 4) * 4);
+                    odd |= (v.x & 0x7f800000u) == 0x7f800000u || (v.y & 0x7f800000u) == 0x7f800000u ||
+                           (v.z & 0x7f800000u) == 0x7f800000u || (v.w & 0x7f800000u) == 0x7f800000u;
+                }
+            odd = __syncthreads_or(odd);
             const float *w = sk + ty * 4 * L::kPPitch;
             constexpr int V = NV >= 4 ? 4 : NV;    // neighbouring outputs: V tx + 16 V jj
-            auto value = [&](int t, int j) { return sv[t * L::kPitch + tx * V + (j / V) * 16 * V + j % V]; };
-            if (!partial) {
+            auto value = [&](int t, float (&v)[NV]) {
+                const float *src = sv + t * L::kPitch + tx * V;
+#pragma unroll
+                for (int j = 0; j < NV; j += V) {
+                    if constexpr (V == 4) *reinterpret_cast<float4 *>(v + j) = *reinterpret_cast<const float4 *>(src + j * 16);
+                    else if constexpr (V == 2) *reinterpret_cast<float2 *>(v + j) = *reinterpret_cast<const float2 *>(src + j * 16);
+                    else v[j] = src[j * 16];
+                }
+            };
+            if (!odd) {
 #pragma unroll 2
                 for (int t = 0; t < kKT; t += 4) {
-                    float a[4][4];
+                    __align__(16) float a[4][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         *reinterpret_cast<float4 *>(a[i]) = *reinterpret_cast<const float4 *>(w + i * L::kPPitch + t);
 #pragma unroll
                     for (int tt = 0; tt < 4; ++tt) {
-                        float v[NV];
+                        __align__(16) float v[NV];
+                        value(t + tt, v);
 #pragma unroll
-                        for (int j = 0; j < NV; ++j) v[j] = value(t + tt, j);
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (NV >= 2) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < NV; ++j) o[i][j] = fmaf(a[i][tt], v[j], o[i][j]);
+                                for (int j = 0; j < NV; j += 2) {
+                                    const float2 y = fma2(make_float2(a[i][tt], a[i][tt]), make_float2(v[j], v[j + 1]),
+                                                          make_float2(o[i][j], o[i][j + 1]));
+                                    o[i][j] = y.x;
+                                    o[i][j + 1] = y.y;
+                                }
+                            } else {
+                                o[i][0] = fmaf(a[i][tt], v[0], o[i][0]);
+                            }
+                        }
                     }
                 }
             } else {
-                // a value that a row does not see must not reach it, not even as 0 times a NaN
-#pragma unroll 4
+#pragma unroll 1
                 for (int t = 0; t < kKT; ++t) {
-                    float v[NV];
-#pragma unroll
-                    for (int j = 0; j < NV; ++j) v[j] = value(t, j);
+                    __align__(16) float v[NV];
+                    value(t, v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float a = w[i * L::kPPitch + t];

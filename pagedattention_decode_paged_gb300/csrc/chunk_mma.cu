@@ -81,11 +81,10 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     zero_bad_sequences<T>(p, D, tid, kThreads);
-    const int per = Sched<R, kKT>::build(p, pre, tid, kThreads, 1);
-    const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
+    Slices slices;
     Sched<R, kKT> it;
-    const bool has = (int)blockIdx.x < slices.W;
-    if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
+    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices)
+                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1));
     if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
     if (!has) return;
 

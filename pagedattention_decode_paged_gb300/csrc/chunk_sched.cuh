@@ -33,6 +33,7 @@ namespace pa {
 namespace chunk {
 
 constexpr int kGroups = 1024;              // sums over sequences kept in shared memory
+constexpr int kWarpSeqs = 128;             // sequences that a warp sums by itself
 
 // One item and the share [k0, k1) of its tiles that this CTA takes.
 struct Item {
@@ -98,6 +99,21 @@ __device__ __forceinline__ int64_t floor_sum(uint64_t n, uint64_t m, uint64_t a,
     }
 }
 
+// Slices: the working CTAs of the grid, no more than there are tiles; CTA w's
+// begins at floor(w total / W) = w q + floor(w r / W) with total = q W + r.
+struct Slices {
+    int64_t total, q;
+    int W, r;
+    __device__ __forceinline__ void divide(int64_t tiles, int grid) {
+        total = tiles;
+        W = (int)min((int64_t)grid, total);
+        q = W > 0 ? (int64_t)quotient(total, W) : 0;
+        r = (int)(total - q * W);
+    }
+    __device__ __forceinline__ int64_t begin(int w) const { return w * q + (uint32_t)(w * r) / (uint32_t)W; }
+    __device__ __forceinline__ int owner(int64_t t) const { return (int)quotient((t + 1) * W - 1, total); }
+};
+
 template <int R, int KT>
 struct Sched {
     // tiles of item i
@@ -131,6 +147,13 @@ struct Sched {
         return s;
     }
 
+    // tiles of sequence b
+    static __device__ __forceinline__ int64_t seq_tiles(const ChunkParams &p, int b) {
+        int pos, error;
+        const int cnt = seq_of(p, b, &pos, &error), nq = items(p, cnt);
+        return cnt > 0 ? p.Hkv * tiles_before(p, pos, cnt, nq, nq) : 0;
+    }
+
     int64_t at, end;           // tile of the current share's first tile, end of the slice
     Item x;
     int64_t first;             // the current item's first tile
@@ -143,14 +166,7 @@ struct Sched {
         auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(n) : "memory"); };
         for (int g = tid; g < groups; g += n) {
             int64_t s = 0;
-            for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) {
-                int pos, error;
-                const int cnt = seq_of(p, b, &pos, &error);
-                if (cnt > 0) {
-                    const int nq = items(p, cnt);
-                    s += p.Hkv * tiles_before(p, pos, cnt, nq, nq);
-                }
-            }
+            for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) s += seq_tiles(p, b);
             pre[g + 1] = s;
         }
         sync();
@@ -184,19 +200,50 @@ struct Sched {
         x.k0 = (int)(at - first);
         x.k1 = (int)min((int64_t)x.n, end - first);
     }
-    // The first share of slice [begin, finish), which is not empty.  Whole warps
-    // call it.
-    __device__ __forceinline__ void seek(const ChunkParams &p, const int64_t *pre, int per, int64_t begin, int64_t finish) {
-        at = begin;
-        end = finish;
-        int lo = 0, hi = (p.B + per - 1) / per;    // pre[lo] <= at < pre[hi]
+    // The first share of this CTA's slice; false when it has none.  Whole warps call
+    // it, and any number of them come to the same.
+    //
+    // Up to kWarpSeqs sequences a warp sums over by itself, without barriers: what a
+    // call spends before its first copy is a chain of loads and of instructions
+    // fetched for the first time (32 tokens behind 2047 cached ones each: 7 us).
+    // More have been summed by build().
+    __device__ __forceinline__ bool locate(const ChunkParams &p, Slices &sl) {
+        const int lane = threadIdx.x & 31, per = (p.B + 31) / 32;
+        int64_t mine = 0;
+        for (int b = lane * per; b < min(p.B, (lane + 1) * per); ++b) mine += seq_tiles(p, b);
+        int64_t incl = mine;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        sl.divide(__shfl_sync(0xffffffffu, incl, 31), gridDim.x);
+        if ((int)blockIdx.x >= sl.W) return false;
+        at = sl.begin(blockIdx.x);
+        end = sl.begin(blockIdx.x + 1);
+        const int l = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
+        enter(p, l * per, at - __shfl_sync(0xffffffffu, incl - mine, l));
+        return true;
+    }
+    __device__ __forceinline__ bool locate(const ChunkParams &p, Slices &sl, const int64_t *pre, int per) {
+        const int groups = (p.B + per - 1) / per;
+        sl.divide(pre[groups], gridDim.x);
+        if ((int)blockIdx.x >= sl.W) return false;
+        at = sl.begin(blockIdx.x);
+        end = sl.begin(blockIdx.x + 1);
+        int lo = 0, hi = groups;                   // pre[lo] <= at < pre[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid] <= at) lo = mid;
             else hi = mid;
         }
-        int64_t off = at - pre[lo], head = 0;
-        int b = lo * per;
+        enter(p, lo * per, at - pre[lo]);
+        return true;
+    }
+
+    // The share at tile `off` of those of sequences b and on.
+    __device__ __forceinline__ void enter(const ChunkParams &p, int b, int64_t off) {
+        int64_t head = 0;
         for (;; ++b) {
             load_seq(p, b);
             if (x.cnt == 0) continue;
@@ -255,20 +302,6 @@ struct Sched {
         return true;
     }
     __device__ __forceinline__ bool cut() const { return x.k0 > 0 || x.k1 < x.n; }
-};
-
-// Slices: the working CTAs of the grid, no more than there are tiles; CTA w's
-// begins at floor(w total / W) = w q + floor(w r / W) with total = q W + r.
-struct Slices {
-    int64_t total, q;
-    int W, r;
-    __device__ __forceinline__ Slices(int64_t tiles, int grid) : total(tiles) {
-        W = (int)min((int64_t)grid, total);
-        q = W > 0 ? (int64_t)quotient(total, W) : 0;
-        r = (int)(total - q * W);
-    }
-    __device__ __forceinline__ int64_t begin(int w) const { return w * q + (uint32_t)(w * r) / (uint32_t)W; }
-    __device__ __forceinline__ int owner(int64_t t) const { return (int)quotient((t + 1) * W - 1, total); }
 };
 
 // This CTA's entry of the cuts, from the first share of its slice (has: it has

@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescS = f16_idesc(kBf16, false, false, 128, kKT);
     constexpr uint32_t kIdescO = f16_idesc(kBf16, false, true, 128, D);
     using Schedule = Sched<R, kKT>;
-    grid_dependency_wait();
     allow_dependents();
     extern __shared__ __align__(1024) unsigned char smem[];   // swizzled tiles: 1024-byte aligned
     const uint32_t sb = smem_u32(smem);
@@ -360,15 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kProducerWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        const int per = Schedule::build(p, pre, threadIdx.x - kProducerWarp * 32, kThreads - kProducerWarp * 32, 1);
+        // what went before: tensor memory, barriers and the weights' first step wait for
+        // none of it
+        grid_dependency_wait();
+        int per = 0;
+        if (p.B > kWarpSeqs) per = Schedule::build(p, pre, threadIdx.x - kProducerWarp * 32, kThreads - kProducerWarp * 32, 1);
         if (warp == kProducerWarp) {
             // lane s copies box s (box_rows positions) of each tile; table entries are
             // looked up a tile ahead
-            const Slices slices(pre[(p.B + per - 1) / per], gridDim.x);
+            Slices slices;
             Schedule it;
-            bool has = (int)blockIdx.x < slices.W;
-            if (has) it.seek(p, pre, per, slices.begin(blockIdx.x), slices.begin(blockIdx.x + 1));
-            if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
+            bool has = p.B <= kWarpSeqs ? it.locate(p, slices) : it.locate(p, slices, pre, per);
             __syncwarp();
             fence_proxy_async_smem();              // the ring's copies come after the sums
             const int boxes = kKT / box_rows;
@@ -429,8 +430,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y = ahead;
                     needed = ahead_needed;
                 }
+                if (i == 1 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, true, slices);
                 has = it.next(p);
             }
+            if (i == 0 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, false, slices);
             publish(true);
             // every copy has landed before the CTA may exit
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
