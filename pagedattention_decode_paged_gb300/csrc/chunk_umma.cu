@@ -167,6 +167,16 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
         ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
+// As mbar_wait, in a loop of a few instructions: there are some thirty waits, and
+// what the roles fetch besides their work they wait for (unrolled by 4, as the
+// compiler will: 8 prompts of 900 to 2047 tokens, 64 heads: 454 us, 401 so).
+__device__ __forceinline__ bool mbar_wait_loop(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitLimit; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
 // True in one lane of the warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool abort = false;
     // item i of the CTA, or null at the end (or after a wait that gave up)
     auto item = [&](uint32_t i) -> const Share * {
-        if (!mbar_wait(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
+        if (!mbar_wait_loop(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
         const Share *x = ring + i % kItems;
         return abort || x->k0 < 0 ? nullptr : x;
     };
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
             uint32_t g = 0, i = 0;
             auto publish = [&](bool stop) {
-                if (i >= kItems && !mbar_wait(bar(L::ITEM_EMPTY + i % kItems), (i / kItems - 1) & 1)) abort = true;
+                if (i >= kItems && !mbar_wait_loop(bar(L::ITEM_EMPTY + i % kItems), (i / kItems - 1) & 1)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
                 Share *x = reinterpret_cast<Share *>(smem + L::kItem) + i % kItems;
                 if (lane == 0) {
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t n = half ? L::kV : L::kK, slot = g % n, round = g / n;
                         const uint32_t full = bar((half ? L::V_FULL : L::K_FULL) + slot);
-                        if (round > 0 && !mbar_wait(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
+                        if (round > 0 && !mbar_wait_loop(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
                         abort = __any_sync(0xffffffffu, abort);
                         if (abort) break;
                         if (lane == 0) {
@@ -436,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i == 0 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, false, slices);
             publish(true);
             // every copy has landed before the CTA may exit
-            for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
-            for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
+            for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait_loop(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
+            for (uint32_t u = g > L::kV ? g - L::kV : 0; u < g; ++u) mbar_wait_loop(bar(L::V_FULL + u % L::kV), (u / L::kV) & 1);
         } else if (warp < kQWarp) {
             // Products of tile s.  The whole warp walks the steps, so that what the
             // products are given is known to be the same in all lanes; one lane issues
@@ -461,9 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
             bool scored = false;
-            if (!mbar_wait(bar(L::WARM), 0)) abort = true;
+            if (!mbar_wait_loop(bar(L::WARM), 0)) abort = true;
             auto wait = [&](uint32_t b, uint32_t bit) {
-                if (!mbar_wait(b, (phase & bit) != 0)) abort = true;
+                if (!mbar_wait_loop(b, (phase & bit) != 0)) abort = true;
                 phase ^= bit;
             };
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (scored) wait(bars + L::S_FREE * 8 + of_s, kPhS);
                         scored = true;
                     }
-                    if (!L::kApart && w && !mbar_wait(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                    if (!L::kApart && w && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                     if (turns > 0 || s == 1) wait(bars + L::TURN * 8 + of_s, kPhT);
                     ++turns;
                     tc05_fence_after_sync();
@@ -527,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (w) {
                         // O += P V of step k
                         if (L::kApart) {
-                            if (!mbar_wait(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                            if (!mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                             tc05_fence_after_sync();
                         }
                         if (leader && odd == 0) {
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every product has completed before tensor memory is freed
             if (leader) umma_commit(bars + (L::END + s) * 8);
-            mbar_wait(bars + (L::END + s) * 8, 0);
+            mbar_wait_loop(bars + (L::END + s) * 8, 0);
             __syncwarp();
         } else if (warp == kQWarp) {
             // query rows (the scores of rows that are not there go nowhere): one copy a
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!active[s]) continue;
-                    if (items[s] > 0 && !mbar_wait(bar(L::Q_FREE + s), (items[s] - 1) & 1)) abort = true;
+                    if (items[s] > 0 && !mbar_wait_loop(bar(L::Q_FREE + s), (items[s] - 1) & 1)) abort = true;
                     abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
                     const int r0 = DIFF ? 0 : s * 128, n0 = x_n0 + r0, nr = min(128, nrows - r0);
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // copies have landed before the CTA may exit
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                if (items[s] > 0) mbar_wait(bar(L::Q_FULL + s), (items[s] - 1) & 1);
+                if (items[s] > 0) mbar_wait_loop(bar(L::Q_FULL + s), (items[s] - 1) & 1);
         } else {
             // V tiles, a row of a tile to a thread, then the item's outputs, a row to a
             // thread: tensor memory of the warp's quarter
@@ -630,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *rows = reinterpret_cast<const float *>(smem + L::kRows);
             uint32_t g = 0, i = 0, done[2] = {0, 0};
             auto wait = [&](uint32_t b, uint32_t parity) {
-                if (!abort && !mbar_wait(b, parity)) abort = true;
+                if (!abort && !mbar_wait_loop(b, parity)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
                 return !abort;
             };
@@ -819,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t g = 0, i = 0, ns = 0, items = 0;
         float *rows = reinterpret_cast<float *>(smem + L::kRows);
         auto wait = [&](uint32_t b, uint32_t parity) {
-            if (!abort && !mbar_wait(b, parity)) abort = true;
+            if (!abort && !mbar_wait_loop(b, parity)) abort = true;
             abort = __any_sync(0xffffffffu, abort);
             return !abort;
         };
