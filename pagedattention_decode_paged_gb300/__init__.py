@@ -101,8 +101,9 @@ class Diff(ctypes.Structure):
 
 # The structs as bytes (a third of a Structure's time to build).
 _SHAPE, _ROPE, _ROWS = struct.Struct("@6i2qi0q"), struct.Struct("@P3i2Pf0q"), struct.Struct("@3P3qi0q")
-_DIFF = struct.Struct("@2P2f0q")
-assert [s.size for s in (_SHAPE, _ROPE, _ROWS, _DIFF)] == [ctypes.sizeof(t) for t in (Shape, Rope, NewRows, Diff)]
+_DIFF, _AXES = struct.Struct("@2P2f0q"), struct.Struct("@PiP")
+assert [s.size for s in (_SHAPE, _ROPE, _ROWS, _DIFF, _AXES)] == \
+    [ctypes.sizeof(t) for t in (Shape, Rope, NewRows, Diff, RopeAxes)]
 
 _lock = threading.Lock()
 _lib = None
@@ -689,10 +690,10 @@ def _append_rows(name, q_out, q, k_new, v_new, k_pool, v_pool, kv_scales, k_scal
         return _issue(load().paged_kv_append_fp4, (shape, rows, *pools, *tail), name, prepare)
     rope = _ROPE.pack(_addr(cos_sin) or 0, most, R, interleaved, _addr(q_norm) or 0, _addr(k_norm) or 0, eps)
     if pair_axis is not None:
-        pairs = ctypes.create_string_buffer(bytes(pair_axis), R // 2)
-        axes = RopeAxes(axis_positions.data_ptr(), A, ctypes.addressof(pairs))
-        return _issue(load().paged_kv_append_rope_axes,
-                      (shape, rope, ctypes.byref(axes), rows, _addr(q_out), *pools, *tail), name, prepare, (axes, pairs))
+        pairs = ctypes.c_char_p(bytes(pair_axis))              # read before the call returns
+        axes = _AXES.pack(axis_positions.data_ptr(), A, ctypes.cast(pairs, ctypes.c_void_p).value)
+        return _issue(load().paged_kv_append_rope_axes, (shape, rope, axes, rows, _addr(q_out), *pools, *tail), name,
+                      prepare, (pairs,))
     return _issue(getattr(load(), name), (shape, rope, rows, _addr(q_out), *pools, *tail), name, prepare)
 
 
