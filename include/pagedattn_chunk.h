@@ -54,8 +54,9 @@ extern "C" {
  *
  * Numerics: scores, softmax and sums are fp32, and so are the products of the
  * fp32 type.  With 16-bit types the weights enter the second product rounded
- * to the type, each off by at most half a step of itself (fp16: or 2^-25 of
- * the largest).
+ * to the type, each off by at most half a step of itself (2^-8 for bf16, 2^-11
+ * for fp16, or 2^-25 of the largest); in the differential form as two parts,
+ * off by the square of that (2^-16; 2^-22, or 2^-25 of the largest).
  *
  * Workspace: at least paged_attention_chunk_workspace() bytes on the device,
  * 16-byte aligned, of any content; nothing in it is kept from call to call.
@@ -90,7 +91,8 @@ pa_status paged_attention_chunk(const pa_shape *shape, void *out, const void *q,
  *   out = y * out_scale
  * lambdas: device fp32 [num_heads]; norm_weight: E elements of the shape's
  * dtype for all heads, 16-byte aligned; eps >= 0 and finite when there is a
- * weight; out_scale finite.  Everything else is as for paged_attention_chunk,
+ * weight; out_scale finite.  The two sums are taken apart, so where a V[j] is
+ * infinite o may be NaN.  Everything else is as for paged_attention_chunk,
  * the workspace included; zeros stay zeros.  head_dim is 32, 64, 128 or 256
  * (16-bit) or 32, 64 or 128 (fp32).  scale is usually 1/sqrt(E/2).
  * (The pages have no differential heads: the form is stated here.)

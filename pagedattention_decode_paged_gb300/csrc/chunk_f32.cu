@@ -169,10 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = t0 + tx + 16 * j;
-                    float v = s[i][j] * p.scale_log2;
-                    if (partial && (t < row_lo[i] || t > row_hi[i])) v = -INFINITY;
-                    s[i][j] = v;
-                    mx = fmaxf(mx, v);
+                    if (!(partial && (t < row_lo[i] || t > row_hi[i]))) mx = fmaxf(mx, s[i][j] * p.scale_log2);
                 }
 #pragma unroll
                 for (int h = 1; h < 16; h <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
@@ -181,7 +178,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = exp2f(s[i][j] - ref);
+                    // the product unrounded: what the maximum was rounded to is the same for the whole row
+                    const int t = t0 + tx + 16 * j;
+                    const bool sees = !(partial && (t < row_lo[i] || t > row_hi[i]));
+                    s[i][j] = sees ? exp2f(fmaf(s[i][j], p.scale_log2, -ref)) : 0.f;
                     sum += s[i][j];
                 }
                 l[i] = l[i] * alpha + sum;

@@ -5,7 +5,9 @@
 // An item is 64 query rows (32 of each map in the differential form), a warp
 // 16 of them; tiles are 64 cache positions.  Per tile
 //     S = Q K^T,  P = 2^(scale log2(e) S - m),  O = O 2^(m_old - m) + P V
-// with the running maximum m and sum l of each row in registers.  Rows of K and
+// with the running maximum m and sum l of each row in registers, the weights
+// rounded to the type for the second product (in the differential form as two
+// parts, rounded weight and rest: its two sums may all but cancel).  Rows of K and
 // V come by 16-byte asynchronous copies from wherever the block table puts
 // them, one tile ahead of the products; each row's place is looked up two tiles
 // ahead.
@@ -55,7 +57,7 @@ struct Layout {
     static constexpr uint32_t kStage = kK;                    // end of an item: rows of O in fp32
     static constexpr int kPitch = D + 4;
     static constexpr uint32_t kP = kV + 2 * kTile;            // weights, where V is not finite
-    static constexpr uint32_t kSums = kP + kRows * kKT * 2;   // sums of the rows
+    static constexpr uint32_t kSums = kP + kRows * kKT * 4;   // sums of the rows
     static constexpr uint32_t kOff = kSums + kRows * 4;       // [2][64] places of the rows
     static constexpr uint32_t kBad = kOff + 2 * kKT * 8;      // [2] bad table entries of a tile, a bit per row
     static constexpr uint32_t kPre = kBad + 16;
@@ -234,26 +236,36 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
             if (!odd) {
 #pragma unroll
                 for (int kk = 0; kk < kKT / 16; ++kk) {
-                    uint32_t a[4];
-                    a[0] = Elem<T>::pack2(s[2 * kk][0], s[2 * kk][1]);
-                    a[1] = Elem<T>::pack2(s[2 * kk][2], s[2 * kk][3]);
-                    a[2] = Elem<T>::pack2(s[2 * kk + 1][0], s[2 * kk + 1][1]);
-                    a[3] = Elem<T>::pack2(s[2 * kk + 1][2], s[2 * kk + 1][3]);
+                    uint32_t a[4], rest[4];        // rest: differential form
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float (&w)[4] = s[2 * kk + (h >> 1)];
+                        const float w0 = w[2 * (h & 1)], w1 = w[2 * (h & 1) + 1];
+                        a[h] = Elem<T>::pack2(w0, w1);
+                        float r0, r1;
+                        Elem<T>::unpack2(a[h], r0, r1);
+                        rest[h] = Elem<T>::pack2(w0 - r0, w1 - r1);
+                    }
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                         uint32_t b0, b1, b2, b3;
                         ldsm_x4_trans(vb + at<D>(kk * 16 + (lane & 15), j * 2 + (lane >> 4)), b0, b1, b2, b3);
                         MmaOp<T>::run(o[2 * j], a, b0, b1);
                         MmaOp<T>::run(o[2 * j + 1], a, b2, b3);
+                        if (DIFF) {
+                            MmaOp<T>::run(o[2 * j], rest, b0, b1);
+                            MmaOp<T>::run(o[2 * j + 1], rest, b2, b3);
+                        }
                     }
                 }
             } else {
-                uint32_t *pw = reinterpret_cast<uint32_t *>(smem + L::kP) + warp * 16 * (kKT / 2);
+                float *pw = reinterpret_cast<float *>(smem + L::kP) + warp * 16 * kKT;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        pw[(lane / 4 + 8 * h) * (kKT / 2) + i * 4 + (lane & 3)] = Elem<T>::pack2(s[i][2 * h], s[i][2 * h + 1]);
+                        *reinterpret_cast<float2 *>(pw + (lane / 4 + 8 * h) * kKT + i * 8 + (lane & 3) * 2) =
+                            make_float2(s[i][2 * h], s[i][2 * h + 1]);
                 __syncwarp();
 #pragma unroll 1
                 for (int t = 0; t < kKT; ++t) {
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
                     bool sees[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        w[h] = Elem<T>::to_float(reinterpret_cast<const T *>(pw)[(lane / 4 + 8 * h) * kKT + t]);
+                        w[h] = pw[(lane / 4 + 8 * h) * kKT + t];
                         sees[h] = t0 + t >= row_lo[h] && t0 + t <= row_hi[h];
                     }
 #pragma unroll

@@ -24,6 +24,13 @@
 // not finite the rows' threads weigh that tile's values one by one, each only
 // those it sees (the product would let 0 times them reach every row).
 //
+// The weights are rounded to the type on their way into the second product, at
+// most half a step of themselves off; an output that sums many of them is then as
+// far from exact as its own rounding.  In the differential form, where two such
+// sums may all but cancel, they go as two parts, rounded weight and rest (in the
+// columns that S has and P not): 1.5 times the error of an exact product's rounded
+// result without, 1.0 with (32 tokens behind 2047, bf16).
+//
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
 // maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
 // of a row above 1.
@@ -292,8 +299,8 @@ struct Layout {
     static constexpr uint32_t kEnd = kRows + 2 * 2 * 128 * 4;
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
     static constexpr size_t kBytes = kEnd;
-    static constexpr bool kApart = D == 64;                   // P has columns of its own
-    static constexpr uint32_t kColS = 0, kColO = D == 64 ? 384 : 256;   // S_s at 128 s, O_s D columns each
+    static constexpr bool kApart = D == 64 && !DIFF;          // P has columns of its own
+    static constexpr uint32_t kColS = 0, kColO = kApart ? 384 : 256;   // S_s at 128 s, O_s D columns each
     static constexpr uint32_t kColP = kApart ? 256 : 0, kPStep = kApart ? 64 : 128;
     static_assert(kBytes <= 232448, "shared memory per CTA");
     static_assert((kGroups + 1) * 8 <= kK * kTile, "the sums fit the ring");
@@ -542,16 +549,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (leader && odd == 0) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
+                            for (int kk = 0; kk < 4; ++kk) {
                                 umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k != a);
+                                if (DIFF) umma_ts(col_o, col_p + 64 + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
+                            }
                         }
                         wait(bars + L::P_FULL * 8 + of_s, kPhP);
                         tc05_fence_after_sync();
                         if (leader) {
                             if (odd == 0) {
 #pragma unroll
-                                for (int kk = 4; kk < 8; ++kk)
+                                for (int kk = 4; kk < 8; ++kk) {
                                     umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
+                                    if (DIFF)
+                                        umma_ts(col_o, col_p + 64 + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
+                                }
                             }
                             if (L::kApart) umma_commit(bars + L::P_EMPTY * 8 + of_s);
                             if (k + stride >= e) umma_commit(bars + L::O_DONE * 8 + of_s);
@@ -941,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
-                    uint32_t w[16];
+                    uint32_t w[16], rest[DIFF ? 16 : 1];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 e = fma2(make_float2(f(c + 2 * i), f(c + 2 * i + 1)), make_float2(scale, scale), make_float2(nb, nb));
@@ -949,8 +961,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         e.y = ex2_approx(e.y);
                         sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = Elem<T>::pack2(e.x, e.y);
+                        if (DIFF) {
+                            float2 r;
+                            Elem<T>::unpack2(w[i], r.x, r.y);
+                            rest[i] = Elem<T>::pack2(e.x - r.x, e.y - r.y);
+                        }
                     }
                     tmem_st16(col_p + c / 2, w);
+                    if (DIFF) tmem_st16(col_p + 64 + c / 2, rest);
                     if (c == 32) {                 // the product of the first 64 positions may begin
                         tmem_wait_st();
                         tc05_fence_before_sync();
@@ -983,7 +1001,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 asm volatile("" : "+r"(w2));
                                 float w[2];
                                 Elem<T>::unpack2(w2, w[0], w[1]);
-                                const float wt = (t & 1) ? w[1] : w[0];
+                                float wt = (t & 1) ? w[1] : w[0];
+                                if (DIFF) {
+                                    tmem_ld1(col_p + 64 + t / 2, w2);
+                                    tmem_wait_ld();
+                                    asm volatile("" : "+r"(w2));
+                                    Elem<T>::unpack2(w2, w[0], w[1]);
+                                    wt += (t & 1) ? w[1] : w[0];
+                                }
                                 const bool sees = t0 + t >= row_lo && t0 + t <= row_hi;
                                 const unsigned char *vr = smem + L::kVRing + slot * L::kTile + (t >> 3) * L::kGroup +
                                                           (c0 >> 6) * 1024 + (t & 7) * 128;

@@ -133,8 +133,9 @@ class Chunk:
                 big = ((qm.abs() @ torch.where(km.isfinite(), km, 0.0).abs().T) * abs(self.scale)).masked_fill(~seen, 0.0)
                 xmax = torch.where(seen, x.abs(), 0.0).amax(-1, keepdim=True)
                 score = (e + 2) * 2 * u * big.amax(-1, keepdim=True) + 4 * u * xmax + 2.0 ** -22
-                # the weight's rounding to the type, and fp16's smallest step
-                weight = 0.0 if self.dtype == F32 else half_step(self.dtype)
+                # the weight's rounding to the type (as two parts in the differential form: the
+                # rest's rounding), and fp16's smallest step
+                weight = 0.0 if self.dtype == F32 else half_step(self.dtype) ** maps
                 av = a @ plain.abs()
                 tm = av * (2 * score + weight) * (1 + 2.0 ** -6)
                 if self.dtype == F16:
