@@ -324,3 +324,74 @@ def test_three_operators_as_a_layer_runs_them():
             assert ((out[b, :n].double() - want).abs() <= 2.0 ** -8 * (av + want.abs()) + 2.0 ** -12 * av).all()
         pos += cnt
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (6, 2), (14, 2), (16, 1), (64, 1), (128, 1), (200, 1), (256, 1)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_prompts_of_any_group(H, Hkv, window):
+    """Tiles of whole tokens and tiles that cut one, several items of a head."""
+    run(H=H, Hkv=Hkv, D=128, T=150, B=2, pos=[70, 0], counts=[150, 131], window=window, ref_device="cuda")
+    run(H=H, Hkv=Hkv, D=64, T=150, B=2, pos=[70, 0], counts=[150, 131], window=window, diff=True, dtype=F16,
+        ref_device="cuda")
+
+
+@pytest.mark.parametrize("bs,gap", [(8, 1024), (16, 8 * 128), (128, 2048), (256, 1024), (24, 5 * 1024)])
+def test_gaps_between_blocks(bs, gap):
+    """Block strides that whole groups of 8 rows divide: gaps of poison are not read as rows."""
+    for diff in (False, True):
+        run(bs=bs, gap=gap, D=128, T=90, B=2, H=4, Hkv=2, pos=[200, 0], diff=diff)
+        run(bs=bs, gap=gap, D=64, T=90, B=2, H=4, Hkv=2, pos=[200, 0], diff=diff, dtype=F16)
+
+
+@pytest.mark.parametrize("dtype,D,bs", [(BF16, 128, 16), (F16, 64, 3), (F32, 64, 16)])
+@pytest.mark.parametrize("B", [32, 33, 127, 128, 129])
+def test_batches_around_those_a_warp_sums(B, dtype, D, bs):
+    g = torch.Generator().manual_seed(B)
+    cnt = torch.randint(0, 3, (B,), generator=g).tolist()
+    cnt[0] = cnt[-1] = 0
+    pos = torch.randint(0, 300, (B,), generator=g).tolist()
+    run(B=B, T=2, counts=cnt, pos=pos, H=4, Hkv=2, D=D, bs=bs, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype,D,bs", [(BF16, 128, 16), (BF16, 128, 3), (F16, 64, 16), (F32, 64, 16)])
+def test_blocks_past_32_bit_offsets(dtype, D, bs):
+    """Blocks near the end of pools of more than 2^32 bytes, queries and outputs in small tensors."""
+    Hkv, H, T = 2, 4, 5
+    per = 2 * Hkv * bs * D
+    es = torch.empty(0, dtype=dtype).element_size()
+    NB = (1 << 32) // (per * es) + 50
+    if torch.cuda.mem_get_info()[0] < NB * per * es + (1 << 30):
+        pytest.skip("not enough memory")
+    pool = torch.empty(NB * per, dtype=dtype, device="cuda")
+    s = Chunk(dtype=dtype, D=D, B=1, T=T, H=H, Hkv=Hkv, bs=bs, pos=[4 * bs + 1])
+    table = torch.full_like(s.table, -1)
+    for j in range(s.MB):
+        if int(s.table[0, j]) < 0:
+            continue
+        far = NB - 1 - 7 * j
+        table[0, j] = far
+        pool[far * per:(far + 1) * per] = s.flat[int(s.table[0, j]) * per:(int(s.table[0, j]) + 1) * per].cuda()
+    q, out = s.q.contiguous().cuda(), s.out.cuda()
+    table, pos = table.cuda(), s.pos.cuda()
+    kw = dict(num_kv_heads=Hkv, block_size=bs, num_blocks=NB, block_stride=per)
+    ws = pa.chunk_workspace_for(q, table, **kw)
+    pa.paged_attention_chunk(out, q, pool, pool[Hkv * bs * D:], table, pos, s.scale, ws, **kw)
+    s.check(out)
+
+
+def test_many_calls_in_a_row_repeat():
+    """Calls back to back, short and long ones in turn, with one workspace: each waits for
+    the one before where it has to."""
+    cases = [Chunk(B=1, T=1, H=8, Hkv=2, D=128, pos=[300]), Chunk(B=3, T=200, H=8, Hkv=2, D=128, pos=[0, 500, 33]),
+             Chunk(B=2, T=3, H=8, Hkv=2, D=64, dtype=F16, pos=[2000, 7]), Chunk(B=1, T=4, H=4, Hkv=1, D=32, pos=[900]),
+             Chunk(B=2, T=30, H=4, Hkv=2, D=128, diff=True, pos=[100, 700])]
+    first = [c.call() for c in cases]
+    ws = max((c.keep[5] for c in cases), key=lambda w: w.numel())
+    calls = [c.call(ws=ws, prepare=True) for c in cases]
+    for _ in range(30):
+        for _, call in calls:
+            call()
+    torch.cuda.synchronize()
+    for c, (out, _), want in zip(cases, calls, first):
+        assert torch.equal(out, want)
+        c.check(out, device="cuda")
