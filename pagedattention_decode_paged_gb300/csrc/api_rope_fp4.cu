@@ -3,7 +3,7 @@
 // here allocates device memory or synchronises the host.
 #include <math.h>
 
-#include "pa_rope_fp4.h"
+#include "pa_axes.h"
 
 namespace {
 
@@ -99,7 +99,7 @@ pa_status append(const pa_shape *s, const pa_rope *rope, const pa_rope_axes *axe
         !aligned16(rows->v) || ks * es % 16 != 0 || vs * es % 16 != 0 || !aligned16(k_pool) || !aligned16(v_pool) ||
         (fp4 && !aligned16(kv_scales)))
         return PA_ERR_MISALIGNED;
-    pa::RopeAppendParams p{};
+    pa::RopeAxesParams p{};
     p.q = q ? rows->q : nullptr;
     p.k = rows->k;
     p.v = rows->v;

@@ -8,13 +8,13 @@
 namespace pa {
 
 template <typename T, int D>
-static cudaError_t launch_axes(const RopeAppendParams &p, cudaStream_t stream) {
+static cudaError_t launch_axes(const RopeAxesParams &p, cudaStream_t stream) {
     return p.pairs ? launch_mode<T, D, false, kNeighbours, true>(p, stream)
                    : launch_mode<T, D, false, kSplit, true>(p, stream);
 }
 
 template <typename T>
-static cudaError_t launch_typed(int head_dim, const RopeAppendParams &p, cudaStream_t s) {
+static cudaError_t launch_typed(int head_dim, const RopeAxesParams &p, cudaStream_t s) {
     switch (head_dim) {
         case 16:
             if constexpr (sizeof(T) == 4) return launch_axes<T, 16>(p, s);
@@ -29,7 +29,7 @@ static cudaError_t launch_typed(int head_dim, const RopeAppendParams &p, cudaStr
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_rope_append_axes(int dtype, int head_dim, const RopeAppendParams &p, cudaStream_t stream) {
+cudaError_t launch_rope_append_axes(int dtype, int head_dim, const RopeAxesParams &p, cudaStream_t stream) {
     if (p.B == 0 || p.T == 0) return cudaSuccess;
     switch (dtype) {
         case PA_F32: return launch_typed<float>(head_dim, p, stream);

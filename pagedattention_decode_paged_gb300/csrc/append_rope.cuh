@@ -36,8 +36,10 @@
 // magnitude that could overflow takes IEEE divisions instead.
 #pragma once
 
+#include <type_traits>
+
 #include "fp4.cuh"
-#include "pa_rope_fp4.h"
+#include "pa_axes.h"
 
 namespace pa {
 
@@ -236,9 +238,12 @@ template <typename T, bool FP4>
 constexpr int kRopeCtas = sizeof(T) == 4 ? 10 : FP4 ? 11 : 14;
 
 // AXES: pair i turns by the token's position on axis pair_axis[i].
+template <bool AXES>
+using RopeParams = std::conditional_t<AXES, RopeAxesParams, RopeAppendParams>;
+
 template <typename T, int D, bool FP4, RopeMode MODE, bool AXES = false>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas<T, FP4>)
-rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, const int kv_run, const int kv_runs) {
+rope_append_kernel(const __grid_constant__ RopeParams<AXES> p, const int q_run, const int kv_run, const int kv_runs) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int LPR = D / 8;                     // lanes per row
@@ -497,7 +502,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendParams p, const int q_run, 
 }
 
 template <typename T, int D, bool FP4, RopeMode MODE, bool AXES = false>
-static cudaError_t launch_mode(const RopeAppendParams &p, cudaStream_t stream) {
+static cudaError_t launch_mode(const RopeParams<AXES> &p, cudaStream_t stream) {
     constexpr int RPW = 32 / (D / 8), QB = kRopeBatch<T>, KB = QB / 2;
     const int nq = ((p.q != nullptr ? p.H : 0) + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
     int sms = 0;

@@ -4,7 +4,6 @@
 #pragma once
 
 #include "pa_internal.h"
-#include "pagedattn_axes.h"
 #include "pagedattn_fp4.h"
 #include "pagedattn_rope.h"
 
@@ -33,17 +32,11 @@ struct RopeAppendParams {
     int32_t max_position, R, pairs;
     float eps;
     float k_g, v_g;
-    // positions of several axes (null: the cache position)
-    const int32_t *axis_positions;   // [axes][B][T]
-    int32_t axes;
-    uint8_t pair_axis[32];     // axis of pair i in bits 2 (i % 4) of byte i / 4
 };
 
 // fp4: write the 4-bit cache (fp4_head_dim), else a cache of `dtype` (rope_append_supported).
 bool rope_append_supported(int dtype, int head_dim);
 cudaError_t launch_rope_append(int dtype, int head_dim, bool fp4, const RopeAppendParams &p, cudaStream_t stream);
-
-cudaError_t launch_rope_append_axes(int dtype, int head_dim, const RopeAppendParams &p, cudaStream_t stream);
 
 struct GatherFp4Params {
     void *k_out;
