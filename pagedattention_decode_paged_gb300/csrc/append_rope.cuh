@@ -255,6 +255,11 @@ rope_append_kernel(const __grid_constant__ RopeParams<AXES> p, const int q_run, 
     const int t = (int)(token - (int64_t)b * p.T);
     const int n = p.counts != nullptr ? __ldg(p.counts + b) : p.T;
     const int32_t start = __ldg(p.positions + b);
+    int32_t axis_pos[4];                           // one token's: the same for the whole warp
+    if constexpr (AXES) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a) axis_pos[a] = __ldg(p.axis_positions + (int64_t)(a < p.axes ? a : 0) * p.B * p.T + token);
+    }
 
     const int lane = threadIdx.x & 31, sub = lane % LPR, lr = lane / LPR;
     const int HQ = p.q != nullptr ? p.H : 0;
@@ -300,14 +305,10 @@ rope_append_kernel(const __grid_constant__ RopeParams<AXES> p, const int q_run, 
                    (!AXES && p.R > 0 && (int64_t)start + n > (int64_t)p.max_position);
     if (bad_pos && reporter) report(p.err_word, PA_DEVERR_BAD_POS);
     if (t >= n) return;
-    int32_t axis_pos[4];
-    if constexpr (AXES) {                          // one token's: the same for the whole warp
+    if constexpr (AXES) {
         bool bad = false;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            axis_pos[a] = __ldg(p.axis_positions + (int64_t)(a < p.axes ? a : 0) * p.B * p.T + token);
-            bad |= (uint32_t)axis_pos[a] >= (uint32_t)p.max_position;
-        }
+        for (int a = 0; a < 4; ++a) bad |= (uint32_t)axis_pos[a] >= (uint32_t)p.max_position;
         if (bad && blockIdx.y == 0 && lane == 0) report(p.err_word, PA_DEVERR_BAD_POS);
         bad_pos |= bad;
     }
