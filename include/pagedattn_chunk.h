@@ -63,7 +63,7 @@ extern "C" {
  * Calls that may overlap on the GPU (streams, captured graphs) need
  * workspaces of their own.  The size depends on the shape (batch, heads and
  * tables of any size share one) and on the current device; 0 for a shape that
- * the entry points reject.
+ * the entry points reject or that has no sequences.
  * (The workspace query has no counterpart on the pages.)
  *
  * Shapes: head_dim 32, 64, 128 or 256 (16-bit) or 16, 32, 64 or 128 (fp32);
@@ -92,7 +92,9 @@ pa_status paged_attention_chunk(const pa_shape *shape, void *out, const void *q,
  * lambdas: device fp32 [num_heads]; norm_weight: E elements of the shape's
  * dtype for all heads, 16-byte aligned; eps >= 0 and finite when there is a
  * weight; out_scale finite.  The two sums are taken apart, so where a V[j] is
- * infinite o may be NaN.  Everything else is as for paged_attention_chunk,
+ * infinite o may be NaN.  The squares of o_d and their sum are fp32: where it
+ * passes 2^128, r is 0; where every square is 0 and eps is 0, r is infinite and
+ * the row NaN or infinities.  Everything else is as for paged_attention_chunk,
  * the workspace included; zeros stay zeros.  head_dim is 32, 64, 128 or 256
  * (16-bit) or 32, 64 or 128 (fp32).  scale is usually 1/sqrt(E/2).
  * (The pages have no differential heads: the form is stated here.)

@@ -8,8 +8,10 @@
 // that a record's rows are read in whole lines, each once; at most two records
 // per CTA of the first launch exist, so the whole launch reads at most 2 * grid
 // of them.  Few rows leave lanes over: those take the records in turn (1 token of 8
-// heads behind 131071 of them, 38 records each: 123 us without).  The joined
-// rows go through shared memory to a warp each.
+// heads behind 131071 of them, 38 records each: the call 123 us without, 104 so).
+// The joined rows go through shared memory to a warp each.  Bound by latency: cuts,
+// records and outputs are three dependent trips to L2 (4 tokens behind 2048 in 32
+// sequences, 64 heads: 10 MB of records, about 4 us after the first launch).
 #include "chunk_sched.cuh"
 
 namespace pa {
@@ -21,7 +23,7 @@ constexpr int kMergeRows = 32;
 
 // rows: of a map in a record.
 template <typename T, int D, bool DIFF>
-__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows, const int fold) {
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows) {
     grid_dependency_wait();
     allow_dependents();
     constexpr int MAPS = DIFF ? 2 : 1;
@@ -33,12 +35,9 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     const int r0 = blockIdx.y * kMergeRows;
     if (cut.b < 0 || r0 >= cut.rows) return;
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    // states of a row: one of each CTA, or two (a short item's rows r and fold + r)
-    const int two = cut.rows <= fold ? 1 : 0, states = (cut.last - w + 2) << two, all = rows * MAPS;
-    auto record = [&](int s) {
-        const int cta = s >> two;
-        return p.records + (int64_t)(cta == 0 ? (w - 1) * 2 + 1 : (w - 1 + cta) * 2) * p.rec_floats;
-    };
+    // a state of each CTA that shares the item
+    const int states = cut.last - w + 2, all = rows * MAPS;
+    auto record = [&](int s) { return p.records + (int64_t)(s == 0 ? (w - 1) * 2 + 1 : (w - 1 + s) * 2) * p.rec_floats; };
     // rows of a warp: 8, 16 or 32; lanes `take` and on of a row take every `step`th state
     const int left = cut.rows - r0, lrows = left <= 8 ? 8 : left <= 16 ? 16 : 32, step = 32 / lrows, take = lane / lrows;
     const int i_row = lane & (lrows - 1);
@@ -47,11 +46,11 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     if (part < PARTS) {
 #pragma unroll 1
         for (int map = 0; map < MAPS; ++map) {
-            auto row_of = [&](int s) { return map * rows + r + ((s & two) != 0 ? fold : 0); };
+            const int row = map * rows + r;
             float M = -INFINITY;
 #pragma unroll 8
             for (int s = take; s < states; s += step) {
-                const float *ml = record(s) + (int64_t)all * D + row_of(s);
+                const float *ml = record(s) + (int64_t)all * D + row;
                 M = fmaxf(M, __ldg(ml));
                 bad |= __ldg(ml + all) < 0.f;
             }
@@ -65,7 +64,6 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
             for (int i = 0; i < C4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
             for (int s = take; s < states; s += step) {
-                const int row = row_of(s);
                 const float *rec = record(s), *ml = rec + (int64_t)all * D + row;
                 const float f = merge_weight(__ldg(ml), M);
                 L += f * __ldg(ml + all);
@@ -122,8 +120,8 @@ cudaError_t launch_typed(const ChunkParams &p, const ChunkPlan &plan, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = PA_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (plan.maps == 2) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, true>, p, plan.rows, plan.fold);
-    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, false>, p, plan.rows, plan.fold);
+    if (plan.maps == 2) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, true>, p, plan.rows);
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T, D, false>, p, plan.rows);
 }
 
 }  // namespace

@@ -14,7 +14,15 @@
 // threads of one tile take the exponentials of a step the tensor core multiplies
 // for the other.  An item of up to 128 rows (single tokens, ends of prompts) has
 // its steps dealt to the two tiles in turn instead, and their states are joined
-// at its end.
+// at its end (of the item or of the CTA's share of it; 4 tokens behind 2048 in 32
+// sequences, 64 heads: 66 us with two states to a share's record, 62 with one).
+//
+// What bounds it: long contexts, the tensor core (4096 tokens behind 28672, 64
+// heads on 8: 2.69 ms, 1.53 PFLOP/s of what is seen, 80% of a library product's
+// rate); prompts, the same with the way of a step through both products and the
+// exponentials, twice as many columns at the diagonal as are seen, starts and ends of items
+// (8 of 900 to 2047 tokens: 407 us, 1.11 PFLOP/s); few rows, the copies of K and V
+// and 20 us of start, records and merge (the 62 us: 3.6 TB/s from memory).
 //
 // Roles (512 threads): warps 0-3 and 4-7 the weights of tile 0 and 1; warp 8 the
 // schedule and the copies of K and V; warps 9 and 10 the products of tile 0 and 1,
@@ -250,6 +258,35 @@ __device__ __forceinline__ void store_row(uint32_t o_a, uint32_t o_b, float f0, 
                 *reinterpret_cast<uint4 *>(row + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
             }
         }
+    }
+}
+
+// A row's state to a record of 256 rows: O_a f0, with BOTH + O_b f1 (a factor of 0:
+// nothing of it, whatever it holds), its maximum m and sum l.
+template <int D, bool BOTH>
+__device__ __forceinline__ void put_record(float *rec, int row, uint32_t o_a, uint32_t o_b, float f0, float f1, float m, float l,
+                                           bool there) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        uint32_t a[16], b[16];
+        tmem_ld16(o_a + c, a);
+        if (BOTH) tmem_ld16(o_b + c, b);
+        tmem_landed<16>(a);
+        if (BOTH) pin16(b);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = f0 == 0.f ? 0.f : __uint_as_float(a[j + i]) * f0;
+                if (BOTH && f1 != 0.f) y[i] = fmaf(__uint_as_float(b[j + i]), f1, y[i]);
+            }
+            if (there) *reinterpret_cast<float4 *>(record_at(rec, 256, row, c + j)) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+    }
+    if (there) {
+        rec[256 * D + row] = m;
+        rec[256 * D + 256 + row] = l;
     }
 }
 
@@ -650,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = (warp & 3) * 32 + lane;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const float *rows = reinterpret_cast<const float *>(smem + L::kRows);
-            uint32_t g = 0, i = 0, done[2] = {0, 0};
+            uint32_t g = 0, i = 0, done = 0;      // done: a parity for each tile
             auto wait = [&](uint32_t b, uint32_t parity) {
                 if (!abort && !mbar_wait_loop(b, parity)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
@@ -711,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!active[s]) continue;
-                    if (!wait(bar(L::ROWS_FULL + s), done[s] & 1)) break;
+                    if (!wait(bar(L::ROWS_FULL + s), done >> s & 1)) break;
                     l[s] = rows[s * 256 + r];
                     m[s] = rows[s * 256 + 128 + r];
                     __syncwarp();
@@ -725,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return reinterpret_cast<T *>(p.out) + (((int64_t)sh.b * p.T + tok) * p.H + head) * D;
                 };
                 auto o_done = [&](int s) {
-                    const bool ok = wait(bar(L::O_DONE + s), done[s] & 1);
-                    ++done[s];
+                    const bool ok = wait(bar(L::O_DONE + s), done >> s & 1);
+                    done ^= 1u << s;
                     tc05_fence_after_sync();
                     return ok;
                 };
@@ -736,42 +773,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(bar(L::O_FREE + s));
                 };
                 const uint32_t o0 = tmem + lanes + L::kColO, o1 = o0 + D;
-                if (sh.cut || !same) {
+                auto rec = [&]() { return p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats; };
+                if (!same || (DIFF && sh.cut)) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const int row = same ? r : s * 128 + r;
-                        const bool there = row < sh.nrows;
-                        if (active[s] && !o_done(s)) break;
-                        if (l[s] < 0.f && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
+                        const bool there = row < sh.nrows, has_o = s ? active[1] : active[0];
+                        const float ls = s ? l[1] : l[0], ms = s ? m[1] : m[0];
+                        if (has_o && !o_done(s)) break;
+                        if (ls < 0.f && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
                         if (sh.cut) {
-                            float *rec = p.records + ((int64_t)blockIdx.x * 2 + (sh.k0 == 0)) * p.rec_floats;
-                            if (__any_sync(0xffffffffu, there)) {
-#pragma unroll 1
-                                for (int c = 0; c < D; c += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16((s ? o1 : o0) + c, o);
-                                    tmem_landed<16>(o);
-                                    if (!active[s])
-#pragma unroll
-                                        for (int j = 0; j < 16; ++j) o[j] = 0;
-                                    if (there)
-#pragma unroll
-                                        for (int j = 0; j < 16; j += 4)
-                                            *reinterpret_cast<uint4 *>(record_at(rec, 256, s * 128 + r, c + j)) =
-                                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                                }
-                                if (there) {
-                                    rec[256 * D + s * 128 + r] = m[s];
-                                    rec[256 * D + 256 + s * 128 + r] = l[s];
-                                }
-                            }
+                            if (__any_sync(0xffffffffu, there))
+                                put_record<D, false>(rec(), s * 128 + r, o0 + s * D, 0, has_o ? 1.f : 0.f, 0.f, ms, ls, there);
                         } else {
                             int head;
                             T *dst = place(row, head);
-                            store_row<T, D, false>(s ? o1 : o0, 0, l[s] == 0.f ? 0.f : 1.f / l[s], 0.f, dst, there, l[s] < 0.f, nullptr,
-                                                   wide);
+                            store_row<T, D, false>(o0 + s * D, 0, ls == 0.f ? 0.f : 1.f / ls, 0.f, dst, there, ls < 0.f, nullptr, wide);
                         }
-                        if (active[s]) o_free(s);
+                        if (has_o) o_free(s);
                     }
                     if (abort) break;
                 } else {
@@ -779,11 +798,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!o_done(0) || (active[1] && !o_done(1))) break;
                     if (zero && there) report(p.err_word, PA_DEVERR_BAD_BLOCK);
                     if (__any_sync(0xffffffffu, there)) {
-                        int head;
-                        T *dst = place(r, head);
                         float f0, f1;
                         const T *w = nullptr;
                         if constexpr (DIFF) {
+                            int head;
+                            place(r, head);
                             f0 = l[0] == 0.f ? 0.f : p.out_scale / l[0];
                             f1 = there && l[1] != 0.f ? -__ldg(p.lambdas + head) * p.out_scale / l[1] : 0.f;
                             w = reinterpret_cast<const T *>(p.norm_weight);
@@ -811,13 +830,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         } else {
                             const float M = fmaxf(m[0], m[1]);
-                            const float w0 = merge_weight(m[0], M), w1 = merge_weight(m[1], M);
-                            const float sum = w0 * l[0] + w1 * l[1], inv = sum == 0.f ? 0.f : 1.f / sum;
-                            f0 = w0 * inv;
-                            f1 = w1 * inv;
+                            f0 = merge_weight(m[0], M);
+                            f1 = merge_weight(m[1], M);
+                            const float sum = f0 * l[0] + f1 * l[1];
+                            if (sh.cut) {          // one state of both tiles
+                                put_record<D, true>(rec(), r, o0, o1, f0, active[1] ? f1 : 0.f, M, zero ? -1.f : sum, there);
+                            } else {
+                                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                                f0 *= inv;
+                                f1 *= inv;
+                            }
                         }
-                        if (DIFF || active[1]) store_row<T, D, true>(o0, o1, f0, f1, dst, there, zero, w, wide);
-                        else store_row<T, D, false>(o0, 0, f0, 0.f, dst, there, zero, nullptr, wide);
+                        if (DIFF || !sh.cut) {
+                            int head;
+                            T *dst = place(r, head);
+                            if (DIFF || active[1]) store_row<T, D, true>(o0, o1, f0, f1, dst, there, zero, w, wide);
+                            else store_row<T, D, false>(o0, 0, f0, 0.f, dst, there, zero, nullptr, wide);
+                        }
                     }
                     o_free(0);
                     if (active[1]) o_free(1);
@@ -1080,7 +1109,6 @@ cudaError_t plan_one(ChunkPlan *plan) {
     plan->grid = sms;
     plan->maps = DIFF ? 2 : 1;
     plan->rows = 256 / plan->maps;
-    plan->fold = DIFF ? 0 : 128;
     plan->rec_floats = chunk_rec_floats(256, D);
     return cudaSuccess;
 }

@@ -52,7 +52,6 @@ struct ChunkPlan {
     int grid = 0;
     int rows = 0;              // query rows of an item (of each map)
     int maps = 1;
-    int fold = 0;              // an item of up to `fold` rows has two states of each: row r and row fold + r
     int rec_floats = 0;        // floats of a record: rows * maps of head_dim, their maxima and their sums
 };
 inline int chunk_rec_floats(int rows_all_maps, int head_dim) { return rows_all_maps * (head_dim + 2); }
