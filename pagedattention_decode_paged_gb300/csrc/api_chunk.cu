@@ -39,15 +39,23 @@ pa_status check_shape(const pa_shape *s, bool diff) {
 
 // Rows of the tcgen05 kernel's boxes: what divides a tile of 128 positions and a
 // block; 0 where the pool does not fit them (rows of a block in whole groups of
-// 8, TMA row coordinates in int32).
+// 8, TMA row coordinates in int32): rows are copied one by one then.
 int umma_box_rows(const pa_shape *s) {
-    if (!pa::chunk_umma_supported(s->dtype, s->head_dim) || s->block_size % 8 != 0) return 0;
+    if (s->block_size % 8 != 0) return 0;
     if (s->block_stride % (8 * s->head_dim) != 0) return 0;
     if (s->num_blocks > (int64_t)INT32_MAX / (s->block_stride / s->head_dim)) return 0;
     int rows = 128;
     while (s->block_size % rows != 0) rows /= 2;
     return rows;
 }
+
+// Row by row, one warp of the tcgen05 kernel's CTA copies K and V; on mma.sync the
+// four of each of up to seven CTAs do.  Query rows of a kv head (tokens of the padded
+// batch times heads of the group) above which the products outweigh that: 32
+// sequences, 64 heads on 8 of 128, blocks of 1, 128 rows behind 2047 tokens 201 us
+// against 192, behind none 25.7 against 19.4; 256 rows 217 against 361 and 28 against
+// 34; 8 rows 178 against 96.
+constexpr int kRowsAbove = 128;
 
 // The kernel for a call, and its plan on the current device.
 enum Kernel { kF32, kMma, kUmma };
@@ -56,25 +64,25 @@ struct Choice {
     int box_rows = 0;
     pa::ChunkPlan plan;
 };
-cudaError_t choose(const pa_shape *s, bool diff, float scale_log2, Choice *c) {
-    if (s->dtype == PA_F32) {
-        c->kernel = kF32;
-        return pa::plan_chunk_f32(s->head_dim, diff, &c->plan);
-    }
-    c->box_rows = umma_box_rows(s);
+cudaError_t plan(const pa_shape *s, bool diff, Choice *c) {
+    if (c->kernel == kF32) return pa::plan_chunk_f32(s->head_dim, diff, &c->plan);
+    if (c->kernel == kMma) return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, &c->plan);
+    return pa::plan_chunk_umma(s->dtype, s->head_dim, diff, c->box_rows, &c->plan);
+}
+cudaError_t choose(const pa_shape *s, bool diff, float scale_log2, int64_t rows, Choice *c) {
+    c->kernel = s->dtype == PA_F32 ? kF32 : kMma;
     // the tcgen05 kernel takes the maximum before it scales
-    if (c->box_rows > 0 && scale_log2 > 0.f) {
-        c->kernel = kUmma;
-        return pa::plan_chunk_umma(s->dtype, s->head_dim, diff, &c->plan);
+    if (s->dtype != PA_F32 && pa::chunk_umma_supported(s->dtype, s->head_dim) && scale_log2 > 0.f) {
+        c->box_rows = umma_box_rows(s);
+        if (c->box_rows > 0 || rows > kRowsAbove) c->kernel = kUmma;
     }
-    c->kernel = kMma;
-    return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, &c->plan);
+    return plan(s, diff, c);
 }
 cudaError_t launch(const pa_shape *s, const pa::ChunkParams &p, const Choice &c, cudaStream_t stream) {
     if (c.kernel == kF32) return pa::launch_chunk_f32(s->head_dim, p, c.plan, stream);
     if (c.kernel == kMma) return pa::launch_chunk_mma(s->dtype, s->head_dim, p, c.plan, stream);
-    CUtensorMap kmap, vmap;
-    if (!pa::chunk_pool_map(&kmap, s, p.k_pool, c.box_rows) || !pa::chunk_pool_map(&vmap, s, p.v_pool, c.box_rows))
+    CUtensorMap kmap{}, vmap{};
+    if (c.box_rows > 0 && (!pa::chunk_pool_map(&kmap, s, p.k_pool, c.box_rows) || !pa::chunk_pool_map(&vmap, s, p.v_pool, c.box_rows)))
         return cudaErrorInvalidValue;
     // a tile of 128 rows is whole tokens; no more of them than there are
     CUtensorMap qmap{};
@@ -116,7 +124,7 @@ pa_status run(const pa_shape *s, const pa_diff *diff, void *out, const void *q, 
         !aligned16(workspace))
         return PA_ERR_MISALIGNED;
     Choice c;
-    if (choose(s, diff != nullptr, scale_log2, &c) != cudaSuccess) return PA_ERR_CUDA;
+    if (choose(s, diff != nullptr, scale_log2, (int64_t)max_tokens * G, &c) != cudaSuccess) return PA_ERR_CUDA;
     const pa::ChunkPlan &plan = c.plan;
     if (workspace_bytes < ws_bytes(plan)) return PA_ERR_WORKSPACE;
     pa::ChunkParams p{};
@@ -167,10 +175,16 @@ extern "C" {
 size_t paged_attention_chunk_workspace(const pa_shape *shape) {
     if (check_shape(shape, false) != PA_OK || shape->batch == 0) return 0;
     size_t n = 0;
-    for (int i = 0; i < 4; ++i) {              // with and without a second map, scales of either sign
+    for (int i = 0; i < 4; ++i) {              // every kernel that may be chosen, with and without a second map
         Choice c;
-        if (!pa::chunk_supported(shape->dtype, shape->head_dim, i % 2 != 0)) continue;
-        if (choose(shape, i % 2 != 0, i < 2 ? 1.f : -1.f, &c) != cudaSuccess) return 0;
+        const bool diff = i % 2 != 0;
+        c.kernel = shape->dtype == PA_F32 ? kF32 : i < 2 ? kMma : kUmma;
+        if (!pa::chunk_supported(shape->dtype, shape->head_dim, diff)) continue;
+        if (c.kernel == kUmma) {
+            if (!pa::chunk_umma_supported(shape->dtype, shape->head_dim)) continue;
+            c.box_rows = umma_box_rows(shape);
+        }
+        if (plan(shape, diff, &c) != cudaSuccess) return 0;
         n = std::max(n, ws_bytes(c.plan));
     }
     return n;

@@ -12,8 +12,10 @@
 // them, one tile ahead of the products; each row's place is looked up two tiles
 // ahead.  Bound by the warps' own latency, four or eight of them on an SM (issue
 // 17%, tensor pipe 26%): 4 prompts of 1024 tokens, 16 heads on 4 of 256 320 us, 108
-// TFLOP/s; 32 heads on 8 of 128 in blocks of 3 243 us, 141 TFLOP/s.  It is here for
-// the shapes that tensor memory and boxes of 8 rows do not fit.
+// TFLOP/s; 1 token behind 2047, 32 sequences, 64 heads on 8 of 128 in blocks of 1
+// 96 us, 2.9 TB/s.  It is here for the shapes that tensor memory does not fit, for
+// scales that are not positive and for few rows over blocks that boxes of 8 rows do
+// not fit.
 #include "chunk_sched.cuh"
 
 namespace pa {

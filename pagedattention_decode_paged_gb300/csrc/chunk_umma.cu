@@ -1,6 +1,6 @@
 // chunk_umma.cu -- attention of several new tokens on the fifth-generation
 // tensor cores (tcgen05.mma, scores, weights and outputs in tensor memory),
-// 16-bit types, head_dim 64 and 128, blocks of a multiple of 8 tokens.
+// 16-bit types, head_dim 64 and 128.
 //
 // An item is 256 query rows in two tiles of 128 (in the differential form 128
 // rows, a tile for each map), a step a tile of 128 cache positions:
@@ -57,7 +57,6 @@ constexpr int kThreads = 512;
 constexpr int kKT = 128;                   // cache positions per tile
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 11, kOutWarp = 12;
 constexpr float kLazy = 8.f;
-constexpr int kBadRing = 8;
 constexpr int kItems = 4;                  // items of the schedule that roles may be apart
 
 // What the roles know of an item: the CTA's share [k0, k1) of its steps, which
@@ -298,6 +297,11 @@ struct Layout {
     static constexpr uint32_t kGroup = 8 * D * 2;             // 8 rows of K or V
     static constexpr uint32_t kTile = kKT * D * 2;
     static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 4;   // tiles in flight or waiting
+    // Words of a step are read until its second product is issued, and written anew from
+    // the copy of K kBadRing steps on, which waits for the scores kK steps before itself;
+    // those come after the second product of the step before them.
+    static constexpr int kBadRing = D == 128 ? 4 : 8;
+    static_assert(kBadRing >= kK + 2 && kBadRing > kV, "words of a step in use");
     static constexpr uint32_t kQSlab = 128 * 128;
     static constexpr int kQSlabs = E <= 64 ? 1 : E / 64;     // (rows of 64 elements stay whole in the differential form)
     static constexpr uint32_t kQTile = kQSlabs * kQSlab;
@@ -329,8 +333,9 @@ struct Layout {
         NBARS = END + 2
     };
     static constexpr uint32_t kTmem = kBars + NBARS * 8;
-    static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] bad table entries of a tile, a bit per 8 rows
-    static constexpr uint32_t kOdd = kBad + kBadRing * 4;     // [kBadRing][4] a V tile's 32 rows are not all finite
+    static constexpr uint32_t kBad = (kTmem + 4 + 15) & ~15u; // [kBadRing] a tile has bad table entries
+    static constexpr uint32_t kBadRows = kBad + kBadRing * 4; // [kBadRing][4] then: a bit per row
+    static constexpr uint32_t kOdd = kBadRows + kBadRing * 16;   // [kBadRing][4] a V tile's 32 rows are not all finite
     static constexpr uint32_t kItem = kOdd + kBadRing * 16;   // [kItems], and one of no rows
     static constexpr uint32_t kRows = (kItem + (kItems + 1) * sizeof(Share) + 15) & ~15u;   // [2][2][128] sums and maxima of rows
     static constexpr uint32_t kEnd = kRows + 2 * 2 * 128 * 4;
@@ -345,7 +350,8 @@ struct Layout {
 
 }  // namespace
 
-template <typename T, int D, bool DIFF>
+// ROWS: K and V are copied row by row (box_rows is 0), else in boxes.
+template <typename T, int D, bool DIFF, bool ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_umma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkParams p, const int box_rows,
@@ -361,9 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = smem_u32(smem);
     auto bar = [&](int i) { return sb + L::kBars + i * 8; };
     volatile uint32_t *badm = reinterpret_cast<volatile uint32_t *>(smem + L::kBad);
+    volatile uint32_t *badr = reinterpret_cast<volatile uint32_t *>(smem + L::kBadRows);
     volatile uint32_t *oddm = reinterpret_cast<volatile uint32_t *>(smem + L::kOdd);
     auto odd_words = [&](uint32_t step) {
-        const volatile uint64_t *o = reinterpret_cast<const volatile uint64_t *>(oddm + step % kBadRing * 4);
+        const volatile uint64_t *o = reinterpret_cast<const volatile uint64_t *>(oddm + step % L::kBadRing * 4);
         return o[0] | o[1];
     };
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
@@ -388,8 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *none = Share{};
         none->stride = none->k1 = none->e[0] = none->e[1] = 1;
         none->all_hi[0] = none->all_hi[1] = -1;    // as a tile that not all rows see alike
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
+        if (!ROWS) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
         if (q_tokens > 0) prefetch_tensormap(&qmap);
         mbar_init_fence();
     }
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool has = p.B <= kWarpSeqs ? it.locate(p, slices) : it.locate(p, slices, pre, per);
             __syncwarp();
             fence_proxy_async_smem();              // the ring's copies come after the sums
-            const int boxes = kKT / box_rows;
+            const int boxes = ROWS ? 0 : kKT / box_rows;
             const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
             uint32_t g = 0, i = 0;
             auto publish = [&](bool stop) {
@@ -442,9 +451,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++i;
                 return x;
             };
+            // Blocks that are not whole groups of 8 rows: rows of 16-byte copies by all
+            // lanes.  A tile is given to the products when the next one has been begun.
+            // Bound by this warp's copies (4 prompts of 1024 tokens, 32 heads on 8 of 128,
+            // blocks of 3: 134 us, of 16, in boxes: 64; on mma.sync 243).
+            uint32_t pending = 0;                  // barrier of the tile begun last
+            auto landed = [&](uint32_t next) {
+                if (pending != 0) {
+                    if (next != 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pending);
+                }
+                pending = next;
+            };
+            auto gather = [&](const Share &sh) {
+                constexpr int C = D / 8, RPI = 32 / C;   // lanes of a row, rows at once
+                const int need_lo = sh.need_lo, need_hi = sh.need_hi, ch = lane % C, first = lane / C;
+                const uint32_t column = (uint32_t)((ch ^ first) & 7) << 4;   // of row `first` of 8; others' differ by their bits
+                // blocks of rows lane + 32 j of tile k: -1 not needed, -2 bad
+                auto look_up = [&](int k, int (&blk)[4]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = (it.x.lo + k) * kKT + lane + 32 * j;
+                        blk[j] = -1;
+                        if (k < it.x.k1 && t >= need_lo && t <= need_hi) {
+                            blk[j] = __ldg(p.block_table + (int64_t)it.x.b * p.MB + (p.bs_shift >= 0 ? t >> p.bs_shift : t / p.bs));
+                            if (blk[j] < 0 || blk[j] >= p.num_blocks) blk[j] = -2;
+                        }
+                    }
+                };
+                int ahead[4];
+                look_up(it.x.k0, ahead);
+                for (int k = it.x.k0; k < it.x.k1; ++k, ++g) {
+                    int64_t at[4];                 // places
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = (it.x.lo + k) * kKT + lane + 32 * j;
+                        const int in_block = p.bs_shift >= 0 ? t & (p.bs - 1) : t % p.bs;
+                        at[j] = ahead[j];
+                        if (at[j] >= 0) at[j] = at[j] * p.block_stride_bytes + ((int64_t)it.x.hk * p.bs + in_block) * (D * 2);
+                    }
+                    look_up(k + 1, ahead);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t n = half ? L::kV : L::kK, slot = g % n, round = g / n;
+                        if (round > 0 && !mbar_wait_loop(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
+                        abort = __any_sync(0xffffffffu, abort);
+                        if (abort) return;
+                        if (half == 0) {
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t rows = __ballot_sync(0xffffffffu, at[j] == -2);
+                                if (lane == 0) badr[g % L::kBadRing * 4 + j] = rows;
+                                any |= rows;
+                            }
+                            if (lane == 0) badm[g % L::kBadRing] = any;
+                        }
+                        const uint32_t dst = sb + (half ? L::kVRing : L::kKRing) + slot * L::kTile + (ch >> 3) * 1024 + first * 128;
+                        const char *pool = (half ? p.v_pool : p.k_pool) + ch * 16;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t there = __ballot_sync(0xffffffffu, at[j] >= 0);
+                            const int64_t from = at[j] < 0 ? 0 : at[j];
+#pragma unroll 2
+                            for (int q = 0; q < 4; ++q)    // groups of 8 rows
+#pragma unroll
+                                for (int u = 0; u < 8; u += RPI) {
+                                    const int64_t o = __shfl_sync(0xffffffffu, from, q * 8 + u + first);
+                                    cp16(dst + (j * 4 + q) * L::kGroup + u * 128 + (column ^ (u << 4)), pool + o,
+                                         (there >> (q * 8 + u + first) & 1) != 0);
+                                }
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        landed(bar((half ? L::V_FULL : L::K_FULL) + slot));
+                    }
+                }
+            };
             while (has && !abort) {
                 const Share &sh = *publish(false);
-                auto look_up = [&](int k, bool &needed) -> int32_t {   // row of the box, -1 bad
+                [[maybe_unused]] auto look_up = [&](int k, bool &needed) -> int32_t {   // row of the box, -1 bad
                     const int t = (it.x.lo + k) * kKT + lane * box_rows;
                     needed = k < it.x.k1 && lane < boxes && t <= sh.need_hi && t + box_rows > sh.need_lo;
                     if (!needed) return 0;
@@ -453,41 +541,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (blk < 0 || (int64_t)blk >= p.num_blocks) return -1;
                     return blk * p.rows_per_block + it.x.hk * p.bs + (t - j * p.bs);
                 };
-                bool needed, ahead_needed;
-                int32_t y = look_up(it.x.k0, needed);
-                for (int k = it.x.k0; k < it.x.k1 && !abort; ++k, ++g) {
-                    const int32_t ahead = look_up(k + 1, ahead_needed);
-                    const bool bad = needed && y < 0, take = needed && y >= 0;
-                    // a bit per 8 rows, as the looking warps and the rows' threads test them
-                    const uint32_t bits = __reduce_or_sync(
-                        0xffffffffu, bad ? (uint32_t)(((1u << (box_rows / 8)) - 1) << (lane * (box_rows / 8))) : 0u);
-                    const uint32_t bytes = __reduce_add_sync(0xffffffffu, take ? box_bytes : 0u);
+                if constexpr (ROWS) {
+                    gather(sh);
+                } else {
+                    bool needed, ahead_needed;
+                    int32_t y = look_up(it.x.k0, needed);
+                    for (int k = it.x.k0; k < it.x.k1 && !abort; ++k, ++g) {
+                        const int32_t ahead = look_up(k + 1, ahead_needed);
+                        const bool bad = needed && y < 0, take = needed && y >= 0;
+                        const uint32_t bits = __ballot_sync(0xffffffffu, bad);
+                        const uint32_t bytes = __reduce_add_sync(0xffffffffu, take ? box_bytes : 0u);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t n = half ? L::kV : L::kK, slot = g % n, round = g / n;
-                        const uint32_t full = bar((half ? L::V_FULL : L::K_FULL) + slot);
-                        if (round > 0 && !mbar_wait_loop(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
-                        abort = __any_sync(0xffffffffu, abort);
-                        if (abort) break;
-                        if (lane == 0) {
-                            if (half == 0) badm[g % kBadRing] = bits;
-                            mbar_arrive_expect_tx(full, bytes);
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t n = half ? L::kV : L::kK, slot = g % n, round = g / n;
+                            const uint32_t full = bar((half ? L::V_FULL : L::K_FULL) + slot);
+                            if (round > 0 && !mbar_wait_loop(bar((half ? L::V_EMPTY : L::K_EMPTY) + slot), (round - 1) & 1)) abort = true;
+                            abort = __any_sync(0xffffffffu, abort);
+                            if (abort) break;
+                            if (half == 0) {
+                                if (bits != 0 && lane < 4) {           // a bit per row of a bad box
+                                    uint32_t rows = 0;
+#pragma unroll 1
+                                    for (int j = 0; j < 32; j += 8) rows |= (bits >> (lane * 32 + j) / box_rows & 1) * (0xffu << j);
+                                    badr[g % L::kBadRing * 4 + lane] = rows;
+                                }
+                                if (lane == 0) badm[g % L::kBadRing] = bits;
+                                __syncwarp();
+                            }
+                            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                            __syncwarp();
+                            if (take) {
+                                const uint32_t dst = sb + (half ? L::kVRing : L::kKRing) + slot * L::kTile + lane * box_bytes;
+                                const CUtensorMap *map = half ? &vmap : &kmap;
+                                if (D == 128) tma_4d_g2s(dst, map, 0, 0, 0, y >> 3, full);
+                                else tma_2d_g2s(dst, map, 0, y, full);
+                            }
                         }
-                        __syncwarp();
-                        if (take) {
-                            const uint32_t dst = sb + (half ? L::kVRing : L::kKRing) + slot * L::kTile + lane * box_bytes;
-                            const CUtensorMap *map = half ? &vmap : &kmap;
-                            if (D == 128) tma_4d_g2s(dst, map, 0, 0, 0, y >> 3, full);
-                            else tma_2d_g2s(dst, map, 0, y, full);
-                        }
+                        y = ahead;
+                        needed = ahead_needed;
                     }
-                    y = ahead;
-                    needed = ahead_needed;
                 }
                 if (i == 1 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, true, slices);
                 has = it.next(p);
             }
             if (i == 0 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, false, slices);
+            if (ROWS) landed(0);
             publish(true);
             // every copy has landed before the CTA may exit
             for (uint32_t u = g > L::kK ? g - L::kK : 0; u < g; ++u) mbar_wait_loop(bar(L::K_FULL + u % L::kK), (u / L::kK) & 1);
@@ -699,12 +797,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto look = [&](const Share &sh, int k) {
                     const uint32_t slot = g % L::kV;
                     if (!wait(bar(L::V_FULL + slot), (g / L::kV) & 1)) return;
-                    const uint32_t bad = badm[g % kBadRing];
+                    const uint32_t bad = badm[g % L::kBadRing];
                     bool odd = false;
                     if (bad != 0 || sh.partial(k)) {
                         const int t = (sh.lo + k) * kKT + r;
                         uint4 *row = reinterpret_cast<uint4 *>(smem + L::kVRing + slot * L::kTile + (r >> 3) * L::kGroup + (r & 7) * 128);
-                        const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad >> (r >> 3) & 1) != 0;
+                        const bool unseen = t < sh.need_lo || t > sh.need_hi || (bad != 0 && (badr[g % L::kBadRing * 4 + (warp & 3)] >> lane & 1) != 0);
                         // an exponent of all ones carries into the sign's place
                         constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
                         uint32_t carry = 0;
@@ -723,10 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         odd = !unseen && (carry & 0x80008000u) != 0;
                         fence_proxy_async_smem();
                     }
-                    // the word was last read for step g - kBadRing, whose tile has left the ring
+                    // the word was last read for step g - L::kBadRing, whose tile has left the ring
                     odd = __any_sync(0xffffffffu, odd);
                     if (lane == 0) {
-                        oddm[g % kBadRing * 4 + (warp & 3)] = odd;
+                        oddm[g % L::kBadRing * 4 + (warp & 3)] = odd;
                         mbar_arrive(bar(L::READY + slot));
                     }
                     ++g;
@@ -911,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t v[128];
                 auto f = [&v](int i) { return __uint_as_float(v[i]); };
                 const uint32_t step = g + (uint32_t)(k - k_base);
-                const uint32_t bad = badm[step % kBadRing];
+                const uint32_t bad = badm[step % L::kBadRing];
                 const int t0 = t_base + k * kKT;
                 // Code that runs seldom is kept in loops: what it costs is its fetch (the
                 // first step of a launch takes four times the others).
@@ -951,8 +1049,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0 && warm) mbar_arrive(bar(L::S_FREE + s));
                 }
                 if (bad != 0) {
-                    const int b0 = max(0, row_lo - t0) >> 3, b1 = min(kKT - 1, row_hi - t0) >> 3;   // groups of 8 it sees
-                    if (b0 <= b1 && (bad >> b0 << b0 & (0xffffu >> (15 - b1))) != 0) row_bad = true;
+#pragma unroll 1
+                    for (int c = 0; c < kKT; c += 32) {            // of 32 positions, those it sees
+                        const int b0 = max(0, row_lo - t0 - c), b1 = min(31, row_hi - t0 - c);
+                        if (b0 <= b1 && (badr[step % L::kBadRing * 4 + c / 32] >> b0 << b0 & (0xffffffffu >> (31 - b1))) != 0)
+                            row_bad = true;
+                    }
                 }
 #pragma unroll
                 for (int i = 64; i < 128; i += 8)
@@ -1098,11 +1200,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <typename T, int D, bool DIFF>
+template <typename T, int D, bool DIFF, bool ROWS>
 cudaError_t plan_one(ChunkPlan *plan) {
     static std::atomic<int> limit[64];
     int sms = 0;
-    cudaError_t e = ensure_smem_limit(chunk_umma_kernel<T, D, DIFF>, Layout<D, DIFF>::kBytes, limit);
+    cudaError_t e = ensure_smem_limit(chunk_umma_kernel<T, D, DIFF, ROWS>, Layout<D, DIFF>::kBytes, limit);
     if (e != cudaSuccess) return e;
     e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
@@ -1113,12 +1215,38 @@ cudaError_t plan_one(ChunkPlan *plan) {
     return cudaSuccess;
 }
 
-template <typename T, int D, bool DIFF>
-cudaError_t launch_one(const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap, int box_rows,
-                       const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan, cudaStream_t stream) {
-    return launch_clustered(chunk_umma_kernel<T, D, DIFF>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
+template <typename T, int D, bool DIFF, bool ROWS>
+cudaError_t launch_one(const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream, const CUtensorMap &kmap,
+                       const CUtensorMap &vmap, int box_rows, const CUtensorMap &qmap, int q_tokens) {
+    return launch_clustered(chunk_umma_kernel<T, D, DIFF, ROWS>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
                             vmap, qmap, p, box_rows, q_tokens);
 }
+
+template <typename T, int D, typename F>
+cudaError_t with_form(bool diff, bool rows, F f) {
+    if (diff) return rows ? f.template operator()<T, D, true, true>() : f.template operator()<T, D, true, false>();
+    return rows ? f.template operator()<T, D, false, true>() : f.template operator()<T, D, false, false>();
+}
+template <typename F>
+cudaError_t with_kernel(int dtype, int head_dim, bool diff, bool rows, F f) {
+    if (dtype == PA_F16) return head_dim == 64 ? with_form<__half, 64>(diff, rows, f) : with_form<__half, 128>(diff, rows, f);
+    return head_dim == 64 ? with_form<__nv_bfloat16, 64>(diff, rows, f) : with_form<__nv_bfloat16, 128>(diff, rows, f);
+}
+
+struct Planner {
+    ChunkPlan *plan;
+    template <typename T, int D, bool DIFF, bool ROWS>
+    cudaError_t operator()() const { return plan_one<T, D, DIFF, ROWS>(plan); }
+};
+struct Launcher {
+    const ChunkParams &p;
+    const CUtensorMap &kmap, &vmap, &qmap;
+    int box_rows, q_tokens;
+    const ChunkPlan &plan;
+    cudaStream_t stream;
+    template <typename T, int D, bool DIFF, bool ROWS>
+    cudaError_t operator()() const { return launch_one<T, D, DIFF, ROWS>(p, plan, stream, kmap, vmap, box_rows, qmap, q_tokens); }
+};
 
 }  // namespace
 
@@ -1126,28 +1254,15 @@ bool chunk_umma_supported(int dtype, int head_dim) {
     return (dtype == PA_F16 || dtype == PA_BF16) && (head_dim == 64 || head_dim == 128);
 }
 
-cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan) {
-    if (dtype == PA_F16) {
-        if (head_dim == 64) return diff ? plan_one<__half, 64, true>(plan) : plan_one<__half, 64, false>(plan);
-        return diff ? plan_one<__half, 128, true>(plan) : plan_one<__half, 128, false>(plan);
-    }
-    if (head_dim == 64) return diff ? plan_one<__nv_bfloat16, 64, true>(plan) : plan_one<__nv_bfloat16, 64, false>(plan);
-    return diff ? plan_one<__nv_bfloat16, 128, true>(plan) : plan_one<__nv_bfloat16, 128, false>(plan);
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, int box_rows, ChunkPlan *plan) {
+    return with_kernel(dtype, head_dim, diff, box_rows == 0, Planner{plan});
 }
 
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
                               int box_rows, const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan,
                               cudaStream_t stream) {
-    const bool diff = plan.maps == 2;
-    auto go = [&](auto kern64, auto kern64d, auto kern128, auto kern128d) {
-        if (head_dim == 64) return diff ? kern64d(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream) : kern64(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream);
-        return diff ? kern128d(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream) : kern128(p, kmap, vmap, box_rows, qmap, q_tokens, plan, stream);
-    };
-    if (dtype == PA_F16)
-        return go(launch_one<__half, 64, false>, launch_one<__half, 64, true>, launch_one<__half, 128, false>,
-                  launch_one<__half, 128, true>);
-    return go(launch_one<__nv_bfloat16, 64, false>, launch_one<__nv_bfloat16, 64, true>, launch_one<__nv_bfloat16, 128, false>,
-              launch_one<__nv_bfloat16, 128, true>);
+    return with_kernel(dtype, head_dim, plan.maps == 2, box_rows == 0,
+                       Launcher{p, kmap, vmap, qmap, box_rows, q_tokens, plan, stream});
 }
 
 }  // namespace pa

@@ -65,9 +65,10 @@ cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
 cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
 
 // 16-bit types, head_dim 64 and 128, on tcgen05; tensor maps of the pools in
-// boxes of box_rows rows, a divisor of 128 and of the block size.
+// boxes of box_rows rows, a divisor of 128 and of the block size, or box_rows 0 and
+// no maps: row by row.
 bool chunk_umma_supported(int dtype, int head_dim);
-cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, int box_rows, ChunkPlan *plan);
 // qmap: the queries in boxes of q_tokens tokens of a group's heads (q_tokens 0:
 // a tile is not whole tokens, and the map is not used).
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,

@@ -353,10 +353,11 @@ def test_batches_around_those_a_warp_sums(B, dtype, D, bs):
     run(B=B, T=2, counts=cnt, pos=pos, H=4, Hkv=2, D=D, bs=bs, dtype=dtype)
 
 
-@pytest.mark.parametrize("dtype,D,bs", [(BF16, 128, 16), (BF16, 128, 3), (F16, 64, 16), (F32, 64, 16)])
-def test_blocks_past_32_bit_offsets(dtype, D, bs):
+@pytest.mark.parametrize("dtype,D,bs,T", [(BF16, 128, 16, 5), (BF16, 128, 3, 5), (BF16, 128, 3, 80), (F16, 64, 16, 5),
+                                          (F32, 64, 16, 5)])
+def test_blocks_past_32_bit_offsets(dtype, D, bs, T):
     """Blocks near the end of pools of more than 2^32 bytes, queries and outputs in small tensors."""
-    Hkv, H, T = 2, 4, 5
+    Hkv, H = 2, 4
     per = 2 * Hkv * bs * D
     es = torch.empty(0, dtype=dtype).element_size()
     NB = (1 << 32) // (per * es) + 50
@@ -395,3 +396,42 @@ def test_many_calls_in_a_row_repeat():
     for c, (out, _), want in zip(cases, calls, first):
         assert torch.equal(out, want)
         c.check(out, device="cuda")
+
+
+# blocks that boxes of 8 rows do not fit, on either side of 128 query rows per kv head
+@pytest.mark.parametrize("dtype,D,diff", [(BF16, 128, False), (F16, 64, False), (F16, 128, True), (BF16, 64, True)])
+@pytest.mark.parametrize("bs", [1, 3, 5, 12, 130])
+def test_rows_copied_one_by_one(bs, dtype, D, diff):
+    run(bs=bs, dtype=dtype, D=D, diff=diff, B=3, T=131, H=8, Hkv=2, pos=[0, 61, 700], counts=[131, 1, 77])
+    run(bs=bs, dtype=dtype, D=D, diff=diff, B=2, T=131, H=6, Hkv=2, pos=[500, 5], window=130)
+
+
+@pytest.mark.parametrize("T", [31, 32, 33, 64, 65])
+@pytest.mark.parametrize("bs,D", [(3, 128), (1, 64)])
+def test_rows_copied_one_by_one_from_few_rows_on(bs, D, T):
+    run(bs=bs, D=D, dtype=BF16, B=2, T=T, H=8, Hkv=2, pos=[300, 0], counts=[T, T - 1])
+
+
+def test_rows_copied_one_by_one_in_long_contexts_and_many_sequences():
+    run(bs=3, dtype=BF16, D=128, B=1, T=20, H=8, Hkv=1, pos=[9001], ref_device="cuda")
+    run(bs=1, dtype=F16, D=64, B=2, T=40, H=16, Hkv=2, pos=[4000, 31], counts=[40, 2], ref_device="cuda")
+    g = torch.Generator().manual_seed(7)
+    cnt = torch.randint(0, 11, (300,), generator=g).tolist()
+    pos = torch.randint(0, 70, (300,), generator=g).tolist()
+    run(bs=3, dtype=BF16, D=128, B=300, T=10, counts=cnt, pos=pos, H=32, Hkv=2)
+
+
+@pytest.mark.parametrize("window", [0, 130])
+@pytest.mark.parametrize("dtype,D,diff", [(BF16, 128, False), (F16, 64, False), (BF16, 128, True)])
+def test_bad_blocks_of_rows_copied_one_by_one(dtype, D, diff, window):
+    s = Chunk(dtype=dtype, D=D, bs=1, B=2, T=200, H=4, Hkv=2, pos=[100, 0], counts=[200, 200], window=window, diff=diff)
+    table, rows = s.table.clone(), {}
+    for b, places, entry in ((0, (251, 259), -1), (1, (120,), s.NB)):
+        for t in places:
+            table[b, t] = entry
+        rows[b] = [i for i in range(200) if any(t <= int(s.pos[b]) + i and (not window or t > int(s.pos[b]) + i - window)
+                                                for t in places)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = s.call(table=table, err=err)
+    assert int(err.item()) == pa.DEVERR_BAD_BLOCK
+    s.check(out, zero_rows=rows)
