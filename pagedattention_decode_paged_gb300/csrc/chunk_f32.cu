@@ -6,8 +6,8 @@
 // then too few warps wait for them: 4 prompts of 1024 tokens, 16 heads on 4 of 128,
 // 539 us for 490).  Products and sums are fp32 fused multiply-adds: the tensor
 // cores' tf32 keeps 11 bits.  Two CTAs an SM, so that one computes while the
-// other's tile is on its way.  36 TFLOP/s on those prompts, of 75 that the CUDA
-// cores have: loads from shared memory (61% of their rate) and waits for them.
+// other's tile is on its way.  35 TFLOP/s on those prompts, of 75 that the CUDA
+// cores have: loads from shared memory (their pipe 71% busy) and waits for them.
 #include "chunk_sched.cuh"
 
 namespace pa {

@@ -18,11 +18,12 @@
 // sequences, 64 heads: 66 us with two states to a share's record, 62 with one).
 //
 // What bounds it: long contexts, the tensor core (4096 tokens behind 28672, 64
-// heads on 8: 2.69 ms, 1.53 PFLOP/s of what is seen, 80% of a library product's
-// rate); prompts, the same with the way of a step through both products and the
-// exponentials, twice as many columns at the diagonal as are seen, starts and ends of items
-// (8 of 900 to 2047 tokens: 407 us, 1.11 PFLOP/s); few rows, the copies of K and V
-// and 20 us of start, records and merge (the 62 us: 3.6 TB/s from memory).
+// heads on 8 of 128: 2.63 ms, 1.57 PFLOP/s of what is seen, 82% of a library product's
+// rate); prompts, a step's way through both products and the exponentials, columns of
+// the diagonal that are not seen, starts and ends of items (8 of 900 to 2047 tokens: 410 us,
+// 1.10 PFLOP/s, the tensor core busy 59% of the time); few rows, the copies of K and V
+// and 20 us of start, records and merge (the 62 us: 3.5 TB/s from memory); blocks that
+// are copied row by row, the copying warp.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the weights of tile 0 and 1; warp 8 the
 // schedule and the copies of K and V; warps 9 and 10 the products of tile 0 and 1,
