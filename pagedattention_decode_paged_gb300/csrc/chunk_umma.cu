@@ -1063,7 +1063,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // the products before S (P over S), or those that read the last weights, are done
-                if (L::kApart && ns > 1 && !wait(bar(L::P_EMPTY + s), ns & 1)) break;
+                if (L::kApart && ns > 1) {
+                    // in this layout the scores come before that product: their fence does not cover it
+                    if (!wait(bar(L::P_EMPTY + s), ns & 1)) break;
+                    tc05_fence_after_sync();
+                }
                 const bool grown = (mx - m) * scale > kLazy;
                 if (__any_sync(0xffffffffu, grown)) {
                     const float alpha = grown ? ex2_approx((m - mx) * scale) : 1.f;
@@ -1116,7 +1120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait(bar(L::READY + slot), (step / L::kV) & 1)) break;
                     if (odd_words(step) != 0) {
                         // O of the first step: once the last item's has been read
-                        if (k == sh.begin(s) && items > 0 && !wait(bar(L::O_FREE + s), (items - 1) & 1)) break;
+                        if (k == sh.begin(s) && items > 0) {
+                            if (!wait(bar(L::O_FREE + s), (items - 1) & 1)) break;
+                            tc05_fence_after_sync();
+                        }
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t o32[32];
