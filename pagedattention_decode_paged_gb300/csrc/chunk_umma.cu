@@ -412,10 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc05_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
     const Share *ring = reinterpret_cast<const Share *>(smem + L::kItem);
+    // A wait gave up.  Lanes may come to that apart, so each warp votes before it acts on it.
     bool abort = false;
     // item i of the CTA, or null at the end (or after a wait that gave up)
     auto item = [&](uint32_t i) -> const Share * {
-        if (!mbar_wait_loop(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
+        if (!abort && !mbar_wait_loop(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
+        abort = __any_sync(0xffffffffu, abort);
         const Share *x = ring + i % kItems;
         return abort || x->k0 < 0 ? nullptr : x;
     };
@@ -615,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
             bool scored = false;
             if (!mbar_wait_loop(bar(L::WARM), 0)) abort = true;
+            // (the vote comes at the end of a step)
             auto wait = [&](uint32_t b, uint32_t bit) {
-                if (!mbar_wait_loop(b, (phase & bit) != 0)) abort = true;
+                if (!abort && !mbar_wait_loop(b, (phase & bit) != 0)) abort = true;
                 phase ^= bit;
             };
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (scored) wait(bars + L::S_FREE * 8 + of_s, kPhS);
                         scored = true;
                     }
-                    if (!L::kApart && w && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                    if (!L::kApart && w && !abort && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                     if (turns > 0 || s == 1) wait(bars + L::TURN * 8 + of_s, kPhT);
                     ++turns;
                     tc05_fence_after_sync();
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (w) {
                         // O += P V of step k
                         if (L::kApart) {
-                            if (!mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                            if (!abort && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                             tc05_fence_after_sync();
                         }
                         if (leader && odd == 0) {
@@ -718,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         k_lo += L::kTile >> 4;
                         if (++ks == L::kK) ks = 0, k_lo -= L::kK * (L::kTile >> 4);
                     }
+                    abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
                 }
                 if (abort) break;
