@@ -412,11 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc05_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
     const Share *ring = reinterpret_cast<const Share *>(smem + L::kItem);
-    // A wait gave up.  Lanes may come to that apart, so each warp votes before it acts on it.
+    // A wait gave up.  Lanes may come to that apart: a warp votes before it does anything
+    // together again.
     bool abort = false;
     // item i of the CTA, or null at the end (or after a wait that gave up)
     auto item = [&](uint32_t i) -> const Share * {
-        if (!abort && !mbar_wait_loop(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
+        if (!mbar_wait_loop(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) abort = true;
         abort = __any_sync(0xffffffffu, abort);
         const Share *x = ring + i % kItems;
         return abort || x->k0 < 0 ? nullptr : x;
@@ -617,9 +618,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
             bool scored = false;
             if (!mbar_wait_loop(bar(L::WARM), 0)) abort = true;
-            // (the vote comes at the end of a step)
+            // A lane that gave up leaves the item's steps by itself; it meets the others at the
+            // next item()'s vote (a vote at each step: 8 prompts of 900 to 2047 tokens 430 us,
+            // 417 so).
             auto wait = [&](uint32_t b, uint32_t bit) {
-                if (!abort && !mbar_wait_loop(b, (phase & bit) != 0)) abort = true;
+                if (!mbar_wait_loop(b, (phase & bit) != 0)) abort = true;
                 phase ^= bit;
             };
             for (const Share *x; (x = item(i)) != nullptr; ++i) {
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (scored) wait(bars + L::S_FREE * 8 + of_s, kPhS);
                         scored = true;
                     }
-                    if (!L::kApart && w && !abort && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                    if (!L::kApart && w && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                     if (turns > 0 || s == 1) wait(bars + L::TURN * 8 + of_s, kPhT);
                     ++turns;
                     tc05_fence_after_sync();
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (w) {
                         // O += P V of step k
                         if (L::kApart) {
-                            if (!abort && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                            if (!mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                             tc05_fence_after_sync();
                         }
                         if (leader && odd == 0) {
@@ -721,10 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         k_lo += L::kTile >> 4;
                         if (++ks == L::kK) ks = 0, k_lo -= L::kK * (L::kTile >> 4);
                     }
-                    abort = __any_sync(0xffffffffu, abort);
                     if (abort) break;
                 }
-                if (abort) break;
                 // rounds of query tile 0 that warp 10 had nothing of pass all the same
                 if (s == 1 && q0_loaded && !(stride == 2 && q_here)) phase ^= kPhQ1;
             }
@@ -981,9 +982,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // while the first tiles are on their way: it fetches the instructions.
         bool warm = false;
         for (;;) {
-            const Share *xi = warm ? item(i) : ring + kItems;
-            if (xi == nullptr) break;
-            const Share &sh = *xi;
+            if (warm && !wait(bar(L::ITEM_FULL + i % kItems), (i / kItems) & 1)) break;
+            const Share &sh = ring[warm ? i % kItems : kItems];
+            if (sh.k0 < 0) break;
             const int stride = sh.stride;
             const int r0 = DIFF || stride == 2 ? 0 : s * 128, row = r0 + r, n = sh.n0 + row;   // row of the item
             const bool there = row < sh.nrows;

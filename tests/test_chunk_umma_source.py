@@ -32,27 +32,39 @@ def test_waits_for_tensor_memory_are_followed_by_its_fence(kernel):
         assert min(fence, leaves) < use, f"{m.group(1)}: {kernel[m.start():m.start() + 60]!r}"
 
 
+ACTS = r"if \(abort\)|return abort|return !abort|&& !abort; |while \(has && !abort\)|__shfl_sync\(|__syncwarp\(|__any_sync\(0xffffffffu, (?!abort)"
+VOTE = r"abort = __any_sync\(0xffffffffu, abort\);"
+
+
+def products(kernel):
+    at = kernel.index("auto wait = [&](uint32_t b, uint32_t bit)")
+    return at, kernel.index("umma_commit(bars + (L::END + s) * 8)", at)
+
+
 def test_a_warp_votes_before_it_acts_on_a_wait_that_gave_up(kernel):
-    """Lanes may run out of polls apart: whatever leaves a loop, returns or goes on to
-    what the whole warp does together is decided by a vote."""
+    """Lanes may run out of polls apart: what the whole warp leaves, returns from or does
+    together is decided by a vote."""
+    p0, p1 = products(kernel)
+    warm = kernel.index("L::WARM), 0)) abort = true;")
     sets = [m.end() for m in re.finditer(r"\babort = true;", kernel)]
-    assert len(sets) > 8
-    warm = kernel.index("L::WARM), 0)) abort = true;")             # the first item's vote comes next
-    for at in sets:
-        vote = first(kernel, r"abort = __any_sync\(0xffffffffu, abort\);", at)
-        if kernel[warm:at].count("\n") == 0 and at > warm:
-            vote = first(kernel, r"= item\(i\)", at)
-        acts = first(kernel, r"if \(abort\)|return abort|return !abort|&& !abort; |while \(has && !abort\)|__shfl_sync\(0xffffffffu, v, 0\)", at)
-        if "auto wait = [&](uint32_t b, uint32_t bit)" in kernel[max(0, at - 160):at]:
-            # the product warps' helper: its callers' step ends with the vote
-            assert kernel.count("abort = __any_sync(0xffffffffu, abort);\n                    if (abort) break;\n                }\n                if (abort) break;") == 1
-            continue
-        assert vote < acts, kernel[at - 120:at + 200]
+    outside = [at for at in sets if not warm < at < p1]
+    assert len(outside) > 6
+    for at in outside:
+        assert first(kernel, VOTE, at) < first(kernel, ACTS, at), kernel[at - 120:at + 200]
+    # every item is fetched with a vote, or through a role's own wait, which has one
+    for m in re.finditer(r"L::ITEM_FULL \+", kernel):
+        line = kernel[kernel.rindex("\n", 0, m.start()):m.start()]
+        if "!wait(" not in line and "mbar_arrive" not in line and "i >= " not in line:
+            assert first(kernel, VOTE, m.end()) < first(kernel, r"return abort", m.end())
 
 
-def test_no_wait_is_begun_by_a_product_warp_that_gave_up(kernel):
-    products = kernel[kernel.index("auto wait = [&](uint32_t b, uint32_t bit)"):kernel.index("warp == kQWarp")]
-    loops = [m.start() for m in re.finditer(r"mbar_wait_loop\(", products)]
-    for at in loops:
-        line = products[products.rindex("\n", 0, at):at]
-        assert "!abort &&" in line or "L::END" in products[at:at + 60], line
+def test_lanes_of_a_product_warp_that_part_meet_again_at_a_vote(kernel):
+    """A lane that gave up leaves the steps of an item by itself: nothing in them, nor on
+    the way to the next item's vote, is done by the whole warp."""
+    p0, p1 = products(kernel)
+    text = kernel[p0:p1]
+    loop = text.index("for (int k = k0 - stride; k < k1; ++k)")
+    assert "(x = item(i)) != nullptr" in text[:loop]
+    steps = text[text.index("bool q_here"):]
+    assert not re.search(r"_sync\(|__syncwarp|elect_one|return", steps.replace("tc05_fence_after_sync(", "").replace("tc05_fence_before_sync(", ""))
+    assert re.findall(r"if \(abort\) \w+", steps) == ["if (abort) break"]
