@@ -55,8 +55,12 @@ extern "C" {
  * Numerics: scores, softmax and sums are fp32, and so are the products of the
  * fp32 type.  With 16-bit types the weights enter the second product rounded
  * to the type, each off by at most half a step of itself (2^-8 for bf16, 2^-11
- * for fp16, or 2^-25 of the largest); in the differential form as two parts,
- * off by the square of that (2^-16; 2^-22, or 2^-25 of the largest).
+ * for fp16, or 2^-25 of the largest), and what they were rounded to is what the
+ * rows are normalised by.  In the differential form, and with bf16 in calls of
+ * at most 128 query rows of a kv head (max_tokens * num_heads / num_kv_heads:
+ * single and speculative tokens), they enter as two parts, off by the square
+ * of that (2^-16; 2^-22, or 2^-25 of the largest).  Both are what
+ * paged_attention_decode does with the same cache.
  *
  * Workspace: at least paged_attention_chunk_workspace() bytes on the device,
  * 16-byte aligned, of any content; nothing in it is kept from call to call.

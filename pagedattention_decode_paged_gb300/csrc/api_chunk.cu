@@ -57,20 +57,32 @@ int umma_box_rows(const pa_shape *s) {
 // 34; 8 rows 178 against 96.
 constexpr int kRowsAbove = 128;
 
+// Query rows of a kv head (tokens of the padded batch times heads of the group) up to
+// which bf16 weights are held in two parts, as the decode of the same cache holds them:
+// single and speculative tokens come out as exact from either.  They wait for memory (7
+// to 9% for the second part); prompts would wait for the products (24 to 33%).  fp16 has
+// one part, and is normalised by what it was rounded to, in both.
+constexpr int kRowsInTwoParts = 128;
+bool two_parts(const pa_shape *s, bool diff, int64_t rows) {
+    return diff || (s->dtype == PA_BF16 && rows <= kRowsInTwoParts);
+}
+
 // The kernel for a call, and its plan on the current device.
 enum Kernel { kF32, kMma, kUmma };
 struct Choice {
     Kernel kernel;
     int box_rows = 0;
+    bool two_parts = false;
     pa::ChunkPlan plan;
 };
 cudaError_t plan(const pa_shape *s, bool diff, Choice *c) {
     if (c->kernel == kF32) return pa::plan_chunk_f32(s->head_dim, diff, &c->plan);
-    if (c->kernel == kMma) return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, &c->plan);
-    return pa::plan_chunk_umma(s->dtype, s->head_dim, diff, c->box_rows, &c->plan);
+    if (c->kernel == kMma) return pa::plan_chunk_mma(s->dtype, s->head_dim, diff, c->two_parts, &c->plan);
+    return pa::plan_chunk_umma(s->dtype, s->head_dim, diff, c->two_parts, c->box_rows, &c->plan);
 }
 cudaError_t choose(const pa_shape *s, bool diff, float scale_log2, int64_t rows, Choice *c) {
     c->kernel = s->dtype == PA_F32 ? kF32 : kMma;
+    c->two_parts = two_parts(s, diff, rows);
     // the tcgen05 kernel takes the maximum before it scales
     if (s->dtype != PA_F32 && pa::chunk_umma_supported(s->dtype, s->head_dim) && scale_log2 > 0.f) {
         c->box_rows = umma_box_rows(s);
@@ -175,14 +187,17 @@ extern "C" {
 size_t paged_attention_chunk_workspace(const pa_shape *shape) {
     if (check_shape(shape, false) != PA_OK || shape->batch == 0) return 0;
     size_t n = 0;
-    for (int i = 0; i < 4; ++i) {              // every kernel that may be chosen, with and without a second map
-        Choice c;
-        const bool diff = i % 2 != 0;
-        c.kernel = shape->dtype == PA_F32 ? kF32 : i < 2 ? kMma : kUmma;
+    for (int i = 0; i < 8; ++i) {              // every kernel that may be chosen: of many rows and of few, with
+        Choice c;                              // and without a second map
+        const bool diff = i & 1;
+        const int64_t rows = i & 2 ? kRowsInTwoParts : INT32_MAX;
+        c.kernel = shape->dtype == PA_F32 ? kF32 : i < 4 ? kMma : kUmma;
+        c.two_parts = two_parts(shape, diff, rows);
         if (!pa::chunk_supported(shape->dtype, shape->head_dim, diff)) continue;
         if (c.kernel == kUmma) {
             if (!pa::chunk_umma_supported(shape->dtype, shape->head_dim)) continue;
             c.box_rows = umma_box_rows(shape);
+            if (c.box_rows == 0 && rows <= kRowsAbove) continue;
         }
         if (plan(shape, diff, &c) != cudaSuccess) return 0;
         n = std::max(n, ws_bytes(c.plan));

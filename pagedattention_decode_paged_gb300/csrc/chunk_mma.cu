@@ -6,8 +6,11 @@
 // 16 of them; tiles are 64 cache positions.  Per tile
 //     S = Q K^T,  P = 2^(scale log2(e) S - m),  O = O 2^(m_old - m) + P V
 // with the running maximum m and sum l of each row in registers, the weights
-// rounded to the type for the second product (in the differential form as two
-// parts, rounded weight and rest: its two sums may all but cancel).  Rows of K and
+// rounded to the type for the second product and summed as rounded, or (TWO) as two
+// parts, rounded weight and rest: in the differential form, whose two sums may all but
+// cancel, and for few rows in bf16, as the decode holds them (32 single tokens behind
+// 2047, 64 heads on 8 of 128 in blocks of 1: 96 us with one part, 105 so; head_dim 256
+// for all rows would take the prompts below to 356).  Rows of K and
 // V come by 16-byte asynchronous copies from wherever the block table puts
 // them, one tile ahead of the products; each row's place is looked up two tiles
 // ahead.  Bound by the warps' own latency, four or eight of them on an SM (issue
@@ -72,7 +75,8 @@ struct Layout {
 
 }  // namespace
 
-template <typename T, int D, bool DIFF>
+// TWO: weights go into the second product in two parts, rounded weight and rest.
+template <typename T, int D, bool DIFF, bool TWO>
 __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_constant__ ChunkParams p) {
     using L = Layout<D, DIFF>;
     constexpr int E = L::E, R = DIFF ? kRows / 2 : kRows;
@@ -211,13 +215,15 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
                 m[h] = mx;
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float w = ex2_approx(s[i][2 * h + j] - ref);
-                        s[i][2 * h + j] = w;
-                        sum += w;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    float &w0 = s[i][2 * h], &w1 = s[i][2 * h + 1];
+                    w0 = ex2_approx(w0 - ref);
+                    w1 = ex2_approx(w1 - ref);
+                    // one part: exactly the weights that the product uses, in the sum too
+                    if (!TWO) Elem<T>::unpack2(Elem<T>::pack2(w0, w1), w0, w1);
+                    sum += w0;
+                    sum += w1;
+                }
                 l[h] = l[h] * alpha[h] + sum;
                 if (bad != 0) {
                     const int a = max(0, row_lo[h] - t0), e = min(kKT - 1, row_hi[h] - t0);
@@ -241,15 +247,17 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
             if (!odd) {
 #pragma unroll
                 for (int kk = 0; kk < kKT / 16; ++kk) {
-                    uint32_t a[4], rest[4];        // rest: differential form
+                    uint32_t a[4], rest[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const float (&w)[4] = s[2 * kk + (h >> 1)];
                         const float w0 = w[2 * (h & 1)], w1 = w[2 * (h & 1) + 1];
                         a[h] = Elem<T>::pack2(w0, w1);
-                        float r0, r1;
-                        Elem<T>::unpack2(a[h], r0, r1);
-                        rest[h] = Elem<T>::pack2(w0 - r0, w1 - r1);
+                        if constexpr (TWO) {
+                            float r0, r1;
+                            Elem<T>::unpack2(a[h], r0, r1);
+                            rest[h] = Elem<T>::pack2(w0 - r0, w1 - r1);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
                         ldsm_x4_trans(vb + at<D>(kk * 16 + (lane & 15), j * 2 + (lane >> 4)), b0, b1, b2, b3);
                         MmaOp<T>::run(o[2 * j], a, b0, b1);
                         MmaOp<T>::run(o[2 * j + 1], a, b2, b3);
-                        if (DIFF) {
+                        if constexpr (TWO) {
                             MmaOp<T>::run(o[2 * j], rest, b0, b1);
                             MmaOp<T>::run(o[2 * j + 1], rest, b2, b3);
                         }
@@ -346,11 +354,11 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
 
 namespace {
 
-template <typename T, int D, bool DIFF>
+template <typename T, int D, bool DIFF, bool TWO>
 cudaError_t plan_one(ChunkPlan *plan) {
     static std::atomic<int> limit[64];
     static std::atomic<int64_t> cache[64];
-    auto kern = chunk_mma_kernel<T, D, DIFF>;
+    auto kern = chunk_mma_kernel<T, D, DIFF, TWO>;
     constexpr size_t smem = Layout<D, DIFF>::kBytes;
     cudaError_t e = ensure_smem_limit(kern, smem, limit);
     if (e != cudaSuccess) return e;
@@ -363,53 +371,57 @@ cudaError_t plan_one(ChunkPlan *plan) {
     plan->grid = n * sms;
     plan->maps = DIFF ? 2 : 1;
     plan->rows = kRows / plan->maps;
+    plan->two_parts = TWO;
     plan->rec_floats = chunk_rec_floats(kRows, D);
     return cudaSuccess;
 }
 
-template <typename T, int D, bool DIFF>
+template <typename T, int D, bool DIFF, bool TWO>
 cudaError_t launch_one(const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream) {
-    return launch_clustered(chunk_mma_kernel<T, D, DIFF>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, p);
+    return launch_clustered(chunk_mma_kernel<T, D, DIFF, TWO>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, p);
 }
 
-template <typename T, bool DIFF, typename F>
+template <typename T, bool DIFF, bool TWO, typename F>
 cudaError_t with_dim(int head_dim, F f) {
     switch (head_dim) {
-        case 32: return f.template operator()<T, 32, DIFF>();
-        case 64: return f.template operator()<T, 64, DIFF>();
-        case 128: return f.template operator()<T, 128, DIFF>();
-        case 256: return f.template operator()<T, 256, DIFF>();
+        case 32: return f.template operator()<T, 32, DIFF, TWO>();
+        case 64: return f.template operator()<T, 64, DIFF, TWO>();
+        case 128: return f.template operator()<T, 128, DIFF, TWO>();
+        case 256: return f.template operator()<T, 256, DIFF, TWO>();
     }
     return cudaErrorInvalidValue;
 }
 template <typename F>
-cudaError_t with_kernel(int dtype, int head_dim, bool diff, F f) {
-    if (dtype == PA_F16) return diff ? with_dim<__half, true>(head_dim, f) : with_dim<__half, false>(head_dim, f);
-    if (dtype == PA_BF16)
-        return diff ? with_dim<__nv_bfloat16, true>(head_dim, f) : with_dim<__nv_bfloat16, false>(head_dim, f);
-    return cudaErrorInvalidValue;
+cudaError_t with_kernel(int dtype, int head_dim, bool diff, bool two, F f) {
+    if (dtype == PA_F16) {
+        if (two && !diff) return cudaErrorInvalidValue;
+        return diff ? with_dim<__half, true, true>(head_dim, f) : with_dim<__half, false, false>(head_dim, f);
+    }
+    if (dtype != PA_BF16) return cudaErrorInvalidValue;
+    if (diff) return with_dim<__nv_bfloat16, true, true>(head_dim, f);
+    return two ? with_dim<__nv_bfloat16, false, true>(head_dim, f) : with_dim<__nv_bfloat16, false, false>(head_dim, f);
 }
 
 struct Planner {
     ChunkPlan *plan;
-    template <typename T, int D, bool DIFF>
-    cudaError_t operator()() const { return plan_one<T, D, DIFF>(plan); }
+    template <typename T, int D, bool DIFF, bool TWO>
+    cudaError_t operator()() const { return plan_one<T, D, DIFF, TWO>(plan); }
 };
 struct Launcher {
     const ChunkParams &p;
     const ChunkPlan &plan;
     cudaStream_t stream;
-    template <typename T, int D, bool DIFF>
-    cudaError_t operator()() const { return launch_one<T, D, DIFF>(p, plan, stream); }
+    template <typename T, int D, bool DIFF, bool TWO>
+    cudaError_t operator()() const { return launch_one<T, D, DIFF, TWO>(p, plan, stream); }
 };
 
 }  // namespace
 
-cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, ChunkPlan *plan) {
-    return with_kernel(dtype, head_dim, diff, Planner{plan});
+cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, bool two_parts, ChunkPlan *plan) {
+    return with_kernel(dtype, head_dim, diff, two_parts, Planner{plan});
 }
 cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream) {
-    return with_kernel(dtype, head_dim, plan.maps == 2, Launcher{p, plan, stream});
+    return with_kernel(dtype, head_dim, plan.maps == 2, plan.two_parts, Launcher{p, plan, stream});
 }
 
 }  // namespace pa

@@ -9,8 +9,9 @@
 // with P_s = 2^(scale log2(e) (S_s - m)) by the 128 threads of tile s, a row
 // each, between the two.  K and V arrive by TMA as 128-byte swizzled rows, K the
 // K-major B operand of the first product, V the MN-major B operand of the
-// second; P is the A operand of the second in tensor memory, at head_dim 128 over
-// the columns that S had (tensor memory is full), at 64 beside them.  While the
+// second; P is the A operand of the second in tensor memory, over the columns that
+// S had (at head_dim 64 there is room beside them for one part of the weights: 4
+// prompts of 2048, 32 heads on 8, 121 us there, 123 here).  While the
 // threads of one tile take the exponentials of a step the tensor core multiplies
 // for the other.  An item of up to 128 rows (single tokens, ends of prompts) has
 // its steps dealt to the two tiles in turn instead, and their states are joined
@@ -34,11 +35,16 @@
 // those it sees (the product would let 0 times them reach every row).
 //
 // The weights are rounded to the type on their way into the second product, at
-// most half a step of themselves off; an output that sums many of them is then as
-// far from exact as its own rounding.  In the differential form, where two such
-// sums may all but cancel, they go as two parts, rounded weight and rest (in the
-// columns that S has and P not): 1.5 times the error of an exact product's rounded
-// result without, 1.0 with (32 tokens behind 2047, bf16).
+// most half a step of themselves off, and summed as rounded: rows are normalised by
+// what they were weighed with, so that a rounding that many weights share does not
+// stay in the output (unrounded sums: 8 prompts of 900 to 2047 tokens 417 us, 422 so;
+// 16 of 450 to 1000 with a window of 512 201 and 207).  An output that sums many of
+// them is then as far from exact as its own rounding (1.4 times the error of an exact
+// product's rounded result).  TWO: rounded weight and rest (in the columns that S has
+// and P not), 1.0 times: in the differential form, where two such sums may all but
+// cancel, and for few rows in bf16, which the decode holds so too (32 x 4 tokens behind
+// 2048, 64 heads, 62 us with one part, 66 so).  Two parts for all would take the
+// prompts to 530 us and 4096 tokens behind 28672 from 2.7 ms to 3.6.
 //
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
 // maximum has grown by more than 2^8 since, so weights stay below 2^8 and the sum
@@ -214,6 +220,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// a += the two 16-bit elements of w: an instruction each, where unpacking them first
+// takes one more (8 prompts of 900 to 2047 tokens, 64 heads: 434 us, 422 so)
+template <typename T>
+__device__ __forceinline__ void add_halves(float2 &a, uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.f16 %0, x, %0;\n\tadd.rn.f32.f16 %1, y, %1;\n\t}"
+            : "+f"(a.x), "+f"(a.y) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
+            : "+f"(a.x), "+f"(a.y) : "r"(w));
+}
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
@@ -316,11 +334,9 @@ struct Layout {
         V_EMPTY = V_FULL + kV,     // [kV]
         READY = V_EMPTY + kV,      // [kV] the tile has been looked over
         S_FULL = READY + kV,       // [2] scores
-        S_FREE = S_FULL + 2,       // [2] P apart from S: the scores have been read
-        P_HALF = S_FREE + 2,       // [2] weights of the first 64 positions
+        P_HALF = S_FULL + 2,       // [2] weights of the first 64 positions
         P_FULL = P_HALF + 2,       // [2] all weights
-        P_EMPTY = P_FULL + 2,      // [2] P apart from S: the product that reads the weights is done
-        O_DONE = P_EMPTY + 2,      // [2] last product of an item
+        O_DONE = P_FULL + 2,       // [2] last product of an item
         O_FREE = O_DONE + 2,       // [2] its result has been read
         Q_FULL = O_FREE + 2,       // [2] query rows
         Q_FREE = Q_FULL + 2,       // [2]
@@ -342,9 +358,8 @@ struct Layout {
     static constexpr uint32_t kEnd = kRows + 2 * 2 * 128 * 4;
     static constexpr uint32_t kPre = kKRing;                  // before the first copy
     static constexpr size_t kBytes = kEnd;
-    static constexpr bool kApart = D == 64 && !DIFF;          // P has columns of its own
-    static constexpr uint32_t kColS = 0, kColO = kApart ? 384 : 256;   // S_s at 128 s, O_s D columns each
-    static constexpr uint32_t kColP = kApart ? 256 : 0, kPStep = kApart ? 64 : 128;
+    static constexpr uint32_t kColS = 0, kColO = 256;         // S_s at 128 s, O_s D columns each
+    static constexpr uint32_t kRest = 64;                     // P_s over S_s: rounded weights, then what they leave
     static_assert(kBytes <= 232448, "shared memory per CTA");
     static_assert((kGroups + 1) * 8 <= kK * kTile, "the sums fit the ring");
 };
@@ -352,7 +367,8 @@ struct Layout {
 }  // namespace
 
 // ROWS: K and V are copied row by row (box_rows is 0), else in boxes.
-template <typename T, int D, bool DIFF, bool ROWS>
+// TWO: weights go into the second product in two parts, rounded weight and rest.
+template <typename T, int D, bool DIFF, bool ROWS, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_umma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap, const __grid_constant__ ChunkParams p, const int box_rows,
@@ -385,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= L::V_EMPTY && i < L::V_EMPTY + L::kV) count = 2;
             if (i == L::S_FULL || i == L::S_FULL + 1) count = 2;      // the products, and what their warp knows
             if (i == L::Q_FREE || i == L::Q_FREE + 1) count = 2;
-            if (i >= L::S_FREE && i < L::P_EMPTY) count = 4;          // the warps of a tile
+            if (i >= L::P_HALF && i < L::O_DONE) count = 4;           // the warps of a tile
             if (i == L::O_FREE || i == L::O_FREE + 1) count = 4;      // the warps of the outputs
             if (i >= L::ROWS_FULL && i < L::WARM) count = 4;
             if (i == L::WARM) count = 8;
@@ -606,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kFlags = (1u << 14) | (2u << 29);
             constexpr uint32_t kQHi = kFlags | (1024 >> 4), kKvHi = kFlags | (L::kGroup >> 4);
             const uint32_t base = __shfl_sync(0xffffffffu, sb, 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t col_s = tm + L::kColS + s * 128, col_o = tm + L::kColO + s * D, col_p = tm + L::kColP + s * L::kPStep;
+            const uint32_t col_s = tm + L::kColS + s * 128, col_o = tm + L::kColO + s * D;
             const uint32_t q_lo = ((base + L::kQ) >> 4) + (DIFF && E < 64 ? s * (E * 2 >> 4) : 0);
             // of the slot
             uint32_t k_lo = ((base + L::kKRing) >> 4) + (DIFF ? (s * E >> 6) * (1024 >> 4) + ((s * E & 63) * 2 >> 4) : 0);
@@ -615,8 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t step = 0, i = 0, ks = 0, vs = 0, items = 0, turns = 0;
             // a bit per barrier: the parity of the round that is waited for next
             uint32_t phase = 0;
-            constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhS = 32, kPhT = 64, kPhQ1 = 128;
-            bool scored = false;
+            constexpr uint32_t kPhK = 1, kPhV = 2, kPhQ = 4, kPhP = 8, kPhO = 16, kPhT = 32, kPhQ1 = 64;
             if (!mbar_wait_loop(bar(L::WARM), 0)) abort = true;
             // A lane that gave up leaves the item's steps by itself; it meets the others at the
             // next item()'s vote (a vote at each step: 8 prompts of 900 to 2047 tokens 430 us,
@@ -659,11 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         odd = odd_words(step);
                         if (k == a && items++ > 0) wait(bars + L::O_FREE * 8 + of_s, kPhO);
                     }
-                    if (L::kApart && q) {
-                        if (scored) wait(bars + L::S_FREE * 8 + of_s, kPhS);
-                        scored = true;
-                    }
-                    if (!L::kApart && w && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
+                    if (w && !mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
                     if (turns > 0 || s == 1) wait(bars + L::TURN * 8 + of_s, kPhT);
                     ++turns;
                     tc05_fence_after_sync();
@@ -682,36 +693,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     };
-                    if (L::kApart && q) score();
+                    // 64 of the positions of O += P V
+                    auto weigh = [&](int kk0, bool first) {
+#pragma unroll
+                        for (int kk = kk0; kk < kk0 + 4; ++kk) {
+                            const uint32_t v = v_lo + kk * (2 * L::kGroup >> 4);
+                            umma_ts(col_o, col_s + kk * 8, v, kKvHi, kIdescO, kk > kk0 || !first);
+                            if (TWO) umma_ts(col_o, col_s + L::kRest + kk * 8, v, kKvHi, kIdescO, true);
+                        }
+                    };
                     if (w) {
                         // O += P V of step k
-                        if (L::kApart) {
-                            if (!mbar_wait_loop(bars + L::P_HALF * 8 + of_s, (phase & kPhP) != 0)) abort = true;
-                            tc05_fence_after_sync();
-                        }
-                        if (leader && odd == 0) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, kk > 0 || k != a);
-                                if (DIFF) umma_ts(col_o, col_p + 64 + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
-                            }
-                        }
+                        if (leader && odd == 0) weigh(0, k == a);
                         wait(bars + L::P_FULL * 8 + of_s, kPhP);
                         tc05_fence_after_sync();
                         if (leader) {
-                            if (odd == 0) {
-#pragma unroll
-                                for (int kk = 4; kk < 8; ++kk) {
-                                    umma_ts(col_o, col_p + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
-                                    if (DIFF)
-                                        umma_ts(col_o, col_p + 64 + kk * 8, v_lo + kk * (2 * L::kGroup >> 4), kKvHi, kIdescO, true);
-                                }
-                            }
-                            if (L::kApart) umma_commit(bars + L::P_EMPTY * 8 + of_s);
+                            if (odd == 0) weigh(4, false);
                             if (k + stride >= e) umma_commit(bars + L::O_DONE * 8 + of_s);
                         }
                     }
-                    if (!L::kApart && q) score();
+                    if (q) score();
                     if (leader) mbar_arrive(bars + L::TURN * 8 + (of_s ^ 8));
                     if (pv) {
                         if (leader) umma_commit(bars + (L::V_EMPTY + vs) * 8);
@@ -969,7 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + L::kColS + s * 128, col_o = tmem + lanes + L::kColO + s * D;
-        const uint32_t col_p = tmem + lanes + L::kColP + s * L::kPStep;
         const float scale = p.scale_log2;
         uint32_t g = 0, i = 0, ns = 0, items = 0;
         float *rows = reinterpret_cast<float *>(smem + L::kRows);
@@ -1002,9 +1002,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++ns;
                 }
                 if (idle) {
-                    // in step with the others: an arrival for the next step would count for this one
-                    if (L::kApart && lane == 0) mbar_arrive(bar(L::S_FREE + s));
-                    if (L::kApart && ns > 1 && !wait(bar(L::P_EMPTY + s), ns & 1)) break;
                     if (lane == 0) {
                         mbar_arrive(bar(L::P_HALF + s));
                         mbar_arrive(bar(L::P_FULL + s));
@@ -1049,11 +1046,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
                 tmem_landed<64>(v + 64);
-                if (L::kApart) {
-                    tc05_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0 && warm) mbar_arrive(bar(L::S_FREE + s));
-                }
                 if (bad != 0) {
 #pragma unroll 1
                     for (int c = 0; c < kKT; c += 32) {            // of 32 positions, those it sees
@@ -1067,12 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], fmaxf(f(i + j), f(i + 4 + j)));
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                // the products before S (P over S), or those that read the last weights, are done
-                if (L::kApart && ns > 1) {
-                    // in this layout the scores come before that product: their fence does not cover it
-                    if (!wait(bar(L::P_EMPTY + s), ns & 1)) break;
-                    tc05_fence_after_sync();
-                }
+                // the last step's second product was issued before these scores: it is done
                 const bool grown = (mx - m) * scale > kLazy;
                 if (__any_sync(0xffffffffu, grown)) {
                     const float alpha = grown ? ex2_approx((m - mx) * scale) : 1.f;
@@ -1094,22 +1081,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
-                    uint32_t w[16], rest[DIFF ? 16 : 1];
+                    uint32_t w[16], rest[TWO ? 16 : 1];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 e = fma2(make_float2(f(c + 2 * i), f(c + 2 * i + 1)), make_float2(scale, scale), make_float2(nb, nb));
                         e.x = ex2_approx(e.x);
                         e.y = ex2_approx(e.y);
-                        sum[i & 1] = add2(sum[i & 1], e);
+                        // the sum: of exactly the weights that the product uses
+                        if (TWO) sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = Elem<T>::pack2(e.x, e.y);
-                        if (DIFF) {
+                        if (TWO) {
                             float2 r;
                             Elem<T>::unpack2(w[i], r.x, r.y);
                             rest[i] = Elem<T>::pack2(e.x - r.x, e.y - r.y);
+                        } else {
+                            add_halves<T>(sum[i & 1], w[i]);
                         }
                     }
-                    tmem_st16(col_p + c / 2, w);
-                    if (DIFF) tmem_st16(col_p + 64 + c / 2, rest);
+                    tmem_st16(col_s + c / 2, w);
+                    if (TWO) tmem_st16(col_s + L::kRest + c / 2, rest);
                     if (c == 32) {                 // the product of the first 64 positions may begin
                         tmem_wait_st();
                         tc05_fence_before_sync();
@@ -1139,20 +1129,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i) o[i] = k > sh.begin(s) ? __uint_as_float(o32[i]) : 0.f;
 #pragma unroll 1
                             for (int t = 0; t < kKT; ++t) {
-                                uint32_t w2;
-                                tmem_ld1(col_p + t / 2, w2);
+                                uint32_t w2, rest = 0;
+                                tmem_ld1(col_s + t / 2, w2);
+                                if (TWO) tmem_ld1(col_s + L::kRest + t / 2, rest);
                                 tmem_wait_ld();
-                                asm volatile("" : "+r"(w2));
-                                float w[2];
+                                asm volatile("" : "+r"(w2), "+r"(rest));
+                                float w[2], r[2];
                                 Elem<T>::unpack2(w2, w[0], w[1]);
-                                float wt = (t & 1) ? w[1] : w[0];
-                                if (DIFF) {
-                                    tmem_ld1(col_p + 64 + t / 2, w2);
-                                    tmem_wait_ld();
-                                    asm volatile("" : "+r"(w2));
-                                    Elem<T>::unpack2(w2, w[0], w[1]);
-                                    wt += (t & 1) ? w[1] : w[0];
-                                }
+                                Elem<T>::unpack2(rest, r[0], r[1]);
+                                const float wt = (t & 1) ? w[1] + r[1] : w[0] + r[0];
                                 const bool sees = t0 + t >= row_lo && t0 + t <= row_hi;
                                 const unsigned char *vr = smem + L::kVRing + slot * L::kTile + (t >> 3) * L::kGroup +
                                                           (c0 >> 6) * 1024 + (t & 7) * 128;
@@ -1213,43 +1198,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <typename T, int D, bool DIFF, bool ROWS>
+template <typename T, int D, bool DIFF, bool ROWS, bool TWO>
 cudaError_t plan_one(ChunkPlan *plan) {
     static std::atomic<int> limit[64];
     int sms = 0;
-    cudaError_t e = ensure_smem_limit(chunk_umma_kernel<T, D, DIFF, ROWS>, Layout<D, DIFF>::kBytes, limit);
+    cudaError_t e = ensure_smem_limit(chunk_umma_kernel<T, D, DIFF, ROWS, TWO>, Layout<D, DIFF>::kBytes, limit);
     if (e != cudaSuccess) return e;
     e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     plan->grid = sms;
     plan->maps = DIFF ? 2 : 1;
     plan->rows = 256 / plan->maps;
+    plan->two_parts = TWO;
     plan->rec_floats = chunk_rec_floats(256, D);
     return cudaSuccess;
 }
 
-template <typename T, int D, bool DIFF, bool ROWS>
+template <typename T, int D, bool DIFF, bool ROWS, bool TWO>
 cudaError_t launch_one(const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream, const CUtensorMap &kmap,
                        const CUtensorMap &vmap, int box_rows, const CUtensorMap &qmap, int q_tokens) {
-    return launch_clustered(chunk_umma_kernel<T, D, DIFF, ROWS>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
+    return launch_clustered(chunk_umma_kernel<T, D, DIFF, ROWS, TWO>, plan.grid, kThreads, Layout<D, DIFF>::kBytes, 1, stream, kmap,
                             vmap, qmap, p, box_rows, q_tokens);
 }
 
 template <typename T, int D, typename F>
-cudaError_t with_form(bool diff, bool rows, F f) {
-    if (diff) return rows ? f.template operator()<T, D, true, true>() : f.template operator()<T, D, true, false>();
-    return rows ? f.template operator()<T, D, false, true>() : f.template operator()<T, D, false, false>();
+cudaError_t with_form(bool diff, bool rows, bool two, F f) {
+    if (diff) return rows ? f.template operator()<T, D, true, true, true>() : f.template operator()<T, D, true, false, true>();
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        if (two && !rows) return f.template operator()<T, D, false, false, true>();
+    if (two) return cudaErrorInvalidValue;         // (no call is row by row with so few rows)
+    return rows ? f.template operator()<T, D, false, true, false>() : f.template operator()<T, D, false, false, false>();
 }
 template <typename F>
-cudaError_t with_kernel(int dtype, int head_dim, bool diff, bool rows, F f) {
-    if (dtype == PA_F16) return head_dim == 64 ? with_form<__half, 64>(diff, rows, f) : with_form<__half, 128>(diff, rows, f);
-    return head_dim == 64 ? with_form<__nv_bfloat16, 64>(diff, rows, f) : with_form<__nv_bfloat16, 128>(diff, rows, f);
+cudaError_t with_kernel(int dtype, int head_dim, bool diff, bool rows, bool two, F f) {
+    if (dtype == PA_F16)
+        return head_dim == 64 ? with_form<__half, 64>(diff, rows, two, f) : with_form<__half, 128>(diff, rows, two, f);
+    return head_dim == 64 ? with_form<__nv_bfloat16, 64>(diff, rows, two, f)
+                          : with_form<__nv_bfloat16, 128>(diff, rows, two, f);
 }
 
 struct Planner {
     ChunkPlan *plan;
-    template <typename T, int D, bool DIFF, bool ROWS>
-    cudaError_t operator()() const { return plan_one<T, D, DIFF, ROWS>(plan); }
+    template <typename T, int D, bool DIFF, bool ROWS, bool TWO>
+    cudaError_t operator()() const { return plan_one<T, D, DIFF, ROWS, TWO>(plan); }
 };
 struct Launcher {
     const ChunkParams &p;
@@ -1257,8 +1248,8 @@ struct Launcher {
     int box_rows, q_tokens;
     const ChunkPlan &plan;
     cudaStream_t stream;
-    template <typename T, int D, bool DIFF, bool ROWS>
-    cudaError_t operator()() const { return launch_one<T, D, DIFF, ROWS>(p, plan, stream, kmap, vmap, box_rows, qmap, q_tokens); }
+    template <typename T, int D, bool DIFF, bool ROWS, bool TWO>
+    cudaError_t operator()() const { return launch_one<T, D, DIFF, ROWS, TWO>(p, plan, stream, kmap, vmap, box_rows, qmap, q_tokens); }
 };
 
 }  // namespace
@@ -1267,14 +1258,14 @@ bool chunk_umma_supported(int dtype, int head_dim) {
     return (dtype == PA_F16 || dtype == PA_BF16) && (head_dim == 64 || head_dim == 128);
 }
 
-cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, int box_rows, ChunkPlan *plan) {
-    return with_kernel(dtype, head_dim, diff, box_rows == 0, Planner{plan});
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, bool two_parts, int box_rows, ChunkPlan *plan) {
+    return with_kernel(dtype, head_dim, diff, box_rows == 0, two_parts, Planner{plan});
 }
 
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
                               int box_rows, const CUtensorMap &qmap, int q_tokens, const ChunkPlan &plan,
                               cudaStream_t stream) {
-    return with_kernel(dtype, head_dim, plan.maps == 2, box_rows == 0,
+    return with_kernel(dtype, head_dim, plan.maps == 2, box_rows == 0, plan.two_parts,
                        Launcher{p, kmap, vmap, qmap, box_rows, q_tokens, plan, stream});
 }
 

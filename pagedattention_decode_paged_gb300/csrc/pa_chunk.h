@@ -52,6 +52,7 @@ struct ChunkPlan {
     int grid = 0;
     int rows = 0;              // query rows of an item (of each map)
     int maps = 1;
+    bool two_parts = false;    // 16-bit types: weights as rounded weight and rest
     int rec_floats = 0;        // floats of a record: rows * maps of head_dim, their maxima and their sums
 };
 inline int chunk_rec_floats(int rows_all_maps, int head_dim) { return rows_all_maps * (head_dim + 2); }
@@ -61,14 +62,14 @@ bool chunk_supported(int dtype, int head_dim, bool diff);
 // fp32 on the CUDA cores, 16-bit on mma.sync (any block size).
 cudaError_t plan_chunk_f32(int head_dim, bool diff, ChunkPlan *plan);
 cudaError_t launch_chunk_f32(int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
-cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, ChunkPlan *plan);
+cudaError_t plan_chunk_mma(int dtype, int head_dim, bool diff, bool two_parts, ChunkPlan *plan);
 cudaError_t launch_chunk_mma(int dtype, int head_dim, const ChunkParams &p, const ChunkPlan &plan, cudaStream_t stream);
 
 // 16-bit types, head_dim 64 and 128, on tcgen05; tensor maps of the pools in
 // boxes of box_rows rows, a divisor of 128 and of the block size, or box_rows 0 and
 // no maps: row by row.
 bool chunk_umma_supported(int dtype, int head_dim);
-cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, int box_rows, ChunkPlan *plan);
+cudaError_t plan_chunk_umma(int dtype, int head_dim, bool diff, bool two_parts, int box_rows, ChunkPlan *plan);
 // qmap: the queries in boxes of q_tokens tokens of a group's heads (q_tokens 0:
 // a tile is not whole tokens, and the map is not used).
 cudaError_t launch_chunk_umma(int dtype, int head_dim, const ChunkParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
