@@ -66,12 +66,15 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_f32_kernel(const __grid_con
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
 
-    zero_bad_sequences<float>(p, D, tid, kThreads);
     Slices slices;
     Sched<R, kKT> it;
-    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices)
-                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1));
-    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
+    int errors;
+    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices, &errors)
+                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1, &errors));
+    if (warp == 0) {
+        if (p.B <= kWarpSeqs) errors = all_errors(p, errors);
+        if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices, errors);
+    }
     if (!has) return;
 
     const int map = DIFF ? ty / 8 : 0;         // of this thread's rows 4 ty .. 4 ty + 3

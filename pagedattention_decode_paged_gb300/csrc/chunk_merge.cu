@@ -21,6 +21,22 @@ namespace {
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 32;
 
+// Zeros in the rows of the sequences whose positions are out of range, by all threads
+// of the launch (a prompt of 16384 tokens, 64 heads of 128, is 268 MB).
+__device__ __noinline__ void zero_bad_sequences(const ChunkParams &p, int row_bytes) {
+    const int64_t threads = (int64_t)gridDim.x * gridDim.y * kMergeThreads;
+    const int64_t me = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kMergeThreads + threadIdx.x;
+    for (int b = 0; b < p.B; ++b) {
+        int pos, error;
+        chunk::seq_of(p, b, &pos, &error);
+        if (error != PA_DEVERR_BAD_POS) continue;
+        const int64_t token = (int64_t)p.H * row_bytes / 16;
+        const int64_t n = (p.counts != nullptr ? __ldg(p.counts + b) : p.T) * token;
+        uint4 *out = reinterpret_cast<uint4 *>(p.out) + (int64_t)b * p.T * token;
+        for (int64_t i = me; i < n; i += threads) out[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // rows: of a map in a record.
 template <typename T, int D, bool DIFF>
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p, const int rows) {
@@ -33,6 +49,7 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     const int w = blockIdx.x;
     const ChunkCut cut = p.cuts[w];
     const int r0 = blockIdx.y * kMergeRows;
+    if (cut.zeros != 0) zero_bad_sequences(p, D * (int)sizeof(T));
     if (cut.b < 0 || r0 >= cut.rows) return;
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     // a state of each CTA that shares the item

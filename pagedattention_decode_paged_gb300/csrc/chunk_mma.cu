@@ -91,12 +91,15 @@ __global__ void __launch_bounds__(kThreads) chunk_mma_kernel(const __grid_consta
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::kPre);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    zero_bad_sequences<T>(p, D, tid, kThreads);
     Slices slices;
     Sched<R, kKT> it;
-    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices)
-                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1));
-    if (tid == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices);
+    int errors;
+    const bool has = p.B <= kWarpSeqs ? it.locate(p, slices, &errors)
+                                      : it.locate(p, slices, pre, Sched<R, kKT>::build(p, pre, tid, kThreads, 1, &errors));
+    if (warp == 0) {
+        if (p.B <= kWarpSeqs) errors = all_errors(p, errors);
+        if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, has, slices, errors);
+    }
     if (!has) return;
 
     const int map = DIFF ? warp >> 1 : 0;

@@ -17,7 +17,8 @@
 // if it begins an item that goes on in the next slice; and CTA w writes
 // cuts[w]: which item its slice begins inside of, if that item's first tile
 // belongs to the slice before, and the last CTA that shares it.  The second
-// launch joins them.  No CTA waits for another.  In a record 4 neighbouring
+// launch joins them, and zeroes the rows of sequences whose positions are out of
+// range, where nothing waits for it.  No CTA waits for another.  In a record 4 neighbouring
 // columns of neighbouring rows lie side by side, so that a row to a thread is
 // written and read in whole lines.
 //
@@ -147,10 +148,11 @@ struct Sched {
         return s;
     }
 
-    // tiles of sequence b
-    static __device__ __forceinline__ int64_t seq_tiles(const ChunkParams &p, int b) {
+    // tiles of sequence b; its error is added to *errors
+    static __device__ __forceinline__ int64_t seq_tiles(const ChunkParams &p, int b, int *errors) {
         int pos, error;
         const int cnt = seq_of(p, b, &pos, &error), nq = items(p, cnt);
+        *errors |= error;
         return cnt > 0 ? p.Hkv * tiles_before(p, pos, cnt, nq, nq) : 0;
     }
 
@@ -160,16 +162,24 @@ struct Sched {
 
     // Sums over groups of sequences; pre: [kGroups + 1] in shared memory.  Threads
     // 0 to n - 1 (whole warps) call it, with a named barrier of their own; it ends
-    // with that barrier.  Returns the sequences of a group.
-    static __device__ __forceinline__ int build(const ChunkParams &p, int64_t *pre, int tid, int n, int barrier) {
+    // with that barrier.  Returns the sequences of a group.  *errors: of all sequences,
+    // though of positions alone (others are reported here).
+    static __device__ __forceinline__ int build(const ChunkParams &p, int64_t *pre, int tid, int n, int barrier, int *errors) {
         const int per = (p.B + kGroups - 1) / kGroups, groups = (p.B + per - 1) / per;
         auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(n) : "memory"); };
+        int mine = 0;
         for (int g = tid; g < groups; g += n) {
             int64_t s = 0;
-            for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) s += seq_tiles(p, b);
+            for (int b = g * per; b < min(p.B, (g + 1) * per); ++b) s += seq_tiles(p, b, &mine);
             pre[g + 1] = s;
         }
-        sync();
+        if (mine != 0 && blockIdx.x == 0) report(p.err_word, mine);
+        asm volatile(
+            "{\n\t.reg .pred mine, any;\n\tsetp.ne.u32 mine, %3, 0;\n\tbar.red.or.pred any, %1, %2, mine;\n\t"
+            "selp.s32 %0, %4, 0, any;\n\t}"
+            : "=r"(*errors)
+            : "r"(barrier), "r"(n), "r"(mine & PA_DEVERR_BAD_POS), "n"(PA_DEVERR_BAD_POS)
+            : "memory");
         if (tid < 32) {                            // inclusive sums, 32 at a time
             int64_t run = 0;
             for (int g0 = 0; g0 < groups; g0 += 32) {
@@ -206,11 +216,12 @@ struct Sched {
     // Up to kWarpSeqs sequences a warp sums over by itself, without barriers: what a
     // call spends before its first copy is a chain of loads and of instructions
     // fetched for the first time (32 tokens behind 2047 cached ones each: 7 us).
-    // More have been summed by build().
-    __device__ __forceinline__ bool locate(const ChunkParams &p, Slices &sl) {
+    // More have been summed by build().  *errors: of the lane's sequences.
+    __device__ __forceinline__ bool locate(const ChunkParams &p, Slices &sl, int *errors) {
         const int lane = threadIdx.x & 31, per = (p.B + 31) / 32;
         int64_t mine = 0;
-        for (int b = lane * per; b < min(p.B, (lane + 1) * per); ++b) mine += seq_tiles(p, b);
+        *errors = 0;
+        for (int b = lane * per; b < min(p.B, (lane + 1) * per); ++b) mine += seq_tiles(p, b, errors);
         int64_t incl = mine;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
@@ -305,11 +316,12 @@ struct Sched {
 };
 
 // This CTA's entry of the cuts, from the first share of its slice (has: it has
-// one).
+// one) and the errors of the sequences.
 template <int R, int KT>
-__device__ __forceinline__ ChunkCut cut_entry(const ChunkParams &p, const Sched<R, KT> &s, bool has, const Slices &sl) {
+__device__ __forceinline__ ChunkCut cut_entry(const ChunkParams &p, const Sched<R, KT> &s, bool has, const Slices &sl, int errors) {
     ChunkCut c{};
     c.b = -1;
+    c.zeros = (errors & PA_DEVERR_BAD_POS) != 0;
     if (!has || s.x.k0 == 0 || s.first < sl.begin((int)blockIdx.x - 1)) return c;
     c.b = s.x.b;
     c.hk = s.x.hk;
@@ -322,22 +334,12 @@ __device__ __forceinline__ ChunkCut cut_entry(const ChunkParams &p, const Sched<
 // Columns c to c + 3 of a row of a record (of `rows` rows in all).
 __device__ __forceinline__ float *record_at(float *rec, int rows, int row, int c) { return rec + ((c >> 2) * rows + row) * 4 + (c & 3); }
 
-// Report sequences whose arguments are out of range, and zero the rows of
-// those whose positions are; sequence b is CTA b % gridDim's.  Called by `threads`
-// threads, this one `tid`.
-template <typename T>
-__device__ __forceinline__ void zero_bad_sequences(const ChunkParams &p, int D, int tid, int threads) {
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        int pos, error;
-        seq_of(p, b, &pos, &error);
-        if (error == 0) continue;
-        if (tid == 0) report(p.err_word, error);
-        if (error != PA_DEVERR_BAD_POS) continue;
-        const int cnt = p.counts != nullptr ? p.counts[b] : p.T;
-        const int64_t row = (int64_t)p.H * D, n = cnt * row;
-        T *out = reinterpret_cast<T *>(p.out) + (int64_t)b * p.T * row;
-        for (int64_t i = tid; i < n; i += threads) out[i] = Elem<T>::from_float(0.f);
-    }
+// The errors that the lanes of a warp found in their sequences, put together and
+// reported by CTA 0.
+__device__ __forceinline__ int all_errors(const ChunkParams &p, int errors) {
+    errors = (int)__reduce_or_sync(0xffffffffu, (unsigned)errors);
+    if (errors != 0 && blockIdx.x == 0 && (threadIdx.x & 31) == 0) report(p.err_word, errors);
+    return errors;
 }
 
 // Byte offset in the pools of the row that holds cache position t of kv head

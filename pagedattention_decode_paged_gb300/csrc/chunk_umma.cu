@@ -445,19 +445,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // what went before: tensor memory, barriers and the weights' first step wait for
         // none of it
         grid_dependency_wait();
-        int per = 0;
-        if (p.B > kWarpSeqs) per = Schedule::build(p, pre, threadIdx.x - kProducerWarp * 32, kThreads - kProducerWarp * 32, 1);
+        int per = 0, errors;
+        if (p.B > kWarpSeqs)
+            per = Schedule::build(p, pre, threadIdx.x - kProducerWarp * 32, kThreads - kProducerWarp * 32, 1, &errors);
         if (warp == kProducerWarp) {
             // lane s copies box s (box_rows positions) of each tile; table entries are
             // looked up a tile ahead
             Slices slices;
             Schedule it;
-            bool has = p.B <= kWarpSeqs ? it.locate(p, slices) : it.locate(p, slices, pre, per);
+            bool has = p.B <= kWarpSeqs ? it.locate(p, slices, &errors) : it.locate(p, slices, pre, per);
             __syncwarp();
             fence_proxy_async_smem();              // the ring's copies come after the sums
             const int boxes = ROWS ? 0 : kKT / box_rows;
             const uint32_t box_bytes = (uint32_t)box_rows * D * 2;
             uint32_t g = 0, i = 0;
+            auto put_cut = [&](bool any) {
+                const int of_all = p.B <= kWarpSeqs ? all_errors(p, errors) : errors;
+                if (lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, any, slices, of_all);
+            };
             auto publish = [&](bool stop) {
                 if (i >= kItems && !mbar_wait_loop(bar(L::ITEM_EMPTY + i % kItems), (i / kItems - 1) & 1)) abort = true;
                 abort = __any_sync(0xffffffffu, abort);
@@ -601,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         needed = ahead_needed;
                     }
                 }
-                if (i == 1 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, true, slices);
+                if (i == 1) put_cut(true);
                 has = it.next(p);
             }
-            if (i == 0 && lane == 0) p.cuts[blockIdx.x] = cut_entry<R, kKT>(p, it, false, slices);
+            if (i == 0) put_cut(false);
             if (ROWS) landed(0);
             publish(true);
             // every copy has landed before the CTA may exit
@@ -798,7 +803,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 abort = __any_sync(0xffffffffu, abort);
                 return !abort;
             };
-            zero_bad_sequences<T>(p, D, threadIdx.x - kOutWarp * 32, 128);
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
             // look over the V tile of step k of an item, tile g of the CTA
             auto look = [&](const Share &sh, int k) {

@@ -44,7 +44,8 @@ struct ChunkCut {
     int32_t hk;                // kv head
     int32_t n0, rows;          // first of the head's rows, rows
     int32_t last;
-    int32_t pad[3];
+    int32_t zeros;             // the same in all: sequences with positions out of range, whose rows the launch zeroes
+    int32_t pad[2];
 };
 
 // What a kernel variant needs of the workspace on the current device.
