@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
     if (cut.zeros != 0) zero_bad_sequences(p, D * (int)sizeof(T));
     if (cut.b < 0 || r0 >= cut.rows) return;
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    // a state of each CTA that shares the item
+    // A state of each CTA that shares the item.  The launch before writes them while this
+    // one may be resident already, so they are not for the read-only path.
     const int states = cut.last - w + 2, all = rows * MAPS;
     auto record = [&](int s) { return p.records + (int64_t)(s == 0 ? (w - 1) * 2 + 1 : (w - 1 + s) * 2) * p.rec_floats; };
     // rows of a warp: 8, 16 or 32; lanes `take` and on of a row take every `step`th state
@@ -68,8 +69,8 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll 8
             for (int s = take; s < states; s += step) {
                 const float *ml = record(s) + (int64_t)all * D + row;
-                M = fmaxf(M, __ldg(ml));
-                bad |= __ldg(ml + all) < 0.f;
+                M = fmaxf(M, __ldcg(ml));
+                bad |= __ldcg(ml + all) < 0.f;
             }
             for (int h = lrows; h < 32; h <<= 1) {
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, h));
@@ -82,11 +83,11 @@ __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const __grid
 #pragma unroll 4
             for (int s = take; s < states; s += step) {
                 const float *rec = record(s), *ml = rec + (int64_t)all * D + row;
-                const float f = merge_weight(__ldg(ml), M);
-                L += f * __ldg(ml + all);
+                const float f = merge_weight(__ldcg(ml), M);
+                L += f * __ldcg(ml + all);
 #pragma unroll
                 for (int i = 0; i < C4; ++i) {
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(rec) + (part * C4 + i) * all + row);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec) + (part * C4 + i) * all + row);
                     acc[i].x += f * v.x, acc[i].y += f * v.y, acc[i].z += f * v.z, acc[i].w += f * v.w;
                 }
             }
