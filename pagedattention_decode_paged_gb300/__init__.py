@@ -864,13 +864,16 @@ def _attend_rows(name, out, q, k_pool, v_pool, block_table, positions, scale, wo
     if k_pool.dtype != dt or v_pool.dtype != dt:
         raise ValueError("the pools must be of the queries' dtype")
     _pools_hold(k_pool, v_pool, None, num_kv_heads, D, block_size, num_blocks, block_stride)
+    diff = name == "paged_attention_chunk_diff"
+    if diff and lambdas is None:
+        raise ValueError("the differential form needs lambdas, one per head")
     on = _launch_stream(stream, name, q, out, k_pool, v_pool, block_table, positions, counts, workspace, err_word,
                         lambdas, norm)
     shape = _SHAPE.pack(B, H, num_kv_heads, D, block_size, MB, num_blocks, block_stride, dtype_code(dt))
     args = (out.data_ptr(), q.data_ptr(), qs, T, k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
             positions.data_ptr(), _addr(counts), scale, window, workspace.data_ptr(), workspace.numel(), _addr(err_word),
             on)
-    if lambdas is None:
+    if not diff:
         return _issue(load().paged_attention_chunk, (shape, *args), name, prepare)
     if lambdas.dtype != torch.float32 or not lambdas.is_contiguous() or lambdas.numel() != H:
         raise ValueError("lambdas must hold one contiguous torch.float32 element per head")
