@@ -728,8 +728,8 @@ def paged_kv_append_rope_axes(q_out, q, k_new, v_new, k_pool, v_pool, block_tabl
     """paged_kv_append_rope for tokens with positions on several axes: pair i
     turns by axis_positions[pair_axis[i]] ([axes][B][T] int32); pair_axis is
     bytes (or ints) of rotary_dim/2 axes, see rope_axes."""
-    if cos_sin is None or axis_positions is None:
-        raise ValueError("axes need cos_sin and axis_positions")
+    if cos_sin is None or axis_positions is None or pair_axis is None or axis_positions.dim() == 0:
+        raise ValueError("axes need cos_sin, axis_positions [axes][B][T] and pair_axis")
     return _append_rows("paged_kv_append_rope_axes", q_out, q, k_new, v_new, k_pool, v_pool, None, 1.0, 1.0, block_table,
                         positions, counts, cos_sin, None, interleaved, q_norm, k_norm, eps, block_size, num_blocks,
                         block_stride, err_word, stream, prepare, axis_positions, pair_axis)

@@ -36,3 +36,23 @@ def test_the_differential_form_without_lambdas_is_refused(issued, prepare):
     pa.paged_attention_chunk(*args, s.scale, ws, prepare=prepare, **kw)
     assert [what for _, what in issued] == ["paged_attention_chunk_diff", "paged_attention_chunk"]
     assert [fn.__name__ for fn, _ in issued] == [what for _, what in issued]
+
+
+@pytest.mark.parametrize("prepare", [False, True])
+@pytest.mark.parametrize("over", [dict(pair_axis=None), dict(axis_positions=None), dict(cos_sin=None),
+                                  dict(axis_positions=torch.tensor(3, dtype=torch.int32))])
+def test_the_append_with_axes_without_its_axes_is_refused(issued, over, prepare):
+    """pair_axis=None went on to the entry point with another operator's arguments."""
+    B, T, H, D = 2, 3, 2, 32
+    x = torch.zeros((B, T, H, D), dtype=torch.float16)
+    pool = torch.zeros((4, 2, H, 16, D), dtype=torch.float16)
+    flat = pool.view(-1)
+    args = dict(q_out=x, q=x, k_new=x, v_new=x, k_pool=flat, v_pool=flat[pool.stride(1):],
+                block_table=torch.zeros((B, 2), dtype=torch.int32), positions=torch.zeros(B, dtype=torch.int32),
+                axis_positions=torch.zeros((3, B, T), dtype=torch.int32), cos_sin=torch.zeros((9, D)),
+                pair_axis=pa.rope_axes((6, 5, 5)), block_size=16, num_blocks=4, block_stride=pool.stride(0))
+    with pytest.raises(ValueError, match="pair_axis"):
+        pa.paged_kv_append_rope_axes(**{**args, **over}, prepare=prepare)
+    assert not issued
+    pa.paged_kv_append_rope_axes(**args, prepare=prepare)
+    assert [what for _, what in issued] == ["paged_kv_append_rope_axes"]
