@@ -31,9 +31,6 @@ constexpr int kThreads = 128;
 constexpr int kKT = 64;                    // cache positions per tile
 constexpr int kRows = 64;                  // query rows of all maps
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {

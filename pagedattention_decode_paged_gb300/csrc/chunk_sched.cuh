@@ -1,5 +1,5 @@
-// chunk_sched.cuh -- the schedule of attention of several new tokens, and the
-// last step of a row.
+// chunk_sched.cuh -- the schedule of attention of several new tokens, the last
+// step of a row, and what else its kernels share.
 //
 // The query rows of a (sequence, kv head) are numbered token by token, the G
 // heads of the group beside one another: row n is head n % G of token n / G.
@@ -43,6 +43,20 @@ struct Item {
     int lo, n;                 // first tile of cache positions, tiles
     int k0, k1;
 };
+
+// 16 bytes to shared memory, asynchronously (cp.async groups); zeros unless `take`.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+// Two fused products and sums in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 
 // New tokens of sequence b and where they start; 0 when there is nothing to do
 // or an argument is out of range (*error: the PA_DEVERR bit).
