@@ -51,20 +51,30 @@ int umma_box_rows(const pa_shape *s) {
 
 // Row by row, one warp of the tcgen05 kernel's CTA copies K and V; on mma.sync the
 // four of each of up to seven CTAs do.  Query rows of a kv head (tokens of the padded
-// batch times heads of the group) above which the products outweigh that: 32
-// sequences, 64 heads on 8 of 128, blocks of 1, 128 rows behind 2047 tokens 201 us
-// against 192, behind none 25.7 against 19.4; 256 rows 217 against 361 and 28 against
-// 34; 8 rows 178 against 96.
+// batch times heads of the group) above which the products outweigh that.  tcgen05
+// against mma.sync, fp16, behind 2047 tokens: 32 sequences, 64 heads on 8 of 128, blocks
+// of 1: 8 rows 178 and 96 us, 64 rows 195 and 108, 128 rows 202 and 196, 256 rows 218
+// and 367; 16 sequences, 32 heads on 8 of 64, blocks of 3: 128 rows 82 and 64, 256 rows 91
+// and 111; 32 heads of 128: 128 rows 403 and 368, 256 rows 445 and 724; behind none 128
+// rows 26 and 20, 16 and 11, 42 and 42, 256 rows 29 and 35, 17 and 16, 78 and 92.  Of one
+// kv head in 4 sequences there is too little for either (256 rows 29 and 27).  The host
+// knows the padded batch, not the counts: a step of one piece of 512 tokens beside 63
+// single ones over blocks of 1 takes tcgen05's 541 us for 525.
 constexpr int kRowsAbove = 128;
 
 // Query rows of a kv head (tokens of the padded batch times heads of the group) up to
-// which bf16 weights are held in two parts, as the decode of the same cache holds them:
-// single and speculative tokens come out as exact from either.  They wait for memory (7
-// to 9% for the second part); prompts would wait for the products (24 to 33%).  fp16 has
-// one part, and is normalised by what it was rounded to, in both.
+// which weights are held in two parts, so that single and speculative tokens come out as
+// exact as from the decode of the same cache (32 single tokens behind 2047, 64 heads on 8
+// of 128: errors of 1.0 times the rounding of an exact result, 1.35 to 1.4 with one part).
+// They mostly wait for memory (7 to 9% for the second part; 64 of 32 heads without
+// groups, 128 rows multiplied for each, 28%); prompts would wait for the products (24 to
+// 33%).  By the call, not by the sequence: a kernel with both forms takes 480 us for the
+// 422 of 8 prompts of 900 to 2047 tokens, and 199 for 159 where single tokens are mixed
+// with pieces of prompts.
 constexpr int kRowsInTwoParts = 128;
+static_assert(kRowsInTwoParts <= kRowsAbove, "no kernel has two parts of the plain form row by row");
 bool two_parts(const pa_shape *s, bool diff, int64_t rows) {
-    return diff || (s->dtype == PA_BF16 && rows <= kRowsInTwoParts);
+    return diff || (s->dtype != PA_F32 && rows <= kRowsInTwoParts);
 }
 
 // The kernel for a call, and its plan on the current device.

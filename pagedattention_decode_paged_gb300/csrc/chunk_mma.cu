@@ -8,17 +8,18 @@
 // with the running maximum m and sum l of each row in registers, the weights
 // rounded to the type for the second product and summed as rounded, or (TWO) as two
 // parts, rounded weight and rest: in the differential form, whose two sums may all but
-// cancel, and for few rows in bf16, as the decode holds them (32 single tokens behind
+// cancel, and for few rows, as the decode holds them (32 single tokens behind
 // 2047, 64 heads on 8 of 128 in blocks of 1: 96 us with one part, 105 so; head_dim 256
 // for all rows would take the prompts below to 356).  Rows of K and
 // V come by 16-byte asynchronous copies from wherever the block table puts
 // them, one tile ahead of the products; each row's place is looked up two tiles
 // ahead.  Bound by the warps' own latency, four or eight of them on an SM (issue
-// 17%, tensor pipe 26%): 4 prompts of 1024 tokens, 16 heads on 4 of 256 320 us, 108
+// 17%, tensor pipe 26%): 4 prompts of 1024 tokens, 16 heads on 4 of 256 320 us, 107
 // TFLOP/s; 1 token behind 2047, 32 sequences, 64 heads on 8 of 128 in blocks of 1
-// 96 us, 2.9 TB/s.  It is here for the shapes that tensor memory does not fit, for
-// scales that are not positive and for few rows over blocks that boxes of 8 rows do
-// not fit.
+// 105 us, 2.6 TB/s.  At head_dim 256 two parts do not fit the registers: a thread stores
+// 128 to 134 bytes of its own and loads 592 to 596 (fp16 with one part 40 and 56).
+// It is here for head_dim 32 and 256, which chunk_umma.cu is not built for, for scales
+// that are not positive and for few rows over blocks that boxes of 8 rows do not fit.
 #include "chunk_sched.cuh"
 
 namespace pa {
@@ -391,15 +392,16 @@ cudaError_t with_dim(int head_dim, F f) {
     }
     return cudaErrorInvalidValue;
 }
+template <typename T, typename F>
+cudaError_t with_form(int head_dim, bool diff, bool two, F f) {
+    if (diff) return with_dim<T, true, true>(head_dim, f);
+    return two ? with_dim<T, false, true>(head_dim, f) : with_dim<T, false, false>(head_dim, f);
+}
 template <typename F>
 cudaError_t with_kernel(int dtype, int head_dim, bool diff, bool two, F f) {
-    if (dtype == PA_F16) {
-        if (two && !diff) return cudaErrorInvalidValue;
-        return diff ? with_dim<__half, true, true>(head_dim, f) : with_dim<__half, false, false>(head_dim, f);
-    }
-    if (dtype != PA_BF16) return cudaErrorInvalidValue;
-    if (diff) return with_dim<__nv_bfloat16, true, true>(head_dim, f);
-    return two ? with_dim<__nv_bfloat16, false, true>(head_dim, f) : with_dim<__nv_bfloat16, false, false>(head_dim, f);
+    if (dtype == PA_F16) return with_form<__half>(head_dim, diff, two, f);
+    if (dtype == PA_BF16) return with_form<__nv_bfloat16>(head_dim, diff, two, f);
+    return cudaErrorInvalidValue;
 }
 
 struct Planner {

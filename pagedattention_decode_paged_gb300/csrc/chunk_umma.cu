@@ -16,15 +16,16 @@
 // for the other.  An item of up to 128 rows (single tokens, ends of prompts) has
 // its steps dealt to the two tiles in turn instead, and their states are joined
 // at its end (of the item or of the CTA's share of it; 4 tokens behind 2048 in 32
-// sequences, 64 heads: 66 us with two states to a share's record, 62 with one).
+// sequences, 64 heads, one part of weights: 66 us with two states to a share's record,
+// 62 with one).
 //
 // What bounds it: long contexts, the tensor core (4096 tokens behind 28672, 64
-// heads on 8 of 128: 2.63 ms, 1.57 PFLOP/s of what is seen, 82% of a library product's
-// rate); prompts, a step's way through both products and the exponentials, columns of
-// the diagonal that are not seen, starts and ends of items (8 of 900 to 2047 tokens: 410 us,
-// 1.10 PFLOP/s, the tensor core busy 59% of the time); few rows, the copies of K and V
-// and 20 us of start, records and merge (the 62 us: 3.5 TB/s from memory); blocks that
-// are copied row by row, the copying warp.
+// heads on 8 of 128: 2.75 ms back to back, 1.50 PFLOP/s of what is seen, 78% of a library
+// product's rate in a burst); prompts, a step's way through both products and the
+// exponentials, columns of the diagonal that are not seen, starts and ends of items (8 of
+// 900 to 2047 tokens: 422 us, 1.07 PFLOP/s, the tensor core busy 58% of the time); few
+// rows, the copies of K and V and 20 us of start, records and merge (32 x 4 tokens behind
+// 2048: 67 us, 3.4 TB/s from memory); blocks that are copied row by row, the copying warp.
 //
 // Roles (512 threads): warps 0-3 and 4-7 the weights of tile 0 and 1; warp 8 the
 // schedule and the copies of K and V; warps 9 and 10 the products of tile 0 and 1,
@@ -42,8 +43,8 @@
 // them is then as far from exact as its own rounding (1.4 times the error of an exact
 // product's rounded result).  TWO: rounded weight and rest (in the columns that S has
 // and P not), 1.0 times: in the differential form, where two such sums may all but
-// cancel, and for few rows in bf16, which the decode holds so too (32 x 4 tokens behind
-// 2048, 64 heads, 62 us with one part, 66 so).  Two parts for all would take the
+// cancel, and for few rows, so that they come out as from the decode (32 x 4 tokens behind
+// 2048, 64 heads, 62 us with one part, 67 so).  Two parts for all would take the
 // prompts to 530 us and 4096 tokens behind 28672 from 2.7 ms to 3.6.
 //
 // m is the maximum at the time it was last taken: O is rescaled only when a row's
@@ -1217,9 +1218,7 @@ cudaError_t launch_one(const ChunkParams &p, const ChunkPlan &plan, cudaStream_t
 template <typename T, int D, typename F>
 cudaError_t with_form(bool diff, bool rows, bool two, F f) {
     if (diff) return rows ? f.template operator()<T, D, true, true, true>() : f.template operator()<T, D, true, false, true>();
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        if (two && !rows) return f.template operator()<T, D, false, false, true>();
-    if (two) return cudaErrorInvalidValue;         // (no call is row by row with so few rows)
+    if (two) return rows ? cudaErrorInvalidValue : f.template operator()<T, D, false, false, true>();
     return rows ? f.template operator()<T, D, false, true, false>() : f.template operator()<T, D, false, false, false>();
 }
 template <typename F>

@@ -94,7 +94,7 @@ class Marks:
 
 
 def two_parts(s):
-    return s.diff or (s.dtype == BF16 and s.T * (s.H // s.Hkv) <= 128)
+    return s.diff or (s.dtype != F32 and s.T * (s.H // s.Hkv) <= 128)
 
 
 def stairs(n):

@@ -1,5 +1,5 @@
 """GPU checks of how 16-bit weights enter the second product: in two parts for
-few rows of bf16 and in the differential form, else in one, and then normalised by
+few rows and in the differential form, else in one, and then normalised by
 what they were rounded to.  Keys are such that scores hold no rounding but the
 scale's: what is left is the weights'."""
 import math
@@ -33,19 +33,21 @@ def fill(s, keys, values):
             s.block(blk, 1)[:, slot] = values[t].to(s.dtype)
 
 
-# (bf16: single tokens, speculative ones, 128 rows; blocks in boxes and on mma.sync)
+# (single tokens, speculative ones, 128 rows; blocks in boxes and on mma.sync)
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("T,H,Hkv", [(1, 8, 1), (1, 4, 4), (4, 8, 2), (16, 8, 1), (128, 2, 2)])
 @pytest.mark.parametrize("D,bs", [(64, 16), (128, 16), (128, 3), (32, 16), (256, 16), (64, 1)])
-def test_values_that_all_but_cancel_keep_their_bits_in_calls_of_few_rows(D, bs, T, H, Hkv):
+def test_values_that_all_but_cancel_keep_their_bits_in_calls_of_few_rows(D, bs, T, H, Hkv, dtype):
     """Neighbouring positions weigh almost alike and hold opposite values.  Each weight off
-    by its square of half a step (2^-16), the exponent by 4 roundings of fp32, 2^-22 for
-    the exponential, 2 roundings a position for the sums of both."""
-    s = Chunk(dtype=BF16, D=D, bs=bs, B=2, T=T, H=H, Hkv=Hkv, pos=[31, 0], scale=1.0)
+    by the square of half a step (2^-16; 2^-22, or 2^-25 of the largest), the exponent by 4
+    roundings of fp32, 2^-22 for the exponential, 2 roundings a position for the sums of
+    both."""
+    s = Chunk(dtype=dtype, D=D, bs=bs, B=2, T=T, H=H, Hkv=Hkv, pos=[31, 0], scale=1.0)
     g = torch.Generator().manual_seed(4)
     n = 31 + T
-    keys = torch.stack((-torch.rand(n, generator=g) * 3, torch.rand(n, generator=g) / 64), -1).to(BF16)
+    keys = torch.stack((-torch.rand(n, generator=g) * 3, torch.rand(n, generator=g) / 64), -1).to(dtype)
     keys[1::2, 0] = keys[:n // 2 * 2:2, 0]
-    values = (torch.where(torch.rand(n, D, generator=g) < 0.5, 1.0, 1.25)).to(BF16)
+    values = (torch.where(torch.rand(n, D, generator=g) < 0.5, 1.0, 1.25)).to(dtype)
     values[1::2] = -values[:n // 2 * 2:2]
     fill(s, keys, values)
     out = s.call().cpu().double()
@@ -57,8 +59,10 @@ def test_values_that_all_but_cancel_keep_their_bits_in_calls_of_few_rows(D, bs, 
             w = (x[:m] - x[:m].max()).exp()
             a = w / w.sum()
             want, av = a @ values[:m].double(), a @ values[:m].double().abs()
-            tol = av * (2 * (4 * u * float(x[:m].abs().max()) + 2.0 ** -22) + half_step(BF16) ** 2 + 2 * (m + 8) * 2 * u)
-            tol = tol + half_step(BF16) * (want.abs() + tol)
+            tol = av * (2 * (4 * u * float(x[:m].abs().max()) + 2.0 ** -22) + half_step(dtype) ** 2 + 2 * (m + 8) * 2 * u)
+            if dtype == F16:
+                tol = tol + 2.0 ** -25 * values[:m].double().abs().sum(0) / w.sum()
+            tol = tol + half_step(dtype) * (want.abs() + tol)
             off = ((out[b, t] - want).abs() / tol).max()
             assert off <= 1, f"sequence {b}, token {t}: {float(off):.2f} of the bound"
 
