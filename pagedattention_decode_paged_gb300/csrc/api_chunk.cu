@@ -52,7 +52,8 @@ int umma_box_rows(const pa_shape *s) {
 // Row by row, one warp of the tcgen05 kernel's CTA copies K and V; on mma.sync the
 // four of each of up to seven CTAs do.  Query rows of a kv head (tokens of the padded
 // batch times heads of the group) above which the products outweigh that.  tcgen05
-// against mma.sync, fp16, behind 2047 tokens: 32 sequences, 64 heads on 8 of 128, blocks
+// against mma.sync, fp16, one part of weights (two, as up to 128 rows have them, add a
+// tenth on mma.sync), behind 2047 tokens: 32 sequences, 64 heads on 8 of 128, blocks
 // of 1: 8 rows 178 and 96 us, 64 rows 195 and 108, 128 rows 202 and 196, 256 rows 218
 // and 367; 16 sequences, 32 heads on 8 of 64, blocks of 3: 128 rows 82 and 64, 256 rows 91
 // and 111; 32 heads of 128: 128 rows 403 and 368, 256 rows 445 and 724; behind none 128

@@ -11,7 +11,7 @@
 // heads behind 131071 of them, 38 records each: the call 123 us without, 104 so).
 // The joined rows go through shared memory to a warp each.  Bound by latency: cuts,
 // records and outputs are three dependent trips to L2 (4 tokens behind 2048 in 32
-// sequences, 64 heads: 5 MB of records, about 4 us after the first launch, 8.2 alone).
+// sequences, 64 heads: 5 MB of records, about 4 us after the first launch, 8.9 alone).
 #include "chunk_sched.cuh"
 
 namespace pa {

@@ -14,7 +14,7 @@
 // V come by 16-byte asynchronous copies from wherever the block table puts
 // them, one tile ahead of the products; each row's place is looked up two tiles
 // ahead.  Bound by the warps' own latency, four or eight of them on an SM (issue
-// 17%, tensor pipe 26%): 4 prompts of 1024 tokens, 16 heads on 4 of 256 320 us, 107
+// 18%, tensor pipe 26%): 4 prompts of 1024 tokens, 16 heads on 4 of 256 320 us, 107
 // TFLOP/s; 1 token behind 2047, 32 sequences, 64 heads on 8 of 128 in blocks of 1
 // 105 us, 2.6 TB/s.  At head_dim 256 two parts do not fit the registers: a thread stores
 // 128 to 134 bytes of its own and loads 592 to 596 (fp16 with one part 40 and 56).

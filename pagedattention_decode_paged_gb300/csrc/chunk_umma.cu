@@ -23,7 +23,7 @@
 // heads on 8 of 128: 2.75 ms back to back, 1.50 PFLOP/s of what is seen, 78% of a library
 // product's rate in a burst); prompts, a step's way through both products and the
 // exponentials, columns of the diagonal that are not seen, starts and ends of items (8 of
-// 900 to 2047 tokens: 422 us, 1.07 PFLOP/s, the tensor core busy 58% of the time); few
+// 900 to 2047 tokens: 422 us, 1.07 PFLOP/s, the tensor core busy 56% of the time); few
 // rows, the copies of K and V and 20 us of start, records and merge (32 x 4 tokens behind
 // 2048: 67 us, 3.4 TB/s from memory); blocks that are copied row by row, the copying warp.
 //
