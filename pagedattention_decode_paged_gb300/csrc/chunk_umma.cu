@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float2 e = fma2(make_float2(f(c + 2 * i), f(c + 2 * i + 1)), make_float2(scale, scale), make_float2(nb, nb));
                         e.x = ex2_approx(e.x);
                         e.y = ex2_approx(e.y);
-                        // the sum: of exactly the weights that the product uses
+                        // the sum: of the weights that the product uses (two parts: but for the rest's rounding)
                         if (TWO) sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = Elem<T>::pack2(e.x, e.y);
                         if (TWO) {
